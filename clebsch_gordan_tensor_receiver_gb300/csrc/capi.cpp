@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -1021,5 +1022,262 @@ extern "C" uvu_status uvu_radial_hidden_bwd(uvu_plan_t plan, int64_t n_edges, co
     cudaError_t e = launch_radial_hidden_bwd(n_edges, r, r_cut, p_env, net, weights, dh, dr, dweights, workspace, f64, sms,
                                              static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "radial network reverse pass launch");
+    return ok();
+}
+
+// ---------------------------------------------------------------------- node-update operators
+namespace uvu {
+namespace {
+
+uvu_status block_dtype(uvu_dtype t) {
+    if (t == UVU_F32 || t == UVU_BF16 || t == UVU_F16) return UVU_OK;
+    if (t == UVU_F64) return fail(UVU_ERR_UNSUPPORTED, "the node-update operators take UVU_F32, UVU_BF16 and UVU_F16");
+    return fail(UVU_ERR_INVALID_ARGUMENT, "unknown dtype");
+}
+
+// Tensors of these operators may be views: alignment to the element is enough.
+uvu_status need_elem(const void* p, uvu_dtype t, const char* name) {
+    if (!p) return fail(UVU_ERR_INVALID_ARGUMENT, std::string(name) + " is NULL");
+    const uintptr_t size = t == UVU_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(p) & (size - 1))
+        return fail(UVU_ERR_INVALID_ARGUMENT, std::string(name) + " is not aligned to its element");
+    return UVU_OK;
+}
+
+// The device's SM count, kept per device: the query costs more than the smallest of these kernels.
+uvu_status sm_count_cached(int* sms) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev >= 0 && dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return UVU_OK;
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    if (dev >= 0 && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+    return UVU_OK;
+}
+
+uvu_status check_workspace(const void* ws, size_t have, size_t want, const char* fn) {
+    if (want == 0) return UVU_OK;
+    if (!ws || have < want || !aligned16(ws))
+        return fail(UVU_ERR_INVALID_ARGUMENT, std::string("workspace is NULL, misaligned or smaller than ") + fn + "()");
+    return UVU_OK;
+}
+
+uvu_status norm_shape(uvu_dtype dtype, int64_t n_rows, int n_graphs, int64_t max_rows, int channels, int groups, NormShape* s) {
+    UVU_TRY(block_dtype(dtype));
+    if (n_rows < 0 || n_rows >= std::numeric_limits<int32_t>::max())
+        return fail(UVU_ERR_INVALID_ARGUMENT, "n_rows must be in [0, 2^31 - 1)");
+    if (n_graphs < 1 || n_graphs > (1 << 24)) return fail(UVU_ERR_INVALID_ARGUMENT, "n_graphs must be in [1, 2^24]");
+    if (max_rows < 0) return fail(UVU_ERR_INVALID_ARGUMENT, "max_rows must be >= 0");
+    if (groups < 1 || channels < 1 || channels > 8192 || channels % groups)
+        return fail(UVU_ERR_INVALID_ARGUMENT, "channels must be a multiple of groups in [1, 8192]");
+    *s = NormShape{dtype, n_rows, n_graphs, std::min(max_rows, n_rows), channels, groups, UVU_ACT_NONE, 0.0};
+    return UVU_OK;
+}
+
+uvu_status dropout_call(const char* what, uvu_dtype dtype, int64_t n_draws, int inner, double p, uint64_t seed, uint64_t offset,
+                        const void* x, const char* x_name, const void* residual, void* y, const char* y_name, uvu_stream_t stream) {
+    UVU_TRY(block_dtype(dtype));
+    if (inner < 1) return fail(UVU_ERR_INVALID_ARGUMENT, "inner must be >= 1");
+    if (n_draws < 0 || n_draws > (int64_t(1) << 60) / inner) return fail(UVU_ERR_INVALID_ARGUMENT, "n_draws * inner must be in [0, 2^60]");
+    if (!(p >= 0.0 && p <= 1.0)) return fail(UVU_ERR_INVALID_ARGUMENT, "p must be in [0, 1]");
+    if (n_draws == 0) return ok();
+    UVU_TRY(need_elem(x, dtype, x_name));
+    UVU_TRY(need_elem(y, dtype, y_name));
+    if (residual) UVU_TRY(need_elem(residual, dtype, "residual"));
+    int sms = 0;
+    UVU_TRY(sm_count_cached(&sms));
+    const uint32_t limit = uint32_t(p * 65536.0 + 0.5);
+    cudaError_t e = launch_dropout(dtype, n_draws * inner, inner, limit, seed, offset, x, residual, y, sms,
+                                   static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    return ok();
+}
+
+uvu_status attn_check(const uvu_attn_shape* s) {
+    if (!s) return fail(UVU_ERR_INVALID_ARGUMENT, "shape is NULL");
+    UVU_TRY(block_dtype(s->dtype));
+    if (s->n_graphs < 1 || s->n_graphs > (1 << 24)) return fail(UVU_ERR_INVALID_ARGUMENT, "n_graphs must be in [1, 2^24]");
+    if (s->n_q < 0 || s->n_k < 0 || s->n_q >= std::numeric_limits<int32_t>::max() || s->n_k >= std::numeric_limits<int32_t>::max())
+        return fail(UVU_ERR_INVALID_ARGUMENT, "n_q and n_k must be in [0, 2^31 - 1)");
+    if (s->max_q < 0 || s->max_k < 0) return fail(UVU_ERR_INVALID_ARGUMENT, "max_q and max_k must be >= 0");
+    if (s->kv_heads < 1 || s->kv_heads > 65535 || s->q_heads < 1 || s->q_heads > 65535 || s->q_heads % s->kv_heads)
+        return fail(UVU_ERR_INVALID_ARGUMENT, "q_heads must be a multiple of kv_heads, both in [1, 65535]");
+    if (s->head_dim < 1) return fail(UVU_ERR_INVALID_ARGUMENT, "head_dim must be >= 1");
+    if (s->head_dim > 128) return fail(UVU_ERR_UNSUPPORTED, "head_dim must be <= 128");
+    if (!std::isfinite(s->scale)) return fail(UVU_ERR_INVALID_ARGUMENT, "scale must be finite");
+    if (s->reserved != 0) return fail(UVU_ERR_INVALID_ARGUMENT, "reserved must be 0");
+    for (int64_t v : {s->q_row, s->q_head, s->k_row, s->k_head, s->v_row, s->v_head, s->o_row, s->o_head})
+        if (v < 0 || v > (int64_t(1) << 40)) return fail(UVU_ERR_INVALID_ARGUMENT, "strides must be in [0, 2^40]");
+    return UVU_OK;
+}
+
+uvu_attn_shape attn_clamped(uvu_attn_shape s) {
+    s.max_q = std::min(s.max_q, s.n_q);
+    s.max_k = std::min(s.max_k, s.n_k);
+    return s;
+}
+
+}  // namespace
+}  // namespace uvu
+
+extern "C" uvu_status uvu_group_norm_workspace(uvu_dtype dtype, int64_t n_rows, int n_graphs, int64_t max_rows, int channels,
+                                               int groups, size_t* fwd_bytes, size_t* bwd_bytes) {
+    NormShape s;
+    UVU_TRY(norm_shape(dtype, n_rows, n_graphs, max_rows, channels, groups, &s));
+    if (fwd_bytes) *fwd_bytes = norm_workspace(s, false);
+    if (bwd_bytes) *bwd_bytes = norm_workspace(s, true);
+    return ok();
+}
+
+extern "C" uvu_status uvu_group_norm_fwd(uvu_dtype dtype, int64_t n_rows, int n_graphs, int64_t max_rows, int channels,
+                                         int groups, uvu_act act, double eps, const int32_t* offsets, const void* x,
+                                         const float* gamma, const float* beta, void* y, float* mean, float* rstd,
+                                         void* workspace, size_t workspace_bytes, uvu_stream_t stream) {
+    UVU_RANGE("uvu_group_norm_fwd");
+    NormShape s;
+    UVU_TRY(norm_shape(dtype, n_rows, n_graphs, max_rows, channels, groups, &s));
+    if (act != UVU_ACT_NONE && act != UVU_ACT_SILU) return fail(UVU_ERR_INVALID_ARGUMENT, "unknown activation");
+    if (!(eps >= 0) || !std::isfinite(eps)) return fail(UVU_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
+    s.act = act;
+    s.eps = eps;
+    UVU_TRY(need_idx(offsets, "offsets"));
+    UVU_TRY(need_elem(mean, UVU_F32, "mean"));
+    UVU_TRY(need_elem(rstd, UVU_F32, "rstd"));
+    if (n_rows > 0) {
+        UVU_TRY(need_elem(x, dtype, "x"));
+        UVU_TRY(need_elem(y, dtype, "y"));
+        UVU_TRY(need_elem(gamma, UVU_F32, "gamma"));
+        UVU_TRY(need_elem(beta, UVU_F32, "beta"));
+    }
+    UVU_TRY(check_workspace(workspace, workspace_bytes, norm_workspace(s, false), "uvu_group_norm_workspace"));
+    cudaError_t e = launch_norm_fwd(s, offsets, x, gamma, beta, y, mean, rstd, workspace, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "group norm launch");
+    return ok();
+}
+
+extern "C" uvu_status uvu_group_norm_bwd(uvu_dtype dtype, int64_t n_rows, int n_graphs, int64_t max_rows, int channels,
+                                         int groups, uvu_act act, const int32_t* offsets, const void* x, const float* gamma,
+                                         const float* beta, const float* mean, const float* rstd, const void* dy, void* dx,
+                                         float* dgamma, float* dbeta, void* workspace, size_t workspace_bytes,
+                                         uvu_stream_t stream) {
+    UVU_RANGE("uvu_group_norm_bwd");
+    NormShape s;
+    UVU_TRY(norm_shape(dtype, n_rows, n_graphs, max_rows, channels, groups, &s));
+    if (act != UVU_ACT_NONE && act != UVU_ACT_SILU) return fail(UVU_ERR_INVALID_ARGUMENT, "unknown activation");
+    s.act = act;
+    UVU_TRY(need_elem(dgamma, UVU_F32, "dgamma"));
+    UVU_TRY(need_elem(dbeta, UVU_F32, "dbeta"));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (n_rows == 0) {
+        cudaError_t e = cudaMemsetAsync(dgamma, 0, size_t(channels) * 4, st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(dbeta, 0, size_t(channels) * 4, st);
+        if (e != cudaSuccess) return cuda_fail(e, "memset");
+        return ok();
+    }
+    UVU_TRY(need_idx(offsets, "offsets"));
+    UVU_TRY(need_elem(x, dtype, "x"));
+    UVU_TRY(need_elem(dy, dtype, "dy"));
+    UVU_TRY(need_elem(dx, dtype, "dx"));
+    UVU_TRY(need_elem(gamma, UVU_F32, "gamma"));
+    UVU_TRY(need_elem(beta, UVU_F32, "beta"));
+    UVU_TRY(need_elem(mean, UVU_F32, "mean"));
+    UVU_TRY(need_elem(rstd, UVU_F32, "rstd"));
+    UVU_TRY(check_workspace(workspace, workspace_bytes, norm_workspace(s, true), "uvu_group_norm_workspace"));
+    cudaError_t e = launch_norm_bwd(s, offsets, x, dy, gamma, beta, mean, rstd, dx, dgamma, dbeta, workspace, st);
+    if (e != cudaSuccess) return cuda_fail(e, "group norm gradient launch");
+    return ok();
+}
+
+extern "C" uvu_status uvu_dropout_fwd(uvu_dtype dtype, int64_t n_draws, int inner, double p, uint64_t seed, uint64_t offset,
+                                      const void* x, const void* residual, void* y, uvu_stream_t stream) {
+    UVU_RANGE("uvu_dropout_fwd");
+    return dropout_call("dropout launch", dtype, n_draws, inner, p, seed, offset, x, "x", residual, y, "y", stream);
+}
+
+extern "C" uvu_status uvu_dropout_bwd(uvu_dtype dtype, int64_t n_draws, int inner, double p, uint64_t seed, uint64_t offset,
+                                      const void* dy, void* dx, uvu_stream_t stream) {
+    UVU_RANGE("uvu_dropout_bwd");
+    return dropout_call("dropout gradient launch", dtype, n_draws, inner, p, seed, offset, dy, "dy", nullptr, dx, "dx", stream);
+}
+
+extern "C" uvu_status uvu_attn_workspace(const uvu_attn_shape* shape, size_t* fwd_bytes, size_t* bwd_bytes) {
+    UVU_TRY(attn_check(shape));
+    int sms = 0;
+    UVU_TRY(sm_count_cached(&sms));
+    size_t f = 0, b = 0;
+    attn_workspace(attn_clamped(*shape), sms, &f, &b);
+    if (fwd_bytes) *fwd_bytes = f;
+    if (bwd_bytes) *bwd_bytes = b;
+    return ok();
+}
+
+extern "C" uvu_status uvu_attn_fwd(const uvu_attn_shape* shape, const int32_t* q_offsets, const int32_t* k_offsets,
+                                   const uint8_t* k_keep, const void* q, const void* k, const void* v, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, uvu_stream_t stream) {
+    UVU_RANGE("uvu_attn_fwd");
+    UVU_TRY(attn_check(shape));
+    if (shape->n_q == 0) return ok();
+    const uvu_attn_shape s = attn_clamped(*shape);
+    UVU_TRY(need_idx(q_offsets, "q_offsets"));
+    UVU_TRY(need_idx(k_offsets, "k_offsets"));
+    UVU_TRY(need_elem(q, s.dtype, "q"));
+    UVU_TRY(need_elem(out, s.dtype, "out"));
+    UVU_TRY(need_elem(lse, UVU_F32, "lse"));
+    if (s.n_k > 0) {
+        UVU_TRY(need_elem(k, s.dtype, "k"));
+        UVU_TRY(need_elem(v, s.dtype, "v"));
+    }
+    int sms = 0;
+    UVU_TRY(sm_count_cached(&sms));
+    size_t want = 0, unused = 0;
+    attn_workspace(s, sms, &want, &unused);
+    UVU_TRY(check_workspace(workspace, workspace_bytes, want, "uvu_attn_workspace"));
+    AttnTensors t = {};
+    t.q_offsets = q_offsets, t.k_offsets = k_offsets, t.keep = k_keep;
+    t.q = q, t.k = k, t.v = v, t.out = out, t.lse = lse;
+    cudaError_t e = launch_attn_fwd(s, t, workspace, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+    return ok();
+}
+
+extern "C" uvu_status uvu_attn_bwd(const uvu_attn_shape* shape, const int32_t* q_offsets, const int32_t* k_offsets,
+                                   const uint8_t* k_keep, const void* q, const void* k, const void* v, const void* out,
+                                   const float* lse, const void* d_out, void* dq, void* dk, void* dv, void* workspace,
+                                   size_t workspace_bytes, uvu_stream_t stream) {
+    UVU_RANGE("uvu_attn_bwd");
+    UVU_TRY(attn_check(shape));
+    const uvu_attn_shape s = attn_clamped(*shape);
+    if (!dk != !dv) return fail(UVU_ERR_INVALID_ARGUMENT, "dk and dv are computed together: both or neither");
+    if (!dq && !dk) return ok();
+    if (s.n_q == 0 && s.n_k == 0) return ok();
+    UVU_TRY(need_idx(q_offsets, "q_offsets"));
+    UVU_TRY(need_idx(k_offsets, "k_offsets"));
+    if (s.n_q > 0) {
+        UVU_TRY(need_elem(q, s.dtype, "q"));
+        UVU_TRY(need_elem(out, s.dtype, "out"));
+        UVU_TRY(need_elem(d_out, s.dtype, "d_out"));
+        UVU_TRY(need_elem(lse, UVU_F32, "lse"));
+        if (dq) UVU_TRY(need_elem(dq, s.dtype, "dq"));
+    }
+    if (s.n_k > 0) {
+        UVU_TRY(need_elem(k, s.dtype, "k"));
+        UVU_TRY(need_elem(v, s.dtype, "v"));
+        if (dk) {
+            UVU_TRY(need_elem(dk, s.dtype, "dk"));
+            UVU_TRY(need_elem(dv, s.dtype, "dv"));
+        }
+    }
+    int sms = 0;
+    UVU_TRY(sm_count_cached(&sms));
+    size_t want = 0, unused = 0;
+    attn_workspace(s, sms, &unused, &want);
+    UVU_TRY(check_workspace(workspace, workspace_bytes, want, "uvu_attn_workspace"));
+    AttnTensors t = {};
+    t.q_offsets = q_offsets, t.k_offsets = k_offsets, t.keep = k_keep;
+    t.q = q, t.k = k, t.v = v, t.out = const_cast<void*>(out), t.lse = const_cast<float*>(lse), t.d_out = d_out;
+    t.dq = dq, t.dk = dk, t.dv = dv;
+    cudaError_t e = launch_attn_bwd(s, t, workspace, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "attention gradient launch");
     return ok();
 }

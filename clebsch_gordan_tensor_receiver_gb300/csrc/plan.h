@@ -185,4 +185,37 @@ cudaError_t launch_mix_fwd(const Plan& p, int64_t N, int W, const void* in, cons
                            cudaStream_t st);
 cudaError_t launch_mix_bwd(const Plan& p, int64_t N, int W, const void* in, const void* M, const void* g, void* d_in,
                            void* dM, void* ws, cudaStream_t st);
+// dropout.cu
+cudaError_t launch_dropout(uvu_dtype dtype, int64_t n, int inner, uint32_t limit, uint64_t seed, uint64_t offset, const void* x,
+                           const void* residual, void* y, int sms, cudaStream_t st);
+// norm.cu
+struct NormShape {
+    uvu_dtype dtype;
+    int64_t rows;
+    int graphs;
+    int64_t max_rows;
+    int channels, groups;
+    uvu_act act;
+    double eps;
+};
+size_t norm_workspace(const NormShape& s, bool bwd);
+cudaError_t launch_norm_fwd(const NormShape& s, const int32_t* offsets, const void* x, const float* gamma, const float* beta,
+                            void* y, float* mean, float* rstd, void* ws, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormShape& s, const int32_t* offsets, const void* x, const void* dy, const float* gamma,
+                            const float* beta, const float* mean, const float* rstd, void* dx, float* dgamma, float* dbeta,
+                            void* ws, cudaStream_t st);
+// attn.cu
+using AttnShape = uvu_attn_shape;
+struct AttnTensors {
+    const int32_t *q_offsets, *k_offsets;
+    const uint8_t* keep;
+    const void *q, *k, *v;
+    void* out;
+    float* lse;
+    const void* d_out;
+    void *dq, *dk, *dv;
+};
+void attn_workspace(const AttnShape& s, int sms, size_t* fwd, size_t* bwd);
+cudaError_t launch_attn_fwd(const AttnShape& s, const AttnTensors& t, void* ws, int sms, cudaStream_t st);
+cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, int sms, cudaStream_t st);
 }  // namespace uvu

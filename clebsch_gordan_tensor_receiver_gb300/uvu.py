@@ -18,7 +18,8 @@ from dataclasses import dataclass
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libuvu.so")
 
-UVU_F32, UVU_F64 = 0, 1
+UVU_F32, UVU_F64, UVU_BF16, UVU_F16 = 0, 1, 2, 3
+UVU_ACT_NONE, UVU_ACT_SILU = 0, 1
 UVU_DX_SENDER, UVU_DX_ATOMIC, UVU_DX_STAGED = 0, 1, 2
 UVU_MODULE_CONV, UVU_MODULE_HVP, UVU_MODULE_TP, UVU_MODULE_TP_SHARED = 0, 1, 2, 3
 UVU_FWD_AUTO, UVU_FWD_RECEIVER, UVU_FWD_SENDER = 0, 1, 2
@@ -38,6 +39,8 @@ EXPORTS = (
     "uvu_radial_hidden", "uvu_conv_fwd_radial", "uvu_radial_module_source",
     "uvu_radial_weights", "uvu_radial_weights_workspace", "uvu_radial_weights_bwd", "uvu_radial_weights_bwd_workspace",
     "uvu_radial_hidden_bwd", "uvu_radial_hidden_bwd_workspace",
+    "uvu_group_norm_fwd", "uvu_group_norm_bwd", "uvu_group_norm_workspace", "uvu_dropout_fwd", "uvu_dropout_bwd",
+    "uvu_attn_fwd", "uvu_attn_bwd", "uvu_attn_workspace",
     "uvu_fma_rate_probe", "uvu_status_string", "uvu_last_error_message",
 )
 
@@ -46,6 +49,16 @@ class UVUError(RuntimeError):
     def __init__(self, status: int, fn: str, msg: str):
         super().__init__(f"{fn}: {STATUS.get(status, status)}: {msg}")
         self.status = status
+
+
+class AttnShape(ctypes.Structure):
+    """uvu_attn_shape of include/uvu.h."""
+
+    _fields_ = ([("dtype", ctypes.c_int), ("n_graphs", ctypes.c_int32)]
+                + [(f, ctypes.c_int64) for f in ("n_q", "n_k", "max_q", "max_k")]
+                + [(f, ctypes.c_int32) for f in ("q_heads", "kv_heads", "head_dim", "reserved")]
+                + [("scale", ctypes.c_double)]
+                + [(f, ctypes.c_int64) for f in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head", "o_row", "o_head")])
 
 
 def _load():
@@ -95,6 +108,14 @@ def _load():
         "uvu_radial_weights_bwd_workspace": [P, I64, I, ctypes.POINTER(SZ)],
         "uvu_radial_hidden_bwd": [P, I64, P, ctypes.c_double, I, I, ctypes.POINTER(I), P, P, P, P, P, SZ, P],
         "uvu_radial_hidden_bwd_workspace": [P, I64, I, ctypes.POINTER(I), ctypes.POINTER(SZ)],
+        "uvu_group_norm_fwd": [I, I64, I, I64, I, I, I, ctypes.c_double] + [P] * 8 + [SZ, P],
+        "uvu_group_norm_bwd": [I, I64, I, I64, I, I, I] + [P] * 11 + [SZ, P],
+        "uvu_group_norm_workspace": [I, I64, I, I64, I, I, ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
+        "uvu_dropout_fwd": [I, I64, I, ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64, P, P, P, P],
+        "uvu_dropout_bwd": [I, I64, I, ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64, P, P, P],
+        "uvu_attn_fwd": [ctypes.POINTER(AttnShape)] + [P] * 9 + [SZ, P],
+        "uvu_attn_bwd": [ctypes.POINTER(AttnShape)] + [P] * 13 + [SZ, P],
+        "uvu_attn_workspace": [ctypes.POINTER(AttnShape), ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -136,7 +157,9 @@ for _n in ("uvu_plan_destroy", "uvu_plan_info", "uvu_plan_cg", "uvu_plan_source"
            "uvu_mix_fwd", "uvu_mix_bwd", "uvu_mix_workspace", "uvu_conv_uvw_fwd",
            "uvu_radial_hidden", "uvu_conv_fwd_radial", "uvu_radial_module_source", "uvu_fma_rate_probe",
            "uvu_radial_weights", "uvu_radial_weights_workspace", "uvu_radial_weights_bwd",
-           "uvu_radial_weights_bwd_workspace", "uvu_radial_hidden_bwd", "uvu_radial_hidden_bwd_workspace"):
+           "uvu_radial_weights_bwd_workspace", "uvu_radial_hidden_bwd", "uvu_radial_hidden_bwd_workspace",
+           "uvu_group_norm_fwd", "uvu_group_norm_bwd", "uvu_group_norm_workspace", "uvu_dropout_fwd", "uvu_dropout_bwd",
+           "uvu_attn_fwd", "uvu_attn_bwd", "uvu_attn_workspace"):
     globals()[_n] = _wrap(_n)
 
 
@@ -457,3 +480,195 @@ class Graph:
                           _ptr(self.send_offsets), _ptr(self.send_eids), _ptr(self.send_recv),
                           _ptr(ws), nb.value, _stream(stream))
         self._ws = ws
+
+
+# ------------------------------------------------------------------- node-update operators
+
+def _block_dtype(t) -> int:
+    import torch
+    code = {torch.float32: UVU_F32, torch.bfloat16: UVU_BF16, torch.float16: UVU_F16, torch.float64: UVU_F64}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"the node-update operators take float32, bfloat16 and float16 tensors, not {t.dtype}")
+    return code
+
+
+def _same(name, t, like, shape=None):
+    """The checks that the C ABI cannot make from a pointer: type, device, shape, contiguity."""
+    if t.dtype != like.dtype or t.device != like.device:
+        raise TypeError(f"{name} must have the type and device of its operands")
+    if shape is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _f32(name, t, shape, device):
+    import torch
+    if t.dtype != torch.float32 or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)} on the operands' device")
+
+
+def _offsets(name, t, device):
+    import torch
+    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or t.numel() < 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [n_graphs + 1] on the operands' device")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    import torch
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def group_norm_workspace_bytes(x, n_graphs, groups, max_rows=None):
+    """(forward bytes, backward bytes) of device workspace for the group norm of x [N][C]."""
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    uvu_group_norm_workspace(_block_dtype(x), x.shape[0], n_graphs, x.shape[0] if max_rows is None else max_rows, x.shape[1],
+                             groups, ctypes.byref(f), ctypes.byref(b))
+    return f.value, b.value
+
+
+def _norm_checks(x, gamma, beta, offsets, groups, mean, rstd):
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be contiguous [rows][channels]")
+    _offsets("offsets", offsets, x.device)
+    for name, t in (("gamma", gamma), ("beta", beta)):
+        _f32(name, t, (x.shape[1],), x.device)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _f32(name, t, (offsets.numel() - 1, groups), x.device)
+
+
+def group_norm_fwd(x, gamma, beta, offsets, groups, y, mean, rstd, act=UVU_ACT_SILU, eps=1e-5, max_rows=None,
+                   workspace=None, stream=None):
+    """Group norm with an activation over a packed batch (see uvu_group_norm_fwd): x, y [N][C], offsets
+    [B+1] int32, mean and rstd [B][groups] fp32 (outputs); `workspace` (uint8) is allocated here with
+    torch if None."""
+    import torch
+    _norm_checks(x, gamma, beta, offsets, groups, mean, rstd)
+    _same("y", y, x, x.shape)
+    n, b = x.shape[0], offsets.numel() - 1
+    most = n if max_rows is None else max_rows
+    if workspace is None:
+        workspace = torch.empty(max(16, group_norm_workspace_bytes(x, b, groups, most)[0]), dtype=torch.uint8, device=x.device)
+    uvu_group_norm_fwd(_block_dtype(x), n, b, most, x.shape[1], groups, act, eps, _at(offsets), _at(x), _at(gamma), _at(beta),
+                       _at(y), _at(mean), _at(rstd), _at(workspace), workspace.numel(), _raw_stream(stream))
+
+
+def group_norm_bwd(dy, x, gamma, beta, offsets, groups, mean, rstd, dx, dgamma, dbeta, act=UVU_ACT_SILU, max_rows=None,
+                   workspace=None, stream=None):
+    """VJP of group_norm_fwd (see uvu_group_norm_bwd)."""
+    import torch
+    _norm_checks(x, gamma, beta, offsets, groups, mean, rstd)
+    _same("dy", dy, x, x.shape)
+    _same("dx", dx, x, x.shape)
+    _f32("dgamma", dgamma, gamma.shape, x.device)
+    _f32("dbeta", dbeta, gamma.shape, x.device)
+    n, b = x.shape[0], offsets.numel() - 1
+    most = n if max_rows is None else max_rows
+    if workspace is None:
+        workspace = torch.empty(max(16, group_norm_workspace_bytes(x, b, groups, most)[1]), dtype=torch.uint8, device=x.device)
+    uvu_group_norm_bwd(_block_dtype(x), n, b, most, x.shape[1], groups, act, _at(offsets), _at(x), _at(gamma), _at(beta),
+                       _at(mean), _at(rstd), _at(dy), _at(dx), _at(dgamma), _at(dbeta), _at(workspace), workspace.numel(),
+                       _raw_stream(stream))
+
+
+def _draws(x, inner):
+    if inner < 1 or x.numel() % inner:
+        raise ValueError("the tensor's size must be a multiple of inner >= 1")
+    return x.numel() // inner
+
+
+def dropout_fwd(x, p, seed, y, offset=0, inner=1, residual=None, stream=None):
+    """y = residual + dropout(x) with the mask of (seed, offset); `inner` consecutive values share a draw
+    (see uvu_dropout_fwd).  All tensors contiguous and of one shape; y may be x or residual."""
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    _same("y", y, x, x.shape)
+    if residual is not None:
+        _same("residual", residual, x, x.shape)
+    uvu_dropout_fwd(_block_dtype(x), _draws(x, inner), inner, p, seed, offset, _at(x), _at(residual), _at(y),
+                    _raw_stream(stream))
+
+
+def dropout_bwd(dy, p, seed, dx, offset=0, inner=1, stream=None):
+    """VJP of dropout_fwd with respect to x; the residual's gradient is dy (see uvu_dropout_bwd)."""
+    if not dy.is_contiguous():
+        raise ValueError("dy must be contiguous")
+    _same("dx", dx, dy, dy.shape)
+    uvu_dropout_bwd(_block_dtype(dy), _draws(dy, inner), inner, p, seed, offset, _at(dy), _at(dx), _raw_stream(stream))
+
+
+class Attention:
+    """Attention of the rows of each graph of a packed batch to that graph's states (see uvu_attn_fwd):
+    q, out [Tq][q_heads][head_dim], k, v [Tk][kv_heads][head_dim] (any row and head strides, values of a
+    head consecutive), q_offsets and k_offsets [B+1] int32.  max_q, max_k: lengths that no graph exceeds
+    (default: all rows).  scale defaults to head_dim ** -0.5."""
+
+    def __init__(self, q_heads, kv_heads, head_dim, q_offsets, k_offsets, max_q=None, max_k=None, scale=None):
+        _offsets("q_offsets", q_offsets, q_offsets.device)
+        _offsets("k_offsets", k_offsets, q_offsets.device)
+        if q_offsets.numel() != k_offsets.numel():
+            raise ValueError("q_offsets and k_offsets must have the same number of graphs")
+        self.q_offsets, self.k_offsets = q_offsets, k_offsets
+        self.q_heads, self.kv_heads, self.head_dim = int(q_heads), int(kv_heads), int(head_dim)
+        self.max_q, self.max_k = max_q, max_k
+        self.scale = float(head_dim) ** -0.5 if scale is None else float(scale)
+
+    def _shape(self, q, k, v, out):
+        for name, t, h in (("q", q, self.q_heads), ("k", k, self.kv_heads), ("v", v, self.kv_heads), ("out", out, self.q_heads)):
+            if t.dim() != 3 or t.shape[1] != h or t.shape[2] != self.head_dim or (t.stride(2) != 1 and t.shape[2] > 1):
+                raise ValueError(f"{name} must be [rows][{h}][{self.head_dim}] with consecutive values in a head")
+            _same(name, t, q)
+        if out.shape[0] != q.shape[0] or v.shape[0] != k.shape[0]:
+            raise ValueError("out must have q's rows and v must have k's")
+        if q.device != self.q_offsets.device:
+            raise ValueError("the operands must be on the offsets' device")
+        nq, nk = q.shape[0], k.shape[0]
+        return AttnShape(_block_dtype(q), self.q_offsets.numel() - 1, nq, nk, nq if self.max_q is None else self.max_q,
+                         nk if self.max_k is None else self.max_k, self.q_heads, self.kv_heads, self.head_dim, 0, self.scale,
+                         q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1), out.stride(0),
+                         out.stride(1))
+
+    def _workspace(self, shape, which, workspace, device):
+        if workspace is None:
+            import torch
+            b = [ctypes.c_size_t(), ctypes.c_size_t()]
+            uvu_attn_workspace(ctypes.byref(shape), ctypes.byref(b[0]), ctypes.byref(b[1]))
+            workspace = torch.empty(max(16, b[which].value), dtype=torch.uint8, device=device)
+        return workspace
+
+    def workspace_bytes(self, q, k):
+        """(forward bytes, backward bytes) of device workspace for operands of q's and k's sizes."""
+        f, b = ctypes.c_size_t(), ctypes.c_size_t()
+        uvu_attn_workspace(ctypes.byref(self._shape(q, k, k, q)), ctypes.byref(f), ctypes.byref(b))
+        return f.value, b.value
+
+    def _keep(self, keep, k):
+        import torch
+        if keep is not None and (keep.dtype not in (torch.uint8, torch.bool) or keep.shape != k.shape[:1]
+                                 or keep.device != k.device or not keep.is_contiguous()):
+            raise ValueError("keep must be a contiguous uint8 or bool tensor [states] on the operands' device")
+        return _at(keep)
+
+    def fwd(self, q, k, v, out, lse, keep=None, workspace=None, stream=None):
+        """out and lse [Tq][q_heads] (fp32); `keep` [Tk] (uint8 or bool): states with 0 take no part;
+        `workspace` (uint8) is allocated here with torch if None."""
+        s = self._shape(q, k, v, out)
+        _f32("lse", lse, q.shape[:2], q.device)
+        ws = self._workspace(s, 0, workspace, q.device)
+        uvu_attn_fwd(ctypes.byref(s), _at(self.q_offsets), _at(self.k_offsets), self._keep(keep, k), _at(q), _at(k), _at(v),
+                     _at(out), _at(lse), _at(ws), ws.numel(), _raw_stream(stream))
+
+    def bwd(self, q, k, v, out, lse, d_out, dq=None, dk=None, dv=None, keep=None, workspace=None, stream=None):
+        """VJP (see uvu_attn_bwd): dq, dk, dv contiguous; dq, or dk and dv, may be None."""
+        s = self._shape(q, k, v, out)
+        _f32("lse", lse, q.shape[:2], q.device)
+        if d_out.shape != out.shape or d_out.stride() != out.stride():
+            raise ValueError("d_out must have the shape and strides of out")
+        for name, t, like in (("d_out", d_out, None), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+            if t is not None:
+                _same(name, t, q, None if like is None else like.shape)
+        ws = self._workspace(s, 1, workspace, q.device)
+        uvu_attn_bwd(ctypes.byref(s), _at(self.q_offsets), _at(self.k_offsets), self._keep(keep, k), _at(q), _at(k), _at(v),
+                     _at(out), _at(lse), _at(d_out), _at(dq), _at(dk), _at(dv), _at(ws), ws.numel(), _raw_stream(stream))

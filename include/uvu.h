@@ -58,7 +58,8 @@ extern "C" {
 typedef struct uvu_plan_s *uvu_plan_t;
 typedef struct CUstream_st *uvu_stream_t; /* same handle as cudaStream_t */
 
-typedef enum { UVU_F32 = 0, UVU_F64 = 1 } uvu_dtype;
+/* Plans take UVU_F32 and UVU_F64; the node-update operators take UVU_F32, UVU_BF16 and UVU_F16. */
+typedef enum { UVU_F32 = 0, UVU_F64 = 1, UVU_BF16 = 2, UVU_F16 = 3 } uvu_dtype;
 
 typedef enum {
     UVU_OK = 0,
@@ -483,6 +484,107 @@ uvu_status uvu_radial_hidden_bwd_workspace(uvu_plan_t plan, int64_t n_edges, int
  * if it is not yet (this fixes the plan's hidden width, as a first uvu_conv_fwd_radial does).
  * The strings stay valid for the plan's lifetime. */
 uvu_status uvu_radial_module_source(uvu_plan_t plan, int hidden, const char **source, const char **log);
+
+/* ---------------------------------------------------------------- node-update operators ---- */
+
+/* What follows a convolution in a model: group norm with an activation, attention of a graph's
+ * nodes to another set of states, dropout with a residual.  They need no plan.
+ *
+ * Packed batches: the rows of the graphs lie back to back, and graph b has the rows
+ * offsets[b] .. offsets[b+1] (int32, n_graphs + 1 entries, monotone, offsets[0] = 0 and the last
+ * entry the number of rows; trusted like a CSR).  Graphs may be empty.  One graph of n rows is the
+ * batch offsets = {0, n}.
+ * Types: tensors of UVU_F32, UVU_BF16 or UVU_F16 (UVU_ERR_UNSUPPORTED for UVU_F64), aligned to their
+ * element; 16-byte aligned tensors whose rows begin on 16-byte boundaries are read in 16-byte
+ * vectors.  Statistics, sums and parameters are fp32, and results are rounded once.
+ * Results do not depend on timing: no sum is formed by atomics. */
+
+typedef enum { UVU_ACT_NONE = 0, UVU_ACT_SILU = 1 } uvu_act;
+
+/* Group norm with an activation, channels last, over a packed batch: with m = n_b channels / groups
+ * values of graph b and group g (its consecutive channels),
+ *     mean = sum x / m,   rstd = (sum (x - mean)^2 / m + eps)^(-1/2),
+ *     y = act((x - mean) rstd gamma + beta),    UVU_ACT_SILU: act(z) = z / (1 + exp(-z)).
+ * x, y [n_rows][channels] contiguous; gamma, beta [channels] fp32; mean, rstd [n_graphs][groups]
+ * fp32, written for the backward (an empty graph: mean 0, rstd eps^(-1/2)).  channels is a multiple
+ * of groups and at most 8192; eps > 0 or 0 with no constant group.  max_rows: no graph has more
+ * rows (the choice of kernel goes by it; n_rows is always right, a smaller value than the longest
+ * graph's costs time, not correctness).  y must not overlap x.  `workspace`: device memory of at
+ * least uvu_group_norm_workspace() bytes, 16-byte aligned. */
+uvu_status uvu_group_norm_fwd(uvu_dtype dtype, int64_t n_rows, int n_graphs, int64_t max_rows, int channels, int groups,
+                              uvu_act act, double eps, const int32_t *offsets, const void *x, const float *gamma,
+                              const float *beta, void *y, float *mean, float *rstd, void *workspace,
+                              size_t workspace_bytes, uvu_stream_t stream);
+
+/* VJP of uvu_group_norm_fwd for the cotangent dy [n_rows][channels]: dx (like x), dgamma, dbeta
+ * [channels] fp32, all overwritten.  mean and rstd as the forward wrote them.  dgamma and dbeta are
+ * sums over all rows, in a fixed order.  n_rows == 0 sets them to zero. */
+uvu_status uvu_group_norm_bwd(uvu_dtype dtype, int64_t n_rows, int n_graphs, int64_t max_rows, int channels, int groups,
+                              uvu_act act, const int32_t *offsets, const void *x, const float *gamma, const float *beta,
+                              const float *mean, const float *rstd, const void *dy, void *dx, float *dgamma, float *dbeta,
+                              void *workspace, size_t workspace_bytes, uvu_stream_t stream);
+
+/* Bytes of device workspace of uvu_group_norm_fwd and _bwd (either pointer may be NULL). */
+uvu_status uvu_group_norm_workspace(uvu_dtype dtype, int64_t n_rows, int n_graphs, int64_t max_rows, int channels,
+                                    int groups, size_t *fwd_bytes, size_t *bwd_bytes);
+
+/* Dropout with an optional residual; the mask is a function of (seed, offset) and never stored:
+ *     y[e] = residual[e] + (keep(e / inner) ? x[e] S : 0),    T = round(65536 p), S = 65536 / (65536 - T)
+ * for the n_draws * inner values e.  keep(d) holds when half-word d % 8 (of each word, the low half
+ * first) of the Philox4x32-10 block with counter offset + d / 8 (64 bits, the upper counter words
+ * zero) and key seed is >= T: p is met to 2^-17, and S is exact for the probability that T stands
+ * for.  The values that share a draw are consecutive: inner = 1 for scalars, the row length of a
+ * channel for an equivariant feature [N][U][D], whose channels are then kept or dropped whole.
+ * A call uses the counters offset .. offset + ceil(n_draws / 8) - 1; calls with disjoint counters
+ * draw independently.  0 <= p <= 1 (T = 65536: nothing is kept and S is not used).  residual may be
+ * NULL; y may be x or residual.  Dropped values of x are not used, whatever they are.
+ * Launches: 1 kernel. */
+uvu_status uvu_dropout_fwd(uvu_dtype dtype, int64_t n_draws, int inner, double p, uint64_t seed, uint64_t offset,
+                           const void *x, const void *residual, void *y, uvu_stream_t stream);
+
+/* VJP of uvu_dropout_fwd: dx[e] = keep(e / inner) ? dy[e] S : 0, the mask drawn again from the same
+ * (seed, offset).  The residual's gradient is dy itself.  dx may be dy.  Launches: 1 kernel. */
+uvu_status uvu_dropout_bwd(uvu_dtype dtype, int64_t n_draws, int inner, double p, uint64_t seed, uint64_t offset,
+                           const void *dy, void *dx, uvu_stream_t stream);
+
+/* Attention of the rows of each graph to that graph's states (a packed batch on both sides, of
+ * different lengths): for head h, its kv head h / (q_heads / kv_heads), and the kept states j,
+ *     S_ij = scale q_i . k_j,  lse_i = log sum_j exp(S_ij),  out_i = sum_j exp(S_ij - lse_i) v_j.
+ * q, out [n_q][q_heads][head_dim], k, v [n_k][kv_heads][head_dim], each with a row and a head stride
+ * in elements (the head_dim values of a head are consecutive; a stride may be any value for an
+ * input, zero included; the rows and heads of out must not overlap).  lse [n_q][q_heads] fp32.
+ * head_dim is 1 .. 128; q_heads is a multiple of kv_heads.  max_q, max_k: no graph has more rows or
+ * states (the split of the work goes by them; wrong values cost time, not correctness).
+ * k_keep [n_k] bytes, or NULL: states with 0 take no part, whatever their k and v hold.  A row
+ * without a kept state gets out = 0 and lse = -inf. */
+typedef struct {
+    uvu_dtype dtype;
+    int32_t n_graphs;
+    int64_t n_q, n_k;
+    int64_t max_q, max_k;
+    int32_t q_heads, kv_heads, head_dim;
+    int32_t reserved; /* 0 */
+    double scale;
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head;
+} uvu_attn_shape;
+
+/* `workspace`: device memory of at least uvu_attn_workspace() bytes, 16-byte aligned. */
+uvu_status uvu_attn_fwd(const uvu_attn_shape *shape, const int32_t *q_offsets, const int32_t *k_offsets,
+                        const uint8_t *k_keep, const void *q, const void *k, const void *v, void *out, float *lse,
+                        void *workspace, size_t workspace_bytes, uvu_stream_t stream);
+
+/* VJP of uvu_attn_fwd for the cotangent d_out (strides of out): dq [n_q][q_heads][head_dim], dk, dv
+ * [n_k][kv_heads][head_dim], contiguous, overwritten; a shared kv head's gradient is the sum over
+ * its query heads.  dq may be NULL, dk and dv may both be NULL.  out and lse as the forward wrote
+ * them.  States that are not kept and rows without a kept state get zeros. */
+uvu_status uvu_attn_bwd(const uvu_attn_shape *shape, const int32_t *q_offsets, const int32_t *k_offsets,
+                        const uint8_t *k_keep, const void *q, const void *k, const void *v, const void *out,
+                        const float *lse, const void *d_out, void *dq, void *dk, void *dv, void *workspace,
+                        size_t workspace_bytes, uvu_stream_t stream);
+
+/* Bytes of device workspace of uvu_attn_fwd and uvu_attn_bwd on the current device (either pointer
+ * may be NULL). */
+uvu_status uvu_attn_workspace(const uvu_attn_shape *shape, size_t *fwd_bytes, size_t *bwd_bytes);
 
 /* ------------------------------------------------------------------------ measurement ---- */
 
