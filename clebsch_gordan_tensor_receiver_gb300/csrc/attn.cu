@@ -360,9 +360,9 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_join(int64_t n, int splits,
 
 // Splits of the inner axis: as many as fill the card's SMs once, when there are fewer tiles than
 // SMs, but no piece shorter than four tiles.
-int splits_for(int64_t tiles, int64_t inner, int sms) {
+int splits_for(int64_t tiles, int64_t inner, int R, int sms) {
     if (tiles <= 0 || tiles >= sms) return 1;
-    const int64_t want = (sms + tiles - 1) / tiles, most = std::max<int64_t>(1, inner / (4 * kT));
+    const int64_t want = (sms + tiles - 1) / tiles, most = std::max<int64_t>(1, inner / (4 * R));
     return int(std::min<int64_t>(std::min(want, most), 64));
 }
 
@@ -370,14 +370,25 @@ int64_t row_tiles(const AttnShape& s, int R) { return s.n_q * (s.q_heads / s.kv_
 int64_t state_tiles(const AttnShape& s, int R) { return s.n_k / R + s.n_graphs; }
 
 struct Choice {
+    int nt;            // row tiles of 128 per block of the 16-bit forward; 0: CUDA cores
+    int64_t fwd_tiles;  // tile numbers of the forward
     int fwd, dq, dkv;  // splits
 };
 Choice choose(const AttnShape& s, int sms) {
     const int64_t group = s.q_heads / s.kv_heads;
     // tiles that have work, at most
-    const int64_t rt = std::min(row_tiles(s, kT), int64_t(s.n_graphs) * ((s.max_q * group + kT - 1) / kT)) * s.kv_heads;
+    const auto rows_busy = [&](int R) {
+        return std::min(row_tiles(s, R), int64_t(s.n_graphs) * ((s.max_q * group + R - 1) / R)) * s.kv_heads;
+    };
     const int64_t kt = std::min(state_tiles(s, kT), int64_t(s.n_graphs) * ((int64_t(s.max_k) + kT - 1) / kT)) * s.kv_heads;
-    return {splits_for(rt, s.max_k, sms), splits_for(rt, s.max_k, sms), splits_for(kt, s.max_q * group, sms)};
+    Choice c;
+    c.nt = s.dtype == UVU_F32 ? 0 : rows_busy(256) >= sms && s.max_q * group > 128 ? 2 : 1;
+    const int R = c.nt ? 128 * c.nt : kT;
+    c.fwd_tiles = row_tiles(s, R);
+    c.fwd = splits_for(rows_busy(R), s.max_k, c.nt ? 128 : kT, sms);
+    c.dq = splits_for(rows_busy(kT), s.max_k, kT, sms);
+    c.dkv = splits_for(kt, s.max_q * group, kT, sms);
+    return c;
 }
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
@@ -393,7 +404,6 @@ cudaError_t fwd_simple(const AttnShape& s, const AttnArgs& a, cudaStream_t st) {
     cudaError_t e = allow_smem(attn_fwd_simple<T, DP>, sm);
     if (e != cudaSuccess) return e;
     attn_fwd_simple<T, DP><<<dim3(unsigned(row_tiles(s, kT)), unsigned(a.Hkv), unsigned(a.splits)), kThreads, sm, st>>>(a);
-    if (a.splits > 1) attn_fwd_join<T><<<unsigned((a.nq * a.Hq + 7) / 8), kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -463,21 +473,22 @@ AttnArgs attn_args(const AttnShape& s, const AttnTensors& t) {
 
 cudaError_t launch_attn_fwd(const AttnShape& s, const AttnTensors& t, void* ws, int sms, cudaStream_t st) {
     AttnArgs a = attn_args(s, t);
-    a.splits = choose(s, sms).fwd;
+    const Choice c = choose(s, sms);
+    a.splits = c.fwd;
     if (a.splits > 1) {
         a.part_lse = static_cast<float*>(ws);
         a.part_o = a.part_lse + align256(size_t(a.splits) * a.nq * a.Hq * 4) / 4;
     }
-    auto go = [&](auto e) {
-        using T = decltype(e);
-        return by_dim<T>(a.D, [&](auto d) { return fwd_simple<T, decltype(d)::value>(s, a, st); });
-    };
+    cudaError_t e = c.nt ? launch_attn_fwd_mma(s.dtype, a, c.nt, c.fwd_tiles, st)
+                         : by_dim<float>(a.D, [&](auto d) { return fwd_simple<float, decltype(d)::value>(s, a, st); });
+    if (e != cudaSuccess || a.splits == 1) return e;
+    const unsigned blocks = unsigned((a.nq * a.Hq + 7) / 8);
     switch (s.dtype) {
-        case UVU_F32: return go(float{});
-        case UVU_BF16: return go(__nv_bfloat16{});
-        case UVU_F16: return go(__half{});
-        default: return cudaErrorInvalidValue;
+        case UVU_F32: attn_fwd_join<float><<<blocks, kThreads, 0, st>>>(a); break;
+        case UVU_BF16: attn_fwd_join<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a); break;
+        default: attn_fwd_join<__half><<<blocks, kThreads, 0, st>>>(a); break;
     }
+    return cudaGetLastError();
 }
 
 cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, int sms, cudaStream_t st) {

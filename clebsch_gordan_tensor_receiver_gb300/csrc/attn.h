@@ -49,4 +49,8 @@ __device__ __forceinline__ AttnTile attn_tile(const int32_t* off, int graphs, in
     return {r0 < rows ? lo : -1, r0, rows};
 }
 
+// attn_mma.cu: the forward of 16-bit operands, nt (1 or 2) row tiles of 128 per block; a.splits > 1
+// leaves partial results for the join.
+cudaError_t launch_attn_fwd_mma(uvu_dtype dtype, const AttnArgs& a, int nt, int64_t row_tiles, cudaStream_t st);
+
 }  // namespace uvu

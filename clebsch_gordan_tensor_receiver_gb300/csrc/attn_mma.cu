@@ -1,0 +1,492 @@
+// Attention on the 5th-generation tensor cores for 16-bit operands.
+//
+// Forward.  A CTA owns NT tiles of 128 packed rows (of one graph and kv head) and walks the graph's
+// states in tiles of 128.  Per state tile j and row tile t:
+//     S_t = Q_t K_j^T            (both operands in shared memory, S in tensor memory)
+//     P_t = exp2(c S_t - m)      (a thread per row reads S, keeps the running maximum m and the sum of P)
+//     O_t = O_t + P_t V_j        (P written over S in tensor memory as 16-bit values; V is used with its rows
+//                                as the summed index, straight from the layout it was loaded in)
+// The maximum that P refers to is only moved (and O_t multiplied by exp2(old - new)) when a row's new
+// maximum exceeds it by more than 2^8: P <= 256 fits both 16-bit types, and nearly all tiles leave O alone.
+//
+// Warp roles: warps 0 .. 4 NT - 1 softmax (a warpgroup per row tile), one warp that issues the matrix
+// instructions, four warps that load.  With NT = 2 the tensor cores work on one row tile while the
+// other's exponentials are formed, and K and V serve 256 rows per load.  The loaders use 16-byte
+// cp.async with zero fill instead of tensor maps: a masked or absent state is zeros in shared memory,
+// whatever memory holds there (0 * NaN would reach O), and any row and head strides work; operands off
+// the 16-byte grid go through registers.  A stage is handed on when its copies have landed, kLag
+// stages after they were issued.
+//
+// Order of the matrix instructions: ... O_0 += P_0 V_j, S_0 = Q_0 K_j+1, O_1 += P_1 V_j, S_1 = Q_1 K_j+1 ...
+// They complete in issue order, so S_t of the next tile may overwrite P_t, and a softmax thread that
+// has seen S_t(j+1) also knows that O_t(j) is complete.
+//
+// Every wait is bounded (two seconds); on expiry the roles leave their loops, the issuer waits for its
+// instructions, the loaders for their copies, and the CTA frees its tensor memory and returns with the
+// status word set.
+#include <algorithm>
+#include <cstdint>
+
+#include "attn.h"
+#include "elem.h"
+#include "tensor_core.h"
+
+namespace uvu {
+
+__device__ unsigned int attn_status_word;
+
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128;      // rows of a row tile, states of a state tile
+constexpr int kMaskRing = 8;    // state masks in flight: more than half the stages, plus two
+constexpr int kLoadWarps = 4;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The packed rows of one kv head from row r0 of a graph on: row r0 + r is query i0 + (j0 + r) / group.
+struct RowsOf {
+    const char* base;   // the graph's first row, first head
+    int64_t row, head;  // strides in bytes
+    uint32_t group;     // query heads that share the kv head (1 for states)
+    int64_t i0;
+    uint32_t j0;
+    __device__ __forceinline__ void from(int64_t r0) {
+        i0 = r0 / group;
+        j0 = uint32_t(r0 - i0 * group);
+    }
+    __device__ __forceinline__ const char* at(int r) const {
+        const uint32_t x = j0 + uint32_t(r), i = group == 1 ? x : x / group;
+        return base + (i0 + i) * row + int64_t(x - i * group) * head;
+    }
+};
+
+// 128 rows of an operand to the tile at `dst` (shared memory); rows that `use` refuses and columns
+// from D on are zeros.  128 threads, consecutive threads on consecutive chunks.
+template <typename T, bool ALIGNED, typename Use>
+__device__ __forceinline__ void load_rows(uint32_t dst, const RowsOf& x, int D, int chunks, int lanes_log2, int t, Use use) {
+    const int c = t & ((1 << lanes_log2) - 1);
+    if (c >= chunks) return;
+    const uint32_t bytes = uint32_t(min(max(D - 8 * c, 0), 8)) * 2;
+    for (int r = t >> lanes_log2; r < kRows; r += 128 >> lanes_log2) {
+        const bool on = use(r) && bytes > 0;
+        const char* src = on ? x.at(r) + c * 16 : x.base;
+        const uint32_t to = dst + tile_offset(r, c);
+        if constexpr (ALIGNED) {
+            copy16(to, src, on ? bytes : 0);
+        } else {
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (on) {
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(src);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (2 * i < bytes) w[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
+        }
+    }
+}
+
+// Copies are handed on a fixed number of groups after they were issued: the group issued `lag`
+// groups ago has landed.
+template <int LAG>
+struct Lagged {
+    int issued = 0;
+    template <typename Arrive>
+    __device__ __forceinline__ void commit(Arrive arrive) {
+        copy_commit();
+        if (++issued > LAG) {
+            copy_wait<LAG>();
+            fence_async();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) arrive(issued - 1 - LAG);
+        }
+    }
+    template <typename Arrive>
+    __device__ __forceinline__ void drain(Arrive arrive) {
+        copy_wait<0>();
+        fence_async();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            for (int i = max(0, issued - LAG); i < issued; ++i) arrive(i);
+    }
+};
+
+__device__ __forceinline__ uint32_t tail_word(int64_t left, int w) {  // bits of the states that exist
+    const int64_t n = left - 32 * w;
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << uint32_t(n)) - 1u;
+}
+
+// Which of a tile's 128 states take part, as four words in every lane of a loader warp.  The mask
+// bytes of the next tile are fetched a tile ahead.
+struct StateMask {
+    const uint8_t* keep;  // of the graph, or null
+    int64_t at, hi;       // first state of the coming tile, end
+    uint32_t word[4], ahead;
+    __device__ __forceinline__ StateMask(const uint8_t* k, int64_t lo, int64_t end) : keep(k), at(lo), hi(end), ahead(0) { fetch(); }
+    __device__ __forceinline__ void fetch() {
+        if (!keep) return;
+        ahead = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int64_t s = at + 32 * w + (threadIdx.x & 31);
+            if (s < hi && keep[s]) ahead |= 1u << w;
+        }
+    }
+    __device__ __forceinline__ void next() {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) word[w] = keep ? __ballot_sync(0xffffffffu, (ahead >> w) & 1) : tail_word(hi - at, w);
+        at += kRows;
+        fetch();
+    }
+    __device__ __forceinline__ bool has(int r) const {
+        const uint32_t w = r < 64 ? (r < 32 ? word[0] : word[1]) : (r < 96 ? word[2] : word[3]);
+        return (w >> (r & 31)) & 1;
+    }
+};
+
+struct Piece {
+    int64_t lo, hi;
+};
+__device__ __forceinline__ Piece piece_of(int64_t n, int s, int splits) {
+    const int64_t tiles = (n + kRows - 1) / kRows, per = (tiles + splits - 1) / splits;
+    return {min(n, s * per * kRows), min(n, (s + 1) * per * kRows)};
+}
+
+// Shared memory of the forward: NT row tiles of Q, the ring of K and V tiles, masks, barriers.
+template <int NT>
+struct FwdLayout {
+    int panels, stages;
+    __host__ __device__ int tile() const { return panels * kPanelBytes; }
+    __host__ __device__ int ring() const { return NT * tile(); }
+    __host__ __device__ int masks() const { return ring() + stages * tile(); }
+    __host__ __device__ int bars() const { return masks() + kMaskRing * 16; }
+    __host__ __device__ int total() const { return bars() + 256 + 1024; }  // + alignment slack
+};
+
+template <typename T, int NT, int LAG, bool ALIGNED>
+__global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 1) attn_fwd_mma(AttnArgs a, FwdLayout<NT> L) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ int s_dead;
+    __shared__ uint32_t s_tmem;
+    const AttnTile tl = attn_tile(a.q_off, a.graphs, a.group, kRows * NT, blockIdx.x);
+    if (tl.graph < 0) return;
+    const int h = blockIdx.y, split = blockIdx.z;
+    const int64_t q0 = a.q_off[tl.graph], k0 = a.k_off[tl.graph];
+    const Piece kr = piece_of(a.k_off[tl.graph + 1] - k0, split, a.splits);
+    const int n_tiles = int((kr.hi - kr.lo + kRows - 1) / kRows);
+    const int n_rows = int(min(tl.rows - tl.row0, int64_t(kRows * NT)));
+    const int nt = NT == 2 && n_rows > kRows ? 2 : 1;  // row tiles in use
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int d16 = (a.D + 15) / 16;
+    const uint32_t q_full = sb + L.bars(), s_full = q_full + 8, p_full = s_full + 16, o_full = p_full + 16, full = o_full + 16,
+                   empty = full + 8 * L.stages, m_full = empty + 8 * L.stages, fin = m_full + 8 * kMaskRing;
+    const uint32_t o_cols = uint32_t(64 * L.panels);
+    const uint32_t tmem_cols = NT == 2 ? 512 : 256;
+    if (threadIdx.x == 0) {
+        s_dead = 0;
+        bar_init(q_full, kLoadWarps);
+        for (int t = 0; t < 2; ++t) {
+            bar_init(s_full + 8 * t, 1);
+            bar_init(p_full + 8 * t, 4);
+            bar_init(o_full + 8 * t, 1);
+        }
+        for (int s = 0; s < L.stages; ++s) {
+            bar_init(full + 8 * s, kLoadWarps);
+            bar_init(empty + 8 * s, 1);
+        }
+        for (int s = 0; s < kMaskRing; ++s) bar_init(m_full + 8 * s, 1);
+        bar_init(fin, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 4 * NT) tmem_alloc(smem_u32(&s_tmem), tmem_cols);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
+    volatile int* dead = &s_dead;
+    unsigned* status = &attn_status_word;
+    const uint32_t* masks = reinterpret_cast<const uint32_t*>(smem + L.masks());
+
+    if (warp < 4 * NT) {
+        // ------------------------------------------------------------------------ softmax
+        const int t = warp >> 2, quad = warp & 3;
+        const int row = t * kRows + quad * 32 + lane;
+        const bool work = t * kRows + quad * 32 < n_rows;  // the warp has rows
+        const uint32_t lanes = uint32_t(quad * 32) << 16;
+        const uint32_t s_at = tmem + uint32_t(t * kRows) + lanes, o_at = tmem + uint32_t(NT * kRows) + uint32_t(t) * o_cols + lanes;
+        const float c = a.scale_log2;
+        float m = -INFINITY, l = 0.f;  // reference maximum in units of c S, and the sum of P
+        bool ok = true;
+        if (t < nt) {
+            for (int j = 0; j < n_tiles; ++j) {
+                uint32_t word[4];
+                if (a.keep) {
+                    ok = __all_sync(0xffffffffu, bar_wait(m_full + 8 * (j % kMaskRing), (j / kMaskRing) & 1, dead, status));
+                    if (!ok) break;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) word[w] = masks[(j % kMaskRing) * 4 + w];
+                } else {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) word[w] = tail_word(kr.hi - kr.lo - int64_t(j) * kRows, w);
+                }
+                ok = __all_sync(0xffffffffu, bar_wait(s_full + 8 * t, j & 1, dead, status));
+                if (!ok) break;
+                fence_after();
+                if (work) {
+                    float x[2][32];
+                    float top = -INFINITY;
+                    tmem_ld32(s_at, x[0]);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        float(&v)[32] = x[b & 1];
+                        tmem_wait_ld(v);
+                        tmem_ld32(s_at + 32 * ((b + 1) & 3), x[(b + 1) & 1]);
+                        if (word[b] == 0xffffffffu) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if ((word[b] >> i) & 1) top = fmaxf(top, v[i]);
+                        }
+                    }
+                    top *= c;
+                    const bool move = top > m + 8.f;
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float to = move ? top : m;
+                        if (j > 0) {
+                            const float f = move ? exp2_approx(m - to) : 1.f;
+                            l *= f;
+                            for (int d = 0; d < d16; ++d) {
+                                float o[16];
+                                tmem_ld16(o_at + 16 * d, o);
+                                tmem_wait_ld(o);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] *= f;
+                                tmem_st16(o_at + 16 * d, o);
+                            }
+                        }
+                        m = to;
+                    }
+                    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        float(&v)[32] = x[b & 1];
+                        tmem_wait_ld(v);
+                        if (b < 3) tmem_ld32(s_at + 32 * (b + 1), x[(b + 1) & 1]);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = exp2_approx(fmaf(v[i], c, -base));
+                        if (word[b] != 0xffffffffu) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((word[b] >> i) & 1)) v[i] = 0.f;
+                        }
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) sum[i & 3] += v[i];
+                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) p[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+                        tmem_st16(s_at + 16 * b, p);
+                    }
+                    tmem_wait_st();
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(p_full + 8 * t);
+            }
+            if (ok && n_tiles > 0) {
+                ok = __all_sync(0xffffffffu, bar_wait(o_full + 8 * t, 0, dead, status));
+                fence_after();
+            }
+            if (ok && work) {
+                const bool valid = row < n_rows;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const int64_t p = tl.row0 + row;
+                const int64_t r = q0 + p / a.group, head = int64_t(h) * a.group + p % a.group;
+                const int64_t rh = (int64_t(split) * a.nq + r) * a.Hq + head;
+                if (valid) (a.splits > 1 ? a.part_lse[rh] : a.lse[r * a.Hq + head]) = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                T* out = static_cast<T*>(a.out) + r * a.o_row + head * a.o_head;
+                const bool vec = ((reinterpret_cast<uintptr_t>(a.out) | uintptr_t(a.o_row * 2) | uintptr_t(a.o_head * 2)) & 15u) == 0;
+                for (int d = 0; d < d16; ++d) {
+                    float o[16];
+                    __syncwarp();
+                    if (n_tiles > 0) {
+                        tmem_ld16(o_at + 16 * d, o);
+                        tmem_wait_ld(o);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
+                    if (!valid) {
+                        // a row past the end: read with its warp, stored nowhere
+                    } else if (a.splits > 1) {
+                        float* po = a.part_o + rh * a.D + 16 * d;
+                        if (a.D % 4 == 0) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (16 * d + 4 * i < a.D)
+                                    *reinterpret_cast<float4*>(po + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (16 * d + i < a.D) po[i] = o[i];
+                        }
+                    } else if (vec && a.D % 8 == 0) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (16 * d + 8 * i < a.D)
+                                *reinterpret_cast<uint4*>(out + 16 * d + 8 * i) =
+                                    make_uint4(pack2<T>(o[8 * i], o[8 * i + 1]), pack2<T>(o[8 * i + 2], o[8 * i + 3]),
+                                               pack2<T>(o[8 * i + 4], o[8 * i + 5]), pack2<T>(o[8 * i + 6], o[8 * i + 7]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (16 * d + i < a.D) out[16 * d + i] = narrow<T>(o[i]);
+                    }
+                }
+            }
+        }
+    } else if (warp == 4 * NT) {
+        // ----------------------------------------------------------------- matrix instructions
+        if (lane == 0) {
+            const uint32_t id_s = mma_desc<T>(kRows, false), id_o = mma_desc<T>(16 * d16, true);
+            auto stage = [&](int i) { return sb + uint32_t(L.ring() + (i % L.stages) * L.tile()); };
+            auto wait_stage = [&](int i) { return bar_wait(full + 8 * (i % L.stages), (i / L.stages) & 1, dead, status); };
+            auto scores = [&](int t, int j) {
+                const uint32_t q = sb + uint32_t(t * L.tile()), k = stage(2 * j);
+                for (int s = 0; s < d16; ++s) mma_ss(tmem + uint32_t(t * kRows), desc_cols(q, s), desc_cols(k, s), id_s, s > 0);
+                mma_commit(s_full + 8 * t);
+            };
+            bool ok = n_tiles > 0 && bar_wait(q_full, 0, dead, status) && wait_stage(0);
+            if (ok) {
+                fence_after();
+                for (int t = 0; t < nt; ++t) scores(t, 0);
+                mma_commit(empty + 8 * 0);
+            }
+            for (int j = 0; j < n_tiles && ok; ++j) {
+                ok = wait_stage(2 * j + 1);
+                for (int t = 0; t < nt && ok; ++t) {
+                    ok = bar_wait(p_full + 8 * t, j & 1, dead, status);
+                    if (!ok) break;
+                    fence_after();
+                    const uint32_t o = tmem + uint32_t(NT * kRows) + uint32_t(t) * o_cols, v = stage(2 * j + 1);
+#pragma unroll
+                    for (int s = 0; s < kRows / 16; ++s)
+                        mma_ts(o, tmem + uint32_t(t * kRows + 8 * s), desc_rows(v, s), id_o, j > 0 || s > 0);
+                    if (j + 1 < n_tiles) {
+                        if (t == 0) {
+                            ok = wait_stage(2 * j + 2);
+                            if (!ok) break;
+                            fence_after();
+                        }
+                        scores(t, j + 1);
+                    } else {
+                        mma_commit(o_full + 8 * t);
+                    }
+                }
+                if (!ok) break;
+                mma_commit(empty + 8 * ((2 * j + 1) % L.stages));
+                if (j + 1 < n_tiles) mma_commit(empty + 8 * ((2 * j + 2) % L.stages));
+            }
+            // every instruction issued has finished before the tensor memory and the stages go
+            mma_commit(fin);
+            bar_wait_last(fin, 0, status);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------------- loaders
+        const int t = threadIdx.x - (4 * NT + 1) * 32;
+        const int chunks = 2 * d16;
+        int lanes_log2 = 1;
+        while ((1 << lanes_log2) < chunks) ++lanes_log2;
+        if (n_tiles > 0) {
+            RowsOf Q{reinterpret_cast<const char*>(static_cast<const T*>(a.q) + q0 * a.q_row + int64_t(h) * a.group * a.q_head),
+                     a.q_row * 2, a.q_head * 2, uint32_t(a.group), 0, 0};
+            RowsOf K{reinterpret_cast<const char*>(static_cast<const T*>(a.k) + k0 * a.k_row + h * a.k_head), a.k_row * 2, 0, 1, 0, 0};
+            RowsOf V{reinterpret_cast<const char*>(static_cast<const T*>(a.v) + k0 * a.v_row + h * a.v_head), a.v_row * 2, 0, 1, 0, 0};
+            // group 0 is Q, group 1 + i is stage i of the ring's sequence K_0 V_0 K_1 V_1 ...
+            auto arrive = [&](int g) { bar_arrive(g == 0 ? q_full : full + 8 * ((g - 1) % L.stages)); };
+            Lagged<LAG> copies;
+            for (int i = 0; i < nt; ++i) {
+                Q.from(tl.row0 + i * kRows);
+                load_rows<T, ALIGNED>(sb + uint32_t(i * L.tile()), Q, a.D, chunks, lanes_log2, t,
+                                      [&](int r) { return i * kRows + r < n_rows; });
+            }
+            copies.commit(arrive);
+            StateMask mask(a.keep ? a.keep + k0 : nullptr, kr.lo, kr.hi);
+            for (int j = 0; j < n_tiles; ++j) {
+                bool ok = true;
+                for (int half = 0; half < 2 && ok; ++half) {
+                    const int i = 2 * j + half;
+                    if (i >= L.stages) ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * (i % L.stages), (i / L.stages - 1) & 1, dead, status));
+                    if (!ok) break;
+                    if (half == 0) {
+                        mask.next();
+                        if (a.keep && warp == 4 * NT + 1 && lane == 0) {
+                            *reinterpret_cast<uint4*>(smem + L.masks() + (j % kMaskRing) * 16) =
+                                make_uint4(mask.word[0], mask.word[1], mask.word[2], mask.word[3]);
+                            bar_arrive(m_full + 8 * (j % kMaskRing));
+                        }
+                    }
+                    RowsOf& X = half ? V : K;
+                    X.i0 = kr.lo + int64_t(j) * kRows;
+                    load_rows<T, ALIGNED>(sb + uint32_t(L.ring() + (i % L.stages) * L.tile()), X, a.D, chunks, lanes_log2, t,
+                                          [&](int r) { return mask.has(r); });
+                    copies.commit(arrive);
+                }
+                if (!ok) break;
+            }
+            copies.drain(arrive);
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 4 * NT) {
+        fence_after();
+        tmem_free(tmem, tmem_cols);
+    }
+}
+
+constexpr int kLag = 3;  // stages >= kLag + 2: the issuer holds a V and the next K at once
+
+template <typename T, int NT, bool ALIGNED>
+cudaError_t fwd(const AttnArgs& a, int64_t row_tiles, cudaStream_t st) {
+    FwdLayout<NT> L;
+    L.panels = a.D > 64 ? 2 : 1;
+    // one panel: 96 KB, two CTAs per SM (NT = 1), or 160 KB; two panels: 224 KB
+    L.stages = NT == 1 ? (L.panels == 1 ? 5 : 6) : (L.panels == 1 ? 8 : 5);
+    auto k = attn_fwd_mma<T, NT, kLag, ALIGNED>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total());
+    if (e != cudaSuccess) return e;
+    k<<<dim3(unsigned(row_tiles), unsigned(a.Hkv), unsigned(a.splits)), (4 * NT + 1 + kLoadWarps) * 32, L.total(), st>>>(a, L);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t fwd_of(const AttnArgs& a, int nt, int64_t row_tiles, cudaStream_t st) {
+    const uintptr_t any = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                          uintptr_t(a.q_row | a.q_head | a.k_row | a.k_head | a.v_row | a.v_head) * 2;
+    if (any & 15u) return nt == 2 ? fwd<T, 2, false>(a, row_tiles, st) : fwd<T, 1, false>(a, row_tiles, st);
+    return nt == 2 ? fwd<T, 2, true>(a, row_tiles, st) : fwd<T, 1, true>(a, row_tiles, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_fwd_mma(uvu_dtype dtype, const AttnArgs& a, int nt, int64_t row_tiles, cudaStream_t st) {
+    return dtype == UVU_BF16 ? fwd_of<__nv_bfloat16>(a, nt, row_tiles, st) : fwd_of<__half>(a, nt, row_tiles, st);
+}
+
+// Status of the tensor-core attention kernels on the current device (bit 0: a bounded wait gave up).
+cudaError_t attn_status(unsigned* word, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(word, attn_status_word, sizeof(unsigned));
+    if (e != cudaSuccess || !reset) return e;
+    const unsigned z = 0;
+    return cudaMemcpyToSymbol(attn_status_word, &z, sizeof(unsigned));
+}
+
+}  // namespace uvu

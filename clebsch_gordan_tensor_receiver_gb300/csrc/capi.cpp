@@ -1105,7 +1105,10 @@ uvu_status attn_check(const uvu_attn_shape* s) {
         return fail(UVU_ERR_INVALID_ARGUMENT, "q_heads must be a multiple of kv_heads, both in [1, 65535]");
     if (s->head_dim < 1) return fail(UVU_ERR_INVALID_ARGUMENT, "head_dim must be >= 1");
     if (s->head_dim > 128) return fail(UVU_ERR_UNSUPPORTED, "head_dim must be <= 128");
-    if (!std::isfinite(s->scale)) return fail(UVU_ERR_INVALID_ARGUMENT, "scale must be finite");
+    const float sc = float(s->scale * 1.4426950408889634);
+    if (!(sc >= std::numeric_limits<float>::min()) || !std::isfinite(sc))
+        return fail(UVU_ERR_INVALID_ARGUMENT, "scale must be positive and a normal fp32 value");
+    if (s->n_q * s->q_heads >= (int64_t(1) << 38)) return fail(UVU_ERR_INVALID_ARGUMENT, "n_q * q_heads must be < 2^38");
     if (s->reserved != 0) return fail(UVU_ERR_INVALID_ARGUMENT, "reserved must be 0");
     for (int64_t v : {s->q_row, s->q_head, s->k_row, s->k_head, s->v_row, s->v_head, s->o_row, s->o_head})
         if (v < 0 || v > (int64_t(1) << 40)) return fail(UVU_ERR_INVALID_ARGUMENT, "strides must be in [0, 2^40]");
@@ -1199,6 +1202,14 @@ extern "C" uvu_status uvu_dropout_bwd(uvu_dtype dtype, int64_t n_draws, int inne
                                       const void* dy, void* dx, uvu_stream_t stream) {
     UVU_RANGE("uvu_dropout_bwd");
     return dropout_call("dropout gradient launch", dtype, n_draws, inner, p, seed, offset, dy, "dy", nullptr, dx, "dx", stream);
+}
+
+extern "C" uvu_status uvu_attn_device_status(unsigned* word, int reset) {
+    UVU_RANGE("uvu_attn_device_status");
+    if (!word) return fail(UVU_ERR_INVALID_ARGUMENT, "word is NULL");
+    cudaError_t e = attn_status(word, reset != 0);
+    if (e != cudaSuccess) return cuda_fail(e, "attention status");
+    return ok();
 }
 
 extern "C" uvu_status uvu_attn_workspace(const uvu_attn_shape* shape, size_t* fwd_bytes, size_t* bwd_bytes) {

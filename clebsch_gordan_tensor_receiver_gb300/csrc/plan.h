@@ -218,4 +218,5 @@ struct AttnTensors {
 void attn_workspace(const AttnShape& s, int sms, size_t* fwd, size_t* bwd);
 cudaError_t launch_attn_fwd(const AttnShape& s, const AttnTensors& t, void* ws, int sms, cudaStream_t st);
 cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, int sms, cudaStream_t st);
+cudaError_t attn_status(unsigned* word, bool reset);
 }  // namespace uvu

@@ -1,0 +1,209 @@
+// Device helpers of the attention kernels: barriers with bounded waits, asynchronous copies, tensor
+// memory and the 16-bit matrix instruction (tcgen05, kind::f16).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+namespace uvu {
+namespace tc {
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
+
+// ---------------------------------------------------------------------------------- barriers
+
+__device__ __forceinline__ void bar_init(uint32_t b, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
+}
+__device__ __forceinline__ bool bar_test(uint32_t b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(b), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ unsigned long long timer_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// Waits for the phase of `parity` to end.  False when another role has given up (*dead) or after
+// about two seconds, which sets *dead and the status word; the caller then leaves its loop.
+__device__ __noinline__ bool bar_wait_slow(uint32_t b, uint32_t parity, volatile int* dead, unsigned* status) {
+    const unsigned long long t0 = timer_ns();
+    for (;;) {
+        for (int i = 0; i < 32; ++i)
+            if (bar_test(b, parity)) return true;
+        if (*dead) return false;
+        if (timer_ns() - t0 > 2000000000ull) {
+            *dead = 1;
+            atomicOr(status, 1u);
+            return false;
+        }
+    }
+}
+// The last wait before a role returns what others still use: bounded, whatever *dead says.
+__device__ __noinline__ void bar_wait_last(uint32_t b, uint32_t parity, unsigned* status) {
+    const unsigned long long t0 = timer_ns();
+    while (!bar_test(b, parity))
+        if (timer_ns() - t0 > 2000000000ull) {
+            atomicOr(status, 1u);
+            return;
+        }
+}
+__device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity, volatile int* dead, unsigned* status) {
+    return bar_test(b, parity) || bar_wait_slow(b, parity, dead, status);
+}
+
+// ------------------------------------------------------------------------------------- copies
+
+// 16 bytes to shared memory, of which the first `bytes` are read and the others are zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Shared memory written by this thread's ordinary or cp.async stores becomes visible to the matrix instructions.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// --------------------------------------------------------------------------- operand tiles
+
+// An operand tile is [rows][64 columns] panels of 16-bit values: 128 bytes a row, groups of 8 rows
+// (1024 bytes), the 16-byte chunk index XORed with the row within its group (128-byte swizzle).
+// One panel of 128 rows is 16 KB; wider tiles are panels one after the other.
+constexpr int kPanelBytes = 16384;
+__device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {  // chunk: 8 columns
+    return uint32_t((chunk >> 3) * kPanelBytes + (row >> 3) * 1024 + (row & 7) * 128 + (((chunk ^ row) & 7) << 4));
+}
+
+constexpr uint64_t kDescBase = (1ull << 46) | (2ull << 61);  // version bits, 128-byte swizzle
+// The tile's columns are the summed index (16 of them, beginning at column 16 k): 8-row groups are 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_cols(uint32_t tile, int k) {
+    const uint32_t a = tile + uint32_t((k >> 2) * kPanelBytes + (k & 3) * 32);
+    return uint64_t((a >> 4) & 0x3FFFu) | (1ull << 16) | (uint64_t(1024 >> 4) << 32) | kDescBase;
+}
+// The tile's rows are the summed index (16 of them, beginning at row 16 k): panels of 64 columns are
+// kPanelBytes apart, groups of 8 rows 1024 bytes.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t tile, int k) {
+    const uint32_t a = tile + uint32_t(k * 2048);
+    return uint64_t((a >> 4) & 0x3FFFu) | (uint64_t(kPanelBytes >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | kDescBase;
+}
+
+// Instruction descriptor of kind::f16 with fp32 sums: M = 128, N = n; B's rows (true) or columns are the summed index.
+template <typename T>
+__device__ __forceinline__ uint32_t mma_desc(int n, bool b_rows) {
+    constexpr uint32_t type = sizeof(T) == 2 && __is_same(T, __nv_bfloat16) ? 1u : 0u;
+    return (1u << 4) | (type << 7) | (type << 10) | (uint32_t(b_rows) << 16) | (uint32_t(n >> 3) << 17) | (8u << 24);
+}
+
+// ------------------------------------------------------------------------------- tensor cores
+
+// D (tensor memory) = [D +] A B, A from shared memory (SS) or tensor memory (TS).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(uint32_t(add)), "r"(id)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(uint32_t(add)), "r"(id)
+        : "memory");
+}
+// The barrier gets an arrival when all matrix instructions issued so far are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// The loads into r are done.  The registers pass through the wait, so that no use can be moved before it.
+__device__ __forceinline__ void tmem_wait_ld(float (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]),
+                   "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])::"memory");
+    asm volatile("" : "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+                      "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
+                 ::"memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(float (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]),
+                   "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])::"memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of the warp's 32 lanes (lane = row), as fp32.
+__device__ __forceinline__ void tmem_ld32(uint32_t a, float (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t a, float (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const float (&r)[16]) {
+    uint32_t u[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(r[i]);
+    tmem_st16(a, u);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Two values rounded to 16 bits, `lo` in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+}  // namespace tc
+}  // namespace uvu

@@ -40,7 +40,7 @@ EXPORTS = (
     "uvu_radial_weights", "uvu_radial_weights_workspace", "uvu_radial_weights_bwd", "uvu_radial_weights_bwd_workspace",
     "uvu_radial_hidden_bwd", "uvu_radial_hidden_bwd_workspace",
     "uvu_group_norm_fwd", "uvu_group_norm_bwd", "uvu_group_norm_workspace", "uvu_dropout_fwd", "uvu_dropout_bwd",
-    "uvu_attn_fwd", "uvu_attn_bwd", "uvu_attn_workspace",
+    "uvu_attn_fwd", "uvu_attn_bwd", "uvu_attn_workspace", "uvu_attn_device_status",
     "uvu_fma_rate_probe", "uvu_status_string", "uvu_last_error_message",
 )
 
@@ -115,6 +115,7 @@ def _load():
         "uvu_dropout_bwd": [I, I64, I, ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64, P, P, P],
         "uvu_attn_fwd": [ctypes.POINTER(AttnShape)] + [P] * 9 + [SZ, P],
         "uvu_attn_bwd": [ctypes.POINTER(AttnShape)] + [P] * 13 + [SZ, P],
+        "uvu_attn_device_status": [ctypes.POINTER(ctypes.c_uint), I],
         "uvu_attn_workspace": [ctypes.POINTER(AttnShape), ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
     }
     for name, args in sig.items():
@@ -159,7 +160,7 @@ for _n in ("uvu_plan_destroy", "uvu_plan_info", "uvu_plan_cg", "uvu_plan_source"
            "uvu_radial_weights", "uvu_radial_weights_workspace", "uvu_radial_weights_bwd",
            "uvu_radial_weights_bwd_workspace", "uvu_radial_hidden_bwd", "uvu_radial_hidden_bwd_workspace",
            "uvu_group_norm_fwd", "uvu_group_norm_bwd", "uvu_group_norm_workspace", "uvu_dropout_fwd", "uvu_dropout_bwd",
-           "uvu_attn_fwd", "uvu_attn_bwd", "uvu_attn_workspace"):
+           "uvu_attn_fwd", "uvu_attn_bwd", "uvu_attn_workspace", "uvu_attn_device_status"):
     globals()[_n] = _wrap(_n)
 
 
@@ -643,6 +644,13 @@ class Attention:
         f, b = ctypes.c_size_t(), ctypes.c_size_t()
         uvu_attn_workspace(ctypes.byref(self._shape(q, k, k, q)), ctypes.byref(f), ctypes.byref(b))
         return f.value, b.value
+
+    @staticmethod
+    def device_status(reset: bool = True) -> int:
+        """Status word of the attention kernels on the current device (0 = no timeout)."""
+        w = ctypes.c_uint()
+        uvu_attn_device_status(ctypes.byref(w), int(reset))
+        return w.value
 
     def _keep(self, keep, k):
         import torch

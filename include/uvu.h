@@ -554,7 +554,7 @@ uvu_status uvu_dropout_bwd(uvu_dtype dtype, int64_t n_draws, int inner, double p
  * in elements (the head_dim values of a head are consecutive; a stride may be any value for an
  * input, zero included; the rows and heads of out must not overlap).  lse [n_q][q_heads] fp32.
  * head_dim is 1 .. 128; q_heads is a multiple of kv_heads.  max_q, max_k: no graph has more rows or
- * states (the split of the work goes by them; wrong values cost time, not correctness).
+ * states (the split of the work goes by them; wrong values cost time, not correctness).  scale > 0.
  * k_keep [n_k] bytes, or NULL: states with 0 take no part, whatever their k and v hold.  A row
  * without a kept state gets out = 0 and lse = -inf. */
 typedef struct {
@@ -585,6 +585,11 @@ uvu_status uvu_attn_bwd(const uvu_attn_shape *shape, const int32_t *q_offsets, c
 /* Bytes of device workspace of uvu_attn_fwd and uvu_attn_bwd on the current device (either pointer
  * may be NULL). */
 uvu_status uvu_attn_workspace(const uvu_attn_shape *shape, size_t *fwd_bytes, size_t *bwd_bytes);
+
+/* Status word of the attention kernels on the current device (host pointer; 0 = no kernel gave up a
+ * bounded wait since the last reset; results of a call that did are not valid).  Synchronises with
+ * the device. */
+uvu_status uvu_attn_device_status(unsigned *word, int reset);
 
 /* ------------------------------------------------------------------------ measurement ---- */
 
