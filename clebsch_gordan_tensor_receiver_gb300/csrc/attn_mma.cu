@@ -41,77 +41,77 @@ using namespace tc;
 
 constexpr int kRows = 128;      // rows of a row tile, states of a state tile
 constexpr int kMaskRing = 8;    // state masks in flight: more than half the stages, plus two
-constexpr int kLoadWarps = 4;
+constexpr int kLoadWarps = 2;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// The packed rows of one kv head from row r0 of a graph on: row r0 + r is query i0 + (j0 + r) / group.
-struct RowsOf {
-    const char* base;   // the graph's first row, first head
-    int64_t row, head;  // strides in bytes
-    uint32_t group;     // query heads that share the kv head (1 for states)
-    int64_t i0;
-    uint32_t j0;
-    __device__ __forceinline__ void from(int64_t r0) {
-        i0 = r0 / group;
-        j0 = uint32_t(r0 - i0 * group);
-    }
-    __device__ __forceinline__ const char* at(int r) const {
-        const uint32_t x = j0 + uint32_t(r), i = group == 1 ? x : x / group;
-        return base + (i0 + i) * row + int64_t(x - i * group) * head;
-    }
+constexpr int kLoadThreads = kLoadWarps * 32;
+
+// How the loader threads share a tile of 128 rows: thread t takes 16-byte chunk t % 2^LG of the rows
+// t / 2^LG, + kStep, ...  2^LG is the power of two that holds the row's chunks.
+template <int LG>
+struct LoadMap {
+    static constexpr int kStep = kLoadThreads >> LG, kIters = kRows / kStep;
+    int row, chunk;
+    uint32_t bytes;  // of the chunk that exist: the others are zeros
+    bool on;         // the chunk is read by the matrix instructions
+    __device__ __forceinline__ LoadMap(int t, int D)
+        : row(t >> LG), chunk(t & ((1 << LG) - 1)), bytes(uint32_t(min(max(D - 8 * chunk, 0), 8)) * 2), on(chunk < 2 * ((D + 15) / 16)) {}
 };
 
-// 128 rows of an operand to the tile at `dst` (shared memory); rows that `use` refuses and columns
-// from D on are zeros.  128 threads, consecutive threads on consecutive chunks.
-template <typename T, bool ALIGNED, typename Use>
-__device__ __forceinline__ void load_rows(uint32_t dst, const RowsOf& x, int D, int chunks, int lanes_log2, int t, Use use) {
-    const int c = t & ((1 << lanes_log2) - 1);
-    if (c >= chunks) return;
-    const uint32_t bytes = uint32_t(min(max(D - 8 * c, 0), 8)) * 2;
-    for (int r = t >> lanes_log2; r < kRows; r += 128 >> lanes_log2) {
-        const bool on = use(r) && bytes > 0;
-        const char* src = on ? x.at(r) + c * 16 : x.base;
-        const uint32_t to = dst + tile_offset(r, c);
-        if constexpr (ALIGNED) {
-            copy16(to, src, on ? bytes : 0);
-        } else {
-            uint32_t w[4] = {0, 0, 0, 0};
-            if (on) {
-                const uint16_t* p = reinterpret_cast<const uint16_t*>(src);
+// One 16-byte chunk (of which `bytes` exist) into shared memory.
+template <bool ALIGNED>
+__device__ __forceinline__ void load_chunk(uint32_t to, const char* src, uint32_t bytes) {
+    if constexpr (ALIGNED) {
+        copy16(to, src, bytes);
+    } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(src);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (2 * i < bytes) w[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
-            }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                         : "memory");
-        }
+        for (int i = 0; i < 8; ++i)
+            if (2 * i < bytes) w[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
     }
 }
 
-// Copies are handed on a fixed number of groups after they were issued: the group issued `lag`
-// groups ago has landed.
-template <int LAG>
-struct Lagged {
-    int issued = 0;
-    template <typename Arrive>
-    __device__ __forceinline__ void commit(Arrive arrive) {
-        copy_commit();
-        if (++issued > LAG) {
-            copy_wait<LAG>();
-            fence_async();
-            __syncwarp();
-            if ((threadIdx.x & 31) == 0) arrive(issued - 1 - LAG);
-        }
+// 128 rows with a constant stride, `src` the first (its chunk included); rows that `use` refuses are
+// zeros.  ALL: every row is used.
+template <int LG, bool ALIGNED, bool ALL, typename Use>
+__device__ __forceinline__ void load_strided(uint32_t dst, const char* src, int64_t stride, const LoadMap<LG>& m, Use use) {
+    using M = LoadMap<LG>;
+    if (!m.on) return;
+    // rows kStep apart share their swizzle when kStep is a multiple of 8; at 4 it alternates
+    const uint32_t even = dst + tile_offset(m.row, m.chunk), odd = dst + tile_offset(m.row + M::kStep, m.chunk) - uint32_t(M::kStep * 128);
+    const char* p = src + m.row * stride;
+#pragma unroll 8
+    for (int i = 0; i < M::kIters; ++i) {
+        load_chunk<ALIGNED>((i & 1 ? odd : even) + uint32_t(i * M::kStep * 128), p, ALL || use(m.row + i * M::kStep) ? m.bytes : 0);
+        p += M::kStep * stride;
     }
-    template <typename Arrive>
-    __device__ __forceinline__ void drain(Arrive arrive) {
-        copy_wait<0>();
-        fence_async();
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0)
-            for (int i = max(0, issued - LAG); i < issued; ++i) arrive(i);
+}
+
+// Packed rows r0 .. r0 + 128 of a kv head's queries: row r is query r / group, head r % group.
+template <int LG, bool ALIGNED>
+__device__ __forceinline__ void load_packed(uint32_t dst, const char* base, int64_t row, int64_t head, int group, int64_t r0, int rows,
+                                            const LoadMap<LG>& m) {
+    using M = LoadMap<LG>;
+    if (group == 1) {
+        auto use = [&](int r) { return r < rows; };
+        if (rows >= kRows)
+            load_strided<LG, ALIGNED, true>(dst, base + r0 * row + m.chunk * 16, row, m, use);
+        else
+            load_strided<LG, ALIGNED, false>(dst, base + r0 * row + m.chunk * 16, row, m, use);
+        return;
     }
-};
+    if (!m.on) return;
+    const int64_t i0 = r0 / group;
+    const uint32_t j0 = uint32_t(r0 - i0 * group), g = uint32_t(group);
+    for (int i = 0; i < M::kIters; ++i) {
+        const int r = m.row + i * M::kStep;
+        const uint32_t x = j0 + uint32_t(r), q = x / g;
+        load_chunk<ALIGNED>(dst + tile_offset(r, m.chunk), base + (i0 + q) * row + int64_t(x - q * g) * head + m.chunk * 16,
+                            r < rows ? m.bytes : 0);
+    }
+}
 
 __device__ __forceinline__ uint32_t tail_word(int64_t left, int w) {  // bits of the states that exist
     const int64_t n = left - 32 * w;
@@ -140,6 +140,7 @@ struct StateMask {
         at += kRows;
         fetch();
     }
+    __device__ __forceinline__ bool all() const { return (word[0] & word[1] & word[2] & word[3]) == 0xffffffffu; }
     __device__ __forceinline__ bool has(int r) const {
         const uint32_t w = r < 64 ? (r < 32 ? word[0] : word[1]) : (r < 96 ? word[2] : word[3]);
         return (w >> (r & 31)) & 1;
@@ -165,7 +166,7 @@ struct FwdLayout {
     __host__ __device__ int total() const { return bars() + 256 + 1024; }  // + alignment slack
 };
 
-template <typename T, int NT, int LAG, bool ALIGNED>
+template <typename T, int NT, int LG, bool ALIGNED>
 __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 1) attn_fwd_mma(AttnArgs a, FwdLayout<NT> L) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_dead;
@@ -188,14 +189,14 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 
     const uint32_t tmem_cols = NT == 2 ? 512 : 256;
     if (threadIdx.x == 0) {
         s_dead = 0;
-        bar_init(q_full, kLoadWarps);
+        bar_init(q_full, kLoadWarps * 32);
         for (int t = 0; t < 2; ++t) {
             bar_init(s_full + 8 * t, 1);
             bar_init(p_full + 8 * t, 4);
             bar_init(o_full + 8 * t, 1);
         }
         for (int s = 0; s < L.stages; ++s) {
-            bar_init(full + 8 * s, kLoadWarps);
+            bar_init(full + 8 * s, kLoadWarps * 32);
             bar_init(empty + 8 * s, 1);
         }
         for (int s = 0; s < kMaskRing; ++s) bar_init(m_full + 8 * s, 1);
@@ -364,12 +365,13 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 
             };
             bool ok = n_tiles > 0 && bar_wait(q_full, 0, dead, status) && wait_stage(0);
             if (ok) {
-                fence_after();
+                fence_async();
                 for (int t = 0; t < nt; ++t) scores(t, 0);
                 mma_commit(empty + 8 * 0);
             }
             for (int j = 0; j < n_tiles && ok; ++j) {
                 ok = wait_stage(2 * j + 1);
+                fence_async();
                 for (int t = 0; t < nt && ok; ++t) {
                     ok = bar_wait(p_full + 8 * t, j & 1, dead, status);
                     if (!ok) break;
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 
                         if (t == 0) {
                             ok = wait_stage(2 * j + 2);
                             if (!ok) break;
-                            fence_after();
+                            fence_async();
                         }
                         scores(t, j + 1);
                     } else {
@@ -400,48 +402,46 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 
         __syncwarp();
     } else {
         // ------------------------------------------------------------------------- loaders
-        const int t = threadIdx.x - (4 * NT + 1) * 32;
-        const int chunks = 2 * d16;
-        int lanes_log2 = 1;
-        while ((1 << lanes_log2) < chunks) ++lanes_log2;
+        const LoadMap<LG> map(threadIdx.x - (4 * NT + 1) * 32, a.D);
         if (n_tiles > 0) {
-            RowsOf Q{reinterpret_cast<const char*>(static_cast<const T*>(a.q) + q0 * a.q_row + int64_t(h) * a.group * a.q_head),
-                     a.q_row * 2, a.q_head * 2, uint32_t(a.group), 0, 0};
-            RowsOf K{reinterpret_cast<const char*>(static_cast<const T*>(a.k) + k0 * a.k_row + h * a.k_head), a.k_row * 2, 0, 1, 0, 0};
-            RowsOf V{reinterpret_cast<const char*>(static_cast<const T*>(a.v) + k0 * a.v_row + h * a.v_head), a.v_row * 2, 0, 1, 0, 0};
-            // group 0 is Q, group 1 + i is stage i of the ring's sequence K_0 V_0 K_1 V_1 ...
-            auto arrive = [&](int g) { bar_arrive(g == 0 ? q_full : full + 8 * ((g - 1) % L.stages)); };
-            Lagged<LAG> copies;
-            for (int i = 0; i < nt; ++i) {
-                Q.from(tl.row0 + i * kRows);
-                load_rows<T, ALIGNED>(sb + uint32_t(i * L.tile()), Q, a.D, chunks, lanes_log2, t,
-                                      [&](int r) { return i * kRows + r < n_rows; });
-            }
-            copies.commit(arrive);
+            // every loader thread arrives: when its copies have landed, or at once after its own stores
+            auto arrive = [&](uint32_t bar) { ALIGNED ? copy_arrive(bar) : bar_arrive(bar); };
+            const char* Q = reinterpret_cast<const char*>(static_cast<const T*>(a.q) + q0 * a.q_row + int64_t(h) * a.group * a.q_head);
+            for (int i = 0; i < nt; ++i)
+                load_packed<LG, ALIGNED>(sb + uint32_t(i * L.tile()), Q, a.q_row * 2, a.q_head * 2, a.group, tl.row0 + i * kRows,
+                                         n_rows - i * kRows, map);
+            arrive(q_full);
+            const char* K = reinterpret_cast<const char*>(static_cast<const T*>(a.k) + (k0 + kr.lo) * a.k_row + h * a.k_head) + map.chunk * 16;
+            const char* V = reinterpret_cast<const char*>(static_cast<const T*>(a.v) + (k0 + kr.lo) * a.v_row + h * a.v_head) + map.chunk * 16;
             StateMask mask(a.keep ? a.keep + k0 : nullptr, kr.lo, kr.hi);
+            auto load = [&](int i, const char* src, int64_t stride) {
+                if (i >= L.stages &&
+                    !__all_sync(0xffffffffu, bar_wait(empty + 8 * (i % L.stages), (i / L.stages - 1) & 1, dead, status)))
+                    return false;
+                const uint32_t dst = sb + uint32_t(L.ring() + (i % L.stages) * L.tile());
+                auto use = [&](int r) { return mask.has(r); };
+                if (mask.all())
+                    load_strided<LG, ALIGNED, true>(dst, src, stride, map, use);
+                else
+                    load_strided<LG, ALIGNED, false>(dst, src, stride, map, use);
+                arrive(full + 8 * (i % L.stages));
+                return true;
+            };
             for (int j = 0; j < n_tiles; ++j) {
-                bool ok = true;
-                for (int half = 0; half < 2 && ok; ++half) {
-                    const int i = 2 * j + half;
-                    if (i >= L.stages) ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * (i % L.stages), (i / L.stages - 1) & 1, dead, status));
-                    if (!ok) break;
-                    if (half == 0) {
-                        mask.next();
-                        if (a.keep && warp == 4 * NT + 1 && lane == 0) {
-                            *reinterpret_cast<uint4*>(smem + L.masks() + (j % kMaskRing) * 16) =
-                                make_uint4(mask.word[0], mask.word[1], mask.word[2], mask.word[3]);
-                            bar_arrive(m_full + 8 * (j % kMaskRing));
-                        }
-                    }
-                    RowsOf& X = half ? V : K;
-                    X.i0 = kr.lo + int64_t(j) * kRows;
-                    load_rows<T, ALIGNED>(sb + uint32_t(L.ring() + (i % L.stages) * L.tile()), X, a.D, chunks, lanes_log2, t,
-                                          [&](int r) { return mask.has(r); });
-                    copies.commit(arrive);
+                mask.next();
+                if (!load(2 * j, K, a.k_row * 2)) break;
+                // the softmax warps read the tile's mask before its V stage is released, and K's stage comes half a ring
+                // later: kMaskRing masks cannot be overtaken
+                if (a.keep && warp == 4 * NT + 1 && lane == 0) {
+                    *reinterpret_cast<uint4*>(smem + L.masks() + (j % kMaskRing) * 16) =
+                        make_uint4(mask.word[0], mask.word[1], mask.word[2], mask.word[3]);
+                    bar_arrive(m_full + 8 * (j % kMaskRing));
                 }
-                if (!ok) break;
+                if (!load(2 * j + 1, V, a.v_row * 2)) break;
+                K += kRows * a.k_row * 2;
+                V += kRows * a.v_row * 2;
             }
-            copies.drain(arrive);
+            copy_wait_all();
         }
     }
     fence_before();
@@ -452,21 +452,26 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 
     }
 }
 
-constexpr int kLag = 3;  // stages >= kLag + 2: the issuer holds a V and the next K at once
-
-template <typename T, int NT, bool ALIGNED>
-cudaError_t fwd(const AttnArgs& a, int64_t row_tiles, cudaStream_t st) {
+template <typename T, int NT, int LG, bool ALIGNED>
+cudaError_t fwd_lg(const AttnArgs& a, int64_t row_tiles, cudaStream_t st) {
     FwdLayout<NT> L;
     L.panels = a.D > 64 ? 2 : 1;
     // one panel: 96 KB, two CTAs per SM (NT = 1), or 160 KB; two panels: 224 KB
     L.stages = NT == 1 ? (L.panels == 1 ? 5 : 6) : (L.panels == 1 ? 8 : 5);
-    auto k = attn_fwd_mma<T, NT, kLag, ALIGNED>;
+    auto k = attn_fwd_mma<T, NT, LG, ALIGNED>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total());
     if (e != cudaSuccess) return e;
     k<<<dim3(unsigned(row_tiles), unsigned(a.Hkv), unsigned(a.splits)), (4 * NT + 1 + kLoadWarps) * 32, L.total(), st>>>(a, L);
     return cudaGetLastError();
 }
 
+template <typename T, int NT, bool ALIGNED>
+cudaError_t fwd(const AttnArgs& a, int64_t row_tiles, cudaStream_t st) {
+    if (a.D <= 16) return fwd_lg<T, NT, 1, ALIGNED>(a, row_tiles, st);
+    if (a.D <= 32) return fwd_lg<T, NT, 2, ALIGNED>(a, row_tiles, st);
+    if (a.D <= 64) return fwd_lg<T, NT, 3, ALIGNED>(a, row_tiles, st);
+    return fwd_lg<T, NT, 4, ALIGNED>(a, row_tiles, st);
+}
 template <typename T>
 cudaError_t fwd_of(const AttnArgs& a, int nt, int64_t row_tiles, cudaStream_t st) {
     const uintptr_t any = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
