@@ -380,14 +380,17 @@ Choice choose(const AttnShape& s, int sms) {
     const auto rows_busy = [&](int R) {
         return std::min(row_tiles(s, R), int64_t(s.n_graphs) * ((s.max_q * group + R - 1) / R)) * s.kv_heads;
     };
-    const int64_t kt = std::min(state_tiles(s, kT), int64_t(s.n_graphs) * ((int64_t(s.max_k) + kT - 1) / kT)) * s.kv_heads;
+    const auto states_busy = [&](int R) {
+        return std::min(state_tiles(s, R), int64_t(s.n_graphs) * ((s.max_k + R - 1) / R)) * s.kv_heads;
+    };
     Choice c;
     c.nt = s.dtype == UVU_F32 ? 0 : rows_busy(256) >= sms && s.max_q * group > 128 ? 2 : 1;
     const int R = c.nt ? 128 * c.nt : kT;
     c.fwd_tiles = row_tiles(s, R);
     c.fwd = splits_for(rows_busy(R), s.max_k, c.nt ? 128 : kT, sms);
-    c.dq = splits_for(rows_busy(kT), s.max_k, kT, sms);
-    c.dkv = splits_for(kt, s.max_q * group, kT, sms);
+    const int B = c.nt ? 128 : kT;  // tile of the backward
+    c.dq = splits_for(rows_busy(B), s.max_k, B, sms);
+    c.dkv = splits_for(states_busy(B), s.max_q * group, B, sms);
     return c;
 }
 
@@ -407,34 +410,16 @@ cudaError_t fwd_simple(const AttnShape& s, const AttnArgs& a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <typename T, int DP>
-cudaError_t bwd_simple(const AttnShape& s, AttnArgs a, const Choice& c, cudaStream_t st) {
+template <int DP, bool KV>
+cudaError_t bwd_simple(const AttnArgs& a, int64_t tiles, cudaStream_t st) {
     const size_t sm = (size_t(4) * kT * (DP + 4) + 2 * kT * kSP) * 4;
-    const auto join_blocks = [](int64_t n) { return unsigned((n + kThreads - 1) / kThreads); };
-    if (a.nq > 0) attn_delta<T><<<unsigned((a.nq * a.Hq + 7) / 8), kThreads, 0, st>>>(a);
-    if (a.dq && a.nq > 0) {
-        a.splits = c.dq;
-        cudaError_t e = allow_smem(attn_bwd_simple<T, DP, false>, sm);
-        if (e != cudaSuccess) return e;
-        attn_bwd_simple<T, DP, false><<<dim3(unsigned(row_tiles(s, kT)), unsigned(a.Hkv), unsigned(a.splits)), kThreads, sm, st>>>(a);
-        const int64_t n = a.nq * a.Hq * a.D;
-        if (a.splits > 1) attn_bwd_join<T><<<join_blocks(n), kThreads, 0, st>>>(n, a.splits, a.part_o, static_cast<T*>(a.dq));
-    }
-    if (a.dk && a.nk > 0) {
-        a.splits = c.dkv;
-        cudaError_t e = allow_smem(attn_bwd_simple<T, DP, true>, sm);
-        if (e != cudaSuccess) return e;
-        attn_bwd_simple<T, DP, true><<<dim3(unsigned(state_tiles(s, kT)), unsigned(a.Hkv), unsigned(a.splits)), kThreads, sm, st>>>(a);
-        const int64_t n = a.nk * a.Hkv * a.D;
-        if (a.splits > 1) {
-            attn_bwd_join<T><<<join_blocks(n), kThreads, 0, st>>>(n, a.splits, a.part_o, static_cast<T*>(a.dk));
-            attn_bwd_join<T><<<join_blocks(n), kThreads, 0, st>>>(n, a.splits, a.part_o + a.splits * n, static_cast<T*>(a.dv));
-        }
-    }
+    cudaError_t e = allow_smem(attn_bwd_simple<float, DP, KV>, sm);
+    if (e != cudaSuccess) return e;
+    attn_bwd_simple<float, DP, KV><<<dim3(unsigned(tiles), unsigned(a.Hkv), unsigned(a.splits)), kThreads, sm, st>>>(a);
     return cudaGetLastError();
 }
 
-template <typename T, typename F>
+template <typename F>
 cudaError_t by_dim(int D, F f) {
     if (D <= 32) return f(std::integral_constant<int, 32>{});
     if (D <= 64) return f(std::integral_constant<int, 64>{});
@@ -480,7 +465,7 @@ cudaError_t launch_attn_fwd(const AttnShape& s, const AttnTensors& t, void* ws, 
         a.part_o = a.part_lse + align256(size_t(a.splits) * a.nq * a.Hq * 4) / 4;
     }
     cudaError_t e = c.nt ? launch_attn_fwd_mma(s.dtype, a, c.nt, c.fwd_tiles, st)
-                         : by_dim<float>(a.D, [&](auto d) { return fwd_simple<float, decltype(d)::value>(s, a, st); });
+                         : by_dim(a.D, [&](auto d) { return fwd_simple<float, decltype(d)::value>(s, a, st); });
     if (e != cudaSuccess || a.splits == 1) return e;
     const unsigned blocks = unsigned((a.nq * a.Hq + 7) / 8);
     switch (s.dtype) {
@@ -496,16 +481,38 @@ cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, 
     a.delta = static_cast<float*>(ws);
     a.part_o = a.delta + align256(size_t(a.nq) * a.Hq * 4) / 4;
     const Choice c = choose(s, sms);
-    auto go = [&](auto e) {
-        using T = decltype(e);
-        return by_dim<T>(a.D, [&](auto d) { return bwd_simple<T, decltype(d)::value>(s, a, c, st); });
+    const auto with_type = [&](auto f) {
+        switch (s.dtype) {
+            case UVU_F32: f(float{}); break;
+            case UVU_BF16: f(__nv_bfloat16{}); break;
+            default: f(__half{}); break;
+        }
+        return cudaGetLastError();
     };
-    switch (s.dtype) {
-        case UVU_F32: return go(float{});
-        case UVU_BF16: return go(__nv_bfloat16{});
-        case UVU_F16: return go(__half{});
-        default: return cudaErrorInvalidValue;
-    }
+    const auto blocks = [](int64_t n) { return unsigned((n + kThreads - 1) / kThreads); };
+    // dq, then dk and dv; the partial sums of one are joined before the other's are written
+    const auto half = [&](bool kv) {
+        a.splits = kv ? c.dkv : c.dq;
+        const int R = c.nt ? 128 : kT;
+        const int64_t tiles = kv ? state_tiles(s, R) : row_tiles(s, R);
+        cudaError_t e = c.nt ? launch_attn_bwd_mma(s.dtype, a, kv, tiles, st) : by_dim(a.D, [&](auto d) {
+            constexpr int DP = decltype(d)::value;
+            return kv ? bwd_simple<DP, true>(a, tiles, st) : bwd_simple<DP, false>(a, tiles, st);
+        });
+        if (e != cudaSuccess || a.splits == 1) return e;
+        const int64_t n = kv ? a.nk * a.Hkv * a.D : a.nq * a.Hq * a.D;
+        return with_type([&](auto t) {
+            using T = decltype(t);
+            attn_bwd_join<T><<<blocks(n), kThreads, 0, st>>>(n, a.splits, a.part_o, static_cast<T*>(kv ? a.dk : a.dq));
+            if (kv) attn_bwd_join<T><<<blocks(n), kThreads, 0, st>>>(n, a.splits, a.part_o + a.splits * n, static_cast<T*>(a.dv));
+        });
+    };
+    cudaError_t e = cudaSuccess;
+    if (a.nq > 0)
+        e = with_type([&](auto t) { attn_delta<decltype(t)><<<unsigned((a.nq * a.Hq + 7) / 8), kThreads, 0, st>>>(a); });
+    if (e == cudaSuccess && a.dq && a.nq > 0) e = half(false);
+    if (e == cudaSuccess && a.dk && a.nk > 0) e = half(true);
+    return e;
 }
 
 }  // namespace uvu

@@ -53,4 +53,7 @@ __device__ __forceinline__ AttnTile attn_tile(const int32_t* off, int graphs, in
 // leaves partial results for the join.
 cudaError_t launch_attn_fwd_mma(uvu_dtype dtype, const AttnArgs& a, int nt, int64_t row_tiles, cudaStream_t st);
 
+// The backward of 16-bit operands: dk and dv (kv) by tiles of 128 states, or dq by tiles of 128 rows.
+cudaError_t launch_attn_bwd_mma(uvu_dtype dtype, const AttnArgs& a, bool kv, int64_t tiles, cudaStream_t st);
+
 }  // namespace uvu
