@@ -1071,6 +1071,8 @@ uvu_status norm_shape(uvu_dtype dtype, int64_t n_rows, int n_graphs, int64_t max
     if (max_rows < 0) return fail(UVU_ERR_INVALID_ARGUMENT, "max_rows must be >= 0");
     if (groups < 1 || channels < 1 || channels > 8192 || channels % groups)
         return fail(UVU_ERR_INVALID_ARGUMENT, "channels must be a multiple of groups in [1, 8192]");
+    if (int64_t(n_graphs) * channels >= std::numeric_limits<int32_t>::max())
+        return fail(UVU_ERR_INVALID_ARGUMENT, "n_graphs * channels must be < 2^31 - 1");
     *s = NormShape{dtype, n_rows, n_graphs, std::min(max_rows, n_rows), channels, groups, UVU_ACT_NONE, 0.0};
     return UVU_OK;
 }
@@ -1128,8 +1130,10 @@ extern "C" uvu_status uvu_group_norm_workspace(uvu_dtype dtype, int64_t n_rows, 
                                                int groups, size_t* fwd_bytes, size_t* bwd_bytes) {
     NormShape s;
     UVU_TRY(norm_shape(dtype, n_rows, n_graphs, max_rows, channels, groups, &s));
-    if (fwd_bytes) *fwd_bytes = norm_workspace(s, false);
-    if (bwd_bytes) *bwd_bytes = norm_workspace(s, true);
+    int sms = 0;
+    UVU_TRY(sm_count_cached(&sms));
+    if (fwd_bytes) *fwd_bytes = norm_workspace(s, false, sms);
+    if (bwd_bytes) *bwd_bytes = norm_workspace(s, true, sms);
     return ok();
 }
 
@@ -1153,8 +1157,10 @@ extern "C" uvu_status uvu_group_norm_fwd(uvu_dtype dtype, int64_t n_rows, int n_
         UVU_TRY(need_elem(gamma, UVU_F32, "gamma"));
         UVU_TRY(need_elem(beta, UVU_F32, "beta"));
     }
-    UVU_TRY(check_workspace(workspace, workspace_bytes, norm_workspace(s, false), "uvu_group_norm_workspace"));
-    cudaError_t e = launch_norm_fwd(s, offsets, x, gamma, beta, y, mean, rstd, workspace, static_cast<cudaStream_t>(stream));
+    int sms = 0;
+    UVU_TRY(sm_count_cached(&sms));
+    UVU_TRY(check_workspace(workspace, workspace_bytes, norm_workspace(s, false, sms), "uvu_group_norm_workspace"));
+    cudaError_t e = launch_norm_fwd(s, offsets, x, gamma, beta, y, mean, rstd, workspace, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "group norm launch");
     return ok();
 }
@@ -1186,8 +1192,10 @@ extern "C" uvu_status uvu_group_norm_bwd(uvu_dtype dtype, int64_t n_rows, int n_
     UVU_TRY(need_elem(beta, UVU_F32, "beta"));
     UVU_TRY(need_elem(mean, UVU_F32, "mean"));
     UVU_TRY(need_elem(rstd, UVU_F32, "rstd"));
-    UVU_TRY(check_workspace(workspace, workspace_bytes, norm_workspace(s, true), "uvu_group_norm_workspace"));
-    cudaError_t e = launch_norm_bwd(s, offsets, x, dy, gamma, beta, mean, rstd, dx, dgamma, dbeta, workspace, st);
+    int sms = 0;
+    UVU_TRY(sm_count_cached(&sms));
+    UVU_TRY(check_workspace(workspace, workspace_bytes, norm_workspace(s, true, sms), "uvu_group_norm_workspace"));
+    cudaError_t e = launch_norm_bwd(s, offsets, x, dy, gamma, beta, mean, rstd, dx, dgamma, dbeta, workspace, sms, st);
     if (e != cudaSuccess) return cuda_fail(e, "group norm gradient launch");
     return ok();
 }

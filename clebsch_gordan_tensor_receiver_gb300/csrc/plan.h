@@ -198,12 +198,12 @@ struct NormShape {
     uvu_act act;
     double eps;
 };
-size_t norm_workspace(const NormShape& s, bool bwd);
+size_t norm_workspace(const NormShape& s, bool bwd, int sms);
 cudaError_t launch_norm_fwd(const NormShape& s, const int32_t* offsets, const void* x, const float* gamma, const float* beta,
-                            void* y, float* mean, float* rstd, void* ws, cudaStream_t st);
+                            void* y, float* mean, float* rstd, void* ws, int sms, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormShape& s, const int32_t* offsets, const void* x, const void* dy, const float* gamma,
                             const float* beta, const float* mean, const float* rstd, void* dx, float* dgamma, float* dbeta,
-                            void* ws, cudaStream_t st);
+                            void* ws, int sms, cudaStream_t st);
 // attn.cu
 using AttnShape = uvu_attn_shape;
 struct AttnTensors {
