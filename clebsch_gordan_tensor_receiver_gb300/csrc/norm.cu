@@ -32,11 +32,28 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128, kMergeThreads = 256;
+
+// Division of values below 2^31 by a divisor that the host knows: n / d = (n m) >> (32 + s) with
+// m = ceil(2^(32+s) / d), s = ceil(log2 d) - 1 (exact for n < 2^31: the error n (m d - 2^(32+s)) stays
+// below 2^(32+s)).  An integer division costs some 25 instructions, which is what a short row's whole
+// arithmetic costs.
+struct Div {
+    uint32_t d, m, s;
+    static Div by(int d) {
+        Div r = {uint32_t(d), 0, 0};
+        while ((uint64_t(1) << (r.s + 1)) < r.d) ++r.s;
+        r.m = uint32_t(((uint64_t(1) << (32 + r.s)) + r.d - 1) / r.d);  // d >= 2: below 2^32
+        return r;
+    }
+    __device__ __forceinline__ int operator()(int n) const { return d == 1 ? n : int(__umulhi(uint32_t(n), m) >> s); }
+};
 
 struct NormArgs {
     int64_t rows;        // N
     int graphs, C, G, per;  // per = C / G
+    Div by_per, by_slabs, by_size, by_lanes;
+    int lanes, par, size;  // threads on a row, rows in parallel, blocks of a cluster
     int R;               // rows of a tile, or of a block's share that shared memory holds
     int slab, slabs;     // channels of a block (on-chip form), slabs of C
     float eps;
@@ -78,25 +95,37 @@ template <int V>
 constexpr int kPairs = V > 1 ? V / 2 : 1;
 template <typename T, int V>
 __device__ __forceinline__ F2 pair_of(const Vec<T, V>& v, int i) {
-    return F2(widen(v.v[2 * i]), V > 1 ? widen(v.v[V > 1 ? 2 * i + 1 : 0]) : 0.f);
+    if constexpr (V == 1)
+        return F2(widen(v.v[0]), 0.f);
+    else
+        return F2(widen(v.v[2 * i]), widen(v.v[2 * i + 1]));
 }
 template <typename T, int V>
 __device__ __forceinline__ void put_pair(Vec<T, V>& v, int i, F2 x) {
     const float2 b = x.both();
-    v.v[2 * i] = narrow<T>(b.x);
-    if (V > 1) v.v[V > 1 ? 2 * i + 1 : 0] = narrow<T>(b.y);
+    if constexpr (V == 1) {
+        v.v[0] = narrow<T>(b.x);
+    } else if constexpr (sizeof(T) == 4) {
+        v.v[2 * i] = b.x;
+        v.v[2 * i + 1] = b.y;
+    } else if constexpr (__is_same(T, __half)) {
+        const __half2 h = __float22half2_rn(b);
+        v.v[2 * i] = h.x, v.v[2 * i + 1] = h.y;
+    } else {
+        const __nv_bfloat162 h = __float22bfloat162_rn(b);
+        v.v[2 * i] = h.x, v.v[2 * i + 1] = h.y;
+    }
 }
 
-__device__ __forceinline__ float exp2f_fast(float x) {  // 2^x, 2 ulp
+// 1 / (1 + exp(-z)): 2^x and 1/x to 2 ulp each; 2^x overflows to infinity where the sigmoid is below 2^-126, and 1/inf = 0.
+__device__ __forceinline__ float sigmoid_of_scaled(float x) {  // x = -z log2(e)
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;\n\tadd.rn.f32 %0, %0, 0f3F800000;\n\trcp.approx.ftz.f32 %0, %0;" : "=f"(y) : "f"(x));
     return y;
 }
-// 1 / (1 + exp(-z)).  __fdividef's result is 0 for a denominator above 2^126: the sigmoid is below 2^-126 there.
 __device__ __forceinline__ F2 sigmoid(F2 z) {
     const float2 e = (z * F2(-1.4426950408889634f, -1.4426950408889634f)).both();
-    const float2 d = (F2(exp2f_fast(e.x), exp2f_fast(e.y)) + F2(1.f, 1.f)).both();
-    return F2(__fdividef(1.f, d.x), __fdividef(1.f, d.y));
+    return F2(sigmoid_of_scaled(e.x), sigmoid_of_scaled(e.y));
 }
 
 // act(z), and dy act'(z)
@@ -129,63 +158,76 @@ __device__ __forceinline__ int tile_graph(const int32_t* offsets, int graphs, in
     return r0 < r1 ? lo : -1;
 }
 
-// The block's threads over `vecs` vectors of a row: consecutive threads take consecutive vectors, and
-// kThreads / lanes rows go in parallel.  f(cv, rl, par): vector cv of the rows rl, rl + par, ...;
-// rows wider than the block take several rounds.  after(cv0, width): between rounds, by all threads.
-template <typename F, typename A>
-__device__ __forceinline__ void over_columns(int vecs, F f, A after) {
-    const int lanes = min(vecs, kThreads), par = kThreads / lanes;
-    const int rl = threadIdx.x / lanes, cl = threadIdx.x - rl * lanes;
-    for (int cv0 = 0; cv0 < vecs; cv0 += lanes) {
-        if (rl < par && cv0 + cl < vecs) f(cv0 + cl, rl, par);
-        after(cv0, min(lanes, vecs - cv0), par);
-    }
-}
-
-// The group of each channel of a vector, from one division.
-template <int V, typename F>
-__device__ __forceinline__ void each_channel(int c0, int per, F f) {
-    int g = c0 / per, left = per - (c0 - g * per);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (left == 0) ++g, left = per;
-        f(i, g);
-        --left;
-    }
-}
-// A value per channel of a vector, as pairs.
+// The block's threads over the vectors of a row of SC channels: consecutive threads take consecutive
+// vectors, and `par` rows go in parallel.  Rows wider than the block take several rounds.
 template <int V>
-struct Channels {
-    F2 v[kPairs<V>];
+struct Columns {
+    int vecs, lanes, par, rl, cl;  // vectors of a row, threads on a row, rows in parallel; the thread's row and vector
+    // the last slab of a row may have fewer vectors than the lanes that the host chose
+    __device__ __forceinline__ Columns(const NormArgs& a, int SC) : vecs(SC / V), lanes(a.lanes), par(a.par) {
+        rl = a.by_lanes(threadIdx.x);
+        cl = int(threadIdx.x) - rl * lanes;
+    }
+    // f(cv): the thread's vectors
     template <typename F>
-    __device__ __forceinline__ void set(int c0, int per, F f) {
-        float x[2 * kPairs<V>];
-        x[2 * kPairs<V> - 1] = 0.f;
-        each_channel<V>(c0, per, [&](int i, int g) { x[i] = f(i, g); });
-#pragma unroll
-        for (int i = 0; i < kPairs<V>; ++i) v[i] = F2(x[2 * i], x[2 * i + 1]);
+    __device__ __forceinline__ void each(F f) const {
+        if (rl < par)
+            for (int cv = cl; cv < vecs; cv += lanes) f(cv);
     }
 };
 
-// NS sums per channel over `rows` rows, to s_chan[s * SC + c].  f(cv) gives the function of (row, acc)
-// that adds a row's terms for vector cv.
+// Values per channel are kept in shared memory and read as the pairs of a thread's vector.
+template <int V>
+struct Channels {
+    F2 v[kPairs<V>];
+    __device__ __forceinline__ explicit Channels(const float* s) {  // 16-byte aligned where V > 1
+        if constexpr (V == 1) {
+            v[0] = F2(*s, 0.f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                const ulonglong2 q = reinterpret_cast<const ulonglong2*>(s)[i];
+                v[2 * i].v = q.x, v[2 * i + 1].v = q.y;
+            }
+        }
+    }
+};
+// f(c) for every channel c of `n`, shared out over the block.
+template <typename F>
+__device__ __forceinline__ void fill_channels(int n, F f) {
+    for (int c = threadIdx.x; c < n; c += kThreads) f(c);
+    __syncthreads();
+}
+
+// f(r, on_chip) for the thread's rows: the first `held` are in shared memory (true_type), others in global memory.  Two loops,
+// so that each has loads of its own kind.
+template <int V, typename F>
+__device__ __forceinline__ void each_row(const Columns<V>& co, int held, int rows, F f) {
+    int r = co.rl;
+#pragma unroll 1
+    for (; r < held; r += co.par) f(r, std::true_type{});
+#pragma unroll 1
+    for (; r < rows; r += co.par) f(r, std::false_type{});
+}
+
+// NS sums per channel over `rows` rows, to s_chan[s * SC + c].  f(cv) gives the function of (row, on_chip,
+// acc) that adds a row's terms for vector cv.
 template <int V, int NS, typename F>
-__device__ __forceinline__ void channel_sums(int rows, int SC, float* s_part, float* s_chan, F f) {
-    const int lanes = min(SC / V, kThreads), width = lanes * V;
-    over_columns(
-        SC / V,
-        [&](int cv, int rl, int par) {
+__device__ __forceinline__ void channel_sums(const Columns<V>& co, int held, int rows, int SC, float* s_part, float* s_chan, F f) {
+    const int width = co.lanes * V;
+    for (int cv0 = 0; cv0 < co.vecs; cv0 += co.lanes) {
+        const int n = min(co.lanes, co.vecs - cv0) * V;
+        if (co.rl < co.par && cv0 + co.cl < co.vecs) {
             F2 acc[NS][kPairs<V>];
 #pragma unroll
             for (int s = 0; s < NS; ++s)
 #pragma unroll
                 for (int i = 0; i < kPairs<V>; ++i) acc[s][i] = F2(0.f, 0.f);
-            auto add = f(cv);
-#pragma unroll 1
-            for (int r = rl; r < rows; r += par) add(r, acc);
+            auto add = f(cv0 + co.cl);
+            each_row(co, held, rows, [&](int r, auto on_chip) { add(r, on_chip, acc); });
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
-                float* o = s_part + (s * par + rl) * width + (cv % lanes) * V;
+                float* o = s_part + (s * co.par + co.rl) * width + co.cl * V;
                 if constexpr (V == 1) {
                     *o = acc[s][0].both().x;
                 } else {
@@ -196,21 +238,21 @@ __device__ __forceinline__ void channel_sums(int rows, int SC, float* s_part, fl
                     }
                 }
             }
-        },
-        [&](int cv0, int n, int par) {
-            __syncthreads();
-            for (int c = threadIdx.x; c < n * V * NS; c += kThreads) {
-                const int s = c / (n * V), cc = c - s * n * V;
-                const float* p = s_part + s * par * width + cc;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+            for (int c = threadIdx.x; c < n; c += kThreads) {
+                const float* p = s_part + s * co.par * width + c;
                 float sum[2] = {0.f, 0.f};
                 int k = 0;
 #pragma unroll 4
-                for (; k + 1 < par; k += 2) sum[0] += p[k * width], sum[1] += p[(k + 1) * width];
-                if (k < par) sum[0] += p[k * width];
-                s_chan[s * SC + cv0 * V + cc] = sum[0] + sum[1];
+                for (; k + 1 < co.par; k += 2) sum[0] += p[k * width], sum[1] += p[(k + 1) * width];
+                if (k < co.par) sum[0] += p[k * width];
+                s_chan[s * SC + cv0 * V + c] = sum[0] + sum[1];
             }
-            __syncthreads();
-        });
+        __syncthreads();
+    }
 }
 
 // Sums of `per` consecutive channel values per group; 4 lanes of a warp share a group.
@@ -237,14 +279,14 @@ __device__ __forceinline__ void stage_vec(T* dst, const T* src) {
     }
 }
 template <typename T, int V>
-__device__ __forceinline__ void stage_rows(T* s, const T* x, int rows, int SC, int64_t C) {
-    over_columns(
-        SC / V,
-        [&](int cv, int rl, int par) {
+__device__ __forceinline__ void stage_rows(const Columns<V>& co, T* s, const T* x, int rows, int SC, int C) {
+    co.each([&](int cv) {
+        T* d = s + co.rl * SC + cv * V;
+        const T* p = x + int64_t(co.rl) * C + cv * V;
+        const int64_t step = int64_t(co.par) * C;
 #pragma unroll 4
-            for (int r = rl; r < rows; r += par) stage_vec<T, V>(s + r * SC + cv * V, x + r * C + cv * V);
-        },
-        [](int, int, int) {});
+        for (int r = co.rl; r < rows; r += co.par, d += co.par * SC, p += step) stage_vec<T, V>(d, p);
+    });
 }
 __device__ __forceinline__ void stage_wait() {
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -256,24 +298,24 @@ __device__ __forceinline__ void stage_wait() {
 struct Share {  // a block's part of a graph
     int b, c0, SC, rank, rows;
     int K;  // blocks that have rows (one, if none has); the others leave at once
-    int64_t n, r0;
+    int n;
+    int64_t r0;
 };
 __device__ __forceinline__ Share share_of(const NormArgs& a) {
     Share s;
-    s.K = int(cg::this_cluster().num_blocks());
-    s.rank = int(cg::this_cluster().block_rank());
-    const int id = int(blockIdx.x) / s.K;
-    s.b = id / a.slabs;
+    const int id = a.by_size(blockIdx.x);
+    s.rank = int(blockIdx.x) - id * a.size;
+    s.b = a.by_slabs(id);
     s.c0 = (id - s.b * a.slabs) * a.slab;
     s.SC = min(a.slab, a.C - s.c0);
-    const int64_t first = a.offsets[s.b];
+    const int first = a.offsets[s.b];
     s.n = a.offsets[s.b + 1] - first;
     // whole shares in rank order, so that short graphs need fewer blocks; a graph longer than max_rows
     // promised is shared out evenly
-    const int64_t each = max(int64_t(a.R), (s.n + s.K - 1) / s.K), lo = min(s.n, s.rank * each);
+    const int each = s.n > a.R * a.size ? (s.n - 1) / a.size + 1 : a.R, lo = int(min(int64_t(s.n), int64_t(s.rank) * each));
     s.r0 = first + lo;
-    s.rows = int(min(s.n, lo + each) - lo);
-    s.K = int(max(int64_t(1), (s.n + each - 1) / each));
+    s.rows = min(s.n - lo, each);
+    s.K = s.n > each ? (s.n - 1) / each + 1 : 1;
     return s;
 }
 
@@ -300,21 +342,26 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_chip(NormArgs a, const T* _
     extern __shared__ __align__(16) unsigned char smem[];
     const Share s = share_of(a);
     if (s.rank >= s.K) return;
-    const int groups = s.SC / a.per, g0 = s.c0 / a.per;
+    const Columns<V> co(a, s.SC);
+    const int groups = a.by_per(s.SC), g0 = a.by_per(s.c0);
     T* s_x = reinterpret_cast<T*>(smem);
     float* s_part = reinterpret_cast<float*>(smem + (size_t(a.R) * a.slab * sizeof(T) + 15) / 16 * 16);
-    float *s_chan = s_part + max(kThreads * V, a.slab), *s_g1 = s_chan + a.slab, *s_g2 = s_g1 + a.slab / a.per,
-          *s_mean = s_g2 + a.slab / a.per, *s_rstd = s_mean + a.slab / a.per;
+    const int pad = (a.slab + 3) & ~3;  // arrays per channel begin on 16 bytes
+    float *s_chan = s_part + kThreads * V, *s_minus = s_chan + pad, *s_k = s_minus + pad, *s_beta = s_k + pad,
+          *s_g1 = s_beta + pad, *s_g2 = s_g1 + a.by_per(a.slab), *s_mean = s_g2 + a.by_per(a.slab), *s_rstd = s_mean + a.by_per(a.slab);
     const T* xs = x + s.r0 * a.C + s.c0;
     const int held = min(s.rows, a.R);
-    stage_rows<T, V>(s_x, xs, held, s.SC, a.C);
+    stage_rows<T, V>(co, s_x, xs, held, s.SC, a.C);
     stage_wait();
-    auto row = [&](int r, int cv) {
-        return load_vec<T, V>(r < held ? s_x + r * s.SC + cv * V : xs + int64_t(r) * a.C + cv * V);
+    auto row = [&](int r, int cv, auto on_chip) {
+        if constexpr (decltype(on_chip)::value)
+            return load_vec<T, V>(s_x + r * s.SC + cv * V);
+        else
+            return load_vec<T, V>(xs + int64_t(r) * a.C + cv * V);
     };
-    channel_sums<V, 1>(s.rows, s.SC, s_part, s_chan, [&](int cv) {
-        return [&, cv](int r, F2 (&acc)[1][kPairs<V>]) {
-            const Vec<T, V> v = row(r, cv);
+    channel_sums<V, 1>(co, held, s.rows, s.SC, s_part, s_chan, [&](int cv) {
+        return [&, cv](int r, auto on_chip, F2 (&acc)[1][kPairs<V>]) {
+            const Vec<T, V> v = row(r, cv, on_chip);
 #pragma unroll
             for (int i = 0; i < kPairs<V>; ++i) acc[0][i] = acc[0][i] + pair_of(v, i);
         };
@@ -322,11 +369,11 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_chip(NormArgs a, const T* _
     group_sums(groups, a.per, s_chan, [&](int g, float v) { s_g1[g] = v; });
     cluster_sums(groups, s.K, s_g1, s_mean);
     const float inv = s.n > 0 ? 1.f / (float(s.n) * float(a.per)) : 0.f;
-    channel_sums<V, 1>(s.rows, s.SC, s_part, s_chan, [&](int cv) {
-        Channels<V> minus;
-        minus.set(cv * V, a.per, [&](int, int g) { return -s_mean[g] * inv; });
-        return [&, cv, minus](int r, F2 (&acc)[1][kPairs<V>]) {
-            const Vec<T, V> v = row(r, cv);
+    fill_channels(s.SC, [&](int c) { s_minus[c] = -s_mean[a.by_per(c)] * inv; });
+    channel_sums<V, 1>(co, held, s.rows, s.SC, s_part, s_chan, [&](int cv) {
+        const Channels<V> minus(s_minus + cv * V);
+        return [&, cv, minus](int r, auto on_chip, F2 (&acc)[1][kPairs<V>]) {
+            const Vec<T, V> v = row(r, cv, on_chip);
 #pragma unroll
             for (int i = 0; i < kPairs<V>; ++i) {
                 const F2 d = pair_of(v, i) + minus.v[i];
@@ -337,33 +384,28 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_chip(NormArgs a, const T* _
     group_sums(groups, a.per, s_chan, [&](int g, float v) { s_g2[g] = v; });
     cluster_sums(groups, s.K, s_g2, s_rstd);
     if (s.K > 1) cg::this_cluster().barrier_arrive();  // the other blocks' sums have been read
-    for (int g = threadIdx.x; g < groups; g += kThreads) {
-        s_rstd[g] = rsqrtf(s_rstd[g] * inv + a.eps);
-        if (s.rank == 0) {
+    fill_channels(s.SC, [&](int c) {
+        const int g = a.by_per(c);
+        const float rstd = rsqrtf(s_rstd[g] * inv + a.eps);
+        s_k[c] = rstd * a.gamma[s.c0 + c];
+        s_beta[c] = a.beta[s.c0 + c];
+        if (s.rank == 0 && c == g * a.per) {
             a.mean[int64_t(s.b) * a.G + g0 + g] = s_mean[g] * inv;
-            a.rstd[int64_t(s.b) * a.G + g0 + g] = s_rstd[g];
+            a.rstd[int64_t(s.b) * a.G + g0 + g] = rstd;
         }
-    }
-    __syncthreads();
+    });
     T* ys = y + s.r0 * a.C + s.c0;
-    over_columns(
-        s.SC / V,
-        [&](int cv, int rl, int par) {
-            Channels<V> minus, k, beta;
-            minus.set(cv * V, a.per, [&](int, int g) { return -s_mean[g] * inv; });
-            k.set(cv * V, a.per, [&](int i, int g) { return s_rstd[g] * a.gamma[s.c0 + cv * V + i]; });
-            beta.set(cv * V, a.per, [&](int i, int) { return a.beta[s.c0 + cv * V + i]; });
-#pragma unroll 1
-            for (int r = rl; r < s.rows; r += par) {
-                const Vec<T, V> v = row(r, cv);
+    co.each([&](int cv) {
+            const Channels<V> minus(s_minus + cv * V), k(s_k + cv * V), beta(s_beta + cv * V);
+            each_row(co, held, s.rows, [&](int r, auto on_chip) {
+                const Vec<T, V> v = row(r, cv, on_chip);
                 Vec<T, V> o;
 #pragma unroll
                 for (int i = 0; i < kPairs<V>; ++i)
                     put_pair(o, i, act_of<ACT>(fma2(pair_of(v, i) + minus.v[i], k.v[i], beta.v[i])));
                 store_vec<T, V>(ys + int64_t(r) * a.C + cv * V, o);
-            }
-        },
-        [](int, int, int) {});
+            });
+    });
     __syncwarp();
     if (s.K > 1) cg::this_cluster().barrier_wait();
 }
@@ -372,12 +414,17 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_chip(NormArgs a, const T* _
 template <int V, int ACT>
 struct BwdChannel {
     Channels<V> minus, rstd, gamma, beta;
-    __device__ __forceinline__ BwdChannel(const NormArgs& a, int b, int c) {
-        const int64_t g0 = int64_t(b) * a.G;
-        minus.set(c, a.per, [&](int, int g) { return -a.mean[g0 + g]; });
-        rstd.set(c, a.per, [&](int, int g) { return a.rstd[g0 + g]; });
-        gamma.set(c, a.per, [&](int i, int) { return a.gamma[c + i]; });
-        beta.set(c, a.per, [&](int i, int) { return a.beta[c + i]; });
+    // s: the arrays that fill() wrote, of vector cv
+    __device__ __forceinline__ BwdChannel(const float* s, int pad, int cv)
+        : minus(s + cv * V), rstd(s + pad + cv * V), gamma(s + 2 * pad + cv * V), beta(s + 3 * pad + cv * V) {}
+    static __device__ __forceinline__ void fill(const NormArgs& a, int b, int c0, int n, float* s, int pad) {
+        fill_channels(n, [&](int c) {
+            const int64_t g = int64_t(b) * a.G + a.by_per(c0 + c);
+            s[c] = -a.mean[g];
+            s[pad + c] = a.rstd[g];
+            s[2 * pad + c] = a.gamma[c0 + c];
+            s[3 * pad + c] = a.beta[c0 + c];
+        });
     }
     __device__ __forceinline__ F2 xh(F2 x, int i) const { return (x + minus.v[i]) * rstd.v[i]; }
     __device__ __forceinline__ F2 dz(F2 dy, F2 xh, int i) const { return dact_of<ACT>(dy, fma2(xh, gamma.v[i], beta.v[i])); }
@@ -393,30 +440,50 @@ struct BwdChannel {
     }
 };
 
+// -mean(t) and -mean(t xh) of each channel's group, from the graph's channel sums.
+__device__ __forceinline__ void group_means(const NormArgs& a, int n_channels, int64_t n, const float* sum0, const float* sum1,
+                                            const float* s_gamma, float* s_m1, float* s_m2) {
+    const float inv = n > 0 ? -1.f / (float(n) * float(a.per)) : 0.f;
+    fill_channels(n_channels, [&](int c) { s_m1[c] = sum0[c] * s_gamma[c], s_m2[c] = sum1[c] * s_gamma[c]; });
+    // a group's result replaces its first channel's value, which its own four lanes have read
+    group_sums(a.by_per(n_channels), a.per, s_m1, [&](int g, float v) { s_m1[g * a.per] = v * inv; });
+    group_sums(a.by_per(n_channels), a.per, s_m2, [&](int g, float v) { s_m2[g * a.per] = v * inv; });
+    __syncthreads();
+    fill_channels(n_channels, [&](int c) {
+        const int g = a.by_per(c) * a.per;
+        if (c != g) s_m1[c] = s_m1[g], s_m2[c] = s_m2[g];
+    });
+}
+
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kThreads, 3) norm_bwd_chip(NormArgs a, const T* __restrict__ x, const T* __restrict__ dy,
+__global__ void __launch_bounds__(kThreads) norm_bwd_chip(NormArgs a, const T* __restrict__ x, const T* __restrict__ dy,
                                                           T* __restrict__ dx, float* __restrict__ sums) {
     extern __shared__ __align__(16) unsigned char smem[];
     const Share s = share_of(a);
     if (s.rank >= s.K) return;
-    const int groups = s.SC / a.per;
+    const Columns<V> co(a, s.SC);
     const size_t tile = (size_t(a.R) * a.slab * sizeof(T) + 15) / 16 * 16;
     T *s_x = reinterpret_cast<T*>(smem), *s_d = reinterpret_cast<T*>(smem + tile);
     float* s_part = reinterpret_cast<float*>(smem + 2 * tile);
-    float *s_chan = s_part + 2 * max(kThreads * V, a.slab), *s_sum = s_chan + 2 * a.slab, *s_m1 = s_sum + 2 * a.slab,
-          *s_m2 = s_m1 + a.slab / a.per;
+    const int pad = (a.slab + 3) & ~3;  // arrays per channel begin on 16 bytes
+    float *s_chan = s_part + 2 * kThreads * V, *s_sum = s_chan + 2 * pad, *s_ch = s_sum + 2 * pad, *s_m1 = s_ch + 4 * pad,
+          *s_m2 = s_m1 + pad;
     const T *xs = x + s.r0 * a.C + s.c0, *ds = dy + s.r0 * a.C + s.c0;
     const int held = min(s.rows, a.R);
-    stage_rows<T, V>(s_x, xs, held, s.SC, a.C);
-    stage_rows<T, V>(s_d, ds, held, s.SC, a.C);
+    stage_rows<T, V>(co, s_x, xs, held, s.SC, a.C);
+    stage_rows<T, V>(co, s_d, ds, held, s.SC, a.C);
+    BwdChannel<V, ACT>::fill(a, s.b, s.c0, s.SC, s_ch, pad);
     stage_wait();
-    auto row = [&](const T* sm, const T* gm, int r, int cv) {
-        return load_vec<T, V>(r < held ? sm + r * s.SC + cv * V : gm + int64_t(r) * a.C + cv * V);
+    auto row = [&](const T* sm, const T* gm, int r, int cv, auto on_chip) {
+        if constexpr (decltype(on_chip)::value)
+            return load_vec<T, V>(sm + r * s.SC + cv * V);
+        else
+            return load_vec<T, V>(gm + int64_t(r) * a.C + cv * V);
     };
-    channel_sums<V, 2>(s.rows, s.SC, s_part, s_chan, [&](int cv) {
-        const BwdChannel<V, ACT> ch(a, s.b, s.c0 + cv * V);
-        return [&, cv, ch](int r, F2 (&acc)[2][kPairs<V>]) {
-            const Vec<T, V> v = row(s_x, xs, r, cv), d = row(s_d, ds, r, cv);
+    channel_sums<V, 2>(co, held, s.rows, s.SC, s_part, s_chan, [&](int cv) {
+        const BwdChannel<V, ACT> ch(s_ch, pad, cv);
+        return [&, cv, ch](int r, auto on_chip, F2 (&acc)[2][kPairs<V>]) {
+            const Vec<T, V> v = row(s_x, xs, r, cv, on_chip), d = row(s_d, ds, r, cv, on_chip);
 #pragma unroll
             for (int i = 0; i < kPairs<V>; ++i) ch.add(pair_of(v, i), pair_of(d, i), i, acc[0][i], acc[1][i]);
         };
@@ -426,30 +493,19 @@ __global__ void __launch_bounds__(kThreads, 3) norm_bwd_chip(NormArgs a, const T
     if (s.rank == 0)
         for (int c = threadIdx.x; c < 2 * s.SC; c += kThreads)
             sums[int64_t(s.b) * 2 * a.C + (c < s.SC ? s.c0 + c : a.C + s.c0 + c - s.SC)] = s_sum[c];
-    for (int c = threadIdx.x; c < 2 * s.SC; c += kThreads) s_part[c] = s_sum[c] * a.gamma[s.c0 + (c < s.SC ? c : c - s.SC)];
-    __syncthreads();
-    const float inv = s.n > 0 ? 1.f / (float(s.n) * float(a.per)) : 0.f;
-    group_sums(groups, a.per, s_part, [&](int g, float v) { s_m1[g] = v * inv; });
-    group_sums(groups, a.per, s_part + s.SC, [&](int g, float v) { s_m2[g] = v * inv; });
-    __syncthreads();
+    group_means(a, s.SC, s.n, s_sum, s_sum + s.SC, s_ch + 2 * pad, s_m1, s_m2);
     T* os = dx + s.r0 * a.C + s.c0;
-    over_columns(
-        s.SC / V,
-        [&](int cv, int rl, int par) {
-            const BwdChannel<V, ACT> ch(a, s.b, s.c0 + cv * V);
-            Channels<V> m1, m2;
-            m1.set(cv * V, a.per, [&](int, int g) { return -s_m1[g]; });
-            m2.set(cv * V, a.per, [&](int, int g) { return -s_m2[g]; });
-#pragma unroll 1
-            for (int r = rl; r < s.rows; r += par) {
-                const Vec<T, V> v = row(s_x, xs, r, cv), d = row(s_d, ds, r, cv);
+    co.each([&](int cv) {
+            const BwdChannel<V, ACT> ch(s_ch, pad, cv);
+            const Channels<V> m1(s_m1 + cv * V), m2(s_m2 + cv * V);
+            each_row(co, held, s.rows, [&](int r, auto on_chip) {
+                const Vec<T, V> v = row(s_x, xs, r, cv, on_chip), d = row(s_d, ds, r, cv, on_chip);
                 Vec<T, V> o;
 #pragma unroll
                 for (int i = 0; i < kPairs<V>; ++i) put_pair(o, i, ch.dx(pair_of(v, i), pair_of(d, i), i, m1.v[i], m2.v[i]));
                 store_vec<T, V>(os + int64_t(r) * a.C + cv * V, o);
-            }
-        },
-        [](int, int, int) {});
+            });
+    });
     __syncwarp();
     if (s.K > 1) cg::this_cluster().barrier_wait();
 }
@@ -462,15 +518,17 @@ __global__ void __launch_bounds__(kThreads) norm_tile_stats(NormArgs a, const T*
     extern __shared__ __align__(16) unsigned char smem[];
     T* s_x = reinterpret_cast<T*>(smem);
     float* s_part = reinterpret_cast<float*>(smem + (size_t(a.R) * a.C * sizeof(T) + 15) / 16 * 16);
-    float *s_chan = s_part + max(kThreads * V, a.C), *s_mean = s_chan + a.C;
+    const int pad = (a.C + 3) & ~3;  // arrays per channel begin on 16 bytes
+    float *s_chan = s_part + kThreads * V, *s_minus = s_chan + pad, *s_mean = s_minus + pad;
     int64_t r0, r1;
     const int b = tile_graph(a.offsets, a.graphs, a.R, blockIdx.x, r0, r1);
     if (b < 0) return;
     const int rows = int(r1 - r0);
-    stage_rows<T, V>(s_x, x + r0 * a.C, rows, a.C, a.C);
+    const Columns<V> co(a, a.C);
+    stage_rows<T, V>(co, s_x, x + r0 * a.C, rows, a.C, a.C);
     stage_wait();
-    channel_sums<V, 1>(rows, a.C, s_part, s_chan, [&](int cv) {
-        return [&, cv](int r, F2 (&acc)[1][kPairs<V>]) {
+    channel_sums<V, 1>(co, rows, rows, a.C, s_part, s_chan, [&](int cv) {
+        return [&, cv](int r, auto on_chip, F2 (&acc)[1][kPairs<V>]) {
             const Vec<T, V> v = load_vec<T, V>(s_x + r * a.C + cv * V);
 #pragma unroll
             for (int i = 0; i < kPairs<V>; ++i) acc[0][i] = acc[0][i] + pair_of(v, i);
@@ -479,10 +537,10 @@ __global__ void __launch_bounds__(kThreads) norm_tile_stats(NormArgs a, const T*
     const float inv = 1.f / (float(rows) * float(a.per));
     group_sums(a.G, a.per, s_chan, [&](int g, float v) { s_mean[g] = v * inv; });
     __syncthreads();
-    channel_sums<V, 1>(rows, a.C, s_part, s_chan, [&](int cv) {
-        Channels<V> minus;
-        minus.set(cv * V, a.per, [&](int, int g) { return -s_mean[g]; });
-        return [&, cv, minus](int r, F2 (&acc)[1][kPairs<V>]) {
+    fill_channels(a.C, [&](int c) { s_minus[c] = -s_mean[a.by_per(c)]; });
+    channel_sums<V, 1>(co, rows, rows, a.C, s_part, s_chan, [&](int cv) {
+        const Channels<V> minus(s_minus + cv * V);
+        return [&, cv, minus](int r, auto on_chip, F2 (&acc)[1][kPairs<V>]) {
             const Vec<T, V> v = load_vec<T, V>(s_x + r * a.C + cv * V);
 #pragma unroll
             for (int i = 0; i < kPairs<V>; ++i) {
@@ -499,9 +557,9 @@ __global__ void __launch_bounds__(kThreads) norm_tile_stats(NormArgs a, const T*
 }
 
 // Forward, pass 2: Chan's merge of a graph's tiles, one block per (graph, group): each thread merges
-// every 256th tile in order, then pairwise within warps and over the warps.
-__global__ void __launch_bounds__(kThreads) norm_merge(NormArgs a, const float* __restrict__ ws) {
-    __shared__ float s_w[3][kThreads / 32];
+// every kMergeThreads-th tile in order, then pairwise within warps and over the warps.
+__global__ void __launch_bounds__(kMergeThreads) norm_merge(NormArgs a, const float* __restrict__ ws) {
+    __shared__ float s_w[3][kMergeThreads / 32];
     const int64_t i = blockIdx.x;
     const int b = int(i / a.G), g = int(i % a.G);
     const int64_t r0 = a.offsets[b], n = a.offsets[b + 1] - r0;
@@ -515,7 +573,7 @@ __global__ void __launch_bounds__(kThreads) norm_merge(NormArgs a, const float* 
             cnt = tot;
         }
     };
-    for (int64_t t = threadIdx.x; t < tiles; t += kThreads) {
+    for (int64_t t = threadIdx.x; t < tiles; t += kMergeThreads) {
         const float2 o = *reinterpret_cast<const float2*>(ws + ((t0 + t) * a.G + g) * 2);
         merge(float(min(int64_t(a.R), n - t * a.R)) * float(a.per), o.x, o.y);
     }
@@ -531,9 +589,9 @@ __global__ void __launch_bounds__(kThreads) norm_merge(NormArgs a, const float* 
     if (lane == 0) s_w[0][w] = cnt, s_w[1][w] = mean, s_w[2][w] = m2;
     __syncthreads();
     if (w > 0) return;
-    const bool on = lane < kThreads / 32;
+    const bool on = lane < kMergeThreads / 32;
     cnt = on ? s_w[0][lane] : 0.f, mean = on ? s_w[1][lane] : 0.f, m2 = on ? s_w[2][lane] : 0.f;
-    lanes(kThreads / 64);
+    lanes(kMergeThreads / 64);
     if (lane == 0) {
         a.mean[i] = mean;
         a.rstd[i] = rsqrtf((cnt > 0.f ? m2 / cnt : 0.f) + a.eps);
@@ -543,22 +601,26 @@ __global__ void __launch_bounds__(kThreads) norm_merge(NormArgs a, const float* 
 // Forward, pass 3: y of a tile, the last tiles first.
 template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kThreads) norm_apply(NormArgs a, const T* __restrict__ x, T* __restrict__ y) {
+    extern __shared__ __align__(16) float s_minus[];
+    const int pad = (a.C + 3) & ~3;  // arrays per channel begin on 16 bytes
+    float *s_k = s_minus + pad, *s_beta = s_k + pad;
     int64_t r0, r1;
     const int b = tile_graph(a.offsets, a.graphs, a.R, gridDim.x - 1 - blockIdx.x, r0, r1);
     if (b < 0) return;
     const T* xt = x + r0 * a.C;
     T* yt = y + r0 * a.C;
     const int rows = int(r1 - r0);
-    over_columns(
-        a.C / V,
-        [&](int cv, int rl, int par) {
-            const int64_t g0 = int64_t(b) * a.G;
-            Channels<V> minus, k, beta;
-            minus.set(cv * V, a.per, [&](int, int g) { return -a.mean[g0 + g]; });
-            k.set(cv * V, a.per, [&](int i, int g) { return a.rstd[g0 + g] * a.gamma[cv * V + i]; });
-            beta.set(cv * V, a.per, [&](int i, int) { return a.beta[cv * V + i]; });
+    fill_channels(a.C, [&](int c) {
+        const int64_t g = int64_t(b) * a.G + a.by_per(c);
+        s_minus[c] = -a.mean[g];
+        s_k[c] = a.rstd[g] * a.gamma[c];
+        s_beta[c] = a.beta[c];
+    });
+    const Columns<V> co(a, a.C);
+    co.each([&](int cv) {
+            const Channels<V> minus(s_minus + cv * V), k(s_k + cv * V), beta(s_beta + cv * V);
 #pragma unroll 4
-            for (int r = rl; r < rows; r += par) {
+            for (int r = co.rl; r < rows; r += co.par) {
                 const Vec<T, V> v = load_vec<T, V>(xt + int64_t(r) * a.C + cv * V);
                 Vec<T, V> o;
 #pragma unroll
@@ -566,23 +628,25 @@ __global__ void __launch_bounds__(kThreads) norm_apply(NormArgs a, const T* __re
                     put_pair(o, i, act_of<ACT>(fma2(pair_of(v, i) + minus.v[i], k.v[i], beta.v[i])));
                 store_vec<T, V>(yt + int64_t(r) * a.C + cv * V, o);
             }
-        },
-        [](int, int, int) {});
+    });
 }
 
 // Backward, pass 1: per-channel sums of dz and dz xh of each tile, ws[t][2][C].
 template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kThreads) norm_bwd_tile_sums(NormArgs a, const T* __restrict__ x, const T* __restrict__ dy,
                                                                float* __restrict__ ws) {
-    extern __shared__ __align__(16) float s_part[];  // [2 max(kThreads V, C)], then the sums [2 C]
-    float* s_chan = s_part + 2 * max(kThreads * V, a.C);
+    extern __shared__ __align__(16) float s_part[];  // [2 kThreads V], the sums [2 pad], the channels [4 pad]
+    const int pad = (a.C + 3) & ~3;                   // arrays per channel begin on 16 bytes
+    float *s_chan = s_part + 2 * kThreads * V, *s_ch = s_chan + 2 * pad;
     int64_t r0, r1;
     const int b = tile_graph(a.offsets, a.graphs, a.R, blockIdx.x, r0, r1);
     if (b < 0) return;
     const T *xt = x + r0 * a.C, *gt = dy + r0 * a.C;
-    channel_sums<V, 2>(int(r1 - r0), a.C, s_part, s_chan, [&](int cv) {
-        const BwdChannel<V, ACT> ch(a, b, cv * V);
-        return [&, cv, ch](int r, F2 (&acc)[2][kPairs<V>]) {
+    BwdChannel<V, ACT>::fill(a, b, 0, a.C, s_ch, pad);
+    const Columns<V> co(a, a.C);
+    channel_sums<V, 2>(co, 0, int(r1 - r0), a.C, s_part, s_chan, [&](int cv) {
+        const BwdChannel<V, ACT> ch(s_ch, pad, cv);
+        return [&, cv, ch](int r, auto on_chip, F2 (&acc)[2][kPairs<V>]) {
             const Vec<T, V> v = load_vec<T, V>(xt + int64_t(r) * a.C + cv * V), d = load_vec<T, V>(gt + int64_t(r) * a.C + cv * V);
 #pragma unroll
             for (int i = 0; i < kPairs<V>; ++i) ch.add(pair_of(v, i), pair_of(d, i), i, acc[0][i], acc[1][i]);
@@ -594,8 +658,8 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_tile_sums(NormArgs a, const
 
 // Backward, pass 2: a graph's channel sums over its tiles to sums[b][2][C]: 32 channels a block, the
 // warps share the tiles, then add in order.
-__global__ void __launch_bounds__(kThreads) norm_bwd_merge(NormArgs a, const float* __restrict__ ws, float* __restrict__ sums) {
-    __shared__ float s[kThreads / 32][32];
+__global__ void __launch_bounds__(kMergeThreads) norm_bwd_merge(NormArgs a, const float* __restrict__ ws, float* __restrict__ sums) {
+    __shared__ float s[kMergeThreads / 32][32];
     const int per_graph = (2 * a.C + 31) / 32;
     const int b = int(blockIdx.x / per_graph), lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = int(blockIdx.x % per_graph) * 32 + lane;
@@ -604,14 +668,14 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_merge(NormArgs a, const flo
     float acc = 0.f;
     if (c < 2 * a.C) {
 #pragma unroll 4
-        for (int64_t t = w; t < tiles; t += kThreads / 32) acc += ws[(t0 + t) * 2 * a.C + c];
+        for (int64_t t = w; t < tiles; t += kMergeThreads / 32) acc += ws[(t0 + t) * 2 * a.C + c];
     }
     s[w][lane] = acc;
     __syncthreads();
     if (w == 0 && c < 2 * a.C) {
         float t = 0.f;
 #pragma unroll
-        for (int k = 0; k < kThreads / 32; ++k) t += s[k][lane];
+        for (int k = 0; k < kMergeThreads / 32; ++k) t += s[k][lane];
         sums[int64_t(b) * 2 * a.C + c] = t;
     }
 }
@@ -620,37 +684,31 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_merge(NormArgs a, const flo
 template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kThreads) norm_bwd_apply(NormArgs a, const T* __restrict__ x, const T* __restrict__ dy,
                                                            const float* __restrict__ sums, T* __restrict__ dx) {
-    extern __shared__ __align__(16) float s_t[];  // gamma times the sums [2 C], then the groups' means [2 G]
-    float *s_m1 = s_t + 2 * a.C, *s_m2 = s_m1 + a.G;
+    extern __shared__ __align__(16) float s_ch[];  // the channels [4 pad], the means of t and t xh per channel [2 pad]
+    const int pad = (a.C + 3) & ~3;                // arrays per channel begin on 16 bytes
+    float *s_m1 = s_ch + 4 * pad, *s_m2 = s_m1 + pad;
     int64_t r0, r1;
     const int b = tile_graph(a.offsets, a.graphs, a.R, gridDim.x - 1 - blockIdx.x, r0, r1);
     if (b < 0) return;
-    const float inv = 1.f / (float(a.offsets[b + 1] - a.offsets[b]) * float(a.per));
-    for (int c = threadIdx.x; c < 2 * a.C; c += kThreads) s_t[c] = sums[int64_t(b) * 2 * a.C + c] * a.gamma[c < a.C ? c : c - a.C];
-    __syncthreads();
-    group_sums(a.G, a.per, s_t, [&](int g, float v) { s_m1[g] = v * inv; });
-    group_sums(a.G, a.per, s_t + a.C, [&](int g, float v) { s_m2[g] = v * inv; });
-    __syncthreads();
+    BwdChannel<V, ACT>::fill(a, b, 0, a.C, s_ch, pad);
+    const float* sum = sums + int64_t(b) * 2 * a.C;
+    group_means(a, a.C, a.offsets[b + 1] - a.offsets[b], sum, sum + a.C, s_ch + 2 * pad, s_m1, s_m2);
     const T *xt = x + r0 * a.C, *gt = dy + r0 * a.C;
     T* ot = dx + r0 * a.C;
     const int rows = int(r1 - r0);
-    over_columns(
-        a.C / V,
-        [&](int cv, int rl, int par) {
-            const BwdChannel<V, ACT> ch(a, b, cv * V);
-            Channels<V> m1, m2;
-            m1.set(cv * V, a.per, [&](int, int g) { return -s_m1[g]; });
-            m2.set(cv * V, a.per, [&](int, int g) { return -s_m2[g]; });
+    const Columns<V> co(a, a.C);
+    co.each([&](int cv) {
+            const BwdChannel<V, ACT> ch(s_ch, pad, cv);
+            const Channels<V> m1(s_m1 + cv * V), m2(s_m2 + cv * V);
 #pragma unroll 2
-            for (int r = rl; r < rows; r += par) {
+            for (int r = co.rl; r < rows; r += co.par) {
                 const Vec<T, V> v = load_vec<T, V>(xt + int64_t(r) * a.C + cv * V), d = load_vec<T, V>(gt + int64_t(r) * a.C + cv * V);
                 Vec<T, V> o;
 #pragma unroll
                 for (int i = 0; i < kPairs<V>; ++i) put_pair(o, i, ch.dx(pair_of(v, i), pair_of(d, i), i, m1.v[i], m2.v[i]));
                 store_vec<T, V>(ot + int64_t(r) * a.C + cv * V, o);
             }
-        },
-        [](int, int, int) {});
+    });
 }
 
 // dgamma and dbeta: the graphs' channel sums added up, 32 of the 2 C sums a block; the warps share
@@ -692,23 +750,29 @@ struct Form {
     int64_t tiles;    // tiled
 };
 
+// Shared memory of a block of the on-chip form beside its rows.
+size_t chip_fixed(bool bwd, int slab, int per, int V) {
+    const size_t pad = (size_t(slab) + 3) & ~size_t(3);
+    return 32 + (bwd ? 2 * size_t(kThreads) * V + 10 * pad : size_t(kThreads) * V + 4 * pad + 4 * size_t(slab / per)) * 4;
+}
+
 // The slab is the least run of whole groups of at least 128 bytes (a full line of each row).  The
-// cluster is the smallest whose blocks hold the longest graph in kSmall bytes each (several blocks per
-// SM overlap one another's phases), else in kLarge bytes; with fewer blocks than SMs it grows while
-// a block keeps 64 rows.
+// cluster is the smallest whose blocks hold the longest graph, several blocks to an SM if possible (they
+// overlap one another's phases); with fewer blocks than SMs it grows while a block keeps 64 rows.
 Form form_of(const NormShape& s, bool bwd, int sms) {
-    const size_t kSmall = bwd ? 56 << 10 : 40 << 10, kLarge = 160 << 10;
-    const size_t e = elem_bytes(s.dtype), operands = bwd ? 2 : 1;
+    const size_t e = elem_bytes(s.dtype);
     const int V = int(16 / e), per = s.channels / s.groups;
+    // shared memory of a block: four (backward: three, its registers' limit) per SM, or one
+    const size_t rooms[2] = {bwd ? 74 << 10 : 56 << 10, 224 << 10};
     Form f = {};
     const int64_t unit = s.channels % V == 0 ? std::lcm(per, V) : per;
     const int64_t want = (int64_t(128 / e) + unit - 1) / unit * unit;
     f.slab = int(std::min<int64_t>(want, s.channels));
     f.slabs = (s.channels + f.slab - 1) / f.slab;
-    const size_t row = size_t(f.slab) * e * operands;
+    const size_t row = size_t(f.slab) * e * (bwd ? 2 : 1), fixed = chip_fixed(bwd, f.slab, per, V);
     const int64_t blocks = int64_t(s.graphs) * f.slabs, longest = std::max<int64_t>(s.max_rows, 1);
-    for (size_t room : {kSmall, kLarge}) {
-        const int64_t R = int64_t(room / row), K = R > 0 ? (longest + R - 1) / R : 9;
+    for (size_t room : rooms) {
+        const int64_t R = room > fixed ? int64_t((room - fixed) / row) : 0, K = R > 0 ? (longest + R - 1) / R : 9;
         if (f.chip || K > 8) continue;
         f.chip = true;
         f.K = int(K);
@@ -746,40 +810,49 @@ cudaError_t launch_cluster(void (*k)(P...), int64_t blocks, int K, size_t smem, 
     return cudaLaunchKernelEx(&c, k, static_cast<P>(args)...);
 }
 
+void set_form(NormArgs& a, const Form& f, int V) {
+    a.R = f.R, a.slab = f.slab, a.slabs = f.slabs, a.size = f.chip ? f.K : 1;
+    a.lanes = std::min((f.chip ? f.slab : a.C) / V, kThreads);
+    a.par = kThreads / a.lanes;
+    a.by_per = Div::by(a.per), a.by_slabs = Div::by(std::max(a.slabs, 1)), a.by_size = Div::by(a.size), a.by_lanes = Div::by(a.lanes);
+}
+
 template <typename T, int V, int ACT>
 cudaError_t fwd(NormArgs a, const Form& f, const T* x, T* y, float* ws, cudaStream_t st) {
-    a.R = f.R, a.slab = f.slab, a.slabs = f.slabs;
+    set_form(a, f, V);
     if (f.chip) {
-        const size_t sm = (size_t(f.R) * f.slab * sizeof(T) + 15) / 16 * 16 +
-                          (size_t(std::max(kThreads * V, f.slab)) + f.slab + 4 * (f.slab / a.per)) * 4;
+        const size_t sm = (size_t(f.R) * f.slab * sizeof(T) + 15) / 16 * 16 + chip_fixed(false, f.slab, a.per, V);
         return launch_cluster(norm_fwd_chip<T, V, ACT>, int64_t(a.graphs) * f.slabs * f.K, f.K, sm, st, a, x, y);
     }
-    const size_t sm = (size_t(f.R) * a.C * sizeof(T) + 15) / 16 * 16 + (size_t(std::max(kThreads * V, a.C)) + a.C + a.G) * 4;
+    const int pad = (a.C + 3) & ~3;
+    const size_t sm = (size_t(f.R) * a.C * sizeof(T) + 15) / 16 * 16 + (size_t(kThreads) * V + 2 * pad + a.G) * 4,
+                 sm3 = size_t(pad) * 12;
     cudaError_t e = allow_smem(norm_tile_stats<T, V>, sm);
+    if (e == cudaSuccess) e = allow_smem(norm_apply<T, V, ACT>, sm3);
     if (e != cudaSuccess) return e;
     norm_tile_stats<T, V><<<unsigned(f.tiles), kThreads, sm, st>>>(a, x, ws);
-    norm_merge<<<unsigned(int64_t(a.graphs) * a.G), kThreads, 0, st>>>(a, ws);
-    norm_apply<T, V, ACT><<<unsigned(f.tiles), kThreads, 0, st>>>(a, x, y);
+    norm_merge<<<unsigned(int64_t(a.graphs) * a.G), kMergeThreads, 0, st>>>(a, ws);
+    norm_apply<T, V, ACT><<<unsigned(f.tiles), kThreads, sm3, st>>>(a, x, y);
     return cudaGetLastError();
 }
 
 template <typename T, int V, int ACT>
 cudaError_t bwd(NormArgs a, const Form& f, const T* x, const T* dy, T* dx, float* dgamma, float* dbeta, float* ws, cudaStream_t st) {
-    a.R = f.R, a.slab = f.slab, a.slabs = f.slabs;
+    set_form(a, f, V);
     float* sums = ws;
     cudaError_t e = cudaSuccess;
     if (f.chip) {
-        const size_t sm = (size_t(f.R) * f.slab * sizeof(T) + 15) / 16 * 32 +
-                          (2 * size_t(std::max(kThreads * V, f.slab)) + 4 * f.slab + 2 * (f.slab / a.per)) * 4;
+        const size_t sm = (size_t(f.R) * f.slab * sizeof(T) + 15) / 16 * 32 + chip_fixed(true, f.slab, a.per, V);
         e = launch_cluster(norm_bwd_chip<T, V, ACT>, int64_t(a.graphs) * f.slabs * f.K, f.K, sm, st, a, x, dy, dx, sums);
     } else {
         float* tiles = ws + align256(size_t(a.graphs) * 2 * a.C * 4) / 4;
-        const size_t sm = (size_t(std::max(kThreads * V, a.C)) * 2 + 2 * size_t(a.C)) * 4, sm3 = (2 * size_t(a.C) + 2 * size_t(a.G)) * 4;
+        const int pad = (a.C + 3) & ~3;
+        const size_t sm = (2 * size_t(kThreads) * V + 6 * size_t(pad)) * 4, sm3 = 6 * size_t(pad) * 4;
         e = allow_smem(norm_bwd_tile_sums<T, V, ACT>, sm);
         if (e == cudaSuccess) e = allow_smem(norm_bwd_apply<T, V, ACT>, sm3);
         if (e != cudaSuccess) return e;
         norm_bwd_tile_sums<T, V, ACT><<<unsigned(f.tiles), kThreads, sm, st>>>(a, x, dy, tiles);
-        norm_bwd_merge<<<unsigned(int64_t(a.graphs) * ((2 * a.C + 31) / 32)), kThreads, 0, st>>>(a, tiles, sums);
+        norm_bwd_merge<<<unsigned(int64_t(a.graphs) * ((2 * a.C + 31) / 32)), kMergeThreads, 0, st>>>(a, tiles, sums);
         norm_bwd_apply<T, V, ACT><<<unsigned(f.tiles), kThreads, sm3, st>>>(a, x, dy, sums, dx);
     }
     if (e != cudaSuccess) return e;

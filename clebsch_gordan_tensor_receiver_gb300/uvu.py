@@ -484,60 +484,86 @@ class Graph:
 
 
 # ------------------------------------------------------------------- node-update operators
+#
+# The smallest of these kernels run for 3 us, so the wrappers check what the C ABI cannot see from a
+# pointer (type, device, shape, strides) and little else: a call costs the host 6 to 9 us.
+
+_CODES = {}  # torch dtype -> uvu_dtype
+
 
 def _block_dtype(t) -> int:
-    import torch
-    code = {torch.float32: UVU_F32, torch.bfloat16: UVU_BF16, torch.float16: UVU_F16, torch.float64: UVU_F64}.get(t.dtype)
+    code = _CODES.get(t.dtype)
     if code is None:
-        raise TypeError(f"the node-update operators take float32, bfloat16 and float16 tensors, not {t.dtype}")
+        import torch
+        _CODES.update({torch.float32: UVU_F32, torch.bfloat16: UVU_BF16, torch.float16: UVU_F16, torch.float64: UVU_F64})
+        code = _CODES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"the node-update operators take float32, bfloat16 and float16 tensors, not {t.dtype}")
     return code
 
 
-def _same(name, t, like, shape=None):
-    """The checks that the C ABI cannot make from a pointer: type, device, shape, contiguity."""
-    if t.dtype != like.dtype or t.device != like.device:
+def _like(name, t, x):
+    """t has x's type, device and shape and is contiguous."""
+    if t.dtype != x.dtype or t.get_device() != x.get_device():
         raise TypeError(f"{name} must have the type and device of its operands")
-    if shape is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.shape != x.shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(x.shape)}, not {tuple(t.shape)}")
 
 
 def _f32(name, t, shape, device):
-    import torch
-    if t.dtype != torch.float32 or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if _CODES.get(t.dtype) != UVU_F32 or t.get_device() != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)} on the operands' device")
 
 
 def _offsets(name, t, device):
+    """Number of graphs of an offsets tensor."""
     import torch
-    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or t.numel() < 2 or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.get_device() != device or t.dim() != 1 or t.numel() < 2 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor [n_graphs + 1] on the operands' device")
+    return t.numel() - 1
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream):
+def _raw_stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _scratch(need, workspace, device):
+    """(pointer, bytes) of a workspace: the caller's, or one from torch."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        import torch
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def group_norm_workspace_bytes(x, n_graphs, groups, max_rows=None):
     """(forward bytes, backward bytes) of device workspace for the group norm of x [N][C]."""
     f, b = ctypes.c_size_t(), ctypes.c_size_t()
-    uvu_group_norm_workspace(_block_dtype(x), x.shape[0], n_graphs, x.shape[0] if max_rows is None else max_rows, x.shape[1],
-                             groups, ctypes.byref(f), ctypes.byref(b))
+    n, c = x.shape
+    uvu_group_norm_workspace(_block_dtype(x), n, n_graphs, n if max_rows is None else max_rows, c, groups, ctypes.byref(f),
+                             ctypes.byref(b))
     return f.value, b.value
 
 
 def _norm_checks(x, gamma, beta, offsets, groups, mean, rstd):
+    code, dev = _block_dtype(x), x.get_device()
     if x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be contiguous [rows][channels]")
-    _offsets("offsets", offsets, x.device)
-    for name, t in (("gamma", gamma), ("beta", beta)):
-        _f32(name, t, (x.shape[1],), x.device)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _f32(name, t, (offsets.numel() - 1, groups), x.device)
+    n, c = x.shape
+    b = _offsets("offsets", offsets, dev)
+    _f32("gamma", gamma, (c,), dev)
+    _f32("beta", beta, (c,), dev)
+    _f32("mean", mean, (b, groups), dev)
+    _f32("rstd", rstd, (b, groups), dev)
+    return code, dev, n, c, b
 
 
 def group_norm_fwd(x, gamma, beta, offsets, groups, y, mean, rstd, act=UVU_ACT_SILU, eps=1e-5, max_rows=None,
@@ -545,59 +571,59 @@ def group_norm_fwd(x, gamma, beta, offsets, groups, y, mean, rstd, act=UVU_ACT_S
     """Group norm with an activation over a packed batch (see uvu_group_norm_fwd): x, y [N][C], offsets
     [B+1] int32, mean and rstd [B][groups] fp32 (outputs); `workspace` (uint8) is allocated here with
     torch if None."""
-    import torch
-    _norm_checks(x, gamma, beta, offsets, groups, mean, rstd)
-    _same("y", y, x, x.shape)
-    n, b = x.shape[0], offsets.numel() - 1
+    code, dev, n, c, b = _norm_checks(x, gamma, beta, offsets, groups, mean, rstd)
+    _like("y", y, x)
     most = n if max_rows is None else max_rows
-    if workspace is None:
-        workspace = torch.empty(max(16, group_norm_workspace_bytes(x, b, groups, most)[0]), dtype=torch.uint8, device=x.device)
-    uvu_group_norm_fwd(_block_dtype(x), n, b, most, x.shape[1], groups, act, eps, _at(offsets), _at(x), _at(gamma), _at(beta),
-                       _at(y), _at(mean), _at(rstd), _at(workspace), workspace.numel(), _raw_stream(stream))
+    need = group_norm_workspace_bytes(x, b, groups, most)[0] if workspace is None else 0
+    ws, size, held = _scratch(need, workspace, x.device)
+    uvu_group_norm_fwd(code, n, b, most, c, groups, act, eps, offsets.data_ptr(), x.data_ptr(), gamma.data_ptr(),
+                       beta.data_ptr(), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), ws, size, _raw_stream(stream, dev))
 
 
 def group_norm_bwd(dy, x, gamma, beta, offsets, groups, mean, rstd, dx, dgamma, dbeta, act=UVU_ACT_SILU, max_rows=None,
                    workspace=None, stream=None):
     """VJP of group_norm_fwd (see uvu_group_norm_bwd)."""
-    import torch
-    _norm_checks(x, gamma, beta, offsets, groups, mean, rstd)
-    _same("dy", dy, x, x.shape)
-    _same("dx", dx, x, x.shape)
-    _f32("dgamma", dgamma, gamma.shape, x.device)
-    _f32("dbeta", dbeta, gamma.shape, x.device)
-    n, b = x.shape[0], offsets.numel() - 1
+    code, dev, n, c, b = _norm_checks(x, gamma, beta, offsets, groups, mean, rstd)
+    _like("dy", dy, x)
+    _like("dx", dx, x)
+    _f32("dgamma", dgamma, (c,), dev)
+    _f32("dbeta", dbeta, (c,), dev)
     most = n if max_rows is None else max_rows
-    if workspace is None:
-        workspace = torch.empty(max(16, group_norm_workspace_bytes(x, b, groups, most)[1]), dtype=torch.uint8, device=x.device)
-    uvu_group_norm_bwd(_block_dtype(x), n, b, most, x.shape[1], groups, act, _at(offsets), _at(x), _at(gamma), _at(beta),
-                       _at(mean), _at(rstd), _at(dy), _at(dx), _at(dgamma), _at(dbeta), _at(workspace), workspace.numel(),
-                       _raw_stream(stream))
+    need = group_norm_workspace_bytes(x, b, groups, most)[1] if workspace is None else 0
+    ws, size, held = _scratch(need, workspace, x.device)
+    uvu_group_norm_bwd(code, n, b, most, c, groups, act, offsets.data_ptr(), x.data_ptr(), gamma.data_ptr(), beta.data_ptr(),
+                       mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(), dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
+                       ws, size, _raw_stream(stream, dev))
 
 
 def _draws(x, inner):
-    if inner < 1 or x.numel() % inner:
+    n = x.numel()
+    if inner < 1 or n % inner:
         raise ValueError("the tensor's size must be a multiple of inner >= 1")
-    return x.numel() // inner
+    return n // inner
 
 
 def dropout_fwd(x, p, seed, y, offset=0, inner=1, residual=None, stream=None):
     """y = residual + dropout(x) with the mask of (seed, offset); `inner` consecutive values share a draw
     (see uvu_dropout_fwd).  All tensors contiguous and of one shape; y may be x or residual."""
+    code = _block_dtype(x)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    _same("y", y, x, x.shape)
+    _like("y", y, x)
     if residual is not None:
-        _same("residual", residual, x, x.shape)
-    uvu_dropout_fwd(_block_dtype(x), _draws(x, inner), inner, p, seed, offset, _at(x), _at(residual), _at(y),
-                    _raw_stream(stream))
+        _like("residual", residual, x)
+    uvu_dropout_fwd(code, _draws(x, inner), inner, p, seed, offset, x.data_ptr(), _at(residual), y.data_ptr(),
+                    _raw_stream(stream, x.get_device()))
 
 
 def dropout_bwd(dy, p, seed, dx, offset=0, inner=1, stream=None):
     """VJP of dropout_fwd with respect to x; the residual's gradient is dy (see uvu_dropout_bwd)."""
+    code = _block_dtype(dy)
     if not dy.is_contiguous():
         raise ValueError("dy must be contiguous")
-    _same("dx", dx, dy, dy.shape)
-    uvu_dropout_bwd(_block_dtype(dy), _draws(dy, inner), inner, p, seed, offset, _at(dy), _at(dx), _raw_stream(stream))
+    _like("dx", dx, dy)
+    uvu_dropout_bwd(code, _draws(dy, inner), inner, p, seed, offset, dy.data_ptr(), dx.data_ptr(),
+                    _raw_stream(stream, dy.get_device()))
 
 
 class Attention:
@@ -607,43 +633,46 @@ class Attention:
     (default: all rows).  scale defaults to head_dim ** -0.5."""
 
     def __init__(self, q_heads, kv_heads, head_dim, q_offsets, k_offsets, max_q=None, max_k=None, scale=None):
-        _offsets("q_offsets", q_offsets, q_offsets.device)
-        _offsets("k_offsets", k_offsets, q_offsets.device)
-        if q_offsets.numel() != k_offsets.numel():
+        self.device = q_offsets.get_device()
+        self.n_graphs = _offsets("q_offsets", q_offsets, self.device)
+        if _offsets("k_offsets", k_offsets, self.device) != self.n_graphs:
             raise ValueError("q_offsets and k_offsets must have the same number of graphs")
         self.q_offsets, self.k_offsets = q_offsets, k_offsets
         self.q_heads, self.kv_heads, self.head_dim = int(q_heads), int(kv_heads), int(head_dim)
         self.max_q, self.max_k = max_q, max_k
         self.scale = float(head_dim) ** -0.5 if scale is None else float(scale)
 
-    def _shape(self, q, k, v, out):
-        for name, t, h in (("q", q, self.q_heads), ("k", k, self.kv_heads), ("v", v, self.kv_heads), ("out", out, self.q_heads)):
-            if t.dim() != 3 or t.shape[1] != h or t.shape[2] != self.head_dim or (t.stride(2) != 1 and t.shape[2] > 1):
-                raise ValueError(f"{name} must be [rows][{h}][{self.head_dim}] with consecutive values in a head")
-            _same(name, t, q)
-        if out.shape[0] != q.shape[0] or v.shape[0] != k.shape[0]:
-            raise ValueError("out must have q's rows and v must have k's")
-        if q.device != self.q_offsets.device:
-            raise ValueError("the operands must be on the offsets' device")
-        nq, nk = q.shape[0], k.shape[0]
-        return AttnShape(_block_dtype(q), self.q_offsets.numel() - 1, nq, nk, nq if self.max_q is None else self.max_q,
-                         nk if self.max_k is None else self.max_k, self.q_heads, self.kv_heads, self.head_dim, 0, self.scale,
-                         q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1), out.stride(0),
-                         out.stride(1))
+    def _operand(self, name, t, heads, rows, dtype):
+        """Strides of [rows][heads][head_dim] with consecutive values in a head."""
+        if t.dtype != dtype or t.get_device() != self.device:
+            raise TypeError(f"{name} must have q's type and be on the offsets' device")
+        if t.shape != (rows, heads, self.head_dim):
+            raise ValueError(f"{name} must be [{rows}][{heads}][{self.head_dim}], not {tuple(t.shape)}")
+        r, h, d = t.stride()
+        if d != 1 and self.head_dim > 1:
+            raise ValueError(f"{name} must have consecutive values in a head")
+        return r, h
 
-    def _workspace(self, shape, which, workspace, device):
-        if workspace is None:
-            import torch
-            b = [ctypes.c_size_t(), ctypes.c_size_t()]
-            uvu_attn_workspace(ctypes.byref(shape), ctypes.byref(b[0]), ctypes.byref(b[1]))
-            workspace = torch.empty(max(16, b[which].value), dtype=torch.uint8, device=device)
-        return workspace
+    def _shape(self, q, k, v, out):
+        nq, nk, dt = q.shape[0], k.shape[0], q.dtype
+        code = _block_dtype(q)
+        qr, qh = self._operand("q", q, self.q_heads, nq, dt)
+        kr, kh = self._operand("k", k, self.kv_heads, nk, dt)
+        vr, vh = self._operand("v", v, self.kv_heads, nk, dt)
+        orow, oh = self._operand("out", out, self.q_heads, nq, dt)
+        return AttnShape(code, self.n_graphs, nq, nk, nq if self.max_q is None else self.max_q,
+                         nk if self.max_k is None else self.max_k, self.q_heads, self.kv_heads, self.head_dim, 0, self.scale,
+                         qr, qh, kr, kh, vr, vh, orow, oh)
+
+    def _need(self, shape, which):
+        b = (ctypes.c_size_t(), ctypes.c_size_t())
+        uvu_attn_workspace(ctypes.byref(shape), ctypes.byref(b[0]), ctypes.byref(b[1]))
+        return b[which].value
 
     def workspace_bytes(self, q, k):
         """(forward bytes, backward bytes) of device workspace for operands of q's and k's sizes."""
-        f, b = ctypes.c_size_t(), ctypes.c_size_t()
-        uvu_attn_workspace(ctypes.byref(self._shape(q, k, k, q)), ctypes.byref(f), ctypes.byref(b))
-        return f.value, b.value
+        s = self._shape(q, k, k, q)
+        return self._need(s, 0), self._need(s, 1)
 
     @staticmethod
     def device_status(reset: bool = True) -> int:
@@ -652,31 +681,35 @@ class Attention:
         uvu_attn_device_status(ctypes.byref(w), int(reset))
         return w.value
 
-    def _keep(self, keep, k):
-        import torch
-        if keep is not None and (keep.dtype not in (torch.uint8, torch.bool) or keep.shape != k.shape[:1]
-                                 or keep.device != k.device or not keep.is_contiguous()):
+    def _keep(self, keep, nk):
+        if keep is None:
+            return None
+        if keep.element_size() != 1 or keep.dtype.is_floating_point or keep.shape != (nk,) or keep.get_device() != self.device \
+                or not keep.is_contiguous():
             raise ValueError("keep must be a contiguous uint8 or bool tensor [states] on the operands' device")
-        return _at(keep)
+        return keep.data_ptr()
 
     def fwd(self, q, k, v, out, lse, keep=None, workspace=None, stream=None):
         """out and lse [Tq][q_heads] (fp32); `keep` [Tk] (uint8 or bool): states with 0 take no part;
         `workspace` (uint8) is allocated here with torch if None."""
         s = self._shape(q, k, v, out)
-        _f32("lse", lse, q.shape[:2], q.device)
-        ws = self._workspace(s, 0, workspace, q.device)
-        uvu_attn_fwd(ctypes.byref(s), _at(self.q_offsets), _at(self.k_offsets), self._keep(keep, k), _at(q), _at(k), _at(v),
-                     _at(out), _at(lse), _at(ws), ws.numel(), _raw_stream(stream))
+        _block_dtype(lse)
+        _f32("lse", lse, (s.n_q, self.q_heads), self.device)
+        ws, size, held = _scratch(self._need(s, 0) if workspace is None else 0, workspace, q.device)
+        uvu_attn_fwd(ctypes.byref(s), self.q_offsets.data_ptr(), self.k_offsets.data_ptr(), self._keep(keep, s.n_k), q.data_ptr(),
+                     k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), ws, size, _raw_stream(stream, self.device))
 
     def bwd(self, q, k, v, out, lse, d_out, dq=None, dk=None, dv=None, keep=None, workspace=None, stream=None):
         """VJP (see uvu_attn_bwd): dq, dk, dv contiguous; dq, or dk and dv, may be None."""
         s = self._shape(q, k, v, out)
-        _f32("lse", lse, q.shape[:2], q.device)
-        if d_out.shape != out.shape or d_out.stride() != out.stride():
-            raise ValueError("d_out must have the shape and strides of out")
-        for name, t, like in (("d_out", d_out, None), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _block_dtype(lse)
+        _f32("lse", lse, (s.n_q, self.q_heads), self.device)
+        if self._operand("d_out", d_out, self.q_heads, s.n_q, q.dtype) != (s.o_row, s.o_head):
+            raise ValueError("d_out must have the strides of out")
+        for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
             if t is not None:
-                _same(name, t, q, None if like is None else like.shape)
-        ws = self._workspace(s, 1, workspace, q.device)
-        uvu_attn_bwd(ctypes.byref(s), _at(self.q_offsets), _at(self.k_offsets), self._keep(keep, k), _at(q), _at(k), _at(v),
-                     _at(out), _at(lse), _at(d_out), _at(dq), _at(dk), _at(dv), _at(ws), ws.numel(), _raw_stream(stream))
+                _like(name, t, like)
+        ws, size, held = _scratch(self._need(s, 1) if workspace is None else 0, workspace, q.device)
+        uvu_attn_bwd(ctypes.byref(s), self.q_offsets.data_ptr(), self.k_offsets.data_ptr(), self._keep(keep, s.n_k), q.data_ptr(),
+                     k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), d_out.data_ptr(), _at(dq), _at(dk), _at(dv), ws,
+                     size, _raw_stream(stream, self.device))
