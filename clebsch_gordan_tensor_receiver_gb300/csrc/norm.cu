@@ -32,7 +32,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 128, kMergeThreads = 256;
+constexpr int kThreads = 128, kMergeThreads = 256, kMaxCluster = 8;
 
 // Division of values below 2^31 by a divisor that the host knows: n / d = (n m) >> (32 + s) with
 // m = ceil(2^(32+s) / d), s = ceil(log2 d) - 1 (exact for n < 2^31: the error n (m d - 2^(32+s)) stays
@@ -118,14 +118,14 @@ __device__ __forceinline__ void put_pair(Vec<T, V>& v, int i, F2 x) {
 }
 
 // 1 / (1 + exp(-z)): 2^x and 1/x to 2 ulp each; 2^x overflows to infinity where the sigmoid is below 2^-126, and 1/inf = 0.
-__device__ __forceinline__ float sigmoid_of_scaled(float x) {  // x = -z log2(e)
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;\n\tadd.rn.f32 %0, %0, 0f3F800000;\n\trcp.approx.ftz.f32 %0, %0;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ F2 sigmoid(F2 z) {
-    const float2 e = (z * F2(-1.4426950408889634f, -1.4426950408889634f)).both();
-    return F2(sigmoid_of_scaled(e.x), sigmoid_of_scaled(e.y));
+    float2 e = (z * F2(-1.4426950408889634f, -1.4426950408889634f)).both();
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    float2 d = (F2(e.x, e.y) + F2(1.f, 1.f)).both();
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(d.y));
+    return F2(d.x, d.y);
 }
 
 // act(z), and dy act'(z)
@@ -298,7 +298,7 @@ __device__ __forceinline__ void stage_wait() {
 struct Share {  // a block's part of a graph
     int b, c0, SC, rank, rows;
     int K;  // blocks that have rows (one, if none has); the others leave at once
-    int n;
+    int n, each;  // rows of the graph, of a full share
     int64_t r0;
 };
 __device__ __forceinline__ Share share_of(const NormArgs& a) {
@@ -313,6 +313,7 @@ __device__ __forceinline__ Share share_of(const NormArgs& a) {
     // whole shares in rank order, so that short graphs need fewer blocks; a graph longer than max_rows
     // promised is shared out evenly
     const int each = s.n > a.R * a.size ? (s.n - 1) / a.size + 1 : a.R, lo = int(min(int64_t(s.n), int64_t(s.rank) * each));
+    s.each = each;
     s.r0 = first + lo;
     s.rows = min(s.n - lo, each);
     s.K = s.n > each ? (s.n - 1) / each + 1 : 1;
@@ -329,9 +330,45 @@ __device__ __forceinline__ void cluster_sums(int count, int K, float* s_group, f
         __syncwarp();
         c.sync();
         for (int i = threadIdx.x; i < count; i += kThreads) {
-            float s = 0.f;
-            for (int k = 0; k < K; ++k) s += c.map_shared_rank(s_group, k)[i];
+            float v[kMaxCluster], s = 0.f;
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k) v[k] = k < K ? c.map_shared_rank(s_group, k)[i] : 0.f;
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k) s += v[k];
             s_sum[i] = s;
+        }
+    }
+    __syncthreads();
+}
+
+// Mean and centred sum of squares of each group over the cluster, from the blocks' own (s_g: means,
+// then sums of squares), merged in rank order.
+__device__ __forceinline__ void cluster_merge(int groups, const Share& s, int per, float* s_g, float* s_mean, float* s_m2) {
+    if (s.K == 1) {
+        __syncthreads();
+        for (int g = threadIdx.x; g < groups; g += kThreads) s_mean[g] = s_g[g], s_m2[g] = s_g[groups + g];
+    } else {
+        cg::cluster_group c = cg::this_cluster();
+        __syncwarp();
+        c.sync();
+        for (int g = threadIdx.x; g < groups; g += kThreads) {
+            float m[kMaxCluster], q[kMaxCluster];
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k)
+                if (k < s.K) m[k] = c.map_shared_rank(s_g, k)[g], q[k] = c.map_shared_rank(s_g, k)[groups + g];
+            float mean = m[0], m2 = q[0];
+            int have = min(s.each, s.n);
+#pragma unroll
+            for (int k = 1; k < kMaxCluster; ++k)
+                if (k < s.K) {
+                    const int n = min(s.each, s.n - have);
+                    const float d = m[k] - mean, w = float(n) / float(have + n);
+                    mean = fmaf(d, w, mean);
+                    m2 += q[k] + d * d * (float(have) * w) * float(per);
+                    have += n;
+                }
+            s_mean[g] = mean;
+            s_m2[g] = m2;
         }
     }
     __syncthreads();
@@ -348,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_chip(NormArgs a, const T* _
     float* s_part = reinterpret_cast<float*>(smem + (size_t(a.R) * a.slab * sizeof(T) + 15) / 16 * 16);
     const int pad = (a.slab + 3) & ~3;  // arrays per channel begin on 16 bytes
     float *s_chan = s_part + kThreads * V, *s_minus = s_chan + pad, *s_k = s_minus + pad, *s_beta = s_k + pad,
-          *s_g1 = s_beta + pad, *s_g2 = s_g1 + a.by_per(a.slab), *s_mean = s_g2 + a.by_per(a.slab), *s_rstd = s_mean + a.by_per(a.slab);
+          *s_g = s_beta + pad, *s_mean = s_g + 2 * a.by_per(a.slab), *s_rstd = s_mean + a.by_per(a.slab);
     const T* xs = x + s.r0 * a.C + s.c0;
     const int held = min(s.rows, a.R);
     stage_rows<T, V>(co, s_x, xs, held, s.SC, a.C);
@@ -366,10 +403,11 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_chip(NormArgs a, const T* _
             for (int i = 0; i < kPairs<V>; ++i) acc[0][i] = acc[0][i] + pair_of(v, i);
         };
     });
-    group_sums(groups, a.per, s_chan, [&](int g, float v) { s_g1[g] = v; });
-    cluster_sums(groups, s.K, s_g1, s_mean);
-    const float inv = s.n > 0 ? 1.f / (float(s.n) * float(a.per)) : 0.f;
-    fill_channels(s.SC, [&](int c) { s_minus[c] = -s_mean[a.by_per(c)] * inv; });
+    // the block's own mean and centred sum of squares per group, then Chan's merge over the cluster: one exchange
+    const float own = s.rows > 0 ? 1.f / (float(s.rows) * float(a.per)) : 0.f;
+    group_sums(groups, a.per, s_chan, [&](int g, float v) { s_g[g] = v * own; });
+    __syncthreads();
+    fill_channels(s.SC, [&](int c) { s_minus[c] = -s_g[a.by_per(c)]; });
     channel_sums<V, 1>(co, held, s.rows, s.SC, s_part, s_chan, [&](int cv) {
         const Channels<V> minus(s_minus + cv * V);
         return [&, cv, minus](int r, auto on_chip, F2 (&acc)[1][kPairs<V>]) {
@@ -381,16 +419,18 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_chip(NormArgs a, const T* _
             }
         };
     });
-    group_sums(groups, a.per, s_chan, [&](int g, float v) { s_g2[g] = v; });
-    cluster_sums(groups, s.K, s_g2, s_rstd);
+    group_sums(groups, a.per, s_chan, [&](int g, float v) { s_g[groups + g] = v; });
+    cluster_merge(groups, s, a.per, s_g, s_mean, s_rstd);
     if (s.K > 1) cg::this_cluster().barrier_arrive();  // the other blocks' sums have been read
+    const float inv = s.n > 0 ? 1.f / (float(s.n) * float(a.per)) : 0.f;
     fill_channels(s.SC, [&](int c) {
         const int g = a.by_per(c);
         const float rstd = rsqrtf(s_rstd[g] * inv + a.eps);
+        s_minus[c] = -s_mean[g];
         s_k[c] = rstd * a.gamma[s.c0 + c];
         s_beta[c] = a.beta[s.c0 + c];
         if (s.rank == 0 && c == g * a.per) {
-            a.mean[int64_t(s.b) * a.G + g0 + g] = s_mean[g] * inv;
+            a.mean[int64_t(s.b) * a.G + g0 + g] = s_mean[g];
             a.rstd[int64_t(s.b) * a.G + g0 + g] = rstd;
         }
     });
@@ -772,11 +812,11 @@ Form form_of(const NormShape& s, bool bwd, int sms) {
     const size_t row = size_t(f.slab) * e * (bwd ? 2 : 1), fixed = chip_fixed(bwd, f.slab, per, V);
     const int64_t blocks = int64_t(s.graphs) * f.slabs, longest = std::max<int64_t>(s.max_rows, 1);
     for (size_t room : rooms) {
-        const int64_t R = room > fixed ? int64_t((room - fixed) / row) : 0, K = R > 0 ? (longest + R - 1) / R : 9;
-        if (f.chip || K > 8) continue;
+        const int64_t R = room > fixed ? int64_t((room - fixed) / row) : 0, K = R > 0 ? (longest + R - 1) / R : kMaxCluster + 1;
+        if (f.chip || K > kMaxCluster) continue;
         f.chip = true;
         f.K = int(K);
-        while (f.K < 8 && blocks * (f.K + 1) <= sms && longest >= 64 * (f.K + 1)) ++f.K;
+        while (f.K < kMaxCluster && blocks * (f.K + 1) <= sms && longest >= 64 * (f.K + 1)) ++f.K;
         f.R = int((longest + f.K - 1) / f.K);
     }
     f.chip = f.chip && blocks * f.K < (int64_t(1) << 31);
