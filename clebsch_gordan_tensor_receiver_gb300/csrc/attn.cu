@@ -369,10 +369,13 @@ int splits_for(int64_t tiles, int64_t inner, int R, int sms) {
 int64_t row_tiles(const AttnShape& s, int R) { return s.n_q * (s.q_heads / s.kv_heads) / R + s.n_graphs; }
 int64_t state_tiles(const AttnShape& s, int R) { return s.n_k / R + s.n_graphs; }
 
+enum class Engine { kCuda, kMma, kPlanes };
 struct Choice {
-    int nt;            // row tiles of 128 per block of the 16-bit forward; 0: CUDA cores
+    Engine engine;
+    int nt;             // row tiles of 128 per block of the 16-bit forward
+    int R;              // rows or states of a tile
     int64_t fwd_tiles;  // tile numbers of the forward
-    int fwd, dq, dkv;  // splits
+    int fwd, dq, dkv;   // splits
 };
 Choice choose(const AttnShape& s, int sms) {
     const int64_t group = s.q_heads / s.kv_heads;
@@ -384,13 +387,13 @@ Choice choose(const AttnShape& s, int sms) {
         return std::min(state_tiles(s, R), int64_t(s.n_graphs) * ((s.max_k + R - 1) / R)) * s.kv_heads;
     };
     Choice c;
-    c.nt = s.dtype == UVU_F32 ? 0 : rows_busy(256) >= sms && s.max_q * group > 128 ? 2 : 1;
-    const int R = c.nt ? 128 * c.nt : kT;
-    c.fwd_tiles = row_tiles(s, R);
-    c.fwd = splits_for(rows_busy(R), s.max_k, c.nt ? 128 : kT, sms);
-    const int B = c.nt ? 128 : kT;  // tile of the backward
-    c.dq = splits_for(rows_busy(B), s.max_k, B, sms);
-    c.dkv = splits_for(states_busy(B), s.max_q * group, B, sms);
+    c.engine = s.dtype != UVU_F32 ? Engine::kMma : s.head_dim <= kPlaneDim ? Engine::kPlanes : Engine::kCuda;
+    c.R = c.engine == Engine::kCuda ? kT : 128;
+    c.nt = c.engine == Engine::kMma && rows_busy(256) >= sms && s.max_q * group > 128 ? 2 : 1;
+    c.fwd_tiles = row_tiles(s, c.R * c.nt);
+    c.fwd = splits_for(rows_busy(c.R * c.nt), s.max_k, c.R, sms);
+    c.dq = splits_for(rows_busy(c.R), s.max_k, c.R, sms);
+    c.dkv = splits_for(states_busy(c.R), s.max_q * group, c.R, sms);
     return c;
 }
 
@@ -431,9 +434,12 @@ cudaError_t by_dim(int D, F f) {
 void attn_workspace(const AttnShape& s, int sms, size_t* fwd, size_t* bwd) {
     const Choice c = choose(s, sms);
     const size_t qh = size_t(s.n_q) * s.q_heads, kh = size_t(s.n_k) * s.kv_heads;
-    *fwd = c.fwd > 1 ? align256(c.fwd * qh * 4) + c.fwd * qh * s.head_dim * 4 : 0;
+    const bool planes = c.engine == Engine::kPlanes;
+    *fwd = c.fwd > 1 ? align256(c.fwd * qh * 4) + align256(c.fwd * qh * s.head_dim * 4) : 0;
+    if (planes) *fwd += attn_planes_bytes(s, false);
     const size_t dq = c.dq > 1 ? c.dq * qh * s.head_dim * 4 : 0, dkv = c.dkv > 1 ? 2 * c.dkv * kh * s.head_dim * 4 : 0;
-    *bwd = align256(qh * 4) + std::max(dq, dkv);
+    *bwd = align256(qh * 4) + align256(std::max(dq, dkv));
+    if (planes) *bwd += attn_planes_bytes(s, true);
 }
 
 AttnArgs attn_args(const AttnShape& s, const AttnTensors& t) {
@@ -460,12 +466,22 @@ cudaError_t launch_attn_fwd(const AttnShape& s, const AttnTensors& t, void* ws, 
     AttnArgs a = attn_args(s, t);
     const Choice c = choose(s, sms);
     a.splits = c.fwd;
+    char* w = static_cast<char*>(ws);
     if (a.splits > 1) {
-        a.part_lse = static_cast<float*>(ws);
-        a.part_o = a.part_lse + align256(size_t(a.splits) * a.nq * a.Hq * 4) / 4;
+        const size_t n = size_t(a.splits) * a.nq * a.Hq;
+        a.part_lse = reinterpret_cast<float*>(w);
+        a.part_o = reinterpret_cast<float*>(w + align256(n * 4));
+        w += align256(n * 4) + align256(n * a.D * 4);
     }
-    cudaError_t e = c.nt ? launch_attn_fwd_mma(s.dtype, a, c.nt, c.fwd_tiles, st)
-                         : by_dim(a.D, [&](auto d) { return fwd_simple<float, decltype(d)::value>(s, a, st); });
+    cudaError_t e = cudaSuccess;
+    switch (c.engine) {
+        case Engine::kMma: e = launch_attn_fwd_mma(s.dtype, a, c.nt, c.fwd_tiles, st); break;
+        case Engine::kPlanes:
+            e = launch_attn_planes(a, w, sms, st);
+            if (e == cudaSuccess) e = launch_attn_fwd_planes(a, w, c.fwd_tiles, st);
+            break;
+        case Engine::kCuda: e = by_dim(a.D, [&](auto d) { return fwd_simple<float, decltype(d)::value>(s, a, st); }); break;
+    }
     if (e != cudaSuccess || a.splits == 1) return e;
     const unsigned blocks = unsigned((a.nq * a.Hq + 7) / 8);
     switch (s.dtype) {
@@ -481,6 +497,8 @@ cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, 
     a.delta = static_cast<float*>(ws);
     a.part_o = a.delta + align256(size_t(a.nq) * a.Hq * 4) / 4;
     const Choice c = choose(s, sms);
+    const size_t dq = c.dq > 1 ? size_t(c.dq) * a.nq * a.Hq : 0, dkv = c.dkv > 1 ? 2 * size_t(c.dkv) * a.nk * a.Hkv : 0;
+    void* planes = reinterpret_cast<char*>(a.part_o) + align256(std::max(dq, dkv) * a.D * 4);
     const auto with_type = [&](auto f) {
         switch (s.dtype) {
             case UVU_F32: f(float{}); break;
@@ -493,12 +511,18 @@ cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, 
     // dq, then dk and dv; the partial sums of one are joined before the other's are written
     const auto half = [&](bool kv) {
         a.splits = kv ? c.dkv : c.dq;
-        const int R = c.nt ? 128 : kT;
-        const int64_t tiles = kv ? state_tiles(s, R) : row_tiles(s, R);
-        cudaError_t e = c.nt ? launch_attn_bwd_mma(s.dtype, a, kv, tiles, st) : by_dim(a.D, [&](auto d) {
-            constexpr int DP = decltype(d)::value;
-            return kv ? bwd_simple<DP, true>(a, tiles, st) : bwd_simple<DP, false>(a, tiles, st);
-        });
+        const int64_t tiles = kv ? state_tiles(s, c.R) : row_tiles(s, c.R);
+        cudaError_t e = cudaSuccess;
+        switch (c.engine) {
+            case Engine::kMma: e = launch_attn_bwd_mma(s.dtype, a, kv, tiles, st); break;
+            case Engine::kPlanes: e = launch_attn_bwd_planes(a, planes, kv, tiles, st); break;
+            case Engine::kCuda:
+                e = by_dim(a.D, [&](auto d) {
+                    constexpr int DP = decltype(d)::value;
+                    return kv ? bwd_simple<DP, true>(a, tiles, st) : bwd_simple<DP, false>(a, tiles, st);
+                });
+                break;
+        }
         if (e != cudaSuccess || a.splits == 1) return e;
         const int64_t n = kv ? a.nk * a.Hkv * a.D : a.nq * a.Hq * a.D;
         return with_type([&](auto t) {
@@ -510,8 +534,19 @@ cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, 
     cudaError_t e = cudaSuccess;
     if (a.nq > 0)
         e = with_type([&](auto t) { attn_delta<decltype(t)><<<unsigned((a.nq * a.Hq + 7) / 8), kThreads, 0, st>>>(a); });
+    if (e == cudaSuccess && c.engine == Engine::kPlanes) e = launch_attn_planes(a, planes, sms, st);
     if (e == cudaSuccess && a.dq && a.nq > 0) e = half(false);
     if (e == cudaSuccess && a.dk && a.nk > 0) e = half(true);
+    return e;
+}
+
+// Status of the tensor-core attention kernels on the current device (bit 0: a bounded wait gave up).
+cudaError_t attn_status(unsigned* word, bool reset) {
+    unsigned a = 0, b = 0, c = 0;
+    cudaError_t e = attn_fwd_mma_status(&a, reset);
+    if (e == cudaSuccess) e = attn_bwd_mma_status(&b, reset);
+    if (e == cudaSuccess) e = attn_planes_status(&c, reset);
+    *word = a | b | c;
     return e;
 }
 

@@ -56,4 +56,15 @@ cudaError_t launch_attn_fwd_mma(uvu_dtype dtype, const AttnArgs& a, int nt, int6
 // The backward of 16-bit operands: dk and dv (kv) by tiles of 128 states, or dq by tiles of 128 rows.
 cudaError_t launch_attn_bwd_mma(uvu_dtype dtype, const AttnArgs& a, bool kv, int64_t tiles, cudaStream_t st);
 
+// attn_planes.cu: fp32 operands with head_dim <= 64 as three bf16 planes each, in the workspace.
+constexpr int kPlaneDim = 64;
+size_t attn_planes_bytes(const AttnShape& s, bool bwd);
+cudaError_t launch_attn_planes(const AttnArgs& a, void* ws, int sms, cudaStream_t st);
+cudaError_t launch_attn_fwd_planes(const AttnArgs& a, void* ws, int64_t row_tiles, cudaStream_t st);
+cudaError_t launch_attn_bwd_planes(const AttnArgs& a, void* ws, bool kv, int64_t tiles, cudaStream_t st);
+// Status words of the files' kernels.
+cudaError_t attn_fwd_mma_status(unsigned* word, bool reset);
+cudaError_t attn_bwd_mma_status(unsigned* word, bool reset);
+cudaError_t attn_planes_status(unsigned* word, bool reset);
+
 }  // namespace uvu

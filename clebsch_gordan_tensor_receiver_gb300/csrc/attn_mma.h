@@ -1,0 +1,181 @@
+// What the tensor-core attention kernels share: loading of operand tiles, masks, the split of a walk.
+//
+// The loaders use 16-byte cp.async with zero fill instead of tensor maps: a masked or absent state is
+// zeros in shared memory, whatever memory holds there (0 * NaN would reach a sum), and any row and head
+// strides work; operands off the 16-byte grid go through registers.  A stage's barrier counts the
+// loader threads, whose arrivals are tied to their copies; the issuer of the matrix instructions orders
+// what they wrote before its instructions (a proxy fence after the barrier).
+//
+// Every wait is bounded (two seconds); on expiry the roles leave their loops, the issuer waits for its
+// instructions, the loaders for their copies, and the CTA frees its tensor memory and returns with the
+// status word set.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+
+#include "attn.h"
+#include "elem.h"
+#include "tensor_core.h"
+
+namespace uvu {
+namespace {
+
+using namespace tc;
+
+__device__ unsigned int attn_status_word;  // of the including file's kernels; see attn_status()
+
+// The word of this file's kernels (bit 0: a bounded wait gave up); reset clears it.
+cudaError_t read_status(unsigned* word, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(word, attn_status_word, sizeof(unsigned));
+    if (e != cudaSuccess || !reset) return e;
+    const unsigned z = 0;
+    return cudaMemcpyToSymbol(attn_status_word, &z, sizeof(unsigned));
+}
+
+constexpr int kRows = 128;      // rows of a row tile, states of a state tile
+constexpr int kLoadWarps = 2;
+constexpr float kLn2 = 0.6931471805599453f;
+
+constexpr int kLoadThreads = kLoadWarps * 32;
+
+// How the loader threads share a tile of ROWS rows: thread t takes 16-byte chunk t % 2^LG of the rows
+// t / 2^LG, + kStep, ...  2^LG is the power of two that holds the row's chunks.
+template <int LG, int ROWS = kRows>
+struct LoadMap {
+    static constexpr int kStep = kLoadThreads >> LG, kIters = ROWS / kStep;
+    int row, chunk;
+    uint32_t bytes;  // of the chunk that exist: the others are zeros
+    bool on;         // the chunk is read by the matrix instructions
+    __device__ __forceinline__ LoadMap(int t, int D)
+        : row(t >> LG), chunk(t & ((1 << LG) - 1)), bytes(uint32_t(min(max(D - 8 * chunk, 0), 8)) * 2), on(chunk < 2 * ((D + 15) / 16)) {}
+};
+
+// One 16-byte chunk (of which `bytes` exist) into shared memory.
+template <bool ALIGNED>
+__device__ __forceinline__ void load_chunk(uint32_t to, const char* src, uint32_t bytes) {
+    if constexpr (ALIGNED) {
+        copy16(to, src, bytes);
+    } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(src);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (2 * i < bytes) w[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+}
+
+// A tile of rows with a constant stride, `src` the first (its chunk included); rows that `use` refuses are
+// zeros.  ALL: every row is used.
+template <bool ALIGNED, bool ALL, int LG, int ROWS, typename Use>
+__device__ __forceinline__ void load_strided(uint32_t dst, const char* src, int64_t stride, const LoadMap<LG, ROWS>& m, Use use) {
+    using M = LoadMap<LG, ROWS>;
+    if (!m.on) return;
+    // rows kStep apart share their swizzle when kStep is a multiple of 8; at 4 it alternates
+    const uint32_t even = dst + tile_offset(m.row, m.chunk), odd = dst + tile_offset(m.row + M::kStep, m.chunk) - uint32_t(M::kStep * 128);
+    const char* p = src + m.row * stride;
+#pragma unroll 8
+    for (int i = 0; i < M::kIters; ++i) {
+        load_chunk<ALIGNED>((i & 1 ? odd : even) + uint32_t(i * M::kStep * 128), p, ALL || use(m.row + i * M::kStep) ? m.bytes : 0);
+        p += M::kStep * stride;
+    }
+}
+
+// Packed rows of a kv head's queries from r0 on: row r is query r / group, head r % group.
+template <bool ALIGNED, int LG, int ROWS>
+__device__ __forceinline__ void load_packed(uint32_t dst, const char* base, int64_t row, int64_t head, int group, int64_t r0, int rows,
+                                            const LoadMap<LG, ROWS>& m) {
+    using M = LoadMap<LG, ROWS>;
+    if (group == 1) {
+        auto use = [&](int r) { return r < rows; };
+        if (rows >= ROWS)
+            load_strided<ALIGNED, true>(dst, base + r0 * row + m.chunk * 16, row, m, use);
+        else
+            load_strided<ALIGNED, false>(dst, base + r0 * row + m.chunk * 16, row, m, use);
+        return;
+    }
+    if (!m.on) return;
+    // query and head of the thread's first row; later rows step by kStep without a division
+    const uint32_t g = uint32_t(group), dq = uint32_t(M::kStep) / g, dj = uint32_t(M::kStep) - dq * g;
+    const int64_t q0 = (r0 + m.row) / group;
+    uint32_t j = uint32_t(r0 + m.row - q0 * group);
+    const char* p = base + q0 * row + int64_t(j) * head + m.chunk * 16;
+    const int64_t step = dq * row + int64_t(dj) * head, wrap = row - int64_t(g) * head;
+#pragma unroll 4
+    for (int i = 0; i < M::kIters; ++i) {
+        const int r = m.row + i * M::kStep;
+        load_chunk<ALIGNED>(dst + tile_offset(r, m.chunk), p, r < rows ? m.bytes : 0);
+        p += step;
+        j += dj;
+        if (j >= g) {
+            j -= g;
+            p += wrap;
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t tail_word(int64_t left, int w) {  // bits of the states that exist
+    const int64_t n = left - 32 * w;
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << uint32_t(n)) - 1u;
+}
+
+// Which of a tile's N states take part, as words in every lane of a loader warp.  The mask bytes of
+// the next tile are fetched a tile ahead.
+template <int N = kRows>
+struct StateMask {
+    static constexpr int kWords = N / 32;
+    const uint8_t* keep;  // of the graph, or null
+    int64_t at, hi;       // first state of the coming tile, end
+    uint32_t word[kWords], ahead;
+    __device__ __forceinline__ StateMask(const uint8_t* k, int64_t lo, int64_t end) : keep(k), at(lo), hi(end), ahead(0) { fetch(); }
+    __device__ __forceinline__ void fetch() {
+        if (!keep) return;
+        ahead = 0;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            const int64_t s = at + 32 * w + (threadIdx.x & 31);
+            if (s < hi && keep[s]) ahead |= 1u << w;
+        }
+    }
+    __device__ __forceinline__ void next() {
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) word[w] = keep ? __ballot_sync(0xffffffffu, (ahead >> w) & 1) : tail_word(hi - at, w);
+        at += N;
+        fetch();
+    }
+    __device__ __forceinline__ bool all() const {
+        uint32_t a = 0xffffffffu;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) a &= word[w];
+        return a == 0xffffffffu;
+    }
+    __device__ __forceinline__ bool has(int r) const {
+        uint32_t x = word[0];
+#pragma unroll
+        for (int w = 1; w < kWords; ++w) x = r >= 32 * w ? word[w] : x;
+        return (x >> (r & 31)) & 1;
+    }
+};
+
+struct Piece {
+    int64_t lo, hi;
+};
+__device__ __forceinline__ Piece piece_of(int64_t n, int s, int splits) {
+    const int64_t tiles = (n + kRows - 1) / kRows, per = (tiles + splits - 1) / splits;
+    return {min(n, s * per * kRows), min(n, (s + 1) * per * kRows)};
+}
+
+// f(dimension class, aligned) for a head dimension: 2^class 16-byte chunks a row.  Operands off the
+// 16-byte grid are rare and take one class for all dimensions.
+template <typename F>
+cudaError_t by_chunks(int D, bool aligned, F f) {
+    if (!aligned) return f(std::integral_constant<int, 4>{}, std::false_type{});
+    if (D <= 16) return f(std::integral_constant<int, 1>{}, std::true_type{});
+    if (D <= 32) return f(std::integral_constant<int, 2>{}, std::true_type{});
+    if (D <= 64) return f(std::integral_constant<int, 3>{}, std::true_type{});
+    return f(std::integral_constant<int, 4>{}, std::true_type{});
+}
+
+}  // namespace
+}  // namespace uvu

@@ -1,0 +1,423 @@
+// The attention backward on the tensor cores for 16-bit operands.
+//
+// KV false: dq of a tile of 128 packed rows, walking the states; KV true: dk and dv of a tile of 128
+// states, walking the packed rows of all heads that share them (so a shared head's gradient needs no
+// second sum).  R1, R2: the tile's own operands, resident; X1, X2: the walked ones, in the ring.
+//              R1  R2  X1  X2      S = R1 X1^T,  dP = R2 X2^T,  P = exp2(c S - lse),  dS = P (dP - delta)
+//     dq       Q   dO  K   V       dq += dS X1
+//     dk, dv   K   V   Q   dO      dk += dS X1,  dv += P X2      (S and dP transposed: lanes are states)
+// Two sweeps instead of one cost S and dP twice (seven products instead of five), but every sum stays
+// in one CTA's tensor memory: no atomics, and results that do not depend on timing.
+//
+// Tensor memory: S, dP (128 columns each), then the sums.  P and dS are written as 16-bit values over
+// the part of S and dP that the same thread has read.  Two warpgroups share a tile: warpgroup w takes
+// columns 64 w .. + 63 of each lane's row.  Order of the matrix instructions:
+//     S(0) dP(0) | dv += P(0) X2, S(1), dk += dS(0) X1, dP(1) | ...
+// so the tensor cores form dv(j) and S(j+1) while the threads turn dP(j) into dS(j), and dk(j) and
+// dP(j+1) while they turn S(j+1) into P(j+1).
+//
+// f16 keeps 2^8 P (undone in the epilogue and in dS): P of long rows would fall below the type's
+// smallest normal value, 2^-14.  bf16 has the exponent range of fp32 and needs no shift.
+#include "attn_mma.h"
+
+namespace uvu {
+namespace {
+
+template <bool KV>
+struct BwdLayout {
+    int panels, stages;
+    __host__ __device__ int tile() const { return panels * kPanelBytes; }
+    __host__ __device__ int ring() const { return 2 * tile(); }
+    __host__ __device__ int aux() const { return ring() + stages * tile(); }  // per walked tile: lse and delta, or the mask
+    __host__ __device__ int aux_bytes() const { return KV ? 2 * kRows * 4 : 16; }
+    __host__ __device__ int bars() const { return aux() + stages / 2 * aux_bytes(); }
+    __host__ __device__ int total() const { return bars() + 256 + 1024; }  // + alignment slack
+};
+
+constexpr int kBwdWarps = 8 + 1 + kLoadWarps;
+
+// 16 columns of a gradient row, times `scale`, to a partial or final row of D values.
+template <typename T>
+__device__ __forceinline__ void store_grad16(const float (&o)[16], float scale, T* dst, float* part, int c0, int D, bool vec) {
+    if (part) {
+        if (D % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c0 + 4 * i < D)
+                    *reinterpret_cast<float4*>(part + c0 + 4 * i) =
+                        make_float4(o[4 * i] * scale, o[4 * i + 1] * scale, o[4 * i + 2] * scale, o[4 * i + 3] * scale);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (c0 + i < D) part[c0 + i] = o[i] * scale;
+        }
+    } else if (vec) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (c0 + 8 * i < D)
+                *reinterpret_cast<uint4*>(dst + c0 + 8 * i) =
+                    make_uint4(pack2<T>(o[8 * i] * scale, o[8 * i + 1] * scale), pack2<T>(o[8 * i + 2] * scale, o[8 * i + 3] * scale),
+                               pack2<T>(o[8 * i + 4] * scale, o[8 * i + 5] * scale), pack2<T>(o[8 * i + 6] * scale, o[8 * i + 7] * scale));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (c0 + i < D) dst[c0 + i] = narrow<T>(o[i] * scale);
+    }
+}
+
+template <typename T, int LG, bool ALIGNED, bool KV>
+__global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(AttnArgs a, BwdLayout<KV> L) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ int s_dead;
+    __shared__ uint32_t s_tmem;
+    const AttnTile tl = KV ? attn_tile(a.k_off, a.graphs, 1, kRows, blockIdx.x) : attn_tile(a.q_off, a.graphs, a.group, kRows, blockIdx.x);
+    if (tl.graph < 0) return;
+    const int h = blockIdx.y, split = blockIdx.z;
+    const int64_t q0 = a.q_off[tl.graph], k0 = a.k_off[tl.graph];
+    const int64_t rows = (a.q_off[tl.graph + 1] - q0) * a.group, states = a.k_off[tl.graph + 1] - k0;
+    const Piece walk = piece_of(KV ? rows : states, split, a.splits);
+    const int n_tiles = int((walk.hi - walk.lo + kRows - 1) / kRows);
+    const int own = int(min(tl.rows - tl.row0, int64_t(kRows)));  // rows of the resident tile
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int d16 = (a.D + 15) / 16, half = L.stages / 2;
+    const uint32_t r_full = sb + L.bars(), s_full = r_full + 8, dp_full = s_full + 8, p_ready = dp_full + 8, ds_ready = p_ready + 8,
+                   done = ds_ready + 8, fin = done + 8, full = fin + 8, empty = full + 8 * L.stages, aux_full = empty + 8 * L.stages;
+    const uint32_t g_cols = uint32_t(64 * L.panels);
+    const uint32_t tmem_cols = 512;
+    if (threadIdx.x == 0) {
+        s_dead = 0;
+        bar_init(r_full, kLoadThreads);
+        bar_init(s_full, 1);
+        bar_init(dp_full, 1);
+        bar_init(p_ready, 8);
+        bar_init(ds_ready, 8);
+        bar_init(done, 1);
+        bar_init(fin, 1);
+        for (int s = 0; s < L.stages; ++s) {
+            bar_init(full + 8 * s, kLoadThreads);
+            bar_init(empty + 8 * s, 1);
+        }
+        for (int s = 0; s < half; ++s) bar_init(aux_full + 8 * s, KV ? kLoadThreads : 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) tmem_alloc(smem_u32(&s_tmem), tmem_cols);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
+    const uint32_t t_dp = tmem + kRows, t_g = tmem + 2 * kRows;  // sums: dq, or dk then dv
+    volatile int* dead = &s_dead;
+    unsigned* status = &attn_status_word;
+    constexpr float kShift = __is_same(T, __half) ? 8.f : 0.f, kUnshift = __is_same(T, __half) ? 0.00390625f : 1.f;
+    constexpr float kLog2e = 1.4426950408889634f;
+
+    if (warp < 8) {
+        // ----------------------------------------------------------------- P and dS
+        const int w = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const bool work = quad * 32 < own;
+        const uint32_t lanes = uint32_t(quad * 32) << 16, col = uint32_t(64 * w);
+        const float c = a.scale_log2;
+        const int64_t p = tl.row0 + row;
+        float lse = INFINITY, delta = 0.f;  // of the thread's row (dq)
+        int64_t rh = 0;
+        bool keep = row < own;
+        if (keep) {
+            if (KV) {
+                rh = (k0 + p) * a.Hkv + h;
+                keep = !a.keep || a.keep[k0 + p];
+            } else {
+                rh = (q0 + p / a.group) * a.Hq + int64_t(h) * a.group + p % a.group;
+                const float x = a.lse[rh];
+                // a row without a kept state: P = exp2(s - inf) = 0
+                lse = x == -INFINITY ? INFINITY : x * kLog2e - kShift;
+                delta = a.delta[rh] * kUnshift;
+            }
+        }
+        bool ok = true;
+        for (int j = 0; j < n_tiles; ++j) {
+            const int ax = j % half;
+            const float* s_lse = reinterpret_cast<const float*>(smem + L.aux() + ax * L.aux_bytes()) + col;
+            const float* s_delta = s_lse + kRows;
+            uint32_t word[2] = {0xffffffffu, 0xffffffffu};
+            if (KV || a.keep) {
+                ok = __all_sync(0xffffffffu, bar_wait(aux_full + 8 * ax, (j / half) & 1, dead, status));
+                if (!ok) break;
+            }
+            if (!KV) {
+                if (a.keep) {
+                    const uint32_t* mw = reinterpret_cast<const uint32_t*>(smem + L.aux() + ax * L.aux_bytes()) + 2 * w;
+                    word[0] = mw[0];
+                    word[1] = mw[1];
+                } else {
+                    const int64_t left = walk.hi - walk.lo - int64_t(j) * kRows;
+                    word[0] = tail_word(left, 2 * w);
+                    word[1] = tail_word(left, 2 * w + 1);
+                }
+            }
+            ok = __all_sync(0xffffffffu, bar_wait(s_full, j & 1, dead, status));
+            if (!ok) break;
+            fence_after();
+            float x[2][32];
+            if (work) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) tmem_ld32(tmem + lanes + col + 32 * b, x[b]);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    tmem_wait_ld(x[b]);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[b][i] = exp2_approx(fmaf(x[b][i], c, KV ? -s_lse[32 * b + i] : -lse));
+                    if (!KV && word[b] != 0xffffffffu) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((word[b] >> i) & 1)) x[b][i] = 0.f;
+                    }
+                    if (KV) {
+                        uint32_t q[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) q[i] = pack2<T>(x[b][2 * i], x[b][2 * i + 1]);
+                        tmem_st16(tmem + lanes + col + 16 * b, q);
+                    }
+                }
+                if (KV) tmem_wait_st();
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(p_ready);
+            ok = __all_sync(0xffffffffu, bar_wait(dp_full, j & 1, dead, status));
+            if (!ok) break;
+            fence_after();
+            if (work) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    float y[32];
+                    tmem_ld32(t_dp + lanes + col + 32 * b, y);
+                    tmem_wait_ld(y);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) y[i] = x[b][i] * fmaf(y[i], kUnshift, KV ? -s_delta[32 * b + i] : -delta);
+                    uint32_t q[16];
+                    if (!KV && word[b] != 0xffffffffu) {  // 0 * (NaN - delta) is not 0
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((word[b] >> i) & 1)) y[i] = 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) q[i] = pack2<T>(y[2 * i], y[2 * i + 1]);
+                    tmem_st16(t_dp + lanes + col + 16 * b, q);
+                }
+                tmem_wait_st();
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(ds_ready);
+        }
+        if (ok && n_tiles > 0) {
+            ok = __all_sync(0xffffffffu, bar_wait(done, 0, dead, status));
+            fence_after();
+        }
+        if (ok && work) {
+            // dk: warpgroup 0, dv: warpgroup 1; dq: the column blocks in turn
+            const int64_t n = KV ? a.nk * a.Hkv : a.nq * a.Hq;
+            T* dst = static_cast<T*>(KV ? (w ? a.dv : a.dk) : a.dq) + rh * a.D;
+            float* part = a.splits > 1 ? a.part_o + ((KV && w ? a.splits + split : split) * n + rh) * a.D : nullptr;
+            const bool vec = a.D % 8 == 0 && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
+            const float scale = KV && w ? kUnshift : a.scale;
+            for (int d = KV ? 0 : w; d < d16; d += KV ? 1 : 2) {
+                float o[16];
+                __syncwarp();
+                if (n_tiles > 0) {
+                    tmem_ld16(t_g + lanes + (KV ? uint32_t(w) * g_cols : 0u) + 16 * d, o);
+                    tmem_wait_ld(o);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = n_tiles > 0 && keep ? o[i] : 0.f;
+                if (row < own) store_grad16<T>(o, scale, dst, part, 16 * d, a.D, vec);
+            }
+        }
+    } else if (warp == 8) {
+        // ----------------------------------------------------------------- matrix instructions
+        if (lane == 0) {
+            const uint32_t id_s = mma_desc<T>(kRows, false), id_g = mma_desc<T>(16 * d16, true);
+            const uint32_t r1 = sb, r2 = sb + uint32_t(L.tile());
+            auto stage = [&](int i) { return sb + uint32_t(L.ring() + (i % L.stages) * L.tile()); };
+            auto wait_stage = [&](int i) {
+                if (!bar_wait(full + 8 * (i % L.stages), (i / L.stages) & 1, dead, status)) return false;
+                fence_async();
+                return true;
+            };
+            auto product = [&](uint32_t d, uint32_t r, uint32_t x, uint32_t bar) {
+                for (int s = 0; s < d16; ++s) mma_ss(d, desc_cols(r, s), desc_cols(x, s), id_s, s > 0);
+                mma_commit(bar);
+            };
+            // d += A X: the 16-bit A of row block s lies in the half that its warpgroup wrote
+            auto sum = [&](uint32_t d, uint32_t A, uint32_t x, bool first) {
+#pragma unroll
+                for (int s = 0; s < kRows / 16; ++s)
+                    mma_ts(d, A + uint32_t((s >> 2) * 64 + (s & 3) * 8), desc_rows(x, s), id_g, !first || s > 0);
+            };
+            bool ok = n_tiles > 0 && bar_wait(r_full, 0, dead, status) && wait_stage(0);
+            if (ok) {
+                product(tmem, r1, stage(0), s_full);
+                ok = wait_stage(1);
+                if (ok) {
+                    product(t_dp, r2, stage(1), dp_full);
+                    if (!KV) mma_commit(empty + 8 * 1);
+                }
+            }
+            for (int j = 0; j < n_tiles && ok; ++j) {
+                ok = bar_wait(p_ready, j & 1, dead, status);
+                if (!ok) break;
+                fence_after();
+                if (KV) {
+                    sum(t_g + g_cols, tmem, stage(2 * j + 1), j == 0);
+                    mma_commit(empty + 8 * ((2 * j + 1) % L.stages));
+                }
+                if (j + 1 < n_tiles) {
+                    ok = wait_stage(2 * j + 2);
+                    if (!ok) break;
+                    product(tmem, r1, stage(2 * j + 2), s_full);
+                }
+                ok = bar_wait(ds_ready, j & 1, dead, status);
+                if (!ok) break;
+                fence_after();
+                sum(t_g, t_dp, stage(2 * j), j == 0);
+                mma_commit(empty + 8 * ((2 * j) % L.stages));
+                if (j + 1 < n_tiles) {
+                    ok = wait_stage(2 * j + 3);
+                    if (!ok) break;
+                    product(t_dp, r2, stage(2 * j + 3), dp_full);
+                    if (!KV) mma_commit(empty + 8 * ((2 * j + 3) % L.stages));
+                } else {
+                    mma_commit(done);
+                }
+            }
+            // every instruction issued has finished before the tensor memory and the stages go
+            mma_commit(fin);
+            bar_wait_last(fin, 0, status);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------------- loaders
+        const int t = threadIdx.x - 9 * 32;
+        const LoadMap<LG> map(t, a.D);
+        if (n_tiles > 0) {
+            auto arrive = [&](uint32_t bar) { ALIGNED ? copy_arrive(bar) : bar_arrive(bar); };
+            const char* Q = reinterpret_cast<const char*>(static_cast<const T*>(a.q) + q0 * a.q_row + int64_t(h) * a.group * a.q_head);
+            const char* dO = reinterpret_cast<const char*>(static_cast<const T*>(a.d_out) + q0 * a.o_row + int64_t(h) * a.group * a.o_head);
+            const int64_t s0 = k0 + (KV ? tl.row0 : walk.lo);
+            const char* K = reinterpret_cast<const char*>(static_cast<const T*>(a.k) + s0 * a.k_row + h * a.k_head) + map.chunk * 16;
+            const char* V = reinterpret_cast<const char*>(static_cast<const T*>(a.v) + s0 * a.v_row + h * a.v_head) + map.chunk * 16;
+            StateMask<> mask(a.keep ? a.keep + k0 : nullptr, KV ? tl.row0 : walk.lo, KV ? states : walk.hi);
+            auto states_tile = [&](uint32_t dst, const char* src, int64_t stride) {
+                auto use = [&](int r) { return mask.has(r); };
+                if (mask.all())
+                    load_strided<ALIGNED, true>(dst, src, stride, map, use);
+                else
+                    load_strided<ALIGNED, false>(dst, src, stride, map, use);
+            };
+            auto rows_tile = [&](uint32_t dst, const char* base, int64_t row, int64_t head, int64_t r0, int n) {
+                load_packed<ALIGNED>(dst, base, row * 2, head * 2, a.group, r0, n, map);
+            };
+            auto free_stage = [&](int i) {
+                return i < L.stages || __all_sync(0xffffffffu, bar_wait(empty + 8 * (i % L.stages), (i / L.stages - 1) & 1, dead, status));
+            };
+            auto stage = [&](int i) { return sb + uint32_t(L.ring() + (i % L.stages) * L.tile()); };
+            if (KV) {
+                mask.next();
+                states_tile(sb, K, a.k_row * 2);
+                states_tile(sb + uint32_t(L.tile()), V, a.v_row * 2);
+            } else {
+                rows_tile(sb, Q, a.q_row, a.q_head, tl.row0, own);
+                rows_tile(sb + uint32_t(L.tile()), dO, a.o_row, a.o_head, tl.row0, own);
+            }
+            arrive(r_full);
+            // lse and delta of the walked rows, fetched a tile ahead
+            float v_lse[2], v_delta[2];
+            auto fetch = [&](int j) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int64_t r = walk.lo + int64_t(j) * kRows + t + 64 * i;
+                    v_lse[i] = -INFINITY, v_delta[i] = 0.f;
+                    if (r < walk.hi) {
+                        const int64_t q = r / a.group, at = (q0 + q) * a.Hq + int64_t(h) * a.group + (r - q * a.group);
+                        v_lse[i] = a.lse[at];
+                        v_delta[i] = a.delta[at];
+                    }
+                }
+            };
+            if (KV) fetch(0);
+            for (int j = 0; j < n_tiles; ++j) {
+                const int64_t lo = walk.lo + int64_t(j) * kRows;
+                const int n = int(min(walk.hi - lo, int64_t(kRows)));
+                if (!free_stage(2 * j)) break;
+                // the tile that used this aux entry before gave up its X1 stage, which is this one
+                if (KV) {
+                    float* s_lse = reinterpret_cast<float*>(smem + L.aux() + (j % half) * L.aux_bytes());
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        // rows past the end and rows without a kept state: P = exp2(s - inf) = 0
+                        s_lse[t + 64 * i] = v_lse[i] == -INFINITY ? INFINITY : v_lse[i] * kLog2e - kShift;
+                        s_lse[kRows + t + 64 * i] = v_delta[i] * kUnshift;
+                    }
+                    bar_arrive(aux_full + 8 * (j % half));
+                    if (j + 1 < n_tiles) fetch(j + 1);
+                    rows_tile(stage(2 * j), Q, a.q_row, a.q_head, lo, n);
+                    arrive(full + 8 * ((2 * j) % L.stages));
+                    if (!free_stage(2 * j + 1)) break;
+                    rows_tile(stage(2 * j + 1), dO, a.o_row, a.o_head, lo, n);
+                    arrive(full + 8 * ((2 * j + 1) % L.stages));
+                } else {
+                    mask.next();
+                    if (a.keep && t == 0) {
+                        *reinterpret_cast<uint4*>(smem + L.aux() + (j % half) * L.aux_bytes()) =
+                            make_uint4(mask.word[0], mask.word[1], mask.word[2], mask.word[3]);
+                        bar_arrive(aux_full + 8 * (j % half));
+                    }
+                    states_tile(stage(2 * j), K, a.k_row * 2);
+                    arrive(full + 8 * ((2 * j) % L.stages));
+                    if (!free_stage(2 * j + 1)) break;
+                    states_tile(stage(2 * j + 1), V, a.v_row * 2);
+                    arrive(full + 8 * ((2 * j + 1) % L.stages));
+                    K += kRows * a.k_row * 2;
+                    V += kRows * a.v_row * 2;
+                }
+            }
+            copy_wait_all();
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        fence_after();
+        tmem_free(tmem, tmem_cols);
+    }
+}
+
+template <typename T, bool KV>
+cudaError_t bwd(const AttnArgs& a, int64_t tiles, cudaStream_t st) {
+    BwdLayout<KV> L;
+    L.panels = a.D > 64 ? 2 : 1;
+    L.stages = L.panels == 1 ? 8 : 4;  // 160 or 192 KB
+    const uintptr_t any = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                          reinterpret_cast<uintptr_t>(a.d_out) |
+                          uintptr_t(a.q_row | a.q_head | a.k_row | a.k_head | a.v_row | a.v_head | a.o_row | a.o_head) * 2;
+    return by_chunks(a.D, (any & 15u) == 0, [&](auto lg, auto aligned) {
+        auto k = attn_bwd_mma<T, decltype(lg)::value, decltype(aligned)::value, KV>;
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total());
+        if (e != cudaSuccess) return e;
+        k<<<dim3(unsigned(tiles), unsigned(a.Hkv), unsigned(a.splits)), kBwdWarps * 32, L.total(), st>>>(a, L);
+        return cudaGetLastError();
+    });
+}
+
+}  // namespace
+
+cudaError_t launch_attn_bwd_mma(uvu_dtype dtype, const AttnArgs& a, bool kv, int64_t tiles, cudaStream_t st) {
+    if (dtype == UVU_BF16) return kv ? bwd<__nv_bfloat16, true>(a, tiles, st) : bwd<__nv_bfloat16, false>(a, tiles, st);
+    return kv ? bwd<__half, true>(a, tiles, st) : bwd<__half, false>(a, tiles, st);
+}
+
+cudaError_t attn_bwd_mma_status(unsigned* word, bool reset) { return read_status(word, reset); }
+
+}  // namespace uvu

@@ -1,0 +1,817 @@
+// Attention of fp32 operands on the 16-bit tensor cores, with fp32 accuracy (head dimensions to 64).
+//
+// An fp32 value is the exact sum of three bf16 values, its leading 8 significant bits, the next 8 and
+// the last 8 (x = x0 + x1 + x2, each remainder cut to its upper half: bf16 has the exponent range of
+// fp32, and a cut of 8 bits leaves an exact remainder).  A product keeps the terms x_i y_j with
+// i + j <= 2; what is dropped is 2^-24 of it.  That is six bf16 products, at 1/6 of their rate still several
+// times the CUDA cores' fp32 rate.
+//   - A first kernel writes the planes of q, k, v (and d_out) to the workspace, [row][head][3][PS] with
+//     PS = 16, 32 or 64 columns a plane (zeros past head_dim), so that the loaders below move them like any 16-bit
+//     operand.  Infinities and NaN stay in x0.
+//   - S (and dP): the six products are issued smallest first into one accumulator.
+//   - P (and dS) are cut into planes by the threads that form them; with X = [X0 | X1 | X2] side by side in
+//     the tile, P0 X, P1 [X0 | X1] and P2 X0 land in columns by order of magnitude: the sums of the small terms
+//     are apart from the large ones, and the threads add them.
+//   - Tensor memory sums each tile afresh; the sums over tiles are fp32 registers (accumulating in tensor
+//     memory loses more than a rounded fp32 addition does, and long rows would show it).
+// Masks, splits and bounded waits as in the 16-bit kernels.
+#include "attn_mma.h"
+
+namespace uvu {
+namespace {
+
+constexpr int kPairWarps = 8;  // two warpgroups share a tile: warpgroup w takes the w-th half of a row's columns
+
+// ----------------------------------------------------------------------------------- planes
+
+struct PlaneJob {
+    const float* x;
+    int64_t row, head;  // strides
+    int64_t rows;
+    int heads;
+    uint16_t* out;  // [rows][heads][3][PS]
+};
+struct PlaneJobs {
+    PlaneJob j[4];
+    int D;
+};
+
+// The planes of two values, packed: the leading plane in p[0].
+__device__ __forceinline__ void cut2(float x, float y, uint32_t (&p)[3]) {
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    p[0] = __byte_perm(a, b, 0x7632);
+    const float x1 = x - __uint_as_float(a & 0xffff0000u), y1 = y - __uint_as_float(b & 0xffff0000u);
+    const uint32_t c = __float_as_uint(x1), d = __float_as_uint(y1);
+    p[1] = __byte_perm(c, d, 0x7632);
+    p[2] = __byte_perm(__float_as_uint(x1 - __uint_as_float(c & 0xffff0000u)), __float_as_uint(y1 - __uint_as_float(d & 0xffff0000u)), 0x7632);
+}
+
+// One thread per 8 columns of a (row, head).
+template <int PS>
+__global__ void __launch_bounds__(256) attn_planes(PlaneJobs jobs) {
+    const PlaneJob& j = jobs.j[blockIdx.y];
+    const int64_t total = j.rows * j.heads * (PS / 8);
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
+        const int c = int(i % (PS / 8)) * 8;
+        const int64_t rh = i / (PS / 8), r = rh / j.heads;
+        const float* x = j.x + r * j.row + (rh - r * j.heads) * j.head + c;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = c + k < jobs.D ? x[k] : 0.f;
+        uint32_t w[3][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t p[3];
+            cut2(v[2 * k], v[2 * k + 1], p);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float z = v[2 * k + e];
+                if (!isfinite(z)) {  // whole in the leading plane (a NaN's upper bits alone could read as infinity)
+                    const uint32_t half = isnan(z) ? 0x7fffu : __float_as_uint(z) >> 16, keep = e ? 0x0000ffffu : 0xffff0000u;
+                    p[0] = (p[0] & keep) | (half << (16 * e));
+                    p[1] &= keep;
+                    p[2] &= keep;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 3; ++q) w[q][k] = p[q];
+        }
+        uint16_t* o = j.out + rh * (3 * PS) + c;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(o + q * PS) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+    }
+}
+
+// An operand's planes in the workspace.
+struct Planes {
+    const uint16_t *q, *k, *v, *d_out;
+};
+
+template <int PS>
+constexpr int kPanels = (3 * PS + 63) / 64;
+
+// A tile of plane rows, panel by panel: ROWS rows with a constant stride (ALL: every row is used).
+template <int PS, int ROWS, bool ALL, typename Use>
+__device__ __forceinline__ void load_planes(uint32_t dst, const char* src, int64_t stride, int t, Use use) {
+#pragma unroll
+    for (int p = 0; p < kPanels<PS>; ++p) {
+        const LoadMap<3, ROWS> m(t, 3 * PS - 64 * p < 64 ? 3 * PS - 64 * p : 64);
+        load_strided<true, ALL>(dst + p * ROWS * 128, src + p * 128 + m.chunk * 16, stride, m, use);
+    }
+}
+template <int PS, int ROWS>
+__device__ __forceinline__ void load_planes_packed(uint32_t dst, const char* base, int64_t row, int64_t head, int group, int64_t r0,
+                                                   int rows, int t) {
+#pragma unroll
+    for (int p = 0; p < kPanels<PS>; ++p) {
+        const LoadMap<3, ROWS> m(t, 3 * PS - 64 * p < 64 ? 3 * PS - 64 * p : 64);
+        load_packed<true>(dst + p * ROWS * 128, base + p * 128, row, head, group, r0, rows, m);
+    }
+}
+
+// The six products of S (or dP) = A B^T, smallest first; panels of `rows` x 128 bytes.
+template <int PS>
+__device__ __forceinline__ void six_products(uint32_t d, uint32_t a, int a_panel, uint32_t b, int b_panel, uint32_t id) {
+    constexpr int kStep = PS / 16;
+    constexpr int kPair[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
+    bool add = false;
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+#pragma unroll
+        for (int s = 0; s < kStep; ++s) {
+            mma_ss(d, desc_cols(a, kPair[i][0] * kStep + s, a_panel), desc_cols(b, kPair[i][1] * kStep + s, b_panel), id, add);
+            add = true;
+        }
+}
+
+// 32 values of a row to the three planes of a 16-bit operand in tensor memory (16 columns each).
+__device__ __forceinline__ void store_planes(const float (&x)[32], uint32_t hi, uint32_t mid, uint32_t lo) {
+    uint32_t w[3][16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        uint32_t p[3];
+        cut2(x[2 * i], x[2 * i + 1], p);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) w[q][i] = p[q];
+    }
+    tmem_st16(hi, w[0]);
+    tmem_st16(mid, w[1]);
+    tmem_st16(lo, w[2]);
+}
+
+// acc[i] += columns i of N at `a`
+template <int N>
+__device__ __forceinline__ void add_columns(uint32_t a, float* acc) {
+    if constexpr (N == 8) {
+        float v[8];
+        tmem_ld8(a, v);
+        tmem_wait_ld(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += v[i];
+    } else {
+#pragma unroll
+        for (int b = 0; b < N / 16; ++b) {
+            float v[16];
+            tmem_ld16(a + 16 * b, v);
+            tmem_wait_ld(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[16 * b + i] += v[i];
+        }
+    }
+}
+
+// N columns from c0 on of a row of D fp32 values, times scale.
+template <int N>
+__device__ __forceinline__ void store_row(float* dst, const float* v, float scale, int c0, int D) {
+    if (D % 4 == 0 && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            if (c0 + i < D)
+                *reinterpret_cast<float4*>(dst + c0 + i) = make_float4(v[i] * scale, v[i + 1] * scale, v[i + 2] * scale, v[i + 3] * scale);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (c0 + i < D) dst[c0 + i] = v[i] * scale;
+    }
+}
+
+// ----------------------------------------------------------------------------------- forward
+
+template <int PS>
+struct FwdPlan {
+    static constexpr int kTile = kPanels<PS> * kPanelBytes, kStages = PS == 64 ? 3 : PS == 32 ? 5 : 8;
+    static constexpr int kRing = kTile, kMasks = kRing + kStages * kTile, kMax = kMasks + 8 * 16, kBars = kMax + 2 * 2 * kRows * 4;
+    static constexpr int kTotal = kBars + 512 + 1024;  // barriers, alignment slack
+    // tensor memory: S (its plane 0 of P written over it), planes 1 and 2 of P, O by order
+    static constexpr uint32_t kMid = kRows, kLo = kRows + 64, kO = kRows + 128;
+};
+
+template <int PS>
+__global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fwd_planes(AttnArgs a, Planes x) {
+    using F = FwdPlan<PS>;
+    constexpr int kHalf = PS / 2, kRing = 8;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ int s_dead;
+    __shared__ uint32_t s_tmem;
+    const AttnTile tl = attn_tile(a.q_off, a.graphs, a.group, kRows, blockIdx.x);
+    if (tl.graph < 0) return;
+    const int h = blockIdx.y, split = blockIdx.z;
+    const int64_t q0 = a.q_off[tl.graph], k0 = a.k_off[tl.graph];
+    const Piece kr = piece_of(a.k_off[tl.graph + 1] - k0, split, a.splits);
+    const int n_tiles = int((kr.hi - kr.lo + kRows - 1) / kRows);
+    const int n_rows = int(min(tl.rows - tl.row0, int64_t(kRows)));
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t q_full = sb + F::kBars, s_full = q_full + 8, p_full = s_full + 8, o_full = p_full + 8, fin = o_full + 8,
+                   pair = fin + 8, full = pair + 32, empty = full + 8 * F::kStages, m_full = empty + 8 * F::kStages;
+    if (threadIdx.x == 0) {
+        s_dead = 0;
+        bar_init(q_full, kLoadThreads);
+        bar_init(s_full, 1);
+        bar_init(p_full, kPairWarps);
+        bar_init(o_full, 1);
+        bar_init(fin, 1);
+        for (int i = 0; i < 4; ++i) bar_init(pair + 8 * i, 2);
+        for (int s = 0; s < F::kStages; ++s) {
+            bar_init(full + 8 * s, kLoadThreads);
+            bar_init(empty + 8 * s, 1);
+        }
+        for (int s = 0; s < kRing; ++s) bar_init(m_full + 8 * s, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kPairWarps) tmem_alloc(smem_u32(&s_tmem), 512);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
+    volatile int* dead = &s_dead;
+    unsigned* status = &attn_status_word;
+
+    if (warp < kPairWarps) {
+        // ------------------------------------------------------------------------ softmax
+        const int w = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const bool work = quad * 32 < n_rows;
+        const uint32_t lanes = uint32_t(quad * 32) << 16, base_t = tmem + lanes;
+        const float c = a.scale_log2;
+        float* s_max = reinterpret_cast<float*>(smem + F::kMax);  // [turn][warpgroup][row]
+        const uint32_t* masks = reinterpret_cast<const uint32_t*>(smem + F::kMasks) + 2 * w;
+        float m = -INFINITY, l = 0.f, acc[kHalf];
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
+        int turn = 0;
+        bool ok = true;
+        // the partner warpgroup's value of the same row
+        auto exchange = [&](float v, float& other) {
+            float* s = s_max + (turn & 1) * 2 * kRows;
+            s[w * kRows + row] = v;
+            __syncwarp();
+            if (lane == 0) bar_arrive(pair + 8 * quad);
+            if (!__all_sync(0xffffffffu, bar_wait(pair + 8 * quad, turn & 1, dead, status))) return false;
+            other = s[(1 - w) * kRows + row];
+            ++turn;
+            return true;
+        };
+        // this warpgroup's half of the columns of O, all orders
+        auto add_o = [&]() {
+            add_columns<kHalf>(base_t + F::kO + 2 * PS + w * kHalf, acc);
+            add_columns<kHalf>(base_t + F::kO + PS + w * kHalf, acc);
+            add_columns<kHalf>(base_t + F::kO + w * kHalf, acc);
+        };
+        for (int j = 0; j < n_tiles; ++j) {
+            uint32_t word[2];
+            if (a.keep) {
+                ok = __all_sync(0xffffffffu, bar_wait(m_full + 8 * (j % kRing), (j / kRing) & 1, dead, status));
+                if (!ok) break;
+                word[0] = masks[(j % kRing) * 4];
+                word[1] = masks[(j % kRing) * 4 + 1];
+            } else {
+                const int64_t left = kr.hi - kr.lo - int64_t(j) * kRows;
+                word[0] = tail_word(left, 2 * w);
+                word[1] = tail_word(left, 2 * w + 1);
+            }
+            ok = __all_sync(0xffffffffu, bar_wait(s_full, j & 1, dead, status));
+            if (!ok) break;
+            fence_after();
+            if (work) {
+                if (j > 0) add_o();  // O of the tile before is complete when S of this one is
+                float v[2][32];
+                float top = -INFINITY;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) tmem_ld32(base_t + 64 * w + 32 * b, v[b]);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    tmem_wait_ld(v[b]);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if ((word[b] >> i) & 1) top = fmaxf(top, v[b][i]);
+                }
+                float other;
+                ok = exchange(top, other);
+                if (!ok) break;
+                const float mn = fmaxf(m, fmaxf(top, other) * c), base = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2_approx(m - base);
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i) acc[i] *= f;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        v[b][i] = (word[b] >> i) & 1 ? exp2_approx(fmaf(v[b][i], c, -base)) : 0.f;
+                        sum[i & 3] += v[b][i];
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    store_planes(v[b], base_t + 64 * w + 16 * b, base_t + F::kMid + 32 * w + 16 * b, base_t + F::kLo + 32 * w + 16 * b);
+                }
+                tmem_wait_st();
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(p_full);
+        }
+        if (ok && n_tiles > 0) {
+            ok = __all_sync(0xffffffffu, bar_wait(o_full, 0, dead, status));
+            fence_after();
+        }
+        if (ok && work) {
+            if (n_tiles > 0) add_o();
+            float other = 0.f;
+            if (exchange(l, other)) {
+                const float sum = w ? other + l : l + other;
+                const int64_t p = tl.row0 + row;
+                const int64_t r = q0 + p / a.group, head = int64_t(h) * a.group + p % a.group;
+                const int64_t rh = (int64_t(split) * a.nq + r) * a.Hq + head;
+                if (row < n_rows) {
+                    if (w == 0)
+                        (a.splits > 1 ? a.part_lse[rh] : a.lse[r * a.Hq + head]) = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+                    if (sum == 0.f) {
+#pragma unroll
+                        for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
+                    }
+                    float* dst = a.splits > 1 ? a.part_o + rh * a.D : static_cast<float*>(a.out) + r * a.o_row + head * a.o_head;
+                    store_row<kHalf>(dst, acc, sum == 0.f ? 0.f : 1.f / sum, w * kHalf, a.D);
+                }
+            }
+        }
+    } else if (warp == kPairWarps) {
+        // ----------------------------------------------------------------- matrix instructions
+        if (lane == 0) {
+            constexpr uint32_t o = F::kO;
+            const uint32_t id_s = mma_desc<__nv_bfloat16>(kRows, false), id3 = mma_desc<__nv_bfloat16>(3 * PS, true),
+                           id2 = mma_desc<__nv_bfloat16>(2 * PS, true), id1 = mma_desc<__nv_bfloat16>(PS, true);
+            auto stage = [&](int i) { return sb + uint32_t(F::kRing + (i % F::kStages) * F::kTile); };
+            auto wait_stage = [&](int i) {
+                if (!bar_wait(full + 8 * (i % F::kStages), (i / F::kStages) & 1, dead, status)) return false;
+                fence_async();
+                return true;
+            };
+            auto scores = [&](int j) {
+                six_products<PS>(tmem, sb, kPanelBytes, stage(2 * j), kPanelBytes, id_s);
+                mma_commit(s_full);
+                mma_commit(empty + 8 * ((2 * j) % F::kStages));
+            };
+            bool ok = n_tiles > 0 && bar_wait(q_full, 0, dead, status) && wait_stage(0);
+            if (ok) scores(0);
+            for (int j = 0; j < n_tiles && ok; ++j) {
+                ok = wait_stage(2 * j + 1) && bar_wait(p_full, j & 1, dead, status);
+                if (!ok) break;
+                fence_after();
+                const uint32_t v = stage(2 * j + 1);
+#pragma unroll
+                for (int s = 0; s < kRows / 16; ++s) {
+                    mma_ts(tmem + o, tmem + uint32_t((s >> 2) * 64 + (s & 3) * 8), desc_rows(v, s), id3, s > 0);
+                    mma_ts(tmem + o + PS, tmem + F::kMid + 8 * s, desc_rows(v, s), id2, true);
+                    mma_ts(tmem + o + 2 * PS, tmem + F::kLo + 8 * s, desc_rows(v, s), id1, true);
+                }
+                mma_commit(empty + 8 * ((2 * j + 1) % F::kStages));
+                if (j + 1 < n_tiles) {
+                    ok = wait_stage(2 * j + 2);
+                    if (ok) scores(j + 1);
+                } else {
+                    mma_commit(o_full);
+                }
+            }
+            mma_commit(fin);
+            bar_wait_last(fin, 0, status);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------------- loaders
+        const int t = threadIdx.x - (kPairWarps + 1) * 32;
+        if (n_tiles > 0) {
+            constexpr int64_t kHead = 3 * PS * 2;  // bytes of a (row, head)
+            load_planes_packed<PS, kRows>(sb, reinterpret_cast<const char*>(x.q) + (q0 * a.Hq + int64_t(h) * a.group) * kHead,
+                                          a.Hq * kHead, kHead, a.group, tl.row0, n_rows, t);
+            copy_arrive(q_full);
+            const char* K = reinterpret_cast<const char*>(x.k) + ((k0 + kr.lo) * a.Hkv + h) * kHead;
+            const char* V = reinterpret_cast<const char*>(x.v) + ((k0 + kr.lo) * a.Hkv + h) * kHead;
+            const int64_t stride = a.Hkv * kHead;
+            StateMask<> mask(a.keep ? a.keep + k0 : nullptr, kr.lo, kr.hi);
+            auto load = [&](int i, const char* src) {
+                if (i >= F::kStages && !__all_sync(0xffffffffu, bar_wait(empty + 8 * (i % F::kStages), (i / F::kStages - 1) & 1, dead, status)))
+                    return false;
+                const uint32_t dst = sb + uint32_t(F::kRing + (i % F::kStages) * F::kTile);
+                auto use = [&](int r) { return mask.has(r); };
+                if (mask.all())
+                    load_planes<PS, kRows, true>(dst, src, stride, t, use);
+                else
+                    load_planes<PS, kRows, false>(dst, src, stride, t, use);
+                copy_arrive(full + 8 * (i % F::kStages));
+                return true;
+            };
+            for (int j = 0; j < n_tiles; ++j) {
+                mask.next();
+                if (!load(2 * j, K)) break;
+                if (a.keep && t == 0) {
+                    *reinterpret_cast<uint4*>(smem + F::kMasks + (j % kRing) * 16) =
+                        make_uint4(mask.word[0], mask.word[1], mask.word[2], mask.word[3]);
+                    bar_arrive(m_full + 8 * (j % kRing));
+                }
+                if (!load(2 * j + 1, V)) break;
+                K += kRows * stride;
+                V += kRows * stride;
+            }
+            copy_wait_all();
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == kPairWarps) {
+        fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------------- backward
+
+// The walk, its order and the roles as in the 16-bit backward, in steps of 64 walked rows (the planes of two
+// resident tiles leave room for four such stages).  Tensor memory: S with plane 0 of P over it, planes 1
+// and 2 of P, dP and the planes of dS likewise, then the sums of one step: the leading terms in PS columns, the
+// small ones in PS more.
+template <int PS, bool KV>
+struct BwdPlan {
+    static constexpr int kWalk = 64, kPanel = kWalk * 128;
+    static constexpr int kTile = kPanels<PS> * kPanelBytes, kStep = kPanels<PS> * kPanel, kStages = PS == 64 ? 4 : 8;
+    static constexpr int kHalfRing = kStages / 2, kRing = 2 * kTile, kAux = kRing + kStages * kStep;
+    static constexpr int kAuxBytes = KV ? 2 * kWalk * 4 : 16, kBars = kAux + kHalfRing * kAuxBytes, kTotal = kBars + 256 + 1024;
+    static constexpr uint32_t kP1 = 64, kP2 = 96, kDp = 128, kD1 = 192, kD2 = 224, kG = 256;
+};
+
+template <int PS, bool KV>
+__global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bwd_planes(AttnArgs a, Planes x) {
+    using B = BwdPlan<PS, KV>;
+    constexpr int kOwn = KV ? PS : PS / 2;  // columns that a thread sums: dk or dv, or half of dq
+    constexpr float kLog2e = 1.4426950408889634f;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ int s_dead;
+    __shared__ uint32_t s_tmem;
+    const AttnTile tl = KV ? attn_tile(a.k_off, a.graphs, 1, kRows, blockIdx.x) : attn_tile(a.q_off, a.graphs, a.group, kRows, blockIdx.x);
+    if (tl.graph < 0) return;
+    const int h = blockIdx.y, split = blockIdx.z;
+    const int64_t q0 = a.q_off[tl.graph], k0 = a.k_off[tl.graph];
+    const int64_t rows = (a.q_off[tl.graph + 1] - q0) * a.group, states = a.k_off[tl.graph + 1] - k0;
+    const Piece walk = piece_of(KV ? rows : states, split, a.splits);
+    const int n_tiles = int((walk.hi - walk.lo + B::kWalk - 1) / B::kWalk);
+    const int own = int(min(tl.rows - tl.row0, int64_t(kRows)));
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t r_full = sb + B::kBars, s_full = r_full + 8, dp_full = s_full + 8, p_ready = dp_full + 8, ds_ready = p_ready + 8,
+                   done = ds_ready + 8, fin = done + 8, full = fin + 8, empty = full + 8 * B::kStages, aux_full = empty + 8 * B::kStages;
+    if (threadIdx.x == 0) {
+        s_dead = 0;
+        bar_init(r_full, kLoadThreads);
+        bar_init(s_full, 1);
+        bar_init(dp_full, 1);
+        bar_init(p_ready, kPairWarps);
+        bar_init(ds_ready, kPairWarps);
+        bar_init(done, 1);
+        bar_init(fin, 1);
+        for (int s = 0; s < B::kStages; ++s) {
+            bar_init(full + 8 * s, kLoadThreads);
+            bar_init(empty + 8 * s, 1);
+        }
+        for (int s = 0; s < B::kHalfRing; ++s) bar_init(aux_full + 8 * s, KV ? kLoadThreads : 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kPairWarps) tmem_alloc(smem_u32(&s_tmem), 512);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
+    volatile int* dead = &s_dead;
+    unsigned* status = &attn_status_word;
+
+    if (warp < kPairWarps) {
+        // ----------------------------------------------------------------- P and dS
+        const int w = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const bool work = quad * 32 < own;
+        const uint32_t base_t = tmem + (uint32_t(quad * 32) << 16);
+        const float c = a.scale_log2;
+        const int64_t p = tl.row0 + row;
+        float lse = INFINITY, delta = 0.f;
+        int64_t rh = 0;
+        bool keep = row < own;
+        if (keep) {
+            if (KV) {
+                rh = (k0 + p) * a.Hkv + h;
+                keep = !a.keep || a.keep[k0 + p];
+            } else {
+                rh = (q0 + p / a.group) * a.Hq + int64_t(h) * a.group + p % a.group;
+                const float v = a.lse[rh];
+                lse = v == -INFINITY ? INFINITY : v * kLog2e;  // a row without a kept state: P = exp2(s - inf) = 0
+                delta = a.delta[rh];
+            }
+        }
+        float acc[kOwn];
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) acc[i] = 0.f;
+        // the sums of the step before: dk (warpgroup 0) or dv (1), or the warpgroup's half of dq; small terms first
+        auto add_sums = [&]() {
+            const uint32_t g = base_t + B::kG + (KV ? w * 2 * PS : w * (PS / 2));
+            add_columns<kOwn>(g + PS, acc);
+            add_columns<kOwn>(g, acc);
+        };
+        bool ok = true;
+        for (int j = 0; j < n_tiles; ++j) {
+            const int ax = j % B::kHalfRing;
+            const float* s_lse = reinterpret_cast<const float*>(smem + B::kAux + ax * B::kAuxBytes) + 32 * w;
+            const float* s_delta = s_lse + B::kWalk;
+            uint32_t word = 0xffffffffu;
+            if (KV || a.keep) {
+                ok = __all_sync(0xffffffffu, bar_wait(aux_full + 8 * ax, (j / B::kHalfRing) & 1, dead, status));
+                if (!ok) break;
+            }
+            if (!KV)
+                word = a.keep ? reinterpret_cast<const uint32_t*>(smem + B::kAux + ax * B::kAuxBytes)[w]
+                              : tail_word(walk.hi - walk.lo - int64_t(j) * B::kWalk, w);
+            ok = __all_sync(0xffffffffu, bar_wait(s_full, j & 1, dead, status));
+            if (!ok) break;
+            fence_after();
+            float v[32];
+            if (work) {
+                if (KV && w == 1 && j > 0) add_sums();  // dv of the step before is complete when S of this one is
+                tmem_ld32(base_t + 32 * w, v);
+                tmem_wait_ld(v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    v[i] = exp2_approx(fmaf(v[i], c, KV ? -s_lse[i] : -lse));
+                    if (!KV && !((word >> i) & 1)) v[i] = 0.f;
+                }
+                if (KV) {
+                    store_planes(v, base_t + 32 * w, base_t + B::kP1 + 16 * w, base_t + B::kP2 + 16 * w);
+                    tmem_wait_st();
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(p_ready);
+            ok = __all_sync(0xffffffffu, bar_wait(dp_full, j & 1, dead, status));
+            if (!ok) break;
+            fence_after();
+            if (work) {
+                if ((!KV || w == 0) && j > 0) add_sums();  // dk, dq of the step before: complete when dP of this one is
+                float y[32];
+                tmem_ld32(base_t + B::kDp + 32 * w, y);
+                tmem_wait_ld(y);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    y[i] = v[i] * (y[i] - (KV ? s_delta[i] : delta));
+                    if (!KV && !((word >> i) & 1)) y[i] = 0.f;
+                }
+                store_planes(y, base_t + B::kDp + 32 * w, base_t + B::kD1 + 16 * w, base_t + B::kD2 + 16 * w);
+                tmem_wait_st();
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(ds_ready);
+        }
+        if (ok && n_tiles > 0) {
+            ok = __all_sync(0xffffffffu, bar_wait(done, 0, dead, status));
+            fence_after();
+        }
+        if (ok && work) {
+            if (n_tiles > 0) add_sums();
+            if (row < own) {
+                const int64_t n = KV ? a.nk * a.Hkv : a.nq * a.Hq;
+                float* dst = static_cast<float*>(KV ? (w ? a.dv : a.dk) : a.dq) + rh * a.D;
+                if (a.splits > 1) dst = a.part_o + ((KV && w ? a.splits + split : split) * n + rh) * a.D;
+                if (!keep) {
+#pragma unroll
+                    for (int i = 0; i < kOwn; ++i) acc[i] = 0.f;
+                }
+                store_row<kOwn>(dst, acc, KV && w ? 1.f : a.scale, KV ? 0 : w * (PS / 2), a.D);
+            }
+        }
+    } else if (warp == kPairWarps) {
+        // ----------------------------------------------------------------- matrix instructions
+        if (lane == 0) {
+            const uint32_t id_s = mma_desc<__nv_bfloat16>(B::kWalk, false), id2 = mma_desc<__nv_bfloat16>(2 * PS, true),
+                           id1 = mma_desc<__nv_bfloat16>(PS, true);
+            const uint32_t r1 = sb, r2 = sb + uint32_t(B::kTile);
+            auto stage = [&](int i) { return sb + uint32_t(B::kRing + (i % B::kStages) * B::kStep); };
+            auto wait_stage = [&](int i) {
+                if (!bar_wait(full + 8 * (i % B::kStages), (i / B::kStages) & 1, dead, status)) return false;
+                fence_async();
+                return true;
+            };
+            auto product = [&](uint32_t d, uint32_t r, uint32_t xs, uint32_t bar) {
+                six_products<PS>(d, r, kPanelBytes, xs, B::kPanel, id_s);
+                mma_commit(bar);
+            };
+            // d = A X over the step's 64 rows, A in planes at a0 (its warpgroups' halves apart), a1, a2
+            auto sum = [&](uint32_t d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t xs) {
+#pragma unroll
+                for (int s = 0; s < B::kWalk / 16; ++s) {
+                    const uint32_t hi = a0 + uint32_t((s >> 1) * 32 + (s & 1) * 8);
+                    mma_ts(d, hi, desc_rows(xs, s, B::kPanel), id2, s > 0);
+                    mma_ts(d + PS, hi, desc_rows(xs, s, B::kPanel, 2 * PS), id1, true);
+                    mma_ts(d + PS, a1 + 8 * s, desc_rows(xs, s, B::kPanel), id1, true);
+                    mma_ts(d + PS, a1 + 8 * s, desc_rows(xs, s, B::kPanel, PS), id1, true);
+                    mma_ts(d + PS, a2 + 8 * s, desc_rows(xs, s, B::kPanel), id1, true);
+                }
+            };
+            bool ok = n_tiles > 0 && bar_wait(r_full, 0, dead, status) && wait_stage(0);
+            if (ok) {
+                product(tmem, r1, stage(0), s_full);
+                ok = wait_stage(1);
+                if (ok) {
+                    product(tmem + B::kDp, r2, stage(1), dp_full);
+                    if (!KV) mma_commit(empty + 8 * 1);
+                }
+            }
+            for (int j = 0; j < n_tiles && ok; ++j) {
+                ok = bar_wait(p_ready, j & 1, dead, status);
+                if (!ok) break;
+                fence_after();
+                if (KV) {
+                    sum(tmem + B::kG + 2 * PS, tmem, tmem + B::kP1, tmem + B::kP2, stage(2 * j + 1));
+                    mma_commit(empty + 8 * ((2 * j + 1) % B::kStages));
+                }
+                if (j + 1 < n_tiles) {
+                    ok = wait_stage(2 * j + 2);
+                    if (!ok) break;
+                    product(tmem, r1, stage(2 * j + 2), s_full);
+                }
+                ok = bar_wait(ds_ready, j & 1, dead, status);
+                if (!ok) break;
+                fence_after();
+                sum(tmem + B::kG, tmem + B::kDp, tmem + B::kD1, tmem + B::kD2, stage(2 * j));
+                mma_commit(empty + 8 * ((2 * j) % B::kStages));
+                if (j + 1 < n_tiles) {
+                    ok = wait_stage(2 * j + 3);
+                    if (!ok) break;
+                    product(tmem + B::kDp, r2, stage(2 * j + 3), dp_full);
+                    if (!KV) mma_commit(empty + 8 * ((2 * j + 3) % B::kStages));
+                } else {
+                    mma_commit(done);
+                }
+            }
+            mma_commit(fin);
+            bar_wait_last(fin, 0, status);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------------- loaders
+        const int t = threadIdx.x - (kPairWarps + 1) * 32;
+        if (n_tiles > 0) {
+            constexpr int64_t kHead = 3 * PS * 2;  // bytes of a (row, head)
+            const int64_t q_at = (q0 * a.Hq + int64_t(h) * a.group) * kHead, q_row = a.Hq * kHead, k_row = a.Hkv * kHead;
+            const char *Q = reinterpret_cast<const char*>(x.q) + q_at, *dO = reinterpret_cast<const char*>(x.d_out) + q_at;
+            const int64_t k_at = ((k0 + (KV ? tl.row0 : walk.lo)) * a.Hkv + h) * kHead;
+            const char *K = reinterpret_cast<const char*>(x.k) + k_at, *V = reinterpret_cast<const char*>(x.v) + k_at;
+            auto free_stage = [&](int i) {
+                return i < B::kStages || __all_sync(0xffffffffu, bar_wait(empty + 8 * (i % B::kStages), (i / B::kStages - 1) & 1, dead, status));
+            };
+            auto stage = [&](int i) { return sb + uint32_t(B::kRing + (i % B::kStages) * B::kStep); };
+            if (KV) {
+                StateMask<> mask(a.keep ? a.keep + k0 : nullptr, tl.row0, states);
+                mask.next();
+                auto use = [&](int r) { return mask.has(r); };
+                load_planes<PS, kRows, false>(sb, K, k_row, t, use);
+                load_planes<PS, kRows, false>(sb + uint32_t(B::kTile), V, k_row, t, use);
+            } else {
+                load_planes_packed<PS, kRows>(sb, Q, q_row, kHead, a.group, tl.row0, own, t);
+                load_planes_packed<PS, kRows>(sb + uint32_t(B::kTile), dO, q_row, kHead, a.group, tl.row0, own, t);
+            }
+            copy_arrive(r_full);
+            // lse and delta of the walked rows, fetched a step ahead
+            float v_lse = -INFINITY, v_delta = 0.f;
+            auto fetch = [&](int j) {
+                const int64_t r = walk.lo + int64_t(j) * B::kWalk + t;
+                v_lse = -INFINITY, v_delta = 0.f;
+                if (r < walk.hi) {
+                    const int64_t q = r / a.group, at = (q0 + q) * a.Hq + int64_t(h) * a.group + (r - q * a.group);
+                    v_lse = a.lse[at];
+                    v_delta = a.delta[at];
+                }
+            };
+            if (KV) fetch(0);
+            StateMask<B::kWalk> mask(!KV && a.keep ? a.keep + k0 : nullptr, walk.lo, walk.hi);
+            for (int j = 0; j < n_tiles; ++j) {
+                const int64_t lo = walk.lo + int64_t(j) * B::kWalk;
+                const int n = int(min(walk.hi - lo, int64_t(B::kWalk)));
+                if (!free_stage(2 * j)) break;
+                // the step that used this aux entry before gave up its X1 stage, which is this one
+                if (KV) {
+                    float* s_lse = reinterpret_cast<float*>(smem + B::kAux + (j % B::kHalfRing) * B::kAuxBytes);
+                    // rows past the end and rows without a kept state: P = exp2(s - inf) = 0
+                    s_lse[t] = v_lse == -INFINITY ? INFINITY : v_lse * kLog2e;
+                    s_lse[B::kWalk + t] = v_delta;
+                    bar_arrive(aux_full + 8 * (j % B::kHalfRing));
+                    if (j + 1 < n_tiles) fetch(j + 1);
+                    load_planes_packed<PS, B::kWalk>(stage(2 * j), Q, q_row, kHead, a.group, lo, n, t);
+                    copy_arrive(full + 8 * ((2 * j) % B::kStages));
+                    if (!free_stage(2 * j + 1)) break;
+                    load_planes_packed<PS, B::kWalk>(stage(2 * j + 1), dO, q_row, kHead, a.group, lo, n, t);
+                    copy_arrive(full + 8 * ((2 * j + 1) % B::kStages));
+                } else {
+                    mask.next();
+                    if (a.keep && t == 0) {
+                        *reinterpret_cast<uint2*>(smem + B::kAux + (j % B::kHalfRing) * B::kAuxBytes) = make_uint2(mask.word[0], mask.word[1]);
+                        bar_arrive(aux_full + 8 * (j % B::kHalfRing));
+                    }
+                    auto use = [&](int r) { return mask.has(r); };
+                    auto load = [&](uint32_t dst, const char* src) {
+                        if (mask.all())
+                            load_planes<PS, B::kWalk, true>(dst, src, k_row, t, use);
+                        else
+                            load_planes<PS, B::kWalk, false>(dst, src, k_row, t, use);
+                    };
+                    load(stage(2 * j), K);
+                    copy_arrive(full + 8 * ((2 * j) % B::kStages));
+                    if (!free_stage(2 * j + 1)) break;
+                    load(stage(2 * j + 1), V);
+                    copy_arrive(full + 8 * ((2 * j + 1) % B::kStages));
+                    K += B::kWalk * k_row;
+                    V += B::kWalk * k_row;
+                }
+            }
+            copy_wait_all();
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == kPairWarps) {
+        fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+template <typename F>
+cudaError_t by_plane(int D, F f) {
+    if (D <= 16) return f(std::integral_constant<int, 16>{});
+    if (D <= 32) return f(std::integral_constant<int, 32>{});
+    return f(std::integral_constant<int, 64>{});
+}
+int plane_stride(int D) { return D <= 16 ? 16 : D <= 32 ? 32 : 64; }
+
+// The planes' places in the workspace, in the order q, k, v, d_out.
+Planes planes_at(const AttnArgs& a, void* ws) {
+    const size_t w = size_t(3) * plane_stride(a.D);
+    uint16_t* p = static_cast<uint16_t*>(ws);
+    Planes x;
+    x.q = p;
+    x.k = x.q + size_t(a.nq) * a.Hq * w;
+    x.v = x.k + size_t(a.nk) * a.Hkv * w;
+    x.d_out = x.v + size_t(a.nk) * a.Hkv * w;
+    return x;
+}
+
+}  // namespace
+
+size_t attn_planes_bytes(const AttnShape& s, bool bwd) {
+    const size_t w = size_t(6) * plane_stride(s.head_dim);
+    const size_t q = size_t(s.n_q) * s.q_heads * w, k = size_t(s.n_k) * s.kv_heads * w;
+    return q + 2 * k + (bwd ? q : 0);
+}
+
+// Writes the planes of q, k, v and, where there is one, d_out.
+cudaError_t launch_attn_planes(const AttnArgs& a, void* ws, int sms, cudaStream_t st) {
+    const Planes x = planes_at(a, ws);
+    PlaneJobs j = {};
+    j.D = a.D;
+    j.j[0] = {static_cast<const float*>(a.q), a.q_row, a.q_head, a.nq, a.Hq, const_cast<uint16_t*>(x.q)};
+    j.j[1] = {static_cast<const float*>(a.k), a.k_row, a.k_head, a.nk, a.Hkv, const_cast<uint16_t*>(x.k)};
+    j.j[2] = {static_cast<const float*>(a.v), a.v_row, a.v_head, a.nk, a.Hkv, const_cast<uint16_t*>(x.v)};
+    j.j[3] = {static_cast<const float*>(a.d_out), a.o_row, a.o_head, a.d_out ? a.nq : 0, a.Hq, const_cast<uint16_t*>(x.d_out)};
+    const int64_t most = std::max(a.nq * a.Hq, a.nk * a.Hkv) * (plane_stride(a.D) / 8);
+    const unsigned blocks = unsigned(std::min<int64_t>((most + 255) / 256, int64_t(sms) * 8));
+    return by_plane(a.D, [&](auto ps) {
+        attn_planes<decltype(ps)::value><<<dim3(blocks, a.d_out ? 4 : 3), 256, 0, st>>>(j);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t launch_attn_fwd_planes(const AttnArgs& a, void* ws, int64_t row_tiles, cudaStream_t st) {
+    const Planes x = planes_at(a, ws);
+    return by_plane(a.D, [&](auto ps) {
+        constexpr int PS = decltype(ps)::value;
+        cudaError_t e = cudaFuncSetAttribute(attn_fwd_planes<PS>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdPlan<PS>::kTotal);
+        if (e != cudaSuccess) return e;
+        attn_fwd_planes<PS><<<dim3(unsigned(row_tiles), unsigned(a.Hkv), unsigned(a.splits)), (kPairWarps + 1 + kLoadWarps) * 32,
+                              FwdPlan<PS>::kTotal, st>>>(a, x);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t launch_attn_bwd_planes(const AttnArgs& a, void* ws, bool kv, int64_t tiles, cudaStream_t st) {
+    const Planes x = planes_at(a, ws);
+    return by_plane(a.D, [&](auto ps) {
+        constexpr int PS = decltype(ps)::value;
+        auto go = [&](auto k, int smem) {
+            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            k<<<dim3(unsigned(tiles), unsigned(a.Hkv), unsigned(a.splits)), (kPairWarps + 1 + kLoadWarps) * 32, smem, st>>>(a, x);
+            return cudaGetLastError();
+        };
+        return kv ? go(attn_bwd_planes<PS, true>, BwdPlan<PS, true>::kTotal) : go(attn_bwd_planes<PS, false>, BwdPlan<PS, false>::kTotal);
+    });
+}
+
+cudaError_t attn_planes_status(unsigned* word, bool reset) { return read_status(word, reset); }
+
+}  // namespace uvu

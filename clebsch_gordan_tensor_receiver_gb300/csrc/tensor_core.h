@@ -36,7 +36,7 @@ __device__ __forceinline__ unsigned long long timer_ns() {
 }
 // Waits for the phase of `parity` to end.  False when another role has given up (*dead) or after
 // about two seconds, which sets *dead and the status word; the caller then leaves its loop.
-__device__ __noinline__ bool bar_wait_slow(uint32_t b, uint32_t parity, volatile int* dead, unsigned* status) {
+static __device__ __noinline__ bool bar_wait_slow(uint32_t b, uint32_t parity, volatile int* dead, unsigned* status) {
     const unsigned long long t0 = timer_ns();
     for (;;) {
         for (int i = 0; i < 32; ++i)
@@ -50,7 +50,7 @@ __device__ __noinline__ bool bar_wait_slow(uint32_t b, uint32_t parity, volatile
     }
 }
 // The last wait before a role returns what others still use: bounded, whatever *dead says.
-__device__ __noinline__ void bar_wait_last(uint32_t b, uint32_t parity, unsigned* status) {
+static __device__ __noinline__ void bar_wait_last(uint32_t b, uint32_t parity, unsigned* status) {
     const unsigned long long t0 = timer_ns();
     while (!bar_test(b, parity))
         if (timer_ns() - t0 > 2000000000ull) {
@@ -87,16 +87,18 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {  // chunk:
 }
 
 constexpr uint64_t kDescBase = (1ull << 46) | (2ull << 61);  // version bits, 128-byte swizzle
-// The tile's columns are the summed index (16 of them, beginning at column 16 k): 8-row groups are 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_cols(uint32_t tile, int k) {
-    const uint32_t a = tile + uint32_t((k >> 2) * kPanelBytes + (k & 3) * 32);
+// The tile's columns are the summed index (16 of them, beginning at column 16 k): 8-row groups are 1024
+// bytes apart.  `panel`: bytes of a panel.
+__device__ __forceinline__ uint64_t desc_cols(uint32_t tile, int k, int panel = kPanelBytes) {
+    const uint32_t a = tile + uint32_t((k >> 2) * panel + (k & 3) * 32);
     return uint64_t((a >> 4) & 0x3FFFu) | (1ull << 16) | (uint64_t(1024 >> 4) << 32) | kDescBase;
 }
 // The tile's rows are the summed index (16 of them, beginning at row 16 k): panels of 64 columns are
-// kPanelBytes apart, groups of 8 rows 1024 bytes.
-__device__ __forceinline__ uint64_t desc_rows(uint32_t tile, int k) {
-    const uint32_t a = tile + uint32_t(k * 2048);
-    return uint64_t((a >> 4) & 0x3FFFu) | (uint64_t(kPanelBytes >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | kDescBase;
+// `panel` bytes apart, groups of 8 rows 1024 bytes.  col: first column; columns from a col that is not a
+// multiple of 64 must end within its panel.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t tile, int k, int panel = kPanelBytes, int col = 0) {
+    const uint32_t a = tile + uint32_t(k * 2048 + (col >> 6) * panel + (col & 63) * 2);
+    return uint64_t((a >> 4) & 0x3FFFu) | (uint64_t(panel >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | kDescBase;
 }
 
 // Instruction descriptor of kind::f16 with fp32 sums: M = 128, N = n; B's rows (true) or columns are the summed index.
@@ -160,6 +162,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, float (&r)[32]) {
           "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
           "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(a));
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t a, float (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(a));
+}
+__device__ __forceinline__ void tmem_wait_ld(float (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7])::"memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t a, float (&r)[16]) {
     asm volatile(
