@@ -1,4 +1,4 @@
-// Arguments of the attention kernels (attn.cu: launch choices and CUDA-core kernels).
+// Arguments of the attention kernels (attn.cu: launch choices and joining kernels).
 #pragma once
 
 #include "plan.h"
@@ -56,8 +56,10 @@ cudaError_t launch_attn_fwd_mma(uvu_dtype dtype, const AttnArgs& a, int nt, int6
 // The backward of 16-bit operands: dk and dv (kv) by tiles of 128 states, or dq by tiles of 128 rows.
 cudaError_t launch_attn_bwd_mma(uvu_dtype dtype, const AttnArgs& a, bool kv, int64_t tiles, cudaStream_t st);
 
-// attn_planes.cu: fp32 operands with head_dim <= 64 as three bf16 planes each, in the workspace.
-constexpr int kPlaneDim = 64;
+// attn_planes.cu: fp32 operands as three bf16 planes each, in the workspace.  The backward's tiles have
+// plane_bwd_tile() rows or states; above a head dimension of 64 it walks at most kPlaneWalk of the others in one piece.
+constexpr int kPlaneWalk = 4096;
+constexpr int plane_bwd_tile(int head_dim) { return head_dim <= 64 ? 128 : 64; }
 size_t attn_planes_bytes(const AttnShape& s, bool bwd);
 cudaError_t launch_attn_planes(const AttnArgs& a, void* ws, int sms, cudaStream_t st);
 cudaError_t launch_attn_fwd_planes(const AttnArgs& a, void* ws, int64_t row_tiles, cudaStream_t st);

@@ -1,4 +1,4 @@
-// Attention of fp32 operands on the 16-bit tensor cores, with fp32 accuracy (head dimensions to 64).
+// Attention of fp32 operands on the 16-bit tensor cores, with fp32 accuracy.
 //
 // An fp32 value is the exact sum of three bf16 values, its leading 8 significant bits, the next 8 and
 // the last 8 (x = x0 + x1 + x2, each remainder cut to its upper half: bf16 has the exponent range of
@@ -6,14 +6,16 @@
 // i + j <= 2; what is dropped is 2^-24 of it.  That is six bf16 products, at 1/6 of their rate still several
 // times the CUDA cores' fp32 rate.
 //   - A first kernel writes the planes of q, k, v (and d_out) to the workspace, [row][head][3][PS] with
-//     PS = 16, 32 or 64 columns a plane (zeros past head_dim), so that the loaders below move them like any 16-bit
+//     PS = 16, 32, 64 or 128 columns a plane (zeros past head_dim), so that the loaders below move them like any 16-bit
 //     operand.  Infinities and NaN stay in x0.
 //   - S (and dP): the six products are issued smallest first into one accumulator.
 //   - P (and dS) are cut into planes by the threads that form them; with X = [X0 | X1 | X2] side by side in
 //     the tile, P0 X, P1 [X0 | X1] and P2 X0 land in columns by order of magnitude: the sums of the small terms
 //     are apart from the large ones, and the threads add them.
 //   - Tensor memory sums each tile afresh; the sums over tiles are fp32 registers (accumulating in tensor
-//     memory loses more than a rounded fp32 addition does, and long rows would show it).
+//     memory loses more than a rounded fp32 addition does, and long rows would show it).  The backward at
+//     PS = 128 has no registers for that: it sums in tensor memory, over walks of at most kPlaneWalk rows
+//     (about 4e-9 of the sum is lost per 16 rows), and the joining kernel adds the walks.
 // Masks, splits and bounded waits as in the 16-bit kernels.
 #include "attn_mma.h"
 
@@ -124,19 +126,33 @@ __device__ __forceinline__ void six_products(uint32_t d, uint32_t a, int a_panel
         }
 }
 
-// 32 values of a row to the three planes of a 16-bit operand in tensor memory (16 columns each).
-__device__ __forceinline__ void store_planes(const float (&x)[32], uint32_t hi, uint32_t mid, uint32_t lo) {
-    uint32_t w[3][16];
+// N (32 or 16) values of a row to the three planes of a 16-bit operand in tensor memory.
+template <int N>
+__device__ __forceinline__ void store_planes(const float (&x)[N], uint32_t hi, uint32_t mid, uint32_t lo) {
+    uint32_t w[3][N / 2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < N / 2; ++i) {
         uint32_t p[3];
         cut2(x[2 * i], x[2 * i + 1], p);
 #pragma unroll
         for (int q = 0; q < 3; ++q) w[q][i] = p[q];
     }
-    tmem_st16(hi, w[0]);
-    tmem_st16(mid, w[1]);
-    tmem_st16(lo, w[2]);
+    const uint32_t at[3] = {hi, mid, lo};
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+        if constexpr (N == 32)
+            tmem_st16(at[q], w[q]);
+        else
+            tmem_st8(at[q], w[q]);
+    }
+}
+__device__ __forceinline__ void load_columns(uint32_t a, float (&v)[32]) { tmem_ld32(a, v); }
+__device__ __forceinline__ void load_columns(uint32_t a, float (&v)[16]) { tmem_ld16(a, v); }
+
+// Column of 16-row block s of a plane-0 operand that its two warpgroups wrote over their halves (`half`
+// columns each) of the fp32 tile.
+__device__ __forceinline__ uint32_t block_column(int s, int half) {
+    return uint32_t(s / (half / 16) * half + s % (half / 16) * 8);
 }
 
 // acc[i] += columns i of N at `a`
@@ -177,19 +193,22 @@ __device__ __forceinline__ void store_row(float* dst, const float* v, float scal
 
 // ----------------------------------------------------------------------------------- forward
 
+// State tiles of 128, or of 64 where a tile's planes would not fit beside Q's (PS = 128).
 template <int PS>
 struct FwdPlan {
-    static constexpr int kTile = kPanels<PS> * kPanelBytes, kStages = PS == 64 ? 3 : PS == 32 ? 5 : 8;
-    static constexpr int kRing = kTile, kMasks = kRing + kStages * kTile, kMax = kMasks + 8 * 16, kBars = kMax + 2 * 2 * kRows * 4;
+    static constexpr int kState = PS == 128 ? 64 : 128, kHalfState = kState / 2, kPanel = kState * 128;
+    static constexpr int kTile = kPanels<PS> * kPanelBytes, kStep = kPanels<PS> * kPanel;
+    static constexpr int kStages = PS == 128 ? 2 : PS == 64 ? 3 : PS == 32 ? 5 : 8;
+    static constexpr int kRing = kTile, kMasks = kRing + kStages * kStep, kMax = kMasks + 8 * 16, kBars = kMax + 2 * 2 * kRows * 4;
     static constexpr int kTotal = kBars + 512 + 1024;  // barriers, alignment slack
-    // tensor memory: S (its plane 0 of P written over it), planes 1 and 2 of P, O by order
-    static constexpr uint32_t kMid = kRows, kLo = kRows + 64, kO = kRows + 128;
+    // tensor memory: S (plane 0 of P written over it), planes 1 and 2 of P, O by order
+    static constexpr uint32_t kMid = kState, kLo = kState + kState / 2, kO = 2 * kState;
 };
 
 template <int PS>
 __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fwd_planes(AttnArgs a, Planes x) {
     using F = FwdPlan<PS>;
-    constexpr int kHalf = PS / 2, kRing = 8;
+    constexpr int kHalf = PS / 2, kRing = 8, kBlocks = F::kHalfState / 32;  // 32-column blocks of a warpgroup
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_dead;
     __shared__ uint32_t s_tmem;
@@ -198,7 +217,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
     const int h = blockIdx.y, split = blockIdx.z;
     const int64_t q0 = a.q_off[tl.graph], k0 = a.k_off[tl.graph];
     const Piece kr = piece_of(a.k_off[tl.graph + 1] - k0, split, a.splits);
-    const int n_tiles = int((kr.hi - kr.lo + kRows - 1) / kRows);
+    const int n_tiles = int((kr.hi - kr.lo + F::kState - 1) / F::kState);
     const int n_rows = int(min(tl.rows - tl.row0, int64_t(kRows)));
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
@@ -235,7 +254,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
         const uint32_t lanes = uint32_t(quad * 32) << 16, base_t = tmem + lanes;
         const float c = a.scale_log2;
         float* s_max = reinterpret_cast<float*>(smem + F::kMax);  // [turn][warpgroup][row]
-        const uint32_t* masks = reinterpret_cast<const uint32_t*>(smem + F::kMasks) + 2 * w;
+        const uint32_t* masks = reinterpret_cast<const uint32_t*>(smem + F::kMasks) + kBlocks * w;
         float m = -INFINITY, l = 0.f, acc[kHalf];
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
@@ -259,28 +278,28 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
             add_columns<kHalf>(base_t + F::kO + w * kHalf, acc);
         };
         for (int j = 0; j < n_tiles; ++j) {
-            uint32_t word[2];
+            uint32_t word[kBlocks];
             if (a.keep) {
                 ok = __all_sync(0xffffffffu, bar_wait(m_full + 8 * (j % kRing), (j / kRing) & 1, dead, status));
                 if (!ok) break;
-                word[0] = masks[(j % kRing) * 4];
-                word[1] = masks[(j % kRing) * 4 + 1];
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) word[b] = masks[(j % kRing) * 4 + b];
             } else {
-                const int64_t left = kr.hi - kr.lo - int64_t(j) * kRows;
-                word[0] = tail_word(left, 2 * w);
-                word[1] = tail_word(left, 2 * w + 1);
+                const int64_t left = kr.hi - kr.lo - int64_t(j) * F::kState;
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) word[b] = tail_word(left, kBlocks * w + b);
             }
             ok = __all_sync(0xffffffffu, bar_wait(s_full, j & 1, dead, status));
             if (!ok) break;
             fence_after();
             if (work) {
                 if (j > 0) add_o();  // O of the tile before is complete when S of this one is
-                float v[2][32];
+                float v[kBlocks][32];
                 float top = -INFINITY;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) tmem_ld32(base_t + 64 * w + 32 * b, v[b]);
+                for (int b = 0; b < kBlocks; ++b) tmem_ld32(base_t + F::kHalfState * w + 32 * b, v[b]);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int b = 0; b < kBlocks; ++b) {
                     tmem_wait_ld(v[b]);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -296,7 +315,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
 #pragma unroll
                 for (int i = 0; i < kHalf; ++i) acc[i] *= f;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int b = 0; b < kBlocks; ++b) {
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
@@ -304,7 +323,8 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
                         sum[i & 3] += v[b][i];
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    store_planes(v[b], base_t + 64 * w + 16 * b, base_t + F::kMid + 32 * w + 16 * b, base_t + F::kLo + 32 * w + 16 * b);
+                    store_planes(v[b], base_t + F::kHalfState * w + 16 * b, base_t + F::kMid + F::kHalfState / 2 * w + 16 * b,
+                                 base_t + F::kLo + F::kHalfState / 2 * w + 16 * b);
                 }
                 tmem_wait_st();
             }
@@ -340,16 +360,16 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
         // ----------------------------------------------------------------- matrix instructions
         if (lane == 0) {
             constexpr uint32_t o = F::kO;
-            const uint32_t id_s = mma_desc<__nv_bfloat16>(kRows, false), id3 = mma_desc<__nv_bfloat16>(3 * PS, true),
+            const uint32_t id_s = mma_desc<__nv_bfloat16>(F::kState, false), id3 = mma_desc<__nv_bfloat16>(3 * PS <= 256 ? 3 * PS : 256, true),
                            id2 = mma_desc<__nv_bfloat16>(2 * PS, true), id1 = mma_desc<__nv_bfloat16>(PS, true);
-            auto stage = [&](int i) { return sb + uint32_t(F::kRing + (i % F::kStages) * F::kTile); };
+            auto stage = [&](int i) { return sb + uint32_t(F::kRing + (i % F::kStages) * F::kStep); };
             auto wait_stage = [&](int i) {
                 if (!bar_wait(full + 8 * (i % F::kStages), (i / F::kStages) & 1, dead, status)) return false;
                 fence_async();
                 return true;
             };
             auto scores = [&](int j) {
-                six_products<PS>(tmem, sb, kPanelBytes, stage(2 * j), kPanelBytes, id_s);
+                six_products<PS>(tmem, sb, kPanelBytes, stage(2 * j), F::kPanel, id_s);
                 mma_commit(s_full);
                 mma_commit(empty + 8 * ((2 * j) % F::kStages));
             };
@@ -361,10 +381,17 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
                 fence_after();
                 const uint32_t v = stage(2 * j + 1);
 #pragma unroll
-                for (int s = 0; s < kRows / 16; ++s) {
-                    mma_ts(tmem + o, tmem + uint32_t((s >> 2) * 64 + (s & 3) * 8), desc_rows(v, s), id3, s > 0);
-                    mma_ts(tmem + o + PS, tmem + F::kMid + 8 * s, desc_rows(v, s), id2, true);
-                    mma_ts(tmem + o + 2 * PS, tmem + F::kLo + 8 * s, desc_rows(v, s), id1, true);
+                for (int s = 0; s < F::kState / 16; ++s) {
+                    const uint32_t hi = tmem + block_column(s, F::kHalfState), mid = tmem + F::kMid + 8 * s, lo = tmem + F::kLo + 8 * s;
+                    const uint64_t v0 = desc_rows(v, s, F::kPanel);
+                    if constexpr (3 * PS <= 256) {
+                        mma_ts(tmem + o, hi, v0, id3, s > 0);
+                    } else {  // 256 columns at most
+                        mma_ts(tmem + o, hi, v0, id2, s > 0);
+                        mma_ts(tmem + o + 2 * PS, hi, desc_rows(v, s, F::kPanel, 2 * PS), id1, s > 0);
+                    }
+                    mma_ts(tmem + o + PS, mid, v0, id2, true);
+                    mma_ts(tmem + o + 2 * PS, lo, v0, id1, true);
                 }
                 mma_commit(empty + 8 * ((2 * j + 1) % F::kStages));
                 if (j + 1 < n_tiles) {
@@ -389,16 +416,16 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
             const char* K = reinterpret_cast<const char*>(x.k) + ((k0 + kr.lo) * a.Hkv + h) * kHead;
             const char* V = reinterpret_cast<const char*>(x.v) + ((k0 + kr.lo) * a.Hkv + h) * kHead;
             const int64_t stride = a.Hkv * kHead;
-            StateMask<> mask(a.keep ? a.keep + k0 : nullptr, kr.lo, kr.hi);
+            StateMask<F::kState> mask(a.keep ? a.keep + k0 : nullptr, kr.lo, kr.hi);
             auto load = [&](int i, const char* src) {
                 if (i >= F::kStages && !__all_sync(0xffffffffu, bar_wait(empty + 8 * (i % F::kStages), (i / F::kStages - 1) & 1, dead, status)))
                     return false;
-                const uint32_t dst = sb + uint32_t(F::kRing + (i % F::kStages) * F::kTile);
+                const uint32_t dst = sb + uint32_t(F::kRing + (i % F::kStages) * F::kStep);
                 auto use = [&](int r) { return mask.has(r); };
                 if (mask.all())
-                    load_planes<PS, kRows, true>(dst, src, stride, t, use);
+                    load_planes<PS, F::kState, true>(dst, src, stride, t, use);
                 else
-                    load_planes<PS, kRows, false>(dst, src, stride, t, use);
+                    load_planes<PS, F::kState, false>(dst, src, stride, t, use);
                 copy_arrive(full + 8 * (i % F::kStages));
                 return true;
             };
@@ -407,12 +434,12 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
                 if (!load(2 * j, K)) break;
                 if (a.keep && t == 0) {
                     *reinterpret_cast<uint4*>(smem + F::kMasks + (j % kRing) * 16) =
-                        make_uint4(mask.word[0], mask.word[1], mask.word[2], mask.word[3]);
+                        make_uint4(mask.word[0], mask.word[1], mask.word[F::kState / 32 - 2], mask.word[F::kState / 32 - 1]);
                     bar_arrive(m_full + 8 * (j % kRing));
                 }
                 if (!load(2 * j + 1, V)) break;
-                K += kRows * stride;
-                V += kRows * stride;
+                K += F::kState * stride;
+                V += F::kState * stride;
             }
             copy_wait_all();
         }
@@ -431,31 +458,37 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
 // resident tiles leave room for four such stages).  Tensor memory: S with plane 0 of P over it, planes 1
 // and 2 of P, dP and the planes of dS likewise, then the sums of one step: the leading terms in PS columns, the
 // small ones in PS more.
+// At PS = 128 the resident tiles have 64 rows (the instructions still take 128: the upper half reads
+// whatever follows in shared memory, into lanes that nobody reads), steps have 32, and dk, dv and dq are summed
+// over the walk in tensor memory, each step's small terms first.
 template <int PS, bool KV>
 struct BwdPlan {
-    static constexpr int kWalk = 64, kPanel = kWalk * 128;
-    static constexpr int kTile = kPanels<PS> * kPanelBytes, kStep = kPanels<PS> * kPanel, kStages = PS == 64 ? 4 : 8;
+    static constexpr bool kWide = PS == 128;
+    static constexpr int kOwn = kWide ? 64 : 128, kWalk = kWide ? 32 : 64, kHalf = kWalk / 2;
+    static constexpr int kOwnPanel = kOwn * 128, kPanel = kWalk * 128;
+    static constexpr int kTile = kPanels<PS> * kOwnPanel, kStep = kPanels<PS> * kPanel, kStages = PS >= 64 ? 4 : 8;
     static constexpr int kHalfRing = kStages / 2, kRing = 2 * kTile, kAux = kRing + kStages * kStep;
-    static constexpr int kAuxBytes = KV ? 2 * kWalk * 4 : 16, kBars = kAux + kHalfRing * kAuxBytes, kTotal = kBars + 256 + 1024;
-    static constexpr uint32_t kP1 = 64, kP2 = 96, kDp = 128, kD1 = 192, kD2 = 224, kG = 256;
+    static constexpr int kAuxBytes = KV ? 2 * kWalk * 4 : 16, kBars = kAux + kHalfRing * kAuxBytes, kTotal = kBars + 512 + 1024;
+    static constexpr uint32_t kP1 = kWalk, kP2 = kP1 + kHalf, kDp = 2 * kWalk, kD1 = kDp + kWalk, kD2 = kD1 + kHalf, kG = 4 * kWalk;
+    static constexpr int kGrad = kWide ? PS : 2 * PS;  // columns of a gradient's sums
 };
 
 template <int PS, bool KV>
 __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bwd_planes(AttnArgs a, Planes x) {
     using B = BwdPlan<PS, KV>;
-    constexpr int kOwn = KV ? PS : PS / 2;  // columns that a thread sums: dk or dv, or half of dq
+    constexpr int kCols = KV ? PS : PS / 2;  // columns of a thread: dk or dv, or half of dq
     constexpr float kLog2e = 1.4426950408889634f;
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_dead;
     __shared__ uint32_t s_tmem;
-    const AttnTile tl = KV ? attn_tile(a.k_off, a.graphs, 1, kRows, blockIdx.x) : attn_tile(a.q_off, a.graphs, a.group, kRows, blockIdx.x);
+    const AttnTile tl = KV ? attn_tile(a.k_off, a.graphs, 1, B::kOwn, blockIdx.x) : attn_tile(a.q_off, a.graphs, a.group, B::kOwn, blockIdx.x);
     if (tl.graph < 0) return;
     const int h = blockIdx.y, split = blockIdx.z;
     const int64_t q0 = a.q_off[tl.graph], k0 = a.k_off[tl.graph];
     const int64_t rows = (a.q_off[tl.graph + 1] - q0) * a.group, states = a.k_off[tl.graph + 1] - k0;
     const Piece walk = piece_of(KV ? rows : states, split, a.splits);
     const int n_tiles = int((walk.hi - walk.lo + B::kWalk - 1) / B::kWalk);
-    const int own = int(min(tl.rows - tl.row0, int64_t(kRows)));
+    const int own = int(min(tl.rows - tl.row0, int64_t(B::kOwn)));
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -506,19 +539,23 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                 delta = a.delta[rh];
             }
         }
-        float acc[kOwn];
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) acc[i] = 0.f;
         // the sums of the step before: dk (warpgroup 0) or dv (1), or the warpgroup's half of dq; small terms first
+        const uint32_t g = base_t + B::kG + (KV ? w * B::kGrad : w * (PS / 2));
+        float acc[B::kWide ? 1 : kCols];
+        if constexpr (!B::kWide) {
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+        }
         auto add_sums = [&]() {
-            const uint32_t g = base_t + B::kG + (KV ? w * 2 * PS : w * (PS / 2));
-            add_columns<kOwn>(g + PS, acc);
-            add_columns<kOwn>(g, acc);
+            if constexpr (!B::kWide) {
+                add_columns<kCols>(g + PS, acc);
+                add_columns<kCols>(g, acc);
+            }
         };
         bool ok = true;
         for (int j = 0; j < n_tiles; ++j) {
             const int ax = j % B::kHalfRing;
-            const float* s_lse = reinterpret_cast<const float*>(smem + B::kAux + ax * B::kAuxBytes) + 32 * w;
+            const float* s_lse = reinterpret_cast<const float*>(smem + B::kAux + ax * B::kAuxBytes) + B::kHalf * w;
             const float* s_delta = s_lse + B::kWalk;
             uint32_t word = 0xffffffffu;
             if (KV || a.keep) {
@@ -526,23 +563,24 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                 if (!ok) break;
             }
             if (!KV)
-                word = a.keep ? reinterpret_cast<const uint32_t*>(smem + B::kAux + ax * B::kAuxBytes)[w]
-                              : tail_word(walk.hi - walk.lo - int64_t(j) * B::kWalk, w);
+                word = (a.keep ? reinterpret_cast<const uint32_t*>(smem + B::kAux + ax * B::kAuxBytes)[B::kWide ? 0 : w]
+                               : tail_word(walk.hi - walk.lo - int64_t(j) * B::kWalk, B::kWide ? 0 : w)) >>
+                       (B::kWide ? 16 * w : 0);
             ok = __all_sync(0xffffffffu, bar_wait(s_full, j & 1, dead, status));
             if (!ok) break;
             fence_after();
-            float v[32];
+            float v[B::kHalf];
             if (work) {
                 if (KV && w == 1 && j > 0) add_sums();  // dv of the step before is complete when S of this one is
-                tmem_ld32(base_t + 32 * w, v);
+                load_columns(base_t + B::kHalf * w, v);
                 tmem_wait_ld(v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
+                for (int i = 0; i < B::kHalf; ++i) {
                     v[i] = exp2_approx(fmaf(v[i], c, KV ? -s_lse[i] : -lse));
                     if (!KV && !((word >> i) & 1)) v[i] = 0.f;
                 }
                 if (KV) {
-                    store_planes(v, base_t + 32 * w, base_t + B::kP1 + 16 * w, base_t + B::kP2 + 16 * w);
+                    store_planes(v, base_t + B::kHalf * w, base_t + B::kP1 + B::kHalf / 2 * w, base_t + B::kP2 + B::kHalf / 2 * w);
                     tmem_wait_st();
                 }
             }
@@ -554,15 +592,16 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
             fence_after();
             if (work) {
                 if ((!KV || w == 0) && j > 0) add_sums();  // dk, dq of the step before: complete when dP of this one is
-                float y[32];
-                tmem_ld32(base_t + B::kDp + 32 * w, y);
+                float y[B::kHalf];
+                load_columns(base_t + B::kDp + B::kHalf * w, y);
                 tmem_wait_ld(y);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
+                for (int i = 0; i < B::kHalf; ++i) {
                     y[i] = v[i] * (y[i] - (KV ? s_delta[i] : delta));
                     if (!KV && !((word >> i) & 1)) y[i] = 0.f;
                 }
-                store_planes(y, base_t + B::kDp + 32 * w, base_t + B::kD1 + 16 * w, base_t + B::kD2 + 16 * w);
+                store_planes(y, base_t + B::kDp + B::kHalf * w, base_t + B::kD1 + B::kHalf / 2 * w,
+                             base_t + B::kD2 + B::kHalf / 2 * w);
                 tmem_wait_st();
             }
             fence_before();
@@ -574,16 +613,31 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
             fence_after();
         }
         if (ok && work) {
-            if (n_tiles > 0) add_sums();
-            if (row < own) {
-                const int64_t n = KV ? a.nk * a.Hkv : a.nq * a.Hq;
-                float* dst = static_cast<float*>(KV ? (w ? a.dv : a.dk) : a.dq) + rh * a.D;
-                if (a.splits > 1) dst = a.part_o + ((KV && w ? a.splits + split : split) * n + rh) * a.D;
+            const int64_t n = KV ? a.nk * a.Hkv : a.nq * a.Hq;
+            float* dst = static_cast<float*>(KV ? (w ? a.dv : a.dk) : a.dq) + rh * a.D;
+            if (a.splits > 1) dst = a.part_o + ((KV && w ? a.splits + split : split) * n + rh) * a.D;
+            const float scale = KV && w ? 1.f : a.scale;
+            const int c0 = KV ? 0 : w * (PS / 2);
+            if constexpr (B::kWide) {
+#pragma unroll 1
+                for (int b = 0; b < kCols / 16; ++b) {
+                    float o[16];
+                    __syncwarp();
+                    if (n_tiles > 0) {
+                        tmem_ld16(g + 16 * b, o);
+                        tmem_wait_ld(o);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = n_tiles > 0 && keep ? o[i] : 0.f;
+                    if (row < own) store_row<16>(dst, o, scale, c0 + 16 * b, a.D);
+                }
+            } else {
+                if (n_tiles > 0) add_sums();
                 if (!keep) {
 #pragma unroll
-                    for (int i = 0; i < kOwn; ++i) acc[i] = 0.f;
+                    for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
                 }
-                store_row<kOwn>(dst, acc, KV && w ? 1.f : a.scale, KV ? 0 : w * (PS / 2), a.D);
+                if (row < own) store_row<kCols>(dst, acc, scale, c0, a.D);
             }
         }
     } else if (warp == kPairWarps) {
@@ -599,19 +653,31 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                 return true;
             };
             auto product = [&](uint32_t d, uint32_t r, uint32_t xs, uint32_t bar) {
-                six_products<PS>(d, r, kPanelBytes, xs, B::kPanel, id_s);
+                six_products<PS>(d, r, B::kOwnPanel, xs, B::kPanel, id_s);
                 mma_commit(bar);
             };
-            // d = A X over the step's 64 rows, A in planes at a0 (its warpgroups' halves apart), a1, a2
-            auto sum = [&](uint32_t d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t xs) {
+            // d = A X over the step's rows, A in planes at a0 (its warpgroups' halves apart), a1, a2; at PS = 128 d += A X
+            auto sum = [&](uint32_t d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t xs, bool first) {
+                auto block = [&](int q, int s) { return q == 0 ? a0 + block_column(s, B::kHalf) : (q == 1 ? a1 : a2) + 8 * s; };
+                if constexpr (B::kWide) {
+                    constexpr int kPair[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
+                    bool add = !first;
 #pragma unroll
-                for (int s = 0; s < B::kWalk / 16; ++s) {
-                    const uint32_t hi = a0 + uint32_t((s >> 1) * 32 + (s & 1) * 8);
-                    mma_ts(d, hi, desc_rows(xs, s, B::kPanel), id2, s > 0);
-                    mma_ts(d + PS, hi, desc_rows(xs, s, B::kPanel, 2 * PS), id1, true);
-                    mma_ts(d + PS, a1 + 8 * s, desc_rows(xs, s, B::kPanel), id1, true);
-                    mma_ts(d + PS, a1 + 8 * s, desc_rows(xs, s, B::kPanel, PS), id1, true);
-                    mma_ts(d + PS, a2 + 8 * s, desc_rows(xs, s, B::kPanel), id1, true);
+                    for (int i = 0; i < 6; ++i)
+#pragma unroll
+                        for (int s = 0; s < B::kWalk / 16; ++s) {
+                            mma_ts(d, block(kPair[i][0], s), desc_rows(xs, s, B::kPanel, kPair[i][1] * PS), id1, add);
+                            add = true;
+                        }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < B::kWalk / 16; ++s) {
+                        mma_ts(d, block(0, s), desc_rows(xs, s, B::kPanel), id2, s > 0);
+                        mma_ts(d + PS, block(0, s), desc_rows(xs, s, B::kPanel, 2 * PS), id1, true);
+                        mma_ts(d + PS, block(1, s), desc_rows(xs, s, B::kPanel), id1, true);
+                        mma_ts(d + PS, block(1, s), desc_rows(xs, s, B::kPanel, PS), id1, true);
+                        mma_ts(d + PS, block(2, s), desc_rows(xs, s, B::kPanel), id1, true);
+                    }
                 }
             };
             bool ok = n_tiles > 0 && bar_wait(r_full, 0, dead, status) && wait_stage(0);
@@ -628,7 +694,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                 if (!ok) break;
                 fence_after();
                 if (KV) {
-                    sum(tmem + B::kG + 2 * PS, tmem, tmem + B::kP1, tmem + B::kP2, stage(2 * j + 1));
+                    sum(tmem + B::kG + B::kGrad, tmem, tmem + B::kP1, tmem + B::kP2, stage(2 * j + 1), j == 0);
                     mma_commit(empty + 8 * ((2 * j + 1) % B::kStages));
                 }
                 if (j + 1 < n_tiles) {
@@ -639,7 +705,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                 ok = bar_wait(ds_ready, j & 1, dead, status);
                 if (!ok) break;
                 fence_after();
-                sum(tmem + B::kG, tmem + B::kDp, tmem + B::kD1, tmem + B::kD2, stage(2 * j));
+                sum(tmem + B::kG, tmem + B::kDp, tmem + B::kD1, tmem + B::kD2, stage(2 * j), j == 0);
                 mma_commit(empty + 8 * ((2 * j) % B::kStages));
                 if (j + 1 < n_tiles) {
                     ok = wait_stage(2 * j + 3);
@@ -668,14 +734,14 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
             };
             auto stage = [&](int i) { return sb + uint32_t(B::kRing + (i % B::kStages) * B::kStep); };
             if (KV) {
-                StateMask<> mask(a.keep ? a.keep + k0 : nullptr, tl.row0, states);
+                StateMask<B::kOwn> mask(a.keep ? a.keep + k0 : nullptr, tl.row0, states);
                 mask.next();
                 auto use = [&](int r) { return mask.has(r); };
-                load_planes<PS, kRows, false>(sb, K, k_row, t, use);
-                load_planes<PS, kRows, false>(sb + uint32_t(B::kTile), V, k_row, t, use);
+                load_planes<PS, B::kOwn, false>(sb, K, k_row, t, use);
+                load_planes<PS, B::kOwn, false>(sb + uint32_t(B::kTile), V, k_row, t, use);
             } else {
-                load_planes_packed<PS, kRows>(sb, Q, q_row, kHead, a.group, tl.row0, own, t);
-                load_planes_packed<PS, kRows>(sb + uint32_t(B::kTile), dO, q_row, kHead, a.group, tl.row0, own, t);
+                load_planes_packed<PS, B::kOwn>(sb, Q, q_row, kHead, a.group, tl.row0, own, t);
+                load_planes_packed<PS, B::kOwn>(sb + uint32_t(B::kTile), dO, q_row, kHead, a.group, tl.row0, own, t);
             }
             copy_arrive(r_full);
             // lse and delta of the walked rows, fetched a step ahead
@@ -683,7 +749,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
             auto fetch = [&](int j) {
                 const int64_t r = walk.lo + int64_t(j) * B::kWalk + t;
                 v_lse = -INFINITY, v_delta = 0.f;
-                if (r < walk.hi) {
+                if (t < B::kWalk && r < walk.hi) {
                     const int64_t q = r / a.group, at = (q0 + q) * a.Hq + int64_t(h) * a.group + (r - q * a.group);
                     v_lse = a.lse[at];
                     v_delta = a.delta[at];
@@ -699,8 +765,10 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                 if (KV) {
                     float* s_lse = reinterpret_cast<float*>(smem + B::kAux + (j % B::kHalfRing) * B::kAuxBytes);
                     // rows past the end and rows without a kept state: P = exp2(s - inf) = 0
-                    s_lse[t] = v_lse == -INFINITY ? INFINITY : v_lse * kLog2e;
-                    s_lse[B::kWalk + t] = v_delta;
+                    if (t < B::kWalk) {
+                        s_lse[t] = v_lse == -INFINITY ? INFINITY : v_lse * kLog2e;
+                        s_lse[B::kWalk + t] = v_delta;
+                    }
                     bar_arrive(aux_full + 8 * (j % B::kHalfRing));
                     if (j + 1 < n_tiles) fetch(j + 1);
                     load_planes_packed<PS, B::kWalk>(stage(2 * j), Q, q_row, kHead, a.group, lo, n, t);
@@ -711,7 +779,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                 } else {
                     mask.next();
                     if (a.keep && t == 0) {
-                        *reinterpret_cast<uint2*>(smem + B::kAux + (j % B::kHalfRing) * B::kAuxBytes) = make_uint2(mask.word[0], mask.word[1]);
+                        *reinterpret_cast<uint2*>(smem + B::kAux + (j % B::kHalfRing) * B::kAuxBytes) = make_uint2(mask.word[0], mask.word[B::kWalk / 32 - 1]);
                         bar_arrive(aux_full + 8 * (j % B::kHalfRing));
                     }
                     auto use = [&](int r) { return mask.has(r); };
@@ -745,9 +813,10 @@ template <typename F>
 cudaError_t by_plane(int D, F f) {
     if (D <= 16) return f(std::integral_constant<int, 16>{});
     if (D <= 32) return f(std::integral_constant<int, 32>{});
-    return f(std::integral_constant<int, 64>{});
+    if (D <= 64) return f(std::integral_constant<int, 64>{});
+    return f(std::integral_constant<int, 128>{});
 }
-int plane_stride(int D) { return D <= 16 ? 16 : D <= 32 ? 32 : 64; }
+int plane_stride(int D) { return D <= 16 ? 16 : D <= 32 ? 32 : D <= 64 ? 64 : 128; }
 
 // The planes' places in the workspace, in the order q, k, v, d_out.
 Planes planes_at(const AttnArgs& a, void* ws) {
