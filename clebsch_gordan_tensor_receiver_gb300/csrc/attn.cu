@@ -25,50 +25,79 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Joins the splits of a row: o = sum_s exp(lse_s - lse) o_s.  One warp per (row, head).
+// Joins the splits of a row: o = sum_s exp(lse_s - lse) o_s.  One warp per (row, head); lane s holds the
+// weights of splits s and s + 32 (kMaxSplits = 64), the columns go by fours where D allows.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) attn_fwd_join(AttnArgs a) {
     const int64_t rh = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     const int64_t total = a.nq * a.Hq;
     if (rh >= total) return;
-    float top = -INFINITY;
-    for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_lse[s * total + rh]);
+    float x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i] = lane + 32 * i < a.splits ? a.part_lse[(lane + 32 * i) * total + rh] : -INFINITY;
+    float top = fmaxf(x[0], x[1]);
 #pragma unroll
     for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-    float sum = 0.f;
-    for (int s = lane; s < a.splits; s += 32) {
-        const float x = a.part_lse[s * total + rh];
-        sum += x == -INFINITY ? 0.f : expf(x - top);
+    float w[2], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        w[i] = x[i] == -INFINITY ? 0.f : expf(x[i] - top);
+        sum += w[i];
     }
 #pragma unroll
     for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    const float lse = sum == 0.f ? -INFINITY : top + logf(sum);
-    if (lane == 0) a.lse[rh] = lse;
+    if (lane == 0) a.lse[rh] = sum == 0.f ? -INFINITY : top + logf(sum);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     T* po = static_cast<T*>(a.out) + (rh / a.Hq) * a.o_row + (rh % a.Hq) * a.o_head;
-    for (int d = lane; d < a.D; d += 32) {
-        float o = 0.f;
+    const float* part = a.part_o + rh * a.D;
+    const int64_t stride = total * a.D;
+    auto weight = [&](int s) { return __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31); };
+    if (a.D % 4 == 0) {
+        const int d = 4 * lane;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
         for (int s = 0; s < a.splits; ++s) {
-            const float x = a.part_lse[s * total + rh];
-            if (x != -INFINITY) o = fmaf(expf(x - lse), a.part_o[(s * total + rh) * a.D + d], o);
+            const float ws = weight(s);
+            if (d < a.D && ws != 0.f) {  // a piece without a kept state wrote zeros
+                const float4 v = *reinterpret_cast<const float4*>(part + s * stride + d);
+                o.x = fmaf(ws, v.x, o.x), o.y = fmaf(ws, v.y, o.y), o.z = fmaf(ws, v.z, o.z), o.w = fmaf(ws, v.w, o.w);
+            }
         }
-        po[d] = narrow<T>(o);
+        if (d < a.D) {
+            po[d] = narrow<T>(o.x * inv), po[d + 1] = narrow<T>(o.y * inv);
+            po[d + 2] = narrow<T>(o.z * inv), po[d + 3] = narrow<T>(o.w * inv);
+        }
+    } else {
+        for (int d0 = 0; d0 < a.D; d0 += 32) {
+            float o = 0.f;
+            for (int s = 0; s < a.splits; ++s) {
+                const float ws = weight(s);
+                if (d0 + lane < a.D && ws != 0.f) o = fmaf(ws, part[s * stride + d0 + lane], o);
+            }
+            if (d0 + lane < a.D) po[d0 + lane] = narrow<T>(o * inv);
+        }
     }
 }
 
-// delta[row][head] = sum_d d_out out.  One warp per (row, head).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) attn_delta(AttnArgs a) {
-    const int64_t rh = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31;
-    if (rh >= a.nq * a.Hq) return;
-    const int64_t at = (rh / a.Hq) * a.o_row + (rh % a.Hq) * a.o_head;
+// delta[row][head] = sum_d d_out out.  2^log2 lanes per (row, head), V columns at a time each.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) attn_delta(AttnArgs a, int log2) {
+    const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x, rh = i >> log2;
+    const int lanes = 1 << log2, l = int(i) & (lanes - 1);
     float s = 0.f;
-    for (int d = lane; d < a.D; d += 32)
-        s = fmaf(widen(static_cast<const T*>(a.d_out)[at + d]), widen(static_cast<const T*>(a.out)[at + d]), s);
+    if (rh < a.nq * a.Hq) {
+        const int64_t row = uint64_t(rh) < (1ull << 32) ? int64_t(uint32_t(rh) / uint32_t(a.Hq)) : rh / a.Hq;
+        const int64_t at = row * a.o_row + (rh - row * a.Hq) * a.o_head;
+        for (int d = l * V; d < a.D; d += lanes * V) {
+            const Vec<T, V> x = load_vec<T, V>(static_cast<const T*>(a.d_out) + at + d),
+                            y = load_vec<T, V>(static_cast<const T*>(a.out) + at + d);
 #pragma unroll
-    for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    if (lane == 0) a.delta[rh] = s;
+            for (int k = 0; k < V; ++k) s = fmaf(widen(x.v[k]), widen(y.v[k]), s);
+        }
+    }
+    for (int k = lanes >> 1; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if (l == 0 && rh < a.nq * a.Hq) a.delta[rh] = s;
 }
 
 // dst[i] = sum_s part[s][i], in the order of the splits.
@@ -81,12 +110,16 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_join(int64_t n, int splits,
     dst[i] = narrow<T>(s);
 }
 
-// Splits of the inner axis: as many as fill the card's SMs once, when there are fewer tiles than
-// SMs, but no piece shorter than four tiles.
-int splits_for(int64_t tiles, int64_t inner, int R, int sms) {
+constexpr int kMaxSplits = 64;  // two weights per lane of the join
+
+// Splits of the inner axis.  Few tiles: as many pieces as fill the card's SMs once, but none shorter than
+// four tiles.  `deep` (the forward, whose pieces cost little to join): four times as many where pieces of eight tiles
+// are left, so that graphs of different lengths even out.
+int splits_for(int64_t tiles, int64_t inner, int R, int sms, bool deep) {
     if (tiles <= 0 || tiles >= sms) return 1;
-    const int64_t want = (sms + tiles - 1) / tiles, most = std::max<int64_t>(1, inner / (4 * R));
-    return int(std::min<int64_t>(std::min(want, most), 64));
+    const int64_t once = std::min((sms + tiles - 1) / tiles, std::max<int64_t>(1, inner / (4 * R)));
+    const int64_t four = deep ? std::min((4 * sms + tiles - 1) / tiles, std::max<int64_t>(1, inner / (8 * R))) : 1;
+    return int(std::min<int64_t>(std::max(once, four), kMaxSplits));
 }
 
 int64_t row_tiles(const AttnShape& s, int R) { return s.n_q * (s.q_heads / s.kv_heads) / R + s.n_graphs; }
@@ -113,9 +146,9 @@ Choice choose(const AttnShape& s, int sms) {
     c.R = c.planes ? plane_bwd_tile(s.head_dim) : 128;
     c.nt = !c.planes && rows_busy(256) >= sms && s.max_q * group > 128 ? 2 : 1;
     c.fwd_tiles = row_tiles(s, 128 * c.nt);
-    c.fwd = splits_for(rows_busy(128 * c.nt), s.max_k, 128, sms);
-    c.dq = splits_for(rows_busy(c.R), s.max_k, 128, sms);
-    c.dkv = splits_for(states_busy(c.R), s.max_q * group, 128, sms);
+    c.fwd = splits_for(rows_busy(128 * c.nt), s.max_k, 128, sms, true);
+    c.dq = splits_for(rows_busy(c.R), s.max_k, 128, sms, false);
+    c.dkv = splits_for(states_busy(c.R), s.max_q * group, 128, sms, false);
     if (c.planes && s.head_dim > 64) {  // sums in tensor memory: short walks
         const auto pieces = [](int64_t n) { return int((n + kPlaneWalk - 1) / kPlaneWalk); };
         c.dq = std::max(c.dq, pieces(s.max_k));
@@ -217,7 +250,17 @@ cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, 
     };
     cudaError_t e = cudaSuccess;
     if (a.nq > 0)
-        e = with_type([&](auto t) { attn_delta<decltype(t)><<<unsigned((a.nq * a.Hq + 7) / 8), kThreads, 0, st>>>(a); });
+        e = with_type([&](auto t) {
+            using T = decltype(t);
+            constexpr int V = 16 / int(sizeof(T));
+            const uintptr_t any = reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.d_out) |
+                                  uintptr_t(a.o_row | a.o_head) * sizeof(T);
+            const bool vec = a.D % V == 0 && (any & 15u) == 0;
+            int log2 = 0;
+            while (log2 < 5 && (1 << log2) * (vec ? V : 1) < a.D) ++log2;
+            const unsigned n = blocks((a.nq * a.Hq) << log2);
+            vec ? attn_delta<T, V><<<n, kThreads, 0, st>>>(a, log2) : attn_delta<T, 1><<<n, kThreads, 0, st>>>(a, log2);
+        });
     if (e == cudaSuccess && c.planes) e = launch_attn_planes(a, planes, sms, st);
     if (e == cudaSuccess && a.dq && a.nq > 0) e = half(false);
     if (e == cudaSuccess && a.dk && a.nk > 0) e = half(true);

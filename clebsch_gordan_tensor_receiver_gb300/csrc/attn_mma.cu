@@ -27,15 +27,16 @@ constexpr int kMaskRing = 8;  // state masks in flight: more than half the stage
 template <int NT>
 struct FwdLayout {
     int panels, stages;
+    int masks_held;  // biases of state tiles in flight: kMaskRing, or 1 without a mask (the last tile's)
     __host__ __device__ int tile() const { return panels * kPanelBytes; }
     __host__ __device__ int ring() const { return NT * tile(); }
     __host__ __device__ int masks() const { return ring() + stages * tile(); }
-    __host__ __device__ int bars() const { return masks() + kMaskRing * 16; }
+    __host__ __device__ int bars() const { return masks() + masks_held * kRows * 4; }
     __host__ __device__ int total() const { return bars() + 256 + 1024; }  // + alignment slack
 };
 
 template <typename T, int NT, int LG, bool ALIGNED>
-__global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 1) attn_fwd_mma(AttnArgs a, FwdLayout<NT> L) {
+__global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG < 4 ? 2 : 1) attn_fwd_mma(AttnArgs a, FwdLayout<NT> L) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_dead;
     __shared__ uint32_t s_tmem;
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 
             bar_init(full + 8 * s, kLoadWarps * 32);
             bar_init(empty + 8 * s, 1);
         }
-        for (int s = 0; s < kMaskRing; ++s) bar_init(m_full + 8 * s, 1);
+        for (int s = 0; s < kMaskRing; ++s) bar_init(m_full + 8 * s, kLoadThreads);
         bar_init(fin, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -78,7 +79,11 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
     volatile int* dead = &s_dead;
     unsigned* status = &attn_status_word;
-    const uint32_t* masks = reinterpret_cast<const uint32_t*>(smem + L.masks());
+    float* biases = reinterpret_cast<float*>(smem + L.masks());
+    // the bias of tile j: every tile's with a mask, else the last one's where it is not full
+    const bool tail = (kr.hi - kr.lo) % kRows != 0;
+    auto masked = [&](int j) { return a.keep || (tail && j == n_tiles - 1); };
+    auto slot = [&](int j) { return a.keep ? j % kMaskRing : 0; };
 
     if (warp < 4 * NT) {
         // ------------------------------------------------------------------------ softmax
@@ -91,36 +96,40 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 
         float m = -INFINITY, l = 0.f;  // reference maximum in units of c S, and the sum of P
         bool ok = true;
         if (t < nt) {
+            // a block with all of an SM's registers holds its row of S; the others read it twice
+            constexpr bool kHold = NT == 2 || LG == 4;
             for (int j = 0; j < n_tiles; ++j) {
-                uint32_t word[4];
-                if (a.keep) {
-                    ok = __all_sync(0xffffffffu, bar_wait(m_full + 8 * (j % kMaskRing), (j / kMaskRing) & 1, dead, status));
+                const bool biased = masked(j);
+                const float* bias = biases + slot(j) * kRows;
+                if (biased) {
+                    ok = __all_sync(0xffffffffu, bar_wait(m_full + 8 * slot(j), a.keep ? (j / kMaskRing) & 1 : 0, dead, status));
                     if (!ok) break;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) word[w] = masks[(j % kMaskRing) * 4 + w];
-                } else {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) word[w] = tail_word(kr.hi - kr.lo - int64_t(j) * kRows, w);
                 }
                 ok = __all_sync(0xffffffffu, bar_wait(s_full + 8 * t, j & 1, dead, status));
                 if (!ok) break;
                 fence_after();
                 if (work) {
-                    float x[2][32];
+                    float x[kHold ? 4 : 2][32];
                     float top = -INFINITY;
-                    tmem_ld32(s_at, x[0]);
+                    if constexpr (kHold) {
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        float(&v)[32] = x[b & 1];
-                        tmem_wait_ld(v);
-                        tmem_ld32(s_at + 32 * ((b + 1) & 3), x[(b + 1) & 1]);
-                        if (word[b] == 0xffffffffu) {
+                        for (int b = 0; b < 4; ++b) tmem_ld32(s_at + 32 * b, x[b]);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
-                        } else {
+                        for (int b = 0; b < 4; ++b) {
+                            tmem_wait_ld(x[b]);
+                            if (biased) add_bias(x[b], bias + 32 * b);
+                        }
+                        const float t0 = fmaxf(row_max(x[0]), row_max(x[1])), t1 = fmaxf(row_max(x[2]), row_max(x[3]));
+                        top = fmaxf(t0, t1);
+                    } else {
+                        tmem_ld32(s_at, x[0]);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if ((word[b] >> i) & 1) top = fmaxf(top, v[i]);
+                        for (int b = 0; b < 4; ++b) {
+                            float(&v)[32] = x[b & 1];
+                            tmem_wait_ld(v);
+                            tmem_ld32(s_at + 32 * ((b + 1) & 3), x[(b + 1) & 1]);
+                            if (biased) add_bias(v, bias + 32 * b);
+                            top = fmaxf(top, row_max(v));
                         }
                     }
                     top *= c;
@@ -142,27 +151,24 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 
                         m = to;
                     }
                     const float base = m == -INFINITY ? 0.f : m;
+                    const F2 c2(c, c), minus(-base, -base);
+                    F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
-                        float(&v)[32] = x[b & 1];
-                        tmem_wait_ld(v);
-                        if (b < 3) tmem_ld32(s_at + 32 * (b + 1), x[(b + 1) & 1]);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = exp2_approx(fmaf(v[i], c, -base));
-                        if (word[b] != 0xffffffffu) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!((word[b] >> i) & 1)) v[i] = 0.f;
+                        float(&v)[32] = x[kHold ? b : b & 1];
+                        if constexpr (!kHold) {
+                            tmem_wait_ld(v);
+                            if (b < 3) tmem_ld32(s_at + 32 * (b + 1), x[(b + 1) & 1]);
+                            if (biased) add_bias(v, bias + 32 * b);
                         }
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) sum[i & 3] += v[i];
-                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        exp_row(v, c2, minus, sum);
                         uint32_t p[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) p[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
                         tmem_st16(s_at + 16 * b, p);
                     }
+                    const float2 s2 = (sum[0] + sum[1]).both();
+                    l += s2.x + s2.y;
                     tmem_wait_st();
                 }
                 fence_before();
@@ -270,7 +276,8 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 
         __syncwarp();
     } else {
         // ------------------------------------------------------------------------- loaders
-        const LoadMap<LG> map(threadIdx.x - (4 * NT + 1) * 32, a.D);
+        const int map_t = threadIdx.x - (4 * NT + 1) * 32;
+        const LoadMap<LG> map(map_t, a.D);
         if (n_tiles > 0) {
             // every loader thread arrives: when its copies have landed, or at once after its own stores
             auto arrive = [&](uint32_t bar) { ALIGNED ? copy_arrive(bar) : bar_arrive(bar); };
@@ -298,12 +305,11 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 ? 2 : 
             for (int j = 0; j < n_tiles; ++j) {
                 mask.next();
                 if (!load(2 * j, K, a.k_row * 2)) break;
-                // the softmax warps read the tile's mask before its V stage is released, and K's stage comes half a ring
-                // later: kMaskRing masks cannot be overtaken
-                if (a.keep && warp == 4 * NT + 1 && lane == 0) {
-                    *reinterpret_cast<uint4*>(smem + L.masks() + (j % kMaskRing) * 16) =
-                        make_uint4(mask.word[0], mask.word[1], mask.word[2], mask.word[3]);
-                    bar_arrive(m_full + 8 * (j % kMaskRing));
+                // the softmax warps read the tile's bias before its V stage is released, and K's stage comes half a ring
+                // later: kMaskRing biases cannot be overtaken
+                if (masked(j)) {
+                    write_bias(biases + slot(j) * kRows, mask, map_t);
+                    bar_arrive(m_full + 8 * slot(j));
                 }
                 if (!load(2 * j + 1, V, a.v_row * 2)) break;
                 K += kRows * a.k_row * 2;
@@ -324,8 +330,10 @@ template <typename T, int NT>
 cudaError_t fwd(const AttnArgs& a, int64_t row_tiles, cudaStream_t st) {
     FwdLayout<NT> L;
     L.panels = a.D > 64 ? 2 : 1;
-    // one panel: 96 KB, two CTAs per SM (NT = 1), or 160 KB; two panels: 224 KB
-    L.stages = NT == 1 ? (L.panels == 1 ? 5 : 6) : (L.panels == 1 ? 8 : 5);
+    // one panel: 96 KB, two CTAs per SM (NT = 1), or 160 KB; two panels: 224 KB, less
+    // a stage where the masks need the room
+    L.masks_held = a.keep ? kMaskRing : 1;
+    L.stages = NT == 1 ? (L.panels == 1 || a.keep ? 5 : 6) : (L.panels == 1 ? 8 : a.keep ? 4 : 5);
     const uintptr_t any = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
                           uintptr_t(a.q_row | a.q_head | a.k_row | a.k_head | a.v_row | a.v_head) * 2;
     return by_chunks(a.D, (any & 15u) == 0, [&](auto lg, auto aligned) {

@@ -158,6 +158,71 @@ struct StateMask {
     }
 };
 
+// Writes 0 or -inf per state of the tile to `bias` (shared memory), by all loader threads.
+template <int N>
+__device__ __forceinline__ void write_bias(float* bias, const StateMask<N>& m, int t) {
+#pragma unroll
+    for (int i = 0; i < (N + kLoadThreads - 1) / kLoadThreads; ++i) {
+        const int r = t + i * kLoadThreads;
+        if (r < N) bias[r] = m.has(r) ? 0.f : -INFINITY;
+    }
+}
+// N columns plus a tile's bias from shared memory (16-byte aligned): masked columns become -inf.
+template <int N>
+__device__ __forceinline__ void add_bias(float (&v)[N], const float* bias) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        const ulonglong2 q = reinterpret_cast<const ulonglong2*>(bias)[i];
+        F2 b0, b1;
+        b0.v = q.x, b1.v = q.y;
+        const float2 x = (F2(v[4 * i], v[4 * i + 1]) + b0).both(), y = (F2(v[4 * i + 2], v[4 * i + 3]) + b1).both();
+        v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = y.x, v[4 * i + 3] = y.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ float row_max(const float (&v)[N]) {
+    float a = max3(v[0], v[1], v[2]), b = max3(v[3], v[4], v[5]);
+#pragma unroll
+    for (int i = 6; i + 1 < N; i += 4) {
+        a = max3(a, v[i], v[i + 1]);
+        if (i + 3 < N) b = max3(b, v[i + 2], v[i + 3]);
+    }
+    return fmaxf(a, b);
+}
+// v = exp2(c v - base), and the values' sum by pairs.
+template <int N>
+__device__ __forceinline__ void exp_row(float (&v)[N], F2 c, F2 minus, F2 (&sum)[2]) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float2 e = fma2(F2(v[2 * i], v[2 * i + 1]), c, minus).both();
+        v[2 * i] = exp2_approx(e.x), v[2 * i + 1] = exp2_approx(e.y);
+        sum[i & 1] = sum[i & 1] + F2(v[2 * i], v[2 * i + 1]);
+    }
+}
+
+// The two steps of the backward on N columns of a row.  p = exp2(c s + e), then p (dp u - delta); e and delta are the
+// row's, or per column (shared memory, 16-byte aligned; PER).
+template <bool PER, int N>
+__device__ __forceinline__ void bwd_p(float (&s)[N], F2 c, float e, const float* es) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        F2 add(e, e);
+        if constexpr (PER) add.v = reinterpret_cast<const uint64_t*>(es)[i];
+        const float2 x = fma2(F2(s[2 * i], s[2 * i + 1]), c, add).both();
+        s[2 * i] = exp2_approx(x.x), s[2 * i + 1] = exp2_approx(x.y);
+    }
+}
+template <bool PER, int N>
+__device__ __forceinline__ void bwd_ds(float (&dp)[N], const float (&p)[N], F2 u, float minus_delta, const float* minus_deltas) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        F2 add(minus_delta, minus_delta);
+        if constexpr (PER) add.v = reinterpret_cast<const uint64_t*>(minus_deltas)[i];
+        const float2 x = (F2(p[2 * i], p[2 * i + 1]) * fma2(F2(dp[2 * i], dp[2 * i + 1]), u, add)).both();
+        dp[2 * i] = x.x, dp[2 * i + 1] = x.y;
+    }
+}
+
 struct Piece {
     int64_t lo, hi;
 };

@@ -28,8 +28,8 @@ struct BwdLayout {
     int panels, stages;
     __host__ __device__ int tile() const { return panels * kPanelBytes; }
     __host__ __device__ int ring() const { return 2 * tile(); }
-    __host__ __device__ int aux() const { return ring() + stages * tile(); }  // per walked tile: lse and delta, or the mask
-    __host__ __device__ int aux_bytes() const { return KV ? 2 * kRows * 4 : 16; }
+    __host__ __device__ int aux() const { return ring() + stages * tile(); }  // per walked tile: -lse and -delta, or the states' bias
+    __host__ __device__ int aux_bytes() const { return (KV ? 2 : 1) * kRows * 4; }
     __host__ __device__ int bars() const { return aux() + stages / 2 * aux_bytes(); }
     __host__ __device__ int total() const { return bars() + 256 + 1024; }  // + alignment slack
 };
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(AttnArgs a, Bw
             bar_init(full + 8 * s, kLoadThreads);
             bar_init(empty + 8 * s, 1);
         }
-        for (int s = 0; s < half; ++s) bar_init(aux_full + 8 * s, KV ? kLoadThreads : 1);
+        for (int s = 0; s < half; ++s) bar_init(aux_full + 8 * s, kLoadThreads);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 8) tmem_alloc(smem_u32(&s_tmem), tmem_cols);
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(AttnArgs a, Bw
         const uint32_t lanes = uint32_t(quad * 32) << 16, col = uint32_t(64 * w);
         const float c = a.scale_log2;
         const int64_t p = tl.row0 + row;
-        float lse = INFINITY, delta = 0.f;  // of the thread's row (dq)
+        float lse = -INFINITY, delta = 0.f;  // minus the thread's row's (dq)
         int64_t rh = 0;
         bool keep = row < own;
         if (keep) {
@@ -131,30 +131,20 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(AttnArgs a, Bw
                 rh = (q0 + p / a.group) * a.Hq + int64_t(h) * a.group + p % a.group;
                 const float x = a.lse[rh];
                 // a row without a kept state: P = exp2(s - inf) = 0
-                lse = x == -INFINITY ? INFINITY : x * kLog2e - kShift;
-                delta = a.delta[rh] * kUnshift;
+                lse = x == -INFINITY ? -INFINITY : kShift - x * kLog2e;
+                delta = -a.delta[rh] * kUnshift;
             }
         }
+        const bool tail = (walk.hi - walk.lo) % kRows != 0;
         bool ok = true;
         for (int j = 0; j < n_tiles; ++j) {
             const int ax = j % half;
-            const float* s_lse = reinterpret_cast<const float*>(smem + L.aux() + ax * L.aux_bytes()) + col;
+            const float* s_lse = reinterpret_cast<const float*>(smem + L.aux() + ax * L.aux_bytes()) + col;  // or the bias
             const float* s_delta = s_lse + kRows;
-            uint32_t word[2] = {0xffffffffu, 0xffffffffu};
-            if (KV || a.keep) {
-                ok = __all_sync(0xffffffffu, bar_wait(aux_full + 8 * ax, (j / half) & 1, dead, status));
+            const bool biased = !KV && (a.keep || (tail && j == n_tiles - 1));
+            if (KV || biased) {
+                ok = __all_sync(0xffffffffu, bar_wait(aux_full + 8 * ax, a.keep || KV ? (j / half) & 1 : 0, dead, status));
                 if (!ok) break;
-            }
-            if (!KV) {
-                if (a.keep) {
-                    const uint32_t* mw = reinterpret_cast<const uint32_t*>(smem + L.aux() + ax * L.aux_bytes()) + 2 * w;
-                    word[0] = mw[0];
-                    word[1] = mw[1];
-                } else {
-                    const int64_t left = walk.hi - walk.lo - int64_t(j) * kRows;
-                    word[0] = tail_word(left, 2 * w);
-                    word[1] = tail_word(left, 2 * w + 1);
-                }
             }
             ok = __all_sync(0xffffffffu, bar_wait(s_full, j & 1, dead, status));
             if (!ok) break;
@@ -166,13 +156,8 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(AttnArgs a, Bw
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     tmem_wait_ld(x[b]);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[b][i] = exp2_approx(fmaf(x[b][i], c, KV ? -s_lse[32 * b + i] : -lse));
-                    if (!KV && word[b] != 0xffffffffu) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((word[b] >> i) & 1)) x[b][i] = 0.f;
-                    }
+                    if (biased) add_bias(x[b], s_lse + 32 * b);
+                    bwd_p<KV>(x[b], F2(c, c), lse, s_lse + 32 * b);
                     if (KV) {
                         uint32_t q[16];
 #pragma unroll
@@ -194,14 +179,8 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(AttnArgs a, Bw
                     float y[32];
                     tmem_ld32(t_dp + lanes + col + 32 * b, y);
                     tmem_wait_ld(y);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) y[i] = x[b][i] * fmaf(y[i], kUnshift, KV ? -s_delta[32 * b + i] : -delta);
+                    bwd_ds<KV>(y, x[b], F2(kUnshift, kUnshift), delta, s_delta + 32 * b);
                     uint32_t q[16];
-                    if (!KV && word[b] != 0xffffffffu) {  // 0 * (NaN - delta) is not 0
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((word[b] >> i) & 1)) y[i] = 0.f;
-                    }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) q[i] = pack2<T>(y[2 * i], y[2 * i + 1]);
                     tmem_st16(t_dp + lanes + col + 16 * b, q);
@@ -357,8 +336,8 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(AttnArgs a, Bw
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         // rows past the end and rows without a kept state: P = exp2(s - inf) = 0
-                        s_lse[t + 64 * i] = v_lse[i] == -INFINITY ? INFINITY : v_lse[i] * kLog2e - kShift;
-                        s_lse[kRows + t + 64 * i] = v_delta[i] * kUnshift;
+                        s_lse[t + 64 * i] = v_lse[i] == -INFINITY ? -INFINITY : kShift - v_lse[i] * kLog2e;
+                        s_lse[kRows + t + 64 * i] = -v_delta[i] * kUnshift;
                     }
                     bar_arrive(aux_full + 8 * (j % half));
                     if (j + 1 < n_tiles) fetch(j + 1);
@@ -369,9 +348,8 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(AttnArgs a, Bw
                     arrive(full + 8 * ((2 * j + 1) % L.stages));
                 } else {
                     mask.next();
-                    if (a.keep && t == 0) {
-                        *reinterpret_cast<uint4*>(smem + L.aux() + (j % half) * L.aux_bytes()) =
-                            make_uint4(mask.word[0], mask.word[1], mask.word[2], mask.word[3]);
+                    if (a.keep || n < kRows) {
+                        write_bias(reinterpret_cast<float*>(smem + L.aux() + (j % half) * L.aux_bytes()), mask, t);
                         bar_arrive(aux_full + 8 * (j % half));
                     }
                     states_tile(stage(2 * j), K, a.k_row * 2);

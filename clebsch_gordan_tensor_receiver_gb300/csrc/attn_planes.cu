@@ -48,40 +48,49 @@ __device__ __forceinline__ void cut2(float x, float y, uint32_t (&p)[3]) {
     p[2] = __byte_perm(__float_as_uint(x1 - __uint_as_float(c & 0xffff0000u)), __float_as_uint(y1 - __uint_as_float(d & 0xffff0000u)), 0x7632);
 }
 
-// One thread per 8 columns of a (row, head).
+// 32 threads on the 8-column chunks of a row's heads, 8 rows a block.
 template <int PS>
 __global__ void __launch_bounds__(256) attn_planes(PlaneJobs jobs) {
+    constexpr int kChunks = PS / 8;
     const PlaneJob& j = jobs.j[blockIdx.y];
-    const int64_t total = j.rows * j.heads * (PS / 8);
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-        const int c = int(i % (PS / 8)) * 8;
-        const int64_t rh = i / (PS / 8), r = rh / j.heads;
-        const float* x = j.x + r * j.row + (rh - r * j.heads) * j.head + c;
-        float v[8];
+    const bool vec = jobs.D % 4 == 0 && j.row % 4 == 0 && j.head % 4 == 0 && (reinterpret_cast<uintptr_t>(j.x) & 15u) == 0;
+    for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < j.rows; r += int64_t(gridDim.x) * 8)
+        for (int e = threadIdx.x & 31; e < j.heads * kChunks; e += 32) {
+            const int h = e / kChunks, c = e % kChunks * 8;
+            const float* x = j.x + r * j.row + h * j.head + c;
+            float v[8];
+            if (vec) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = c + k < jobs.D ? x[k] : 0.f;
-        uint32_t w[3][4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t p[3];
-            cut2(v[2 * k], v[2 * k + 1], p);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float z = v[2 * k + e];
-                if (!isfinite(z)) {  // whole in the leading plane (a NaN's upper bits alone could read as infinity)
-                    const uint32_t half = isnan(z) ? 0x7fffu : __float_as_uint(z) >> 16, keep = e ? 0x0000ffffu : 0xffff0000u;
-                    p[0] = (p[0] & keep) | (half << (16 * e));
-                    p[1] &= keep;
-                    p[2] &= keep;
+                for (int k = 0; k < 8; k += 4) {
+                    const float4 q = c + k < jobs.D ? *reinterpret_cast<const float4*>(x + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v[k] = q.x, v[k + 1] = q.y, v[k + 2] = q.z, v[k + 3] = q.w;
                 }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = c + k < jobs.D ? x[k] : 0.f;
             }
+            uint32_t w[3][4];
 #pragma unroll
-            for (int q = 0; q < 3; ++q) w[q][k] = p[q];
+            for (int k = 0; k < 4; ++k) {
+                uint32_t p[3];
+                cut2(v[2 * k], v[2 * k + 1], p);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float z = v[2 * k + i];
+                    if (!isfinite(z)) {  // whole in the leading plane (a NaN's upper bits alone could read as infinity)
+                        const uint32_t half = isnan(z) ? 0x7fffu : __float_as_uint(z) >> 16, keep = i ? 0x0000ffffu : 0xffff0000u;
+                        p[0] = (p[0] & keep) | (half << (16 * i));
+                        p[1] &= keep;
+                        p[2] &= keep;
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < 3; ++q) w[q][k] = p[q];
+            }
+            uint16_t* o = j.out + (r * j.heads + h) * (3 * PS) + c;
+#pragma unroll
+            for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(o + q * PS) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
         }
-        uint16_t* o = j.out + rh * (3 * PS) + c;
-#pragma unroll
-        for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(o + q * PS) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
-    }
 }
 
 // An operand's planes in the workspace.
@@ -199,7 +208,7 @@ struct FwdPlan {
     static constexpr int kState = PS == 128 ? 64 : 128, kHalfState = kState / 2, kPanel = kState * 128;
     static constexpr int kTile = kPanels<PS> * kPanelBytes, kStep = kPanels<PS> * kPanel;
     static constexpr int kStages = PS == 128 ? 2 : PS == 64 ? 3 : PS == 32 ? 5 : 8;
-    static constexpr int kRing = kTile, kMasks = kRing + kStages * kStep, kMax = kMasks + 8 * 16, kBars = kMax + 2 * 2 * kRows * 4;
+    static constexpr int kRing = kTile, kMasks = kRing + kStages * kStep, kMax = kMasks + 8 * kState * 4, kBars = kMax + 2 * 2 * kRows * 4;
     static constexpr int kTotal = kBars + 512 + 1024;  // barriers, alignment slack
     // tensor memory: S (plane 0 of P written over it), planes 1 and 2 of P, O by order
     static constexpr uint32_t kMid = kState, kLo = kState + kState / 2, kO = 2 * kState;
@@ -236,7 +245,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
             bar_init(full + 8 * s, kLoadThreads);
             bar_init(empty + 8 * s, 1);
         }
-        for (int s = 0; s < kRing; ++s) bar_init(m_full + 8 * s, 1);
+        for (int s = 0; s < kRing; ++s) bar_init(m_full + 8 * s, kLoadThreads);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kPairWarps) tmem_alloc(smem_u32(&s_tmem), 512);
@@ -246,6 +255,11 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
     volatile int* dead = &s_dead;
     unsigned* status = &attn_status_word;
+    float* biases = reinterpret_cast<float*>(smem + F::kMasks);
+    // the bias of tile j: every tile's with a mask, else the last one's where it is not full
+    const bool tail = (kr.hi - kr.lo) % F::kState != 0;
+    auto masked = [&](int j) { return a.keep || (tail && j == n_tiles - 1); };
+    auto slot = [&](int j) { return a.keep ? j % kRing : 0; };
 
     if (warp < kPairWarps) {
         // ------------------------------------------------------------------------ softmax
@@ -254,7 +268,6 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
         const uint32_t lanes = uint32_t(quad * 32) << 16, base_t = tmem + lanes;
         const float c = a.scale_log2;
         float* s_max = reinterpret_cast<float*>(smem + F::kMax);  // [turn][warpgroup][row]
-        const uint32_t* masks = reinterpret_cast<const uint32_t*>(smem + F::kMasks) + kBlocks * w;
         float m = -INFINITY, l = 0.f, acc[kHalf];
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
@@ -278,16 +291,11 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
             add_columns<kHalf>(base_t + F::kO + w * kHalf, acc);
         };
         for (int j = 0; j < n_tiles; ++j) {
-            uint32_t word[kBlocks];
-            if (a.keep) {
-                ok = __all_sync(0xffffffffu, bar_wait(m_full + 8 * (j % kRing), (j / kRing) & 1, dead, status));
+            const bool biased = masked(j);
+            const float* bias = biases + slot(j) * F::kState + F::kHalfState * w;
+            if (biased) {
+                ok = __all_sync(0xffffffffu, bar_wait(m_full + 8 * slot(j), a.keep ? (j / kRing) & 1 : 0, dead, status));
                 if (!ok) break;
-#pragma unroll
-                for (int b = 0; b < kBlocks; ++b) word[b] = masks[(j % kRing) * 4 + b];
-            } else {
-                const int64_t left = kr.hi - kr.lo - int64_t(j) * F::kState;
-#pragma unroll
-                for (int b = 0; b < kBlocks; ++b) word[b] = tail_word(left, kBlocks * w + b);
             }
             ok = __all_sync(0xffffffffu, bar_wait(s_full, j & 1, dead, status));
             if (!ok) break;
@@ -301,9 +309,8 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
                     tmem_wait_ld(v[b]);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if ((word[b] >> i) & 1) top = fmaxf(top, v[b][i]);
+                    if (biased) add_bias(v[b], bias + 32 * b);
+                    top = fmaxf(top, row_max(v[b]));
                 }
                 float other;
                 ok = exchange(top, other);
@@ -314,18 +321,15 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
                 l *= f;
 #pragma unroll
                 for (int i = 0; i < kHalf; ++i) acc[i] *= f;
+                F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        v[b][i] = (word[b] >> i) & 1 ? exp2_approx(fmaf(v[b][i], c, -base)) : 0.f;
-                        sum[i & 3] += v[b][i];
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    exp_row(v[b], F2(c, c), F2(-base, -base), sum);
                     store_planes(v[b], base_t + F::kHalfState * w + 16 * b, base_t + F::kMid + F::kHalfState / 2 * w + 16 * b,
                                  base_t + F::kLo + F::kHalfState / 2 * w + 16 * b);
                 }
+                const float2 s2 = (sum[0] + sum[1]).both();
+                l += s2.x + s2.y;
                 tmem_wait_st();
             }
             fence_before();
@@ -432,10 +436,9 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
             for (int j = 0; j < n_tiles; ++j) {
                 mask.next();
                 if (!load(2 * j, K)) break;
-                if (a.keep && t == 0) {
-                    *reinterpret_cast<uint4*>(smem + F::kMasks + (j % kRing) * 16) =
-                        make_uint4(mask.word[0], mask.word[1], mask.word[F::kState / 32 - 2], mask.word[F::kState / 32 - 1]);
-                    bar_arrive(m_full + 8 * (j % kRing));
+                if (masked(j)) {
+                    write_bias(biases + slot(j) * F::kState, mask, t);
+                    bar_arrive(m_full + 8 * slot(j));
                 }
                 if (!load(2 * j + 1, V)) break;
                 K += F::kState * stride;
@@ -468,7 +471,8 @@ struct BwdPlan {
     static constexpr int kOwnPanel = kOwn * 128, kPanel = kWalk * 128;
     static constexpr int kTile = kPanels<PS> * kOwnPanel, kStep = kPanels<PS> * kPanel, kStages = PS >= 64 ? 4 : 8;
     static constexpr int kHalfRing = kStages / 2, kRing = 2 * kTile, kAux = kRing + kStages * kStep;
-    static constexpr int kAuxBytes = KV ? 2 * kWalk * 4 : 16, kBars = kAux + kHalfRing * kAuxBytes, kTotal = kBars + 512 + 1024;
+    static constexpr int kAuxBytes = (KV ? 2 : 1) * kWalk * 4,  // -lse and -delta of the step, or the states' bias
+         kBars = kAux + kHalfRing * kAuxBytes, kTotal = kBars + 512 + 1024;
     static constexpr uint32_t kP1 = kWalk, kP2 = kP1 + kHalf, kDp = 2 * kWalk, kD1 = kDp + kWalk, kD2 = kD1 + kHalf, kG = 4 * kWalk;
     static constexpr int kGrad = kWide ? PS : 2 * PS;  // columns of a gradient's sums
 };
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
             bar_init(full + 8 * s, kLoadThreads);
             bar_init(empty + 8 * s, 1);
         }
-        for (int s = 0; s < B::kHalfRing; ++s) bar_init(aux_full + 8 * s, KV ? kLoadThreads : 1);
+        for (int s = 0; s < B::kHalfRing; ++s) bar_init(aux_full + 8 * s, kLoadThreads);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kPairWarps) tmem_alloc(smem_u32(&s_tmem), 512);
@@ -525,7 +529,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
         const uint32_t base_t = tmem + (uint32_t(quad * 32) << 16);
         const float c = a.scale_log2;
         const int64_t p = tl.row0 + row;
-        float lse = INFINITY, delta = 0.f;
+        float lse = -INFINITY, delta = 0.f;  // minus the thread's row's (dq)
         int64_t rh = 0;
         bool keep = row < own;
         if (keep) {
@@ -535,8 +539,8 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
             } else {
                 rh = (q0 + p / a.group) * a.Hq + int64_t(h) * a.group + p % a.group;
                 const float v = a.lse[rh];
-                lse = v == -INFINITY ? INFINITY : v * kLog2e;  // a row without a kept state: P = exp2(s - inf) = 0
-                delta = a.delta[rh];
+                lse = v == -INFINITY ? -INFINITY : -v * kLog2e;  // a row without a kept state: P = exp2(s - inf) = 0
+                delta = -a.delta[rh];
             }
         }
         // the sums of the step before: dk (warpgroup 0) or dv (1), or the warpgroup's half of dq; small terms first
@@ -552,20 +556,17 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                 add_columns<kCols>(g, acc);
             }
         };
+        const bool tail = (walk.hi - walk.lo) % B::kWalk != 0;
         bool ok = true;
         for (int j = 0; j < n_tiles; ++j) {
             const int ax = j % B::kHalfRing;
             const float* s_lse = reinterpret_cast<const float*>(smem + B::kAux + ax * B::kAuxBytes) + B::kHalf * w;
             const float* s_delta = s_lse + B::kWalk;
-            uint32_t word = 0xffffffffu;
-            if (KV || a.keep) {
-                ok = __all_sync(0xffffffffu, bar_wait(aux_full + 8 * ax, (j / B::kHalfRing) & 1, dead, status));
+            const bool biased = !KV && (a.keep || (tail && j == n_tiles - 1));
+            if (KV || biased) {
+                ok = __all_sync(0xffffffffu, bar_wait(aux_full + 8 * ax, a.keep || KV ? (j / B::kHalfRing) & 1 : 0, dead, status));
                 if (!ok) break;
             }
-            if (!KV)
-                word = (a.keep ? reinterpret_cast<const uint32_t*>(smem + B::kAux + ax * B::kAuxBytes)[B::kWide ? 0 : w]
-                               : tail_word(walk.hi - walk.lo - int64_t(j) * B::kWalk, B::kWide ? 0 : w)) >>
-                       (B::kWide ? 16 * w : 0);
             ok = __all_sync(0xffffffffu, bar_wait(s_full, j & 1, dead, status));
             if (!ok) break;
             fence_after();
@@ -574,11 +575,8 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                 if (KV && w == 1 && j > 0) add_sums();  // dv of the step before is complete when S of this one is
                 load_columns(base_t + B::kHalf * w, v);
                 tmem_wait_ld(v);
-#pragma unroll
-                for (int i = 0; i < B::kHalf; ++i) {
-                    v[i] = exp2_approx(fmaf(v[i], c, KV ? -s_lse[i] : -lse));
-                    if (!KV && !((word >> i) & 1)) v[i] = 0.f;
-                }
+                if (biased) add_bias(v, s_lse);
+                bwd_p<KV>(v, F2(c, c), lse, s_lse);
                 if (KV) {
                     store_planes(v, base_t + B::kHalf * w, base_t + B::kP1 + B::kHalf / 2 * w, base_t + B::kP2 + B::kHalf / 2 * w);
                     tmem_wait_st();
@@ -595,11 +593,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                 float y[B::kHalf];
                 load_columns(base_t + B::kDp + B::kHalf * w, y);
                 tmem_wait_ld(y);
-#pragma unroll
-                for (int i = 0; i < B::kHalf; ++i) {
-                    y[i] = v[i] * (y[i] - (KV ? s_delta[i] : delta));
-                    if (!KV && !((word >> i) & 1)) y[i] = 0.f;
-                }
+                bwd_ds<KV>(y, v, F2(1.f, 1.f), delta, s_delta);
                 store_planes(y, base_t + B::kDp + B::kHalf * w, base_t + B::kD1 + B::kHalf / 2 * w,
                              base_t + B::kD2 + B::kHalf / 2 * w);
                 tmem_wait_st();
@@ -766,8 +760,8 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                     float* s_lse = reinterpret_cast<float*>(smem + B::kAux + (j % B::kHalfRing) * B::kAuxBytes);
                     // rows past the end and rows without a kept state: P = exp2(s - inf) = 0
                     if (t < B::kWalk) {
-                        s_lse[t] = v_lse == -INFINITY ? INFINITY : v_lse * kLog2e;
-                        s_lse[B::kWalk + t] = v_delta;
+                        s_lse[t] = v_lse == -INFINITY ? -INFINITY : -v_lse * kLog2e;
+                        s_lse[B::kWalk + t] = -v_delta;
                     }
                     bar_arrive(aux_full + 8 * (j % B::kHalfRing));
                     if (j + 1 < n_tiles) fetch(j + 1);
@@ -778,8 +772,8 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                     copy_arrive(full + 8 * ((2 * j + 1) % B::kStages));
                 } else {
                     mask.next();
-                    if (a.keep && t == 0) {
-                        *reinterpret_cast<uint2*>(smem + B::kAux + (j % B::kHalfRing) * B::kAuxBytes) = make_uint2(mask.word[0], mask.word[B::kWalk / 32 - 1]);
+                    if (a.keep || n < B::kWalk) {
+                        write_bias(reinterpret_cast<float*>(smem + B::kAux + (j % B::kHalfRing) * B::kAuxBytes), mask, t);
                         bar_arrive(aux_full + 8 * (j % B::kHalfRing));
                     }
                     auto use = [&](int r) { return mask.has(r); };
@@ -847,8 +841,7 @@ cudaError_t launch_attn_planes(const AttnArgs& a, void* ws, int sms, cudaStream_
     j.j[1] = {static_cast<const float*>(a.k), a.k_row, a.k_head, a.nk, a.Hkv, const_cast<uint16_t*>(x.k)};
     j.j[2] = {static_cast<const float*>(a.v), a.v_row, a.v_head, a.nk, a.Hkv, const_cast<uint16_t*>(x.v)};
     j.j[3] = {static_cast<const float*>(a.d_out), a.o_row, a.o_head, a.d_out ? a.nq : 0, a.Hq, const_cast<uint16_t*>(x.d_out)};
-    const int64_t most = std::max(a.nq * a.Hq, a.nk * a.Hkv) * (plane_stride(a.D) / 8);
-    const unsigned blocks = unsigned(std::min<int64_t>((most + 255) / 256, int64_t(sms) * 8));
+    const unsigned blocks = unsigned(std::min<int64_t>((std::max(a.nq, a.nk) + 7) / 8, int64_t(sms) * 8));
     return by_plane(a.D, [&](auto ps) {
         attn_planes<decltype(ps)::value><<<dim3(blocks, a.d_out ? 4 : 3), 256, 0, st>>>(j);
         return cudaGetLastError();

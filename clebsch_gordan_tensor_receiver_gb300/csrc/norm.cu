@@ -62,34 +62,6 @@ struct NormArgs {
     float *mean, *rstd;  // [B][G]
 };
 
-// Pairs of fp32 values: one packed instruction does both (add, mul, fma .f32x2), which halves the
-// arithmetic that a value costs beside the two special-function instructions of its sigmoid.
-struct F2 {
-    uint64_t v;
-    __device__ __forceinline__ F2() {}
-    __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
-    __device__ __forceinline__ float2 both() const {
-        float2 r;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-        return r;
-    }
-};
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-
 // The pairs of a vector; a single element is paired with zero.
 template <int V>
 constexpr int kPairs = V > 1 ? V / 2 : 1;
