@@ -149,10 +149,9 @@ Choice choose(const AttnShape& s, int sms) {
     c.fwd = splits_for(rows_busy(128 * c.nt), s.max_k, 128, sms, true);
     c.dq = splits_for(rows_busy(c.R), s.max_k, 128, sms, false);
     c.dkv = splits_for(states_busy(c.R), s.max_q * group, 128, sms, false);
-    if (c.planes && s.head_dim > 64) {  // sums in tensor memory: short walks
-        const auto pieces = [](int64_t n) { return int((n + kPlaneWalk - 1) / kPlaneWalk); };
-        c.dq = std::max(c.dq, pieces(s.max_k));
-        c.dkv = std::max(c.dkv, pieces(s.max_q * group));
+    if (const int walk = c.planes ? plane_walk(s.head_dim) : 0) {  // sums in tensor memory: short walks
+        c.dq = std::max(c.dq, int((s.max_k + walk - 1) / walk));
+        c.dkv = std::max(c.dkv, int((s.max_q * group + walk - 1) / walk));
     }
     return c;
 }
@@ -167,7 +166,7 @@ void attn_workspace(const AttnShape& s, int sms, size_t* fwd, size_t* bwd) {
     *fwd = c.fwd > 1 ? align256(c.fwd * qh * 4) + align256(c.fwd * qh * s.head_dim * 4) : 0;
     if (c.planes) *fwd += attn_planes_bytes(s, false);
     const size_t dq = c.dq > 1 ? c.dq * qh * s.head_dim * 4 : 0, dkv = c.dkv > 1 ? 2 * c.dkv * kh * s.head_dim * 4 : 0;
-    *bwd = align256(qh * 4) + align256(std::max(dq, dkv));
+    *bwd = align256(qh * 4) + align256(dq) + align256(dkv);
     if (c.planes) *bwd += attn_planes_bytes(s, true);
 }
 
@@ -221,11 +220,21 @@ cudaError_t launch_attn_fwd(const AttnShape& s, const AttnTensors& t, void* ws, 
 
 cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, int sms, cudaStream_t st) {
     AttnArgs a = attn_args(s, t);
-    a.delta = static_cast<float*>(ws);
-    a.part_o = a.delta + align256(size_t(a.nq) * a.Hq * 4) / 4;
     const Choice c = choose(s, sms);
-    const size_t dq = c.dq > 1 ? size_t(c.dq) * a.nq * a.Hq : 0, dkv = c.dkv > 1 ? 2 * size_t(c.dkv) * a.nk * a.Hkv : 0;
-    void* planes = reinterpret_cast<char*>(a.part_o) + align256(std::max(dq, dkv) * a.D * 4);
+    const bool want_q = a.dq && a.nq > 0, want_kv = a.dk && a.nk > 0;
+    const int64_t n_q = a.nq * a.Hq * a.D, n_kv = a.nk * a.Hkv * a.D;
+    char* w = static_cast<char*>(ws);
+    const auto take = [&](size_t bytes) {
+        char* p = w;
+        w += align256(bytes);
+        return reinterpret_cast<float*>(p);
+    };
+    a.delta = take(size_t(a.nq) * a.Hq * 4);
+    a.splits_q = c.dq, a.splits_kv = c.dkv;
+    a.part_q = take(c.dq > 1 ? size_t(c.dq) * n_q * 4 : 0);
+    a.part_kv = take(c.dkv > 1 ? 2 * size_t(c.dkv) * n_kv * 4 : 0);
+    a.kv_tiles = want_kv ? state_tiles(s, c.R) : 0;
+    const int64_t q_tiles = want_q ? row_tiles(s, c.R) : 0;
     const auto with_type = [&](auto f) {
         switch (s.dtype) {
             case UVU_F32: f(float{}); break;
@@ -235,36 +244,37 @@ cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, 
         return cudaGetLastError();
     };
     const auto blocks = [](int64_t n) { return unsigned((n + kThreads - 1) / kThreads); };
-    // dq, then dk and dv; the partial sums of one are joined before the other's are written
-    const auto half = [&](bool kv) {
-        a.splits = kv ? c.dkv : c.dq;
-        const int64_t tiles = kv ? state_tiles(s, c.R) : row_tiles(s, c.R);
-        cudaError_t e = c.planes ? launch_attn_bwd_planes(a, planes, kv, tiles, st) : launch_attn_bwd_mma(s.dtype, a, kv, tiles, st);
-        if (e != cudaSuccess || a.splits == 1) return e;
-        const int64_t n = kv ? a.nk * a.Hkv * a.D : a.nq * a.Hq * a.D;
-        return with_type([&](auto t) {
-            using T = decltype(t);
-            attn_bwd_join<T><<<blocks(n), kThreads, 0, st>>>(n, a.splits, a.part_o, static_cast<T*>(kv ? a.dk : a.dq));
-            if (kv) attn_bwd_join<T><<<blocks(n), kThreads, 0, st>>>(n, a.splits, a.part_o + a.splits * n, static_cast<T*>(a.dv));
-        });
-    };
     cudaError_t e = cudaSuccess;
-    if (a.nq > 0)
-        e = with_type([&](auto t) {
-            using T = decltype(t);
-            constexpr int V = 16 / int(sizeof(T));
-            const uintptr_t any = reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.d_out) |
-                                  uintptr_t(a.o_row | a.o_head) * sizeof(T);
-            const bool vec = a.D % V == 0 && (any & 15u) == 0;
-            int log2 = 0;
-            while (log2 < 5 && (1 << log2) * (vec ? V : 1) < a.D) ++log2;
-            const unsigned n = blocks((a.nq * a.Hq) << log2);
-            vec ? attn_delta<T, V><<<n, kThreads, 0, st>>>(a, log2) : attn_delta<T, 1><<<n, kThreads, 0, st>>>(a, log2);
-        });
-    if (e == cudaSuccess && c.planes) e = launch_attn_planes(a, planes, sms, st);
-    if (e == cudaSuccess && a.dq && a.nq > 0) e = half(false);
-    if (e == cudaSuccess && a.dk && a.nk > 0) e = half(true);
-    return e;
+    if (c.planes) {
+        e = launch_attn_planes(a, w, sms, st);
+        if (e == cudaSuccess) e = launch_attn_bwd_planes(a, w, q_tiles, st);
+    } else {
+        if (a.nq > 0)
+            e = with_type([&](auto t) {
+                using T = decltype(t);
+                constexpr int V = 16 / int(sizeof(T));
+                const uintptr_t any = reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.d_out) |
+                                      uintptr_t(a.o_row | a.o_head) * sizeof(T);
+                const bool vec = a.D % V == 0 && (any & 15u) == 0;
+                int log2 = 0;
+                while (log2 < 5 && (1 << log2) * (vec ? V : 1) < a.D) ++log2;
+                const unsigned n = blocks((a.nq * a.Hq) << log2);
+                vec ? attn_delta<T, V><<<n, kThreads, 0, st>>>(a, log2) : attn_delta<T, 1><<<n, kThreads, 0, st>>>(a, log2);
+            });
+        if (e == cudaSuccess) e = launch_attn_bwd_mma(s.dtype, a, q_tiles, st);
+    }
+    if (e != cudaSuccess) return e;
+    return with_type([&](auto t) {
+        using T = decltype(t);
+        const auto join = [&](int64_t n, int splits, const float* part, void* dst) {
+            attn_bwd_join<T><<<blocks(n), kThreads, 0, st>>>(n, splits, part, static_cast<T*>(dst));
+        };
+        if (want_q && c.dq > 1) join(n_q, c.dq, a.part_q, a.dq);
+        if (want_kv && c.dkv > 1) {
+            join(n_kv, c.dkv, a.part_kv, a.dk);
+            join(n_kv, c.dkv, a.part_kv + c.dkv * n_kv, a.dv);
+        }
+    });
 }
 
 // Status of the tensor-core attention kernels on the current device (bit 0: a bounded wait gave up).

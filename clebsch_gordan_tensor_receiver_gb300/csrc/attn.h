@@ -21,49 +21,68 @@ struct AttnArgs {
     const void* d_out;
     void *dq, *dk, *dv;  // contiguous
     float* delta;        // [nq][Hq]: sum_d d_out out
-    // split over the long axis: partial results, joined by a second kernel (splits == 1: none)
+    // split over the long axis: partial results, joined by a second kernel (1: none)
     int splits;
-    float* part_o;    // forward [splits][nq][Hq][D]; backward: partial gradients
+    float* part_o;    // [splits][nq][Hq][D]
     float* part_lse;  // [splits][nq][Hq]
+    // backward: dk and dv, then dq in one launch
+    int64_t kv_tiles;  // tile numbers of dk and dv (0: not asked for); the others are dq's
+    int splits_kv, splits_q;
+    float *part_kv, *part_q;  // [2][splits_kv][nk][Hkv][D], [splits_q][nq][Hq][D]
 };
 
 // Tile t of a packed batch whose graph b has (off[b+1] - off[b]) * per rows, R rows a tile:
 // t(b) = off[b] * per / R + b is monotone in b and leaves every graph at least the tiles that it
 // needs, so a grid of total * per / R + B tiles covers any batch; the spare numbers are empty.
 struct AttnTile {
-    int graph;     // -1: a spare number
-    int64_t row0;  // first packed row, counted from the graph's first
-    int64_t rows;  // packed rows of the graph
+    int graph;            // -1: a spare number
+    int64_t row0, rows;   // first packed row of the tile, and packed rows of the graph
+    int64_t first;        // the graph's first row
+    int64_t other, n;     // the first row and the rows of the graph on the other side
 };
-__device__ __forceinline__ AttnTile attn_tile(const int32_t* off, int graphs, int per, int R, int64_t t) {
-    int lo = 0, hi = graphs;  // the last b with t(b) <= t
-    while (hi - lo > 1) {
+// By all threads of the block (it synchronises them).  One round of loads finds the graph of a moderate batch,
+// each thread testing some; a large one is searched by halves first.
+template <int R>
+__device__ __forceinline__ AttnTile attn_tile(const int32_t* off, const int32_t* other, int graphs, int per, int64_t t) {
+    __shared__ int s[5];
+    int lo = 0, hi = graphs;  // the last b with t(b) <= t is in [lo, hi)
+    while (hi - lo > 4 * int(blockDim.x)) {
         const int mid = (lo + hi) >> 1;
         if (int64_t(off[mid]) * per / R + mid <= t)
             lo = mid;
         else
             hi = mid;
     }
-    const int64_t a = off[lo], rows = (off[lo + 1] - a) * per;
-    const int64_t r0 = (t - (a * per / R + lo)) * R;
-    return {r0 < rows ? lo : -1, r0, rows};
+    for (int b = lo + int(threadIdx.x); b < hi; b += int(blockDim.x)) {
+        const int x = off[b], y = off[b + 1], u = other[b], v = other[b + 1];
+        if (int64_t(x) * per / R + b <= t && (b + 1 == graphs || t < int64_t(y) * per / R + b + 1))
+            s[0] = b, s[1] = x, s[2] = y, s[3] = u, s[4] = v;
+    }
+    __syncthreads();
+    AttnTile r;
+    r.first = s[1], r.rows = int64_t(s[2] - s[1]) * per, r.other = s[3], r.n = s[4] - s[3];
+    r.row0 = (t - (int64_t(s[1]) * per / R + s[0])) * R;
+    r.graph = r.row0 < r.rows ? s[0] : -1;
+    return r;
 }
 
 // attn_mma.cu: the forward of 16-bit operands, nt (1 or 2) row tiles of 128 per block; a.splits > 1
 // leaves partial results for the join.
 cudaError_t launch_attn_fwd_mma(uvu_dtype dtype, const AttnArgs& a, int nt, int64_t row_tiles, cudaStream_t st);
 
-// The backward of 16-bit operands: dk and dv (kv) by tiles of 128 states, or dq by tiles of 128 rows.
-cudaError_t launch_attn_bwd_mma(uvu_dtype dtype, const AttnArgs& a, bool kv, int64_t tiles, cudaStream_t st);
+// The backward of 16-bit operands in tiles of 128 states or rows: a.kv_tiles tiles of dk and dv, q_tiles of dq.
+cudaError_t launch_attn_bwd_mma(uvu_dtype dtype, const AttnArgs& a, int64_t q_tiles, cudaStream_t st);
 
 // attn_planes.cu: fp32 operands as three bf16 planes each, in the workspace.  The backward's tiles have
-// plane_bwd_tile() rows or states; above a head dimension of 64 it walks at most kPlaneWalk of the others in one piece.
-constexpr int kPlaneWalk = 4096;
+// plane_bwd_tile() rows or states.  Where it sums in tensor memory (plane_walk() > 0) it walks at most so many of
+// the others in one piece.
 constexpr int plane_bwd_tile(int head_dim) { return head_dim <= 64 ? 128 : 64; }
+constexpr int plane_walk(int head_dim) { return head_dim > 32 && head_dim <= 64 ? 0 : 4096; }
 size_t attn_planes_bytes(const AttnShape& s, bool bwd);
+// Writes the planes of q, k and v; for the backward those of d_out too, and delta.
 cudaError_t launch_attn_planes(const AttnArgs& a, void* ws, int sms, cudaStream_t st);
 cudaError_t launch_attn_fwd_planes(const AttnArgs& a, void* ws, int64_t row_tiles, cudaStream_t st);
-cudaError_t launch_attn_bwd_planes(const AttnArgs& a, void* ws, bool kv, int64_t tiles, cudaStream_t st);
+cudaError_t launch_attn_bwd_planes(const AttnArgs& a, void* ws, int64_t q_tiles, cudaStream_t st);
 // Status words of the files' kernels.
 cudaError_t attn_fwd_mma_status(unsigned* word, bool reset);
 cudaError_t attn_bwd_mma_status(unsigned* word, bool reset);

@@ -40,11 +40,11 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_dead;
     __shared__ uint32_t s_tmem;
-    const AttnTile tl = attn_tile(a.q_off, a.graphs, a.group, kRows * NT, blockIdx.x);
+    const AttnTile tl = attn_tile<kRows * NT>(a.q_off, a.k_off, a.graphs, a.group, blockIdx.x);
     if (tl.graph < 0) return;
     const int h = blockIdx.y, split = blockIdx.z;
-    const int64_t q0 = a.q_off[tl.graph], k0 = a.k_off[tl.graph];
-    const Piece kr = piece_of(a.k_off[tl.graph + 1] - k0, split, a.splits);
+    const int64_t q0 = tl.first, k0 = tl.other;
+    const Piece kr = piece_of(tl.n, split, a.splits);
     const int n_tiles = int((kr.hi - kr.lo + kRows - 1) / kRows);
     const int n_rows = int(min(tl.rows - tl.row0, int64_t(kRows * NT)));
     const int nt = NT == 2 && n_rows > kRows ? 2 : 1;  // row tiles in use

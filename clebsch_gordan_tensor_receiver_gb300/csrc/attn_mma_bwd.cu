@@ -6,7 +6,7 @@
 //              R1  R2  X1  X2      S = R1 X1^T,  dP = R2 X2^T,  P = exp2(c S - lse),  dS = P (dP - delta)
 //     dq       Q   dO  K   V       dq += dS X1
 //     dk, dv   K   V   Q   dO      dk += dS X1,  dv += P X2      (S and dP transposed: lanes are states)
-// Two sweeps instead of one cost S and dP twice (seven products instead of five), but every sum stays
+// Both kinds of tile are in one launch, the longer dk, dv tiles first.  Two sweeps instead of one cost S and dP twice (seven products instead of five), but every sum stays
 // in one CTA's tensor memory: no atomics, and results that do not depend on timing.
 //
 // Tensor memory: S, dP (128 columns each), then the sums.  P and dS are written as 16-bit values over
@@ -66,16 +66,17 @@ __device__ __forceinline__ void store_grad16(const float (&o)[16], float scale, 
 }
 
 template <typename T, int LG, bool ALIGNED, bool KV>
-__global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(AttnArgs a, BwdLayout<KV> L) {
+__device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>& L, int64_t tile) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_dead;
     __shared__ uint32_t s_tmem;
-    const AttnTile tl = KV ? attn_tile(a.k_off, a.graphs, 1, kRows, blockIdx.x) : attn_tile(a.q_off, a.graphs, a.group, kRows, blockIdx.x);
+    const int h = blockIdx.y, split = blockIdx.z, splits = KV ? a.splits_kv : a.splits_q;
+    if (split >= splits) return;
+    const AttnTile tl = KV ? attn_tile<kRows>(a.k_off, a.q_off, a.graphs, 1, tile) : attn_tile<kRows>(a.q_off, a.k_off, a.graphs, a.group, tile);
     if (tl.graph < 0) return;
-    const int h = blockIdx.y, split = blockIdx.z;
-    const int64_t q0 = a.q_off[tl.graph], k0 = a.k_off[tl.graph];
-    const int64_t rows = (a.q_off[tl.graph + 1] - q0) * a.group, states = a.k_off[tl.graph + 1] - k0;
-    const Piece walk = piece_of(KV ? rows : states, split, a.splits);
+    const int64_t q0 = KV ? tl.other : tl.first, k0 = KV ? tl.first : tl.other;
+    const int64_t rows = KV ? tl.n * a.group : tl.rows, states = KV ? tl.rows : tl.n;
+    const Piece walk = piece_of(KV ? rows : states, split, splits);
     const int n_tiles = int((walk.hi - walk.lo + kRows - 1) / kRows);
     const int own = int(min(tl.rows - tl.row0, int64_t(kRows)));  // rows of the resident tile
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(AttnArgs a, Bw
             // dk: warpgroup 0, dv: warpgroup 1; dq: the column blocks in turn
             const int64_t n = KV ? a.nk * a.Hkv : a.nq * a.Hq;
             T* dst = static_cast<T*>(KV ? (w ? a.dv : a.dk) : a.dq) + rh * a.D;
-            float* part = a.splits > 1 ? a.part_o + ((KV && w ? a.splits + split : split) * n + rh) * a.D : nullptr;
+            float* part = splits > 1 ? (KV ? a.part_kv : a.part_q) + ((KV && w ? splits + split : split) * n + rh) * a.D : nullptr;
             const bool vec = a.D % 8 == 0 && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
             const float scale = KV && w ? kUnshift : a.scale;
             for (int d = KV ? 0 : w; d < d16; d += KV ? 1 : 2) {
@@ -372,28 +373,37 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(AttnArgs a, Bw
     }
 }
 
-template <typename T, bool KV>
-cudaError_t bwd(const AttnArgs& a, int64_t tiles, cudaStream_t st) {
-    BwdLayout<KV> L;
-    L.panels = a.D > 64 ? 2 : 1;
-    L.stages = L.panels == 1 ? 8 : 4;  // 160 or 192 KB
+template <typename T, int LG, bool ALIGNED>
+__global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(const __grid_constant__ AttnArgs a, BwdLayout<true> Lkv, BwdLayout<false> Lq) {
+    if (blockIdx.x < a.kv_tiles)
+        bwd_tile<T, LG, ALIGNED, true>(a, Lkv, blockIdx.x);
+    else
+        bwd_tile<T, LG, ALIGNED, false>(a, Lq, blockIdx.x - a.kv_tiles);
+}
+
+template <typename T>
+cudaError_t bwd(const AttnArgs& a, int64_t q_tiles, cudaStream_t st) {
+    BwdLayout<true> kv;
+    BwdLayout<false> q;
+    kv.panels = q.panels = a.D > 64 ? 2 : 1;
+    kv.stages = q.stages = kv.panels == 1 ? 8 : 4;  // 160 or 192 KB
     const uintptr_t any = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
                           reinterpret_cast<uintptr_t>(a.d_out) |
                           uintptr_t(a.q_row | a.q_head | a.k_row | a.k_head | a.v_row | a.v_head | a.o_row | a.o_head) * 2;
     return by_chunks(a.D, (any & 15u) == 0, [&](auto lg, auto aligned) {
-        auto k = attn_bwd_mma<T, decltype(lg)::value, decltype(aligned)::value, KV>;
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total());
+        auto k = attn_bwd_mma<T, decltype(lg)::value, decltype(aligned)::value>;
+        const int smem = std::max(kv.total(), q.total());
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        k<<<dim3(unsigned(tiles), unsigned(a.Hkv), unsigned(a.splits)), kBwdWarps * 32, L.total(), st>>>(a, L);
+        k<<<dim3(unsigned(a.kv_tiles + q_tiles), unsigned(a.Hkv), unsigned(std::max(a.splits_kv, a.splits_q))), kBwdWarps * 32, smem, st>>>(a, kv, q);
         return cudaGetLastError();
     });
 }
 
 }  // namespace
 
-cudaError_t launch_attn_bwd_mma(uvu_dtype dtype, const AttnArgs& a, bool kv, int64_t tiles, cudaStream_t st) {
-    if (dtype == UVU_BF16) return kv ? bwd<__nv_bfloat16, true>(a, tiles, st) : bwd<__nv_bfloat16, false>(a, tiles, st);
-    return kv ? bwd<__half, true>(a, tiles, st) : bwd<__half, false>(a, tiles, st);
+cudaError_t launch_attn_bwd_mma(uvu_dtype dtype, const AttnArgs& a, int64_t q_tiles, cudaStream_t st) {
+    return dtype == UVU_BF16 ? bwd<__nv_bfloat16>(a, q_tiles, st) : bwd<__half>(a, q_tiles, st);
 }
 
 cudaError_t attn_bwd_mma_status(unsigned* word, bool reset) { return read_status(word, reset); }

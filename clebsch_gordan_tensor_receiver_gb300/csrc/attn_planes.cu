@@ -13,16 +13,14 @@
 //     the tile, P0 X, P1 [X0 | X1] and P2 X0 land in columns by order of magnitude: the sums of the small terms
 //     are apart from the large ones, and the threads add them.
 //   - Tensor memory sums each tile afresh; the sums over tiles are fp32 registers (accumulating in tensor
-//     memory loses more than a rounded fp32 addition does, and long rows would show it).  The backward at
-//     PS = 128 has no registers for that: it sums in tensor memory, over walks of at most kPlaneWalk rows
-//     (about 4e-9 of the sum is lost per 16 rows), and the joining kernel adds the walks.
+//     memory loses more than a rounded fp32 addition does, and long rows would show it).  Where the backward
+//     has no registers for that it sums in tensor memory, over walks of at most plane_walk() rows (about 4e-9 of the
+//     sum is lost per 16 rows), and the joining kernel adds the walks.
 // Masks, splits and bounded waits as in the 16-bit kernels.
 #include "attn_mma.h"
 
 namespace uvu {
 namespace {
-
-constexpr int kPairWarps = 8;  // two warpgroups share a tile: warpgroup w takes the w-th half of a row's columns
 
 // ----------------------------------------------------------------------------------- planes
 
@@ -32,10 +30,12 @@ struct PlaneJob {
     int64_t rows;
     int heads;
     uint16_t* out;  // [rows][heads][3][PS]
+    bool vec;       // fours of columns are 16-byte aligned
 };
 struct PlaneJobs {
     PlaneJob j[4];
     int D;
+    bool vec_o;  // of out and d_out
 };
 
 // The planes of two values, packed: the leading plane in p[0].
@@ -48,18 +48,43 @@ __device__ __forceinline__ void cut2(float x, float y, uint32_t (&p)[3]) {
     p[2] = __byte_perm(__float_as_uint(x1 - __uint_as_float(c & 0xffff0000u)), __float_as_uint(y1 - __uint_as_float(d & 0xffff0000u)), 0x7632);
 }
 
-// 32 threads on the 8-column chunks of a row's heads, 8 rows a block.
+// A thread per 8 columns of a (row, head), 64 rows a block; the backward's last slice of the grid forms delta, a
+// thread per (row, head).
 template <int PS>
-__global__ void __launch_bounds__(256) attn_planes(PlaneJobs jobs) {
-    constexpr int kChunks = PS / 8;
+__global__ void __launch_bounds__(256) attn_planes(PlaneJobs jobs, AttnArgs a) {
+    constexpr int kChunks = PS / 8, kBlockRows = 64;
+    if (blockIdx.y == 4) {
+        for (int64_t r0 = int64_t(blockIdx.x) * kBlockRows; r0 < a.nq; r0 += int64_t(gridDim.x) * kBlockRows) {
+            const int n = int(min(int64_t(kBlockRows), a.nq - r0)) * a.Hq;
+            for (int i = threadIdx.x; i < n; i += 256) {
+                const int r = i / a.Hq, h = i - r * a.Hq;
+                const int64_t at = (r0 + r) * a.o_row + h * a.o_head;
+                const float *x = static_cast<const float*>(a.d_out) + at, *y = static_cast<const float*>(a.out) + at;
+                float s = 0.f;
+                if (jobs.vec_o) {
+                    for (int d = 0; d < a.D; d += 4) {
+                        const float4 u = *reinterpret_cast<const float4*>(x + d), v = *reinterpret_cast<const float4*>(y + d);
+                        s = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, s))));
+                    }
+                } else {
+                    for (int d = 0; d < a.D; ++d) s = fmaf(x[d], y[d], s);
+                }
+                a.delta[(r0 + r) * a.Hq + h] = s;
+            }
+        }
+        return;
+    }
     const PlaneJob& j = jobs.j[blockIdx.y];
-    const bool vec = jobs.D % 4 == 0 && j.row % 4 == 0 && j.head % 4 == 0 && (reinterpret_cast<uintptr_t>(j.x) & 15u) == 0;
-    for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < j.rows; r += int64_t(gridDim.x) * 8)
-        for (int e = threadIdx.x & 31; e < j.heads * kChunks; e += 32) {
+    const int per = j.heads * kChunks;
+    for (int64_t r0 = int64_t(blockIdx.x) * kBlockRows; r0 < j.rows; r0 += int64_t(gridDim.x) * kBlockRows) {
+        const int n = int(min(int64_t(kBlockRows), j.rows - r0)) * per;
+        for (int i = threadIdx.x; i < n; i += 256) {
+            const int rr = i / per, e = i - rr * per;
+            const int64_t r = r0 + rr;
             const int h = e / kChunks, c = e % kChunks * 8;
             const float* x = j.x + r * j.row + h * j.head + c;
             float v[8];
-            if (vec) {
+            if (j.vec) {
 #pragma unroll
                 for (int k = 0; k < 8; k += 4) {
                     const float4 q = c + k < jobs.D ? *reinterpret_cast<const float4*>(x + k) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -91,6 +116,7 @@ __global__ void __launch_bounds__(256) attn_planes(PlaneJobs jobs) {
 #pragma unroll
             for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(o + q * PS) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
         }
+    }
 }
 
 // An operand's planes in the workspace.
@@ -202,30 +228,33 @@ __device__ __forceinline__ void store_row(float* dst, const float* v, float scal
 
 // ----------------------------------------------------------------------------------- forward
 
-// State tiles of 128, or of 64 where a tile's planes would not fit beside Q's (PS = 128).
+// PS <= 32: one warpgroup per row tile, state tiles of 64, 256 columns of tensor memory and at most 102 KB: two CTAs an
+// SM, whose products and exponentials overlap.  Above, one CTA an SM whose two warpgroups share a tile, warpgroup w taking
+// the w-th half of a row's columns; state tiles of 128, or of 64 where a tile's planes would not fit beside Q's (PS = 128).
 template <int PS>
 struct FwdPlan {
-    static constexpr int kState = PS == 128 ? 64 : 128, kHalfState = kState / 2, kPanel = kState * 128;
+    static constexpr int kGroups = PS <= 32 ? 1 : 2, kWarps = 4 * kGroups, kThreads = (kWarps + 1 + kLoadWarps) * 32;
+    static constexpr int kState = PS == 64 ? 128 : 64, kHalfState = kState / kGroups, kPanel = kState * 128;
     static constexpr int kTile = kPanels<PS> * kPanelBytes, kStep = kPanels<PS> * kPanel;
-    static constexpr int kStages = PS == 128 ? 2 : PS == 64 ? 3 : PS == 32 ? 5 : 8;
+    static constexpr int kStages = PS == 128 ? 2 : PS == 64 ? 3 : PS == 32 ? 4 : 8;
     static constexpr int kRing = kTile, kMasks = kRing + kStages * kStep, kMax = kMasks + 8 * kState * 4, kBars = kMax + 2 * 2 * kRows * 4;
     static constexpr int kTotal = kBars + 512 + 1024;  // barriers, alignment slack
     // tensor memory: S (plane 0 of P written over it), planes 1 and 2 of P, O by order
-    static constexpr uint32_t kMid = kState, kLo = kState + kState / 2, kO = 2 * kState;
+    static constexpr uint32_t kMid = kState, kLo = kState + kState / 2, kO = 2 * kState, kColumns = kO + 3 * PS <= 256 ? 256 : 512;
 };
 
 template <int PS>
-__global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fwd_planes(AttnArgs a, Planes x) {
+__global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns == 256 ? 2 : 1) attn_fwd_planes(AttnArgs a, Planes x) {
     using F = FwdPlan<PS>;
-    constexpr int kHalf = PS / 2, kRing = 8, kBlocks = F::kHalfState / 32;  // 32-column blocks of a warpgroup
+    constexpr int kHalf = PS / F::kGroups, kRing = 8, kBlocks = F::kHalfState / 32;  // 32-column blocks of a warpgroup
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_dead;
     __shared__ uint32_t s_tmem;
-    const AttnTile tl = attn_tile(a.q_off, a.graphs, a.group, kRows, blockIdx.x);
+    const AttnTile tl = attn_tile<kRows>(a.q_off, a.k_off, a.graphs, a.group, blockIdx.x);
     if (tl.graph < 0) return;
     const int h = blockIdx.y, split = blockIdx.z;
-    const int64_t q0 = a.q_off[tl.graph], k0 = a.k_off[tl.graph];
-    const Piece kr = piece_of(a.k_off[tl.graph + 1] - k0, split, a.splits);
+    const int64_t q0 = tl.first, k0 = tl.other;
+    const Piece kr = piece_of(tl.n, split, a.splits);
     const int n_tiles = int((kr.hi - kr.lo + F::kState - 1) / F::kState);
     const int n_rows = int(min(tl.rows - tl.row0, int64_t(kRows)));
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -237,7 +266,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
         s_dead = 0;
         bar_init(q_full, kLoadThreads);
         bar_init(s_full, 1);
-        bar_init(p_full, kPairWarps);
+        bar_init(p_full, F::kWarps);
         bar_init(o_full, 1);
         bar_init(fin, 1);
         for (int i = 0; i < 4; ++i) bar_init(pair + 8 * i, 2);
@@ -248,7 +277,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
         for (int s = 0; s < kRing; ++s) bar_init(m_full + 8 * s, kLoadThreads);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kPairWarps) tmem_alloc(smem_u32(&s_tmem), 512);
+    if (warp == F::kWarps) tmem_alloc(smem_u32(&s_tmem), F::kColumns);
     fence_before();
     __syncthreads();
     fence_after();
@@ -261,7 +290,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
     auto masked = [&](int j) { return a.keep || (tail && j == n_tiles - 1); };
     auto slot = [&](int j) { return a.keep ? j % kRing : 0; };
 
-    if (warp < kPairWarps) {
+    if (warp < F::kWarps) {
         // ------------------------------------------------------------------------ softmax
         const int w = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         const bool work = quad * 32 < n_rows;
@@ -275,6 +304,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
         bool ok = true;
         // the partner warpgroup's value of the same row
         auto exchange = [&](float v, float& other) {
+            if constexpr (F::kGroups == 1) return true;
             float* s = s_max + (turn & 1) * 2 * kRows;
             s[w * kRows + row] = v;
             __syncwarp();
@@ -312,7 +342,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
                     if (biased) add_bias(v[b], bias + 32 * b);
                     top = fmaxf(top, row_max(v[b]));
                 }
-                float other;
+                float other = -INFINITY;
                 ok = exchange(top, other);
                 if (!ok) break;
                 const float mn = fmaxf(m, fmaxf(top, other) * c), base = mn == -INFINITY ? 0.f : mn;
@@ -360,7 +390,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
                 }
             }
         }
-    } else if (warp == kPairWarps) {
+    } else if (warp == F::kWarps) {
         // ----------------------------------------------------------------- matrix instructions
         if (lane == 0) {
             constexpr uint32_t o = F::kO;
@@ -411,7 +441,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
         __syncwarp();
     } else {
         // ------------------------------------------------------------------------- loaders
-        const int t = threadIdx.x - (kPairWarps + 1) * 32;
+        const int t = threadIdx.x - (F::kWarps + 1) * 32;
         if (n_tiles > 0) {
             constexpr int64_t kHead = 3 * PS * 2;  // bytes of a (row, head)
             load_planes_packed<PS, kRows>(sb, reinterpret_cast<const char*>(x.q) + (q0 * a.Hq + int64_t(h) * a.group) * kHead,
@@ -449,48 +479,52 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_fw
     }
     fence_before();
     __syncthreads();
-    if (warp == kPairWarps) {
+    if (warp == F::kWarps) {
         fence_after();
-        tmem_free(tmem, 512);
+        tmem_free(tmem, F::kColumns);
     }
 }
 
 // ---------------------------------------------------------------------------------- backward
 
-// The walk, its order and the roles as in the 16-bit backward, in steps of 64 walked rows (the planes of two
-// resident tiles leave room for four such stages).  Tensor memory: S with plane 0 of P over it, planes 1
-// and 2 of P, dP and the planes of dS likewise, then the sums of one step: the leading terms in PS columns, the
-// small ones in PS more.
-// At PS = 128 the resident tiles have 64 rows (the instructions still take 128: the upper half reads
-// whatever follows in shared memory, into lanes that nobody reads), steps have 32, and dk, dv and dq are summed
-// over the walk in tensor memory, each step's small terms first.
+// The walk, its order and the roles as in the 16-bit backward, in steps of 32 or 64 walked rows.  Tensor memory:
+// S with plane 0 of P over it, planes 1 and 2 of P, dP and the planes of dS likewise, then the sums.
+//   PS <= 32   one warpgroup, steps of 32, 256 columns of tensor memory and at most 98 KB: two CTAs an SM.  The sums
+//              stay in tensor memory over the walk, each step's small terms first.
+//   PS = 64    two warpgroups, steps of 64 (the planes of two resident tiles leave room for four such stages).  The
+//              sums of one step: the leading terms in PS columns, the small ones in PS more; registers over the walk.
+//   PS = 128   two warpgroups, steps of 32, resident tiles of 64 rows (the instructions still take 128: the upper half
+//              reads whatever follows in shared memory, into lanes that nobody reads), sums in tensor memory.
 template <int PS, bool KV>
 struct BwdPlan {
-    static constexpr bool kWide = PS == 128;
-    static constexpr int kOwn = kWide ? 64 : 128, kWalk = kWide ? 32 : 64, kHalf = kWalk / 2;
+    static constexpr bool kHeld = PS != 64;  // sums held in tensor memory
+    static constexpr int kGroups = PS <= 32 ? 1 : 2, kWarps = 4 * kGroups;
+    static constexpr int kOwn = PS == 128 ? 64 : 128, kWalk = PS == 64 ? 64 : 32, kHalf = kWalk / kGroups;
     static constexpr int kOwnPanel = kOwn * 128, kPanel = kWalk * 128;
-    static constexpr int kTile = kPanels<PS> * kOwnPanel, kStep = kPanels<PS> * kPanel, kStages = PS >= 64 ? 4 : 8;
+    static constexpr int kTile = kPanels<PS> * kOwnPanel, kStep = kPanels<PS> * kPanel, kStages = PS == 16 ? 8 : 4;
     static constexpr int kHalfRing = kStages / 2, kRing = 2 * kTile, kAux = kRing + kStages * kStep;
-    static constexpr int kAuxBytes = (KV ? 2 : 1) * kWalk * 4,  // -lse and -delta of the step, or the states' bias
-         kBars = kAux + kHalfRing * kAuxBytes, kTotal = kBars + 512 + 1024;
-    static constexpr uint32_t kP1 = kWalk, kP2 = kP1 + kHalf, kDp = 2 * kWalk, kD1 = kDp + kWalk, kD2 = kD1 + kHalf, kG = 4 * kWalk;
-    static constexpr int kGrad = kWide ? PS : 2 * PS;  // columns of a gradient's sums
+    static constexpr int kAuxBytes = (KV ? 2 : 1) * kWalk * 4;  // -lse and -delta of the step, or the states' bias
+    static constexpr int kBars = kAux + kHalfRing * kAuxBytes, kTotal = kBars + 512 + 1024;
+    static constexpr uint32_t kP1 = kWalk, kP2 = kP1 + kWalk / 2, kDp = 2 * kWalk, kD1 = kDp + kWalk, kD2 = kD1 + kWalk / 2, kG = 4 * kWalk;
+    static constexpr int kGrad = kHeld ? PS : 2 * PS;  // columns of a gradient's sums
+    static constexpr uint32_t kColumns = kG + 2 * kGrad <= 256 ? 256 : 512;
 };
 
 template <int PS, bool KV>
-__global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bwd_planes(AttnArgs a, Planes x) {
+__device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int64_t tile) {
     using B = BwdPlan<PS, KV>;
-    constexpr int kCols = KV ? PS : PS / 2;  // columns of a thread: dk or dv, or half of dq
+    constexpr int kCols = KV ? PS : PS / B::kGroups;  // columns of a gradient that a thread writes
     constexpr float kLog2e = 1.4426950408889634f;
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_dead;
     __shared__ uint32_t s_tmem;
-    const AttnTile tl = KV ? attn_tile(a.k_off, a.graphs, 1, B::kOwn, blockIdx.x) : attn_tile(a.q_off, a.graphs, a.group, B::kOwn, blockIdx.x);
+    const int h = blockIdx.y, split = blockIdx.z, splits = KV ? a.splits_kv : a.splits_q;
+    if (split >= splits) return;
+    const AttnTile tl = KV ? attn_tile<B::kOwn>(a.k_off, a.q_off, a.graphs, 1, tile) : attn_tile<B::kOwn>(a.q_off, a.k_off, a.graphs, a.group, tile);
     if (tl.graph < 0) return;
-    const int h = blockIdx.y, split = blockIdx.z;
-    const int64_t q0 = a.q_off[tl.graph], k0 = a.k_off[tl.graph];
-    const int64_t rows = (a.q_off[tl.graph + 1] - q0) * a.group, states = a.k_off[tl.graph + 1] - k0;
-    const Piece walk = piece_of(KV ? rows : states, split, a.splits);
+    const int64_t q0 = KV ? tl.other : tl.first, k0 = KV ? tl.first : tl.other;
+    const int64_t rows = KV ? tl.n * a.group : tl.rows, states = KV ? tl.rows : tl.n;
+    const Piece walk = piece_of(KV ? rows : states, split, splits);
     const int n_tiles = int((walk.hi - walk.lo + B::kWalk - 1) / B::kWalk);
     const int own = int(min(tl.rows - tl.row0, int64_t(B::kOwn)));
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -503,8 +537,8 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
         bar_init(r_full, kLoadThreads);
         bar_init(s_full, 1);
         bar_init(dp_full, 1);
-        bar_init(p_ready, kPairWarps);
-        bar_init(ds_ready, kPairWarps);
+        bar_init(p_ready, B::kWarps);
+        bar_init(ds_ready, B::kWarps);
         bar_init(done, 1);
         bar_init(fin, 1);
         for (int s = 0; s < B::kStages; ++s) {
@@ -514,7 +548,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
         for (int s = 0; s < B::kHalfRing; ++s) bar_init(aux_full + 8 * s, kLoadThreads);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kPairWarps) tmem_alloc(smem_u32(&s_tmem), 512);
+    if (warp == B::kWarps) tmem_alloc(smem_u32(&s_tmem), B::kColumns);
     fence_before();
     __syncthreads();
     fence_after();
@@ -522,7 +556,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
     volatile int* dead = &s_dead;
     unsigned* status = &attn_status_word;
 
-    if (warp < kPairWarps) {
+    if (warp < B::kWarps) {
         // ----------------------------------------------------------------- P and dS
         const int w = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         const bool work = quad * 32 < own;
@@ -543,15 +577,15 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                 delta = -a.delta[rh];
             }
         }
-        // the sums of the step before: dk (warpgroup 0) or dv (1), or the warpgroup's half of dq; small terms first
-        const uint32_t g = base_t + B::kG + (KV ? w * B::kGrad : w * (PS / 2));
-        float acc[B::kWide ? 1 : kCols];
-        if constexpr (!B::kWide) {
+        // the sums of the step before: dk (warpgroup 0) or dv (1), or the warpgroup's part of dq; small terms first
+        const uint32_t g = base_t + B::kG + (KV ? w * B::kGrad : w * kCols);
+        float acc[B::kHeld ? 1 : kCols];
+        if constexpr (!B::kHeld) {
 #pragma unroll
             for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
         }
         auto add_sums = [&]() {
-            if constexpr (!B::kWide) {
+            if constexpr (!B::kHeld) {
                 add_columns<kCols>(g + PS, acc);
                 add_columns<kCols>(g, acc);
             }
@@ -608,33 +642,37 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
         }
         if (ok && work) {
             const int64_t n = KV ? a.nk * a.Hkv : a.nq * a.Hq;
-            float* dst = static_cast<float*>(KV ? (w ? a.dv : a.dk) : a.dq) + rh * a.D;
-            if (a.splits > 1) dst = a.part_o + ((KV && w ? a.splits + split : split) * n + rh) * a.D;
-            const float scale = KV && w ? 1.f : a.scale;
-            const int c0 = KV ? 0 : w * (PS / 2);
-            if constexpr (B::kWide) {
+            // dk, dv: warpgroup 0 and 1, or one after the other by the only one
 #pragma unroll 1
-                for (int b = 0; b < kCols / 16; ++b) {
-                    float o[16];
-                    __syncwarp();
-                    if (n_tiles > 0) {
-                        tmem_ld16(g + 16 * b, o);
-                        tmem_wait_ld(o);
+            for (int which = w; which < (KV ? 2 : w + 1); which += B::kGroups) {
+                float* dst = static_cast<float*>(KV ? (which ? a.dv : a.dk) : a.dq) + rh * a.D;
+                if (splits > 1) dst = (KV ? a.part_kv : a.part_q) + ((KV && which ? splits + split : split) * n + rh) * a.D;
+                const float scale = KV && which ? 1.f : a.scale;
+                const int c0 = KV ? 0 : w * kCols;
+                if constexpr (B::kHeld) {
+#pragma unroll 1
+                    for (int b = 0; b < kCols / 16; ++b) {
+                        float o[16];
+                        __syncwarp();
+                        if (n_tiles > 0) {
+                            tmem_ld16(base_t + B::kG + (KV ? which * B::kGrad : c0) + 16 * b, o);
+                            tmem_wait_ld(o);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = n_tiles > 0 && keep ? o[i] : 0.f;
+                        if (row < own) store_row<16>(dst, o, scale, c0 + 16 * b, a.D);
                     }
+                } else {
+                    if (n_tiles > 0) add_sums();
+                    if (!keep) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = n_tiles > 0 && keep ? o[i] : 0.f;
-                    if (row < own) store_row<16>(dst, o, scale, c0 + 16 * b, a.D);
+                        for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+                    }
+                    if (row < own) store_row<kCols>(dst, acc, scale, c0, a.D);
                 }
-            } else {
-                if (n_tiles > 0) add_sums();
-                if (!keep) {
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-                }
-                if (row < own) store_row<kCols>(dst, acc, scale, c0, a.D);
             }
         }
-    } else if (warp == kPairWarps) {
+    } else if (warp == B::kWarps) {
         // ----------------------------------------------------------------- matrix instructions
         if (lane == 0) {
             const uint32_t id_s = mma_desc<__nv_bfloat16>(B::kWalk, false), id2 = mma_desc<__nv_bfloat16>(2 * PS, true),
@@ -650,10 +688,10 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
                 six_products<PS>(d, r, B::kOwnPanel, xs, B::kPanel, id_s);
                 mma_commit(bar);
             };
-            // d = A X over the step's rows, A in planes at a0 (its warpgroups' halves apart), a1, a2; at PS = 128 d += A X
+            // d = A X over the step's rows, A in planes at a0 (its warpgroups' halves apart), a1, a2; or d += A X where the sums are held
             auto sum = [&](uint32_t d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t xs, bool first) {
                 auto block = [&](int q, int s) { return q == 0 ? a0 + block_column(s, B::kHalf) : (q == 1 ? a1 : a2) + 8 * s; };
-                if constexpr (B::kWide) {
+                if constexpr (B::kHeld) {
                     constexpr int kPair[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
                     bool add = !first;
 #pragma unroll
@@ -716,7 +754,7 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
         __syncwarp();
     } else {
         // ------------------------------------------------------------------------- loaders
-        const int t = threadIdx.x - (kPairWarps + 1) * 32;
+        const int t = threadIdx.x - (B::kWarps + 1) * 32;
         if (n_tiles > 0) {
             constexpr int64_t kHead = 3 * PS * 2;  // bytes of a (row, head)
             const int64_t q_at = (q0 * a.Hq + int64_t(h) * a.group) * kHead, q_row = a.Hq * kHead, k_row = a.Hkv * kHead;
@@ -797,10 +835,22 @@ __global__ void __launch_bounds__((kPairWarps + 1 + kLoadWarps) * 32, 1) attn_bw
     }
     fence_before();
     __syncthreads();
-    if (warp == kPairWarps) {
+    if (warp == B::kWarps) {
         fence_after();
-        tmem_free(tmem, 512);
+        tmem_free(tmem, B::kColumns);
     }
+}
+
+template <int PS>
+constexpr int kBwdThreads = (BwdPlan<PS, true>::kWarps + 1 + kLoadWarps) * 32;
+
+template <int PS>
+__global__ void __launch_bounds__(kBwdThreads<PS>, BwdPlan<PS, true>::kColumns == 256 ? 2 : 1)
+    attn_bwd_planes(const __grid_constant__ AttnArgs a, Planes x) {
+    if (blockIdx.x < a.kv_tiles)
+        bwd_tile<PS, true>(a, x, blockIdx.x);
+    else
+        bwd_tile<PS, false>(a, x, blockIdx.x - a.kv_tiles);
 }
 
 template <typename F>
@@ -832,18 +882,27 @@ size_t attn_planes_bytes(const AttnShape& s, bool bwd) {
     return q + 2 * k + (bwd ? q : 0);
 }
 
-// Writes the planes of q, k, v and, where there is one, d_out.
 cudaError_t launch_attn_planes(const AttnArgs& a, void* ws, int sms, cudaStream_t st) {
     const Planes x = planes_at(a, ws);
+    const auto vec = [&](const void* p, int64_t row, int64_t head) {
+        return a.D % 4 == 0 && row % 4 == 0 && head % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+    };
+    const auto job = [&](const void* p, int64_t row, int64_t head, int64_t rows, int heads, const uint16_t* out) {
+        return PlaneJob{static_cast<const float*>(p), row, head, rows, heads, const_cast<uint16_t*>(out), vec(p, row, head)};
+    };
     PlaneJobs j = {};
     j.D = a.D;
-    j.j[0] = {static_cast<const float*>(a.q), a.q_row, a.q_head, a.nq, a.Hq, const_cast<uint16_t*>(x.q)};
-    j.j[1] = {static_cast<const float*>(a.k), a.k_row, a.k_head, a.nk, a.Hkv, const_cast<uint16_t*>(x.k)};
-    j.j[2] = {static_cast<const float*>(a.v), a.v_row, a.v_head, a.nk, a.Hkv, const_cast<uint16_t*>(x.v)};
-    j.j[3] = {static_cast<const float*>(a.d_out), a.o_row, a.o_head, a.d_out ? a.nq : 0, a.Hq, const_cast<uint16_t*>(x.d_out)};
-    const unsigned blocks = unsigned(std::min<int64_t>((std::max(a.nq, a.nk) + 7) / 8, int64_t(sms) * 8));
+    j.j[0] = job(a.q, a.q_row, a.q_head, a.nq, a.Hq, x.q);
+    j.j[1] = job(a.k, a.k_row, a.k_head, a.nk, a.Hkv, x.k);
+    j.j[2] = job(a.v, a.v_row, a.v_head, a.nk, a.Hkv, x.v);
+    const bool bwd = a.delta != nullptr;
+    if (bwd) {
+        j.j[3] = job(a.d_out, a.o_row, a.o_head, a.nq, a.Hq, x.d_out);
+        j.vec_o = j.j[3].vec && vec(a.out, a.o_row, a.o_head);
+    }
+    const unsigned blocks = unsigned(std::min<int64_t>((std::max(a.nq, a.nk) + 63) / 64, int64_t(sms) * 8));
     return by_plane(a.D, [&](auto ps) {
-        attn_planes<decltype(ps)::value><<<dim3(blocks, a.d_out ? 4 : 3), 256, 0, st>>>(j);
+        attn_planes<decltype(ps)::value><<<dim3(blocks, bwd ? 5 : 3), 256, 0, st>>>(j, a);
         return cudaGetLastError();
     });
 }
@@ -852,25 +911,24 @@ cudaError_t launch_attn_fwd_planes(const AttnArgs& a, void* ws, int64_t row_tile
     const Planes x = planes_at(a, ws);
     return by_plane(a.D, [&](auto ps) {
         constexpr int PS = decltype(ps)::value;
-        cudaError_t e = cudaFuncSetAttribute(attn_fwd_planes<PS>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdPlan<PS>::kTotal);
+        using F = FwdPlan<PS>;
+        cudaError_t e = cudaFuncSetAttribute(attn_fwd_planes<PS>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kTotal);
         if (e != cudaSuccess) return e;
-        attn_fwd_planes<PS><<<dim3(unsigned(row_tiles), unsigned(a.Hkv), unsigned(a.splits)), (kPairWarps + 1 + kLoadWarps) * 32,
-                              FwdPlan<PS>::kTotal, st>>>(a, x);
+        attn_fwd_planes<PS><<<dim3(unsigned(row_tiles), unsigned(a.Hkv), unsigned(a.splits)), F::kThreads, F::kTotal, st>>>(a, x);
         return cudaGetLastError();
     });
 }
 
-cudaError_t launch_attn_bwd_planes(const AttnArgs& a, void* ws, bool kv, int64_t tiles, cudaStream_t st) {
+cudaError_t launch_attn_bwd_planes(const AttnArgs& a, void* ws, int64_t q_tiles, cudaStream_t st) {
     const Planes x = planes_at(a, ws);
     return by_plane(a.D, [&](auto ps) {
         constexpr int PS = decltype(ps)::value;
-        auto go = [&](auto k, int smem) {
-            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess) return e;
-            k<<<dim3(unsigned(tiles), unsigned(a.Hkv), unsigned(a.splits)), (kPairWarps + 1 + kLoadWarps) * 32, smem, st>>>(a, x);
-            return cudaGetLastError();
-        };
-        return kv ? go(attn_bwd_planes<PS, true>, BwdPlan<PS, true>::kTotal) : go(attn_bwd_planes<PS, false>, BwdPlan<PS, false>::kTotal);
+        constexpr int smem = std::max(BwdPlan<PS, true>::kTotal, BwdPlan<PS, false>::kTotal);
+        cudaError_t e = cudaFuncSetAttribute(attn_bwd_planes<PS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        attn_bwd_planes<PS><<<dim3(unsigned(a.kv_tiles + q_tiles), unsigned(a.Hkv), unsigned(std::max(a.splits_kv, a.splits_q))),
+                              kBwdThreads<PS>, smem, st>>>(a, x);
+        return cudaGetLastError();
     });
 }
 
