@@ -102,10 +102,10 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
                 const bool biased = masked(j);
                 const float* bias = biases + slot(j) * kRows;
                 if (biased) {
-                    ok = __all_sync(0xffffffffu, bar_wait(m_full + 8 * slot(j), a.keep ? (j / kMaskRing) & 1 : 0, dead, status));
+                    ok = warp_wait(m_full + 8 * slot(j), a.keep ? (j / kMaskRing) & 1 : 0, dead, status);
                     if (!ok) break;
                 }
-                ok = __all_sync(0xffffffffu, bar_wait(s_full + 8 * t, j & 1, dead, status));
+                ok = warp_wait(s_full + 8 * t, j & 1, dead, status);
                 if (!ok) break;
                 fence_after();
                 if (work) {
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
                 if (lane == 0) bar_arrive(p_full + 8 * t);
             }
             if (ok && n_tiles > 0) {
-                ok = __all_sync(0xffffffffu, bar_wait(o_full + 8 * t, 0, dead, status));
+                ok = warp_wait(o_full + 8 * t, 0, dead, status);
                 fence_after();
             }
             if (ok && work) {
@@ -228,32 +228,35 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
         }
     } else if (warp == 4 * NT) {
         // ----------------------------------------------------------------- matrix instructions
-        if (lane == 0) {
+        {
+            const uint32_t lead = elect_lane();
             const uint32_t id_s = mma_desc<T>(kRows, false), id_o = mma_desc<T>(16 * d16, true);
             auto stage = [&](int i) { return sb + uint32_t(L.ring() + (i % L.stages) * L.tile()); };
-            auto wait_stage = [&](int i) { return bar_wait(full + 8 * (i % L.stages), (i / L.stages) & 1, dead, status); };
+            auto wait_stage = [&](int i) { return warp_wait(full + 8 * (i % L.stages), (i / L.stages) & 1, dead, status); };
             auto scores = [&](int t, int j) {
                 const uint32_t q = sb + uint32_t(t * L.tile()), k = stage(2 * j);
-                for (int s = 0; s < d16; ++s) mma_ss(tmem + uint32_t(t * kRows), desc_cols(q, s), desc_cols(k, s), id_s, s > 0);
-                mma_commit(s_full + 8 * t);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    if (s < d16) mma_ss(lead, tmem + uint32_t(t * kRows), desc_cols(q, s), desc_cols(k, s), id_s, s > 0);
+                mma_commit(lead, s_full + 8 * t);
             };
-            bool ok = n_tiles > 0 && bar_wait(q_full, 0, dead, status) && wait_stage(0);
+            bool ok = n_tiles > 0 && warp_wait(q_full, 0, dead, status) && wait_stage(0);
             if (ok) {
                 fence_async();
                 for (int t = 0; t < nt; ++t) scores(t, 0);
-                mma_commit(empty + 8 * 0);
+                mma_commit(lead, empty + 8 * 0);
             }
             for (int j = 0; j < n_tiles && ok; ++j) {
                 ok = wait_stage(2 * j + 1);
                 fence_async();
                 for (int t = 0; t < nt && ok; ++t) {
-                    ok = bar_wait(p_full + 8 * t, j & 1, dead, status);
+                    ok = warp_wait(p_full + 8 * t, j & 1, dead, status);
                     if (!ok) break;
                     fence_after();
                     const uint32_t o = tmem + uint32_t(NT * kRows) + uint32_t(t) * o_cols, v = stage(2 * j + 1);
 #pragma unroll
                     for (int s = 0; s < kRows / 16; ++s)
-                        mma_ts(o, tmem + uint32_t(t * kRows + 8 * s), desc_rows(v, s), id_o, j > 0 || s > 0);
+                        mma_ts(lead, o, tmem + uint32_t(t * kRows + 8 * s), desc_rows(v, s), id_o, j > 0 || s > 0);
                     if (j + 1 < n_tiles) {
                         if (t == 0) {
                             ok = wait_stage(2 * j + 2);
@@ -262,15 +265,15 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
                         }
                         scores(t, j + 1);
                     } else {
-                        mma_commit(o_full + 8 * t);
+                        mma_commit(lead, o_full + 8 * t);
                     }
                 }
                 if (!ok) break;
-                mma_commit(empty + 8 * ((2 * j + 1) % L.stages));
-                if (j + 1 < n_tiles) mma_commit(empty + 8 * ((2 * j + 2) % L.stages));
+                mma_commit(lead, empty + 8 * ((2 * j + 1) % L.stages));
+                if (j + 1 < n_tiles) mma_commit(lead, empty + 8 * ((2 * j + 2) % L.stages));
             }
             // every instruction issued has finished before the tensor memory and the stages go
-            mma_commit(fin);
+            mma_commit(lead, fin);
             bar_wait_last(fin, 0, status);
         }
         __syncwarp();
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
             auto arrive = [&](uint32_t bar) { ALIGNED ? copy_arrive(bar) : bar_arrive(bar); };
             const char* Q = reinterpret_cast<const char*>(static_cast<const T*>(a.q) + q0 * a.q_row + int64_t(h) * a.group * a.q_head);
             for (int i = 0; i < nt; ++i)
-                load_packed<ALIGNED>(sb + uint32_t(i * L.tile()), Q, a.q_row * 2, a.q_head * 2, a.group, tl.row0 + i * kRows,
+                load_packed<ALIGNED, false>(sb + uint32_t(i * L.tile()), Q, a.q_row * 2, a.q_head * 2, a.group, tl.row0 + i * kRows,
                                          n_rows - i * kRows, map);
             arrive(q_full);
             const char* K = reinterpret_cast<const char*>(static_cast<const T*>(a.k) + (k0 + kr.lo) * a.k_row + h * a.k_head) + map.chunk * 16;
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
             StateMask<> mask(a.keep ? a.keep + k0 : nullptr, kr.lo, kr.hi);
             auto load = [&](int i, const char* src, int64_t stride) {
                 if (i >= L.stages &&
-                    !__all_sync(0xffffffffu, bar_wait(empty + 8 * (i % L.stages), (i / L.stages - 1) & 1, dead, status)))
+                    !warp_wait(empty + 8 * (i % L.stages), (i / L.stages - 1) & 1, dead, status))
                     return false;
                 const uint32_t dst = sb + uint32_t(L.ring() + (i % L.stages) * L.tile());
                 auto use = [&](int r) { return mask.has(r); };

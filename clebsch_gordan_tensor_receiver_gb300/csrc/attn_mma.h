@@ -82,12 +82,13 @@ __device__ __forceinline__ void load_strided(uint32_t dst, const char* src, int6
     }
 }
 
-// Packed rows of a kv head's queries from r0 on: row r is query r / group, head r % group.
-template <bool ALIGNED, int LG, int ROWS>
+// Packed rows of a kv head's queries from r0 on: row r is query r / group, head r % group.  Rows from `rows` on are
+// zeros, or left alone (!ZERO: rows of the M side, whose lanes nobody reads).
+template <bool ALIGNED, bool ZERO, int LG, int ROWS>
 __device__ __forceinline__ void load_packed(uint32_t dst, const char* base, int64_t row, int64_t head, int group, int64_t r0, int rows,
                                             const LoadMap<LG, ROWS>& m) {
     using M = LoadMap<LG, ROWS>;
-    if (group == 1) {
+    if (group == 1 && (ZERO || rows >= ROWS)) {
         auto use = [&](int r) { return r < rows; };
         if (rows >= ROWS)
             load_strided<ALIGNED, true>(dst, base + r0 * row + m.chunk * 16, row, m, use);
@@ -105,6 +106,7 @@ __device__ __forceinline__ void load_packed(uint32_t dst, const char* base, int6
 #pragma unroll 4
     for (int i = 0; i < M::kIters; ++i) {
         const int r = m.row + i * M::kStep;
+        if (!ZERO && r >= rows) break;
         load_chunk<ALIGNED>(dst + tile_offset(r, m.chunk), p, r < rows ? m.bytes : 0);
         p += step;
         j += dj;

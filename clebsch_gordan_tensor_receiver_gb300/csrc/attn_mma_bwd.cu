@@ -144,10 +144,10 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
             const float* s_delta = s_lse + kRows;
             const bool biased = !KV && (a.keep || (tail && j == n_tiles - 1));
             if (KV || biased) {
-                ok = __all_sync(0xffffffffu, bar_wait(aux_full + 8 * ax, a.keep || KV ? (j / half) & 1 : 0, dead, status));
+                ok = warp_wait(aux_full + 8 * ax, a.keep || KV ? (j / half) & 1 : 0, dead, status);
                 if (!ok) break;
             }
-            ok = __all_sync(0xffffffffu, bar_wait(s_full, j & 1, dead, status));
+            ok = warp_wait(s_full, j & 1, dead, status);
             if (!ok) break;
             fence_after();
             float x[2][32];
@@ -171,7 +171,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(p_ready);
-            ok = __all_sync(0xffffffffu, bar_wait(dp_full, j & 1, dead, status));
+            ok = warp_wait(dp_full, j & 1, dead, status);
             if (!ok) break;
             fence_after();
             if (work) {
@@ -193,7 +193,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
             if (lane == 0) bar_arrive(ds_ready);
         }
         if (ok && n_tiles > 0) {
-            ok = __all_sync(0xffffffffu, bar_wait(done, 0, dead, status));
+            ok = warp_wait(done, 0, dead, status);
             fence_after();
         }
         if (ok && work) {
@@ -217,63 +217,66 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
         }
     } else if (warp == 8) {
         // ----------------------------------------------------------------- matrix instructions
-        if (lane == 0) {
+        {
+            const uint32_t lead = elect_lane();
             const uint32_t id_s = mma_desc<T>(kRows, false), id_g = mma_desc<T>(16 * d16, true);
             const uint32_t r1 = sb, r2 = sb + uint32_t(L.tile());
             auto stage = [&](int i) { return sb + uint32_t(L.ring() + (i % L.stages) * L.tile()); };
             auto wait_stage = [&](int i) {
-                if (!bar_wait(full + 8 * (i % L.stages), (i / L.stages) & 1, dead, status)) return false;
+                if (!warp_wait(full + 8 * (i % L.stages), (i / L.stages) & 1, dead, status)) return false;
                 fence_async();
                 return true;
             };
             auto product = [&](uint32_t d, uint32_t r, uint32_t x, uint32_t bar) {
-                for (int s = 0; s < d16; ++s) mma_ss(d, desc_cols(r, s), desc_cols(x, s), id_s, s > 0);
-                mma_commit(bar);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    if (s < d16) mma_ss(lead, d, desc_cols(r, s), desc_cols(x, s), id_s, s > 0);
+                mma_commit(lead, bar);
             };
             // d += A X: the 16-bit A of row block s lies in the half that its warpgroup wrote
             auto sum = [&](uint32_t d, uint32_t A, uint32_t x, bool first) {
 #pragma unroll
                 for (int s = 0; s < kRows / 16; ++s)
-                    mma_ts(d, A + uint32_t((s >> 2) * 64 + (s & 3) * 8), desc_rows(x, s), id_g, !first || s > 0);
+                    mma_ts(lead, d, A + uint32_t((s >> 2) * 64 + (s & 3) * 8), desc_rows(x, s), id_g, !first || s > 0);
             };
-            bool ok = n_tiles > 0 && bar_wait(r_full, 0, dead, status) && wait_stage(0);
+            bool ok = n_tiles > 0 && warp_wait(r_full, 0, dead, status) && wait_stage(0);
             if (ok) {
                 product(tmem, r1, stage(0), s_full);
                 ok = wait_stage(1);
                 if (ok) {
                     product(t_dp, r2, stage(1), dp_full);
-                    if (!KV) mma_commit(empty + 8 * 1);
+                    if (!KV) mma_commit(lead, empty + 8 * 1);
                 }
             }
             for (int j = 0; j < n_tiles && ok; ++j) {
-                ok = bar_wait(p_ready, j & 1, dead, status);
+                ok = warp_wait(p_ready, j & 1, dead, status);
                 if (!ok) break;
                 fence_after();
                 if (KV) {
                     sum(t_g + g_cols, tmem, stage(2 * j + 1), j == 0);
-                    mma_commit(empty + 8 * ((2 * j + 1) % L.stages));
+                    mma_commit(lead, empty + 8 * ((2 * j + 1) % L.stages));
                 }
                 if (j + 1 < n_tiles) {
                     ok = wait_stage(2 * j + 2);
                     if (!ok) break;
                     product(tmem, r1, stage(2 * j + 2), s_full);
                 }
-                ok = bar_wait(ds_ready, j & 1, dead, status);
+                ok = warp_wait(ds_ready, j & 1, dead, status);
                 if (!ok) break;
                 fence_after();
                 sum(t_g, t_dp, stage(2 * j), j == 0);
-                mma_commit(empty + 8 * ((2 * j) % L.stages));
+                mma_commit(lead, empty + 8 * ((2 * j) % L.stages));
                 if (j + 1 < n_tiles) {
                     ok = wait_stage(2 * j + 3);
                     if (!ok) break;
                     product(t_dp, r2, stage(2 * j + 3), dp_full);
-                    if (!KV) mma_commit(empty + 8 * ((2 * j + 3) % L.stages));
+                    if (!KV) mma_commit(lead, empty + 8 * ((2 * j + 3) % L.stages));
                 } else {
-                    mma_commit(done);
+                    mma_commit(lead, done);
                 }
             }
             // every instruction issued has finished before the tensor memory and the stages go
-            mma_commit(fin);
+            mma_commit(lead, fin);
             bar_wait_last(fin, 0, status);
         }
         __syncwarp();
@@ -297,10 +300,10 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                     load_strided<ALIGNED, false>(dst, src, stride, map, use);
             };
             auto rows_tile = [&](uint32_t dst, const char* base, int64_t row, int64_t head, int64_t r0, int n) {
-                load_packed<ALIGNED>(dst, base, row * 2, head * 2, a.group, r0, n, map);
+                load_packed<ALIGNED, KV>(dst, base, row * 2, head * 2, a.group, r0, n, map);
             };
             auto free_stage = [&](int i) {
-                return i < L.stages || __all_sync(0xffffffffu, bar_wait(empty + 8 * (i % L.stages), (i / L.stages - 1) & 1, dead, status));
+                return i < L.stages || warp_wait(empty + 8 * (i % L.stages), (i / L.stages - 1) & 1, dead, status);
             };
             auto stage = [&](int i) { return sb + uint32_t(L.ring() + (i % L.stages) * L.tile()); };
             if (KV) {

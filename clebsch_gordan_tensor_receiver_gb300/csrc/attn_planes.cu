@@ -136,19 +136,19 @@ __device__ __forceinline__ void load_planes(uint32_t dst, const char* src, int64
         load_strided<true, ALL>(dst + p * ROWS * 128, src + p * 128 + m.chunk * 16, stride, m, use);
     }
 }
-template <int PS, int ROWS>
+template <int PS, int ROWS, bool ZERO>
 __device__ __forceinline__ void load_planes_packed(uint32_t dst, const char* base, int64_t row, int64_t head, int group, int64_t r0,
                                                    int rows, int t) {
 #pragma unroll
     for (int p = 0; p < kPanels<PS>; ++p) {
         const LoadMap<3, ROWS> m(t, 3 * PS - 64 * p < 64 ? 3 * PS - 64 * p : 64);
-        load_packed<true>(dst + p * ROWS * 128, base + p * 128, row, head, group, r0, rows, m);
+        load_packed<true, ZERO>(dst + p * ROWS * 128, base + p * 128, row, head, group, r0, rows, m);
     }
 }
 
 // The six products of S (or dP) = A B^T, smallest first; panels of `rows` x 128 bytes.
 template <int PS>
-__device__ __forceinline__ void six_products(uint32_t d, uint32_t a, int a_panel, uint32_t b, int b_panel, uint32_t id) {
+__device__ __forceinline__ void six_products(uint32_t lead, uint32_t d, uint32_t a, int a_panel, uint32_t b, int b_panel, uint32_t id) {
     constexpr int kStep = PS / 16;
     constexpr int kPair[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
     bool add = false;
@@ -156,7 +156,7 @@ __device__ __forceinline__ void six_products(uint32_t d, uint32_t a, int a_panel
     for (int i = 0; i < 6; ++i)
 #pragma unroll
         for (int s = 0; s < kStep; ++s) {
-            mma_ss(d, desc_cols(a, kPair[i][0] * kStep + s, a_panel), desc_cols(b, kPair[i][1] * kStep + s, b_panel), id, add);
+            mma_ss(lead, d, desc_cols(a, kPair[i][0] * kStep + s, a_panel), desc_cols(b, kPair[i][1] * kStep + s, b_panel), id, add);
             add = true;
         }
 }
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
             s[w * kRows + row] = v;
             __syncwarp();
             if (lane == 0) bar_arrive(pair + 8 * quad);
-            if (!__all_sync(0xffffffffu, bar_wait(pair + 8 * quad, turn & 1, dead, status))) return false;
+            if (!warp_wait(pair + 8 * quad, turn & 1, dead, status)) return false;
             other = s[(1 - w) * kRows + row];
             ++turn;
             return true;
@@ -324,10 +324,10 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
             const bool biased = masked(j);
             const float* bias = biases + slot(j) * F::kState + F::kHalfState * w;
             if (biased) {
-                ok = __all_sync(0xffffffffu, bar_wait(m_full + 8 * slot(j), a.keep ? (j / kRing) & 1 : 0, dead, status));
+                ok = warp_wait(m_full + 8 * slot(j), a.keep ? (j / kRing) & 1 : 0, dead, status);
                 if (!ok) break;
             }
-            ok = __all_sync(0xffffffffu, bar_wait(s_full, j & 1, dead, status));
+            ok = warp_wait(s_full, j & 1, dead, status);
             if (!ok) break;
             fence_after();
             if (work) {
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
             if (lane == 0) bar_arrive(p_full);
         }
         if (ok && n_tiles > 0) {
-            ok = __all_sync(0xffffffffu, bar_wait(o_full, 0, dead, status));
+            ok = warp_wait(o_full, 0, dead, status);
             fence_after();
         }
         if (ok && work) {
@@ -392,25 +392,26 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
         }
     } else if (warp == F::kWarps) {
         // ----------------------------------------------------------------- matrix instructions
-        if (lane == 0) {
+        {
+            const uint32_t lead = elect_lane();
             constexpr uint32_t o = F::kO;
             const uint32_t id_s = mma_desc<__nv_bfloat16>(F::kState, false), id3 = mma_desc<__nv_bfloat16>(3 * PS <= 256 ? 3 * PS : 256, true),
                            id2 = mma_desc<__nv_bfloat16>(2 * PS, true), id1 = mma_desc<__nv_bfloat16>(PS, true);
             auto stage = [&](int i) { return sb + uint32_t(F::kRing + (i % F::kStages) * F::kStep); };
             auto wait_stage = [&](int i) {
-                if (!bar_wait(full + 8 * (i % F::kStages), (i / F::kStages) & 1, dead, status)) return false;
+                if (!warp_wait(full + 8 * (i % F::kStages), (i / F::kStages) & 1, dead, status)) return false;
                 fence_async();
                 return true;
             };
             auto scores = [&](int j) {
-                six_products<PS>(tmem, sb, kPanelBytes, stage(2 * j), F::kPanel, id_s);
-                mma_commit(s_full);
-                mma_commit(empty + 8 * ((2 * j) % F::kStages));
+                six_products<PS>(lead, tmem, sb, kPanelBytes, stage(2 * j), F::kPanel, id_s);
+                mma_commit(lead, s_full);
+                mma_commit(lead, empty + 8 * ((2 * j) % F::kStages));
             };
-            bool ok = n_tiles > 0 && bar_wait(q_full, 0, dead, status) && wait_stage(0);
+            bool ok = n_tiles > 0 && warp_wait(q_full, 0, dead, status) && wait_stage(0);
             if (ok) scores(0);
             for (int j = 0; j < n_tiles && ok; ++j) {
-                ok = wait_stage(2 * j + 1) && bar_wait(p_full, j & 1, dead, status);
+                ok = wait_stage(2 * j + 1) && warp_wait(p_full, j & 1, dead, status);
                 if (!ok) break;
                 fence_after();
                 const uint32_t v = stage(2 * j + 1);
@@ -419,23 +420,23 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
                     const uint32_t hi = tmem + block_column(s, F::kHalfState), mid = tmem + F::kMid + 8 * s, lo = tmem + F::kLo + 8 * s;
                     const uint64_t v0 = desc_rows(v, s, F::kPanel);
                     if constexpr (3 * PS <= 256) {
-                        mma_ts(tmem + o, hi, v0, id3, s > 0);
+                        mma_ts(lead, tmem + o, hi, v0, id3, s > 0);
                     } else {  // 256 columns at most
-                        mma_ts(tmem + o, hi, v0, id2, s > 0);
-                        mma_ts(tmem + o + 2 * PS, hi, desc_rows(v, s, F::kPanel, 2 * PS), id1, s > 0);
+                        mma_ts(lead, tmem + o, hi, v0, id2, s > 0);
+                        mma_ts(lead, tmem + o + 2 * PS, hi, desc_rows(v, s, F::kPanel, 2 * PS), id1, s > 0);
                     }
-                    mma_ts(tmem + o + PS, mid, v0, id2, true);
-                    mma_ts(tmem + o + 2 * PS, lo, v0, id1, true);
+                    mma_ts(lead, tmem + o + PS, mid, v0, id2, true);
+                    mma_ts(lead, tmem + o + 2 * PS, lo, v0, id1, true);
                 }
-                mma_commit(empty + 8 * ((2 * j + 1) % F::kStages));
+                mma_commit(lead, empty + 8 * ((2 * j + 1) % F::kStages));
                 if (j + 1 < n_tiles) {
                     ok = wait_stage(2 * j + 2);
                     if (ok) scores(j + 1);
                 } else {
-                    mma_commit(o_full);
+                    mma_commit(lead, o_full);
                 }
             }
-            mma_commit(fin);
+            mma_commit(lead, fin);
             bar_wait_last(fin, 0, status);
         }
         __syncwarp();
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
         const int t = threadIdx.x - (F::kWarps + 1) * 32;
         if (n_tiles > 0) {
             constexpr int64_t kHead = 3 * PS * 2;  // bytes of a (row, head)
-            load_planes_packed<PS, kRows>(sb, reinterpret_cast<const char*>(x.q) + (q0 * a.Hq + int64_t(h) * a.group) * kHead,
+            load_planes_packed<PS, kRows, false>(sb, reinterpret_cast<const char*>(x.q) + (q0 * a.Hq + int64_t(h) * a.group) * kHead,
                                           a.Hq * kHead, kHead, a.group, tl.row0, n_rows, t);
             copy_arrive(q_full);
             const char* K = reinterpret_cast<const char*>(x.k) + ((k0 + kr.lo) * a.Hkv + h) * kHead;
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
             const int64_t stride = a.Hkv * kHead;
             StateMask<F::kState> mask(a.keep ? a.keep + k0 : nullptr, kr.lo, kr.hi);
             auto load = [&](int i, const char* src) {
-                if (i >= F::kStages && !__all_sync(0xffffffffu, bar_wait(empty + 8 * (i % F::kStages), (i / F::kStages - 1) & 1, dead, status)))
+                if (i >= F::kStages && !warp_wait(empty + 8 * (i % F::kStages), (i / F::kStages - 1) & 1, dead, status))
                     return false;
                 const uint32_t dst = sb + uint32_t(F::kRing + (i % F::kStages) * F::kStep);
                 auto use = [&](int r) { return mask.has(r); };
@@ -598,10 +599,10 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
             const float* s_delta = s_lse + B::kWalk;
             const bool biased = !KV && (a.keep || (tail && j == n_tiles - 1));
             if (KV || biased) {
-                ok = __all_sync(0xffffffffu, bar_wait(aux_full + 8 * ax, a.keep || KV ? (j / B::kHalfRing) & 1 : 0, dead, status));
+                ok = warp_wait(aux_full + 8 * ax, a.keep || KV ? (j / B::kHalfRing) & 1 : 0, dead, status);
                 if (!ok) break;
             }
-            ok = __all_sync(0xffffffffu, bar_wait(s_full, j & 1, dead, status));
+            ok = warp_wait(s_full, j & 1, dead, status);
             if (!ok) break;
             fence_after();
             float v[B::kHalf];
@@ -619,7 +620,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(p_ready);
-            ok = __all_sync(0xffffffffu, bar_wait(dp_full, j & 1, dead, status));
+            ok = warp_wait(dp_full, j & 1, dead, status);
             if (!ok) break;
             fence_after();
             if (work) {
@@ -637,7 +638,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
             if (lane == 0) bar_arrive(ds_ready);
         }
         if (ok && n_tiles > 0) {
-            ok = __all_sync(0xffffffffu, bar_wait(done, 0, dead, status));
+            ok = warp_wait(done, 0, dead, status);
             fence_after();
         }
         if (ok && work) {
@@ -674,19 +675,20 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
         }
     } else if (warp == B::kWarps) {
         // ----------------------------------------------------------------- matrix instructions
-        if (lane == 0) {
+        {
+            const uint32_t lead = elect_lane();
             const uint32_t id_s = mma_desc<__nv_bfloat16>(B::kWalk, false), id2 = mma_desc<__nv_bfloat16>(2 * PS, true),
                            id1 = mma_desc<__nv_bfloat16>(PS, true);
             const uint32_t r1 = sb, r2 = sb + uint32_t(B::kTile);
             auto stage = [&](int i) { return sb + uint32_t(B::kRing + (i % B::kStages) * B::kStep); };
             auto wait_stage = [&](int i) {
-                if (!bar_wait(full + 8 * (i % B::kStages), (i / B::kStages) & 1, dead, status)) return false;
+                if (!warp_wait(full + 8 * (i % B::kStages), (i / B::kStages) & 1, dead, status)) return false;
                 fence_async();
                 return true;
             };
             auto product = [&](uint32_t d, uint32_t r, uint32_t xs, uint32_t bar) {
-                six_products<PS>(d, r, B::kOwnPanel, xs, B::kPanel, id_s);
-                mma_commit(bar);
+                six_products<PS>(lead, d, r, B::kOwnPanel, xs, B::kPanel, id_s);
+                mma_commit(lead, bar);
             };
             // d = A X over the step's rows, A in planes at a0 (its warpgroups' halves apart), a1, a2; or d += A X where the sums are held
             auto sum = [&](uint32_t d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t xs, bool first) {
@@ -698,57 +700,57 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
                     for (int i = 0; i < 6; ++i)
 #pragma unroll
                         for (int s = 0; s < B::kWalk / 16; ++s) {
-                            mma_ts(d, block(kPair[i][0], s), desc_rows(xs, s, B::kPanel, kPair[i][1] * PS), id1, add);
+                            mma_ts(lead, d, block(kPair[i][0], s), desc_rows(xs, s, B::kPanel, kPair[i][1] * PS), id1, add);
                             add = true;
                         }
                 } else {
 #pragma unroll
                     for (int s = 0; s < B::kWalk / 16; ++s) {
-                        mma_ts(d, block(0, s), desc_rows(xs, s, B::kPanel), id2, s > 0);
-                        mma_ts(d + PS, block(0, s), desc_rows(xs, s, B::kPanel, 2 * PS), id1, true);
-                        mma_ts(d + PS, block(1, s), desc_rows(xs, s, B::kPanel), id1, true);
-                        mma_ts(d + PS, block(1, s), desc_rows(xs, s, B::kPanel, PS), id1, true);
-                        mma_ts(d + PS, block(2, s), desc_rows(xs, s, B::kPanel), id1, true);
+                        mma_ts(lead, d, block(0, s), desc_rows(xs, s, B::kPanel), id2, s > 0);
+                        mma_ts(lead, d + PS, block(0, s), desc_rows(xs, s, B::kPanel, 2 * PS), id1, true);
+                        mma_ts(lead, d + PS, block(1, s), desc_rows(xs, s, B::kPanel), id1, true);
+                        mma_ts(lead, d + PS, block(1, s), desc_rows(xs, s, B::kPanel, PS), id1, true);
+                        mma_ts(lead, d + PS, block(2, s), desc_rows(xs, s, B::kPanel), id1, true);
                     }
                 }
             };
-            bool ok = n_tiles > 0 && bar_wait(r_full, 0, dead, status) && wait_stage(0);
+            bool ok = n_tiles > 0 && warp_wait(r_full, 0, dead, status) && wait_stage(0);
             if (ok) {
                 product(tmem, r1, stage(0), s_full);
                 ok = wait_stage(1);
                 if (ok) {
                     product(tmem + B::kDp, r2, stage(1), dp_full);
-                    if (!KV) mma_commit(empty + 8 * 1);
+                    if (!KV) mma_commit(lead, empty + 8 * 1);
                 }
             }
             for (int j = 0; j < n_tiles && ok; ++j) {
-                ok = bar_wait(p_ready, j & 1, dead, status);
+                ok = warp_wait(p_ready, j & 1, dead, status);
                 if (!ok) break;
                 fence_after();
                 if (KV) {
                     sum(tmem + B::kG + B::kGrad, tmem, tmem + B::kP1, tmem + B::kP2, stage(2 * j + 1), j == 0);
-                    mma_commit(empty + 8 * ((2 * j + 1) % B::kStages));
+                    mma_commit(lead, empty + 8 * ((2 * j + 1) % B::kStages));
                 }
                 if (j + 1 < n_tiles) {
                     ok = wait_stage(2 * j + 2);
                     if (!ok) break;
                     product(tmem, r1, stage(2 * j + 2), s_full);
                 }
-                ok = bar_wait(ds_ready, j & 1, dead, status);
+                ok = warp_wait(ds_ready, j & 1, dead, status);
                 if (!ok) break;
                 fence_after();
                 sum(tmem + B::kG, tmem + B::kDp, tmem + B::kD1, tmem + B::kD2, stage(2 * j), j == 0);
-                mma_commit(empty + 8 * ((2 * j) % B::kStages));
+                mma_commit(lead, empty + 8 * ((2 * j) % B::kStages));
                 if (j + 1 < n_tiles) {
                     ok = wait_stage(2 * j + 3);
                     if (!ok) break;
                     product(tmem + B::kDp, r2, stage(2 * j + 3), dp_full);
-                    if (!KV) mma_commit(empty + 8 * ((2 * j + 3) % B::kStages));
+                    if (!KV) mma_commit(lead, empty + 8 * ((2 * j + 3) % B::kStages));
                 } else {
-                    mma_commit(done);
+                    mma_commit(lead, done);
                 }
             }
-            mma_commit(fin);
+            mma_commit(lead, fin);
             bar_wait_last(fin, 0, status);
         }
         __syncwarp();
@@ -762,7 +764,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
             const int64_t k_at = ((k0 + (KV ? tl.row0 : walk.lo)) * a.Hkv + h) * kHead;
             const char *K = reinterpret_cast<const char*>(x.k) + k_at, *V = reinterpret_cast<const char*>(x.v) + k_at;
             auto free_stage = [&](int i) {
-                return i < B::kStages || __all_sync(0xffffffffu, bar_wait(empty + 8 * (i % B::kStages), (i / B::kStages - 1) & 1, dead, status));
+                return i < B::kStages || warp_wait(empty + 8 * (i % B::kStages), (i / B::kStages - 1) & 1, dead, status);
             };
             auto stage = [&](int i) { return sb + uint32_t(B::kRing + (i % B::kStages) * B::kStep); };
             if (KV) {
@@ -772,8 +774,8 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
                 load_planes<PS, B::kOwn, false>(sb, K, k_row, t, use);
                 load_planes<PS, B::kOwn, false>(sb + uint32_t(B::kTile), V, k_row, t, use);
             } else {
-                load_planes_packed<PS, B::kOwn>(sb, Q, q_row, kHead, a.group, tl.row0, own, t);
-                load_planes_packed<PS, B::kOwn>(sb + uint32_t(B::kTile), dO, q_row, kHead, a.group, tl.row0, own, t);
+                load_planes_packed<PS, B::kOwn, false>(sb, Q, q_row, kHead, a.group, tl.row0, own, t);
+                load_planes_packed<PS, B::kOwn, false>(sb + uint32_t(B::kTile), dO, q_row, kHead, a.group, tl.row0, own, t);
             }
             copy_arrive(r_full);
             // lse and delta of the walked rows, fetched a step ahead
@@ -803,10 +805,10 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
                     }
                     bar_arrive(aux_full + 8 * (j % B::kHalfRing));
                     if (j + 1 < n_tiles) fetch(j + 1);
-                    load_planes_packed<PS, B::kWalk>(stage(2 * j), Q, q_row, kHead, a.group, lo, n, t);
+                    load_planes_packed<PS, B::kWalk, true>(stage(2 * j), Q, q_row, kHead, a.group, lo, n, t);
                     copy_arrive(full + 8 * ((2 * j) % B::kStages));
                     if (!free_stage(2 * j + 1)) break;
-                    load_planes_packed<PS, B::kWalk>(stage(2 * j + 1), dO, q_row, kHead, a.group, lo, n, t);
+                    load_planes_packed<PS, B::kWalk, true>(stage(2 * j + 1), dO, q_row, kHead, a.group, lo, n, t);
                     copy_arrive(full + 8 * ((2 * j + 1) % B::kStages));
                 } else {
                     mask.next();

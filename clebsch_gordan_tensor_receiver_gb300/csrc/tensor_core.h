@@ -61,6 +61,10 @@ static __device__ __noinline__ void bar_wait_last(uint32_t b, uint32_t parity, u
 __device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity, volatile int* dead, unsigned* status) {
     return bar_test(b, parity) || bar_wait_slow(b, parity, dead, status);
 }
+// By a whole warp.
+__device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile int* dead, unsigned* status) {
+    return __all_sync(0xffffffffu, bar_wait(b, parity, dead, status));
+}
 
 // ------------------------------------------------------------------------------------- copies
 
@@ -86,19 +90,20 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {  // chunk:
     return uint32_t((chunk >> 3) * kPanelBytes + (row >> 3) * 1024 + (row & 7) * 128 + (((chunk ^ row) & 7) << 4));
 }
 
-constexpr uint64_t kDescBase = (1ull << 46) | (2ull << 61);  // version bits, 128-byte swizzle
-// The tile's columns are the summed index (16 of them, beginning at column 16 k): 8-row groups are 1024
-// bytes apart.  `panel`: bytes of a panel.
+// Shared-memory descriptors.  The lower word is the start address and the panel stride in units of 16
+// bytes; the upper one the stride of 8-row groups (1024 bytes), version bits and the 128-byte swizzle.
+// Tiles begin on 1024 bytes, so a step inside one is an addition to the lower word.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t desc_of(uint32_t low) { return (uint64_t(kDescHigh) << 32) | low; }
+// The tile's columns are the summed index (16 of them, beginning at column 16 k).  `panel`: bytes of a panel.
 __device__ __forceinline__ uint64_t desc_cols(uint32_t tile, int k, int panel = kPanelBytes) {
-    const uint32_t a = tile + uint32_t((k >> 2) * panel + (k & 3) * 32);
-    return uint64_t((a >> 4) & 0x3FFFu) | (1ull << 16) | (uint64_t(1024 >> 4) << 32) | kDescBase;
+    return desc_of((tile >> 4) + uint32_t(((k >> 2) * panel + (k & 3) * 32) >> 4) + (1u << 16));
 }
-// The tile's rows are the summed index (16 of them, beginning at row 16 k): panels of 64 columns are
-// `panel` bytes apart, groups of 8 rows 1024 bytes.  col: first column; columns from a col that is not a
-// multiple of 64 must end within its panel.
+// The tile's rows are the summed index (16 of them, beginning at row 16 k); panels of 64 columns are
+// `panel` bytes apart.  col: first column; columns from a col that is not a multiple of 64 must end within
+// its panel.
 __device__ __forceinline__ uint64_t desc_rows(uint32_t tile, int k, int panel = kPanelBytes, int col = 0) {
-    const uint32_t a = tile + uint32_t(k * 2048 + (col >> 6) * panel + (col & 63) * 2);
-    return uint64_t((a >> 4) & 0x3FFFu) | (uint64_t(panel >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | kDescBase;
+    return desc_of((tile >> 4) + uint32_t((k * 2048 + (col >> 6) * panel + (col & 63) * 2) >> 4) + (uint32_t(panel >> 4) << 16));
 }
 
 // Instruction descriptor of kind::f16 with fp32 sums: M = 128, N = n; B's rows (true) or columns are the summed index.
@@ -110,22 +115,35 @@ __device__ __forceinline__ uint32_t mma_desc(int n, bool b_rows) {
 
 // ------------------------------------------------------------------------------- tensor cores
 
+// The issuing warp runs whole, so that addresses and descriptors stay in uniform registers, and one
+// elected lane issues: with one lane alone in a branch, forming the operands cost twice the time of the products.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r;
+}
 // D (tensor memory) = [D +] A B, A from shared memory (SS) or tensor memory (TS).
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(uint32_t(add)), "r"(id)
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(uint32_t(add)), "r"(id), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %3, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(uint32_t(add)), "r"(id)
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(uint32_t(add)), "r"(id), "r"(lead)
         : "memory");
 }
 // The barrier gets an arrival when all matrix instructions issued so far are done.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+        "r"(lead)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
