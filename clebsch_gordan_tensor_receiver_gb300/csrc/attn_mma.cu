@@ -45,12 +45,12 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
     const int h = blockIdx.y, split = blockIdx.z;
     const int64_t q0 = tl.first, k0 = tl.other;
     const Piece kr = piece_of(tl.n, split, a.splits);
-    const int n_tiles = int((kr.hi - kr.lo + kRows - 1) / kRows);
-    const int n_rows = int(min(tl.rows - tl.row0, int64_t(kRows * NT)));
+    const int n_tiles = uniform(int((kr.hi - kr.lo + kRows - 1) / kRows));
+    const int n_rows = uniform(int(min(tl.rows - tl.row0, int64_t(kRows * NT))));
     const int nt = NT == 2 && n_rows > kRows ? 2 : 1;  // row tiles in use
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t sb = smem_u32(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sb = uniform(smem_u32(smem));
+    const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int d16 = (a.D + 15) / 16;
     const uint32_t q_full = sb + L.bars(), s_full = q_full + 8, p_full = s_full + 16, o_full = p_full + 16, full = o_full + 16,
                    empty = full + 8 * L.stages, m_full = empty + 8 * L.stages, fin = m_full + 8 * kMaskRing;
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
+    const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t*>(&s_tmem));
     volatile int* dead = &s_dead;
     unsigned* status = &attn_status_word;
     float* biases = reinterpret_cast<float*>(smem + L.masks());

@@ -77,11 +77,11 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
     const int64_t q0 = KV ? tl.other : tl.first, k0 = KV ? tl.first : tl.other;
     const int64_t rows = KV ? tl.n * a.group : tl.rows, states = KV ? tl.rows : tl.n;
     const Piece walk = piece_of(KV ? rows : states, split, splits);
-    const int n_tiles = int((walk.hi - walk.lo + kRows - 1) / kRows);
+    const int n_tiles = uniform(int((walk.hi - walk.lo + kRows - 1) / kRows));
     const int own = int(min(tl.rows - tl.row0, int64_t(kRows)));  // rows of the resident tile
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t sb = smem_u32(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sb = uniform(smem_u32(smem));
+    const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int d16 = (a.D + 15) / 16, half = L.stages / 2;
     const uint32_t r_full = sb + L.bars(), s_full = r_full + 8, dp_full = s_full + 8, p_ready = dp_full + 8, ds_ready = p_ready + 8,
                    done = ds_ready + 8, fin = done + 8, full = fin + 8, empty = full + 8 * L.stages, aux_full = empty + 8 * L.stages;
@@ -107,7 +107,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
+    const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t*>(&s_tmem));
     const uint32_t t_dp = tmem + kRows, t_g = tmem + 2 * kRows;  // sums: dq, or dk then dv
     volatile int* dead = &s_dead;
     unsigned* status = &attn_status_word;

@@ -255,11 +255,11 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
     const int h = blockIdx.y, split = blockIdx.z;
     const int64_t q0 = tl.first, k0 = tl.other;
     const Piece kr = piece_of(tl.n, split, a.splits);
-    const int n_tiles = int((kr.hi - kr.lo + F::kState - 1) / F::kState);
-    const int n_rows = int(min(tl.rows - tl.row0, int64_t(kRows)));
+    const int n_tiles = uniform(int((kr.hi - kr.lo + F::kState - 1) / F::kState));
+    const int n_rows = uniform(int(min(tl.rows - tl.row0, int64_t(kRows))));
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t sb = smem_u32(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sb = uniform(smem_u32(smem));
+    const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t q_full = sb + F::kBars, s_full = q_full + 8, p_full = s_full + 8, o_full = p_full + 8, fin = o_full + 8,
                    pair = fin + 8, full = pair + 32, empty = full + 8 * F::kStages, m_full = empty + 8 * F::kStages;
     if (threadIdx.x == 0) {
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
+    const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t*>(&s_tmem));
     volatile int* dead = &s_dead;
     unsigned* status = &attn_status_word;
     float* biases = reinterpret_cast<float*>(smem + F::kMasks);
@@ -526,11 +526,11 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
     const int64_t q0 = KV ? tl.other : tl.first, k0 = KV ? tl.first : tl.other;
     const int64_t rows = KV ? tl.n * a.group : tl.rows, states = KV ? tl.rows : tl.n;
     const Piece walk = piece_of(KV ? rows : states, split, splits);
-    const int n_tiles = int((walk.hi - walk.lo + B::kWalk - 1) / B::kWalk);
+    const int n_tiles = uniform(int((walk.hi - walk.lo + B::kWalk - 1) / B::kWalk));
     const int own = int(min(tl.rows - tl.row0, int64_t(B::kOwn)));
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t sb = smem_u32(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sb = uniform(smem_u32(smem));
+    const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t r_full = sb + B::kBars, s_full = r_full + 8, dp_full = s_full + 8, p_ready = dp_full + 8, ds_ready = p_ready + 8,
                    done = ds_ready + 8, fin = done + 8, full = fin + 8, empty = full + 8 * B::kStages, aux_full = empty + 8 * B::kStages;
     if (threadIdx.x == 0) {
@@ -553,7 +553,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
+    const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t*>(&s_tmem));
     volatile int* dead = &s_dead;
     unsigned* status = &attn_status_word;
 

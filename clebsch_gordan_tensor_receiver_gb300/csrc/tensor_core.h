@@ -12,6 +12,11 @@ namespace tc {
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
 
+// A value that is the same in all lanes, as the compiler can see it too: addresses, loop bounds and descriptors
+// formed from it stay in uniform registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+__device__ __forceinline__ int uniform(int x) { return int(uniform(uint32_t(x))); }
+
 // ---------------------------------------------------------------------------------- barriers
 
 __device__ __forceinline__ void bar_init(uint32_t b, uint32_t n) {
@@ -34,15 +39,30 @@ __device__ __forceinline__ unsigned long long timer_ns() {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
+// The same, asleep for up to 20 us where the phase has not ended: a polling warp takes issue slots from
+// the others (a third of all instructions, before).
+__device__ __forceinline__ bool bar_sleep(uint32_t b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(b), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
 // Waits for the phase of `parity` to end.  False when another role has given up (*dead) or after
-// about two seconds, which sets *dead and the status word; the caller then leaves its loop.
+// about two seconds, which sets *dead and the status word; the caller then leaves its loop.  The global
+// timer is far away (a read costs as much as several matrix instructions), so it is looked at rarely.
 static __device__ __noinline__ bool bar_wait_slow(uint32_t b, uint32_t parity, volatile int* dead, unsigned* status) {
-    const unsigned long long t0 = timer_ns();
+    unsigned long long t0 = 0;
     for (;;) {
-        for (int i = 0; i < 32; ++i)
-            if (bar_test(b, parity)) return true;
-        if (*dead) return false;
-        if (timer_ns() - t0 > 2000000000ull) {
+        for (int i = 0; i < 64; ++i) {
+            if (bar_sleep(b, parity)) return true;
+            if (*dead) return false;
+        }
+        const unsigned long long now = timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > 2000000000ull) {
             *dead = 1;
             atomicOr(status, 1u);
             return false;
@@ -51,12 +71,17 @@ static __device__ __noinline__ bool bar_wait_slow(uint32_t b, uint32_t parity, v
 }
 // The last wait before a role returns what others still use: bounded, whatever *dead says.
 static __device__ __noinline__ void bar_wait_last(uint32_t b, uint32_t parity, unsigned* status) {
-    const unsigned long long t0 = timer_ns();
-    while (!bar_test(b, parity))
-        if (timer_ns() - t0 > 2000000000ull) {
+    unsigned long long t0 = 0;
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (bar_sleep(b, parity)) return;
+        const unsigned long long now = timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > 2000000000ull) {
             atomicOr(status, 1u);
             return;
         }
+    }
 }
 __device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity, volatile int* dead, unsigned* status) {
     return bar_test(b, parity) || bar_wait_slow(b, parity, dead, status);
