@@ -149,10 +149,6 @@ Choice choose(const AttnShape& s, int sms) {
     c.fwd = splits_for(rows_busy(128 * c.nt), s.max_k, 128, sms, true);
     c.dq = splits_for(rows_busy(c.R), s.max_k, 128, sms, false);
     c.dkv = splits_for(states_busy(c.R), s.max_q * group, 128, sms, false);
-    if (const int walk = c.planes ? plane_walk(s.head_dim) : 0) {  // sums in tensor memory: short walks
-        c.dq = std::max(c.dq, int((s.max_k + walk - 1) / walk));
-        c.dkv = std::max(c.dkv, int((s.max_q * group + walk - 1) / walk));
-    }
     return c;
 }
 
@@ -234,7 +230,9 @@ cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, 
     a.part_q = take(c.dq > 1 ? size_t(c.dq) * n_q * 4 : 0);
     a.part_kv = take(c.dkv > 1 ? 2 * size_t(c.dkv) * n_kv * 4 : 0);
     a.kv_tiles = want_kv ? state_tiles(s, c.R) : 0;
-    const int64_t q_tiles = want_q ? row_tiles(s, c.R) : 0;
+    a.q_tiles = want_q ? row_tiles(s, c.R) : 0;
+    a.q_first = s.max_k > s.max_q * a.group;
+    if ((a.kv_tiles + a.q_tiles) * a.Hkv > INT32_MAX) return cudaErrorInvalidConfiguration;
     const auto with_type = [&](auto f) {
         switch (s.dtype) {
             case UVU_F32: f(float{}); break;
@@ -247,7 +245,7 @@ cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, 
     cudaError_t e = cudaSuccess;
     if (c.planes) {
         e = launch_attn_planes(a, w, sms, st);
-        if (e == cudaSuccess) e = launch_attn_bwd_planes(a, w, q_tiles, st);
+        if (e == cudaSuccess) e = launch_attn_bwd_planes(a, w, st);
     } else {
         if (a.nq > 0)
             e = with_type([&](auto t) {
@@ -261,7 +259,7 @@ cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, 
                 const unsigned n = blocks((a.nq * a.Hq) << log2);
                 vec ? attn_delta<T, V><<<n, kThreads, 0, st>>>(a, log2) : attn_delta<T, 1><<<n, kThreads, 0, st>>>(a, log2);
             });
-        if (e == cudaSuccess) e = launch_attn_bwd_mma(s.dtype, a, q_tiles, st);
+        if (e == cudaSuccess) e = launch_attn_bwd_mma(s.dtype, a, st);
     }
     if (e != cudaSuccess) return e;
     return with_type([&](auto t) {

@@ -6,15 +6,17 @@
 //              R1  R2  X1  X2      S = R1 X1^T,  dP = R2 X2^T,  P = exp2(c S - lse),  dS = P (dP - delta)
 //     dq       Q   dO  K   V       dq += dS X1
 //     dk, dv   K   V   Q   dO      dk += dS X1,  dv += P X2      (S and dP transposed: lanes are states)
-// Both kinds of tile are in one launch, the longer dk, dv tiles first.  Two sweeps instead of one cost S and dP twice (seven products instead of five), but every sum stays
-// in one CTA's tensor memory: no atomics, and results that do not depend on timing.
+// Both kinds of tile are in one launch.  Two sweeps instead of one cost S and dP twice (seven products instead of five),
+// but every sum stays in one CTA's tensor memory: no atomics, and results that do not depend on timing.  An
+// accumulating instruction there loses about 2^-26 of the sum, so 2^15 rows lose 2^-15: below the 16-bit results' rounding.
 //
 // Tensor memory: S, dP (128 columns each), then the sums.  P and dS are written as 16-bit values over
 // the part of S and dP that the same thread has read.  Two warpgroups share a tile: warpgroup w takes
 // columns 64 w .. + 63 of each lane's row.  Order of the matrix instructions:
 //     S(0) dP(0) | dv += P(0) X2, S(1), dk += dS(0) X1, dP(1) | ...
 // so the tensor cores form dv(j) and S(j+1) while the threads turn dP(j) into dS(j), and dk(j) and
-// dP(j+1) while they turn S(j+1) into P(j+1).
+// dP(j+1) while they turn S(j+1) into P(j+1).  (A second S, to head dimension 64 where columns are left for it: 1757
+// against 1733 us for 16 heads of 64 at 4 x 4096 rows and states, forward and backward.)
 //
 // f16 keeps 2^8 P (undone in the epilogue and in dS): P of long rows would fall below the type's
 // smallest normal value, 2^-14.  bf16 has the exponent range of fp32 and needs no shift.
@@ -66,11 +68,11 @@ __device__ __forceinline__ void store_grad16(const float (&o)[16], float scale, 
 }
 
 template <typename T, int LG, bool ALIGNED, bool KV>
-__device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>& L, int64_t tile) {
+__device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>& L, int64_t tile, int h) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_dead;
     __shared__ uint32_t s_tmem;
-    const int h = blockIdx.y, split = blockIdx.z, splits = KV ? a.splits_kv : a.splits_q;
+    const int split = blockIdx.z, splits = KV ? a.splits_kv : a.splits_q;
     if (split >= splits) return;
     const AttnTile tl = KV ? attn_tile<kRows>(a.k_off, a.q_off, a.graphs, 1, tile) : attn_tile<kRows>(a.q_off, a.k_off, a.graphs, a.group, tile);
     if (tl.graph < 0) return;
@@ -378,14 +380,15 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
 
 template <typename T, int LG, bool ALIGNED>
 __global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(const __grid_constant__ AttnArgs a, BwdLayout<true> Lkv, BwdLayout<false> Lq) {
-    if (blockIdx.x < a.kv_tiles)
-        bwd_tile<T, LG, ALIGNED, true>(a, Lkv, blockIdx.x);
+    const BwdTile t = bwd_tile_of(a);
+    if (t.kv)
+        bwd_tile<T, LG, ALIGNED, true>(a, Lkv, t.tile, t.head);
     else
-        bwd_tile<T, LG, ALIGNED, false>(a, Lq, blockIdx.x - a.kv_tiles);
+        bwd_tile<T, LG, ALIGNED, false>(a, Lq, t.tile, t.head);
 }
 
 template <typename T>
-cudaError_t bwd(const AttnArgs& a, int64_t q_tiles, cudaStream_t st) {
+cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
     BwdLayout<true> kv;
     BwdLayout<false> q;
     kv.panels = q.panels = a.D > 64 ? 2 : 1;
@@ -398,15 +401,15 @@ cudaError_t bwd(const AttnArgs& a, int64_t q_tiles, cudaStream_t st) {
         const int smem = std::max(kv.total(), q.total());
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        k<<<dim3(unsigned(a.kv_tiles + q_tiles), unsigned(a.Hkv), unsigned(std::max(a.splits_kv, a.splits_q))), kBwdWarps * 32, smem, st>>>(a, kv, q);
+        k<<<bwd_grid(a), kBwdWarps * 32, smem, st>>>(a, kv, q);
         return cudaGetLastError();
     });
 }
 
 }  // namespace
 
-cudaError_t launch_attn_bwd_mma(uvu_dtype dtype, const AttnArgs& a, int64_t q_tiles, cudaStream_t st) {
-    return dtype == UVU_BF16 ? bwd<__nv_bfloat16>(a, q_tiles, st) : bwd<__half>(a, q_tiles, st);
+cudaError_t launch_attn_bwd_mma(uvu_dtype dtype, const AttnArgs& a, cudaStream_t st) {
+    return dtype == UVU_BF16 ? bwd<__nv_bfloat16>(a, st) : bwd<__half>(a, st);
 }
 
 cudaError_t attn_bwd_mma_status(unsigned* word, bool reset) { return read_status(word, reset); }

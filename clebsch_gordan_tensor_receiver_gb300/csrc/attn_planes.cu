@@ -13,9 +13,9 @@
 //     the tile, P0 X, P1 [X0 | X1] and P2 X0 land in columns by order of magnitude: the sums of the small terms
 //     are apart from the large ones, and the threads add them.
 //   - Tensor memory sums each tile afresh; the sums over tiles are fp32 registers (accumulating in tensor
-//     memory loses more than a rounded fp32 addition does, and long rows would show it).  Where the backward
-//     has no registers for that it sums in tensor memory, over walks of at most plane_walk() rows (about 4e-9 of the
-//     sum is lost per 16 rows), and the joining kernel adds the walks.
+//     memory loses about 2^-26 of the sum each time, and 3000 rows showed it).  Where the backward has no
+//     registers for that, tensor memory sums 512 rows, the small terms in columns of their own (or 64 rows, all in the
+//     same), and the threads add that to the gradient in memory.
 // Masks, splits and bounded waits as in the 16-bit kernels.
 #include "attn_mma.h"
 
@@ -211,10 +211,25 @@ __device__ __forceinline__ void add_columns(uint32_t a, float* acc) {
     }
 }
 
-// N columns from c0 on of a row of D fp32 values, times scale.
+// N columns from c0 on of a row of D fp32 values, times scale; `add`: to what this thread stored there before (as
+// reductions, which it does not wait for; one thread to an element, so their order is its own).
 template <int N>
-__device__ __forceinline__ void store_row(float* dst, const float* v, float scale, int c0, int D) {
-    if (D % 4 == 0 && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+__device__ __forceinline__ void store_row(float* dst, const float* v, float scale, int c0, int D, bool add = false) {
+    const bool vec = D % 4 == 0 && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
+    if (add) {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4)
+                if (c0 + i < D)
+                    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst + c0 + i), "f"(v[i] * scale),
+                                 "f"(v[i + 1] * scale), "f"(v[i + 2] * scale), "f"(v[i + 3] * scale)
+                                 : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (c0 + i < D) atomicAdd(dst + c0 + i, v[i] * scale);
+        }
+    } else if (vec) {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
             if (c0 + i < D)
@@ -491,14 +506,18 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
 // The walk, its order and the roles as in the 16-bit backward, in steps of 32 or 64 walked rows.  Tensor memory:
 // S with plane 0 of P over it, planes 1 and 2 of P, dP and the planes of dS likewise, then the sums.
 //   PS <= 32   one warpgroup, steps of 32, 256 columns of tensor memory and at most 98 KB: two CTAs an SM.  The sums
-//              stay in tensor memory over the walk, each step's small terms first.
+//              of 512 rows in tensor memory.
 //   PS = 64    two warpgroups, steps of 64 (the planes of two resident tiles leave room for four such stages).  The
-//              sums of one step: the leading terms in PS columns, the small ones in PS more; registers over the walk.
+//              sums of one step in tensor memory, the others in registers.
 //   PS = 128   two warpgroups, steps of 32, resident tiles of 64 rows (the instructions still take 128: the upper half
-//              reads whatever follows in shared memory, into lanes that nobody reads), sums in tensor memory.
+//              reads whatever follows in shared memory, into lanes that nobody reads).  The sums of 512 rows in tensor memory
+//              for dq; of 64 rows for dk and dv, whose small terms go to the columns of the leading ones, as tensor
+//              memory has no others (69 TFLOP/s forward and backward at 4 x 2048 rows, 4096 states, 4 heads; with dk and dv in
+//              two halves of 64 columns, which forms S and dP twice, 46).
+// A gradient's leading terms are in PS columns, its small ones in PS more.
 template <int PS, bool KV>
 struct BwdPlan {
-    static constexpr bool kHeld = PS != 64;  // sums held in tensor memory
+    static constexpr bool kHeld = PS != 64;  // sums of kFlush steps in tensor memory, else of one
     static constexpr int kGroups = PS <= 32 ? 1 : 2, kWarps = 4 * kGroups;
     static constexpr int kOwn = PS == 128 ? 64 : 128, kWalk = PS == 64 ? 64 : 32, kHalf = kWalk / kGroups;
     static constexpr int kOwnPanel = kOwn * 128, kPanel = kWalk * 128;
@@ -507,19 +526,20 @@ struct BwdPlan {
     static constexpr int kAuxBytes = (KV ? 2 : 1) * kWalk * 4;  // -lse and -delta of the step, or the states' bias
     static constexpr int kBars = kAux + kHalfRing * kAuxBytes, kTotal = kBars + 512 + 1024;
     static constexpr uint32_t kP1 = kWalk, kP2 = kP1 + kWalk / 2, kDp = 2 * kWalk, kD1 = kDp + kWalk, kD2 = kD1 + kWalk / 2, kG = 4 * kWalk;
-    static constexpr int kGrad = kHeld ? PS : 2 * PS;  // columns of a gradient's sums
+    static constexpr bool kTogether = PS == 128 && KV;
+    static constexpr int kFlush = (kTogether ? 64 : 512) / kWalk, kGrad = kTogether ? PS : 2 * PS;  // steps, columns of a gradient's sums
     static constexpr uint32_t kColumns = kG + 2 * kGrad <= 256 ? 256 : 512;
 };
 
 template <int PS, bool KV>
-__device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int64_t tile) {
+__device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int64_t tile, int h) {
     using B = BwdPlan<PS, KV>;
     constexpr int kCols = KV ? PS : PS / B::kGroups;  // columns of a gradient that a thread writes
     constexpr float kLog2e = 1.4426950408889634f;
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_dead;
     __shared__ uint32_t s_tmem;
-    const int h = blockIdx.y, split = blockIdx.z, splits = KV ? a.splits_kv : a.splits_q;
+    const int split = blockIdx.z, splits = KV ? a.splits_kv : a.splits_q;
     if (split >= splits) return;
     const AttnTile tl = KV ? attn_tile<B::kOwn>(a.k_off, a.q_off, a.graphs, 1, tile) : attn_tile<B::kOwn>(a.q_off, a.k_off, a.graphs, a.group, tile);
     if (tl.graph < 0) return;
@@ -578,17 +598,42 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
                 delta = -a.delta[rh];
             }
         }
-        // the sums of the step before: dk (warpgroup 0) or dv (1), or the warpgroup's part of dq; small terms first
-        const uint32_t g = base_t + B::kG + (KV ? w * B::kGrad : w * kCols);
+        const int64_t n = KV ? a.nk * a.Hkv : a.nq * a.Hq;
+        const int c0 = KV ? 0 : w * kCols;
+        // dk (0) or dv (1), or dq
+        auto gradient = [&](int which) {
+            if (splits > 1) return (KV ? a.part_kv : a.part_q) + ((KV && which ? splits + split : split) * n + rh) * a.D;
+            return static_cast<float*>(KV ? (which ? a.dv : a.dk) : a.dq) + rh * a.D;
+        };
+        auto columns = [&](int which) { return base_t + B::kG + (KV ? which * B::kGrad : w * kCols); };
         float acc[B::kHeld ? 1 : kCols];
         if constexpr (!B::kHeld) {
 #pragma unroll
             for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
         }
-        auto add_sums = [&]() {
+        // What tensor memory has summed before step j (all of it: its last product is complete), small terms first: into
+        // registers after every step, or into the gradient after kFlush.
+        auto take = [&](int which, int j) {
+            if (j == 0) return;
             if constexpr (!B::kHeld) {
-                add_columns<kCols>(g + PS, acc);
-                add_columns<kCols>(g, acc);
+                add_columns<kCols>(columns(which) + PS, acc);
+                add_columns<kCols>(columns(which), acc);
+            } else if (j % B::kFlush == 0 || j == n_tiles) {
+                const float scale = KV && which ? 1.f : a.scale;
+#pragma unroll 1
+                for (int b = 0; b < kCols / 16; ++b) {
+                    float o[16], small[16];
+                    __syncwarp();
+                    tmem_ld16(columns(which) + 16 * b, o);
+                    if constexpr (!B::kTogether) {
+                        tmem_ld16(columns(which) + PS + 16 * b, small);
+                        tmem_wait_ld(small);
+                    }
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = keep ? (B::kTogether ? o[i] : o[i] + small[i]) : 0.f;
+                    if (row < own) store_row<16>(gradient(which), o, scale, c0 + 16 * b, a.D, j > B::kFlush);
+                }
             }
         };
         const bool tail = (walk.hi - walk.lo) % B::kWalk != 0;
@@ -607,7 +652,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
             fence_after();
             float v[B::kHalf];
             if (work) {
-                if (KV && w == 1 && j > 0) add_sums();  // dv of the step before is complete when S of this one is
+                if (KV && (B::kGroups == 1 || w == 1)) take(1, j);  // dv of the step before is complete when S of this one is
                 load_columns(base_t + B::kHalf * w, v);
                 tmem_wait_ld(v);
                 if (biased) add_bias(v, s_lse);
@@ -624,7 +669,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
             if (!ok) break;
             fence_after();
             if (work) {
-                if ((!KV || w == 0) && j > 0) add_sums();  // dk, dq of the step before: complete when dP of this one is
+                if (!KV || w == 0) take(0, j);  // dk, dq of the step before: complete when dP of this one is
                 float y[B::kHalf];
                 load_columns(base_t + B::kDp + B::kHalf * w, y);
                 tmem_wait_ld(y);
@@ -642,34 +687,20 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
             fence_after();
         }
         if (ok && work) {
-            const int64_t n = KV ? a.nk * a.Hkv : a.nq * a.Hq;
             // dk, dv: warpgroup 0 and 1, or one after the other by the only one
 #pragma unroll 1
             for (int which = w; which < (KV ? 2 : w + 1); which += B::kGroups) {
-                float* dst = static_cast<float*>(KV ? (which ? a.dv : a.dk) : a.dq) + rh * a.D;
-                if (splits > 1) dst = (KV ? a.part_kv : a.part_q) + ((KV && which ? splits + split : split) * n + rh) * a.D;
-                const float scale = KV && which ? 1.f : a.scale;
-                const int c0 = KV ? 0 : w * kCols;
-                if constexpr (B::kHeld) {
-#pragma unroll 1
-                    for (int b = 0; b < kCols / 16; ++b) {
-                        float o[16];
-                        __syncwarp();
-                        if (n_tiles > 0) {
-                            tmem_ld16(base_t + B::kG + (KV ? which * B::kGrad : c0) + 16 * b, o);
-                            tmem_wait_ld(o);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = n_tiles > 0 && keep ? o[i] : 0.f;
-                        if (row < own) store_row<16>(dst, o, scale, c0 + 16 * b, a.D);
-                    }
-                } else {
-                    if (n_tiles > 0) add_sums();
+                const int at = KV ? which : 0;
+                take(at, n_tiles);
+                if constexpr (!B::kHeld) {
                     if (!keep) {
 #pragma unroll
                         for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
                     }
-                    if (row < own) store_row<kCols>(dst, acc, scale, c0, a.D);
+                    if (row < own) store_row<kCols>(gradient(at), acc, KV && at ? 1.f : a.scale, c0, a.D);
+                } else if (n_tiles == 0 && row < own) {
+                    const float none[16] = {};
+                    for (int b = 0; b < kCols / 16; ++b) store_row<16>(gradient(at), none, 0.f, c0 + 16 * b, a.D);
                 }
             }
         }
@@ -690,30 +721,27 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
                 six_products<PS>(lead, d, r, B::kOwnPanel, xs, B::kPanel, id_s);
                 mma_commit(lead, bar);
             };
-            // d = A X over the step's rows, A in planes at a0 (its warpgroups' halves apart), a1, a2; or d += A X where the sums are held
-            auto sum = [&](uint32_t d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t xs, bool first) {
+            // d = A X over the step's rows, or d += A X (not `fresh`), A in planes at a0 (its warpgroups' halves apart), a1, a2:
+            // P0 X0 into PS columns, the small terms into PS more
+            auto sum = [&](uint32_t d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t xs, bool fresh) {
                 auto block = [&](int q, int s) { return q == 0 ? a0 + block_column(s, B::kHalf) : (q == 1 ? a1 : a2) + 8 * s; };
-                if constexpr (B::kHeld) {
-                    constexpr int kPair[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
-                    bool add = !first;
 #pragma unroll
-                    for (int i = 0; i < 6; ++i)
-#pragma unroll
-                        for (int s = 0; s < B::kWalk / 16; ++s) {
-                            mma_ts(lead, d, block(kPair[i][0], s), desc_rows(xs, s, B::kPanel, kPair[i][1] * PS), id1, add);
-                            add = true;
-                        }
-                } else {
-#pragma unroll
-                    for (int s = 0; s < B::kWalk / 16; ++s) {
-                        mma_ts(lead, d, block(0, s), desc_rows(xs, s, B::kPanel), id2, s > 0);
-                        mma_ts(lead, d + PS, block(0, s), desc_rows(xs, s, B::kPanel, 2 * PS), id1, true);
-                        mma_ts(lead, d + PS, block(1, s), desc_rows(xs, s, B::kPanel), id1, true);
-                        mma_ts(lead, d + PS, block(1, s), desc_rows(xs, s, B::kPanel, PS), id1, true);
-                        mma_ts(lead, d + PS, block(2, s), desc_rows(xs, s, B::kPanel), id1, true);
+                for (int s = 0; s < B::kWalk / 16; ++s) {
+                    auto x = [&](int plane) { return desc_rows(xs, s, B::kPanel, plane * PS); };
+                    const uint32_t small = d + (B::kTogether ? 0 : PS);
+                    if constexpr (B::kTogether) {
+                        mma_ts(lead, d, block(0, s), x(0), id1, !fresh || s > 0);
+                        mma_ts(lead, d, block(0, s), x(1), id1, true);
+                    } else {
+                        mma_ts(lead, d, block(0, s), x(0), id2, !fresh || s > 0);  // [X0 | X1]
                     }
+                    mma_ts(lead, small, block(0, s), x(2), id1, true);
+                    mma_ts(lead, small, block(1, s), x(0), id1, true);
+                    mma_ts(lead, small, block(1, s), x(1), id1, true);
+                    mma_ts(lead, small, block(2, s), x(0), id1, true);
                 }
             };
+            auto fresh = [](int j) { return !B::kHeld || j % B::kFlush == 0; };
             bool ok = n_tiles > 0 && warp_wait(r_full, 0, dead, status) && wait_stage(0);
             if (ok) {
                 product(tmem, r1, stage(0), s_full);
@@ -728,7 +756,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
                 if (!ok) break;
                 fence_after();
                 if (KV) {
-                    sum(tmem + B::kG + B::kGrad, tmem, tmem + B::kP1, tmem + B::kP2, stage(2 * j + 1), j == 0);
+                    sum(tmem + B::kG + B::kGrad, tmem, tmem + B::kP1, tmem + B::kP2, stage(2 * j + 1), fresh(j));
                     mma_commit(lead, empty + 8 * ((2 * j + 1) % B::kStages));
                 }
                 if (j + 1 < n_tiles) {
@@ -739,7 +767,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
                 ok = warp_wait(ds_ready, j & 1, dead, status);
                 if (!ok) break;
                 fence_after();
-                sum(tmem + B::kG, tmem + B::kDp, tmem + B::kD1, tmem + B::kD2, stage(2 * j), j == 0);
+                sum(tmem + B::kG, tmem + B::kDp, tmem + B::kD1, tmem + B::kD2, stage(2 * j), fresh(j));
                 mma_commit(lead, empty + 8 * ((2 * j) % B::kStages));
                 if (j + 1 < n_tiles) {
                     ok = wait_stage(2 * j + 3);
@@ -849,10 +877,11 @@ constexpr int kBwdThreads = (BwdPlan<PS, true>::kWarps + 1 + kLoadWarps) * 32;
 template <int PS>
 __global__ void __launch_bounds__(kBwdThreads<PS>, BwdPlan<PS, true>::kColumns == 256 ? 2 : 1)
     attn_bwd_planes(const __grid_constant__ AttnArgs a, Planes x) {
-    if (blockIdx.x < a.kv_tiles)
-        bwd_tile<PS, true>(a, x, blockIdx.x);
+    const BwdTile t = bwd_tile_of(a);
+    if (t.kv)
+        bwd_tile<PS, true>(a, x, t.tile, t.head);
     else
-        bwd_tile<PS, false>(a, x, blockIdx.x - a.kv_tiles);
+        bwd_tile<PS, false>(a, x, t.tile, t.head);
 }
 
 template <typename F>
@@ -921,15 +950,14 @@ cudaError_t launch_attn_fwd_planes(const AttnArgs& a, void* ws, int64_t row_tile
     });
 }
 
-cudaError_t launch_attn_bwd_planes(const AttnArgs& a, void* ws, int64_t q_tiles, cudaStream_t st) {
+cudaError_t launch_attn_bwd_planes(const AttnArgs& a, void* ws, cudaStream_t st) {
     const Planes x = planes_at(a, ws);
     return by_plane(a.D, [&](auto ps) {
         constexpr int PS = decltype(ps)::value;
         constexpr int smem = std::max(BwdPlan<PS, true>::kTotal, BwdPlan<PS, false>::kTotal);
         cudaError_t e = cudaFuncSetAttribute(attn_bwd_planes<PS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        attn_bwd_planes<PS><<<dim3(unsigned(a.kv_tiles + q_tiles), unsigned(a.Hkv), unsigned(std::max(a.splits_kv, a.splits_q))),
-                              kBwdThreads<PS>, smem, st>>>(a, x);
+        attn_bwd_planes<PS><<<bwd_grid(a), kBwdThreads<PS>, smem, st>>>(a, x);
         return cudaGetLastError();
     });
 }

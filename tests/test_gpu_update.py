@@ -338,6 +338,33 @@ def test_attention_gradient_against_differences(kind):
         assert abs(want - have) <= 2e-4 * (1 + abs(want)), (n, want, have)
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_attention_long_walks(kind, d):
+    """Many tiles in both directions, where the roles of a block run ahead of one another: no wait gives up, and rows and
+    states picked at random agree with the oracle."""
+    nq, nk, hq, hk = 3100, 2900, 4, 2
+    P, keep, at, qo, ko = attn_problem(([nq, nq], [nk, nk], hq, hk, d, 0.9), kind)
+    uvu.Attention.device_status()
+    got = attn_run(at, *(P[n][0] for n in ("q", "k", "v", "do")), keep, kind)
+    torch.cuda.synchronize()
+    assert uvu.Attention.device_status() == 0
+    q, k, v, do = (P[n][1] for n in ("q", "k", "v", "do"))
+    rows = np.sort(np.random.default_rng(3).choice(nq, 40, replace=False))
+    out, lse, mag = update.attention(q[rows], k[:nk], v[:nk], [0, 40], [0, nk], at.scale, keep[:nk])
+    grads, err = update.attention_vjp(q[rows], k[:nk], v[:nk], [0, 40], [0, nk], at.scale, do[rows], keep[:nk], UNIT[kind])
+    at_rows = torch.from_numpy(rows).cuda()
+    near(got[0][at_rows], out, kind, 2 * UNIT[kind] * mag, "out")
+    near(got[1][at_rows], lse, "f32", what="lse")
+    near(got[2][at_rows], grads[0], kind, err[0], "dq")
+    # dk and dv of the second graph, one kv head, from all of its rows
+    second = slice(nq, 2 * nq)
+    grads, err = update.attention_vjp(q[second, :2], k[nk:, :1], v[nk:, :1], [0, nq], [0, nk], at.scale, do[second, :2], keep[nk:],
+                                      UNIT[kind])
+    for g, ref, e, name in ((got[3], grads[1], err[1], "dk"), (got[4], grads[2], err[2], "dv")):
+        near(g[nk:, :1], ref, kind, e, name)
+
+
 def test_attention_repeats_bit_for_bit():
     for kind in TYPES:
         P, keep, at, qo, ko = attn_problem(([300, 4], [700, 900], 8, 2, 64, 0.9), kind)
