@@ -297,11 +297,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
                     !warp_wait(empty + 8 * (i % L.stages), (i / L.stages - 1) & 1, dead, status))
                     return false;
                 const uint32_t dst = sb + uint32_t(L.ring() + (i % L.stages) * L.tile());
-                auto use = [&](int r) { return mask.has(r); };
-                if (mask.all())
-                    load_strided<ALIGNED, true>(dst, src, stride, map, use);
-                else
-                    load_strided<ALIGNED, false>(dst, src, stride, map, use);
+                load_states<ALIGNED>(dst, src, stride, map, mask);
                 arrive(full + 8 * (i % L.stages));
                 return true;
             };

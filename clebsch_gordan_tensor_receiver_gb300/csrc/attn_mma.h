@@ -34,16 +34,16 @@ cudaError_t read_status(unsigned* word, bool reset) {
 }
 
 constexpr int kRows = 128;      // rows of a row tile, states of a state tile
-constexpr int kLoadWarps = 2;
+constexpr int kLoadWarps = 2;   // where nothing else is said
 constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kLoadThreads = kLoadWarps * 32;
 
 // How the loader threads share a tile of ROWS rows: thread t takes 16-byte chunk t % 2^LG of the rows
 // t / 2^LG, + kStep, ...  2^LG is the power of two that holds the row's chunks.
-template <int LG, int ROWS = kRows>
+template <int LG, int ROWS_ = kRows, int THREADS = kLoadThreads>
 struct LoadMap {
-    static constexpr int kStep = kLoadThreads >> LG, kIters = ROWS / kStep;
+    static constexpr int ROWS = ROWS_, kStep = THREADS >> LG, kIters = ROWS / kStep;
     int row, chunk;
     uint32_t bytes;  // of the chunk that exist: the others are zeros
     bool on;         // the chunk is read by the matrix instructions
@@ -66,42 +66,39 @@ __device__ __forceinline__ void load_chunk(uint32_t to, const char* src, uint32_
     }
 }
 
-// A tile of rows with a constant stride, `src` the first (its chunk included); rows that `use` refuses are
-// zeros.  ALL: every row is used.
-template <bool ALIGNED, bool ALL, int LG, int ROWS, typename Use>
-__device__ __forceinline__ void load_strided(uint32_t dst, const char* src, int64_t stride, const LoadMap<LG, ROWS>& m, Use use) {
-    using M = LoadMap<LG, ROWS>;
+// A tile of rows, the thread's own `step` bytes apart from p on; those that use(i) refuses are zeros.  ALL: every row is used.
+template <bool ALIGNED, bool ALL, typename M, typename Use>
+__device__ __forceinline__ void load_rows(uint32_t dst, const char* p, int64_t step, const M& m, Use use) {
     if (!m.on) return;
     // rows kStep apart share their swizzle when kStep is a multiple of 8; at 4 it alternates
     const uint32_t even = dst + tile_offset(m.row, m.chunk), odd = dst + tile_offset(m.row + M::kStep, m.chunk) - uint32_t(M::kStep * 128);
-    const char* p = src + m.row * stride;
 #pragma unroll 8
     for (int i = 0; i < M::kIters; ++i) {
-        load_chunk<ALIGNED>((i & 1 ? odd : even) + uint32_t(i * M::kStep * 128), p, ALL || use(m.row + i * M::kStep) ? m.bytes : 0);
-        p += M::kStep * stride;
+        load_chunk<ALIGNED>((i & 1 ? odd : even) + uint32_t(i * M::kStep * 128), p, ALL || use(i) ? m.bytes : 0);
+        p += step;
     }
 }
 
 // Packed rows of a kv head's queries from r0 on: row r is query r / group, head r % group.  Rows from `rows` on are
 // zeros, or left alone (!ZERO: rows of the M side, whose lanes nobody reads).
-template <bool ALIGNED, bool ZERO, int LG, int ROWS>
+template <bool ALIGNED, bool ZERO, typename M>
 __device__ __forceinline__ void load_packed(uint32_t dst, const char* base, int64_t row, int64_t head, int group, int64_t r0, int rows,
-                                            const LoadMap<LG, ROWS>& m) {
-    using M = LoadMap<LG, ROWS>;
-    if (group == 1 && (ZERO || rows >= ROWS)) {
-        auto use = [&](int r) { return r < rows; };
-        if (rows >= ROWS)
-            load_strided<ALIGNED, true>(dst, base + r0 * row + m.chunk * 16, row, m, use);
-        else
-            load_strided<ALIGNED, false>(dst, base + r0 * row + m.chunk * 16, row, m, use);
-        return;
-    }
+                                            const M& m) {
     if (!m.on) return;
     // query and head of the thread's first row; later rows step by kStep without a division
-    const uint32_t g = uint32_t(group), dq = uint32_t(M::kStep) / g, dj = uint32_t(M::kStep) - dq * g;
-    const int64_t q0 = (r0 + m.row) / group;
+    const uint32_t g = uint32_t(group), dq = g == 1 ? uint32_t(M::kStep) : uint32_t(M::kStep) / g, dj = uint32_t(M::kStep) - dq * g;
+    const int64_t q0 = group == 1 ? r0 + m.row : (r0 + m.row) / group;
     uint32_t j = uint32_t(r0 + m.row - q0 * group);
     const char* p = base + q0 * row + int64_t(j) * head + m.chunk * 16;
+    // the group divides kStep (1, 2, 4 of 4 to 32): the thread's rows are all of one head, a constant stride apart
+    if (dj == 0 && (ZERO || rows >= M::ROWS)) {
+        auto use = [&](int i) { return m.row + i * M::kStep < rows; };
+        if (rows >= M::ROWS)
+            load_rows<ALIGNED, true>(dst, p, dq * row, m, use);
+        else
+            load_rows<ALIGNED, false>(dst, p, dq * row, m, use);
+        return;
+    }
     const int64_t step = dq * row + int64_t(dj) * head, wrap = row - int64_t(g) * head;
 #pragma unroll 4
     for (int i = 0; i < M::kIters; ++i) {
@@ -116,6 +113,30 @@ __device__ __forceinline__ void load_packed(uint32_t dst, const char* base, int6
         }
     }
 }
+
+// A thread's packed rows r, r + step, ... of a kv head, and where their statistics are ([queries][heads]; `first`: of the
+// first query's first head), without a division after the first row.
+struct RowWalk {
+    int64_t r, at, next_at;
+    uint32_t j, g, dj, step;
+    int heads;
+    __device__ __forceinline__ RowWalk(int64_t row, int group, int64_t first, int heads_, int step_) : r(row), g(group), step(step_), heads(heads_) {
+        const int64_t q = r / group;
+        j = uint32_t(r - q * group);
+        at = first + q * heads + j;
+        dj = step % g;
+        next_at = int64_t(step / g) * heads + dj;
+    }
+    __device__ __forceinline__ void next() {
+        r += step;
+        at += next_at;
+        j += dj;
+        if (j >= g) {
+            j -= g;
+            at += heads - int64_t(g);
+        }
+    }
+};
 
 __device__ __forceinline__ uint32_t tail_word(int64_t left, int w) {  // bits of the states that exist
     const int64_t n = left - 32 * w;
@@ -152,6 +173,24 @@ struct StateMask {
         for (int w = 0; w < kWords; ++w) a &= word[w];
         return a == 0xffffffffu;
     }
+    // The states row, row + STEP, ... (row < STEP) as the bits 0, 1, ... of a word.
+    template <int STEP>
+    __device__ __forceinline__ uint32_t every(int row) const {
+        static_assert(STEP >= 4 && STEP <= 64 && N / STEP <= 32, "fits one word");
+        constexpr int kWord = STEP < 32 ? 32 / STEP : 1;  // bits from a word
+        uint32_t mine = 0;
+#pragma unroll
+        for (int i = 0; i < (N + STEP - 1) / STEP; i += kWord) {
+            const int w = i * STEP / 32;
+            uint32_t x = (STEP == 64 && row >= 32 ? word[w + 1 < kWords ? w + 1 : w] : word[w]) >> (row & 31);
+            // groups of n bits STEP n apart join in pairs
+            if constexpr (STEP == 4) x &= 0x11111111u, x = (x | x >> 3) & 0x03030303u, x = (x | x >> 6) & 0x000f000fu, x = x | x >> 12;
+            if constexpr (STEP == 8) x &= 0x01010101u, x = (x | x >> 7) & 0x00030003u, x = x | x >> 14;
+            if constexpr (STEP == 16) x &= 0x00010001u, x = x | x >> 15;
+            mine |= (x & ((1u << kWord) - 1)) << i;
+        }
+        return mine;
+    }
     __device__ __forceinline__ bool has(int r) const {
         uint32_t x = word[0];
 #pragma unroll
@@ -161,11 +200,11 @@ struct StateMask {
 };
 
 // Writes 0 or -inf per state of the tile to `bias` (shared memory), by all loader threads.
-template <int N>
+template <int THREADS = kLoadThreads, int N>
 __device__ __forceinline__ void write_bias(float* bias, const StateMask<N>& m, int t) {
 #pragma unroll
-    for (int i = 0; i < (N + kLoadThreads - 1) / kLoadThreads; ++i) {
-        const int r = t + i * kLoadThreads;
+    for (int i = 0; i < (N + THREADS - 1) / THREADS; ++i) {
+        const int r = t + i * THREADS;
         if (r < N) bias[r] = m.has(r) ? 0.f : -INFINITY;
     }
 }
@@ -223,6 +262,16 @@ __device__ __forceinline__ void bwd_ds(float (&dp)[N], const float (&p)[N], F2 u
         const float2 x = (F2(p[2 * i], p[2 * i + 1]) * fma2(F2(dp[2 * i], dp[2 * i + 1]), u, add)).both();
         dp[2 * i] = x.x, dp[2 * i + 1] = x.y;
     }
+}
+
+// A tile of states with a constant stride, `src` the first (the thread's chunk included); those that take no part are zeros.
+template <bool ALIGNED, typename M>
+__device__ __forceinline__ void load_states(uint32_t dst, const char* src, int64_t stride, const M& m, const StateMask<M::ROWS>& mask) {
+    const uint32_t mine = mask.template every<M::kStep>(m.row);
+    if (mask.all())
+        load_rows<ALIGNED, true>(dst, src + m.row * stride, M::kStep * stride, m, [](int) { return true; });
+    else
+        load_rows<ALIGNED, false>(dst, src + m.row * stride, M::kStep * stride, m, [&](int i) { return (mine >> i) & 1; });
 }
 
 struct Piece {

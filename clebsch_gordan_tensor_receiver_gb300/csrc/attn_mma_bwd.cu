@@ -36,7 +36,9 @@ struct BwdLayout {
     __host__ __device__ int total() const { return bars() + 256 + 1024; }  // + alignment slack
 };
 
-constexpr int kBwdWarps = 8 + 1 + kLoadWarps;
+// Four warps that load: with two, dk and dv of 16 heads of 64 at 4 x 4096 rows and states took 792 us instead of 723 (and the
+// forward, whose softmax needs the registers, 720 instead of 400 with four).
+constexpr int kBwdLoad = 4 * 32, kBwdWarps = 8 + 1 + kBwdLoad / 32;
 
 // 16 columns of a gradient row, times `scale`, to a partial or final row of D values.
 template <typename T>
@@ -91,7 +93,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
     const uint32_t tmem_cols = 512;
     if (threadIdx.x == 0) {
         s_dead = 0;
-        bar_init(r_full, kLoadThreads);
+        bar_init(r_full, kBwdLoad);
         bar_init(s_full, 1);
         bar_init(dp_full, 1);
         bar_init(p_ready, 8);
@@ -99,10 +101,10 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
         bar_init(done, 1);
         bar_init(fin, 1);
         for (int s = 0; s < L.stages; ++s) {
-            bar_init(full + 8 * s, kLoadThreads);
+            bar_init(full + 8 * s, kBwdLoad);
             bar_init(empty + 8 * s, 1);
         }
-        for (int s = 0; s < half; ++s) bar_init(aux_full + 8 * s, kLoadThreads);
+        for (int s = 0; s < half; ++s) bar_init(aux_full + 8 * s, kBwdLoad);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 8) tmem_alloc(smem_u32(&s_tmem), tmem_cols);
@@ -285,7 +287,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
     } else {
         // ------------------------------------------------------------------------- loaders
         const int t = threadIdx.x - 9 * 32;
-        const LoadMap<LG> map(t, a.D);
+        const LoadMap<LG, kRows, kBwdLoad> map(t, a.D);
         if (n_tiles > 0) {
             auto arrive = [&](uint32_t bar) { ALIGNED ? copy_arrive(bar) : bar_arrive(bar); };
             const char* Q = reinterpret_cast<const char*>(static_cast<const T*>(a.q) + q0 * a.q_row + int64_t(h) * a.group * a.q_head);
@@ -294,13 +296,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
             const char* K = reinterpret_cast<const char*>(static_cast<const T*>(a.k) + s0 * a.k_row + h * a.k_head) + map.chunk * 16;
             const char* V = reinterpret_cast<const char*>(static_cast<const T*>(a.v) + s0 * a.v_row + h * a.v_head) + map.chunk * 16;
             StateMask<> mask(a.keep ? a.keep + k0 : nullptr, KV ? tl.row0 : walk.lo, KV ? states : walk.hi);
-            auto states_tile = [&](uint32_t dst, const char* src, int64_t stride) {
-                auto use = [&](int r) { return mask.has(r); };
-                if (mask.all())
-                    load_strided<ALIGNED, true>(dst, src, stride, map, use);
-                else
-                    load_strided<ALIGNED, false>(dst, src, stride, map, use);
-            };
+            auto states_tile = [&](uint32_t dst, const char* src, int64_t stride) { load_states<ALIGNED>(dst, src, stride, map, mask); };
             auto rows_tile = [&](uint32_t dst, const char* base, int64_t row, int64_t head, int64_t r0, int n) {
                 load_packed<ALIGNED, KV>(dst, base, row * 2, head * 2, a.group, r0, n, map);
             };
@@ -318,20 +314,21 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
             }
             arrive(r_full);
             // lse and delta of the walked rows, fetched a tile ahead
-            float v_lse[2], v_delta[2];
-            auto fetch = [&](int j) {
+            constexpr int kEach = kRows / kBwdLoad;
+            float v_lse[kEach], v_delta[kEach];
+            RowWalk stats(walk.lo + t, a.group, q0 * a.Hq + int64_t(h) * a.group, a.Hq, kBwdLoad);
+            auto fetch = [&]() {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int64_t r = walk.lo + int64_t(j) * kRows + t + 64 * i;
+                for (int i = 0; i < kEach; ++i) {
                     v_lse[i] = -INFINITY, v_delta[i] = 0.f;
-                    if (r < walk.hi) {
-                        const int64_t q = r / a.group, at = (q0 + q) * a.Hq + int64_t(h) * a.group + (r - q * a.group);
-                        v_lse[i] = a.lse[at];
-                        v_delta[i] = a.delta[at];
+                    if (stats.r < walk.hi) {
+                        v_lse[i] = a.lse[stats.at];
+                        v_delta[i] = a.delta[stats.at];
                     }
+                    stats.next();
                 }
             };
-            if (KV) fetch(0);
+            if (KV) fetch();
             for (int j = 0; j < n_tiles; ++j) {
                 const int64_t lo = walk.lo + int64_t(j) * kRows;
                 const int n = int(min(walk.hi - lo, int64_t(kRows)));
@@ -340,13 +337,13 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                 if (KV) {
                     float* s_lse = reinterpret_cast<float*>(smem + L.aux() + (j % half) * L.aux_bytes());
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
+                    for (int i = 0; i < kEach; ++i) {
                         // rows past the end and rows without a kept state: P = exp2(s - inf) = 0
-                        s_lse[t + 64 * i] = v_lse[i] == -INFINITY ? -INFINITY : kShift - v_lse[i] * kLog2e;
-                        s_lse[kRows + t + 64 * i] = -v_delta[i] * kUnshift;
+                        s_lse[t + kBwdLoad * i] = v_lse[i] == -INFINITY ? -INFINITY : kShift - v_lse[i] * kLog2e;
+                        s_lse[kRows + t + kBwdLoad * i] = -v_delta[i] * kUnshift;
                     }
                     bar_arrive(aux_full + 8 * (j % half));
-                    if (j + 1 < n_tiles) fetch(j + 1);
+                    if (j + 1 < n_tiles) fetch();
                     rows_tile(stage(2 * j), Q, a.q_row, a.q_head, lo, n);
                     arrive(full + 8 * ((2 * j) % L.stages));
                     if (!free_stage(2 * j + 1)) break;
@@ -355,7 +352,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                 } else {
                     mask.next();
                     if (a.keep || n < kRows) {
-                        write_bias(reinterpret_cast<float*>(smem + L.aux() + (j % half) * L.aux_bytes()), mask, t);
+                        write_bias<kBwdLoad>(reinterpret_cast<float*>(smem + L.aux() + (j % half) * L.aux_bytes()), mask, t);
                         bar_arrive(aux_full + 8 * (j % half));
                     }
                     states_tile(stage(2 * j), K, a.k_row * 2);

@@ -127,18 +127,45 @@ struct Planes {
 template <int PS>
 constexpr int kPanels = (3 * PS + 63) / 64;
 
-// A tile of plane rows, panel by panel: ROWS rows with a constant stride (ALL: every row is used).
+// A tile of plane rows, all panels of a row together: the thread's rows are `step` bytes apart from p on (its chunk
+// included); those that use(i) refuses are zeros.  ALL: every row is used.
 template <int PS, int ROWS, bool ALL, typename Use>
-__device__ __forceinline__ void load_planes(uint32_t dst, const char* src, int64_t stride, int t, Use use) {
+__device__ __forceinline__ void load_plane_rows(uint32_t dst, const char* p, int64_t step, int t, Use use) {
+    constexpr int kLast = (3 * PS - 64 * (kPanels<PS> - 1)) / 8;  // chunks of the last panel
+    const uint32_t to = dst + tile_offset(t >> 3, t & 7);
+    const bool last = (t & 7) < kLast;
+#pragma unroll 4
+    for (int i = 0; i < ROWS / 8; ++i) {
+        const uint32_t bytes = ALL || use(i) ? 16 : 0;
 #pragma unroll
-    for (int p = 0; p < kPanels<PS>; ++p) {
-        const LoadMap<3, ROWS> m(t, 3 * PS - 64 * p < 64 ? 3 * PS - 64 * p : 64);
-        load_strided<true, ALL>(dst + p * ROWS * 128, src + p * 128 + m.chunk * 16, stride, m, use);
+        for (int k = 0; k < kPanels<PS>; ++k)
+            if (k + 1 < kPanels<PS> || last) copy16(to + uint32_t(i * 1024 + k * ROWS * 128), p + k * 128, bytes);
+        p += step;
     }
 }
+static_assert(kLoadThreads == 64, "eight rows of eight chunks a step");
+template <int PS, int ROWS>
+__device__ __forceinline__ void load_planes(uint32_t dst, const char* src, int64_t stride, int t, const StateMask<ROWS>& mask) {
+    const char* p = src + (t >> 3) * stride + (t & 7) * 16;
+    if (mask.all()) {
+        load_plane_rows<PS, ROWS, true>(dst, p, 8 * stride, t, [](int) { return true; });
+    } else {
+        const uint32_t mine = mask.template every<8>(t >> 3);
+        load_plane_rows<PS, ROWS, false>(dst, p, 8 * stride, t, [&](int i) { return (mine >> i) & 1; });
+    }
+}
+// Packed rows, as load_packed().
 template <int PS, int ROWS, bool ZERO>
 __device__ __forceinline__ void load_planes_packed(uint32_t dst, const char* base, int64_t row, int64_t head, int group, int64_t r0,
                                                    int rows, int t) {
+    if (group == 1 && (ZERO || rows >= ROWS)) {
+        const char* p = base + (r0 + (t >> 3)) * row + (t & 7) * 16;
+        if (rows >= ROWS)
+            load_plane_rows<PS, ROWS, true>(dst, p, 8 * row, t, [](int) { return true; });
+        else
+            load_plane_rows<PS, ROWS, false>(dst, p, 8 * row, t, [&](int i) { return (t >> 3) + 8 * i < rows; });
+        return;
+    }
 #pragma unroll
     for (int p = 0; p < kPanels<PS>; ++p) {
         const LoadMap<3, ROWS> m(t, 3 * PS - 64 * p < 64 ? 3 * PS - 64 * p : 64);
@@ -471,11 +498,7 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
                 if (i >= F::kStages && !warp_wait(empty + 8 * (i % F::kStages), (i / F::kStages - 1) & 1, dead, status))
                     return false;
                 const uint32_t dst = sb + uint32_t(F::kRing + (i % F::kStages) * F::kStep);
-                auto use = [&](int r) { return mask.has(r); };
-                if (mask.all())
-                    load_planes<PS, F::kState, true>(dst, src, stride, t, use);
-                else
-                    load_planes<PS, F::kState, false>(dst, src, stride, t, use);
+                load_planes<PS>(dst, src, stride, t, mask);
                 copy_arrive(full + 8 * (i % F::kStages));
                 return true;
             };
@@ -798,9 +821,8 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
             if (KV) {
                 StateMask<B::kOwn> mask(a.keep ? a.keep + k0 : nullptr, tl.row0, states);
                 mask.next();
-                auto use = [&](int r) { return mask.has(r); };
-                load_planes<PS, B::kOwn, false>(sb, K, k_row, t, use);
-                load_planes<PS, B::kOwn, false>(sb + uint32_t(B::kTile), V, k_row, t, use);
+                load_planes<PS>(sb, K, k_row, t, mask);
+                load_planes<PS>(sb + uint32_t(B::kTile), V, k_row, t, mask);
             } else {
                 load_planes_packed<PS, B::kOwn, false>(sb, Q, q_row, kHead, a.group, tl.row0, own, t);
                 load_planes_packed<PS, B::kOwn, false>(sb + uint32_t(B::kTile), dO, q_row, kHead, a.group, tl.row0, own, t);
@@ -808,16 +830,16 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
             copy_arrive(r_full);
             // lse and delta of the walked rows, fetched a step ahead
             float v_lse = -INFINITY, v_delta = 0.f;
-            auto fetch = [&](int j) {
-                const int64_t r = walk.lo + int64_t(j) * B::kWalk + t;
+            RowWalk stats(walk.lo + t, a.group, q0 * a.Hq + int64_t(h) * a.group, a.Hq, B::kWalk);
+            auto fetch = [&]() {
                 v_lse = -INFINITY, v_delta = 0.f;
-                if (t < B::kWalk && r < walk.hi) {
-                    const int64_t q = r / a.group, at = (q0 + q) * a.Hq + int64_t(h) * a.group + (r - q * a.group);
-                    v_lse = a.lse[at];
-                    v_delta = a.delta[at];
+                if (t < B::kWalk && stats.r < walk.hi) {
+                    v_lse = a.lse[stats.at];
+                    v_delta = a.delta[stats.at];
                 }
+                stats.next();
             };
-            if (KV) fetch(0);
+            if (KV) fetch();
             StateMask<B::kWalk> mask(!KV && a.keep ? a.keep + k0 : nullptr, walk.lo, walk.hi);
             for (int j = 0; j < n_tiles; ++j) {
                 const int64_t lo = walk.lo + int64_t(j) * B::kWalk;
@@ -832,7 +854,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
                         s_lse[B::kWalk + t] = -v_delta;
                     }
                     bar_arrive(aux_full + 8 * (j % B::kHalfRing));
-                    if (j + 1 < n_tiles) fetch(j + 1);
+                    if (j + 1 < n_tiles) fetch();
                     load_planes_packed<PS, B::kWalk, true>(stage(2 * j), Q, q_row, kHead, a.group, lo, n, t);
                     copy_arrive(full + 8 * ((2 * j) % B::kStages));
                     if (!free_stage(2 * j + 1)) break;
@@ -844,17 +866,10 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
                         write_bias(reinterpret_cast<float*>(smem + B::kAux + (j % B::kHalfRing) * B::kAuxBytes), mask, t);
                         bar_arrive(aux_full + 8 * (j % B::kHalfRing));
                     }
-                    auto use = [&](int r) { return mask.has(r); };
-                    auto load = [&](uint32_t dst, const char* src) {
-                        if (mask.all())
-                            load_planes<PS, B::kWalk, true>(dst, src, k_row, t, use);
-                        else
-                            load_planes<PS, B::kWalk, false>(dst, src, k_row, t, use);
-                    };
-                    load(stage(2 * j), K);
+                    load_planes<PS>(stage(2 * j), K, k_row, t, mask);
                     copy_arrive(full + 8 * ((2 * j) % B::kStages));
                     if (!free_stage(2 * j + 1)) break;
-                    load(stage(2 * j + 1), V);
+                    load_planes<PS>(stage(2 * j + 1), V, k_row, t, mask);
                     copy_arrive(full + 8 * ((2 * j + 1) % B::kStages));
                     K += B::kWalk * k_row;
                     V += B::kWalk * k_row;
