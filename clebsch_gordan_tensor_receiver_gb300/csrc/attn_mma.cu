@@ -231,46 +231,53 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
         {
             const uint32_t lead = elect_lane();
             const uint32_t id_s = mma_desc<T>(kRows, false), id_o = mma_desc<T>(16 * d16, true);
-            auto stage = [&](int i) { return sb + uint32_t(L.ring() + (i % L.stages) * L.tile()); };
-            auto wait_stage = [&](int i) { return warp_wait(full + 8 * (i % L.stages), (i / L.stages) & 1, dead, status); };
-            auto scores = [&](int t, int j) {
-                const uint32_t q = sb + uint32_t(t * L.tile()), k = stage(2 * j);
+            Ring ring(L.stages);
+            auto wait_stage = [&]() { return warp_wait(full + 8 * ring.at, ring.parity, dead, status); };
+            auto stage = [&]() { return sb + uint32_t(L.ring() + ring.at * L.tile()); };
+            auto scores = [&](int t, uint32_t k) {
+                const uint32_t q = sb + uint32_t(t * L.tile());
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
                     if (s < d16) mma_ss(lead, tmem + uint32_t(t * kRows), desc_cols(q, s), desc_cols(k, s), id_s, s > 0);
                 mma_commit(lead, s_full + 8 * t);
             };
-            bool ok = n_tiles > 0 && warp_wait(q_full, 0, dead, status) && wait_stage(0);
+            bool ok = n_tiles > 0 && warp_wait(q_full, 0, dead, status) && wait_stage();
             if (ok) {
                 fence_async();
-                for (int t = 0; t < nt; ++t) scores(t, 0);
+                for (int t = 0; t < nt; ++t) scores(t, stage());
                 mma_commit(lead, empty + 8 * 0);
+                ring.next();
             }
             for (int j = 0; j < n_tiles && ok; ++j) {
-                ok = wait_stage(2 * j + 1);
+                ok = wait_stage();
                 fence_async();
+                const int v_at = ring.at;
+                const uint32_t v = stage();
+                ring.next();
+                const uint32_t k = stage();
                 for (int t = 0; t < nt && ok; ++t) {
                     ok = warp_wait(p_full + 8 * t, j & 1, dead, status);
                     if (!ok) break;
                     fence_after();
-                    const uint32_t o = tmem + uint32_t(NT * kRows) + uint32_t(t) * o_cols, v = stage(2 * j + 1);
+                    const uint32_t o = tmem + uint32_t(NT * kRows) + uint32_t(t) * o_cols;
 #pragma unroll
                     for (int s = 0; s < kRows / 16; ++s)
                         mma_ts(lead, o, tmem + uint32_t(t * kRows + 8 * s), desc_rows(v, s), id_o, j > 0 || s > 0);
                     if (j + 1 < n_tiles) {
                         if (t == 0) {
-                            ok = wait_stage(2 * j + 2);
+                            ok = wait_stage();
                             if (!ok) break;
                             fence_async();
                         }
-                        scores(t, j + 1);
+                        scores(t, k);
                     } else {
                         mma_commit(lead, o_full + 8 * t);
                     }
                 }
                 if (!ok) break;
-                mma_commit(lead, empty + 8 * ((2 * j + 1) % L.stages));
-                if (j + 1 < n_tiles) mma_commit(lead, empty + 8 * ((2 * j + 2) % L.stages));
+                mma_commit(lead, empty + 8 * v_at);
+                if (j + 1 < n_tiles) mma_commit(lead, empty + 8 * ring.at);
+                ring.next();
             }
             // every instruction issued has finished before the tensor memory and the stages go
             mma_commit(lead, fin);
@@ -292,25 +299,25 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
             const char* K = reinterpret_cast<const char*>(static_cast<const T*>(a.k) + (k0 + kr.lo) * a.k_row + h * a.k_head) + map.chunk * 16;
             const char* V = reinterpret_cast<const char*>(static_cast<const T*>(a.v) + (k0 + kr.lo) * a.v_row + h * a.v_head) + map.chunk * 16;
             StateMask<> mask(a.keep ? a.keep + k0 : nullptr, kr.lo, kr.hi);
-            auto load = [&](int i, const char* src, int64_t stride) {
-                if (i >= L.stages &&
-                    !warp_wait(empty + 8 * (i % L.stages), (i / L.stages - 1) & 1, dead, status))
-                    return false;
-                const uint32_t dst = sb + uint32_t(L.ring() + (i % L.stages) * L.tile());
+            Ring ring(L.stages);
+            auto load = [&](const char* src, int64_t stride) {
+                if (ring.uses >= L.stages && !warp_wait(empty + 8 * ring.at, ring.parity ^ 1, dead, status)) return false;
+                const uint32_t dst = sb + uint32_t(L.ring() + ring.at * L.tile());
                 load_states<ALIGNED>(dst, src, stride, map, mask);
-                arrive(full + 8 * (i % L.stages));
+                arrive(full + 8 * ring.at);
+                ring.next();
                 return true;
             };
             for (int j = 0; j < n_tiles; ++j) {
                 mask.next();
-                if (!load(2 * j, K, a.k_row * 2)) break;
+                if (!load(K, a.k_row * 2)) break;
                 // the softmax warps read the tile's bias before its V stage is released, and K's stage comes half a ring
                 // later: kMaskRing biases cannot be overtaken
                 if (masked(j)) {
                     write_bias(biases + slot(j) * kRows, mask, map_t);
                     bar_arrive(m_full + 8 * slot(j));
                 }
-                if (!load(2 * j + 1, V, a.v_row * 2)) break;
+                if (!load(V, a.v_row * 2)) break;
                 K += kRows * a.k_row * 2;
                 V += kRows * a.v_row * 2;
             }

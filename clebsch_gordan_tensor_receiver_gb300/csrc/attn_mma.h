@@ -274,6 +274,18 @@ __device__ __forceinline__ void load_states(uint32_t dst, const char* src, int64
         load_rows<ALIGNED, false>(dst, src + m.row * stride, M::kStep * stride, m, [&](int i) { return (mine >> i) & 1; });
 }
 
+// The stages of a ring in the order of their uses, without a division (by a variable it costs as much as several matrix
+// instructions).
+struct Ring {
+    int n, at = 0, uses = 0;
+    uint32_t parity = 0;  // of the use's phase
+    __device__ __forceinline__ explicit Ring(int stages) : n(stages) {}
+    __device__ __forceinline__ void next() {
+        ++uses;
+        if (++at == n) at = 0, parity ^= 1;
+    }
+};
+
 struct Piece {
     int64_t lo, hi;
 };

@@ -27,7 +27,9 @@ namespace {
 
 template <bool KV>
 struct BwdLayout {
-    int panels, stages;
+    int panels, log_stages, stages;  // a power of two: a division by a variable costs the issuer as much as several instructions
+    __device__ int at(int i) const { return i & (stages - 1); }               // of the ring's use i: its stage,
+    __device__ uint32_t parity(int i) const { return (i >> log_stages) & 1; }  // its phase
     __host__ __device__ int tile() const { return panels * kPanelBytes; }
     __host__ __device__ int ring() const { return 2 * tile(); }
     __host__ __device__ int aux() const { return ring() + stages * tile(); }  // per walked tile: -lse and -delta, or the states' bias
@@ -143,12 +145,12 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
         const bool tail = (walk.hi - walk.lo) % kRows != 0;
         bool ok = true;
         for (int j = 0; j < n_tiles; ++j) {
-            const int ax = j % half;
+            const int ax = j & (half - 1);
             const float* s_lse = reinterpret_cast<const float*>(smem + L.aux() + ax * L.aux_bytes()) + col;  // or the bias
             const float* s_delta = s_lse + kRows;
             const bool biased = !KV && (a.keep || (tail && j == n_tiles - 1));
             if (KV || biased) {
-                ok = warp_wait(aux_full + 8 * ax, a.keep || KV ? (j / half) & 1 : 0, dead, status);
+                ok = warp_wait(aux_full + 8 * ax, a.keep || KV ? L.parity(2 * j) : 0, dead, status);
                 if (!ok) break;
             }
             ok = warp_wait(s_full, j & 1, dead, status);
@@ -225,9 +227,9 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
             const uint32_t lead = elect_lane();
             const uint32_t id_s = mma_desc<T>(kRows, false), id_g = mma_desc<T>(16 * d16, true);
             const uint32_t r1 = sb, r2 = sb + uint32_t(L.tile());
-            auto stage = [&](int i) { return sb + uint32_t(L.ring() + (i % L.stages) * L.tile()); };
+            auto stage = [&](int i) { return sb + uint32_t(L.ring() + L.at(i) * L.tile()); };
             auto wait_stage = [&](int i) {
-                if (!warp_wait(full + 8 * (i % L.stages), (i / L.stages) & 1, dead, status)) return false;
+                if (!warp_wait(full + 8 * L.at(i), L.parity(i), dead, status)) return false;
                 fence_async();
                 return true;
             };
@@ -258,7 +260,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                 fence_after();
                 if (KV) {
                     sum(t_g + g_cols, tmem, stage(2 * j + 1), j == 0);
-                    mma_commit(lead, empty + 8 * ((2 * j + 1) % L.stages));
+                    mma_commit(lead, empty + 8 * L.at(2 * j + 1));
                 }
                 if (j + 1 < n_tiles) {
                     ok = wait_stage(2 * j + 2);
@@ -269,12 +271,12 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                 if (!ok) break;
                 fence_after();
                 sum(t_g, t_dp, stage(2 * j), j == 0);
-                mma_commit(lead, empty + 8 * ((2 * j) % L.stages));
+                mma_commit(lead, empty + 8 * L.at(2 * j));
                 if (j + 1 < n_tiles) {
                     ok = wait_stage(2 * j + 3);
                     if (!ok) break;
                     product(t_dp, r2, stage(2 * j + 3), dp_full);
-                    if (!KV) mma_commit(lead, empty + 8 * ((2 * j + 3) % L.stages));
+                    if (!KV) mma_commit(lead, empty + 8 * L.at(2 * j + 3));
                 } else {
                     mma_commit(lead, done);
                 }
@@ -301,9 +303,9 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                 load_packed<ALIGNED, KV>(dst, base, row * 2, head * 2, a.group, r0, n, map);
             };
             auto free_stage = [&](int i) {
-                return i < L.stages || warp_wait(empty + 8 * (i % L.stages), (i / L.stages - 1) & 1, dead, status);
+                return i < L.stages || warp_wait(empty + 8 * L.at(i), L.parity(i - L.stages), dead, status);
             };
-            auto stage = [&](int i) { return sb + uint32_t(L.ring() + (i % L.stages) * L.tile()); };
+            auto stage = [&](int i) { return sb + uint32_t(L.ring() + L.at(i) * L.tile()); };
             if (KV) {
                 mask.next();
                 states_tile(sb, K, a.k_row * 2);
@@ -335,31 +337,31 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                 if (!free_stage(2 * j)) break;
                 // the tile that used this aux entry before gave up its X1 stage, which is this one
                 if (KV) {
-                    float* s_lse = reinterpret_cast<float*>(smem + L.aux() + (j % half) * L.aux_bytes());
+                    float* s_lse = reinterpret_cast<float*>(smem + L.aux() + (j & (half - 1)) * L.aux_bytes());
 #pragma unroll
                     for (int i = 0; i < kEach; ++i) {
                         // rows past the end and rows without a kept state: P = exp2(s - inf) = 0
                         s_lse[t + kBwdLoad * i] = v_lse[i] == -INFINITY ? -INFINITY : kShift - v_lse[i] * kLog2e;
                         s_lse[kRows + t + kBwdLoad * i] = -v_delta[i] * kUnshift;
                     }
-                    bar_arrive(aux_full + 8 * (j % half));
+                    bar_arrive(aux_full + 8 * (j & (half - 1)));
                     if (j + 1 < n_tiles) fetch();
                     rows_tile(stage(2 * j), Q, a.q_row, a.q_head, lo, n);
-                    arrive(full + 8 * ((2 * j) % L.stages));
+                    arrive(full + 8 * L.at(2 * j));
                     if (!free_stage(2 * j + 1)) break;
                     rows_tile(stage(2 * j + 1), dO, a.o_row, a.o_head, lo, n);
-                    arrive(full + 8 * ((2 * j + 1) % L.stages));
+                    arrive(full + 8 * L.at(2 * j + 1));
                 } else {
                     mask.next();
                     if (a.keep || n < kRows) {
-                        write_bias<kBwdLoad>(reinterpret_cast<float*>(smem + L.aux() + (j % half) * L.aux_bytes()), mask, t);
-                        bar_arrive(aux_full + 8 * (j % half));
+                        write_bias<kBwdLoad>(reinterpret_cast<float*>(smem + L.aux() + (j & (half - 1)) * L.aux_bytes()), mask, t);
+                        bar_arrive(aux_full + 8 * (j & (half - 1)));
                     }
                     states_tile(stage(2 * j), K, a.k_row * 2);
-                    arrive(full + 8 * ((2 * j) % L.stages));
+                    arrive(full + 8 * L.at(2 * j));
                     if (!free_stage(2 * j + 1)) break;
                     states_tile(stage(2 * j + 1), V, a.v_row * 2);
-                    arrive(full + 8 * ((2 * j + 1) % L.stages));
+                    arrive(full + 8 * L.at(2 * j + 1));
                     K += kRows * a.k_row * 2;
                     V += kRows * a.v_row * 2;
                 }
@@ -389,7 +391,8 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
     BwdLayout<true> kv;
     BwdLayout<false> q;
     kv.panels = q.panels = a.D > 64 ? 2 : 1;
-    kv.stages = q.stages = kv.panels == 1 ? 8 : 4;  // 160 or 192 KB
+    kv.log_stages = q.log_stages = kv.panels == 1 ? 3 : 2;  // 160 or 192 KB
+    kv.stages = q.stages = 1 << kv.log_stages;
     const uintptr_t any = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
                           reinterpret_cast<uintptr_t>(a.d_out) |
                           uintptr_t(a.q_row | a.q_head | a.k_row | a.k_head | a.v_row | a.v_head | a.o_row | a.o_head) * 2;
