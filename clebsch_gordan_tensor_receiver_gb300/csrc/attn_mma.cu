@@ -237,7 +237,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
             auto scores = [&](int t, uint32_t k) {
                 const uint32_t q = sb + uint32_t(t * L.tile());
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
+                for (int s = 0; s < 1 << (LG - 1); ++s)  // all of them, or fewer off the class's largest head dimension
                     if (s < d16) mma_ss(lead, tmem + uint32_t(t * kRows), desc_cols(q, s), desc_cols(k, s), id_s, s > 0);
                 mma_commit(lead, s_full + 8 * t);
             };

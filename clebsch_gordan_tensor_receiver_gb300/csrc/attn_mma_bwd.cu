@@ -235,7 +235,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
             };
             auto product = [&](uint32_t d, uint32_t r, uint32_t x, uint32_t bar) {
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
+                for (int s = 0; s < 1 << (LG - 1); ++s)  // all of them, or fewer off the class's largest head dimension
                     if (s < d16) mma_ss(lead, d, desc_cols(r, s), desc_cols(x, s), id_s, s > 0);
                 mma_commit(lead, bar);
             };
