@@ -15,7 +15,15 @@
 //
 // Order of the matrix instructions: ... O_0 += P_0 V_j, S_0 = Q_0 K_j+1, O_1 += P_1 V_j, S_1 = Q_1 K_j+1 ...
 // They complete in issue order, so S_t of the next tile may overwrite P_t, and a softmax thread that
-// has seen S_t(j+1) also knows that O_t(j) is complete.
+// has seen S_t(j+1) also knows that O_t(j) is complete.  The products with the first half of P begin while the
+// second half's exponentials are formed (1454 -> 1496 TFLOP/s at 4096 rows, 8192 states, 16 heads of 128, 4 graphs).
+//
+// Bound: the chain S - exponentials - O of a row tile.  Per tile of 128 x 128 the products take some 1020 clocks at head
+// dimension 128 (about 580 at 64) and the exponentials 512 (32 a clock and SM), and with two row tiles an SM one's
+// exponentials overlap the other's products, less the waits between the roles: 1760 clocks a tile at 128, 1490 at 64
+// (405 and 340 us for 16 heads, 4 x 4096 rows and states).  Tried and slower: steps of 64 states with two or three S
+// (848 -> 1050 us), two warpgroups a row tile.  P is rounded to 16 bits for its product with V, which takes 16-bit operands;
+// its sum l is of the unrounded values.  One token over long encodings is bound by memory: 64 pieces of the walk, 3580 GB/s.
 #include "attn_mma.h"
 
 namespace uvu {
@@ -32,7 +40,7 @@ struct FwdLayout {
     __host__ __device__ int ring() const { return NT * tile(); }
     __host__ __device__ int masks() const { return ring() + stages * tile(); }
     __host__ __device__ int bars() const { return masks() + masks_held * kRows * 4; }
-    __host__ __device__ int total() const { return bars() + 256 + 1024; }  // + alignment slack
+    __host__ __device__ int total() const { return bars() + 288 + 1024; }  // barriers, alignment slack
 };
 
 template <typename T, int NT, int LG, bool ALIGNED>
@@ -52,7 +60,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
     const uint32_t sb = uniform(smem_u32(smem));
     const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int d16 = (a.D + 15) / 16;
-    const uint32_t q_full = sb + L.bars(), s_full = q_full + 8, p_full = s_full + 16, o_full = p_full + 16, full = o_full + 16,
+    const uint32_t q_full = sb + L.bars(), s_full = q_full + 8, p_half = s_full + 16, p_full = p_half + 16, o_full = p_full + 16, full = o_full + 16,
                    empty = full + 8 * L.stages, m_full = empty + 8 * L.stages, fin = m_full + 8 * kMaskRing;
     const uint32_t o_cols = uint32_t(64 * L.panels);
     const uint32_t tmem_cols = NT == 2 ? 512 : 256;
@@ -61,6 +69,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
         bar_init(q_full, kLoadWarps * 32);
         for (int t = 0; t < 2; ++t) {
             bar_init(s_full + 8 * t, 1);
+            bar_init(p_half + 8 * t, 4);
             bar_init(p_full + 8 * t, 4);
             bar_init(o_full + 8 * t, 1);
         }
@@ -166,6 +175,12 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
 #pragma unroll
                         for (int i = 0; i < 16; ++i) p[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
                         tmem_st16(s_at + 16 * b, p);
+                        if (b == 1) {
+                            tmem_wait_st();
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0) bar_arrive(p_half + 8 * t);
+                        }
                     }
                     const float2 s2 = (sum[0] + sum[1]).both();
                     l += s2.x + s2.y;
@@ -173,7 +188,10 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
                 }
                 fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(p_full + 8 * t);
+                if (lane == 0) {
+                    if (!work) bar_arrive(p_half + 8 * t);
+                    bar_arrive(p_full + 8 * t);
+                }
             }
             if (ok && n_tiles > 0) {
                 ok = warp_wait(o_full + 8 * t, 0, dead, status);
@@ -256,13 +274,17 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
                 ring.next();
                 const uint32_t k = stage();
                 for (int t = 0; t < nt && ok; ++t) {
-                    ok = warp_wait(p_full + 8 * t, j & 1, dead, status);
-                    if (!ok) break;
-                    fence_after();
                     const uint32_t o = tmem + uint32_t(NT * kRows) + uint32_t(t) * o_cols;
 #pragma unroll
-                    for (int s = 0; s < kRows / 16; ++s)
-                        mma_ts(lead, o, tmem + uint32_t(t * kRows + 8 * s), desc_rows(v, s), id_o, j > 0 || s > 0);
+                    for (int half = 0; half < 2 && ok; ++half) {
+                        ok = warp_wait((half ? p_full : p_half) + 8 * t, j & 1, dead, status);
+                        if (!ok) break;
+                        fence_after();
+#pragma unroll
+                        for (int s = 4 * half; s < 4 * half + 4; ++s)
+                            mma_ts(lead, o, tmem + uint32_t(t * kRows + 8 * s), desc_rows(v, s), id_o, j > 0 || s > 0);
+                    }
+                    if (!ok) break;
                     if (j + 1 < n_tiles) {
                         if (t == 0) {
                             ok = wait_stage();
