@@ -112,14 +112,11 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_join(int64_t n, int splits,
 
 constexpr int kMaxSplits = 64;  // two weights per lane of the join
 
-// Splits of the inner axis.  Few tiles: as many pieces as fill the card's SMs once, but none shorter than
-// four tiles.  `deep` (the forward, whose pieces cost little to join): four times as many where pieces of eight tiles
-// are left, so that graphs of different lengths even out.
-int splits_for(int64_t tiles, int64_t inner, int R, int sms, bool deep) {
+// Splits of the inner axis.  Few tiles: as many pieces as fill the card's SMs once, but none shorter than four tiles
+// (8 rows over 16384 states, 32 heads of 128: 74 us, 162 unsplit; four times as many pieces 77).
+int splits_for(int64_t tiles, int64_t inner, int R, int sms) {
     if (tiles <= 0 || tiles >= sms) return 1;
-    const int64_t once = std::min((sms + tiles - 1) / tiles, std::max<int64_t>(1, inner / (4 * R)));
-    const int64_t four = deep ? std::min((4 * sms + tiles - 1) / tiles, std::max<int64_t>(1, inner / (8 * R))) : 1;
-    return int(std::min<int64_t>(std::max(once, four), kMaxSplits));
+    return int(std::min({(sms + tiles - 1) / tiles, std::max<int64_t>(1, inner / (4 * R)), int64_t(kMaxSplits)}));
 }
 
 int64_t row_tiles(const AttnShape& s, int R) { return s.n_q * (s.q_heads / s.kv_heads) / R + s.n_graphs; }
@@ -144,11 +141,14 @@ Choice choose(const AttnShape& s, int sms) {
     Choice c;
     c.planes = s.dtype == UVU_F32;
     c.R = c.planes ? plane_bwd_tile(s.head_dim) : 128;
+    // Two row tiles a block once they fill the SMs (K and V loaded once for 256 rows, one tile's exponentials under the
+    // other's products: 735 against 1207 us at 4 x 4096 rows, 8192 states, 16 heads of 128); below that one, which leaves no
+    // SM idle (16 graphs of 256 rows and 300 states, 2 heads of 128: 11.9 against 15.2 us).
     c.nt = !c.planes && rows_busy(256) >= sms && s.max_q * group > 128 ? 2 : 1;
     c.fwd_tiles = row_tiles(s, 128 * c.nt);
-    c.fwd = splits_for(rows_busy(128 * c.nt), s.max_k, 128, sms, true);
-    c.dq = splits_for(rows_busy(c.R), s.max_k, 128, sms, false);
-    c.dkv = splits_for(states_busy(c.R), s.max_q * group, 128, sms, false);
+    c.fwd = splits_for(rows_busy(128 * c.nt), s.max_k, 128, sms);
+    c.dq = splits_for(rows_busy(c.R), s.max_k, 128, sms);
+    c.dkv = splits_for(states_busy(c.R), s.max_q * group, 128, sms);
     return c;
 }
 

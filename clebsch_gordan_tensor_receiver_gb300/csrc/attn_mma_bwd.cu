@@ -18,6 +18,12 @@
 // dP(j+1) while they turn S(j+1) into P(j+1).  (A second S, to head dimension 64 where columns are left for it: 1757
 // against 1733 us for 16 heads of 64 at 4 x 4096 rows and states, forward and backward.)
 //
+// Measured, 16 heads at 4 x 4096 rows and states: dq 489 us, dk and dv 643 us at head dimension 64; 724 and 855 at 128 (a
+// third to a half of the tensor cores' time).  Bound: the threads' P and dS (64 exponentials a thread and step at 8 a clock
+// and quarter of an SM) and the hand-overs between them and the issuing warp, some 700 clocks each.  Half tiles handed over one
+// warpgroup at a time were slower (639 and 695 us at 64).
+//
+// P and dS are rounded to the operands' type for their products, which take no other; the sums are fp32.
 // f16 keeps 2^8 P (undone in the epilogue and in dS): P of long rows would fall below the type's
 // smallest normal value, 2^-14.  bf16 has the exponent range of fp32 and needs no shift.
 #include "attn_mma.h"

@@ -17,6 +17,10 @@
 //     registers for that, tensor memory sums 512 rows, the small terms in columns of their own (or 64 rows, all in the
 //     same), and the threads add that to the gradient in memory.
 // Masks, splits and bounded waits as in the 16-bit kernels.
+// Measured, forward and backward at 4 x 2048 rows and 4096 states, in TFLOP/s of the formula's products: 142 (4 heads of 64),
+// 103 (4 of 32), 67 (8 of 16), 70 (4 of 128); forward alone at 64 153.  Six products for one: the tensor cores' rate over
+// six would be 309.  Bound by the waits between the roles, and at small head dimensions by the least time of an
+// instruction, about 40 clocks however few its columns.
 #include "attn_mma.h"
 
 namespace uvu {
