@@ -112,11 +112,22 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_join(int64_t n, int splits,
 
 constexpr int kMaxSplits = 64;  // two weights per lane of the join
 
-// Splits of the inner axis.  Few tiles: as many pieces as fill the card's SMs once, but none shorter than four tiles
-// (8 rows over 16384 states, 32 heads of 128: 74 us, 162 unsplit; four times as many pieces 77).
-int splits_for(int64_t tiles, int64_t inner, int R, int sms) {
+// Pieces of the inner axis where the tiles are fewer than the SMs: the fewest that leave at most a tenth of the last wave of
+// `slots` blocks empty, within `waves` waves (or else the best of them), none shorter than four tiles.  The backward,
+// whose pieces cost fp32 sums to join, takes one wave.  Single
+// rows over 8 x 16384 states, 32/8 heads of 128: 101 us, 125 in the fewest pieces that give every SM one; 16 x 8192 states,
+// 8/2 heads of 64, two blocks an SM: 25 and 29 us; one sequence unsplit 162 against 72 us (8 ragged ones to 16384 states).
+int splits_for(int64_t tiles, int64_t inner, int R, int sms, int blocks_per_sm, int waves) {
     if (tiles <= 0 || tiles >= sms) return 1;
-    return int(std::min({(sms + tiles - 1) / tiles, std::max<int64_t>(1, inner / (4 * R)), int64_t(kMaxSplits)}));
+    const int64_t slots = int64_t(sms) * blocks_per_sm;
+    const int64_t most = std::min({inner / (4 * R), waves * slots / tiles, int64_t(kMaxSplits)});
+    int64_t best = 1;
+    double filled = 0.;
+    for (int64_t n = 1; n <= most && filled < .9; ++n) {
+        const int64_t full = (n * tiles + slots - 1) / slots * slots;
+        if (double(n * tiles) / double(full) > filled) best = n, filled = double(n * tiles) / double(full);
+    }
+    return int(best);
 }
 
 int64_t row_tiles(const AttnShape& s, int R) { return s.n_q * (s.q_heads / s.kv_heads) / R + s.n_graphs; }
@@ -146,9 +157,10 @@ Choice choose(const AttnShape& s, int sms) {
     // SM idle (16 graphs of 256 rows and 300 states, 2 heads of 128: 11.9 against 15.2 us).
     c.nt = !c.planes && rows_busy(256) >= sms && s.max_q * group > 128 ? 2 : 1;
     c.fwd_tiles = row_tiles(s, 128 * c.nt);
-    c.fwd = splits_for(rows_busy(128 * c.nt), s.max_k, 128, sms);
-    c.dq = splits_for(rows_busy(c.R), s.max_k, 128, sms);
-    c.dkv = splits_for(states_busy(c.R), s.max_q * group, 128, sms);
+    c.fwd = splits_for(rows_busy(128 * c.nt), s.max_k, 128, sms, c.nt == 1 && s.head_dim <= (c.planes ? 32 : 64) ? 2 : 1, 4);
+    const int bwd_blocks = c.planes && s.head_dim <= 32 ? 2 : 1;
+    c.dq = splits_for(rows_busy(c.R), s.max_k, 128, sms, bwd_blocks, 1);
+    c.dkv = splits_for(states_busy(c.R), s.max_q * group, 128, sms, bwd_blocks, 1);
     return c;
 }
 

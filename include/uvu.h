@@ -556,7 +556,10 @@ uvu_status uvu_dropout_bwd(uvu_dtype dtype, int64_t n_draws, int inner, double p
  * head_dim is 1 .. 128; q_heads is a multiple of kv_heads.  max_q, max_k: no graph has more rows or
  * states (the split of the work goes by them; wrong values cost time, not correctness).  scale > 0.
  * k_keep [n_k] bytes, or NULL: states with 0 take no part, whatever their k and v hold.  A row
- * without a kept state gets out = 0 and lse = -inf. */
+ * without a kept state gets out = 0 and lse = -inf.  A NaN or infinity in a kept operand gives NaN in the
+ * rows that it reaches.  16-bit operands: P (and dS in the backward) are rounded to their type for the
+ * products with v (k, q, d_out); everything else is fp32.  fp32 operands: products of fp32 accuracy on the tensor
+ * cores, from three bf16 terms a value. */
 typedef struct {
     uvu_dtype dtype;
     int32_t n_graphs;
