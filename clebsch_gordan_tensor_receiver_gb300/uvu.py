@@ -199,6 +199,17 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _workspace(need, device, stream=None):
+    """`need` bytes from torch's pool of the stream that the kernels run on.  The wrappers drop the
+    reference when they return: a block of another stream's pool could then be handed out again while
+    the kernels still use it."""
+    import torch
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=device)
+
+
 @dataclass
 class PlanInfo:
     mul: int
@@ -285,9 +296,8 @@ class Plan:
 
     def radial_weights(self, h, w_last, w, workspace=None, stream=None):
         """Materialised last layer w = h W_last (see uvu_radial_weights)."""
-        import torch
         if workspace is None:
-            workspace = torch.empty(max(16, self.radial_weights_workspace(h.shape[1])), dtype=torch.uint8, device=h.device)
+            workspace = _workspace(max(16, self.radial_weights_workspace(h.shape[1])), h.device, stream)
         uvu_radial_weights(self.handle, h.shape[0], _ptr(h), int(h.shape[1]), _ptr(w_last), _ptr(w), _ptr(workspace),
                            workspace.numel(), _stream(stream))
 
@@ -298,10 +308,9 @@ class Plan:
 
     def radial_weights_bwd(self, h, w_last, dw, dh=None, dw_last=None, workspace=None, stream=None):
         """dh = dw W_last^T and dW_last = h^T dw (see uvu_radial_weights_bwd)."""
-        import torch
         E, H = h.shape
         if workspace is None:
-            workspace = torch.empty(max(16, self.radial_weights_bwd_workspace(E, H)), dtype=torch.uint8, device=h.device)
+            workspace = _workspace(max(16, self.radial_weights_bwd_workspace(E, H)), h.device, stream)
         uvu_radial_weights_bwd(self.handle, E, _ptr(h), int(H), _ptr(w_last), _ptr(dw), _ptr(dh), _ptr(dw_last),
                                _ptr(workspace), workspace.numel(), _stream(stream))
 
@@ -313,11 +322,9 @@ class Plan:
 
     def radial_hidden_bwd(self, r, r_cut, p_env, widths, weights, dh, dr, dweights, workspace=None, stream=None):
         """Edge-length and layer gradients of <dh, h> (see uvu_radial_hidden_bwd)."""
-        import torch
         wd = (ctypes.c_int * len(widths))(*[int(v) for v in widths])
         if workspace is None:
-            workspace = torch.empty(max(16, self.radial_hidden_bwd_workspace(r.numel(), widths)), dtype=torch.uint8,
-                                    device=r.device)
+            workspace = _workspace(max(16, self.radial_hidden_bwd_workspace(r.numel(), widths)), r.device, stream)
         uvu_radial_hidden_bwd(self.handle, r.numel(), _ptr(r), float(r_cut), int(p_env), len(widths) - 1, wd,
                               _ptr(weights), _ptr(dh), _ptr(dr), _ptr(dweights), _ptr(workspace), workspace.numel(),
                               _stream(stream))
@@ -340,8 +347,7 @@ class Plan:
         need = self.tp_workspace_bytes(batch, w_shared) if dw is not None else 0
         if need:
             if workspace is None:
-                import torch
-                workspace = torch.empty(need, dtype=torch.uint8, device=d_out.device)
+                workspace = _workspace(need, d_out.device, stream)
             ws_ptr, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
         uvu_tp_bwd(self.handle, batch, _ptr(x), _ptr(y), _ptr(w), int(bool(w_shared)), _ptr(d_out),
                    _ptr(dx), _ptr(dy), _ptr(dw), ws_ptr, ws_bytes, _stream(stream))
@@ -372,28 +378,28 @@ class Plan:
         uvu_mix_workspace(self.handle, n_nodes, w_out, ctypes.byref(f), ctypes.byref(b))
         return f.value, b.value
 
-    def _mix_ws(self, n_nodes, w_out, bwd, workspace, device):
+    def _mix_ws(self, n_nodes, w_out, bwd, workspace, device, stream):
+        """(pointer, bytes, the tensor, which the caller holds until its launches are done)."""
         need = self.mix_workspace_bytes(n_nodes, w_out)[1 if bwd else 0]
         if workspace is None:
-            import torch
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-        return _ptr(workspace), workspace.numel() * workspace.element_size()
+            workspace = _workspace(max(need, 16), device, stream)
+        return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
 
     def mix_fwd(self, n_nodes, w_out, inp, M, out, workspace=None, stream=None):
         """Per-path channel mixing of a UVU output (see uvu_mix_fwd); `workspace` (uint8) is
         allocated here with torch if None."""
-        ws, nb = self._mix_ws(n_nodes, w_out, False, workspace, out.device)
+        ws, nb, held = self._mix_ws(n_nodes, w_out, False, workspace, out.device, stream)
         uvu_mix_fwd(self.handle, n_nodes, w_out, _ptr(inp), _ptr(M), _ptr(out), ws, nb, _stream(stream))
 
     def mix_bwd(self, n_nodes, w_out, inp, M, d_out, d_in=None, dM=None, workspace=None, stream=None):
         """VJP of mix_fwd (see uvu_mix_bwd)."""
-        ws, nb = self._mix_ws(n_nodes, w_out, True, workspace, d_out.device)
+        ws, nb, held = self._mix_ws(n_nodes, w_out, True, workspace, d_out.device, stream)
         uvu_mix_bwd(self.handle, n_nodes, w_out, _ptr(inp), _ptr(M), _ptr(d_out), _ptr(d_in), _ptr(dM),
                     ws, nb, _stream(stream))
 
     def uvw_fwd(self, n_nodes, x, Y, w, recv_offsets, src, M, w_out, uvu_out, out, workspace=None, stream=None):
         """Factorised UVW convolution (see uvu_conv_uvw_fwd)."""
-        ws, nb = self._mix_ws(n_nodes, w_out, False, workspace, out.device)
+        ws, nb, held = self._mix_ws(n_nodes, w_out, False, workspace, out.device, stream)
         uvu_conv_uvw_fwd(self.handle, n_nodes, src.numel(), _ptr(x), _ptr(Y), _ptr(w), _ptr(recv_offsets),
                          _ptr(src), _ptr(M), w_out, _ptr(uvu_out), _ptr(out), ws, nb, _stream(stream))
 
@@ -427,8 +433,7 @@ class Plan:
         if dx_mode == UVU_DX_STAGED and dx is not None:
             need = self.workspace_bytes(n_nodes, n_edges, dx_mode)
             if workspace is None:
-                import torch
-                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=src.device)
+                workspace = _workspace(max(need, 16), src.device, stream)
             ws_ptr, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
         uvu_conv_bwd(self.handle, n_nodes, n_edges, _ptr(x), _ptr(Y), _ptr(w),
                      _ptr(recv_offsets), _ptr(src), _ptr(send_offsets), _ptr(send_eids),
@@ -447,8 +452,7 @@ def _hvp_method(self, n_nodes, x, Y, w, recv_offsets, src, send_offsets, send_ei
         uvu_conv_hvp_workspace(self.handle, n_nodes, n_edges, ctypes.byref(b))
         if b.value:
             if workspace is None:
-                import torch
-                workspace = torch.empty(b.value, dtype=torch.uint8, device=src.device)
+                workspace = _workspace(b.value, src.device, stream)
             ws_ptr, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
     uvu_conv_hvp(self.handle, n_nodes, n_edges, _ptr(x), _ptr(Y), _ptr(w), _ptr(recv_offsets),
                  _ptr(src), _ptr(send_offsets), _ptr(send_eids), _ptr(d_out), _ptr(ax), _ptr(aY),
@@ -473,7 +477,7 @@ class Graph:
                                  _stream(stream))
         nb = ctypes.c_size_t()
         uvu_csr_transpose_workspace(n_nodes, self.n_edges, ctypes.byref(nb))
-        ws = torch.empty(max(nb.value, 16), dtype=torch.uint8, device=dev)
+        ws = _workspace(max(nb.value, 16), dev, stream)
         self.send_offsets = torch.empty(n_nodes + 1, dtype=torch.int32, device=dev)
         self.send_eids = torch.empty(max(self.n_edges, 1), dtype=torch.int32, device=dev)
         self.send_recv = torch.empty(max(self.n_edges, 1), dtype=torch.int32, device=dev)
@@ -534,13 +538,12 @@ def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device)
 
 
-def _scratch(need, workspace, device):
-    """(pointer, bytes) of a workspace: the caller's, or one from torch."""
+def _scratch(need, workspace, device, stream=None):
+    """(pointer, bytes, the tensor) of a workspace: the caller's, or one from torch."""
     if workspace is None:
         if need == 0:
             return None, 0, None
-        import torch
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _workspace(need, device, stream)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -575,7 +578,7 @@ def group_norm_fwd(x, gamma, beta, offsets, groups, y, mean, rstd, act=UVU_ACT_S
     _like("y", y, x)
     most = n if max_rows is None else max_rows
     need = group_norm_workspace_bytes(x, b, groups, most)[0] if workspace is None else 0
-    ws, size, held = _scratch(need, workspace, x.device)
+    ws, size, held = _scratch(need, workspace, x.device, stream)
     uvu_group_norm_fwd(code, n, b, most, c, groups, act, eps, offsets.data_ptr(), x.data_ptr(), gamma.data_ptr(),
                        beta.data_ptr(), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), ws, size, _raw_stream(stream, dev))
 
@@ -590,7 +593,7 @@ def group_norm_bwd(dy, x, gamma, beta, offsets, groups, mean, rstd, dx, dgamma, 
     _f32("dbeta", dbeta, (c,), dev)
     most = n if max_rows is None else max_rows
     need = group_norm_workspace_bytes(x, b, groups, most)[1] if workspace is None else 0
-    ws, size, held = _scratch(need, workspace, x.device)
+    ws, size, held = _scratch(need, workspace, x.device, stream)
     uvu_group_norm_bwd(code, n, b, most, c, groups, act, offsets.data_ptr(), x.data_ptr(), gamma.data_ptr(), beta.data_ptr(),
                        mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(), dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
                        ws, size, _raw_stream(stream, dev))
@@ -695,7 +698,7 @@ class Attention:
         s = self._shape(q, k, v, out)
         _block_dtype(lse)
         _f32("lse", lse, (s.n_q, self.q_heads), self.device)
-        ws, size, held = _scratch(self._need(s, 0) if workspace is None else 0, workspace, q.device)
+        ws, size, held = _scratch(self._need(s, 0) if workspace is None else 0, workspace, q.device, stream)
         uvu_attn_fwd(ctypes.byref(s), self.q_offsets.data_ptr(), self.k_offsets.data_ptr(), self._keep(keep, s.n_k), q.data_ptr(),
                      k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), ws, size, _raw_stream(stream, self.device))
 
@@ -709,7 +712,7 @@ class Attention:
         for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
             if t is not None:
                 _like(name, t, like)
-        ws, size, held = _scratch(self._need(s, 1) if workspace is None else 0, workspace, q.device)
+        ws, size, held = _scratch(self._need(s, 1) if workspace is None else 0, workspace, q.device, stream)
         uvu_attn_bwd(ctypes.byref(s), self.q_offsets.data_ptr(), self.k_offsets.data_ptr(), self._keep(keep, s.n_k), q.data_ptr(),
                      k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), d_out.data_ptr(), _at(dq), _at(dk), _at(dv), ws,
                      size, _raw_stream(stream, self.device))
