@@ -1151,11 +1151,12 @@ extern "C" uvu_status uvu_group_norm_fwd(uvu_dtype dtype, int64_t n_rows, int n_
     UVU_TRY(need_idx(offsets, "offsets"));
     UVU_TRY(need_elem(mean, UVU_F32, "mean"));
     UVU_TRY(need_elem(rstd, UVU_F32, "rstd"));
+    // the kernels read the parameters whatever the number of rows
+    UVU_TRY(need_elem(gamma, UVU_F32, "gamma"));
+    UVU_TRY(need_elem(beta, UVU_F32, "beta"));
     if (n_rows > 0) {
         UVU_TRY(need_elem(x, dtype, "x"));
         UVU_TRY(need_elem(y, dtype, "y"));
-        UVU_TRY(need_elem(gamma, UVU_F32, "gamma"));
-        UVU_TRY(need_elem(beta, UVU_F32, "beta"));
     }
     int sms = 0;
     UVU_TRY(sm_count_cached(&sms));

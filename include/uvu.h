@@ -506,7 +506,8 @@ typedef enum { UVU_ACT_NONE = 0, UVU_ACT_SILU = 1 } uvu_act;
  *     mean = sum x / m,   rstd = (sum (x - mean)^2 / m + eps)^(-1/2),
  *     y = act((x - mean) rstd gamma + beta),    UVU_ACT_SILU: act(z) = z / (1 + exp(-z)).
  * x, y [n_rows][channels] contiguous; gamma, beta [channels] fp32; mean, rstd [n_graphs][groups]
- * fp32, written for the backward (an empty graph: mean 0, rstd eps^(-1/2)).  channels is a multiple
+ * fp32, written for the backward (an empty graph: mean 0, rstd eps^(-1/2)).  x and y may be NULL
+ * where n_rows == 0, the others never.  channels is a multiple
  * of groups and at most 8192; eps > 0 or 0 with no constant group.  max_rows: no graph has more
  * rows (the choice of kernel goes by it; n_rows is always right, a smaller value than the longest
  * graph's costs time, not correctness).  y must not overlap x.  `workspace`: device memory of at
