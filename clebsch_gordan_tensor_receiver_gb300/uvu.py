@@ -506,6 +506,17 @@ def _block_dtype(t) -> int:
     return code
 
 
+def _device(t) -> int:
+    """The device number of a CUDA tensor on the current device, where the kernels are launched."""
+    d = t.get_device()
+    if d < 0:
+        raise TypeError("the node-update operators take CUDA tensors")
+    import torch
+    if d != torch.cuda.current_device():
+        raise ValueError(f"tensors are on device {d}, but the current device is {torch.cuda.current_device()}")
+    return d
+
+
 def _like(name, t, x):
     """t has x's type, device and shape and is contiguous."""
     if t.dtype != x.dtype or t.get_device() != x.get_device():
@@ -540,6 +551,8 @@ def _raw_stream(stream, device):
 
 def _scratch(need, workspace, device, stream=None):
     """(pointer, bytes, the tensor) of a workspace: the caller's, or one from torch."""
+    if workspace is not None and (workspace.get_device() != device or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous and on the operands' device")
     if workspace is None:
         if need == 0:
             return None, 0, None
@@ -557,7 +570,7 @@ def group_norm_workspace_bytes(x, n_graphs, groups, max_rows=None):
 
 
 def _norm_checks(x, gamma, beta, offsets, groups, mean, rstd):
-    code, dev = _block_dtype(x), x.get_device()
+    code, dev = _block_dtype(x), _device(x)
     if x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be contiguous [rows][channels]")
     n, c = x.shape
@@ -578,7 +591,7 @@ def group_norm_fwd(x, gamma, beta, offsets, groups, y, mean, rstd, act=UVU_ACT_S
     _like("y", y, x)
     most = n if max_rows is None else max_rows
     need = group_norm_workspace_bytes(x, b, groups, most)[0] if workspace is None else 0
-    ws, size, held = _scratch(need, workspace, x.device, stream)
+    ws, size, held = _scratch(need, workspace, dev, stream)
     uvu_group_norm_fwd(code, n, b, most, c, groups, act, eps, offsets.data_ptr(), x.data_ptr(), gamma.data_ptr(),
                        beta.data_ptr(), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), ws, size, _raw_stream(stream, dev))
 
@@ -593,7 +606,7 @@ def group_norm_bwd(dy, x, gamma, beta, offsets, groups, mean, rstd, dx, dgamma, 
     _f32("dbeta", dbeta, (c,), dev)
     most = n if max_rows is None else max_rows
     need = group_norm_workspace_bytes(x, b, groups, most)[1] if workspace is None else 0
-    ws, size, held = _scratch(need, workspace, x.device, stream)
+    ws, size, held = _scratch(need, workspace, dev, stream)
     uvu_group_norm_bwd(code, n, b, most, c, groups, act, offsets.data_ptr(), x.data_ptr(), gamma.data_ptr(), beta.data_ptr(),
                        mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(), dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
                        ws, size, _raw_stream(stream, dev))
@@ -609,24 +622,24 @@ def _draws(x, inner):
 def dropout_fwd(x, p, seed, y, offset=0, inner=1, residual=None, stream=None):
     """y = residual + dropout(x) with the mask of (seed, offset); `inner` consecutive values share a draw
     (see uvu_dropout_fwd).  All tensors contiguous and of one shape; y may be x or residual."""
-    code = _block_dtype(x)
+    code, dev = _block_dtype(x), _device(x)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     _like("y", y, x)
     if residual is not None:
         _like("residual", residual, x)
     uvu_dropout_fwd(code, _draws(x, inner), inner, p, seed, offset, x.data_ptr(), _at(residual), y.data_ptr(),
-                    _raw_stream(stream, x.get_device()))
+                    _raw_stream(stream, dev))
 
 
 def dropout_bwd(dy, p, seed, dx, offset=0, inner=1, stream=None):
     """VJP of dropout_fwd with respect to x; the residual's gradient is dy (see uvu_dropout_bwd)."""
-    code = _block_dtype(dy)
+    code, dev = _block_dtype(dy), _device(dy)
     if not dy.is_contiguous():
         raise ValueError("dy must be contiguous")
     _like("dx", dx, dy)
     uvu_dropout_bwd(code, _draws(dy, inner), inner, p, seed, offset, dy.data_ptr(), dx.data_ptr(),
-                    _raw_stream(stream, dy.get_device()))
+                    _raw_stream(stream, dev))
 
 
 class Attention:
@@ -636,7 +649,7 @@ class Attention:
     (default: all rows).  scale defaults to head_dim ** -0.5."""
 
     def __init__(self, q_heads, kv_heads, head_dim, q_offsets, k_offsets, max_q=None, max_k=None, scale=None):
-        self.device = q_offsets.get_device()
+        self.device = _device(q_offsets)
         self.n_graphs = _offsets("q_offsets", q_offsets, self.device)
         if _offsets("k_offsets", k_offsets, self.device) != self.n_graphs:
             raise ValueError("q_offsets and k_offsets must have the same number of graphs")
@@ -657,6 +670,7 @@ class Attention:
         return r, h
 
     def _shape(self, q, k, v, out):
+        _device(self.q_offsets)
         nq, nk, dt = q.shape[0], k.shape[0], q.dtype
         code = _block_dtype(q)
         qr, qh = self._operand("q", q, self.q_heads, nq, dt)
@@ -698,7 +712,7 @@ class Attention:
         s = self._shape(q, k, v, out)
         _block_dtype(lse)
         _f32("lse", lse, (s.n_q, self.q_heads), self.device)
-        ws, size, held = _scratch(self._need(s, 0) if workspace is None else 0, workspace, q.device, stream)
+        ws, size, held = _scratch(self._need(s, 0) if workspace is None else 0, workspace, self.device, stream)
         uvu_attn_fwd(ctypes.byref(s), self.q_offsets.data_ptr(), self.k_offsets.data_ptr(), self._keep(keep, s.n_k), q.data_ptr(),
                      k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), ws, size, _raw_stream(stream, self.device))
 
@@ -712,7 +726,7 @@ class Attention:
         for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
             if t is not None:
                 _like(name, t, like)
-        ws, size, held = _scratch(self._need(s, 1) if workspace is None else 0, workspace, q.device, stream)
+        ws, size, held = _scratch(self._need(s, 1) if workspace is None else 0, workspace, self.device, stream)
         uvu_attn_bwd(ctypes.byref(s), self.q_offsets.data_ptr(), self.k_offsets.data_ptr(), self._keep(keep, s.n_k), q.data_ptr(),
                      k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), d_out.data_ptr(), _at(dq), _at(dk), _at(dv), ws,
                      size, _raw_stream(stream, self.device))

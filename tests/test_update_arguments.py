@@ -1,9 +1,10 @@
 """Arguments of the node-update operators, checked before any launch: these tests need no GPU."""
-import ctypes
+import types
 
 import pytest
+import torch
 
-from clebsch_gordan_tensor_receiver_gb300 import uvu
+from clebsch_gordan_tensor_receiver_gb300 import autograd, uvu
 
 A = 4096  # a pointer that nothing may follow
 
@@ -21,3 +22,38 @@ def test_group_norm_without_parameters(missing, rows):
     gamma, beta = (None if missing == n else A for n in ("gamma", "beta"))
     status, text = refused(uvu.uvu_group_norm_fwd, uvu.UVU_F32, rows, 1, rows, 8, 2, 0, 1e-5, A, A, gamma, beta, A, A, A, None, 0, None)
     assert status == 1 and f"{missing} is NULL" in text
+
+
+def test_tensors_of_the_host():
+    """Tensors that agree with one another but lie in host memory."""
+    x, w, off = torch.zeros(4, 8), torch.ones(8), torch.tensor([0, 4], dtype=torch.int32)
+    m, q, lse = torch.zeros(1, 2), torch.zeros(4, 2, 8), torch.zeros(4, 2)
+    for f in (lambda: uvu.group_norm_fwd(x, w, w, off, 2, x.clone(), m, m.clone()),
+              lambda: uvu.group_norm_bwd(x, x, w, w, off, 2, m, m, x.clone(), w.clone(), w.clone()),
+              lambda: uvu.dropout_fwd(x, 0.1, 1, x.clone()),
+              lambda: uvu.dropout_bwd(x, 0.1, 1, x.clone()),
+              lambda: uvu.Attention(2, 2, 8, off, off).fwd(q, q, q, q.clone(), lse),
+              lambda: autograd.group_norm(x, w, w, off, 2),
+              lambda: autograd.dropout(x, 0.1, 1)):
+        with pytest.raises(TypeError, match="CUDA tensors"):
+            f()
+
+
+def test_tensors_of_another_device(monkeypatch):
+    """The kernels are launched on the current device."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    there = types.SimpleNamespace(get_device=lambda: 1)
+    with pytest.raises(ValueError, match="device 1"):
+        uvu._device(there)
+    here = types.SimpleNamespace(get_device=lambda: 0)
+    assert uvu._device(here) == 0
+
+
+def test_workspace_of_the_caller():
+    """A workspace in host memory, and one whose bytes are not all its own."""
+    host = torch.empty(64, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace"):
+        uvu._scratch(64, host, 0)
+    with pytest.raises(ValueError, match="workspace"):
+        uvu._scratch(64, host[:1].expand(64), -1)
+    assert uvu._scratch(64, host, -1)[:2] == (host.data_ptr(), 64)
