@@ -1269,8 +1269,7 @@ extern "C" uvu_status uvu_attn_bwd(const uvu_attn_shape* shape, const int32_t* q
     UVU_TRY(attn_check(shape));
     const uvu_attn_shape s = attn_clamped(*shape);
     if (!dk != !dv) return fail(UVU_ERR_INVALID_ARGUMENT, "dk and dv are computed together: both or neither");
-    if (!dq && !dk) return ok();
-    if (s.n_q == 0 && s.n_k == 0) return ok();
+    if (!(dq && s.n_q > 0) && !(dk && s.n_k > 0)) return ok();  // nothing to write
     UVU_TRY(need_idx(q_offsets, "q_offsets"));
     UVU_TRY(need_idx(k_offsets, "k_offsets"));
     if (s.n_q > 0) {

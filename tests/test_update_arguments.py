@@ -1,4 +1,5 @@
 """Arguments of the node-update operators, checked before any launch: these tests need no GPU."""
+import ctypes
 import types
 
 import pytest
@@ -57,3 +58,10 @@ def test_workspace_of_the_caller():
     with pytest.raises(ValueError, match="workspace"):
         uvu._scratch(64, host[:1].expand(64), -1)
     assert uvu._scratch(64, host, -1)[:2] == (host.data_ptr(), 64)
+
+
+@pytest.mark.parametrize("nq, nk, dq, dkv", [(0, 5, A, None), (5, 0, None, A), (0, 0, A, A), (0, 5, None, None)])
+def test_gradients_without_values(nq, nk, dq, dkv):
+    """Only gradients of no rows or no states are asked for, with pointers that are not NULL: nothing is launched."""
+    s = uvu.AttnShape(uvu.UVU_F32, 1, nq, nk, nq, nk, 1, 1, 8, 0, 1.0, 8, 8, 8, 8, 8, 8, 8, 8)
+    uvu.uvu_attn_bwd(ctypes.byref(s), *[A] * 9, dq, dkv, dkv, None, 0, None)
