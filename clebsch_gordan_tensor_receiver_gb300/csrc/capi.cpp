@@ -421,7 +421,9 @@ extern "C" uvu_status uvu_plan_device_status(uvu_plan_t plan, unsigned* word, in
     std::string err;
     uvu_status s = module_for_current_device(p, &m, &err);
     if (s != UVU_OK) return fail(s, err);
-    cudaError_t e = cudaMemcpy(word, m->status_word, sizeof(unsigned), cudaMemcpyDeviceToHost);
+    // a copy alone waits for the legacy stream, not for streams that do not block on it
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = cudaMemcpy(word, m->status_word, sizeof(unsigned), cudaMemcpyDeviceToHost);
     for (auto& a : m->aux) {  // the auxiliary modules' own words
         if (e != cudaSuccess || !a.status_word) continue;
         unsigned w2 = 0;
@@ -1216,7 +1218,8 @@ extern "C" uvu_status uvu_dropout_bwd(uvu_dtype dtype, int64_t n_draws, int inne
 extern "C" uvu_status uvu_attn_device_status(unsigned* word, int reset) {
     UVU_RANGE("uvu_attn_device_status");
     if (!word) return fail(UVU_ERR_INVALID_ARGUMENT, "word is NULL");
-    cudaError_t e = attn_status(word, reset != 0);
+    cudaError_t e = cudaDeviceSynchronize();  // streams that do not block on the legacy one, too
+    if (e == cudaSuccess) e = attn_status(word, reset != 0);
     if (e != cudaSuccess) return cuda_fail(e, "attention status");
     return ok();
 }
