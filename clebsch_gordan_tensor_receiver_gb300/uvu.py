@@ -659,7 +659,8 @@ class Attention:
         self.scale = float(head_dim) ** -0.5 if scale is None else float(scale)
 
     def _operand(self, name, t, heads, rows, dtype):
-        """Strides of [rows][heads][head_dim] with consecutive values in a head."""
+        """Strides of [rows][heads][head_dim] with consecutive values in a head; 0 for an axis of one, whose
+        stride torch leaves arbitrary."""
         if t.dtype != dtype or t.get_device() != self.device:
             raise TypeError(f"{name} must have q's type and be on the offsets' device")
         if t.shape != (rows, heads, self.head_dim):
@@ -667,7 +668,7 @@ class Attention:
         r, h, d = t.stride()
         if d != 1 and self.head_dim > 1:
             raise ValueError(f"{name} must have consecutive values in a head")
-        return r, h
+        return r if rows > 1 else 0, h if heads > 1 else 0
 
     def _shape(self, q, k, v, out):
         _device(self.q_offsets)

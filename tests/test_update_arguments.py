@@ -65,3 +65,17 @@ def test_gradients_without_values(nq, nk, dq, dkv):
     """Only gradients of no rows or no states are asked for, with pointers that are not NULL: nothing is launched."""
     s = uvu.AttnShape(uvu.UVU_F32, 1, nq, nk, nq, nk, 1, 1, 8, 0, 1.0, 8, 8, 8, 8, 8, 8, 8, 8)
     uvu.uvu_attn_bwd(ctypes.byref(s), *[A] * 9, dq, dkv, dkv, None, 0, None)
+
+
+@pytest.mark.parametrize("rows, heads", [(5, 1), (1, 5), (1, 1), (5, 3), (0, 3)])
+def test_strides_of_axes_of_one(rows, heads):
+    """A tensor and its transpose of transpose are the same operand; torch calls both contiguous."""
+    at = object.__new__(uvu.Attention)
+    at.device, at.head_dim = -1, 8
+    plain, turned = torch.zeros(rows, heads, 8), torch.zeros(heads, rows, 8).transpose(0, 1)
+    if min(rows, heads) < 2:
+        assert turned.is_contiguous() and at._operand("d_out", turned, heads, rows, plain.dtype) == \
+            at._operand("out", plain, heads, rows, plain.dtype)
+    else:
+        assert at._operand("out", plain, heads, rows, plain.dtype) == (24, 8)
+        assert at._operand("out", turned, heads, rows, plain.dtype) == (8, 40)
