@@ -80,24 +80,71 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_join(AttnArgs a) {
     }
 }
 
-// delta[row][head] = sum_d d_out out.  2^log2 lanes per (row, head), V columns at a time each.
+// delta[row][head] = sum_d d_out out.  2^log2 lanes per (row, head), V columns at a time each.  For f16 also do2, in a
+// second slice of the grid v2 (v's (state, kv head) in place of (row, head)), and the maxima are set to zero.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) attn_delta(AttnArgs a, int log2) {
+    constexpr bool kNorms = __is_same(T, __half);
     const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x, rh = i >> log2;
     const int lanes = 1 << log2, l = int(i) & (lanes - 1);
-    float s = 0.f;
-    if (rh < a.nq * a.Hq) {
-        const int64_t row = uint64_t(rh) < (1ull << 32) ? int64_t(uint32_t(rh) / uint32_t(a.Hq)) : rh / a.Hq;
-        const int64_t at = row * a.o_row + (rh - row * a.Hq) * a.o_head;
+    const bool of_v = kNorms && blockIdx.y == 1;
+    const int heads = of_v ? a.Hkv : a.Hq;
+    const int64_t row = uint64_t(rh) < (1ull << 32) ? int64_t(uint32_t(rh) / uint32_t(heads)) : rh / heads;
+    const bool on = row < (of_v ? a.nk : a.nq);
+    float s = 0.f, square = 0.f;
+    if (on && !(of_v && a.keep && !a.keep[row])) {
+        const int64_t head = rh - row * heads, at = of_v ? row * a.v_row + head * a.v_head : row * a.o_row + head * a.o_head;
         for (int d = l * V; d < a.D; d += lanes * V) {
-            const Vec<T, V> x = load_vec<T, V>(static_cast<const T*>(a.d_out) + at + d),
-                            y = load_vec<T, V>(static_cast<const T*>(a.out) + at + d);
+            const Vec<T, V> x = load_vec<T, V>(static_cast<const T*>(of_v ? a.v : a.d_out) + at + d);
+            if (!of_v) {
+                const Vec<T, V> y = load_vec<T, V>(static_cast<const T*>(a.out) + at + d);
 #pragma unroll
-            for (int k = 0; k < V; ++k) s = fmaf(widen(x.v[k]), widen(y.v[k]), s);
+                for (int k = 0; k < V; ++k) s = fmaf(widen(x.v[k]), widen(y.v[k]), s);
+            }
+            if constexpr (kNorms) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) square = fmaf(widen(x.v[k]), widen(x.v[k]), square);
+            }
         }
     }
-    for (int k = lanes >> 1; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    if (l == 0 && rh < a.nq * a.Hq) a.delta[rh] = s;
+    for (int k = lanes >> 1; k; k >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, k);
+        if constexpr (kNorms) square += __shfl_xor_sync(0xffffffffu, square, k);
+    }
+    if (l == 0 && on) {
+        if (!of_v) a.delta[rh] = s;
+        if constexpr (kNorms) (of_v ? a.v2 : a.do2)[rh] = square;
+    }
+    if constexpr (kNorms) {
+        unsigned* top = of_v ? a.v2_top : a.do2_top;
+        for (int64_t t = i; t < int64_t(a.graphs) * a.Hkv; t += int64_t(gridDim.x) * kThreads) top[t] = 0;
+    }
+}
+
+// do2_top and v2_top: a block takes the maximum of kTopRows packed rows (or states) of a graph and kv head.  The squares'
+// bits are ordered like unsigned numbers (a NaN's above all), and a maximum does not depend on the order of the blocks.
+constexpr int kTopRows = 2048;
+__global__ void __launch_bounds__(kThreads) attn_tops(AttnArgs a) {
+    __shared__ unsigned s_top;
+    const bool of_v = blockIdx.z == 1;
+    const int per = of_v ? 1 : a.group, h = blockIdx.y;
+    if (int64_t(blockIdx.x) >= (of_v ? a.nk : a.nq) * per / kTopRows + a.graphs) return;
+    if (threadIdx.x == 0) s_top = 0;
+    const AttnTile tl = of_v ? attn_tile<kTopRows>(a.k_off, a.q_off, a.graphs, 1, blockIdx.x)
+                             : attn_tile<kTopRows>(a.q_off, a.k_off, a.graphs, per, blockIdx.x);
+    if (tl.graph < 0) return;
+    const int n = int(min(int64_t(kTopRows), tl.rows - tl.row0));
+    const float* x = of_v ? a.v2 : a.do2;
+    unsigned top = 0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int64_t p = tl.row0 + i, r = per == 1 ? p : p / per;
+        top = max(top, __float_as_uint(x[((tl.first + r) * a.Hkv + h) * per + (p - r * per)]));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0) atomicMax(&s_top, top);
+    __syncthreads();
+    if (threadIdx.x == 0) atomicMax((of_v ? a.v2_top : a.do2_top) + int64_t(tl.graph) * a.Hkv + h, s_top);
 }
 
 // dst[i] = sum_s part[s][i], in the order of the splits.
@@ -166,6 +213,8 @@ Choice choose(const AttnShape& s, int sms) {
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
+size_t tops_bytes(const AttnShape& s) { return size_t(2) * s.n_graphs * s.kv_heads * 4; }  // do2_top and v2_top
+
 }  // namespace
 
 void attn_workspace(const AttnShape& s, int sms, size_t* fwd, size_t* bwd) {
@@ -175,6 +224,7 @@ void attn_workspace(const AttnShape& s, int sms, size_t* fwd, size_t* bwd) {
     if (c.planes) *fwd += attn_planes_bytes(s, false);
     const size_t dq = c.dq > 1 ? c.dq * qh * s.head_dim * 4 : 0, dkv = c.dkv > 1 ? 2 * c.dkv * kh * s.head_dim * 4 : 0;
     *bwd = align256(qh * 4) + align256(dq) + align256(dkv);
+    if (s.dtype == UVU_F16) *bwd += align256(qh * 4) + align256(kh * 4) + align256(tops_bytes(s));
     if (c.planes) *bwd += attn_planes_bytes(s, true);
 }
 
@@ -243,6 +293,12 @@ cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, 
     a.part_kv = take(c.dkv > 1 ? 2 * size_t(c.dkv) * n_kv * 4 : 0);
     a.kv_tiles = want_kv ? state_tiles(s, c.R) : 0;
     a.q_tiles = want_q ? row_tiles(s, c.R) : 0;
+    if (s.dtype == UVU_F16) {
+        a.do2 = take(size_t(a.nq) * a.Hq * 4);
+        a.v2 = take(size_t(a.nk) * a.Hkv * 4);
+        a.do2_top = reinterpret_cast<unsigned*>(take(tops_bytes(s)));
+        a.v2_top = a.do2_top + size_t(a.graphs) * a.Hkv;
+    }
     a.q_first = s.max_k > s.max_q * a.group;
     if ((a.kv_tiles + a.q_tiles) * a.Hkv > INT32_MAX) return cudaErrorInvalidConfiguration;
     const auto with_type = [&](auto f) {
@@ -259,17 +315,22 @@ cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, 
         e = launch_attn_planes(a, w, sms, st);
         if (e == cudaSuccess) e = launch_attn_bwd_planes(a, w, st);
     } else {
-        if (a.nq > 0)
+        if (a.nq > 0)  // without a row nothing needs delta or a scale
             e = with_type([&](auto t) {
                 using T = decltype(t);
                 constexpr int V = 16 / int(sizeof(T));
+                constexpr bool kNorms = __is_same(T, __half);
                 const uintptr_t any = reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.d_out) |
-                                      uintptr_t(a.o_row | a.o_head) * sizeof(T);
+                                      uintptr_t(a.o_row | a.o_head) * sizeof(T) |
+                                      (kNorms ? reinterpret_cast<uintptr_t>(a.v) | uintptr_t(a.v_row | a.v_head) * sizeof(T) : 0);
                 const bool vec = a.D % V == 0 && (any & 15u) == 0;
                 int log2 = 0;
                 while (log2 < 5 && (1 << log2) * (vec ? V : 1) < a.D) ++log2;
-                const unsigned n = blocks((a.nq * a.Hq) << log2);
+                const dim3 n(blocks((kNorms ? std::max(a.nq * a.Hq, a.nk * a.Hkv) : a.nq * a.Hq) << log2), kNorms ? 2 : 1);
                 vec ? attn_delta<T, V><<<n, kThreads, 0, st>>>(a, log2) : attn_delta<T, 1><<<n, kThreads, 0, st>>>(a, log2);
+                if (kNorms)
+                    attn_tops<<<dim3(unsigned(std::max(a.nq * a.group, a.nk) / kTopRows + a.graphs), unsigned(a.Hkv), 2), kThreads, 0,
+                                st>>>(a);
             });
         if (e == cudaSuccess) e = launch_attn_bwd_mma(s.dtype, a, st);
     }

@@ -23,6 +23,9 @@ struct AttnArgs {
     const void* d_out;
     void *dq, *dk, *dv;  // contiguous
     float* delta;        // [nq][Hq]: sum_d d_out out
+    // f16 operands: what the scale of dS follows (attn_mma_bwd.cu)
+    float *do2, *v2;             // [nq][Hq]: sum_d d_out^2; [nk][Hkv]: sum_d v^2 of kept states, else 0
+    unsigned *do2_top, *v2_top;  // [graphs][Hkv]: their maxima over a graph's rows and the kv head's heads, as bits
     // split over the long axis: partial results, joined by a second kernel (1: none)
     int splits;
     float* part_o;    // [splits][nq][Hq][D]

@@ -25,8 +25,13 @@
 //
 // P and dS are rounded to the operands' type for their products, which take no other; the sums are fp32.  delta comes from the rounded
 // output: d_q of a bf16 batch is off by 2.6e-3 (relative) where its own rounding gives 1.7e-3.
-// f16 keeps 2^8 P (undone in the epilogue and in dS): P of long rows would fall below the type's
-// smallest normal value, 2^-14.  bf16 has the exponent range of fp32 and needs no shift.
+// bf16 has the exponent range of fp32.  f16 does not, so its P and dS are held at a scale, undone in the epilogue:
+//   - 2^8 P (for dv): P of long rows would fall below the type's smallest normal value, 2^-14.
+//   - 2^e dS: |dS| <= 2 P |do| max_j |v_j| follows the cotangent's size.  e puts this bound at most at 2^15: nothing overflows, and
+//     dS keeps its bits down to 2^-29 of the bound.  A row of dq has its own |do|; dk sums over rows and takes the largest of
+//     the graph's rows and the kv head's heads.  Squares and maxima come with delta (attn.cu), for 2.5% of the backward: 8 graphs
+//     to 4096 rows, 16/4 heads of 64, 1045 -> 1073 us; 3 us of the smallest.  dq over 4096 states is off by 6.9e-4 with cotangents of
+//     size 1e-3 (its own rounding: 6.5e-4) and would be by 5.2e-3 with dS at no scale, since 2^-14 is far above it.
 #include "attn_mma.h"
 
 namespace uvu {
@@ -48,6 +53,16 @@ struct BwdLayout {
 // Four warps that load: with two, dk and dv of 16 heads of 64 at 4 x 4096 rows and states took 792 us instead of 723 (and the
 // forward, whose softmax needs the registers, 720 instead of 400 with four).
 constexpr int kBwdLoad = 4 * 32, kBwdWarps = 8 + 1 + kBwdLoad / 32;
+
+// e of the scale 2^e of dS: 2 |do| |v| 2^e <= 2^15, from the squares' product below 2^(x + 1).  Without a bound (an operand that
+// is not finite) or without a value the scale is 1.
+__device__ __forceinline__ int ds_exponent(float do2, float v2) {
+    const float b = do2 * v2;
+    if (!(b > 0.f) || b == INFINITY) return 0;
+    const int x = int(__float_as_uint(b) >> 23) - 127;
+    return 14 - ((x + 2) >> 1);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
 // 16 columns of a gradient row, times `scale`, to a partial or final row of D values.
 template <typename T>
@@ -124,7 +139,13 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
     const uint32_t t_dp = tmem + kRows, t_g = tmem + 2 * kRows;  // sums: dq, or dk then dv
     volatile int* dead = &s_dead;
     unsigned* status = &attn_status_word;
-    constexpr float kShift = __is_same(T, __half) ? 8.f : 0.f, kUnshift = __is_same(T, __half) ? 0.00390625f : 1.f;
+    constexpr bool kScaled = __is_same(T, __half);
+    constexpr float kShift = kScaled ? 8.f : 0.f, kUnshift = kScaled ? 0.00390625f : 1.f;
+    // the exponent of dS's scale: (2^8 P) (dP u - delta u) with u = 2^(e - 8) for dk, (2^e P) (dP - delta) for dq
+    auto exponent = [&](float do2) { return ds_exponent(do2, __uint_as_float(a.v2_top[int64_t(tl.graph) * a.Hkv + h])); };
+    auto tile_exponent = [&]() {  // of dk: the same for the whole tile
+        return kScaled && n_tiles > 0 ? exponent(__uint_as_float(a.do2_top[int64_t(tl.graph) * a.Hkv + h])) : 0;
+    };
     constexpr float kLog2e = 1.4426950408889634f;
 
     if (warp < 8) {
@@ -136,6 +157,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
         const int64_t p = tl.row0 + row;
         float lse = -INFINITY, delta = 0.f;  // minus the thread's row's (dq)
         int64_t rh = 0;
+        int e_ds = KV ? tile_exponent() : 0;
         bool keep = row < own;
         if (keep) {
             if (KV) {
@@ -144,11 +166,13 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
             } else {
                 rh = (q0 + p / a.group) * a.Hq + int64_t(h) * a.group + p % a.group;
                 const float x = a.lse[rh];
-                // a row without a kept state: P = exp2(s - inf) = 0
-                lse = x == -INFINITY ? -INFINITY : kShift - x * kLog2e;
-                delta = -a.delta[rh] * kUnshift;
+                if (kScaled) e_ds = exponent(a.do2[rh]);
+                // P is not stored here, so dS's scale is its own.  A row without a kept state: P = exp2(s - inf) = 0
+                lse = x == -INFINITY ? -INFINITY : float(e_ds) - x * kLog2e;
+                delta = -a.delta[rh];
             }
         }
+        const float u = KV ? kUnshift * power_of_two(e_ds) : 1.f;
         const bool tail = (walk.hi - walk.lo) % kRows != 0;
         bool ok = true;
         for (int j = 0; j < n_tiles; ++j) {
@@ -193,7 +217,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                     float y[32];
                     tmem_ld32(t_dp + lanes + col + 32 * b, y);
                     tmem_wait_ld(y);
-                    bwd_ds<KV>(y, x[b], F2(kUnshift, kUnshift), delta, s_delta + 32 * b);
+                    bwd_ds<KV>(y, x[b], F2(u, u), delta, s_delta + 32 * b);
                     uint32_t q[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) q[i] = pack2<T>(y[2 * i], y[2 * i + 1]);
@@ -215,7 +239,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
             T* dst = static_cast<T*>(KV ? (w ? a.dv : a.dk) : a.dq) + rh * a.D;
             float* part = splits > 1 ? (KV ? a.part_kv : a.part_q) + ((KV && w ? splits + split : split) * n + rh) * a.D : nullptr;
             const bool vec = a.D % 8 == 0 && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
-            const float scale = KV && w ? kUnshift : a.scale;
+            const float scale = KV && w ? kUnshift : a.scale * power_of_two(-e_ds);
             for (int d = KV ? 0 : w; d < d16; d += KV ? 1 : 2) {
                 float o[16];
                 __syncwarp();
@@ -338,6 +362,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                 }
             };
             if (KV) fetch();
+            const float u = KV ? kUnshift * power_of_two(tile_exponent()) : 1.f;
             for (int j = 0; j < n_tiles; ++j) {
                 const int64_t lo = walk.lo + int64_t(j) * kRows;
                 const int n = int(min(walk.hi - lo, int64_t(kRows)));
@@ -349,7 +374,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                     for (int i = 0; i < kEach; ++i) {
                         // rows past the end and rows without a kept state: P = exp2(s - inf) = 0
                         s_lse[t + kBwdLoad * i] = v_lse[i] == -INFINITY ? -INFINITY : kShift - v_lse[i] * kLog2e;
-                        s_lse[kRows + t + kBwdLoad * i] = -v_delta[i] * kUnshift;
+                        s_lse[kRows + t + kBwdLoad * i] = -v_delta[i] * u;
                     }
                     bar_arrive(aux_full + 8 * (j & (half - 1)));
                     if (j + 1 < n_tiles) fetch();

@@ -559,7 +559,8 @@ uvu_status uvu_dropout_bwd(uvu_dtype dtype, int64_t n_draws, int inner, double p
  * k_keep [n_k] bytes, or NULL: states with 0 take no part, whatever their k and v hold.  A row
  * without a kept state gets out = 0 and lse = -inf.  A NaN or infinity in a kept operand gives NaN in the
  * rows that it reaches.  16-bit operands: P (and dS in the backward) are rounded to their type for the
- * products with v (k, q, d_out); everything else is fp32.  fp32 operands: products of fp32 accuracy on the tensor
+ * products with v (k, q, d_out), in the backward of UVU_F16 at powers of two that follow the size of d_out and v, so that
+ * small cotangents keep their bits and large ones do not overflow; everything else is fp32.  fp32 operands: products of fp32 accuracy on the tensor
  * cores, from three bf16 terms a value. */
 typedef struct {
     uvu_dtype dtype;

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from clebsch_gordan_tensor_receiver_gb300 import autograd, uvu
+from oracle import update
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +31,87 @@ def test_gradient_of_a_heads_first_consumer(rows, heads, kind):
     got = torch.autograd.grad(autograd.cross_attention(q, k, v, at).transpose(0, 1), (q, k, v), g)
     want = torch.autograd.grad(autograd.cross_attention(q, k, v, at), (q, k, v), torch.empty_like(q).copy_(g.transpose(0, 1)))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------- small and large 16-bit cotangents
+
+def values(t):
+    return t.double().cpu().numpy()
+
+
+def relative(got, ref):
+    return float(np.linalg.norm(values(got) - ref) / np.linalg.norm(ref))
+
+
+def gradient_limit(ref, dtype):
+    """Of the relative Frobenius error of dq, dk or dv.  The result's own rounding, e0, is taken from the exact values (below a
+    type's smallest normal number it is more than u).  P or dS is rounded to the type for the product: u = 2^-p at most for each
+    term, some 0.4 u in the norm of a sum.  delta from the rounded output shifts a row's dS by at most another u |do| |out| P.
+    Together at most 1.25 e0 + 2 u, with room for fp32's 2^-20."""
+    u = 2.0 ** -11 if dtype == torch.float16 else 2.0 ** -8
+    t = torch.from_numpy(ref)
+    e0 = float((t.to(dtype).double() - t).norm() / t.norm())
+    return 1.25 * e0 + 2 * u
+
+
+def gradients(q, k, v, do, at, keep=None):
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    at.fwd(q, k, v, out, lse, keep=keep)
+    g = [torch.empty_like(t) for t in (q, k, v)]
+    at.bwd(q, k, v, out, lse, do, *g, keep=keep)
+    return g
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("size", [1.0, 1e-2, 1e-3, 1e-4])
+@pytest.mark.parametrize("states", [4096, 16384])
+def test_gradients_of_small_cotangents(states, size, kind):
+    """P (dP - delta) of many states and a small cotangent lies far below f16's smallest normal number."""
+    dtype, nq, off = TYPES[kind], 40, ([0, 40], [0, states])
+    at = uvu.Attention(2, 1, 64, i32(off[0]), i32(off[1]))
+    q, k, v = rand(1, nq, 2, 64, dtype=dtype), rand(2, states, 1, 64, dtype=dtype), rand(3, states, 1, 64, dtype=dtype)
+    do = (rand(4, nq, 2, 64) * size).to(dtype)
+    ref, _ = update.attention_vjp(*map(values, (q, k, v)), *off, at.scale, values(do))
+    for name, got, r in zip(("dq", "dk", "dv"), gradients(q, k, v, do, at), ref):
+        assert relative(got, r) <= gradient_limit(r, dtype), (name, relative(got, r), gradient_limit(r, dtype))
+
+
+def test_gradients_of_large_cotangents():
+    """dP beyond f16's range, gradients within it."""
+    off = ([0, 6, 30], [0, 2, 33])
+    at = uvu.Attention(1, 1, 64, i32(off[0]), i32(off[1]))
+    q, k, v = (rand(i, n, 1, 64, dtype=torch.float16) for i, n in ((1, 30), (2, 33), (3, 33)))
+    do = (rand(4, 30, 1, 64) * 1e4).to(torch.float16)
+    k, v = k * 0.25, v * 4
+    ref, _ = update.attention_vjp(*map(values, (q, k, v)), *off, at.scale, values(do))
+    assert np.abs(values(do)[:6, 0] @ values(v)[:2, 0].T).max() > 2 * 65504 and max(np.abs(r).max() for r in ref[:2]) < 65504
+    for name, got, r in list(zip(("dq", "dk"), gradients(q, k, v, do, at), ref)):
+        assert relative(got, r) <= gradient_limit(r, torch.float16), (name, relative(got, r), gradient_limit(r, torch.float16))
+
+
+def test_gradients_of_cotangents_of_many_sizes():
+    """Graphs, heads and rows whose cotangents differ by orders of magnitude: each graph's and kv head's dk and dv, and each row's dq,
+    as if alone.  Masked states hold infinities, which no scale may follow."""
+    off, dtype = ([0, 70, 70, 200], [0, 3000, 3000, 5100]), torch.float16
+    at = uvu.Attention(4, 2, 64, i32(off[0]), i32(off[1]), 130, 3000)
+    q, k, v = rand(1, 200, 4, 64, dtype=dtype), rand(2, 5100, 2, 64, dtype=dtype), rand(3, 5100, 2, 64, dtype=dtype)
+    size = torch.ones(200, 4, 1, device="cuda")
+    size[:70] *= 1e-3
+    size[:, 2:] *= 0.1
+    size[70::2] *= 1e-2  # every other row of the last graph
+    do = (rand(4, 200, 4, 64) * size).to(dtype)
+    keep = (rand(5, 5100) < 1.3).to(torch.uint8)
+    v[keep == 0] = float("inf")
+    host = [values(t) for t in (q, k, v)]
+    host[2][keep.cpu().numpy() == 0] = 0
+    ref, _ = update.attention_vjp(*host, *off, at.scale, values(do), keep.cpu().numpy())
+    dq, dk, dv = gradients(q, k, v, do, at, keep)
+    for a, b in ((0, 70), (70, 200)):
+        for h in range(4):
+            for part in (slice(a, b, 2), slice(a + 1, b, 2)):
+                r = ref[0][part, h]
+                assert relative(dq[part, h], r) <= gradient_limit(r, dtype), (a, h)
+    for a, b in ((0, 3000), (3000, 5100)):
+        for h in range(2):
+            for got, r in ((dk, ref[1]), (dv, ref[2])):
+                assert relative(got[a:b, h], r[a:b, h]) <= gradient_limit(r[a:b, h], dtype), (a, h)
