@@ -47,7 +47,7 @@ struct FwdLayout {
 template <typename T, int NT, int LG, bool ALIGNED>
 __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG < 4 ? 2 : 1) attn_fwd_mma(AttnArgs a, FwdLayout<NT> L) {
     extern __shared__ unsigned char smem_raw[];
-    __shared__ int s_dead;
+    __shared__ int s_dead, s_kept;  // s_kept: a mask has kept one of the piece's states
     __shared__ uint32_t s_tmem;
     const AttnTile tl = attn_tile<kRows * NT>(a.q_off, a.k_off, a.graphs, a.group, blockIdx.x);
     if (tl.graph < 0) return;
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
     const uint32_t o_cols = uint32_t(64 * L.panels);
     const uint32_t tmem_cols = NT == 2 ? 512 : 256;
     if (threadIdx.x == 0) {
-        s_dead = 0;
+        s_dead = s_kept = 0;
         bar_init(q_full, kLoadWarps * 32);
         for (int t = 0; t < 2; ++t) {
             bar_init(s_full + 8 * t, 1);
@@ -200,6 +200,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
             }
             if (ok && work) {
                 const bool valid = row < n_rows;
+                if (a.keep && !*static_cast<volatile int*>(&s_kept)) l = 0.f;  // nothing to attend to, whatever q holds
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const int64_t p = tl.row0 + row;
                 const int64_t r = q0 + p / a.group, head = int64_t(h) * a.group + p % a.group;
@@ -337,6 +338,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
                 // the softmax warps read the tile's bias before its V stage is released, and K's stage comes half a ring
                 // later: kMaskRing biases cannot be overtaken
                 if (masked(j)) {
+                    if (map_t == 0 && mask.any()) s_kept = 1;
                     write_bias(biases + slot(j) * kRows, mask, map_t);
                     bar_arrive(m_full + 8 * slot(j));
                 }

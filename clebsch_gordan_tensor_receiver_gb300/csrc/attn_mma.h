@@ -173,6 +173,12 @@ struct StateMask {
         for (int w = 0; w < kWords; ++w) a &= word[w];
         return a == 0xffffffffu;
     }
+    __device__ __forceinline__ bool any() const {
+        uint32_t a = 0;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) a |= word[w];
+        return a != 0;
+    }
     // The states row, row + STEP, ... (row < STEP) as the bits 0, 1, ... of a word.
     template <int STEP>
     __device__ __forceinline__ uint32_t every(int row) const {

@@ -167,8 +167,10 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                 rh = (q0 + p / a.group) * a.Hq + int64_t(h) * a.group + p % a.group;
                 const float x = a.lse[rh];
                 if (kScaled) e_ds = exponent(a.do2[rh]);
-                // P is not stored here, so dS's scale is its own.  A row without a kept state: P = exp2(s - inf) = 0
+                // P is not stored here, so dS's scale is its own.  A row without a kept state: P = exp2(s - inf) = 0, and a
+                // zero gradient, whatever q and d_out hold
                 lse = x == -INFINITY ? -INFINITY : float(e_ds) - x * kLog2e;
+                keep = x != -INFINITY;
                 delta = -a.delta[rh];
             }
         }

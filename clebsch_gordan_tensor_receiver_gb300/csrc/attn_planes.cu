@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
     using F = FwdPlan<PS>;
     constexpr int kHalf = PS / F::kGroups, kRing = 8, kBlocks = F::kHalfState / 32;  // 32-column blocks of a warpgroup
     extern __shared__ unsigned char smem_raw[];
-    __shared__ int s_dead;
+    __shared__ int s_dead, s_kept;  // s_kept: a mask has kept one of the piece's states
     __shared__ uint32_t s_tmem;
     const AttnTile tl = attn_tile<kRows>(a.q_off, a.k_off, a.graphs, a.group, blockIdx.x);
     if (tl.graph < 0) return;
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
     const uint32_t q_full = sb + F::kBars, s_full = q_full + 8, p_full = s_full + 8, o_full = p_full + 8, fin = o_full + 8,
                    pair = fin + 8, full = pair + 32, empty = full + 8 * F::kStages, m_full = empty + 8 * F::kStages;
     if (threadIdx.x == 0) {
-        s_dead = 0;
+        s_dead = s_kept = 0;
         bar_init(q_full, kLoadThreads);
         bar_init(s_full, 1);
         bar_init(p_full, F::kWarps);
@@ -420,7 +420,8 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
             if (n_tiles > 0) add_o();
             float other = 0.f;
             if (exchange(l, other)) {
-                const float sum = w ? other + l : l + other;
+                // nothing to attend to, whatever q holds: 0
+                const float sum = a.keep && !*static_cast<volatile int*>(&s_kept) ? 0.f : w ? other + l : l + other;
                 const int64_t p = tl.row0 + row;
                 const int64_t r = q0 + p / a.group, head = int64_t(h) * a.group + p % a.group;
                 const int64_t rh = (int64_t(split) * a.nq + r) * a.Hq + head;
@@ -510,6 +511,7 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
                 mask.next();
                 if (!load(2 * j, K)) break;
                 if (masked(j)) {
+                    if (t == 0 && mask.any()) s_kept = 1;
                     write_bias(biases + slot(j) * F::kState, mask, t);
                     bar_arrive(m_full + 8 * slot(j));
                 }
@@ -621,7 +623,8 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
             } else {
                 rh = (q0 + p / a.group) * a.Hq + int64_t(h) * a.group + p % a.group;
                 const float v = a.lse[rh];
-                lse = v == -INFINITY ? -INFINITY : -v * kLog2e;  // a row without a kept state: P = exp2(s - inf) = 0
+                lse = v == -INFINITY ? -INFINITY : -v * kLog2e;  // a row without a kept state: P = exp2(s - inf) = 0 ...
+                keep = v != -INFINITY;                           // ... and a zero gradient, whatever q and d_out hold
                 delta = -a.delta[rh];
             }
         }

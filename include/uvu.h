@@ -557,7 +557,8 @@ uvu_status uvu_dropout_bwd(uvu_dtype dtype, int64_t n_draws, int inner, double p
  * head_dim is 1 .. 128; q_heads is a multiple of kv_heads.  max_q, max_k: no graph has more rows or
  * states (the split of the work goes by them; wrong values cost time, not correctness).  scale > 0.
  * k_keep [n_k] bytes, or NULL: states with 0 take no part, whatever their k and v hold.  A row
- * without a kept state gets out = 0 and lse = -inf.  A NaN or infinity in a kept operand gives NaN in the
+ * without a kept state gets out = 0 and lse = -inf, and a zero gradient, whatever its q and d_out hold; a kept
+ * state whose score is -inf weighs nothing.  Otherwise a NaN or infinity in a kept operand gives NaN in the
  * rows that it reaches.  16-bit operands: P (and dS in the backward) are rounded to their type for the
  * products with v (k, q, d_out), in the backward of UVU_F16 at powers of two that follow the size of d_out and v, so that
  * small cotangents keep their bits and large ones do not overflow; everything else is fp32.  fp32 operands: products of fp32 accuracy on the tensor

@@ -115,3 +115,30 @@ def test_gradients_of_cotangents_of_many_sizes():
         for h in range(2):
             for got, r in ((dk, ref[1]), (dv, ref[2])):
                 assert relative(got[a:b, h], r[a:b, h]) <= gradient_limit(r[a:b, h], dtype), (a, h)
+
+
+# ------------------------------------------------------------------- rows whose mask leaves nothing
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("rows, states", [(1, 70), (150, 300), (1, 6000)])
+def test_rows_without_a_kept_state(rows, states, d, kind):
+    """Zeros, lse -inf and zero gradients, as for a graph without states, whatever q and d_out hold; the other graph's rows, whose
+    NaN meet kept states, are NaN."""
+    dtype, n = TYPES[kind], 3 * rows
+    at = uvu.Attention(2, 1, d, i32([0, rows, 2 * rows, n]), i32([0, states, states, 2 * states]), rows, states)
+    q, k, v, do = (rand(i, m, h, d, dtype=dtype) for i, (m, h) in enumerate(((n, 2), (2 * states, 1), (2 * states, 1), (n, 2))))
+    q[:rows, 0], q[0, 1, 0], do[:rows, :, 0] = float("nan"), float("inf"), float("nan")
+    q[rows], do[rows] = float("nan"), float("inf")
+    q[2 * rows, 0] = float("nan")
+    keep = torch.ones(2 * states, dtype=torch.uint8, device="cuda")
+    keep[:states] = 0
+    keep[states + states // 2:] = 0  # pieces of the last graph are masked, too
+    out, lse = torch.empty_like(q), torch.empty(n, 2, device="cuda")
+    at.fwd(q, k, v, out, lse, keep=keep)
+    g = [torch.full_like(t, float("nan")) for t in (q, k, v)]
+    at.bwd(q, k, v, out, lse, do, *g, keep=keep)
+    assert (out[:2 * rows] == 0).all() and torch.isneginf(lse[:2 * rows]).all() and (g[0][:2 * rows] == 0).all()
+    assert (g[1][:states] == 0).all() and (g[2][:states] == 0).all()
+    assert torch.isnan(out[2 * rows, 0]).all() and torch.isnan(lse[2 * rows, 0]) and torch.isnan(g[0][2 * rows, 0]).all()
+    assert torch.isfinite(out[2 * rows, 1]).all() and torch.isfinite(lse[2 * rows, 1])
