@@ -248,7 +248,7 @@ def node_update(m, offsets, context, attention: "uvu.Attention", weights, groups
     q = (s @ w_q).view(n, attention.q_heads, attention.head_dim)
     k = (context @ w_k).view(-1, attention.kv_heads, attention.head_dim)
     v = (context @ w_v).view(-1, attention.kv_heads, attention.head_dim)
-    a = cross_attention(q, k, v, attention, keep).reshape(n, -1) @ w_o
+    a = cross_attention(q, k, v, attention, keep).reshape(n, attention.q_heads * attention.head_dim) @ w_o
     s = dropout(a, p, seed, offset, residual=s)
     h = dropout(m * torch.sigmoid(s)[:, :, None], p, seed, offset + (n * u + 7) // 8, inner=d)
     return s, h

@@ -142,3 +142,19 @@ def test_rows_without_a_kept_state(rows, states, d, kind):
     assert (g[1][:states] == 0).all() and (g[2][:states] == 0).all()
     assert torch.isnan(out[2 * rows, 0]).all() and torch.isnan(lse[2 * rows, 0]) and torch.isnan(g[0][2 * rows, 0]).all()
     assert torch.isfinite(out[2 * rows, 1]).all() and torch.isfinite(lse[2 * rows, 1])
+
+
+# ------------------------------------------------------------------------------------ empty batches
+
+@pytest.mark.parametrize("nodes, states", [(0, 0), (0, 5), (6, 0)])
+def test_node_update_of_empty_sides(nodes, states):
+    """A batch without nodes, or whose encoder has no states: finite outputs and gradients of the right shapes."""
+    at = uvu.Attention(4, 2, 16, i32([0, 0, nodes]), i32([0, 0, states]))
+    m, ctx = rand(1, nodes, 64, 4).requires_grad_(True), rand(2, states, 24).requires_grad_(True)
+    weights = [rand(3 + i, *s).requires_grad_(True) for i, s in enumerate(((64,), (64,), (64, 64), (24, 32), (24, 32), (64, 64)))]
+    s, h = autograd.node_update(m, at.q_offsets, ctx, at, weights, 8, p=0.25, seed=3)
+    assert s.shape == (nodes, 64) and h.shape == (nodes, 64, 4)
+    g = torch.autograd.grad(s.sum() + h.sum(), (m, ctx, *weights))
+    assert all(torch.isfinite(t).all() for t in (s, h, *g))
+    if states == 0:  # nothing is attended to
+        assert all((t == 0).all() for t in (g[1], *g[4:]))
