@@ -614,8 +614,8 @@ def group_norm_bwd(dy, x, gamma, beta, offsets, groups, mean, rstd, dx, dgamma, 
 
 def _draws(x, inner):
     n = x.numel()
-    if inner < 1 or n % inner:
-        raise ValueError("the tensor's size must be a multiple of inner >= 1")
+    if inner < 1 or inner >= 2 ** 31 or n % inner:  # the C entry takes an int
+        raise ValueError("the tensor's size must be a multiple of inner, which is in [1, 2^31)")
     return n // inner
 
 

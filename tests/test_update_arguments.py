@@ -79,3 +79,11 @@ def test_strides_of_axes_of_one(rows, heads):
     else:
         assert at._operand("out", plain, heads, rows, plain.dtype) == (24, 8)
         assert at._operand("out", turned, heads, rows, plain.dtype) == (8, 40)
+
+
+def test_inner_beyond_an_int():
+    """2^32 + 1 would arrive in the library as 1."""
+    for inner in (2 ** 31, 2 ** 32 + 1):
+        with pytest.raises(ValueError, match="inner"):
+            uvu._draws(torch.empty(2 * inner, device="meta"), inner)
+    assert uvu._draws(torch.empty(2 ** 32 - 2, device="meta"), 2 ** 31 - 1) == 2
