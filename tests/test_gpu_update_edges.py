@@ -6,7 +6,7 @@ import torch
 
 from clebsch_gordan_tensor_receiver_gb300 import autograd, uvu
 from oracle import update
-from update_limits import TYPES, gradient_limit, output_limit, relative, values
+from update_limits import TYPES, gradient_limit, output_limit, relative, unit, values
 
 pytestmark = pytest.mark.gpu
 
@@ -140,7 +140,7 @@ def test_node_update_of_empty_sides(nodes, states):
         assert all((t == 0).all() for t in (g[1], *g[4:]))
 
 
-# ------------------------------------------------------------------------- norms of 16-bit results
+# ----------------------------------------------------------- norms of 16-bit results, two row tiles a block
 
 NORMED = [  # q lengths, k lengths, q heads, kv heads, head dim, kept share (None: no mask)
     ([40, 0, 200], [900, 5, 333], 4, 2, 64, 0.9), ([300], [1500], 2, 2, 16, None), ([129, 7], [700, 90], 6, 2, 33, 0.6),
@@ -172,3 +172,28 @@ def test_norms_of_16_bit_results(case, kind):
     ref, _ = update.attention_vjp(*map(values, (q, k, v)), qo, ko, at.scale, values(do), host)
     for name, got, r in zip(("dq", "dk", "dv"), gradients(q, k, v, do, at, keep), ref):
         assert relative(got, r) <= gradient_limit(r, dtype), (name, relative(got, r), gradient_limit(r, dtype))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("share", [None, 0.8])
+@pytest.mark.parametrize("d, view", [(16, 0), (30, 0), (32, 0), (64, 0), (64, 1), (96, 0), (128, 0), (128, 1)])
+def test_two_row_tiles_a_block(d, view, share, kind):
+    """The forward that takes 256 rows a block, which it does once they fill the SMs: all classes of head dimensions, with
+    and without a mask, operands off the 16-byte grid, walks longer than the ring of masks, graphs whose second tile is empty."""
+    dtype, hk = TYPES[kind], 8
+    case = ([4000, 129, 1, 0, 900], [1300, 70, 257, 3, 0], hk, hk, d, share)
+    assert ((5030 // 256 + 5) * hk) >= torch.cuda.get_device_properties(0).multi_processor_count
+    (q, k, v, _), keep, qo, ko, at = of_case(case, dtype, view)
+    out, lse = torch.full_like(q, float("nan")), torch.full(q.shape[:2], float("nan"), device="cuda")
+    at.fwd(q, k, v, out, lse, keep=keep)
+    ref, ref_lse, mag = update.attention(*map(values, (q, k, v)), qo, ko, at.scale, None if keep is None else keep.cpu().numpy())
+    got = values(lse)
+    assert np.array_equal(np.isneginf(got), np.isneginf(ref_lse))
+    kept = ~np.isneginf(ref_lse)
+    assert np.abs(got[kept] - ref_lse[kept]).max() <= 1e-4
+    assert (np.abs(values(out) - ref) <= 3 * unit(dtype) * (np.abs(ref) + mag) + 1e-4).all()
+    for a, b in ((0, 4000), (4000, 4129), (4129, 4130)):
+        for h in range(hk):
+            assert relative(out[a:b, h], ref[a:b, h]) <= output_limit(ref[a:b, h], dtype), (a, h)
+    assert (out[4130:] == 0).all()
+    assert uvu.Attention.device_status() == 0
