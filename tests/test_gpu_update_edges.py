@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from clebsch_gordan_tensor_receiver_gb300 import autograd, uvu
+from gpu_util import check
 from oracle import update
 from update_limits import TYPES, gradient_limit, output_limit, relative, unit, values
 
@@ -197,3 +198,28 @@ def test_two_row_tiles_a_block(d, view, share, kind):
             assert relative(out[a:b, h], ref[a:b, h]) <= output_limit(ref[a:b, h], dtype), (a, h)
     assert (out[4130:] == 0).all()
     assert uvu.Attention.device_status() == 0
+
+
+# ---------------------------------------------------------------- group norm of graphs longer than promised
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("most", [1, None])
+def test_group_norm_of_a_long_graph_with_a_mean(most, kind):
+    """Values of 5 +- 1.5 over 140000 rows, also with a max_rows that promised one, element by element (no row begins on 16 bytes):
+    the statistics keep fp32's accuracy whatever the length, so mean, rstd, dgamma and dbeta meet the fp32 tolerance."""
+    n, c, groups, dtype = 140000, 96, 2, TYPES[kind]
+    flat, dy = (rand(1, n * c + 1) * 1.5 + 5).to(dtype), rand(2, n, c, dtype=dtype)
+    x, off = flat[1:].view(n, c), i32([0, n])
+    gamma, beta = 1 + 0.2 * rand(3, c), 0.2 * rand(4, c)
+    y, dx, mean, rstd, dg, db = (torch.full(s, float("nan"), dtype=t, device="cuda") for s, t in
+                                 (((n, c), dtype), ((n, c), dtype), ((1, groups), torch.float32), ((1, groups), torch.float32),
+                                  ((c,), torch.float32), ((c,), torch.float32)))
+    uvu.group_norm_fwd(x, gamma, beta, off, groups, y, mean, rstd, max_rows=most)
+    uvu.group_norm_bwd(dy, x, gamma, beta, off, groups, mean, rstd, dx, dg, db, max_rows=most)
+    host = [values(t) for t in (x, gamma, beta)]
+    _, rm, rr = update.group_norm(*host, [0, n], groups, True, 1e-5)
+    _, rg, rb = update.group_norm_vjp(*host, [0, n], groups, True, 1e-5, values(dy))
+    for got, ref, what in ((mean, rm, "mean"), (rstd, rr, "rstd"), (dg, rg, "dgamma"), (db, rb, "dbeta")):
+        check(values(got), ref, False, what)
+    # 5 +- 1.5 is known to 5 * 2^-24 in fp32; a sum of 48 n values may cost a few of these, not a hundred
+    assert np.abs(values(mean) - rm).max() <= 8 * 5 * 2.0 ** -24
