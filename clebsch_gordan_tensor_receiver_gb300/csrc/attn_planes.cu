@@ -214,6 +214,7 @@ __device__ __forceinline__ void store_planes(const float (&x)[N], uint32_t hi, u
 }
 __device__ __forceinline__ void load_columns(uint32_t a, float (&v)[32]) { tmem_ld32(a, v); }
 __device__ __forceinline__ void load_columns(uint32_t a, float (&v)[16]) { tmem_ld16(a, v); }
+__device__ __forceinline__ void load_columns(uint32_t a, float (&v)[8]) { tmem_ld8(a, v); }
 
 // Column of 16-row block s of a plane-0 operand that its two warpgroups wrote over their halves (`half`
 // columns each) of the fp32 tile.
@@ -221,23 +222,24 @@ __device__ __forceinline__ uint32_t block_column(int s, int half) {
     return uint32_t(s / (half / 16) * half + s % (half / 16) * 8);
 }
 
-// acc[i] += columns i of N at `a`
-template <int N>
+// acc[i] += the sum of column i of N in each of ORDERS blocks of PS columns from `a` on, the small terms (the last block) first:
+// added to acc one by one they would be lost in a long walk's sum (out over 2^20 states of one sign: off by 2.1e-5, so by 1.7e-6).
+template <int N, int PS, int ORDERS>
 __device__ __forceinline__ void add_columns(uint32_t a, float* acc) {
-    if constexpr (N == 8) {
-        float v[8];
-        tmem_ld8(a, v);
-        tmem_wait_ld(v);
+    constexpr int kBlock = N < 16 ? N : 16;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += v[i];
-    } else {
+    for (int b = 0; b < N / kBlock; ++b) {
+        float v[ORDERS][kBlock];
 #pragma unroll
-        for (int b = 0; b < N / 16; ++b) {
-            float v[16];
-            tmem_ld16(a + 16 * b, v);
-            tmem_wait_ld(v);
+        for (int o = 0; o < ORDERS; ++o) load_columns(a + o * PS + kBlock * b, v[o]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[16 * b + i] += v[i];
+        for (int o = 0; o < ORDERS; ++o) tmem_wait_ld(v[o]);
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i) {
+            float sum = v[ORDERS - 1][i];
+#pragma unroll
+            for (int o = ORDERS - 2; o >= 0; --o) sum += v[o][i];
+            acc[kBlock * b + i] += sum;
         }
     }
 }
@@ -361,11 +363,7 @@ __global__ void __launch_bounds__(FwdPlan<PS>::kThreads, FwdPlan<PS>::kColumns =
             return true;
         };
         // this warpgroup's half of the columns of O, all orders
-        auto add_o = [&]() {
-            add_columns<kHalf>(base_t + F::kO + 2 * PS + w * kHalf, acc);
-            add_columns<kHalf>(base_t + F::kO + PS + w * kHalf, acc);
-            add_columns<kHalf>(base_t + F::kO + w * kHalf, acc);
-        };
+        auto add_o = [&]() { add_columns<kHalf, PS, 3>(base_t + F::kO + w * kHalf, acc); };
         for (int j = 0; j < n_tiles; ++j) {
             const bool biased = masked(j);
             const float* bias = biases + slot(j) * F::kState + F::kHalfState * w;
@@ -646,8 +644,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const Planes& x, int
         auto take = [&](int which, int j) {
             if (j == 0) return;
             if constexpr (!B::kHeld) {
-                add_columns<kCols>(columns(which) + PS, acc);
-                add_columns<kCols>(columns(which), acc);
+                add_columns<kCols, PS, 2>(columns(which), acc);
             } else if (j % B::kFlush == 0 || j == n_tiles) {
                 const float scale = KV && which ? 1.f : a.scale;
 #pragma unroll 1

@@ -223,3 +223,32 @@ def test_group_norm_of_a_long_graph_with_a_mean(most, kind):
         check(values(got), ref, False, what)
     # 5 +- 1.5 is known to 5 * 2^-24 in fp32; a sum of 48 n values may cost a few of these, not a hundred
     assert np.abs(values(mean) - rm).max() <= 8 * 5 * 2.0 ** -24
+
+
+# ------------------------------------------------------------------------------ sums over very long walks
+
+def exact_rows(q, k, v, scale, rows):
+    """out and lse of some rows of one head, in fp64 on the device."""
+    s = q[rows, 0].double() @ k[:, 0].double().T * scale
+    lse = torch.logsumexp(s, 1)
+    return torch.exp(s - lse[:, None]) @ v[:, 0].double(), lse
+
+
+def long_walk(kind, nq, nk, d):
+    """Values of one sign, whose sums show every loss: relative Frobenius errors of out (some rows) and lse, and out's values."""
+    dtype = TYPES[kind]
+    q, k, v = rand(1, nq, 1, d, dtype=dtype), rand(2, nk, 1, d, dtype=dtype), (rand(3, nk, 1, d) * 0.1 + 1).to(dtype)
+    at = uvu.Attention(1, 1, d, i32([0, nq]), i32([0, nk]))
+    out, lse = torch.empty_like(q), torch.empty(nq, 1, device="cuda")
+    at.fwd(q, k, v, out, lse)
+    rows = torch.arange(0, nq, max(1, nq // 31), device="cuda")
+    ref, ref_lse = exact_rows(q, k, v, at.scale, rows)
+    assert (lse[rows, 0].double() - ref_lse).abs().max() <= 1e-5
+    return out[rows, 0], values(ref)
+
+
+@pytest.mark.parametrize("nq, d", [(24576, 64), (24576, 20), (24576, 128), (100, 64)])
+def test_sums_of_long_walks_f32(nq, d):
+    """2^20 states in one walk, or in pieces: the fp32 tolerance holds."""
+    got, ref = long_walk("f32", nq, 2 ** 20, d)
+    check(values(got), ref, False, "out")
