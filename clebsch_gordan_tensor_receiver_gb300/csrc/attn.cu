@@ -186,6 +186,7 @@ struct Choice {
     int R;              // rows or states of a tile of the backward
     int64_t fwd_tiles;  // tile numbers of the forward
     int fwd, dq, dkv;   // splits
+    bool hold;          // the forward's walks are long: their sums are held in memory
 };
 Choice choose(const AttnShape& s, int sms) {
     const int64_t group = s.q_heads / s.kv_heads;
@@ -205,6 +206,7 @@ Choice choose(const AttnShape& s, int sms) {
     c.nt = !c.planes && rows_busy(256) >= sms && s.max_q * group > 128 ? 2 : 1;
     c.fwd_tiles = row_tiles(s, 128 * c.nt);
     c.fwd = splits_for(rows_busy(128 * c.nt), s.max_k, 128, sms, c.nt == 1 && s.head_dim <= (c.planes ? 32 : 64) ? 2 : 1, 4);
+    c.hold = !c.planes && s.max_k / c.fwd > 128 * attn_hold_tiles(s.dtype == UVU_F16);
     const int bwd_blocks = c.planes && s.head_dim <= 32 ? 2 : 1;
     c.dq = splits_for(rows_busy(c.R), s.max_k, 128, sms, bwd_blocks, 1);
     c.dkv = splits_for(states_busy(c.R), s.max_q * group, 128, sms, bwd_blocks, 1);
@@ -221,6 +223,7 @@ void attn_workspace(const AttnShape& s, int sms, size_t* fwd, size_t* bwd) {
     const Choice c = choose(s, sms);
     const size_t qh = size_t(s.n_q) * s.q_heads, kh = size_t(s.n_k) * s.kv_heads;
     *fwd = c.fwd > 1 ? align256(c.fwd * qh * 4) + align256(c.fwd * qh * s.head_dim * 4) : 0;
+    if (c.hold && c.fwd == 1) *fwd = align256(qh * s.head_dim * 4);
     if (c.planes) *fwd += attn_planes_bytes(s, false);
     const size_t dq = c.dq > 1 ? c.dq * qh * s.head_dim * 4 : 0, dkv = c.dkv > 1 ? 2 * c.dkv * kh * s.head_dim * 4 : 0;
     *bwd = align256(qh * 4) + align256(dq) + align256(dkv);
@@ -259,6 +262,8 @@ cudaError_t launch_attn_fwd(const AttnShape& s, const AttnTensors& t, void* ws, 
         a.part_o = reinterpret_cast<float*>(w + align256(n * 4));
         w += align256(n * 4) + align256(n * a.D * 4);
     }
+    a.hold = c.hold;
+    if (c.hold && c.fwd == 1) a.part_o = reinterpret_cast<float*>(w);
     cudaError_t e = cudaSuccess;
     if (c.planes) {
         e = launch_attn_planes(a, w, sms, st);

@@ -28,7 +28,8 @@ struct AttnArgs {
     unsigned *do2_top, *v2_top;  // [graphs][Hkv]: their maxima over a graph's rows and the kv head's heads, as bits
     // split over the long axis: partial results, joined by a second kernel (1: none)
     int splits;
-    float* part_o;    // [splits][nq][Hq][D]
+    float* part_o;    // [splits][nq][Hq][D]; of one walk too where it is held
+    bool hold;        // walks are long (attn_hold_tiles)
     float* part_lse;  // [splits][nq][Hq]
     // backward
     int64_t kv_tiles, q_tiles;  // tile numbers of dk and dv, and of dq (0: not asked for)
@@ -71,6 +72,11 @@ __device__ __forceinline__ AttnTile attn_tile(const int32_t* off, const int32_t*
     r.graph = r.row0 < r.rows ? s[0] : -1;
     return r;
 }
+
+// Tiles of 128 states or rows whose products one sum in tensor memory takes.  Each accumulating instruction (16 states) cuts the
+// sum by up to 2^-23 of it: values of one sign lose 1.1e-4 over 16384 states, a fifth of f16's u, and 4e-4 over 65536, a tenth
+// of bf16's.  Longer walks add such sums up in fp32 in memory; without that, 2^20 states were off by 6.7e-3 in f16.
+__host__ __device__ constexpr int attn_hold_tiles(bool f16) { return f16 ? 128 : 512; }
 
 // attn_mma.cu: the forward of 16-bit operands, nt (1 or 2) row tiles of 128 per block; a.splits > 1
 // leaves partial results for the join.

@@ -44,7 +44,33 @@ struct FwdLayout {
     __host__ __device__ int total() const { return bars() + 288 + 1024; }  // barriers, alignment slack
 };
 
-template <typename T, int NT, int LG, bool ALIGNED>
+// Adds a row of O to what a long walk holds of it (null: a lane without a row), held so far at another reference by the factor f.
+static __device__ __noinline__ void hold_row(uint32_t o_at, int D, float* held, float f, bool first) {
+    for (int d = 0; d < D; d += 16) {
+        float o[16];
+        __syncwarp();
+        tmem_ld16(o_at + d, o);
+        tmem_wait_ld(o);
+        if (!held) continue;
+        if (D % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                if (d + i < D) {
+                    float4* at = reinterpret_cast<float4*>(held + d + i);
+                    const float4 h = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *at;
+                    *at = make_float4(fmaf(h.x, f, o[i]), fmaf(h.y, f, o[i + 1]), fmaf(h.z, f, o[i + 2]), fmaf(h.w, f, o[i + 3]));
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (d + i < D) held[d + i] = fmaf(first ? 0.f : held[d + i], f, o[i]);
+        }
+    }
+}
+
+// HELD: long walks, whose sums leave tensor memory every kHold tiles (as a branch of the one kernel it cost single tokens over long
+// encodings 2%).
+template <typename T, int NT, int LG, bool ALIGNED, bool HELD>
 __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG < 4 ? 2 : 1) attn_fwd_mma(AttnArgs a, FwdLayout<NT> L) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_dead, s_kept;  // s_kept: a mask has kept one of the piece's states
@@ -94,6 +120,10 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
     const bool tail = (kr.hi - kr.lo) % kRows != 0;
     auto masked = [&](int j) { return a.keep || (tail && j == n_tiles - 1); };
     auto slot = [&](int j) { return a.keep ? j % kMaskRing : 0; };
+    // O begins anew at these tiles
+    constexpr int kHold = attn_hold_tiles(__is_same(T, __half));
+    const bool held = HELD && n_tiles > kHold;
+    auto fresh = [&](int j) { return j == 0 || (HELD && j % kHold == 0); };
 
     if (warp < 4 * NT) {
         // ------------------------------------------------------------------------ softmax
@@ -104,10 +134,16 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
         const uint32_t s_at = tmem + uint32_t(t * kRows) + lanes, o_at = tmem + uint32_t(NT * kRows) + uint32_t(t) * o_cols + lanes;
         const float c = a.scale_log2;
         float m = -INFINITY, l = 0.f;  // reference maximum in units of c S, and the sum of P
+        float m_held = -INFINITY;      // the reference of what is held in memory
+        auto held_row = [&]() {
+            const int64_t p = tl.row0 + row, rh = (int64_t(split) * a.nq + q0 + p / a.group) * a.Hq + int64_t(h) * a.group + p % a.group;
+            return a.part_o + rh * a.D;
+        };
+        auto held_factor = [&]() { return m_held == m ? 1.f : exp2_approx(m_held - m); };
         bool ok = true;
         if (t < nt) {
             // a block with all of an SM's registers holds its row of S; the others read it twice
-            constexpr bool kHold = NT == 2 || LG == 4;
+            constexpr bool kKeep = NT == 2 || LG == 4;
             for (int j = 0; j < n_tiles; ++j) {
                 const bool biased = masked(j);
                 const float* bias = biases + slot(j) * kRows;
@@ -119,9 +155,13 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
                 if (!ok) break;
                 fence_after();
                 if (work) {
-                    float x[kHold ? 4 : 2][32];
+                    if (HELD && j > 0 && fresh(j)) {  // O of the tile before is complete
+                        hold_row(o_at, a.D, row < n_rows ? held_row() : nullptr, held_factor(), j == kHold);
+                        m_held = m;
+                    }
+                    float x[kKeep ? 4 : 2][32];
                     float top = -INFINITY;
-                    if constexpr (kHold) {
+                    if constexpr (kKeep) {
 #pragma unroll
                         for (int b = 0; b < 4; ++b) tmem_ld32(s_at + 32 * b, x[b]);
 #pragma unroll
@@ -149,7 +189,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
                         if (j > 0) {
                             const float f = move ? exp2_approx(m - to) : 1.f;
                             l *= f;
-                            for (int d = 0; d < d16; ++d) {
+                            for (int d = 0; d < (fresh(j) ? 0 : d16); ++d) {
                                 float o[16];
                                 tmem_ld16(o_at + 16 * d, o);
                                 tmem_wait_ld(o);
@@ -165,8 +205,8 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
                     F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
-                        float(&v)[32] = x[kHold ? b : b & 1];
-                        if constexpr (!kHold) {
+                        float(&v)[32] = x[kKeep ? b : b & 1];
+                        if constexpr (!kKeep) {
                             tmem_wait_ld(v);
                             if (b < 3) tmem_ld32(s_at + 32 * (b + 1), x[(b + 1) & 1]);
                             if (biased) add_bias(v, bias + 32 * b);
@@ -201,7 +241,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
             if (ok && work) {
                 const bool valid = row < n_rows;
                 if (a.keep && !*static_cast<volatile int*>(&s_kept)) l = 0.f;  // nothing to attend to, whatever q holds
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float inv = l == 0.f ? 0.f : 1.f / l, f = held ? held_factor() : 0.f;
                 const int64_t p = tl.row0 + row;
                 const int64_t r = q0 + p / a.group, head = int64_t(h) * a.group + p % a.group;
                 const int64_t rh = (int64_t(split) * a.nq + r) * a.Hq + head;
@@ -214,6 +254,12 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
                     if (n_tiles > 0) {
                         tmem_ld16(o_at + 16 * d, o);
                         tmem_wait_ld(o);
+                    }
+                    if (held && valid) {
+                        const float* from = a.part_o + rh * a.D + 16 * d;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (16 * d + i < a.D) o[i] = fmaf(from[i], f, o[i]);
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
@@ -271,6 +317,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
             for (int j = 0; j < n_tiles && ok; ++j) {
                 ok = wait_stage();
                 fence_async();
+                const bool more = !fresh(j);
                 const int v_at = ring.at;
                 const uint32_t v = stage();
                 ring.next();
@@ -284,7 +331,7 @@ __global__ void __launch_bounds__((4 * NT + 1 + kLoadWarps) * 32, NT == 1 && LG 
                         fence_after();
 #pragma unroll
                         for (int s = 4 * half; s < 4 * half + 4; ++s)
-                            mma_ts(lead, o, tmem + uint32_t(t * kRows + 8 * s), desc_rows(v, s), id_o, j > 0 || s > 0);
+                            mma_ts(lead, o, tmem + uint32_t(t * kRows + 8 * s), desc_rows(v, s), id_o, more || s > 0);
                     }
                     if (!ok) break;
                     if (j + 1 < n_tiles) {
@@ -368,7 +415,9 @@ cudaError_t fwd(const AttnArgs& a, int64_t row_tiles, cudaStream_t st) {
     const uintptr_t any = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
                           uintptr_t(a.q_row | a.q_head | a.k_row | a.k_head | a.v_row | a.v_head) * 2;
     return by_chunks(a.D, (any & 15u) == 0, [&](auto lg, auto aligned) {
-        auto k = attn_fwd_mma<T, NT, decltype(lg)::value, decltype(aligned)::value>;
+        constexpr int LG = decltype(lg)::value;
+        constexpr bool ALIGNED = decltype(aligned)::value;
+        auto k = a.hold ? attn_fwd_mma<T, NT, LG, ALIGNED, true> : attn_fwd_mma<T, NT, LG, ALIGNED, false>;
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total());
         if (e != cudaSuccess) return e;
         k<<<dim3(unsigned(row_tiles), unsigned(a.Hkv), unsigned(a.splits)), (4 * NT + 1 + kLoadWarps) * 32, L.total(), st>>>(a, L);

@@ -252,3 +252,32 @@ def test_sums_of_long_walks_f32(nq, d):
     """2^20 states in one walk, or in pieces: the fp32 tolerance holds."""
     got, ref = long_walk("f32", nq, 2 ** 20, d)
     check(values(got), ref, False, "out")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("nq, nk, d", [(24576, 2 ** 20, 64), (40000, 2 ** 20, 64), (40000, 2 ** 20, 20), (40000, 2 ** 20, 128), (16, 2 ** 23, 64)])
+def test_sums_of_long_walks(nq, nk, d, kind):
+    """A sum in tensor memory loses up to 2^-23 of itself with every 16 states: longer walks do without."""
+    got, ref = long_walk(kind, nq, nk, d)
+    assert relative(got, ref) <= output_limit(ref, TYPES[kind]), relative(got, ref)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("nq", [24576, 40000])
+@pytest.mark.parametrize("d", [32, 33, 128])
+def test_long_walks_with_a_rising_maximum(nq, d, kind):
+    """Scores that rise along the states, with the first ones masked: what a walk holds is taken over at every reference."""
+    dtype, nk = TYPES[kind], 200000
+    rise = torch.linspace(-1, 1, nk, device="cuda")[:, None, None]
+    q = (1 + 0.3 * rand(1, nq, 1, d)).to(dtype)
+    k, v = (rise * 24 / d + 0.02 * rand(2, nk, 1, d)).to(dtype), (rand(3, nk, 1, d) + rise).to(dtype)
+    keep = (rand(4, nk) < 0.5).to(torch.uint8)
+    keep[:70000] = 0
+    at = uvu.Attention(1, 1, d, i32([0, nq]), i32([0, nk]), scale=1.0)
+    out, lse = torch.empty_like(q), torch.empty(nq, 1, device="cuda")
+    at.fwd(q, k, v, out, lse, keep=keep)
+    rows = torch.arange(0, nq, max(1, nq // 31), device="cuda")
+    j = keep != 0
+    ref, ref_lse = exact_rows(q, k[j], v[j], 1.0, rows)
+    assert (lse[rows, 0].double() - ref_lse).abs().max() <= 1e-4
+    assert relative(out[rows, 0], values(ref)) <= output_limit(values(ref), dtype)
