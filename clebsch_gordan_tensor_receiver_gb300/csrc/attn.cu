@@ -186,7 +186,7 @@ struct Choice {
     int R;              // rows or states of a tile of the backward
     int64_t fwd_tiles;  // tile numbers of the forward
     int fwd, dq, dkv;   // splits
-    bool hold;          // the forward's walks are long: their sums are held in memory
+    bool hold, hold_q, hold_kv;  // walks of the forward, of dq, of dk and dv are long: their sums are held in memory
 };
 Choice choose(const AttnShape& s, int sms) {
     const int64_t group = s.q_heads / s.kv_heads;
@@ -206,12 +206,17 @@ Choice choose(const AttnShape& s, int sms) {
     c.nt = !c.planes && rows_busy(256) >= sms && s.max_q * group > 128 ? 2 : 1;
     c.fwd_tiles = row_tiles(s, 128 * c.nt);
     c.fwd = splits_for(rows_busy(128 * c.nt), s.max_k, 128, sms, c.nt == 1 && s.head_dim <= (c.planes ? 32 : 64) ? 2 : 1, 4);
-    c.hold = !c.planes && s.max_k / c.fwd > 128 * attn_hold_tiles(s.dtype == UVU_F16);
+    const auto held = [&](int64_t walk, int pieces) { return !c.planes && walk / pieces > 128 * attn_hold_tiles(s.dtype == UVU_F16); };
+    c.hold = held(s.max_k, c.fwd);
     const int bwd_blocks = c.planes && s.head_dim <= 32 ? 2 : 1;
     c.dq = splits_for(rows_busy(c.R), s.max_k, 128, sms, bwd_blocks, 1);
     c.dkv = splits_for(states_busy(c.R), s.max_q * group, 128, sms, bwd_blocks, 1);
+    c.hold_q = held(s.max_k, c.dq);
+    c.hold_kv = held(s.max_q * group, c.dkv);
     return c;
 }
+bool joins_q(const Choice& c) { return c.dq > 1 || c.hold_q; }
+bool joins_kv(const Choice& c) { return c.dkv > 1 || c.hold_kv; }
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -225,7 +230,7 @@ void attn_workspace(const AttnShape& s, int sms, size_t* fwd, size_t* bwd) {
     *fwd = c.fwd > 1 ? align256(c.fwd * qh * 4) + align256(c.fwd * qh * s.head_dim * 4) : 0;
     if (c.hold && c.fwd == 1) *fwd = align256(qh * s.head_dim * 4);
     if (c.planes) *fwd += attn_planes_bytes(s, false);
-    const size_t dq = c.dq > 1 ? c.dq * qh * s.head_dim * 4 : 0, dkv = c.dkv > 1 ? 2 * c.dkv * kh * s.head_dim * 4 : 0;
+    const size_t dq = joins_q(c) ? c.dq * qh * s.head_dim * 4 : 0, dkv = joins_kv(c) ? 2 * c.dkv * kh * s.head_dim * 4 : 0;
     *bwd = align256(qh * 4) + align256(dq) + align256(dkv);
     if (s.dtype == UVU_F16) *bwd += align256(qh * 4) + align256(kh * 4) + align256(tops_bytes(s));
     if (c.planes) *bwd += attn_planes_bytes(s, true);
@@ -294,8 +299,9 @@ cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, 
     };
     a.delta = take(size_t(a.nq) * a.Hq * 4);
     a.splits_q = c.dq, a.splits_kv = c.dkv;
-    a.part_q = take(c.dq > 1 ? size_t(c.dq) * n_q * 4 : 0);
-    a.part_kv = take(c.dkv > 1 ? 2 * size_t(c.dkv) * n_kv * 4 : 0);
+    a.part_q = joins_q(c) ? take(size_t(c.dq) * n_q * 4) : nullptr;
+    a.part_kv = joins_kv(c) ? take(2 * size_t(c.dkv) * n_kv * 4) : nullptr;
+    a.hold = c.hold_q || c.hold_kv;
     a.kv_tiles = want_kv ? state_tiles(s, c.R) : 0;
     a.q_tiles = want_q ? row_tiles(s, c.R) : 0;
     if (s.dtype == UVU_F16) {
@@ -345,8 +351,8 @@ cudaError_t launch_attn_bwd(const AttnShape& s, const AttnTensors& t, void* ws, 
         const auto join = [&](int64_t n, int splits, const float* part, void* dst) {
             attn_bwd_join<T><<<blocks(n), kThreads, 0, st>>>(n, splits, part, static_cast<T*>(dst));
         };
-        if (want_q && c.dq > 1) join(n_q, c.dq, a.part_q, a.dq);
-        if (want_kv && c.dkv > 1) {
+        if (want_q && joins_q(c)) join(n_q, c.dq, a.part_q, a.dq);
+        if (want_kv && joins_kv(c)) {
             join(n_kv, c.dkv, a.part_kv, a.dk);
             join(n_kv, c.dkv, a.part_kv + c.dkv * n_kv, a.dv);
         }

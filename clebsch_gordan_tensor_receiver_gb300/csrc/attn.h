@@ -29,13 +29,14 @@ struct AttnArgs {
     // split over the long axis: partial results, joined by a second kernel (1: none)
     int splits;
     float* part_o;    // [splits][nq][Hq][D]; of one walk too where it is held
-    bool hold;        // walks are long (attn_hold_tiles)
+    bool hold;        // walks are long (attn_hold_tiles); in the backward some of them
     float* part_lse;  // [splits][nq][Hq]
     // backward
     int64_t kv_tiles, q_tiles;  // tile numbers of dk and dv, and of dq (0: not asked for)
     bool q_first;
     int splits_kv, splits_q;
-    float *part_kv, *part_q;  // [2][splits_kv][nk][Hkv][D], [splits_q][nq][Hq][D]
+    // [2][splits_kv][nk][Hkv][D], [splits_q][nq][Hq][D]; null: one walk, which is not held
+    float *part_kv, *part_q;
 };
 
 // Tile t of a packed batch whose graph b has (off[b+1] - off[b]) * per rows, R rows a tile:

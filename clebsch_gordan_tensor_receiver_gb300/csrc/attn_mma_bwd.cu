@@ -7,8 +7,8 @@
 //     dq       Q   dO  K   V       dq += dS X1
 //     dk, dv   K   V   Q   dO      dk += dS X1,  dv += P X2      (S and dP transposed: lanes are states)
 // Both kinds of tile are in one launch.  Two sweeps instead of one cost S and dP twice (seven products instead of five),
-// but every sum stays in one CTA's tensor memory: no atomics, and results that do not depend on timing.  An
-// accumulating instruction there loses about 2^-26 of the sum, so 2^15 rows lose 2^-15: below the 16-bit results' rounding.
+// but every sum stays in one CTA's tensor memory: no atomics, and results that do not depend on timing.  Long
+// walks take their sums out of tensor memory on the way (attn_hold_tiles), to fp32 values that the join rounds.
 //
 // Tensor memory: S, dP (128 columns each), then the sums.  P and dS are written as 16-bit values over
 // the part of S and dP that the same thread has read.  Two warpgroups share a tile: warpgroup w takes
@@ -93,7 +93,21 @@ __device__ __forceinline__ void store_grad16(const float (&o)[16], float scale, 
     }
 }
 
-template <typename T, int LG, bool ALIGNED, bool KV>
+// Adds every `step`-th 16 columns of a row's sums from d on to what a long walk holds of them (null: a lane without a gradient).
+static __device__ __noinline__ void hold_sums(uint32_t sums, int d, int step, int d16, int D, float* held, float scale, bool first) {
+    for (; d < d16; d += step) {
+        float o[16];
+        __syncwarp();
+        tmem_ld16(sums + 16 * d, o);
+        tmem_wait_ld(o);
+        if (!held) continue;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (16 * d + i < D) held[16 * d + i] = fmaf(o[i], scale, first ? 0.f : held[16 * d + i]);
+    }
+}
+
+template <typename T, int LG, bool ALIGNED, bool HELD, bool KV>
 __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>& L, int64_t tile, int h) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_dead;
@@ -147,6 +161,11 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
         return kScaled && n_tiles > 0 ? exponent(__uint_as_float(a.do2_top[int64_t(tl.graph) * a.Hkv + h])) : 0;
     };
     constexpr float kLog2e = 1.4426950408889634f;
+    // the sums begin anew at these tiles
+    float* const parts = KV ? a.part_kv : a.part_q;
+    constexpr int kHold = attn_hold_tiles(kScaled);
+    const bool held = HELD && parts && n_tiles > kHold;
+    auto fresh = [&](int j) { return j == 0 || (HELD && held && j % kHold == 0); };
 
     if (warp < 8) {
         // ----------------------------------------------------------------- P and dS
@@ -175,6 +194,14 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
             }
         }
         const float u = KV ? kUnshift * power_of_two(e_ds) : 1.f;
+        // the thread's gradient row, dk: warpgroup 0, dv: warpgroup 1
+        const int64_t n_grads = KV ? a.nk * a.Hkv : a.nq * a.Hq;
+        auto part_row = [&]() { return parts + ((KV && w ? splits + split : split) * n_grads + rh) * a.D; };
+        const float grad_scale = KV && w ? kUnshift : a.scale * power_of_two(-e_ds);
+        auto hold = [&](int j) {
+            hold_sums(t_g + lanes + (KV ? uint32_t(w) * g_cols : 0u), KV ? 0 : w, KV ? 1 : 2, d16, a.D, row < own && keep ? part_row() : nullptr,
+                      grad_scale, j == kHold);
+        };
         const bool tail = (walk.hi - walk.lo) % kRows != 0;
         bool ok = true;
         for (int j = 0; j < n_tiles; ++j) {
@@ -191,6 +218,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
             fence_after();
             float x[2][32];
             if (work) {
+                if (HELD && KV && w == 1 && j > 0 && fresh(j)) hold(j);  // dv of the tile before is complete when S of this one is
 #pragma unroll
                 for (int b = 0; b < 2; ++b) tmem_ld32(tmem + lanes + col + 32 * b, x[b]);
 #pragma unroll
@@ -214,6 +242,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
             if (!ok) break;
             fence_after();
             if (work) {
+                if (HELD && !(KV && w == 1) && j > 0 && fresh(j)) hold(j);  // dk, dq: when dP of this one is
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     float y[32];
@@ -236,12 +265,10 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
             fence_after();
         }
         if (ok && work) {
-            // dk: warpgroup 0, dv: warpgroup 1; dq: the column blocks in turn
-            const int64_t n = KV ? a.nk * a.Hkv : a.nq * a.Hq;
+            // dq: the column blocks in turn
             T* dst = static_cast<T*>(KV ? (w ? a.dv : a.dk) : a.dq) + rh * a.D;
-            float* part = splits > 1 ? (KV ? a.part_kv : a.part_q) + ((KV && w ? splits + split : split) * n + rh) * a.D : nullptr;
+            float* part = parts ? part_row() : nullptr;
             const bool vec = a.D % 8 == 0 && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
-            const float scale = KV && w ? kUnshift : a.scale * power_of_two(-e_ds);
             for (int d = KV ? 0 : w; d < d16; d += KV ? 1 : 2) {
                 float o[16];
                 __syncwarp();
@@ -251,7 +278,13 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] = n_tiles > 0 && keep ? o[i] : 0.f;
-                if (row < own) store_grad16<T>(o, scale, dst, part, 16 * d, a.D, vec);
+                if (HELD && held && row < own && keep) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (16 * d + i < a.D) part[16 * d + i] = fmaf(o[i], grad_scale, part[16 * d + i]);
+                } else if (row < own) {
+                    store_grad16<T>(o, grad_scale, dst, part, 16 * d, a.D, vec);
+                }
             }
         }
     } else if (warp == 8) {
@@ -292,7 +325,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                 if (!ok) break;
                 fence_after();
                 if (KV) {
-                    sum(t_g + g_cols, tmem, stage(2 * j + 1), j == 0);
+                    sum(t_g + g_cols, tmem, stage(2 * j + 1), fresh(j));
                     mma_commit(lead, empty + 8 * L.at(2 * j + 1));
                 }
                 if (j + 1 < n_tiles) {
@@ -303,7 +336,7 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
                 ok = warp_wait(ds_ready, j & 1, dead, status);
                 if (!ok) break;
                 fence_after();
-                sum(t_g, t_dp, stage(2 * j), j == 0);
+                sum(t_g, t_dp, stage(2 * j), fresh(j));
                 mma_commit(lead, empty + 8 * L.at(2 * j));
                 if (j + 1 < n_tiles) {
                     ok = wait_stage(2 * j + 3);
@@ -411,13 +444,13 @@ __device__ __forceinline__ void bwd_tile(const AttnArgs& a, const BwdLayout<KV>&
     }
 }
 
-template <typename T, int LG, bool ALIGNED>
+template <typename T, int LG, bool ALIGNED, bool HELD>
 __global__ void __launch_bounds__(kBwdWarps * 32, 1) attn_bwd_mma(const __grid_constant__ AttnArgs a, BwdLayout<true> Lkv, BwdLayout<false> Lq) {
     const BwdTile t = bwd_tile_of(a);
     if (t.kv)
-        bwd_tile<T, LG, ALIGNED, true>(a, Lkv, t.tile, t.head);
+        bwd_tile<T, LG, ALIGNED, HELD, true>(a, Lkv, t.tile, t.head);
     else
-        bwd_tile<T, LG, ALIGNED, false>(a, Lq, t.tile, t.head);
+        bwd_tile<T, LG, ALIGNED, HELD, false>(a, Lq, t.tile, t.head);
 }
 
 template <typename T>
@@ -431,7 +464,9 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
                           reinterpret_cast<uintptr_t>(a.d_out) |
                           uintptr_t(a.q_row | a.q_head | a.k_row | a.k_head | a.v_row | a.v_head | a.o_row | a.o_head) * 2;
     return by_chunks(a.D, (any & 15u) == 0, [&](auto lg, auto aligned) {
-        auto k = attn_bwd_mma<T, decltype(lg)::value, decltype(aligned)::value>;
+        constexpr int LG = decltype(lg)::value;
+        constexpr bool ALIGNED = decltype(aligned)::value;
+        auto k = a.hold ? attn_bwd_mma<T, LG, ALIGNED, true> : attn_bwd_mma<T, LG, ALIGNED, false>;
         const int smem = std::max(kv.total(), q.total());
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;

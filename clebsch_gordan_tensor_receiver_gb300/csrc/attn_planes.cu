@@ -12,8 +12,8 @@
 //   - P (and dS) are cut into planes by the threads that form them; with X = [X0 | X1 | X2] side by side in
 //     the tile, P0 X, P1 [X0 | X1] and P2 X0 land in columns by order of magnitude: the sums of the small terms
 //     are apart from the large ones, and the threads add them.
-//   - Tensor memory sums each tile afresh; the sums over tiles are fp32 registers (accumulating in tensor
-//     memory loses about 2^-26 of the sum each time, and 3000 rows showed it).  Where the backward has no
+//   - Tensor memory sums each tile afresh; the sums over tiles are fp32 registers (each accumulating
+//     instruction cuts a sum in tensor memory by up to 2^-23 of it, and 3000 rows showed it).  Where the backward has no
 //     registers for that, tensor memory sums 512 rows, the small terms in columns of their own (or 64 rows, all in the
 //     same), and the threads add that to the gradient in memory.
 // Masks, splits and bounded waits as in the 16-bit kernels.

@@ -555,7 +555,8 @@ uvu_status uvu_dropout_bwd(uvu_dtype dtype, int64_t n_draws, int inner, double p
  * in elements (the head_dim values of a head are consecutive; a stride may be any value for an
  * input, zero included; the rows and heads of out must not overlap).  lse [n_q][q_heads] fp32.
  * head_dim is 1 .. 128; q_heads is a multiple of kv_heads.  max_q, max_k: no graph has more rows or
- * states (the split of the work goes by them; wrong values cost time, not correctness).  scale > 0.
+ * states (the split of the work goes by them; smaller values cost time and, with 16-bit operands, where a walk over more
+ * than 16384 rows or states (UVU_F16; 65536 in UVU_BF16) is not announced, up to 2^-27 of a result for each of them).  scale > 0.
  * k_keep [n_k] bytes, or NULL: states with 0 take no part, whatever their k and v hold.  A row
  * without a kept state gets out = 0 and lse = -inf, and a zero gradient, whatever its q and d_out hold; a kept
  * state whose score is -inf weighs nothing.  Otherwise a NaN or infinity in a kept operand gives NaN in the

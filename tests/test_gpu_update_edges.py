@@ -281,3 +281,51 @@ def test_long_walks_with_a_rising_maximum(nq, d, kind):
     ref, ref_lse = exact_rows(q, k[j], v[j], 1.0, rows)
     assert (lse[rows, 0].double() - ref_lse).abs().max() <= 1e-4
     assert relative(out[rows, 0], values(ref)) <= output_limit(values(ref), dtype)
+
+
+def one_sign(dtype, nq, nk, hq, hk, d):
+    """Operands whose gradients' terms are mostly of one sign: v follows k, q and d_out have a mean."""
+    q, k = (rand(1, nq, hq, d) * 0.1 + 0.3).to(dtype), rand(2, nk, hk, d, dtype=dtype)
+    return q, k, (k.float() + 0.1 * rand(3, nk, hk, d)).to(dtype), (rand(4, nq, hq, d) * 0.1 + 1).to(dtype)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 128, 36])
+def test_gradient_sums_over_many_states(d, kind):
+    """dq over 2^21 states, unsplit."""
+    nq, nk, dtype = 20480, 2 ** 21, TYPES[kind]
+    q, k, v, do = one_sign(dtype, nq, nk, 1, 1, d)
+    at = uvu.Attention(1, 1, d, i32([0, nq]), i32([0, nk]))
+    got = gradients(q, k, v, do, at)[0]
+    rows = torch.arange(0, nq, 2000, device="cuda")
+    s = q[rows, 0].double() @ k[:, 0].double().T * at.scale
+    p = torch.softmax(s, 1)
+    dp = do[rows, 0].double() @ v[:, 0].double().T
+    ref = (p * (dp - (p * dp).sum(1, keepdim=True)) * at.scale) @ k[:, 0].double()
+    assert relative(got[rows, 0], values(ref)) <= gradient_limit(values(ref), dtype), relative(got[rows, 0], values(ref))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("masked", [False, True])
+def test_gradient_sums_over_many_rows(masked, kind):
+    """dk and dv of states that 2^19 packed rows attend to, unsplit (152 tiles of states), some of them masked."""
+    nq, nk, hk, group, d, dtype = 2 ** 16, 2432, 8, 8, 64, TYPES[kind]
+    q, k, v, do = one_sign(dtype, nq, nk, hk * group, hk, d)
+    keep = (rand(5, nk) < 1).to(torch.uint8) if masked else None
+    at = uvu.Attention(hk * group, hk, d, i32([0, nq]), i32([0, nk]))
+    dk, dv = gradients(q, k, v, do, at, keep)[1:]
+    j = torch.arange(nk, device="cuda") if keep is None else torch.nonzero(keep)[:, 0]
+    h, some = 5, j[::100]
+    K, V = k[j, h].double(), v[j, h].double()
+    r_dk = r_dv = 0
+    for c in range(0, nq, 4096):
+        Q, dO = (t[c:c + 4096, h * group:(h + 1) * group].reshape(-1, d).double() for t in (q, do))
+        p = torch.softmax(Q @ K.T * at.scale, 1)
+        delta = ((p @ V) * dO).sum(1, keepdim=True)
+        p = p[:, ::100]
+        r_dv = r_dv + p.T @ dO
+        r_dk = r_dk + (p * (dO @ V[::100].T - delta) * at.scale).T @ Q
+    for name, got, ref in (("dk", dk, r_dk), ("dv", dv, r_dv)):
+        assert relative(got[some, h], values(ref)) <= gradient_limit(values(ref), dtype), (name, relative(got[some, h], values(ref)))
+    if masked:
+        assert (dk[keep == 0] == 0).all() and (dv[keep == 0] == 0).all()
