@@ -497,7 +497,8 @@ uvu_status uvu_radial_module_source(uvu_plan_t plan, int hidden, const char **so
  * Types: tensors of UVU_F32, UVU_BF16 or UVU_F16 (UVU_ERR_UNSUPPORTED for UVU_F64), aligned to their
  * element; 16-byte aligned tensors whose rows begin on 16-byte boundaries are read in 16-byte
  * vectors.  Statistics, sums and parameters are fp32, and results are rounded once.
- * Results do not depend on timing: no sum is formed by atomics. */
+ * Results do not depend on timing: blocks do not add to one another's sums (where a sum in memory grows by
+ * atomic instructions, one thread does it, in its own order). */
 
 typedef enum { UVU_ACT_NONE = 0, UVU_ACT_SILU = 1 } uvu_act;
 
@@ -590,7 +591,10 @@ uvu_status uvu_attn_bwd(const uvu_attn_shape *shape, const int32_t *q_offsets, c
                         size_t workspace_bytes, uvu_stream_t stream);
 
 /* Bytes of device workspace of uvu_attn_fwd and uvu_attn_bwd on the current device (either pointer
- * may be NULL). */
+ * may be NULL).  What can be large: fp32 operands are held as planes, 6 bytes for each value of q, k and v
+ * (the backward: of d_out too) with head_dim padded to 16, 32, 64 or 128, so 1.5 times the operands at these and
+ * 2.4 times at 40 or 80; and fp32 sums of out or the gradients, for every piece of a walk that is split (few tiles, or
+ * single rows over many states), once for a walk too long for tensor memory (see max_q, max_k). */
 uvu_status uvu_attn_workspace(const uvu_attn_shape *shape, size_t *fwd_bytes, size_t *bwd_bytes);
 
 /* Status word of the attention kernels on the current device (host pointer; 0 = no kernel gave up a
