@@ -218,8 +218,6 @@ Choice choose(const AttnShape& s, int sms) {
 bool joins_q(const Choice& c) { return c.dq > 1 || c.hold_q; }
 bool joins_kv(const Choice& c) { return c.dkv > 1 || c.hold_kv; }
 
-size_t align256(size_t b) { return (b + 255) / 256 * 256; }
-
 size_t tops_bytes(const AttnShape& s) { return size_t(2) * s.n_graphs * s.kv_heads * 4; }  // do2_top and v2_top
 
 }  // namespace

@@ -54,7 +54,6 @@ struct Div {
 };
 
 struct NormArgs {
-    int64_t rows;        // N
     int graphs, C, G, per;  // per = C / G
     Div by_per, by_slabs, by_size, by_lanes;
     int lanes, par, size;  // threads on a row, rows in parallel, blocks of a cluster
@@ -797,7 +796,6 @@ __global__ void __launch_bounds__(1024) norm_bwd_params(int graphs, int C, const
 
 // ------------------------------------------------------------------------------------ choice
 
-size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 size_t elem_bytes(uvu_dtype t) { return t == UVU_F32 ? 4 : 2; }
 
 // How a call is run.
@@ -954,7 +952,6 @@ cudaError_t bwd_of(const NormArgs& a, const Form& f, uvu_act act, const void* x,
 
 NormArgs norm_args(const NormShape& s, const int32_t* offsets, const float* gamma, const float* beta, float* mean, float* rstd) {
     NormArgs a = {};
-    a.rows = s.rows;
     a.graphs = s.graphs;
     a.C = s.channels;
     a.G = s.groups;

@@ -185,6 +185,8 @@ cudaError_t launch_mix_fwd(const Plan& p, int64_t N, int W, const void* in, cons
                            cudaStream_t st);
 cudaError_t launch_mix_bwd(const Plan& p, int64_t N, int W, const void* in, const void* M, const void* g, void* d_in,
                            void* dM, void* ws, cudaStream_t st);
+// Of the parts of a node-update operator's workspace.
+inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 // dropout.cu
 cudaError_t launch_dropout(uvu_dtype dtype, int64_t n, int inner, uint32_t limit, uint64_t seed, uint64_t offset, const void* x,
                            const void* residual, void* y, int sms, cudaStream_t st);
