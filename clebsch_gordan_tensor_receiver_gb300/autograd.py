@@ -7,7 +7,8 @@ in "Receiver-streaming convolutions for channel-wise UVU tensor products", resul
 column) runs on the library's kernels.  Third derivatives are not provided.
 
 `group_norm`, `cross_attention` and `dropout` are the node-update operators with first derivatives,
-and `node_update` chains them after a convolution.
+and `node_update` chains them after a convolution.  `embedding` and `rms_norm` are the lookup of first features
+and the norm between layers, with first derivatives.
 
 Every tensor is a contiguous CUDA tensor of the plan's dtype in the layouts of include/uvu.h;
 `graph` is a `uvu.Graph` (receiver CSR and transposed CSR) of the same edges.  This module only
@@ -252,3 +253,83 @@ def node_update(m, offsets, context, attention: "uvu.Attention", weights, groups
     s = dropout(a, p, seed, offset, residual=s)
     h = dropout(m * torch.sigmoid(s)[:, :, None], p, seed, offset + (n * u + 7) // 8, inner=d)
     return s, h
+
+
+class _Embedding(torch.autograd.Function):
+    """table -> rows of it (uvu_embed_fwd); backward = uvu_embed_bwd."""
+
+    @staticmethod
+    def forward(ctx, table, index, scale, inner, column):
+        shape = (index.shape[0], table.shape[1]) if inner is None else (index.shape[0], table.shape[1], inner)
+        out = torch.empty(shape, dtype=table.dtype, device=table.device)
+        uvu.embed_fwd(index, table, out, scale=scale, column=column)
+        ctx.save_for_backward(index)
+        ctx.scale, ctx.column, ctx.rows = scale, column, table.shape[0]
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        (index,) = ctx.saved_tensors
+        dtable = torch.empty(ctx.rows, dout.shape[1], dtype=dout.dtype, device=dout.device)
+        uvu.embed_bwd(index, _c(dout), dtable, scale=ctx.scale, column=ctx.column)
+        return dtable, None, None, None, None
+
+
+def embedding(index, table, scale: float = 1.0, inner=None, column: int = 0):
+    """scale * table[index] for index [T] int32 and table [rows][C] (fp32, bf16 or f16): [T][C], or with `inner` the features
+    [T][C][inner] whose `column` (that of a 0e irrep) holds the values and whose others are zero.  An index outside the table
+    gives zeros and takes no gradient."""
+    return _Embedding.apply(_c(table), _c(index), float(scale), None if inner is None else int(inner), int(column))
+
+
+class _RmsNorm(torch.autograd.Function):
+    """(x, gamma) -> y (uvu_rms_norm_fwd); backward = uvu_rms_norm_bwd."""
+
+    @staticmethod
+    def forward(ctx, x, gamma, eps):
+        y = torch.empty_like(x)
+        rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        uvu.rms_norm_fwd(x, gamma, y, rstd, eps=eps)
+        ctx.save_for_backward(x, gamma, rstd)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, gamma, rstd = ctx.saved_tensors
+        dx, dgamma = torch.empty_like(x), torch.empty_like(gamma)
+        uvu.rms_norm_bwd(_c(dy), x, gamma, rstd, dx, dgamma)
+        return dx, dgamma, None
+
+
+class _AddRmsNorm(torch.autograd.Function):
+    """(x, residual, gamma) -> (y, h) (uvu_rms_norm_fwd); backward = uvu_rms_norm_bwd, whose dx is both operands' gradient."""
+
+    @staticmethod
+    def forward(ctx, x, residual, gamma, eps):
+        ctx.set_materialize_grads(False)
+        y, h = torch.empty_like(x), torch.empty_like(x)
+        rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        uvu.rms_norm_fwd(x, gamma, y, rstd, residual=residual, h=h, eps=eps)
+        ctx.save_for_backward(h, gamma, rstd)
+        return y, h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh):
+        h, gamma, rstd = ctx.saved_tensors
+        if dy is None:  # only the stream is used
+            return dh, dh, None if dh is None else torch.zeros_like(gamma), None
+        dx, dgamma = torch.empty_like(h), torch.empty_like(gamma)
+        uvu.rms_norm_bwd(_c(dy), h, gamma, rstd, dx, dgamma, dh=None if dh is None else _c(dh))
+        return dx, dx, dgamma, None
+
+
+def rms_norm(x, gamma, residual=None, eps: float = 1e-5):
+    """y = RMS norm of x [N][C] or [N][C][inner] with gamma [C] fp32, over all values of a row (the components of an irrep share
+    their channel's gamma, so equivariant features stay equivariant).  With a residual, (y, h): h = x + residual is the
+    stream that goes on, and y the norm of it."""
+    if residual is None:
+        return _RmsNorm.apply(_c(x), _c(gamma), float(eps))
+    return _AddRmsNorm.apply(_c(x), _c(residual), _c(gamma), float(eps))

@@ -1303,3 +1303,200 @@ extern "C" uvu_status uvu_attn_bwd(const uvu_attn_shape* shape, const int32_t* q
     if (e != cudaSuccess) return cuda_fail(e, "attention gradient launch");
     return ok();
 }
+
+// ----------------------------------------------------- embedding, RMS norm, weight updates
+namespace uvu {
+namespace {
+
+uvu_status embed_shape(uvu_dtype dtype, int64_t n_tokens, int64_t n_rows, int channels, int inner, int column, double scale,
+                       EmbedShape* s) {
+    UVU_TRY(block_dtype(dtype));
+    if (n_tokens < 0 || n_tokens >= std::numeric_limits<int32_t>::max())
+        return fail(UVU_ERR_INVALID_ARGUMENT, "n_tokens must be in [0, 2^31 - 1)");
+    if (n_rows < 1 || n_rows >= std::numeric_limits<int32_t>::max())
+        return fail(UVU_ERR_INVALID_ARGUMENT, "n_rows must be in [1, 2^31 - 1)");
+    if (channels < 1 || channels > 65536 || inner < 1 || inner > 65536 || int64_t(channels) * inner > (1 << 24))
+        return fail(UVU_ERR_INVALID_ARGUMENT, "channels and inner must be in [1, 65536] and their product at most 2^24");
+    if (column < 0 || column >= inner) return fail(UVU_ERR_INVALID_ARGUMENT, "column must be in [0, inner)");
+    if (!std::isfinite(float(scale))) return fail(UVU_ERR_INVALID_ARGUMENT, "scale must be a finite fp32 value");
+    *s = EmbedShape{dtype, n_tokens, n_rows, channels, inner, column, scale};
+    return UVU_OK;
+}
+
+uvu_status rms_shape(uvu_dtype dtype, int64_t n_rows, int channels, int inner, double eps, RmsShape* s) {
+    UVU_TRY(block_dtype(dtype));
+    if (n_rows < 0 || n_rows >= std::numeric_limits<int32_t>::max())
+        return fail(UVU_ERR_INVALID_ARGUMENT, "n_rows must be in [0, 2^31 - 1)");
+    if (channels < 1 || inner < 1 || channels > 8192 || inner > 8192 || channels * inner > 8192)
+        return fail(UVU_ERR_INVALID_ARGUMENT, "channels * inner must be in [1, 8192]");
+    if (!(eps >= 0) || !std::isfinite(float(eps))) return fail(UVU_ERR_INVALID_ARGUMENT, "eps must be a finite fp32 value >= 0");
+    *s = RmsShape{dtype, n_rows, channels, inner, eps};
+    return UVU_OK;
+}
+
+uvu_status rms_operands(uvu_dtype dtype, const void* x, const void* residual, const float* gamma, const void* h) {
+    UVU_TRY(need_elem(x, dtype, "x"));
+    UVU_TRY(need_elem(gamma, UVU_F32, "gamma"));
+    if (!residual != !h) return fail(UVU_ERR_INVALID_ARGUMENT, "residual and h go together: both or neither");
+    if (residual) {
+        UVU_TRY(need_elem(residual, dtype, "residual"));
+        UVU_TRY(need_elem(h, dtype, "h"));
+    }
+    return UVU_OK;
+}
+
+uvu_status ortho_check(const uvu_ortho_shape* s) {
+    if (!s) return fail(UVU_ERR_INVALID_ARGUMENT, "shape is NULL");
+    UVU_TRY(block_dtype(s->dtype));
+    if (s->n_matrices < 0 || s->n_matrices > 65535) return fail(UVU_ERR_INVALID_ARGUMENT, "n_matrices must be in [0, 65535]");
+    if (s->rows < 1 || s->rows > 16384 || s->cols < 1 || s->cols > 16384)
+        return fail(UVU_ERR_INVALID_ARGUMENT, "rows and cols must be in [1, 16384]");
+    if (s->steps < 0 || s->steps > 64) return fail(UVU_ERR_INVALID_ARGUMENT, "steps must be in [0, 64]");
+    if (s->reserved != 0) return fail(UVU_ERR_INVALID_ARGUMENT, "reserved must be 0");
+    for (double v : {s->a, s->b, s->c, s->scale})
+        if (!std::isfinite(float(v))) return fail(UVU_ERR_INVALID_ARGUMENT, "coefficients and scale must be finite fp32 values");
+    if (!(s->eps >= 0) || !std::isfinite(float(s->eps))) return fail(UVU_ERR_INVALID_ARGUMENT, "eps must be a finite fp32 value >= 0");
+    for (int64_t v : {s->g_matrix, s->g_row, s->o_matrix, s->o_row})
+        if (v < 0 || v > (int64_t(1) << 40)) return fail(UVU_ERR_INVALID_ARGUMENT, "strides must be in [0, 2^40]");
+    if ((s->rows > 1 && s->o_row < s->cols) || (s->n_matrices > 1 && s->o_matrix == 0))
+        return fail(UVU_ERR_INVALID_ARGUMENT, "the rows of out must not overlap");
+    return UVU_OK;
+}
+
+}  // namespace
+}  // namespace uvu
+
+extern "C" uvu_status uvu_embed_fwd(uvu_dtype dtype, int64_t n_tokens, int64_t n_rows, int channels, int inner, int column,
+                                    double scale, const int32_t* index, const void* table, void* out, uvu_stream_t stream) {
+    UVU_RANGE("uvu_embed_fwd");
+    EmbedShape s;
+    UVU_TRY(embed_shape(dtype, n_tokens, n_rows, channels, inner, column, scale, &s));
+    if (n_tokens == 0) return ok();
+    UVU_TRY(need_idx(index, "index"));
+    UVU_TRY(need_elem(table, dtype, "table"));
+    UVU_TRY(need_elem(out, dtype, "out"));
+    int sms = 0;
+    UVU_TRY(sm_count_cached(&sms));
+    cudaError_t e = launch_embed_fwd(s, index, table, out, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "embedding launch");
+    return ok();
+}
+
+extern "C" uvu_status uvu_embed_workspace(uvu_dtype dtype, int64_t n_tokens, int64_t n_rows, int channels, int inner, size_t* bytes) {
+    EmbedShape s;
+    if (!bytes) return fail(UVU_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    UVU_TRY(embed_shape(dtype, n_tokens, n_rows, channels, inner, 0, 1.0, &s));
+    *bytes = embed_workspace(s);
+    return ok();
+}
+
+extern "C" uvu_status uvu_embed_bwd(uvu_dtype dtype, int64_t n_tokens, int64_t n_rows, int channels, int inner, int column,
+                                    double scale, const int32_t* index, const void* dout, void* dtable, void* workspace,
+                                    size_t workspace_bytes, uvu_stream_t stream) {
+    UVU_RANGE("uvu_embed_bwd");
+    EmbedShape s;
+    UVU_TRY(embed_shape(dtype, n_tokens, n_rows, channels, inner, column, scale, &s));
+    UVU_TRY(need_elem(dtable, dtype, "dtable"));
+    if (n_tokens > 0) {
+        UVU_TRY(need_idx(index, "index"));
+        UVU_TRY(need_elem(dout, dtype, "dout"));
+        UVU_TRY(check_workspace(workspace, workspace_bytes, embed_workspace(s), "uvu_embed_workspace"));
+    }
+    int sms = 0;
+    UVU_TRY(sm_count_cached(&sms));
+    cudaError_t e = launch_embed_bwd(s, index, dout, dtable, workspace, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "embedding gradient launch");
+    return ok();
+}
+
+extern "C" uvu_status uvu_rms_norm_fwd(uvu_dtype dtype, int64_t n_rows, int channels, int inner, double eps, const void* x,
+                                       const void* residual, const float* gamma, void* h, void* y, float* rstd, uvu_stream_t stream) {
+    UVU_RANGE("uvu_rms_norm_fwd");
+    RmsShape s;
+    UVU_TRY(rms_shape(dtype, n_rows, channels, inner, eps, &s));
+    if (n_rows == 0) return ok();
+    UVU_TRY(rms_operands(dtype, x, residual, gamma, h));
+    UVU_TRY(need_elem(y, dtype, "y"));
+    if (rstd) UVU_TRY(need_elem(rstd, UVU_F32, "rstd"));
+    if (h && h == y) return fail(UVU_ERR_INVALID_ARGUMENT, "h and y are the same tensor");
+    int sms = 0;
+    UVU_TRY(sm_count_cached(&sms));
+    cudaError_t e = launch_rms_fwd(s, x, residual, gamma, h, y, rstd, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "RMS norm launch");
+    return ok();
+}
+
+extern "C" uvu_status uvu_rms_norm_quant(uvu_dtype dtype, int64_t n_rows, int channels, int inner, double eps, int group, const void* x,
+                                         const void* residual, const float* gamma, void* h, void* q, float* scales,
+                                         uvu_stream_t stream) {
+    UVU_RANGE("uvu_rms_norm_quant");
+    RmsShape s;
+    UVU_TRY(rms_shape(dtype, n_rows, channels, inner, eps, &s));
+    if (group < 0) return fail(UVU_ERR_INVALID_ARGUMENT, "group must be >= 0");
+    if (n_rows == 0) return ok();
+    UVU_TRY(rms_operands(dtype, x, residual, gamma, h));
+    if (!q) return fail(UVU_ERR_INVALID_ARGUMENT, "q is NULL");
+    UVU_TRY(need_elem(scales, UVU_F32, "scales"));
+    int sms = 0;
+    UVU_TRY(sm_count_cached(&sms));
+    cudaError_t e = launch_rms_quant(s, group, x, residual, gamma, h, q, scales, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "RMS norm launch");
+    return ok();
+}
+
+extern "C" uvu_status uvu_rms_norm_workspace(uvu_dtype dtype, int64_t n_rows, int channels, int inner, size_t* bytes) {
+    RmsShape s;
+    if (!bytes) return fail(UVU_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    UVU_TRY(rms_shape(dtype, n_rows, channels, inner, 0.0, &s));
+    int sms = 0;
+    UVU_TRY(sm_count_cached(&sms));
+    *bytes = rms_workspace(s, sms);
+    return ok();
+}
+
+extern "C" uvu_status uvu_rms_norm_bwd(uvu_dtype dtype, int64_t n_rows, int channels, int inner, const void* dy, const void* h,
+                                       const float* gamma, const float* rstd, const void* dh, void* dx, float* dgamma, void* workspace,
+                                       size_t workspace_bytes, uvu_stream_t stream) {
+    UVU_RANGE("uvu_rms_norm_bwd");
+    RmsShape s;
+    UVU_TRY(rms_shape(dtype, n_rows, channels, inner, 0.0, &s));
+    UVU_TRY(need_elem(dgamma, UVU_F32, "dgamma"));
+    int sms = 0;
+    if (n_rows > 0) {
+        UVU_TRY(need_elem(dy, dtype, "dy"));
+        UVU_TRY(need_elem(h, dtype, "h"));
+        UVU_TRY(need_elem(gamma, UVU_F32, "gamma"));
+        UVU_TRY(need_elem(rstd, UVU_F32, "rstd"));
+        if (dh) UVU_TRY(need_elem(dh, dtype, "dh"));
+        UVU_TRY(need_elem(dx, dtype, "dx"));
+        UVU_TRY(sm_count_cached(&sms));
+        UVU_TRY(check_workspace(workspace, workspace_bytes, rms_workspace(s, sms), "uvu_rms_norm_workspace"));
+    }
+    cudaError_t e = launch_rms_bwd(s, dy, h, gamma, rstd, dh, dx, dgamma, workspace, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "RMS norm gradient launch");
+    return ok();
+}
+
+extern "C" uvu_status uvu_orthogonalize_workspace(const uvu_ortho_shape* shape, size_t* bytes) {
+    if (!bytes) return fail(UVU_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    UVU_TRY(ortho_check(shape));
+    *bytes = ortho_workspace(*shape);
+    return ok();
+}
+
+extern "C" uvu_status uvu_orthogonalize(const uvu_ortho_shape* shape, const void* g, void* out, void* workspace, size_t workspace_bytes,
+                                        uvu_stream_t stream) {
+    UVU_RANGE("uvu_orthogonalize");
+    UVU_TRY(ortho_check(shape));
+    if (shape->n_matrices == 0) return ok();
+    UVU_TRY(need_elem(g, shape->dtype, "g"));
+    UVU_TRY(need_elem(out, shape->dtype, "out"));
+    if (g == out && (shape->g_row != shape->o_row || shape->g_matrix != shape->o_matrix))
+        return fail(UVU_ERR_INVALID_ARGUMENT, "out may be g with the same strides only");
+    int sms = 0;
+    UVU_TRY(sm_count_cached(&sms));
+    UVU_TRY(check_workspace(workspace, workspace_bytes, ortho_workspace(*shape), "uvu_orthogonalize_workspace"));
+    cudaError_t e = launch_ortho(*shape, g, out, workspace, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "orthogonalisation launch");
+    return ok();
+}

@@ -190,6 +190,35 @@ inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 // dropout.cu
 cudaError_t launch_dropout(uvu_dtype dtype, int64_t n, int inner, uint32_t limit, uint64_t seed, uint64_t offset, const void* x,
                            const void* residual, void* y, int sms, cudaStream_t st);
+// embed.cu
+struct EmbedShape {
+    uvu_dtype dtype;
+    int64_t tokens, rows;
+    int channels, inner, column;
+    double scale;
+};
+size_t embed_workspace(const EmbedShape& s);
+cudaError_t launch_embed_fwd(const EmbedShape& s, const int32_t* index, const void* table, void* out, int sms, cudaStream_t st);
+cudaError_t launch_embed_bwd(const EmbedShape& s, const int32_t* index, const void* dout, void* dtable, void* ws, int sms,
+                             cudaStream_t st);
+// rms.cu
+struct RmsShape {
+    uvu_dtype dtype;
+    int64_t rows;
+    int channels, inner;
+    double eps;
+};
+size_t rms_workspace(const RmsShape& s, int sms);
+cudaError_t launch_rms_fwd(const RmsShape& s, const void* x, const void* residual, const float* gamma, void* h, void* y, float* rstd,
+                           int sms, cudaStream_t st);
+cudaError_t launch_rms_quant(const RmsShape& s, int group, const void* x, const void* residual, const float* gamma, void* h, void* q,
+                             float* scales, int sms, cudaStream_t st);
+cudaError_t launch_rms_bwd(const RmsShape& s, const void* dy, const void* h, const float* gamma, const float* rstd, const void* dh,
+                           void* dx, float* dgamma, void* ws, int sms, cudaStream_t st);
+// ortho.cu
+using OrthoShape = uvu_ortho_shape;
+size_t ortho_workspace(const OrthoShape& s);
+cudaError_t launch_ortho(const OrthoShape& s, const void* g, void* out, void* ws, int sms, cudaStream_t st);
 // norm.cu
 struct NormShape {
     uvu_dtype dtype;

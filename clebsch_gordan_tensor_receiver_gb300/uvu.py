@@ -41,6 +41,9 @@ EXPORTS = (
     "uvu_radial_hidden_bwd", "uvu_radial_hidden_bwd_workspace",
     "uvu_group_norm_fwd", "uvu_group_norm_bwd", "uvu_group_norm_workspace", "uvu_dropout_fwd", "uvu_dropout_bwd",
     "uvu_attn_fwd", "uvu_attn_bwd", "uvu_attn_workspace", "uvu_attn_device_status",
+    "uvu_embed_fwd", "uvu_embed_bwd", "uvu_embed_workspace",
+    "uvu_rms_norm_fwd", "uvu_rms_norm_quant", "uvu_rms_norm_bwd", "uvu_rms_norm_workspace",
+    "uvu_orthogonalize", "uvu_orthogonalize_workspace",
     "uvu_fma_rate_probe", "uvu_status_string", "uvu_last_error_message",
 )
 
@@ -59,6 +62,14 @@ class AttnShape(ctypes.Structure):
                 + [(f, ctypes.c_int32) for f in ("q_heads", "kv_heads", "head_dim", "reserved")]
                 + [("scale", ctypes.c_double)]
                 + [(f, ctypes.c_int64) for f in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head", "o_row", "o_head")])
+
+
+class OrthoShape(ctypes.Structure):
+    """uvu_ortho_shape of include/uvu.h."""
+
+    _fields_ = ([("dtype", ctypes.c_int)] + [(f, ctypes.c_int32) for f in ("n_matrices", "rows", "cols", "steps", "reserved")]
+                + [(f, ctypes.c_double) for f in ("a", "b", "c", "eps", "scale")]
+                + [(f, ctypes.c_int64) for f in ("g_matrix", "g_row", "o_matrix", "o_row")])
 
 
 def _load():
@@ -117,6 +128,15 @@ def _load():
         "uvu_attn_bwd": [ctypes.POINTER(AttnShape)] + [P] * 13 + [SZ, P],
         "uvu_attn_device_status": [ctypes.POINTER(ctypes.c_uint), I],
         "uvu_attn_workspace": [ctypes.POINTER(AttnShape), ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
+        "uvu_embed_fwd": [I, I64, I64, I, I, I, ctypes.c_double] + [P] * 4,
+        "uvu_embed_bwd": [I, I64, I64, I, I, I, ctypes.c_double] + [P] * 4 + [SZ, P],
+        "uvu_embed_workspace": [I, I64, I64, I, I, ctypes.POINTER(SZ)],
+        "uvu_rms_norm_fwd": [I, I64, I, I, ctypes.c_double] + [P] * 7,
+        "uvu_rms_norm_quant": [I, I64, I, I, ctypes.c_double, I] + [P] * 7,
+        "uvu_rms_norm_bwd": [I, I64, I, I] + [P] * 8 + [SZ, P],
+        "uvu_rms_norm_workspace": [I, I64, I, I, ctypes.POINTER(SZ)],
+        "uvu_orthogonalize": [ctypes.POINTER(OrthoShape), P, P, P, SZ, P],
+        "uvu_orthogonalize_workspace": [ctypes.POINTER(OrthoShape), ctypes.POINTER(SZ)],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -160,7 +180,10 @@ for _n in ("uvu_plan_destroy", "uvu_plan_info", "uvu_plan_cg", "uvu_plan_source"
            "uvu_radial_weights", "uvu_radial_weights_workspace", "uvu_radial_weights_bwd",
            "uvu_radial_weights_bwd_workspace", "uvu_radial_hidden_bwd", "uvu_radial_hidden_bwd_workspace",
            "uvu_group_norm_fwd", "uvu_group_norm_bwd", "uvu_group_norm_workspace", "uvu_dropout_fwd", "uvu_dropout_bwd",
-           "uvu_attn_fwd", "uvu_attn_bwd", "uvu_attn_workspace", "uvu_attn_device_status"):
+           "uvu_attn_fwd", "uvu_attn_bwd", "uvu_attn_workspace", "uvu_attn_device_status",
+           "uvu_embed_fwd", "uvu_embed_bwd", "uvu_embed_workspace",
+           "uvu_rms_norm_fwd", "uvu_rms_norm_quant", "uvu_rms_norm_bwd", "uvu_rms_norm_workspace",
+           "uvu_orthogonalize", "uvu_orthogonalize_workspace"):
     globals()[_n] = _wrap(_n)
 
 
@@ -731,3 +754,150 @@ class Attention:
         uvu_attn_bwd(ctypes.byref(s), self.q_offsets.data_ptr(), self.k_offsets.data_ptr(), self._keep(keep, s.n_k), q.data_ptr(),
                      k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), d_out.data_ptr(), _at(dq), _at(dk), _at(dv), ws,
                      size, _raw_stream(stream, self.device))
+
+
+# ------------------------------------------------- embedding, RMS norm, weight updates
+
+def _components(name, t):
+    """(rows, channels, inner) of a contiguous [rows][channels] or [rows][channels][inner] tensor."""
+    if t.dim() not in (2, 3) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [rows][channels] or [rows][channels][inner]")
+    s = t.shape
+    return (s[0], s[1], 1) if len(s) == 2 else tuple(s)
+
+
+def _embed_checks(index, features, table, names):
+    code, dev = _block_dtype(table), _device(table)
+    n, c, inner = _components(names[0], features)
+    if features.dtype != table.dtype or features.get_device() != dev:
+        raise TypeError(f"{names[0]} must have the type and device of {names[1]}")
+    if table.dim() != 2 or table.shape[1] != c or not table.is_contiguous():
+        raise ValueError(f"{names[1]} must be contiguous [rows][{c}]")
+    import torch
+    if index.dtype != torch.int32 or index.get_device() != dev or index.shape != (n,) or not index.is_contiguous():
+        raise ValueError(f"index must be a contiguous int32 tensor [{n}] on the operands' device")
+    return code, dev, n, table.shape[0], c, inner
+
+
+def embed_fwd(index, table, out, scale=1.0, column=0, stream=None):
+    """out[t] = scale * table[index[t]] (see uvu_embed_fwd): index [T] int32, table [rows][C], out [T][C], or
+    [T][C][inner] with the values in `column` and zeros beside it.  An index outside the table gives zeros."""
+    code, dev, n, rows, c, inner = _embed_checks(index, out, table, ("out", "table"))
+    uvu_embed_fwd(code, n, rows, c, inner, column, scale, index.data_ptr(), table.data_ptr(), out.data_ptr(), _raw_stream(stream, dev))
+
+
+def embed_workspace_bytes(dout, dtable) -> int:
+    """Bytes of device workspace for embed_bwd of these gradients' sizes."""
+    n, c, inner = _components("dout", dout)
+    b = ctypes.c_size_t()
+    uvu_embed_workspace(_block_dtype(dtable), n, dtable.shape[0], c, inner, ctypes.byref(b))
+    return b.value
+
+
+def embed_bwd(index, dout, dtable, scale=1.0, column=0, workspace=None, stream=None):
+    """dtable[r] = scale * sum of dout[t] (its `column`) over the tokens of row r (see uvu_embed_bwd); `workspace`
+    (uint8) is allocated here with torch if None."""
+    code, dev, n, rows, c, inner = _embed_checks(index, dout, dtable, ("dout", "dtable"))
+    need = embed_workspace_bytes(dout, dtable) if workspace is None else 0
+    ws, size, held = _scratch(need, workspace, dev, stream)
+    uvu_embed_bwd(code, n, rows, c, inner, column, scale, index.data_ptr(), dout.data_ptr(), dtable.data_ptr(), ws, size,
+                  _raw_stream(stream, dev))
+
+
+def _rms_checks(x, gamma, residual, h):
+    code, dev = _block_dtype(x), _device(x)
+    n, c, inner = _components("x", x)
+    _f32("gamma", gamma, (c,), dev)
+    if (residual is None) != (h is None):
+        raise ValueError("residual and h go together: both or neither")
+    if residual is not None:
+        _like("residual", residual, x)
+        _like("h", h, x)
+    return code, dev, n, c, inner
+
+
+def rms_norm_fwd(x, gamma, y, rstd=None, residual=None, h=None, eps=1e-5, stream=None):
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * gamma over the rows of x [N][C] or [N][C][inner] (see
+    uvu_rms_norm_fwd); gamma [C] and rstd [N] fp32.  residual and h may be None."""
+    code, dev, n, c, inner = _rms_checks(x, gamma, residual, h)
+    _like("y", y, x)
+    if rstd is not None:
+        _f32("rstd", rstd, (n,), dev)
+    uvu_rms_norm_fwd(code, n, c, inner, eps, x.data_ptr(), _at(residual), gamma.data_ptr(), _at(h), y.data_ptr(), _at(rstd),
+                     _raw_stream(stream, dev))
+
+
+def rms_norm_quant(x, gamma, q, scales, group=128, residual=None, h=None, eps=1e-5, stream=None):
+    """rms_norm_fwd with y in 8 bits (see uvu_rms_norm_quant): q like x in float8_e4m3fn (or uint8), scales [N][groups] fp32, one
+    for `group` consecutive values of a row (0: the whole row)."""
+    code, dev, n, c, inner = _rms_checks(x, gamma, residual, h)
+    if q.element_size() != 1 or q.get_device() != dev or q.shape != x.shape or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous 8-bit tensor of shape {tuple(x.shape)} on x's device")
+    if group < 0 or group >= 2 ** 31:
+        raise ValueError("group must be in [0, 2^31)")
+    _f32("scales", scales, (n, -(-c * inner // group) if group else 1), dev)
+    uvu_rms_norm_quant(code, n, c, inner, eps, group, x.data_ptr(), _at(residual), gamma.data_ptr(), _at(h), q.data_ptr(),
+                       scales.data_ptr(), _raw_stream(stream, dev))
+
+
+def rms_norm_workspace_bytes(h) -> int:
+    """Bytes of device workspace for rms_norm_bwd of h's size."""
+    b = ctypes.c_size_t()
+    uvu_rms_norm_workspace(_block_dtype(h), *_components("h", h), ctypes.byref(b))
+    return b.value
+
+
+def rms_norm_bwd(dy, h, gamma, rstd, dx, dgamma, dh=None, workspace=None, stream=None):
+    """VJP of rms_norm_fwd for the cotangents dy of y and dh of h (see uvu_rms_norm_bwd); dx is the gradient of x and of the
+    residual; `workspace` (uint8) is allocated here with torch if None."""
+    code, dev, n, c, inner = _rms_checks(h, gamma, None, None)
+    _like("dy", dy, h)
+    _like("dx", dx, h)
+    if dh is not None:
+        _like("dh", dh, h)
+    _f32("rstd", rstd, (n,), dev)
+    _f32("dgamma", dgamma, (c,), dev)
+    need = rms_norm_workspace_bytes(h) if workspace is None else 0
+    ws, size, held = _scratch(need, workspace, dev, stream)
+    uvu_rms_norm_bwd(code, n, c, inner, dy.data_ptr(), h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), _at(dh), dx.data_ptr(),
+                     dgamma.data_ptr(), ws, size, _raw_stream(stream, dev))
+
+
+MUON = (3.4445, -4.7750, 2.0315)
+
+
+def _matrices(name, t):
+    """(matrices, rows, cols, matrix stride, row stride) of [rows][cols] or [matrices][rows][cols] with consecutive values in a row."""
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [rows][cols] or [matrices][rows][cols]")
+    (b, m, n), (sb, sm, sn) = ((1, *t.shape), (0, *t.stride())) if t.dim() == 2 else (tuple(t.shape), t.stride())
+    if sn != 1 and n > 1:
+        raise ValueError(f"{name} must have consecutive values in a row")
+    return b, m, n, sb if b > 1 else 0, sm if m > 1 else n
+
+
+def _ortho_shape(g, out, steps, coefficients, eps, scale):
+    code, dev = _block_dtype(g), _device(g)
+    if out.dtype != g.dtype or out.get_device() != dev or out.shape != g.shape:
+        raise TypeError("out must have g's type, device and shape")
+    b, m, n, gm, gr = _matrices("g", g)
+    om, orow = _matrices("out", out)[3:]
+    return dev, OrthoShape(code, b, m, n, steps, 0, *coefficients, eps, scale, gm, gr, om, orow)
+
+
+def orthogonalize_workspace_bytes(g) -> int:
+    """Bytes of device workspace for orthogonalize of g's type and size."""
+    b, m, n = _matrices("g", g)[:3]
+    size = ctypes.c_size_t()
+    shape = OrthoShape(_block_dtype(g), b, m, n, 5, 0, *MUON, 0.0, 1.0, m * n, n, m * n, n)
+    uvu_orthogonalize_workspace(ctypes.byref(shape), ctypes.byref(size))
+    return size.value
+
+
+def orthogonalize(g, out, steps=5, coefficients=MUON, eps=1e-7, scale=1.0, workspace=None, stream=None):
+    """out = scale * (g made nearly orthogonal by `steps` Newton-Schulz steps), for each matrix of g [rows][cols] or
+    [matrices][rows][cols] (see uvu_orthogonalize); out may be g; `workspace` (uint8) is allocated here with torch if None."""
+    dev, shape = _ortho_shape(g, out, steps, coefficients, eps, scale)
+    need = orthogonalize_workspace_bytes(g) if workspace is None else 0
+    ws, size, held = _scratch(need, workspace, dev, stream)
+    uvu_orthogonalize(ctypes.byref(shape), g.data_ptr(), out.data_ptr(), ws, size, _raw_stream(stream, dev))

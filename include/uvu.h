@@ -602,6 +602,83 @@ uvu_status uvu_attn_workspace(const uvu_attn_shape *shape, size_t *fwd_bytes, si
  * the device. */
 uvu_status uvu_attn_device_status(unsigned *word, int reset);
 
+/* ------------------------------------------------- embedding, RMS norm, weight updates ---- */
+
+/* What a model does before its first convolution, between two layers, and to its weight matrices after a
+ * step.  Types, alignment, sums and rounding as for the node-update operators. */
+
+/* The features of n_tokens nodes (or states) from the rows of a table:
+ *     out[t][c][i] = scale table[index[t]][c] for i = column, 0 for the other components
+ * index [n_tokens], table [n_rows][channels], out [n_tokens][channels][inner].  inner = 1, column = 0 is the plain
+ * lookup; inner = D and the column of a 0e irrep give the first features [N][U][D] of a model.  An index outside
+ * [0, n_rows) (padding) gives zeros; the table is not read for it.  n_rows in [1, 2^31 - 1), channels in [1, 65536],
+ * inner in [1, 65536], channels * inner at most 2^24.  Launches: 1 kernel. */
+uvu_status uvu_embed_fwd(uvu_dtype dtype, int64_t n_tokens, int64_t n_rows, int channels, int inner, int column, double scale,
+                         const int32_t *index, const void *table, void *out, uvu_stream_t stream);
+
+/* VJP of uvu_embed_fwd for the cotangent dout [n_tokens][channels][inner], of which only `column` is read:
+ *     dtable[r][c] = scale * sum of dout[t][c][column] over the tokens t with index[t] = r,
+ * all of dtable [n_rows][channels] overwritten, rows without a token with zeros.  The sums are fp32, in an
+ * order that the indices alone determine.  `workspace`: at least uvu_embed_workspace() bytes, 16-byte aligned. */
+uvu_status uvu_embed_bwd(uvu_dtype dtype, int64_t n_tokens, int64_t n_rows, int channels, int inner, int column, double scale,
+                         const int32_t *index, const void *dout, void *dtable, void *workspace, size_t workspace_bytes,
+                         uvu_stream_t stream);
+
+/* Bytes of device workspace of uvu_embed_bwd on the current device. */
+uvu_status uvu_embed_workspace(uvu_dtype dtype, int64_t n_tokens, int64_t n_rows, int channels, int inner, size_t *bytes);
+
+/* Root-mean-square norm of rows with the residual's addition:
+ *     h = x + residual (rounded to the type),  rstd = (mean h^2 + eps)^(-1/2),  y = h rstd gamma
+ * x, residual, h, y [n_rows][channels][inner] contiguous, the mean over the channels * inner values of a row, gamma
+ * [channels] fp32: the components of an irrep share its channel's value, so equivariant features stay equivariant.
+ * The norm is of h as it is stored.  residual and h may both be NULL (h is x then).  rstd [n_rows] fp32 is written for
+ * the backward, or NULL.  channels * inner is at most 8192; eps >= 0 (0 with no row of zeros).  h may be x or residual; y may
+ * be x or residual where h is another one.  The squares are summed in fp32: rows of values beyond 1e19 give zeros.
+ * Launches: 1 kernel. */
+uvu_status uvu_rms_norm_fwd(uvu_dtype dtype, int64_t n_rows, int channels, int inner, double eps, const void *x,
+                            const void *residual, const float *gamma, void *h, void *y, float *rstd, uvu_stream_t stream);
+
+/* The same with y in 8 bits for what reads it (a product with 8-bit operands): for each group of `group` consecutive
+ * values of a row (the last may be shorter; group = 0: the whole row)
+ *     scales[row][g] = max |y| / 448,   q = y / scales[row][g] rounded to e4m3 (zeros where the scale is 0).
+ * q [n_rows][channels * inner] bytes, scales [n_rows][ceil(channels * inner / group)] fp32.  y is fp32 before this rounding.
+ * A NaN makes its group's scale and values NaN.  Launches: 1 kernel. */
+uvu_status uvu_rms_norm_quant(uvu_dtype dtype, int64_t n_rows, int channels, int inner, double eps, int group, const void *x,
+                              const void *residual, const float *gamma, void *h, void *q, float *scales, uvu_stream_t stream);
+
+/* VJP of uvu_rms_norm_fwd for the cotangents dy of y and dh of h (NULL: none), from h and rstd as the forward left them:
+ *     dx = dh + rstd (gamma dy - u mean(gamma dy u)),  u = h rstd;   dgamma[c] = sum of dy u over rows and components
+ * dx is the gradient of x and of the residual.  dx, dgamma [channels] fp32 are overwritten; dx may be dy or dh.  The sums
+ * over the rows are fp32 in a fixed order.  `workspace`: at least uvu_rms_norm_workspace() bytes, 16-byte aligned. */
+uvu_status uvu_rms_norm_bwd(uvu_dtype dtype, int64_t n_rows, int channels, int inner, const void *dy, const void *h,
+                            const float *gamma, const float *rstd, const void *dh, void *dx, float *dgamma, void *workspace,
+                            size_t workspace_bytes, uvu_stream_t stream);
+
+/* Bytes of device workspace of uvu_rms_norm_bwd on the current device. */
+uvu_status uvu_rms_norm_workspace(uvu_dtype dtype, int64_t n_rows, int channels, int inner, size_t *bytes);
+
+/* Updates of weight matrices made nearly orthogonal by Newton-Schulz products, as the Muon optimiser does (Jordan, "Muon: an
+ * optimizer for hidden layers in neural networks", 2024): for each of n_matrices matrices G [rows][cols]
+ *     X = G / (|G|_F + eps);   `steps` times  X <- a X + (b X X^T + c (X X^T)^2) X;   out = scale X
+ * (a tall G is turned before and after, which changes nothing but the work).  Batches are mixing matrices [P][U][W], or
+ * one dense layer.  Strides in elements; the values of a row are consecutive; out may be g with the same strides, and must not
+ * overlap it otherwise.  rows, cols in [1, 16384], steps in [0, 64].  Products are of fp32 accuracy.  A matrix of zeros gives
+ * zeros; one with a NaN or an infinity gives NaN; other matrices of the batch are not affected. */
+typedef struct {
+    uvu_dtype dtype;
+    int32_t n_matrices, rows, cols, steps;
+    int32_t reserved; /* 0 */
+    double a, b, c, eps, scale;
+    int64_t g_matrix, g_row, o_matrix, o_row;
+} uvu_ortho_shape;
+
+/* `workspace`: at least uvu_orthogonalize_workspace() bytes, 16-byte aligned. */
+uvu_status uvu_orthogonalize(const uvu_ortho_shape *shape, const void *g, void *out, void *workspace, size_t workspace_bytes,
+                             uvu_stream_t stream);
+
+/* Bytes of device workspace of uvu_orthogonalize on the current device. */
+uvu_status uvu_orthogonalize_workspace(const uvu_ortho_shape *shape, size_t *bytes);
+
 /* ------------------------------------------------------------------------ measurement ---- */
 
 /* Arithmetic-rate probe, the denominator of the FP32 / FP64 pipe fractions that the benchmark
