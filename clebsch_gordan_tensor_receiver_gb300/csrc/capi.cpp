@@ -1500,3 +1500,12 @@ extern "C" uvu_status uvu_orthogonalize(const uvu_ortho_shape* shape, const void
     if (e != cudaSuccess) return cuda_fail(e, "orthogonalisation launch");
     return ok();
 }
+
+extern "C" uvu_status uvu_orthogonalize_device_status(unsigned* word, int reset) {
+    UVU_RANGE("uvu_orthogonalize_device_status");
+    if (!word) return fail(UVU_ERR_INVALID_ARGUMENT, "word is NULL");
+    cudaError_t e = cudaDeviceSynchronize();  // streams that do not block on the legacy one, too
+    if (e == cudaSuccess) e = ortho_status(word, reset != 0);
+    if (e != cudaSuccess) return cuda_fail(e, "orthogonalisation status");
+    return ok();
+}

@@ -219,6 +219,7 @@ cudaError_t launch_rms_bwd(const RmsShape& s, const void* dy, const void* h, con
 using OrthoShape = uvu_ortho_shape;
 size_t ortho_workspace(const OrthoShape& s);
 cudaError_t launch_ortho(const OrthoShape& s, const void* g, void* out, void* ws, int sms, cudaStream_t st);
+cudaError_t ortho_status(unsigned* word, bool reset);
 // norm.cu
 struct NormShape {
     uvu_dtype dtype;

@@ -43,7 +43,7 @@ EXPORTS = (
     "uvu_attn_fwd", "uvu_attn_bwd", "uvu_attn_workspace", "uvu_attn_device_status",
     "uvu_embed_fwd", "uvu_embed_bwd", "uvu_embed_workspace",
     "uvu_rms_norm_fwd", "uvu_rms_norm_quant", "uvu_rms_norm_bwd", "uvu_rms_norm_workspace",
-    "uvu_orthogonalize", "uvu_orthogonalize_workspace",
+    "uvu_orthogonalize", "uvu_orthogonalize_workspace", "uvu_orthogonalize_device_status",
     "uvu_fma_rate_probe", "uvu_status_string", "uvu_last_error_message",
 )
 
@@ -137,6 +137,7 @@ def _load():
         "uvu_rms_norm_workspace": [I, I64, I, I, ctypes.POINTER(SZ)],
         "uvu_orthogonalize": [ctypes.POINTER(OrthoShape), P, P, P, SZ, P],
         "uvu_orthogonalize_workspace": [ctypes.POINTER(OrthoShape), ctypes.POINTER(SZ)],
+        "uvu_orthogonalize_device_status": [ctypes.POINTER(ctypes.c_uint), I],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -183,7 +184,7 @@ for _n in ("uvu_plan_destroy", "uvu_plan_info", "uvu_plan_cg", "uvu_plan_source"
            "uvu_attn_fwd", "uvu_attn_bwd", "uvu_attn_workspace", "uvu_attn_device_status",
            "uvu_embed_fwd", "uvu_embed_bwd", "uvu_embed_workspace",
            "uvu_rms_norm_fwd", "uvu_rms_norm_quant", "uvu_rms_norm_bwd", "uvu_rms_norm_workspace",
-           "uvu_orthogonalize", "uvu_orthogonalize_workspace"):
+           "uvu_orthogonalize", "uvu_orthogonalize_workspace", "uvu_orthogonalize_device_status"):
     globals()[_n] = _wrap(_n)
 
 
@@ -901,3 +902,10 @@ def orthogonalize(g, out, steps=5, coefficients=MUON, eps=1e-7, scale=1.0, works
     need = orthogonalize_workspace_bytes(g) if workspace is None else 0
     ws, size, held = _scratch(need, workspace, dev, stream)
     uvu_orthogonalize(ctypes.byref(shape), g.data_ptr(), out.data_ptr(), ws, size, _raw_stream(stream, dev))
+
+
+def orthogonalize_device_status(reset: bool = True) -> int:
+    """Status word of the orthogonalisation's kernels on the current device (0 = no timeout)."""
+    w = ctypes.c_uint()
+    uvu_orthogonalize_device_status(ctypes.byref(w), int(reset))
+    return w.value

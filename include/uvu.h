@@ -662,7 +662,8 @@ uvu_status uvu_rms_norm_workspace(uvu_dtype dtype, int64_t n_rows, int channels,
  *     X = G / (|G|_F + eps);   `steps` times  X <- a X + (b X X^T + c (X X^T)^2) X;   out = scale X
  * (a tall G is turned before and after, which changes nothing but the work).  Batches are mixing matrices [P][U][W], or
  * one dense layer.  Strides in elements; the values of a row are consecutive; out may be g with the same strides, and must not
- * overlap it otherwise.  rows, cols in [1, 16384], steps in [0, 64].  Products are of fp32 accuracy.  A matrix of zeros gives
+ * overlap it otherwise.  rows, cols in [1, 16384], steps in [0, 64].  Products are of fp32 accuracy, from two fp16 terms a
+ * value on the tensor cores, for values of X and X X^T up to 250 (Muon's coefficients keep them below 2); beyond, NaN.  A matrix of zeros gives
  * zeros; one with a NaN or an infinity gives NaN; other matrices of the batch are not affected. */
 typedef struct {
     uvu_dtype dtype;
@@ -678,6 +679,9 @@ uvu_status uvu_orthogonalize(const uvu_ortho_shape *shape, const void *g, void *
 
 /* Bytes of device workspace of uvu_orthogonalize on the current device. */
 uvu_status uvu_orthogonalize_workspace(const uvu_ortho_shape *shape, size_t *bytes);
+
+/* Status word of the orthogonalisation's kernels on the current device, as uvu_attn_device_status. */
+uvu_status uvu_orthogonalize_device_status(unsigned *word, int reset);
 
 /* ------------------------------------------------------------------------ measurement ---- */
 
