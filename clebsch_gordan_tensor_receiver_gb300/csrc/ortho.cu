@@ -24,6 +24,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "elem.h"
@@ -56,22 +57,34 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // Ordinary writes, of this block's shared memory or another's, come before asynchronous reads.
 __device__ __forceinline__ void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-// hi in the low half, lo in the high one.
-__device__ __forceinline__ uint32_t split(float v) {
-    const __half hi = __float2half_rn(v);
-    const __half lo = __float2half_rn((v - __half2float(hi)) * kLo);
-    return uint32_t(__half_as_ushort(hi)) | uint32_t(__half_as_ushort(lo)) << 16;
+// Two values' halves, each pair with the first value in the low half.
+__device__ __forceinline__ void split(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+    hi = pack2<__half>(v0, v1);
+    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    const float2 r = fma2(F2(h.x, h.y), F2(-kLo, -kLo), F2(v0, v1) * F2(kLo, kLo)).both();
+    lo = pack2<__half>(r.x, r.y);
 }
-__device__ __forceinline__ float joined(uint32_t hi, uint32_t lo) {
-    return fmaf(__half2float(__ushort_as_half(uint16_t(lo))), kLoInv, __half2float(__ushort_as_half(uint16_t(hi))));
-}
-// Eight values' halves as the 16 bytes of each plane.
-__device__ __forceinline__ void planes_of(const uint32_t (&w)[8], uint4& hi, uint4& lo) {
-    hi = make_uint4(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[4], w[5], 0x5410),
-                    __byte_perm(w[6], w[7], 0x5410));
-    lo = make_uint4(__byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632), __byte_perm(w[4], w[5], 0x7632),
-                    __byte_perm(w[6], w[7], 0x7632));
-}
+// Eight values' halves: the 16 bytes of each plane.
+struct Chunk {
+    uint32_t hi[4], lo[4];
+    __device__ __forceinline__ explicit Chunk(const float* v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split(v[2 * i], v[2 * i + 1], hi[i], lo[i]);
+    }
+    __device__ __forceinline__ Chunk(const char* at, size_t plane) {
+        const uint4 h = *reinterpret_cast<const uint4*>(at), l = *reinterpret_cast<const uint4*>(at + plane);
+        hi[0] = h.x, hi[1] = h.y, hi[2] = h.z, hi[3] = h.w, lo[0] = l.x, lo[1] = l.y, lo[2] = l.z, lo[3] = l.w;
+    }
+    __device__ __forceinline__ void store(char* at, size_t plane) const {
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + plane) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    __device__ __forceinline__ float value(int i) const {
+        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[i >> 1])),
+                     l = __half22float2(*reinterpret_cast<const __half2*>(&lo[i >> 1]));
+        return i & 1 ? fmaf(l.y, kLoInv, h.y) : fmaf(l.x, kLoInv, h.x);
+    }
+};
 // A shared-memory address for an operand's descriptor, which has room for the offset in the block's own memory alone: in a cluster the
 // address also has the block's rank, in its upper byte.
 __device__ __forceinline__ uint32_t own_offset(uint32_t address) { return address & 0x3FFFFu; }
@@ -80,27 +93,56 @@ __device__ __forceinline__ uint32_t in_panel(int r, int c) {
     return uint32_t((r >> 3) * 1024 + (r & 7) * 128 + ((((c >> 3) ^ r) & 7) << 4) + (c & 7) * 2);
 }
 
-// A squared norm in fp32 whatever the values' size: the squares of large and of small ones are summed at scales of their own.
+// The squares' sum of values of any size, in fp32: those of large and of small values at scales of their own.  (The card has little fp64:
+// one thread of a block uses it, at the end.)
 struct Squares {
     float small = 0.f, mid = 0.f, large = 0.f;
     __device__ __forceinline__ void add(float v) {
         v = fabsf(v);
         if (v > 0x1p50f) {
-            v *= 0x1p-60f;
+            v *= 0x1p-90f;
             large = fmaf(v, v, large);
         } else if (v < 0x1p-50f) {
-            v *= 0x1p60f;
+            v *= 0x1p90f;
             small = fmaf(v, v, small);
         } else {
             mid = fmaf(v, v, mid);  // a NaN comes here
         }
     }
-    __device__ __forceinline__ double total() const { return double(small) * 0x1p-120 + double(mid) + double(large) * 0x1p120; }
-};
-__device__ __forceinline__ double warp_sum(double v) {
+    // N values at once, at one scale where nothing that counts is lost below 2^-126 or overflows
+    template <int N>
+    __device__ __forceinline__ void add_all(const float (&v)[N]) {
+        float sum = 0.f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
+        for (int i = 0; i < N; ++i) sum = fmaf(v[i], v[i], sum);
+        if (sum > 0x1p-60f && sum < 0x1p100f) {
+            mid += sum;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) add(v[i]);
+        }
+    }
+    __device__ __forceinline__ void over_warp() {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            small += __shfl_xor_sync(0xffffffffu, small, d);
+            mid += __shfl_xor_sync(0xffffffffu, mid, d);
+            large += __shfl_xor_sync(0xffffffffu, large, d);
+        }
+    }
+    __device__ __forceinline__ double total() const { return double(small) * 0x1p-180 + double(mid) + double(large) * 0x1p180; }
+};
+// Over the block, in thread 0.
+template <int WARPS>
+__device__ __forceinline__ double block_squares(Squares q) {
+    __shared__ Squares s_part[WARPS];
+    q.over_warp();
+    if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = q;
+    __syncthreads();
+    if (threadIdx.x >= 32) return 0;
+    q = threadIdx.x < WARPS ? s_part[threadIdx.x] : Squares();
+    q.over_warp();
+    return threadIdx.x == 0 ? q.total() : 0;
 }
 
 // X's element (r, c) in G: G[r][c], or G[c][r] where G is turned.
@@ -113,23 +155,44 @@ struct Side {
 
 // ------------------------------------------------------------------------------- norm and planes
 
-constexpr int kNormBlocks = 64;  // partial sums of a matrix at most
+constexpr int kNormBlocks = 256;  // partial sums of a matrix at most
 
-template <typename T>
-__global__ void __launch_bounds__(512) norm_kernel(int rows, int cols, int64_t g_matrix, int64_t g_row, const T* g, double* part) {
-    const T* a = g + int64_t(blockIdx.y) * g_matrix;
-    Squares s;
-    for (int r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int c = threadIdx.x; c < cols; c += blockDim.x) s.add(widen(a[r * g_row + c]));
-    __shared__ double s_sum[16];
-    const double v = warp_sum(s.total());
-    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = v;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double t = 0;
-        for (int w = 0; w < 16; ++w) t += s_sum[w];
-        part[blockIdx.y * kNormBlocks + blockIdx.x] = t;
+// V consecutive values at p where all V are inside, else those below `left`; zeros beyond.
+template <typename T, int V>
+__device__ __forceinline__ void load_some(const T* p, int left, bool vec, float (&v)[V]) {
+    if (vec && left >= V) {
+        constexpr int kEach = 16 / int(sizeof(T));
+#pragma unroll
+        for (int i = 0; i < V / kEach; ++i) {
+            const Vec<T, kEach> q = load_vec<T, kEach>(p + i * kEach);
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) v[i * kEach + k] = widen(q.v[k]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = i < left ? widen(p[i]) : 0.f;
     }
+}
+
+// 8 values of a row a thread, 4 times at once.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_kernel(int rows, int cols, int64_t g_matrix, int64_t g_row, bool vec, const T* g, double* part) {
+    const T* a = g + int64_t(blockIdx.y) * g_matrix;
+    const int chunks = (cols + 7) / 8;
+    const int count = rows * chunks;
+    Squares q;
+    for (int i0 = blockIdx.x * 1024; i0 < count; i0 += gridDim.x * 1024) {
+        float v[4][8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * 256 + int(threadIdx.x), r = i / chunks, c = (i - r * chunks) * 8;
+            load_some<T, 8>(a + (i < count ? r * g_row + c : 0), i < count ? cols - c : 0, vec, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) q.add_all(v[u]);
+    }
+    const double total = block_squares<8>(q);
+    if (threadIdx.x == 0) part[blockIdx.y * kNormBlocks + blockIdx.x] = total;
 }
 
 // The factor 1 / (|G| + eps), as two: fp32 does not hold the inverse of the smallest norms.  Zeros stay zeros, with eps = 0 too; an
@@ -151,7 +214,8 @@ __device__ __forceinline__ Factor inverse_norm(const double* part, int parts, do
     if (threadIdx.x < 32) {
         double v = 0;
         for (int i = threadIdx.x; i < parts; i += 32) v += part[i];
-        v = warp_sum(v);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
         if (threadIdx.x == 0) s_inv = Factor(v, eps);
     }
     __syncthreads();
@@ -160,30 +224,39 @@ __device__ __forceinline__ Factor inverse_norm(const double* part, int parts, do
 
 // X_0's planes, a 64 x 64 piece a block: (column panel, half a row block, matrix).
 template <typename T>
-__global__ void __launch_bounds__(256) take_kernel(Side s, const T* g, const double* part, int parts, double eps, int panels, size_t plane,
-                                                   char* x) {
+__global__ void __launch_bounds__(256) take_kernel(Side s, bool vec, const T* g, const double* part, int parts, double eps, int panels,
+                                                   size_t plane, char* x) {
     __shared__ float tile[64][65];
-    const Factor inv = inverse_norm(part + int64_t(blockIdx.z) * kNormBlocks, parts, eps);
     const T* a = g + int64_t(blockIdx.z) * s.matrix;
     const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-    for (int i = threadIdx.x; i < 4096; i += 256) {
-        const int u = i >> 6, v = i & 63;  // lanes along the values that are consecutive in G
-        const int r = r0 + (s.turned ? v : u), c = c0 + (s.turned ? u : v);
-        tile[r - r0][c - c0] = r < s.m && c < s.n ? inv.of(widen(a[s.at(r, c)])) * kHeld : 0.f;
-    }
-    __syncthreads();
-    char* to = x + int64_t(blockIdx.z) * 2 * plane + (int64_t(blockIdx.y >> 1) * panels + blockIdx.x) * kPanel;
-    for (int i = threadIdx.x; i < 512; i += 256) {
-        const int r = i >> 3, c = (i & 7) * 8;
-        uint32_t w[8];
+    // 8 values that are consecutive in G: of row u of the piece, or of the turned one's column u
+    const int u = threadIdx.x >> 3, first = (threadIdx.x & 7) * 8;
+    float v[2][8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = split(tile[r][c + k]);
-        uint4 hi, lo;
-        planes_of(w, hi, lo);
-        const uint32_t at = in_panel((blockIdx.y & 1) * 64 + r, c);
-        *reinterpret_cast<uint4*>(to + at) = hi;
-        *reinterpret_cast<uint4*>(to + plane + at) = lo;
+    for (int i = 0; i < 2; ++i) {
+        const int line = (s.turned ? c0 : r0) + u + 32 * i, at = (s.turned ? r0 : c0) + first;
+        const bool live = line < (s.turned ? s.n : s.m);
+        load_some<T, 8>(a + (live ? line * s.row + at : 0), live ? (s.turned ? s.m : s.n) - at : 0, vec, v[i]);
     }
+    const Factor inv = inverse_norm(part + int64_t(blockIdx.z) * kNormBlocks, parts, eps);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = inv.of(v[i][k]) * kHeld;
+    if (s.turned) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) tile[u + 32 * i][first + k] = v[i][k];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = tile[first + k][u + 32 * i];
+    }
+    char* to = x + int64_t(blockIdx.z) * 2 * plane + (int64_t(blockIdx.y >> 1) * panels + blockIdx.x) * kPanel;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) Chunk(v[i]).store(to + in_panel((blockIdx.y & 1) * 64 + u + 32 * i, first), plane);
 }
 
 // No steps: out = scale X_0.
@@ -197,26 +270,47 @@ __global__ void __launch_bounds__(256) scale_kernel(int rows, int cols, int64_t 
         for (int c = threadIdx.x; c < cols; c += blockDim.x) o[r * o_row + c] = narrow<T>(inv.of(widen(a[r * g_row + c])) * scale);
 }
 
-// Eight results of row r, columns c .. c + 7 of X, to the caller's matrix.
+// A tile of results on its way to the caller's matrix: fp32 in shared memory, [rows][width] with the 16-byte chunks of a row exchanged by
+// its number (width is a multiple of 64), so that rows are written whole.  A turned one is written column by column as it is.
+__device__ __forceinline__ int in_stage(int r, int chunk, int width) { return r * width + ((chunk ^ (r & 15)) << 2); }
+template <int N>
+__device__ __forceinline__ void stage(float* to, int r, int c, int width, const float (&v)[N]) {
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k)
+        *reinterpret_cast<float4*>(to + in_stage(r, c / 4 + k, width)) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+}
+// By `threads` threads: rows r0 .. r0 + 127 and columns c0 .. c0 + width - 1 of the matrix.
 template <typename T>
-__device__ __forceinline__ void give(const Side& s, T* out, bool vec, int r, int c, const float (&v)[8]) {
-    if (r >= s.m) return;
-    if (!s.turned && vec && c + 8 <= s.n) {
-        T* o = out + r * s.row + c;
-        T t[8];
+__device__ __forceinline__ void give_staged(const float* from, int threads, const Side& s, T* out, bool vec, int r0, int c0, int width) {
+    const int chunks = width / 8, rows = min(128, s.m - r0);
+    for (int i = threadIdx.x; i < rows * chunks; i += threads) {
+        const int r = i / chunks, k = i - r * chunks, c = c0 + 8 * k;
+        const float4 x = *reinterpret_cast<const float4*>(from + in_stage(r, 2 * k, width)),
+                     y = *reinterpret_cast<const float4*>(from + in_stage(r, 2 * k + 1, width));
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        T* o = out + (r0 + r) * s.row + c;
+        if (vec && c + 8 <= s.n) {
+            constexpr int kEach = 16 / int(sizeof(T));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = narrow<T>(v[i]);
+            for (int b = 0; b < 8 / kEach; ++b) {
+                Vec<T, kEach> q;
 #pragma unroll
-        for (int i = 0; i < int(sizeof(t) / 16); ++i) {
-            uint4 q;
-            __builtin_memcpy(&q, reinterpret_cast<const char*>(t) + 16 * i, 16);
-            reinterpret_cast<uint4*>(o)[i] = q;
+                for (int e = 0; e < kEach; ++e) q.v[e] = narrow<T>(v[b * kEach + e]);
+                store_vec<T, kEach>(o + b * kEach, q);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < s.n) o[e] = narrow<T>(v[e]);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < s.n) out[s.at(r, c + i)] = narrow<T>(v[i]);
     }
+}
+template <typename T, int N>
+__device__ __forceinline__ void give_turned(const Side& s, T* out, int r, int c, const float (&v)[N]) {
+    if (r >= s.m) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (c + i < s.n) out[s.at(r, c + i)] = narrow<T>(v[i]);
 }
 
 // ------------------------------------------------------------------------------------ one product
@@ -224,7 +318,7 @@ __device__ __forceinline__ void give(const Side& s, T* out, bool vec, int r, int
 enum Kind { kGram, kSquare, kApply, kLast };
 
 struct Product {
-    const char *A, *B, *own;  // panels of 128 rows (B of kApply: the rows are the summed index); own: P of kSquare
+    const char *A, *B, *own;  // panels of 128 rows (B of kApply: the rows are the summed index); own: P of kSquare where b is not 0
     char* out;
     size_t a_plane, b_plane, o_plane;      // bytes of a plane; a matrix has two
     int a_panels, b_panels, o_panels;      // of a row block
@@ -232,7 +326,7 @@ struct Product {
     int k_panels;                          // of 64 summed values
     int tiles;                             // of a matrix
     int m;
-    float a, b, c;
+    float diagonal, b, c;                  // kGram: P + diagonal I; kSquare: c P P + b P + diagonal I
     // kLast
     Side side;
     float scale;
@@ -240,7 +334,9 @@ struct Product {
     void* result;
 };
 
-constexpr int kThreads = 320;  // 8 warps that add up and write, one that loads, one that issues the matrix instructions
+constexpr int kSumWarps = 16;  // they add up and write; then one that loads, and one that issues the matrix instructions
+constexpr int kThreads = (kSumWarps + 2) * 32;
+constexpr int kMaxSplits = 8;  // of a long sum
 constexpr int kRunPanels = 1;  // panels of 64 terms between two readings of the hi hi accumulator
 
 template <int BN>
@@ -293,11 +389,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
             bar_init(empty + 8 * s, 1);
         }
         bar_init(d_full, 1);
-        bar_init(d_free, 8);
+        bar_init(d_free, kSumWarps);
         bar_init(fin, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) tmem_alloc(smem_u32(&s_tmem), L::cols);
+    if (warp == kSumWarps + 1) tmem_alloc(smem_u32(&s_tmem), L::cols);
     fence_before();
     __syncthreads();
     fence_after();
@@ -305,14 +401,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
     volatile int* dead = &s_dead;
     unsigned* status = &ortho_status_word;
 
-    float acc[BN / 2];
-    const int quad = warp & 3, half = (warp >> 2) & 1;
+    constexpr int kCols = BN / 4;  // of a warp
+    float acc[kCols];
+    const int quad = warp & 3, quarter = warp >> 2;
     const int row = quad * 32 + lane;  // of the tile
-    if (warp < 8) {
+    if (warp < kSumWarps) {
         // ------------------------------------------------------------------------- sums
-        const uint32_t from = tmem + uint32_t(half * (BN / 2)) + (uint32_t(quad * 32) << 16);
+        const uint32_t from = tmem + uint32_t(quarter * kCols) + (uint32_t(quad * 32) << 16);
 #pragma unroll
-        for (int c = 0; c < BN / 2; ++c) acc[c] = 0.f;
+        for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
         bool ok = true;
         for (int r = 0; r < runs && ok; ++r) {
             ok = warp_wait(d_full, r & 1, dead, status);
@@ -320,12 +417,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
             fence_after();
             const float f = uncut(4 * min(kRunPanels, nk - r * kRunPanels));
 #pragma unroll
-            for (int b = 0; b < BN / 64; ++b) {
-                float v[32];
-                tmem_ld32(from + 32 * b, v);
+            for (int b = 0; b < kCols / 16; ++b) {
+                float v[16];
+                tmem_ld16(from + 16 * b, v);
                 tmem_wait_ld(v);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) acc[32 * b + c] = fmaf(v[c], f, acc[32 * b + c]);
+                for (int c = 0; c < 16; ++c) acc[16 * b + c] = fmaf(v[c], f, acc[16 * b + c]);
             }
             fence_before();
             __syncwarp();
@@ -335,15 +432,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
         if (ok) {
             fence_after();
 #pragma unroll
-            for (int b = 0; b < BN / 64; ++b) {
-                float v[32];
-                tmem_ld32(from + BN + 32 * b, v);
+            for (int b = 0; b < kCols / 16; ++b) {
+                float v[16];
+                tmem_ld16(from + BN + 16 * b, v);
                 tmem_wait_ld(v);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) acc[32 * b + c] = fmaf(v[c], kLoInv, acc[32 * b + c]);
+                for (int c = 0; c < 16; ++c) acc[16 * b + c] = fmaf(v[c], kLoInv, acc[16 * b + c]);
             }
         }
-    } else if (warp == 8) {
+    } else if (warp == kSumWarps) {
         // ------------------------------------------------------------------------ loads
         if (lane == 0) {
             const char* A = p.A + int64_t(matrix) * 2 * p.a_plane + int64_t(i) * p.a_panels * kPanel;
@@ -413,85 +510,88 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
     }
 
     // a split sum is added up over the cluster: each block takes its share of the columns
-    int c0 = half * (BN / 2), count = BN / 2;  // of the tile; this thread's
+    int c0 = quarter * kCols, count = kCols;  // of the tile; this thread's
     if (K == kGram && splits > 1) {
         cg::cluster_group cluster = cg::this_cluster();
         float* mine = reinterpret_cast<float*>(smem);
         __syncthreads();  // the stages have been read
-        if (warp < 8) {
+        if (warp < kSumWarps) {
 #pragma unroll
-            for (int c = 0; c < BN / 2; ++c) mine[(c0 + c) * 128 + row] = acc[c];
+            for (int c = 0; c < kCols; ++c) mine[(c0 + c) * 128 + row] = acc[c];
         }
         cluster.sync();
-        if (warp < 8) {
-            count = BN / 2 / splits;
-            c0 = part * (BN / splits) + half * count;
+        if (warp < kSumWarps) {
+            const int share = BN / splits;
+            count = max(8, share / 4);
+            c0 = part * share + quarter * count;
+            if (quarter * count >= share) count = 0;
 #pragma unroll
-            for (int c = 0; c < BN / 4; ++c) acc[c] = 0.f;
-            for (int s = 0; s < splits; ++s) {
-                const float* other = cluster.map_shared_rank(mine, s);
+            for (int c = 0; c < kCols / 2; ++c) {
+                float v[kMaxSplits];
 #pragma unroll
-                for (int c = 0; c < BN / 4; ++c)
-                    if (c < count) acc[c] += other[(c0 + c) * 128 + row];
+                for (int s = 0; s < kMaxSplits; ++s)
+                    v[s] = c < count && s < splits ? cluster.map_shared_rank(mine, s)[(c0 + c) * 128 + row] : 0.f;
+                acc[c] = 0.f;
+#pragma unroll
+                for (int s = 0; s < kMaxSplits; ++s) acc[c] += v[s];
             }
         }
         cluster.sync();
     }
 
-    if (warp < 8) {
+    if (warp < kSumWarps) {
         // ----------------------------------------------------------------------- results
         const int R = i * 128 + row;
         if (K == kLast) {
             T* out = static_cast<T*>(p.result) + int64_t(matrix) * p.side.matrix;
             const float f = kHeldInv * kHeldInv * p.scale;
 #pragma unroll
-            for (int k = 0; k < BN / 16; ++k) {
-                float v[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] = acc[8 * k + q] * f;
-                give<T>(p.side, out, p.vec, R, j * BN + c0 + 8 * k, v);
+            for (int c = 0; c < kCols; ++c) acc[c] *= f;
+            if (p.side.turned) {
+                give_turned<T>(p.side, out, R, j * BN + c0, acc);
+            } else {
+                // the stages have been read by the matrix instructions, which are done
+                float* rows = reinterpret_cast<float*>(smem);
+                stage(rows, row, c0, BN, acc);
+                asm volatile("bar.sync 1, %0;" ::"n"(kSumWarps * 32) : "memory");
+                give_staged<T>(rows, kSumWarps * 32, p.side, out, p.vec, i * 128, j * BN, BN);
             }
         } else {
             char* out = p.out + int64_t(matrix) * 2 * p.o_plane;
-            const char* own = K == kSquare ? p.own + int64_t(matrix) * 2 * p.o_plane : nullptr;
+            const float f = K == kSquare ? kHeldInv * p.c : kHeldInv;
 #pragma unroll
-            for (int k = 0; k < BN / 16; ++k) {
+            for (int k = 0; k < kCols / 8; ++k) {
                 const int C = j * BN + c0 + 8 * k;
                 if (8 * k < count && !(kSym && (C >> 7) > i)) {
                     const int64_t at = (int64_t(i) * p.o_panels + (C >> 6)) * kPanel + in_panel(row, C & 63);
-                    uint4 ph, pl;
-                    if (K == kSquare) {
-                        ph = *reinterpret_cast<const uint4*>(own + at);
-                        pl = *reinterpret_cast<const uint4*>(own + p.o_plane + at);
-                    }
-                    uint32_t w[8];
+                    float v[8];
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        float v = acc[8 * k + q] * kHeldInv;
-                        if (K == kSquare) {
-                            const uint32_t h2 = q < 2 ? ph.x : q < 4 ? ph.y : q < 6 ? ph.z : ph.w;
-                            const uint32_t l2 = q < 2 ? pl.x : q < 4 ? pl.y : q < 6 ? pl.z : pl.w;
-                            v = p.c * v + p.b * joined(h2 >> (q & 1 ? 16 : 0), l2 >> (q & 1 ? 16 : 0));
-                            if (C + q == R && R < p.m) v += p.a * kHeld;
-                        }
-                        w[q] = split(v);
+                    for (int q = 0; q < 8; ++q) v[q] = acc[8 * k + q] * f;
+                    if (K == kSquare && p.b != 0.f) {
+                        const Chunk own(p.own + int64_t(matrix) * 2 * p.o_plane + at, p.o_plane);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) v[q] = fmaf(p.b, own.value(q), v[q]);
                     }
-                    uint4 hi, lo;
-                    planes_of(w, hi, lo);
-                    *reinterpret_cast<uint4*>(out + at) = hi;
-                    *reinterpret_cast<uint4*>(out + p.o_plane + at) = lo;
+                    if (kSym && R < p.m && uint32_t(R - C) < 8u) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            if (C + q == R) v[q] += p.diagonal * kHeld;
+                    }
+                    const Chunk w(v);
+                    w.store(out + at, p.o_plane);
                     if (kSym && (C >> 7) < i) {
                         // the block above the diagonal: rows and columns change places.  Two lanes exchange a value of two columns,
                         // so that each has two neighbours of one row
                         const bool odd = lane & 1;
 #pragma unroll
-                        for (int q = 0; q < 8; q += 2) {
-                            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w[q] : w[q + 1], 1);
-                            const uint32_t x = odd ? other : w[q], y = odd ? w[q + 1] : other;
-                            const int r = C + q + (odd ? 1 : 0), c = R & ~1;
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t x = __byte_perm(w.hi[q], w.lo[q], 0x5410), y = __byte_perm(w.hi[q], w.lo[q], 0x7632);
+                            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
+                            const uint32_t left = odd ? other : x, right = odd ? y : other;
+                            const int r = C + 2 * q + (odd ? 1 : 0), c = R & ~1;
                             const int64_t to = (int64_t(r >> 7) * p.o_panels + (c >> 6)) * kPanel + in_panel(r & 127, c & 63);
-                            *reinterpret_cast<uint32_t*>(out + to) = __byte_perm(x, y, 0x5410);
-                            *reinterpret_cast<uint32_t*>(out + p.o_plane + to) = __byte_perm(x, y, 0x7632);
+                            *reinterpret_cast<uint32_t*>(out + to) = __byte_perm(left, right, 0x5410);
+                            *reinterpret_cast<uint32_t*>(out + p.o_plane + to) = __byte_perm(left, right, 0x7632);
                         }
                     }
                 }
@@ -500,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
     }
     fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kSumWarps + 1) {
         fence_after();
         tmem_free(tmem, L::cols);
     }
@@ -511,16 +611,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
 // A cluster has a matrix, each of its blocks up to 256 of X's columns (4 panels) and all of P.  P's terms are summed over the
 // cluster: the blocks' partial sums lie where P will be, each block adds up some rows and writes them to all.
 
-constexpr int kChipThreads = 288, kChipPanels = 4;
+constexpr int kChipThreads = 544, kChipPanels = 4;  // 16 warps that add up and write, one that issues the matrix instructions
 constexpr int kChipSmem = 2 * kChipPanels * kPanel + 4 * kPanel + 1024;
+constexpr int kChipBlocks = 8;  // of a cluster at most
 
 struct Chip {
     Side g, out;
     int panels;  // of a block
     int steps;
-    float a, b, c, scale;
+    float shift, b, c, diagonal, scale;  // a step forms R = P + shift I and M = c R R + b R + diagonal I
     double eps;
-    bool vec;
+    bool vec_in, vec_out;
 };
 
 template <typename T>
@@ -529,17 +630,20 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
     __shared__ uint64_t s_bar;
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
-    __shared__ double s_sum[9], s_norm;
-    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char* xs = smem + 4 * kPanel;  // P: hi panels 0, 1, lo 0, 1; X: hi panels, lo panels
+    __shared__ double s_norm;
+    __shared__ Factor s_factor;
+    char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    char* xs = smem + 4 * kPanel;  // P: hi panels 0, 1, lo 0, 1; X: hi panels, lo panels
     const uint32_t sp = own_offset(uniform(smem_u32(smem))), sx = sp + 4 * kPanel;  // for descriptors
     const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    const bool writes = warp < 16;
     cg::cluster_group cluster = cg::this_cluster();
     const int blocks = int(cluster.num_blocks()), rank = int(cluster.block_rank());
     const int matrix = blockIdx.x / blocks;
     const T* g = gp + int64_t(matrix) * p.g.matrix;
     T* out = op + int64_t(matrix) * p.out.matrix;
     const int c0 = rank * p.panels * 64, width = p.panels * 64;  // this block's columns
+    const int cols = max(0, min(width, p.g.n - c0));             // those inside the matrix
     const uint32_t x_plane = uint32_t(p.panels * kPanel), p_plane = 2 * kPanel;
     const uint32_t bar = smem_u32(&s_bar);
     if (threadIdx.x == 0) {
@@ -547,55 +651,74 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
         bar_init(bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 8) tmem_alloc(smem_u32(&s_tmem), 512);
+    if (warp == 16) tmem_alloc(smem_u32(&s_tmem), 512);
 
-    // the norm, over the cluster
-    Squares sq;
-    const int cols = max(0, min(width, p.g.n - c0));
-    for (int i = threadIdx.x; i < p.g.m * cols; i += kChipThreads) {
-        const int u = p.g.turned ? i / p.g.m : i / cols, v = p.g.turned ? i - u * p.g.m : i - u * cols;
-        sq.add(widen(g[p.g.at(p.g.turned ? v : u, c0 + (p.g.turned ? u : v))]));
+    // X_0.  A thread has 8 columns of a row in each half panel (64 rows of 64 columns): lanes along the values that are consecutive in G
+    float v[2 * kChipPanels][8];
+    auto place = [&](int u, int& r, int& c) {
+        const int t = threadIdx.x;
+        r = p.g.turned ? t & 127 : (u & 1) * 64 + (t >> 3);
+        c = (u >> 1) * 64 + (p.g.turned ? ((u & 1) * 4 + (t >> 7)) * 8 : (t & 7) * 8);
+    };
+    Squares squares;
+    if (writes) {
+#pragma unroll
+        for (int u = 0; u < 2 * kChipPanels; ++u)
+            if (u < 2 * p.panels) {
+                int r, c;
+                place(u, r, c);
+                const int left = r < p.g.m ? cols - c : 0;
+                if (p.g.turned) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[u][k] = k < left ? widen(g[(c0 + c + k) * p.g.row + r]) : 0.f;
+                } else {
+                    load_some<T, 8>(g + (left > 0 ? r * p.g.row + c0 + c : 0), left, p.vec_in, v[u]);
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < 2 * kChipPanels; ++u)
+            if (u < 2 * p.panels) squares.add_all(v[u]);
     }
-    const double w_sum = warp_sum(sq.total());
-    if (lane == 0) s_sum[warp] = w_sum;
     fence_before();
-    __syncthreads();
+    const double sum = block_squares<17>(squares);  // (and the tensor memory's address is there)
     fence_after();
     const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t*>(&s_tmem));
-    if (threadIdx.x == 0) {
-        double t = 0;
-        for (int w = 0; w < 9; ++w) t += s_sum[w];
-        s_norm = t;
-    }
-    if (blocks > 1) cluster.sync();
-    else __syncthreads();
-    double total = 0;
-    for (int b = 0; b < blocks; ++b) total += *cluster.map_shared_rank(&s_norm, b);
-    const Factor inv(total, p.eps);
-
-    // X_0's planes: 8 columns of a row at a time
-    for (int i = threadIdx.x; i < 128 * p.panels * 8; i += kChipThreads) {
-        const int r = p.g.turned ? i & 127 : i / (p.panels * 8), k = p.g.turned ? i >> 7 : i - r * (p.panels * 8);
-        uint32_t w[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const int c = c0 + k * 8 + q;
-            w[q] = split(r < p.g.m && c < p.g.n ? inv.of(widen(g[p.g.at(r, c)])) * kHeld : 0.f);
+    if (threadIdx.x == 0) s_norm = sum;
+    if (blocks > 1) {
+        cluster.sync();
+        if (threadIdx.x == 0) {
+            double total = 0;
+            for (int b = 0; b < blocks; ++b) total += *cluster.map_shared_rank(&s_norm, b);
+            s_factor = Factor(total, p.eps);
         }
-        uint4 hi, lo;
-        planes_of(w, hi, lo);
-        const uint32_t at = uint32_t(k >> 3) * kPanel + in_panel(r, (k & 7) * 8);
-        *reinterpret_cast<uint4*>(xs + at) = hi;
-        *reinterpret_cast<uint4*>(xs + x_plane + at) = lo;
+    } else if (threadIdx.x == 0) {
+        s_factor = Factor(sum, p.eps);
     }
+    __syncthreads();
+    const Factor inv = s_factor;
+    if (writes) {
+#pragma unroll
+        for (int u = 0; u < 2 * kChipPanels; ++u)
+            if (u < 2 * p.panels) {
+                int r, c;
+                place(u, r, c);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[u][k] = inv.of(v[u][k]) * kHeld;
+                Chunk(v[u]).store(xs + (c >> 6) * kPanel + in_panel(r, c & 63), x_plane);
+            }
+    }
+
     volatile int* dead = &s_dead;
     unsigned* status = &ortho_status_word;
-    const int quad = warp & 3, half = (warp >> 2) & 1, row = quad * 32 + lane;
+    const int quad = warp & 3, quarter = warp >> 2, row = quad * 32 + lane;
     const uint32_t lanes = uint32_t(quad * 32) << 16;
-    const uint32_t lead = warp == 8 ? elect_lane() : 0;
-    const int k16 = (p.g.m + 15) / 16;  // of a sum over the rows
-    const uint32_t id_p = mma_desc<__half>(128, false), id_x = mma_desc<__half>(width, true);
-    const int c16 = max(1, (cols + 15) / 16);  // of a sum over this block's columns; one at least: zeros
+    const uint32_t lead = warp == 16 ? elect_lane() : 0;
+    const int k16 = (p.g.m + 15) / 16;            // instructions of a sum over the rows
+    const int c16 = max(1, (cols + 15) / 16);     // and over this block's columns; one at least: zeros
+    const int m16 = 16 * k16;                     // P's rows and columns in use; what lies beyond is read by no sum that counts
+    const bool rows_live = writes && quad * 32 < p.g.m, p_live = rows_live && quarter * 32 < m16;
+    const uint32_t id_p = mma_desc<__half>(m16, false), id_x = mma_desc<__half>(width, true);
+    const bool wide = width > 128;
     uint32_t phase = 0;
     bool ok = true;
     // all writes of operands are done; the instructions that `issue` forms run, and everyone waits for them
@@ -604,7 +727,7 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
         fence_before();
         ok = __syncthreads_and(ok);  // after a wait that was given up the block goes on to the end, for the others' sake
         if (!ok) return;
-        if (warp == 8) {
+        if (warp == 16) {
             fence_after();
             issue();
             mma_commit(lead, bar);
@@ -616,40 +739,41 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
     // Accumulators of a product of up to 128 columns: lo at column 256, hi hi in turn at 0, 128 and 384, so that each cuts a third of
     // the sum a third as often; a wider product has one, and lo at 256.
     auto hi_at = [&](int k) { return tmem + (k % 3 == 2 ? 384u : uint32_t(k % 3) * 128u); };
-    // columns c .. c + 31 of a product of n instructions
-    auto sums = [&](int c, int n, bool wide, float (&v)[32]) {
+    // columns c .. c + 31 of a product of n instructions, as pairs
+    auto sums = [&](int c, int n, bool one, float (&v)[32]) {
         float u[32];
         const uint32_t at = uint32_t(c) + lanes;
         tmem_ld32(tmem + at, v);
         tmem_ld32(tmem + 256 + at, u);
         tmem_wait_ld(v);
         tmem_wait_ld(u);
-        const float f0 = uncut(wide ? n : (n + 2) / 3);
+        const float f0 = uncut(one ? n : (n + 2) / 3) * kHeldInv, lo = kLoInv * kHeldInv;
+        F2 w[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], f0, u[i] * kLoInv);
-        if (!wide)
+        for (int i = 0; i < 16; ++i) w[i] = fma2(F2(v[2 * i], v[2 * i + 1]), F2(f0, f0), F2(u[2 * i], u[2 * i + 1]) * F2(lo, lo));
+        if (!one)
             for (int a = 1; a < min(n, 3); ++a) {
                 tmem_ld32(hi_at(a) + at, u);
                 tmem_wait_ld(u);
-                const float f = uncut((n + 2 - a) / 3);
+                const float f = uncut((n + 2 - a) / 3) * kHeldInv;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = fmaf(u[i], f, v[i]);
+                for (int i = 0; i < 16; ++i) w[i] = fma2(F2(u[2 * i], u[2 * i + 1]), F2(f, f), w[i]);
             }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= kHeldInv;
+        for (int i = 0; i < 16; ++i) {
+            const float2 b = w[i].both();
+            v[2 * i] = b.x, v[2 * i + 1] = b.y;
+        }
     };
-    auto write = [&](unsigned char* to, uint32_t plane, int r, int c, const float* v) {
-        uint32_t w[8];
+    auto on_diagonal = [&](int c, float d, float (&v)[32]) {  // columns c .. c + 31
+        if (row < p.g.m && uint32_t(row - c) < 32u) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) w[q] = split(v[q]);
-        uint4 hi, lo;
-        planes_of(w, hi, lo);
-        const uint32_t at = uint32_t(c >> 6) * kPanel + in_panel(r, c & 63);
-        *reinterpret_cast<uint4*>(to + at) = hi;
-        *reinterpret_cast<uint4*>(to + plane + at) = lo;
+            for (int i = 0; i < 32; ++i)
+                if (c + i == row) v[i] += d * kHeld;
+        }
     };
     for (int step = 0; step < p.steps; ++step) {
-        // P = X X^T
+        // R = X X^T + shift I
         product([&] {
             for (int k = 0; k < c16; ++k) {
                 const uint32_t x = sx + uint32_t(k >> 2) * kPanel;
@@ -660,57 +784,72 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
             }
         });
         if (blocks == 1) {
-            if (warp < 8)
-                for (int b = 0; b < 2; ++b) {
-                    const int c = half * 64 + b * 32;
-                    float v[32];
-                    sums(c, c16, false, v);
+            if (p_live) {
+                const int c = quarter * 32;
+                float v[32];
+                sums(c, c16, false, v);
+                on_diagonal(c, p.shift, v);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) write(smem, p_plane, row, c + 8 * k, v + 8 * k);
-                }
+                for (int k = 0; k < 4; ++k)
+                    Chunk(v + 8 * k).store(smem + (c >> 6) * kPanel + in_panel(row, (c & 63) + 8 * k), p_plane);
+            }
         } else {
             float* part = reinterpret_cast<float*>(smem);  // [128][128], 16-byte chunks of a row exchanged by its number
             auto at = [](int r, int chunk) { return r * 128 + ((chunk ^ (r & 31)) << 2); };
-            if (warp < 8)
-                for (int b = 0; b < 2; ++b) {
-                    const int c = half * 64 + b * 32;
-                    float v[32];
-                    sums(c, c16, false, v);
+            if (p_live) {
+                const int c = quarter * 32;
+                float v[32];
+                sums(c, c16, false, v);
+                if (rank == 0) on_diagonal(c, p.shift, v);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<float4*>(part + at(row, c / 4 + k)) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                }
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<float4*>(part + at(row, c / 4 + k)) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
             cluster.sync();
-            const int rows = 128 / blocks;
-            float v[4][8];  // up to 4 chunks of 8 values a thread (2 blocks)
+            // each block adds up its share of the rows: 8 columns a thread, two times for two blocks of all 128 rows
+            const int chunks = m16 / 8, share = (m16 + blocks - 1) / blocks, tasks = share * chunks;
+            float v[2][8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = threadIdx.x + u * 256;
-                if (warp < 8 && i < rows * 16) {
-                    const int r = rank * rows + (i >> 4), chunk = (i & 15) * 2;
+            for (int u = 0; u < 2; ++u) {
+                const int t = threadIdx.x + u * 512;
+                const int row_of = t / chunks, r = rank * share + row_of;
+                if (writes && t < tasks && r < m16) {
+                    const int chunk = (t - row_of * chunks) * 2;
+                    float4 x[kChipBlocks], y[kChipBlocks];
+#pragma unroll
+                    for (int b = 0; b < kChipBlocks; ++b)
+                        if (b < blocks) {
+                            const float* other = cluster.map_shared_rank(part, b);
+                            x[b] = *reinterpret_cast<const float4*>(other + at(r, chunk));
+                            y[b] = *reinterpret_cast<const float4*>(other + at(r, chunk + 1));
+                        }
 #pragma unroll
                     for (int q = 0; q < 8; ++q) v[u][q] = 0.f;
-                    for (int b = 0; b < blocks; ++b) {
-                        const float* other = cluster.map_shared_rank(part, b);
-                        const float4 x = *reinterpret_cast<const float4*>(other + at(r, chunk)),
-                                     y = *reinterpret_cast<const float4*>(other + at(r, chunk + 1));
-                        v[u][0] += x.x, v[u][1] += x.y, v[u][2] += x.z, v[u][3] += x.w;
-                        v[u][4] += y.x, v[u][5] += y.y, v[u][6] += y.z, v[u][7] += y.w;
-                    }
+#pragma unroll
+                    for (int b = 0; b < kChipBlocks; ++b)
+                        if (b < blocks) {
+                            v[u][0] += x[b].x, v[u][1] += x[b].y, v[u][2] += x[b].z, v[u][3] += x[b].w;
+                            v[u][4] += y[b].x, v[u][5] += y[b].y, v[u][6] += y[b].z, v[u][7] += y[b].w;
+                        }
                 }
             }
             cluster.sync();
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = threadIdx.x + u * 256;
-                if (warp < 8 && i < rows * 16)
-                    for (int b = 0; b < blocks; ++b)
-                        write(cluster.map_shared_rank(smem, b), p_plane, rank * rows + (i >> 4), (i & 15) * 8, v[u]);
+            for (int u = 0; u < 2; ++u) {
+                const int t = threadIdx.x + u * 512;
+                const int row_of = t / chunks, r = rank * share + row_of;
+                if (writes && t < tasks && r < m16) {
+                    const int c = (t - row_of * chunks) * 8;
+                    const Chunk w(v[u]);
+#pragma unroll
+                    for (int b = 0; b < kChipBlocks; ++b)
+                        if (b < blocks) w.store(cluster.map_shared_rank(smem, b) + (c >> 6) * kPanel + in_panel(r, c & 63), p_plane);
+                }
             }
             fence_async_all();
             cluster.sync();
         }
-        // M = a I + b P + c P P, where P was
+        // M = c R R + b R + diagonal I, where R was
         product([&] {
             for (int k = 0; k < k16; ++k) {
                 const uint32_t x = sp + uint32_t(k >> 2) * kPanel;
@@ -720,56 +859,59 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
                 mma_ss(lead, tmem + 256, l, h, id_p, true);
             }
         });
-        if (warp < 8)
-            for (int b = 0; b < 2; ++b) {
-                const int c = half * 64 + b * 32;
-                float v[32];
-                sums(c, k16, false, v);
+        if (p_live) {
+            const int c = quarter * 32;
+            float v[32];
+            sums(c, k16, false, v);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t from = uint32_t(half) * kPanel + in_panel(row, b * 32 + 8 * k);
-                    const uint4 ph = *reinterpret_cast<const uint4*>(smem + from), pl = *reinterpret_cast<const uint4*>(smem + p_plane + from);
-                    const uint32_t h2[4] = {ph.x, ph.y, ph.z, ph.w}, l2[4] = {pl.x, pl.y, pl.z, pl.w};
+            for (int i = 0; i < 32; ++i) v[i] *= p.c;
+            on_diagonal(c, p.diagonal, v);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        float& t = v[8 * k + q];
-                        t = p.c * t + p.b * joined(h2[q >> 1] >> (q & 1 ? 16 : 0), l2[q >> 1] >> (q & 1 ? 16 : 0));
-                        if (c + 8 * k + q == row && row < p.g.m) t += p.a * kHeld;
-                    }
-                    write(smem, p_plane, row, c + 8 * k, v + 8 * k);
+            for (int k = 0; k < 4; ++k) {
+                char* to = smem + (c >> 6) * kPanel + in_panel(row, (c & 63) + 8 * k);
+                if (p.b != 0.f) {
+                    const Chunk own(to, p_plane);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[8 * k + q] = fmaf(p.b, own.value(q), v[8 * k + q]);
                 }
+                Chunk(v + 8 * k).store(to, p_plane);
             }
+        }
         // X = M X
         product([&] {
             for (int k = 0; k < k16; ++k) {
                 const uint32_t m = sp + uint32_t(k >> 2) * kPanel;
                 const uint64_t mh = desc_cols(m, k & 3), ml = desc_cols(m + p_plane, k & 3);
                 const uint64_t xh = desc_rows(sx, k), xl = desc_rows(sx + x_plane, k);
-                mma_ss(lead, width > 128 ? tmem : hi_at(k), mh, xh, id_x, k > (width > 128 ? 0 : 2));
+                mma_ss(lead, wide ? tmem : hi_at(k), mh, xh, id_x, k > (wide ? 0 : 2));
                 mma_ss(lead, tmem + 256, mh, xl, id_x, k > 0);
                 mma_ss(lead, tmem + 256, ml, xh, id_x, true);
             }
         });
-        if (warp < 8)
-            for (int b = half; b < p.panels * 2; b += 2) {
+        const bool last = step + 1 == p.steps, through = last && !p.out.turned;
+        if (rows_live)
+            for (int b = quarter; b < p.panels * 2; b += 4) {
                 float v[32];
-                sums(32 * b, k16, width > 128, v);
+                sums(32 * b, k16, wide, v);
+                if (!last) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (step + 1 < p.steps) {
-                        write(xs, x_plane, row, 32 * b + 8 * k, v + 8 * k);
-                    } else {
-                        float o[8];
+                    for (int k = 0; k < 4; ++k)
+                        Chunk(v + 8 * k).store(xs + (b >> 1) * kPanel + in_panel(row, (b & 1) * 32 + 8 * k), x_plane);
+                } else {
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) o[q] = v[8 * k + q] * (kHeldInv * p.scale);
-                        give<T>(p.out, out, p.vec, row, c0 + 32 * b + 8 * k, o);
-                    }
+                    for (int i = 0; i < 32; ++i) v[i] *= kHeldInv * p.scale;
+                    if (through) stage(reinterpret_cast<float*>(xs), row, 32 * b, width, v);
+                    else give_turned<T>(p.out, out, row, c0 + 32 * b, v);
                 }
             }
+        if (through) {
+            __syncthreads();
+            give_staged<T>(reinterpret_cast<const float*>(xs), kChipThreads, p.out, out, p.vec_out, 0, c0, width);
+        }
     }
     fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         if (!ok) bar_wait_last(bar, phase ^ 1, status);
         __syncwarp();
         fence_after();
@@ -796,11 +938,11 @@ Sizes sizes_of(const OrthoShape& s) {
     z.p_panels = 2 * z.blocks;
     z.x_plane = size_t(z.blocks) * z.x_panels * kPanel;
     z.p_plane = size_t(z.blocks) * z.p_panels * kPanel;
-    z.fits = z.m <= 128 && z.n <= 64 * kChipPanels * 8;
+    z.fits = z.m <= 128 && z.n <= 64 * kChipPanels * kChipBlocks;
     z.chip = z.fits && s.steps > 0;
     const int panels = up(z.n, 64) / 64;
     z.chip_blocks = 1;
-    while (z.chip_blocks < 8 && panels > z.chip_blocks * kChipPanels) z.chip_blocks *= 2;
+    while (z.chip_blocks < kChipBlocks && panels > z.chip_blocks * kChipPanels) z.chip_blocks *= 2;
     z.chip_panels = (panels + z.chip_blocks - 1) / z.chip_blocks;
     return z;
 }
@@ -866,7 +1008,7 @@ cudaError_t product(Product p, int matrices, int columns, int sms, cudaStream_t 
     p.tiles = tiles(wide ? 256 : 128);
     int splits = 1;  // of a long sum, where there are few tiles
     if (K == kGram)
-        while (splits < 8 && int64_t(p.tiles) * matrices * splits * 2 <= sms && p.k_panels >= splits * 2 * 4) splits *= 2;
+        while (splits < kMaxSplits && int64_t(p.tiles) * matrices * splits * 2 <= sms && p.k_panels >= splits * 2 * 4) splits *= 2;
     const int64_t grid = int64_t(p.tiles) * matrices * splits;
     return wide ? launch(product_kernel<256, K, T>, grid, kThreads, splits, Tile<256>::smem, st, p)
                 : launch(product_kernel<128, K, T>, grid, kThreads, splits, Tile<128>::smem, st, p);
@@ -879,38 +1021,47 @@ cudaError_t run(const OrthoShape& s, const void* gp, void* op, void* ws, int sms
     const T* g = static_cast<const T*>(gp);
     T* out = static_cast<T*>(op);
     const Side in = {z.m, z.n, z.turned, s.g_matrix, s.g_row}, to = {z.m, z.n, z.turned, s.o_matrix, s.o_row};
-    const bool vec = ((reinterpret_cast<uintptr_t>(op) | uintptr_t(s.o_row) * sizeof(T) | uintptr_t(s.o_matrix) * sizeof(T)) & 15u) == 0;
+    auto aligned = [](const void* t, int64_t row, int64_t matrix) {
+        return ((reinterpret_cast<uintptr_t>(t) | uintptr_t(row) * sizeof(T) | uintptr_t(matrix) * sizeof(T)) & 15u) == 0;
+    };
+    const bool vec_in = aligned(gp, s.g_row, s.g_matrix), vec_out = aligned(op, s.o_row, s.o_matrix);
+    // a I + b P + c P P = c R R + (a - b^2 / 4c) I with R = P + b / 2c I: near the end, where P is near I, R is small, and so
+    // are its products' errors.  Where b / 2c is not of P's size the sum is formed as it stands.
+    const double half = s.c != 0 ? s.b / (2 * s.c) : 0.0;
+    const bool whole = s.c != 0 && std::fabs(half) <= 2.0;
+    const float shift = whole ? float(half) : 0.f, b = whole ? 0.f : float(s.b);
+    const float diagonal = float(whole ? s.a - s.b * half / 2 : s.a);
     if (z.chip) {
-        const Chip c = {in, to, z.chip_panels, s.steps, float(s.a), float(s.b), float(s.c), float(s.scale), s.eps, vec};
+        const Chip c = {in, to, z.chip_panels, s.steps, shift, b, float(s.c), diagonal, float(s.scale), s.eps, vec_in, vec_out};
         return launch(chip_kernel<T>, int64_t(s.n_matrices) * z.chip_blocks, kChipThreads, z.chip_blocks, kChipSmem, st, c, g, out);
     }
-    const int parts = std::min(kNormBlocks, s.rows);
-    norm_kernel<T><<<dim3(parts, s.n_matrices), 512, 0, st>>>(s.rows, s.cols, s.g_matrix, s.g_row, g, w.norm);
+    const int parts = int(std::min<int64_t>(kNormBlocks, (int64_t(s.rows) * ((s.cols + 7) / 8) + 1023) / 1024));
+    norm_kernel<T><<<dim3(parts, s.n_matrices), 256, 0, st>>>(s.rows, s.cols, s.g_matrix, s.g_row, vec_in, g, w.norm);
     if (s.steps == 0) {
         scale_kernel<T><<<dim3(std::min(s.rows, 1024), s.n_matrices), 256, 0, st>>>(s.rows, s.cols, s.g_matrix, s.g_row, s.o_matrix, s.o_row,
                                                                                    float(s.scale), g, w.norm, parts, s.eps, out);
         return cudaGetLastError();
     }
-    take_kernel<T><<<dim3(z.x_panels, z.blocks * 2, s.n_matrices), 256, 0, st>>>(in, g, w.norm, parts, s.eps, z.x_panels, z.x_plane, w.x[0]);
+    take_kernel<T><<<dim3(z.x_panels, z.blocks * 2, s.n_matrices), 256, 0, st>>>(in, vec_in, g, w.norm, parts, s.eps, z.x_panels, z.x_plane,
+                                                                                 w.x[0]);
     cudaError_t e = cudaGetLastError();
     for (int i = 0; i < s.steps && e == cudaSuccess; ++i) {
         const char* x = w.x[i & 1];
         Product p = {};
         p.blocks = z.blocks, p.m = z.m;
-        p.a = float(s.a), p.b = float(s.b), p.c = float(s.c);
         p.A = p.B = x, p.a_plane = p.b_plane = z.x_plane, p.a_panels = p.b_panels = z.x_panels;
         p.out = w.p, p.o_plane = z.p_plane, p.o_panels = z.p_panels;
-        p.k_panels = up(z.n, 64) / 64;
+        p.k_panels = up(z.n, 64) / 64, p.diagonal = shift;
         e = product<kGram, float>(p, s.n_matrices, z.m, sms, st);
         if (e != cudaSuccess) break;
         p.A = p.B = p.own = w.p, p.a_plane = p.b_plane = z.p_plane, p.a_panels = p.b_panels = z.p_panels;
         p.out = w.q;
-        p.k_panels = up(z.m, 64) / 64;
+        p.k_panels = up(z.m, 64) / 64, p.diagonal = diagonal, p.b = b, p.c = float(s.c);
         e = product<kSquare, float>(p, s.n_matrices, z.m, sms, st);
         if (e != cudaSuccess) break;
         p.A = w.q, p.B = x, p.b_plane = z.x_plane, p.b_panels = z.x_panels;
         p.out = w.x[(i + 1) & 1], p.o_plane = z.x_plane, p.o_panels = z.x_panels;
-        p.side = to, p.scale = float(s.scale), p.vec = vec, p.result = out;
+        p.side = to, p.scale = float(s.scale), p.vec = vec_out, p.result = out;
         e = i + 1 < s.steps ? product<kApply, float>(p, s.n_matrices, z.n, sms, st) : product<kLast, T>(p, s.n_matrices, z.n, sms, st);
     }
     return e;
