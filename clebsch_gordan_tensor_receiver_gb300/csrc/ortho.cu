@@ -54,6 +54,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  "r"(bytes), "r"(bar)
                  : "memory");
 }
+// Launches that follow one another: the next kernel's blocks may begin where there is room, and wait here for this one's end.
+__device__ __forceinline__ void next_may_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Ordinary writes, of this block's shared memory or another's, come before asynchronous reads.
 __device__ __forceinline__ void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
@@ -145,12 +148,11 @@ __device__ __forceinline__ double block_squares(Squares q) {
     return threadIdx.x == 0 ? q.total() : 0;
 }
 
-// X's element (r, c) in G: G[r][c], or G[c][r] where G is turned.
+// X's rows and columns, and where the caller's matrix has them: X[r][c] at r * row + c, or at c * row + r where it is turned.
 struct Side {
     int m, n;
     bool turned;
     int64_t matrix, row;
-    __device__ __forceinline__ int64_t at(int r, int c) const { return turned ? c * row + r : r * row + c; }
 };
 
 // ------------------------------------------------------------------------------- norm and planes
@@ -270,47 +272,61 @@ __global__ void __launch_bounds__(256) scale_kernel(int rows, int cols, int64_t 
         for (int c = threadIdx.x; c < cols; c += blockDim.x) o[r * o_row + c] = narrow<T>(inv.of(widen(a[r * g_row + c])) * scale);
 }
 
-// A tile of results on its way to the caller's matrix: fp32 in shared memory, [rows][width] with the 16-byte chunks of a row exchanged by
-// its number (width is a multiple of 64), so that rows are written whole.  A turned one is written column by column as it is.
-__device__ __forceinline__ int in_stage(int r, int chunk, int width) { return r * width + ((chunk ^ (r & 15)) << 2); }
+// A tile of fp32 sums in shared memory, [rows][width], on its way to panels or to the caller's matrix: rows and columns of it are read
+// by other threads than wrote them, so that global memory is written in whole lines.  The 16-byte chunks of a row are exchanged by its
+// number, so that neither direction meets bank conflicts (width is a multiple of 64).
+__device__ __forceinline__ int in_stage(int r, int chunk, int width) { return r * width + ((chunk ^ ((r ^ (r >> 3)) & 15)) << 2); }
 template <int N>
 __device__ __forceinline__ void stage(float* to, int r, int c, int width, const float (&v)[N]) {
 #pragma unroll
     for (int k = 0; k < N / 4; ++k)
         *reinterpret_cast<float4*>(to + in_stage(r, c / 4 + k, width)) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
 }
-// By `threads` threads: rows r0 .. r0 + 127 and columns c0 .. c0 + width - 1 of the matrix.
+// Columns 8 k .. 8 k + 7 of row r, and rows 8 k .. 8 k + 7 of column c.
+__device__ __forceinline__ void staged_row(const float* from, int r, int k, int width, float (&v)[8]) {
+    const float4 x = *reinterpret_cast<const float4*>(from + in_stage(r, 2 * k, width)),
+                 y = *reinterpret_cast<const float4*>(from + in_stage(r, 2 * k + 1, width));
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+}
+__device__ __forceinline__ void staged_column(const float* from, int c, int k, int width, float (&v)[8]) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = from[in_stage(8 * k + q, c >> 2, width) + (c & 3)];
+}
+// The first `left` of eight values, which lie together.
 template <typename T>
-__device__ __forceinline__ void give_staged(const float* from, int threads, const Side& s, T* out, bool vec, int r0, int c0, int width) {
-    const int chunks = width / 8, rows = min(128, s.m - r0);
-    for (int i = threadIdx.x; i < rows * chunks; i += threads) {
-        const int r = i / chunks, k = i - r * chunks, c = c0 + 8 * k;
-        const float4 x = *reinterpret_cast<const float4*>(from + in_stage(r, 2 * k, width)),
-                     y = *reinterpret_cast<const float4*>(from + in_stage(r, 2 * k + 1, width));
-        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        T* o = out + (r0 + r) * s.row + c;
-        if (vec && c + 8 <= s.n) {
-            constexpr int kEach = 16 / int(sizeof(T));
+__device__ __forceinline__ void give8(T* o, int left, bool vec, const float (&v)[8]) {
+    if (vec && left >= 8) {
+        constexpr int kEach = 16 / int(sizeof(T));
 #pragma unroll
-            for (int b = 0; b < 8 / kEach; ++b) {
-                Vec<T, kEach> q;
+        for (int b = 0; b < 8 / kEach; ++b) {
+            Vec<T, kEach> q;
 #pragma unroll
-                for (int e = 0; e < kEach; ++e) q.v[e] = narrow<T>(v[b * kEach + e]);
-                store_vec<T, kEach>(o + b * kEach, q);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < s.n) o[e] = narrow<T>(v[e]);
+            for (int e = 0; e < kEach; ++e) q.v[e] = narrow<T>(v[b * kEach + e]);
+            store_vec<T, kEach>(o + b * kEach, q);
         }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < left) o[e] = narrow<T>(v[e]);
     }
 }
-template <typename T, int N>
-__device__ __forceinline__ void give_turned(const Side& s, T* out, int r, int c, const float (&v)[N]) {
-    if (r >= s.m) return;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (c + i < s.n) out[s.at(r, c + i)] = narrow<T>(v[i]);
+// By `threads` threads: rows r0 .. r0 + 127 and columns c0 .. c0 + width - 1 of X, along what is consecutive in the caller's matrix.
+template <typename T>
+__device__ __forceinline__ void give(const float* from, int threads, const Side& s, T* out, bool vec, int r0, int c0, int width) {
+    const int chunks = s.turned ? 16 : width / 8;
+    const int lines = s.turned ? min(width, s.n - c0) : min(128, s.m - r0);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < lines * chunks; i += threads) {
+        const int line = i / chunks, k = i - line * chunks;
+        float v[8];
+        if (s.turned) {
+            staged_column(from, line, k, width, v);
+            give8<T>(out + (c0 + line) * s.row + r0 + 8 * k, s.m - r0 - 8 * k, vec, v);
+        } else {
+            staged_row(from, line, k, width, v);
+            give8<T>(out + (r0 + line) * s.row + c0 + 8 * k, s.n - c0 - 8 * k, vec, v);
+        }
+    }
 }
 
 // ------------------------------------------------------------------------------------ one product
@@ -348,6 +364,8 @@ struct Tile {
     static constexpr int cols = BN == 256 ? 512 : 256;                    // of tensor memory
 };
 
+__device__ __forceinline__ void sum_warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSumWarps * 32) : "memory"); }
+
 template <int BN, Kind K, typename T>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
     using L = Tile<BN>;
@@ -382,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
     const int k0 = int(int64_t(p.k_panels) * part / splits), k1 = int(int64_t(p.k_panels) * (part + 1) / splits), nk = k1 - k0;
     const int runs = (nk + kRunPanels - 1) / kRunPanels;
 
+    next_may_begin();
     if (threadIdx.x == 0) {
         s_dead = 0;
         for (int s = 0; s < L::stages; ++s) {
@@ -400,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
     const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t*>(&s_tmem));
     volatile int* dead = &s_dead;
     unsigned* status = &ortho_status_word;
+    wait_for_last();  // its results are read, and what it read is written
 
     constexpr int kCols = BN / 4;  // of a warp
     float acc[kCols];
@@ -509,95 +529,75 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
         __syncwarp();
     }
 
-    // a split sum is added up over the cluster: each block takes its share of the columns
-    int c0 = quarter * kCols, count = kCols;  // of the tile; this thread's
-    if (K == kGram && splits > 1) {
-        cg::cluster_group cluster = cg::this_cluster();
-        float* mine = reinterpret_cast<float*>(smem);
-        __syncthreads();  // the stages have been read
-        if (warp < kSumWarps) {
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) mine[(c0 + c) * 128 + row] = acc[c];
-        }
-        cluster.sync();
-        if (warp < kSumWarps) {
-            const int share = BN / splits;
-            count = max(8, share / 4);
-            c0 = part * share + quarter * count;
-            if (quarter * count >= share) count = 0;
-#pragma unroll
-            for (int c = 0; c < kCols / 2; ++c) {
-                float v[kMaxSplits];
-#pragma unroll
-                for (int s = 0; s < kMaxSplits; ++s)
-                    v[s] = c < count && s < splits ? cluster.map_shared_rank(mine, s)[(c0 + c) * 128 + row] : 0.f;
-                acc[c] = 0.f;
-#pragma unroll
-                for (int s = 0; s < kMaxSplits; ++s) acc[c] += v[s];
-            }
-        }
-        cluster.sync();
-    }
-
+    // ------------------------------------------------------------------------------ results
+    float* sums = reinterpret_cast<float*>(smem);  // where the stages were: the instructions that read them are done
     if (warp < kSumWarps) {
-        // ----------------------------------------------------------------------- results
-        const int R = i * 128 + row;
         if (K == kLast) {
-            T* out = static_cast<T*>(p.result) + int64_t(matrix) * p.side.matrix;
-            const float f = kHeldInv * kHeldInv * p.scale;
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) acc[c] *= f;
-            if (p.side.turned) {
-                give_turned<T>(p.side, out, R, j * BN + c0, acc);
-            } else {
-                // the stages have been read by the matrix instructions, which are done
-                float* rows = reinterpret_cast<float*>(smem);
-                stage(rows, row, c0, BN, acc);
-                asm volatile("bar.sync 1, %0;" ::"n"(kSumWarps * 32) : "memory");
-                give_staged<T>(rows, kSumWarps * 32, p.side, out, p.vec, i * 128, j * BN, BN);
-            }
+            for (int c = 0; c < kCols; ++c) acc[c] *= kHeldInv * kHeldInv * p.scale;
+        }
+        stage(sums, row, quarter * kCols, BN, acc);
+    }
+    if (K == kGram && splits > 1) cg::this_cluster().sync();
+    if (warp < kSumWarps) {
+        sum_warps_sync();
+        if (K == kLast) {
+            give<T>(sums, kSumWarps * 32, p.side, static_cast<T*>(p.result) + int64_t(matrix) * p.side.matrix, p.vec, i * 128, j * BN, BN);
         } else {
+            // a split sum is added up over the cluster: each block takes its share of the columns
+            const int share = BN / splits, first = part * share, shift = 31 - __clz(share / 8);
             char* out = p.out + int64_t(matrix) * 2 * p.o_plane;
-            const float f = K == kSquare ? kHeldInv * p.c : kHeldInv;
+            // rolled loops: a block runs this once, and unrolled code took longer to fetch than to run
+#pragma unroll 1
+            for (int t = threadIdx.x; t < 128 << shift; t += kSumWarps * 32) {
+                const int r = t >> shift, k = (first >> 3) + (t & ((1 << shift) - 1)), R = i * 128 + r, C = j * BN + 8 * k;
+                if (kSym && (C >> 7) > i) continue;  // above the diagonal
+                float v[8];
+                staged_row(sums, r, k, BN, v);
+                if (K == kGram && splits > 1) {
+                    staged_row(cg::this_cluster().map_shared_rank(sums, 0), r, k, BN, v);
+                    for (int b = 1; b < splits; ++b) {
+                        float u[8];
+                        staged_row(cg::this_cluster().map_shared_rank(sums, b), r, k, BN, u);
 #pragma unroll
-            for (int k = 0; k < kCols / 8; ++k) {
-                const int C = j * BN + c0 + 8 * k;
-                if (8 * k < count && !(kSym && (C >> 7) > i)) {
-                    const int64_t at = (int64_t(i) * p.o_panels + (C >> 6)) * kPanel + in_panel(row, C & 63);
+                        for (int q = 0; q < 8; ++q) v[q] += u[q];
+                    }
+                }
+                const int64_t at = (int64_t(i) * p.o_panels + (C >> 6)) * kPanel + in_panel(r, C & 63);
+                const float f = K == kSquare ? kHeldInv * p.c : kHeldInv;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] *= f;
+                if (K == kSquare && p.b != 0.f) {
+                    const Chunk own(p.own + int64_t(matrix) * 2 * p.o_plane + at, p.o_plane);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[q] = fmaf(p.b, own.value(q), v[q]);
+                }
+                if (kSym && R < p.m && uint32_t(R - C) < 8u) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (C + q == R) v[q] += p.diagonal * kHeld;
+                }
+                Chunk(v).store(out + at, p.o_plane);
+                if (kSym && (C >> 7) < i) {  // for the block above the diagonal
+                    *reinterpret_cast<float4*>(sums + in_stage(r, 2 * k, BN)) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4*>(sums + in_stage(r, 2 * k + 1, BN)) = make_float4(v[4], v[5], v[6], v[7]);
+                }
+            }
+            if (kSym) {
+                sum_warps_sync();
+                // rows and columns change places
+                const int columns = min(share, (i - j * (BN / 128)) * 128 - first);  // those of blocks below the diagonal
+#pragma unroll 1
+                for (int t = threadIdx.x; t < columns * 16; t += kSumWarps * 32) {
+                    const int c = first + (t >> 4), k = t & 15, C = j * BN + c;
                     float v[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] = acc[8 * k + q] * f;
-                    if (K == kSquare && p.b != 0.f) {
-                        const Chunk own(p.own + int64_t(matrix) * 2 * p.o_plane + at, p.o_plane);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) v[q] = fmaf(p.b, own.value(q), v[q]);
-                    }
-                    if (kSym && R < p.m && uint32_t(R - C) < 8u) {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            if (C + q == R) v[q] += p.diagonal * kHeld;
-                    }
-                    const Chunk w(v);
-                    w.store(out + at, p.o_plane);
-                    if (kSym && (C >> 7) < i) {
-                        // the block above the diagonal: rows and columns change places.  Two lanes exchange a value of two columns,
-                        // so that each has two neighbours of one row
-                        const bool odd = lane & 1;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t x = __byte_perm(w.hi[q], w.lo[q], 0x5410), y = __byte_perm(w.hi[q], w.lo[q], 0x7632);
-                            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
-                            const uint32_t left = odd ? other : x, right = odd ? y : other;
-                            const int r = C + 2 * q + (odd ? 1 : 0), c = R & ~1;
-                            const int64_t to = (int64_t(r >> 7) * p.o_panels + (c >> 6)) * kPanel + in_panel(r & 127, c & 63);
-                            *reinterpret_cast<uint32_t*>(out + to) = __byte_perm(left, right, 0x5410);
-                            *reinterpret_cast<uint32_t*>(out + p.o_plane + to) = __byte_perm(left, right, 0x7632);
-                        }
-                    }
+                    staged_column(sums, c, k, BN, v);
+                    Chunk(v).store(out + (int64_t(C >> 7) * p.o_panels + 2 * i + (k >> 3)) * kPanel + in_panel(C & 127, (k & 7) * 8), p.o_plane);
                 }
             }
         }
     }
+    if (K == kGram && splits > 1) cg::this_cluster().sync();  // the others have read this block's sums
     fence_before();
     __syncthreads();
     if (warp == kSumWarps + 1) {
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
     bool ok = true;
     // all writes of operands are done; the instructions that `issue` forms run, and everyone waits for them
     auto product = [&](auto issue) {
-        fence_async_all();
+        fence_async();
         fence_before();
         ok = __syncthreads_and(ok);  // after a wait that was given up the block goes on to the end, for the others' sake
         if (!ok) return;
@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
                 mma_ss(lead, tmem + 256, ml, xh, id_x, true);
             }
         });
-        const bool last = step + 1 == p.steps, through = last && !p.out.turned;
+        const bool last = step + 1 == p.steps;
         if (rows_live)
             for (int b = quarter; b < p.panels * 2; b += 4) {
                 float v[32];
@@ -900,13 +900,12 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] *= kHeldInv * p.scale;
-                    if (through) stage(reinterpret_cast<float*>(xs), row, 32 * b, width, v);
-                    else give_turned<T>(p.out, out, row, c0 + 32 * b, v);
+                    stage(reinterpret_cast<float*>(xs), row, 32 * b, width, v);
                 }
             }
-        if (through) {
+        if (last) {
             __syncthreads();
-            give_staged<T>(reinterpret_cast<const float*>(xs), kChipThreads, p.out, out, p.vec_out, 0, c0, width);
+            give<T>(reinterpret_cast<const float*>(xs), kChipThreads, p.out, out, p.vec_out, 0, c0, width);
         }
     }
     fence_before();
@@ -974,8 +973,9 @@ Parts parts_of(const OrthoShape& s, const Sizes& z, void* ws) {
     return p;
 }
 
+// follows: the kernel waits for the launch before it itself.
 template <typename... P, typename... Q>
-cudaError_t launch(void (*k)(P...), int64_t blocks, int threads, int cluster, size_t smem, cudaStream_t st, Q... args) {
+cudaError_t launch(void (*k)(P...), int64_t blocks, int threads, int cluster, bool follows, size_t smem, cudaStream_t st, Q... args) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t c = {};
@@ -983,12 +983,14 @@ cudaError_t launch(void (*k)(P...), int64_t blocks, int threads, int cluster, si
     c.blockDim = dim3(unsigned(threads));
     c.dynamicSmemBytes = smem;
     c.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = unsigned(cluster);
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    c.attrs = &at;
-    c.numAttrs = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = unsigned(cluster);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at;
+    c.numAttrs = follows ? 2 : 1;
     return cudaLaunchKernelEx(&c, k, static_cast<P>(args)...);
 }
 
@@ -1010,8 +1012,8 @@ cudaError_t product(Product p, int matrices, int columns, int sms, cudaStream_t 
     if (K == kGram)
         while (splits < kMaxSplits && int64_t(p.tiles) * matrices * splits * 2 <= sms && p.k_panels >= splits * 2 * 4) splits *= 2;
     const int64_t grid = int64_t(p.tiles) * matrices * splits;
-    return wide ? launch(product_kernel<256, K, T>, grid, kThreads, splits, Tile<256>::smem, st, p)
-                : launch(product_kernel<128, K, T>, grid, kThreads, splits, Tile<128>::smem, st, p);
+    return wide ? launch(product_kernel<256, K, T>, grid, kThreads, splits, true, Tile<256>::smem, st, p)
+                : launch(product_kernel<128, K, T>, grid, kThreads, splits, true, Tile<128>::smem, st, p);
 }
 
 template <typename T>
@@ -1033,7 +1035,7 @@ cudaError_t run(const OrthoShape& s, const void* gp, void* op, void* ws, int sms
     const float diagonal = float(whole ? s.a - s.b * half / 2 : s.a);
     if (z.chip) {
         const Chip c = {in, to, z.chip_panels, s.steps, shift, b, float(s.c), diagonal, float(s.scale), s.eps, vec_in, vec_out};
-        return launch(chip_kernel<T>, int64_t(s.n_matrices) * z.chip_blocks, kChipThreads, z.chip_blocks, kChipSmem, st, c, g, out);
+        return launch(chip_kernel<T>, int64_t(s.n_matrices) * z.chip_blocks, kChipThreads, z.chip_blocks, false, kChipSmem, st, c, g, out);
     }
     const int parts = int(std::min<int64_t>(kNormBlocks, (int64_t(s.rows) * ((s.cols + 7) / 8) + 1023) / 1024));
     norm_kernel<T><<<dim3(parts, s.n_matrices), 256, 0, st>>>(s.rows, s.cols, s.g_matrix, s.g_row, vec_in, g, w.norm);
