@@ -201,7 +201,7 @@ size_t embed_workspace(const EmbedShape& s);
 cudaError_t launch_embed_fwd(const EmbedShape& s, const int32_t* index, const void* table, void* out, int sms, cudaStream_t st);
 cudaError_t launch_embed_bwd(const EmbedShape& s, const int32_t* index, const void* dout, void* dtable, void* ws, int sms,
                              cudaStream_t st);
-// rms.cu
+// rms_fwd.cu, rms_quant.cu, rms_bwd.cu
 struct RmsShape {
     uvu_dtype dtype;
     int64_t rows;

@@ -1,0 +1,581 @@
+// What the kernels of the RMS norm share (rms_fwd.cu, rms_quant.cu, rms_bwd.cu).
+//
+//     h = round(x + residual),  r = (mean h^2 + eps)^(-1/2),  y = h r gamma          (a row: channels * inner values)
+//     8 bits, for each group of a row:  s = max |y| / 448,  q = e4m3(y / s)
+//     d_x = d_h + r (t - u mean(t u)),  t = gamma d_y,  u = h r;   d_gamma[c] = sum over rows and components of d_y u
+//
+// gamma is one value a channel, shared by the `inner` components of an irrep, so y is as equivariant as x.  The norm is of h as
+// it is stored: what the next layer and the gradient read is what was normalised.
+//
+// Bound by memory: every tensor moves once.  A row belongs to a team, a part of a warp or a block, whose threads hold it in registers, 16
+// values each at most, between the sum and the result.  The team's next rows are on their way to shared memory meanwhile, by
+// asynchronous copies that cost no registers: with one row ahead in registers the gradient had 48 KB in flight on an SM and ran at half of
+// the memory's rate.  Rows that do not begin on 16 bytes are read value by value, one row ahead in registers (copied in whole chunks, with
+// what lies before and behind them, they took twice the time).  A thread has the same columns of every row that it sees, so gamma is read once, and d_gamma is
+// summed in registers, then over the block's teams in shared memory, and over the blocks, in their order, by a second kernel.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+#include "elem.h"
+#include "plan.h"
+#include "tensor_core.h"
+
+namespace uvu {
+namespace {
+
+enum RmsMode { kRmsFwd, kRmsQuant, kRmsBwd };
+
+constexpr int kTeamRows = 512;      // rows that a team adds up in one fp32 sum of d_gamma
+constexpr int kValues = 16;         // of a thread, at most
+constexpr int kAhead = 3;           // rows on their way, beside the one at work; one where shared memory does not hold three
+constexpr size_t kRowsSmem = 200 << 10;
+constexpr float kTop = 448.f;       // the largest e4m3 value
+
+// V consecutive values as they lie in memory, taken apart and put together two at a time: with one conversion a value the kernels
+// were bound by their 39 instructions a value (forward in bf16).
+template <typename T, int V>
+struct alignas(V * sizeof(T)) Pack {
+    T t[V];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[i] = T(0.f);
+    }
+    __device__ __forceinline__ void get(float* v) const {
+        if constexpr (sizeof(T) == 4 || V == 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = widen(t[i]);
+        } else {
+            uint32_t w[(V + 1) / 2];
+            __builtin_memcpy(w, t, sizeof(w));
+#pragma unroll
+            for (int i = 0; i < (V + 1) / 2; ++i) {
+                if constexpr (__is_same(T, __nv_bfloat16)) {
+                    v[2 * i] = __uint_as_float(w[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                    v[2 * i] = f.x, v[2 * i + 1] = f.y;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void set(const float* v) {
+        if constexpr (sizeof(T) == 4 || V == 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) t[i] = narrow<T>(v[i]);
+        } else {
+            uint32_t w[(V + 1) / 2];
+#pragma unroll
+            for (int i = 0; i < (V + 1) / 2; ++i) w[i] = tc::pack2<T>(v[2 * i], v[2 * i + 1]);
+            __builtin_memcpy(t, w, sizeof(w));
+        }
+    }
+};
+template <int V>
+struct alignas(V) Bytes {
+    uint8_t b[V];
+    __device__ __forceinline__ void set(const float* v) {
+        if constexpr (V == 1) {
+            b[0] = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+        } else {
+            uint16_t w[(V + 1) / 2];
+#pragma unroll
+            for (int i = 0; i < (V + 1) / 2; ++i) w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+            __builtin_memcpy(b, w, sizeof(w));
+        }
+    }
+};
+
+struct RmsArgs {
+    int64_t rows;
+    int width, inner, team;        // width: values of a row
+    int group, groups;             // values that share a scale, and scales of a row
+    float eps;
+    const void* in[3];             // x, residual; gradient: h, dy, dh (residual, dh: or NULL)
+    void* out[2];                  // y, h (NULL without a residual); gradient: dx
+    const float* gamma;
+    float *rstd, *scales, *partial;
+    int64_t block_rows;            // of the gradient
+    int ahead;                     // kAhead or 1
+    int n_in, slot;                // inputs that are there, and bytes of a row's place in shared memory
+};
+
+// ------------------------------------------------------------------------------------ one row
+
+// V consecutive columns a thread and step, K steps; WARP: the team is a power of two of lanes, else the block; FULL: the steps end
+// with the row.
+template <typename T, int V, int K, bool WARP, bool FULL, RmsMode MODE>
+struct RmsRow {
+    float gamma[K * V];
+    float acc[MODE == kRmsBwd ? K * V : 1];
+    int lane, team, width;
+    float inv, eps;
+
+    __device__ __forceinline__ RmsRow(const RmsArgs& a) {
+        team = WARP ? a.team : int(blockDim.x);
+        lane = WARP ? int(threadIdx.x) & (team - 1) : int(threadIdx.x);
+        width = a.width;
+        inv = 1.f / float(width);
+        eps = a.eps;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = column(k) + i;
+                gamma[k * V + i] = e < width ? a.gamma[e / a.inner] : 0.f;
+                if (MODE == kRmsBwd) acc[k * V + i] = 0.f;
+            }
+    }
+    __device__ __forceinline__ int column(int k) const { return (k * team + lane) * V; }
+    __device__ __forceinline__ bool inside(int k) const { return FULL || column(k) < width; }
+
+    // Over the team, in all of its threads.  s_part: another half from row to row, so that the last sum has been read.
+    __device__ __forceinline__ float sum(float v, float* s_part) const {
+        if (WARP) {
+            for (int d = team >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+            return v;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0.f;
+        for (int w = 0; w < team >> 5; ++w) v += s_part[w];
+        return v;
+    }
+    __device__ __forceinline__ void sync() const {
+        if (WARP) __syncwarp();
+        else __syncthreads();
+    }
+
+    // Rows that begin on 16 bytes have places in shared memory, [ahead + 1][n_in][slot] bytes for each team; a thread copies there what
+    // it will read.
+    static constexpr bool kWhole = V * sizeof(T) == 16;
+    static constexpr int kIn = MODE == kRmsBwd ? 3 : 2;
+
+    // `at`: of the row's first value
+    __device__ __forceinline__ void fetch(const RmsArgs& a, int64_t at, bool live, uint32_t to) const {
+#pragma unroll
+        for (int j = 0; j < kIn; ++j)
+            if (live && j < a.n_in) {
+                const T* p = static_cast<const T*>(a.in[j]) + at;
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (inside(k)) tc::copy16(to + j * a.slot + column(k) * int(sizeof(T)), p + column(k), 16);
+            }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // The row that was asked for longest ago is there.
+    __device__ __forceinline__ void arrived(int ahead) const {
+        if (ahead == kAhead) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+        else asm volatile("cp.async.wait_group 1;" ::: "memory");
+    }
+    struct Read {
+        Pack<T, V> t[kIn][K];
+        float r;
+    };
+    // From shared memory (places a.slot bytes apart), or from the tensors.
+    template <bool STAGED>
+    __device__ __forceinline__ void take(const RmsArgs& a, int64_t at, bool live, const unsigned char* from, Read& in) const {
+#pragma unroll
+        for (int j = 0; j < kIn; ++j) {
+            const bool there = live && j < a.n_in;
+            const T* p = STAGED ? reinterpret_cast<const T*>(from + j * a.slot) : static_cast<const T*>(a.in[j]) + at;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (there && inside(k)) in.t[j][k] = *reinterpret_cast<const Pack<T, V>*>(p + column(k));
+                else in.t[j][k].clear();
+            }
+        }
+    }
+
+    // The values of h in v and its 1 / sqrt(mean h^2 + eps); h is written where there is a residual.
+    __device__ __forceinline__ float load(const Read& in, bool res, T* h, bool live, float* s_part, float (&v)[K * V]) const {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            in.t[0][k].get(v + k * V);
+            if (res) {
+                float u[V];
+                in.t[1][k].get(u);
+#pragma unroll
+                for (int i = 0; i < V; ++i) u[i] += v[k * V + i];
+                Pack<T, V> o;
+                o.set(u);
+                o.get(v + k * V);
+                if (live && inside(k)) *reinterpret_cast<Pack<T, V>*>(h + column(k)) = o;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) s = fmaf(v[k * V + i], v[k * V + i], s);
+        }
+        return rsqrtf(fmaf(sum(s, s_part), inv, eps));
+    }
+
+    __device__ __forceinline__ void forward(const Read& in, bool res, T* y, T* h, float* rstd, bool live, float* s_part) const {
+        float v[K * V];
+        const float r = load(in, res, h, live, s_part, v);
+        if (live && lane == 0 && rstd) *rstd = r;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (live && inside(k)) {
+                float u[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) u[i] = v[k * V + i] * r * gamma[k * V + i];
+                Pack<T, V> o;
+                o.set(u);
+                *reinterpret_cast<Pack<T, V>*>(y + column(k)) = o;
+            }
+    }
+
+    // s_top: a word for each group of the row, for the group sizes that lanes do not share evenly.
+    __device__ __forceinline__ void quantise(const Read& in, bool res, uint8_t* q, T* h, float* scales, int group, int groups, bool live,
+                                             float* s_part, unsigned* s_top) const {
+        float v[K * V];
+        const float r = load(in, res, h, live, s_part, v);
+        float top[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            top[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[k * V + i] *= r * gamma[k * V + i];
+                top[k] = nan_max(top[k], fabsf(v[k * V + i]));
+            }
+        }
+        // The largest |y| of a thread's group, for each step.  A group is the row, a power of two of a step's lanes, or a power of two of
+        // a warp's whole steps; others (odd sizes, long ones in a block's rows) are gathered in shared memory.
+        const bool whole = group >= width, even = group % V == 0 && (group & (group - 1)) == 0;
+        const int lanes = group / V, bits = 31 - __clz(group);
+        const bool shared = !whole && !(even && (lanes <= min(team, 32) || (WARP && team == 32)));
+        if (whole) {
+            float t = top[0];
+#pragma unroll
+            for (int k = 1; k < K; ++k) t = nan_max(t, top[k]);
+            for (int d = min(team, 32) >> 1; d > 0; d >>= 1) t = nan_max(t, __shfl_xor_sync(0xffffffffu, t, d));
+            if (!WARP) {
+                float* s_max = s_part + 16;
+                if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = t;
+                __syncthreads();
+                for (int w = 0; w < team >> 5; ++w) t = nan_max(t, s_max[w]);
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) top[k] = t;
+        } else if (!shared) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                for (int d = min(lanes, 32) >> 1; d > 0; d >>= 1) top[k] = nan_max(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
+#pragma unroll
+            for (int d = 1; d < K; d *= 2)
+                if (32 * d < lanes) {
+                    float other[K];
+#pragma unroll
+                    for (int k = 0; k < K; ++k) other[k] = (k ^ d) < K ? top[(k ^ d) < K ? k ^ d : k] : 0.f;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) top[k] = nan_max(top[k], other[k]);
+                }
+        } else {
+            sync();  // the last row's have been read
+            for (int j = lane; j < groups; j += team) s_top[j] = 0u;
+            sync();
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = column(k), g = c / group;
+                if (!live || !inside(k)) continue;
+                if ((c + V - 1) / group == g) {
+                    atomicMax(s_top + g, __float_as_uint(top[k]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) atomicMax(s_top + (c + i) / group, __float_as_uint(fabsf(v[k * V + i])));
+                }
+            }
+            sync();
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = column(k);
+            if (!live || !inside(k)) continue;
+            float u[V];
+            if (!shared) {
+                const float s = top[k] / kTop;
+                if (whole ? c == 0 : (c & (group - 1)) == 0) scales[whole ? 0 : c >> bits] = s;
+                if (s > 0.f && s < 0x1p-125f) {  // its inverse may be beyond fp32
+#pragma unroll
+                    for (int i = 0; i < V; ++i) u[i] = v[k * V + i] / s;
+                } else {
+                    const float si = s == 0.f ? 0.f : 1.f / s;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) u[i] = v[k * V + i] * si;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int g = (c + i) / group;
+                    const float s = __uint_as_float(s_top[g]) / kTop;
+                    if (c + i == g * group) scales[g] = s;
+                    u[i] = s == 0.f ? 0.f : v[k * V + i] / s;
+                }
+            }
+            Bytes<V> o;
+            o.set(u);
+            *reinterpret_cast<Bytes<V>*>(q + c) = o;
+        }
+    }
+
+    // A NaN is kept.
+    __device__ static __forceinline__ float nan_max(float a, float b) {
+        float c;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+        return c;
+    }
+
+    __device__ __forceinline__ void backward(const Read& in, T* dx, bool live, float* s_part) {
+        const float r = in.r;
+        const Pack<T, V>(&xv)[K] = in.t[0], (&gv)[K] = in.t[1], (&hv)[K] = in.t[MODE == kRmsBwd ? 2 : 0];
+        // d_gamma += d_y u, mean(t u) = r mean(gamma d_y h)
+        float dot = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float x[V], g[V];
+            xv[k].get(x);
+            gv[k].get(g);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float u = x[i] * r;
+                acc[k * V + i] = fmaf(g[i], u, acc[k * V + i]);
+                dot = fmaf(g[i] * gamma[k * V + i], u, dot);
+            }
+        }
+        dot = sum(dot, s_part) * inv;
+        const float rd = -r * r * dot;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (live && inside(k)) {
+                float x[V], g[V], t[V];
+                xv[k].get(x);
+                gv[k].get(g);
+                hv[k].get(t);
+#pragma unroll
+                for (int i = 0; i < V; ++i) t[i] = fmaf(g[i] * gamma[k * V + i], r, fmaf(x[i], rd, t[i]));
+                Pack<T, V> o;
+                o.set(t);
+                *reinterpret_cast<Pack<T, V>*>(dx + column(k)) = o;
+            }
+    }
+
+    // The block's sums of d_gamma, over its teams and a channel's components in their order.  s_sum [teams][width]
+    __device__ __forceinline__ void give_gradient(const RmsArgs& a, float* s_sum) const {
+        const int teams = WARP ? int(blockDim.x) / team : 1, mine = WARP ? int(threadIdx.x) / team : 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (column(k) + i < width) s_sum[mine * width + column(k) + i] = acc[k * V + i];
+        __syncthreads();
+        const int channels = width / a.inner;
+        for (int c = threadIdx.x; c < channels; c += blockDim.x) {
+            float s = 0.f;
+            for (int i = 0; i < a.inner; ++i)
+#pragma unroll 4
+                for (int m = 0; m < teams; ++m) s += s_sum[m * width + c * a.inner + i];
+            a.partial[int64_t(blockIdx.x) * channels + c] = s;
+        }
+    }
+};
+
+// ----------------------------------------------------------------------------------- the kernel
+
+template <typename T, int V, int K, bool WARP, bool FULL, RmsMode MODE>
+__global__ void __launch_bounds__(WARP ? 256 : V == 1 ? 1024 : 512) rms_kernel(const RmsArgs a) {
+    __shared__ float s_part[2][32];
+    // the rows' places, then the groups' maxima; at the end the sums of d_gamma
+    extern __shared__ __align__(16) unsigned char smem[];
+    using Row = RmsRow<T, V, K, WARP, FULL, MODE>;
+    Row op(a);
+    const int teams = WARP ? int(blockDim.x) / op.team : 1, mine = WARP ? int(threadIdx.x) / op.team : 0;
+    T* out1 = static_cast<T*>(a.out[1]);
+    unsigned* s_top = reinterpret_cast<unsigned*>(smem + teams * (a.ahead + 1) * a.n_in * a.slot);
+    // the gradient's rows of a block lie together, so that its sums are of rows in their order
+    const int64_t step = MODE == kRmsBwd ? teams : int64_t(gridDim.x) * teams;
+    const int64_t first = MODE == kRmsBwd ? blockIdx.x * a.block_rows : int64_t(blockIdx.x) * teams;
+    const int64_t end = MODE == kRmsBwd ? min(first + a.block_rows, a.rows) : a.rows;
+    typename Row::Read now;
+    const int64_t stride = step * a.width;  // values between a team's rows
+    int half = 0;
+    auto work = [&](int64_t row, int64_t at, bool live) {
+        if constexpr (MODE == kRmsFwd)
+            op.forward(now, out1 != nullptr, static_cast<T*>(a.out[0]) + at, out1 + at, a.rstd ? a.rstd + row : nullptr, live, s_part[half]);
+        else if constexpr (MODE == kRmsQuant)
+            op.quantise(now, out1 != nullptr, static_cast<uint8_t*>(a.out[0]) + at, out1 + at, a.scales + row * a.groups, a.group, a.groups,
+                        live, s_part[half], s_top + mine * a.groups);
+        else
+            op.backward(now, static_cast<T*>(a.out[0]) + at, live, s_part[half]);
+        half ^= 1;
+    };
+    auto rstd_of = [&](int64_t row) { return MODE == kRmsBwd && row < end ? a.rstd[row] : 0.f; };
+    if constexpr (Row::kWhole) {
+        const int places = a.n_in * a.slot;  // bytes of a row's
+        unsigned char* ring = smem + mine * (a.ahead + 1) * places;
+        const uint32_t ring_at = tc::smem_u32(ring);
+        float r[MODE == kRmsBwd ? kAhead : 1] = {};  // rstd of the rows on their way
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i < a.ahead) {
+                const int64_t row = first + mine + i * step;
+                op.fetch(a, row * a.width, row < end, ring_at + i * places);
+                if constexpr (MODE == kRmsBwd) r[i] = rstd_of(row);
+            }
+        int place = 0, free = a.ahead;
+        int64_t row = first + mine, at = row * a.width;
+        const int64_t rows_ahead = a.ahead * step, values_ahead = a.ahead * stride;
+        for (int64_t base = first; base < end; base += step, row += step, at += stride) {
+            op.fetch(a, at + values_ahead, row + rows_ahead < end, ring_at + free * places);
+            op.arrived(a.ahead);
+            op.template take<true>(a, at, row < end, ring + place * places, now);
+            if constexpr (MODE == kRmsBwd) {
+                const float last = rstd_of(row + rows_ahead);
+                now.r = r[0];
+#pragma unroll
+                for (int i = 0; i + 1 < kAhead; ++i) r[i] = r[i + 1];
+                r[kAhead - 1] = last;
+                if (a.ahead == 1) r[0] = last;
+            }
+            work(row, at, row < end);
+            free = place;
+            place = place == a.ahead ? 0 : place + 1;
+        }
+        tc::copy_wait_all();
+    } else {
+        typename Row::Read next;
+        auto ask = [&](int64_t row, int64_t at) {
+            op.template take<false>(a, at, row < end, nullptr, next);
+            next.r = rstd_of(row);
+        };
+        int64_t row = first + mine, at = row * a.width;
+        ask(row, at);
+        for (int64_t base = first; base < end; base += step, row += step, at += stride) {
+            now = next;
+            ask(row + step, at + stride);
+            work(row, at, row < end);
+        }
+    }
+    if constexpr (MODE == kRmsBwd) op.give_gradient(a, reinterpret_cast<float*>(smem));
+}
+
+// ---------------------------------------------------------------------------------------- host
+
+struct RmsPlan {
+    bool warp;
+    int v, k, team, threads;
+};
+// Vectors of 16 bytes where every row begins on one, else of 4 bytes (two 16-bit values) or single values.  Teams as small as their
+// threads' 16 values allow, so that a warp has several narrow rows at work, but so many threads that there is work for every SM.
+inline RmsPlan rms_plan(int64_t rows, int width, int size, uintptr_t any, int sms) {
+    RmsPlan p;
+    const uintptr_t row = uintptr_t(width) * size | any;
+    p.v = row % 16 == 0 ? 16 / size : row % 4 == 0 ? 4 / size : 1;
+    const int vecs = (width + p.v - 1) / p.v, most = kValues / p.v;
+    p.warp = vecs <= 32 * most;
+    p.k = most;
+    if (p.warp) {
+        p.team = std::max(1, 32 / (p.v * size));  // 32 bytes together
+        while (p.team * most < vecs || (p.team < 32 && p.team < vecs && rows * p.team < int64_t(sms) * 1024)) p.team *= 2;
+        while (p.k > 1 && p.team * (p.k / 2) >= vecs) p.k /= 2;
+        if (p.k == 16 && p.team * 12 >= vecs) p.k = 12;
+        p.threads = 256;
+    } else {
+        if (p.v == 1) p.k = 8;  // single values take a register each
+        p.threads = p.team = ((vecs + p.k - 1) / p.k + 31) / 32 * 32;
+    }
+    return p;
+}
+
+// f(V, K, WARP) with the plan's values as types.
+template <typename T, typename F>
+cudaError_t by_plan(const RmsPlan& p, F f) {
+#define UVU_AT(V_, K_, W_) \
+    if (p.v == V_ && p.k == K_ && p.warp == W_) \
+        return f(std::integral_constant<int, V_>(), std::integral_constant<int, K_>(), std::integral_constant<bool, W_>());
+    if constexpr (sizeof(T) == 4) {
+        UVU_AT(4, 1, true) UVU_AT(4, 2, true) UVU_AT(4, 4, true) UVU_AT(4, 4, false)
+    } else {
+        UVU_AT(8, 1, true) UVU_AT(8, 2, true) UVU_AT(8, 2, false)
+        UVU_AT(2, 1, true) UVU_AT(2, 2, true) UVU_AT(2, 4, true) UVU_AT(2, 8, true) UVU_AT(2, 8, false)
+    }
+    UVU_AT(1, 1, true) UVU_AT(1, 2, true) UVU_AT(1, 4, true) UVU_AT(1, 8, true) UVU_AT(1, 12, true) UVU_AT(1, 16, true) UVU_AT(1, 8, false)
+#undef UVU_AT
+    return cudaErrorInvalidValue;
+}
+
+// Rows of a block of the gradient: twice the blocks that the card holds, while a team's sums stay short.
+inline int64_t bwd_block_rows(const RmsPlan& p, int64_t rows, int sms) {
+    const int64_t teams = p.threads / p.team;
+    const int64_t blocks = int64_t(sms) * std::max(2, 1024 / p.threads);
+    const int64_t even = ((rows + blocks - 1) / blocks + teams - 1) / teams * teams;
+    return std::min<int64_t>(even, kTeamRows * teams);
+}
+
+template <typename T, RmsMode MODE>
+cudaError_t rms_launch(RmsArgs a, int sms, cudaStream_t st, int64_t* partials) {
+    uintptr_t any = 0;
+    for (const void* t : {a.in[0], a.in[1], a.in[2], static_cast<const void*>(a.out[0]), static_cast<const void*>(a.out[1])})
+        any |= reinterpret_cast<uintptr_t>(t) * (MODE == kRmsQuant && t == a.out[0] ? sizeof(T) : 1);
+    const RmsPlan p = rms_plan(a.rows, a.width, sizeof(T), any, sms);
+    a.team = p.team;
+    a.n_in = MODE == kRmsBwd ? (a.in[2] ? 3 : 2) : a.in[1] ? 2 : 1;
+    a.slot = p.v * int(sizeof(T)) == 16 ? a.width * int(sizeof(T)) : 0;  // rows off 16 bytes have no places
+    const int64_t teams = p.threads / p.team;
+    const size_t rows = size_t(teams) * a.n_in * a.slot;  // one for each team
+    a.ahead = rows * (kAhead + 1) <= kRowsSmem ? kAhead : 1;
+    size_t smem = rows * (a.ahead + 1);
+    if (MODE == kRmsQuant) smem += size_t(teams) * a.groups * 4;
+    if (MODE == kRmsBwd) smem = std::max(smem, size_t(teams) * a.width * 4);
+    return by_plan<T>(p, [&](auto v, auto k, auto warp) {
+        constexpr int V = decltype(v)::value, K = decltype(k)::value;
+        constexpr bool W = decltype(warp)::value;
+        auto kernel = rms_kernel<T, V, K, W, false, MODE>;
+        if constexpr (V * sizeof(T) == 16)
+            if (p.team * p.k * p.v == a.width) kernel = rms_kernel<T, V, K, W, true, MODE>;
+        if (smem > 40 << 10) {  // with what is static, 48 KB need no leave
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+            if (e != cudaSuccess) return e;
+        }
+        int64_t blocks;
+        if (MODE == kRmsBwd) {
+            a.block_rows = bwd_block_rows(p, a.rows, sms);
+            blocks = (a.rows + a.block_rows - 1) / a.block_rows;
+        } else {
+            static std::atomic<int> known[2];  // registers of a thread: the same on every device
+            std::atomic<int>& registers = known[p.team * p.k * p.v == a.width];
+            int regs = registers.load(std::memory_order_relaxed);
+            if (regs == 0) {
+                cudaFuncAttributes f;
+                cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+                if (e != cudaSuccess) return e;
+                registers.store(regs = std::max(1, f.numRegs), std::memory_order_relaxed);
+            }
+            const int resident = std::max(1, std::min({2048 / p.threads, 65536 / ((regs + 7) / 8 * 8 * p.threads), int((227 << 10) / (smem + 1280))}));
+            blocks = std::min<int64_t>((a.rows + teams - 1) / teams, int64_t(sms) * resident);
+        }
+        if (partials) *partials = blocks;
+        kernel<<<unsigned(blocks), p.threads, smem, st>>>(a);
+        return cudaGetLastError();
+    });
+}
+
+inline RmsArgs rms_args(const RmsShape& s) {
+    RmsArgs a = {};
+    a.rows = s.rows;
+    a.width = s.channels * s.inner;
+    a.inner = s.inner;
+    a.eps = float(s.eps);
+    return a;
+}
+
+}  // namespace
+}  // namespace uvu

@@ -1,0 +1,62 @@
+// The gradient of the RMS norm: see rms.h.
+#include "rms.h"
+
+namespace uvu {
+namespace {
+
+// d_gamma[c] = sum over the blocks of partial[b][c]: 32 channels a block, 32 threads for each.
+__global__ void __launch_bounds__(1024) rms_join_kernel(const float* partial, int blocks, int channels, float* out) {
+    __shared__ float s[32][33];
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    float sum = 0.f;
+    if (c < channels) {
+        int b = threadIdx.y;
+        for (; b + 96 < blocks; b += 128) {  // four loads on their way
+            const float* p = partial + int64_t(b) * channels + c;
+            const float v0 = p[0], v1 = p[int64_t(32) * channels], v2 = p[int64_t(64) * channels], v3 = p[int64_t(96) * channels];
+            sum += (v0 + v1) + (v2 + v3);
+        }
+        for (; b < blocks; b += 32) sum += partial[int64_t(b) * channels + c];
+    }
+    s[threadIdx.y][threadIdx.x] = sum;
+    __syncthreads();
+    sum = s[threadIdx.x][threadIdx.y];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const int out_c = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && out_c < channels) out[out_c] = sum;
+}
+
+}  // namespace
+
+size_t rms_workspace(const RmsShape& s, int sms) {
+    if (s.rows == 0) return 0;
+    // the tensors' alignment is not known here: the most blocks of any
+    int64_t most = 0;
+    for (uintptr_t any : {0, 4, 2, 1}) {
+        const int64_t each = bwd_block_rows(rms_plan(s.rows, s.channels * s.inner, s.dtype == UVU_F32 ? 4 : 2, any, sms), s.rows, sms);
+        most = std::max(most, (s.rows + each - 1) / each);
+    }
+    return size_t(most) * s.channels * 4;
+}
+
+cudaError_t launch_rms_bwd(const RmsShape& s, const void* dy, const void* h, const float* gamma, const float* rstd, const void* dh,
+                           void* dx, float* dgamma, void* ws, int sms, cudaStream_t st) {
+    if (s.rows == 0) return cudaMemsetAsync(dgamma, 0, size_t(s.channels) * 4, st);
+    RmsArgs a = rms_args(s);
+    a.in[0] = h, a.in[1] = dy, a.in[2] = dh, a.out[0] = dx, a.gamma = gamma;
+    a.rstd = const_cast<float*>(rstd), a.partial = static_cast<float*>(ws);
+    int64_t blocks = 0;
+    cudaError_t e = cudaErrorInvalidValue;
+    switch (s.dtype) {
+        case UVU_F32: e = rms_launch<float, kRmsBwd>(a, sms, st, &blocks); break;
+        case UVU_BF16: e = rms_launch<__nv_bfloat16, kRmsBwd>(a, sms, st, &blocks); break;
+        case UVU_F16: e = rms_launch<__half, kRmsBwd>(a, sms, st, &blocks); break;
+        default: break;
+    }
+    if (e != cudaSuccess) return e;
+    rms_join_kernel<<<(s.channels + 31) / 32, dim3(32, 32), 0, st>>>(a.partial, int(blocks), s.channels, dgamma);
+    return cudaGetLastError();
+}
+
+}  // namespace uvu

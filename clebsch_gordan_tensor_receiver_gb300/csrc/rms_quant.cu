@@ -1,0 +1,20 @@
+// RMS norm with the residual's addition and an output of 8 bits with scales: see rms.h.
+#include "rms.h"
+
+namespace uvu {
+
+cudaError_t launch_rms_quant(const RmsShape& s, int group, const void* x, const void* residual, const float* gamma, void* h, void* q,
+                             float* scales, int sms, cudaStream_t st) {
+    RmsArgs a = rms_args(s);
+    a.in[0] = x, a.in[1] = residual, a.gamma = gamma, a.out[0] = q, a.out[1] = h, a.scales = scales;
+    a.group = group ? std::min(group, a.width) : a.width;
+    a.groups = (a.width + a.group - 1) / a.group;
+    switch (s.dtype) {
+        case UVU_F32: return rms_launch<float, kRmsQuant>(a, sms, st, nullptr);
+        case UVU_BF16: return rms_launch<__nv_bfloat16, kRmsQuant>(a, sms, st, nullptr);
+        case UVU_F16: return rms_launch<__half, kRmsQuant>(a, sms, st, nullptr);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace uvu
