@@ -28,7 +28,7 @@
 namespace uvu {
 namespace {
 
-enum RmsMode { kRmsFwd, kRmsQuant, kRmsBwd };
+enum RmsMode { kRmsFwd, kRmsQuant, kRmsQuantAny, kRmsBwd };  // Any: groups that lanes do not share evenly
 
 constexpr int kTeamRows = 512;      // rows that a team adds up in one fp32 sum of d_gamma
 constexpr int kValues = 16;         // of a thread, at most
@@ -232,7 +232,22 @@ struct RmsRow {
             }
     }
 
-    // s_top: a word for each group of the row, for the group sizes that lanes do not share evenly.
+    // One scale and what the values are multiplied with; `top`: the group's largest |y|.
+    __device__ __forceinline__ static float scale_of(float top) { return top * (1.f / kTop); }
+    template <int N>
+    __device__ __forceinline__ static void scaled(float top, const float* v, float (&u)[N]) {
+        if (top > 0x1p-116f && top < 0x1p120f) {
+            const float f = __fdividef(kTop, top);
+#pragma unroll
+            for (int i = 0; i < N; ++i) u[i] = v[i] * f;
+        } else {  // the inverse may be beyond fp32; zeros stay zeros, a NaN makes all NaN
+            const float s = scale_of(top);
+#pragma unroll
+            for (int i = 0; i < N; ++i) u[i] = s == 0.f ? 0.f : v[i] / s;
+        }
+    }
+
+    // s_top (kRmsQuantAny): a word for each group of the row.
     __device__ __forceinline__ void quantise(const Read& in, bool res, uint8_t* q, T* h, float* scales, int group, int groups, bool live,
                                              float* s_part, unsigned* s_top) const {
         float v[K * V];
@@ -247,82 +262,91 @@ struct RmsRow {
                 top[k] = nan_max(top[k], fabsf(v[k * V + i]));
             }
         }
-        // The largest |y| of a thread's group, for each step.  A group is the row, a power of two of a step's lanes, or a power of two of
-        // a warp's whole steps; others (odd sizes, long ones in a block's rows) are gathered in shared memory.
-        const bool whole = group >= width, even = group % V == 0 && (group & (group - 1)) == 0;
-        const int lanes = group / V, bits = 31 - __clz(group);
-        const bool shared = !whole && !(even && (lanes <= min(team, 32) || (WARP && team == 32)));
-        if (whole) {
-            float t = top[0];
-#pragma unroll
-            for (int k = 1; k < K; ++k) t = nan_max(t, top[k]);
-            for (int d = min(team, 32) >> 1; d > 0; d >>= 1) t = nan_max(t, __shfl_xor_sync(0xffffffffu, t, d));
-            if (!WARP) {
-                float* s_max = s_part + 16;
-                if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = t;
-                __syncthreads();
-                for (int w = 0; w < team >> 5; ++w) t = nan_max(t, s_max[w]);
-            }
-#pragma unroll
-            for (int k = 0; k < K; ++k) top[k] = t;
-        } else if (!shared) {
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                for (int d = min(lanes, 32) >> 1; d > 0; d >>= 1) top[k] = nan_max(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
-#pragma unroll
-            for (int d = 1; d < K; d *= 2)
-                if (32 * d < lanes) {
-                    float other[K];
-#pragma unroll
-                    for (int k = 0; k < K; ++k) other[k] = (k ^ d) < K ? top[(k ^ d) < K ? k ^ d : k] : 0.f;
-#pragma unroll
-                    for (int k = 0; k < K; ++k) top[k] = nan_max(top[k], other[k]);
-                }
-        } else {
+        if constexpr (MODE == kRmsQuantAny) {
             sync();  // the last row's have been read
             for (int j = lane; j < groups; j += team) s_top[j] = 0u;
+            sync();
+            const bool by_warp = team >= 32 && group % (32 * V) == 0;  // the lanes of a step share a group
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = column(k), g = c / group;
+                if (by_warp) {
+                    const unsigned most = __reduce_max_sync(0xffffffffu, live && inside(k) ? __float_as_uint(top[k]) : 0u);
+                    if ((threadIdx.x & 31) == 0 && g < groups) atomicMax(s_top + g, most);
+                } else if (live && inside(k)) {
+                    if ((c + V - 1) / group == g) {
+                        atomicMax(s_top + g, __float_as_uint(top[k]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) atomicMax(s_top + (c + i) / group, __float_as_uint(fabsf(v[k * V + i])));
+                    }
+                }
+            }
             sync();
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int c = column(k), g = c / group;
                 if (!live || !inside(k)) continue;
+                float u[V];
                 if ((c + V - 1) / group == g) {
-                    atomicMax(s_top + g, __float_as_uint(top[k]));
+                    scaled(__uint_as_float(s_top[g]), v + k * V, u);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) atomicMax(s_top + (c + i) / group, __float_as_uint(fabsf(v[k * V + i])));
+                    for (int i = 0; i < V; ++i) {
+                        float one[1];
+                        scaled(__uint_as_float(s_top[(c + i) / group]), v + k * V + i, one);
+                        u[i] = one[0];
+                    }
                 }
+                Bytes<V> o;
+                o.set(u);
+                *reinterpret_cast<Bytes<V>*>(q + c) = o;
             }
-            sync();
-        }
+            for (int j = lane; j < groups; j += team)
+                if (live) scales[j] = scale_of(__uint_as_float(s_top[j]));
+        } else {
+            // The largest |y| of a thread's group, for each step.  A group is the row, a power of two of a step's lanes, or a power of two
+            // of a warp's whole steps.
+            const bool whole = group >= width;
+            const int lanes = group / V, bits = 31 - __clz(group);
+            if (whole) {
+                float t = top[0];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = column(k);
-            if (!live || !inside(k)) continue;
-            float u[V];
-            if (!shared) {
-                const float s = top[k] / kTop;
-                if (whole ? c == 0 : (c & (group - 1)) == 0) scales[whole ? 0 : c >> bits] = s;
-                if (s > 0.f && s < 0x1p-125f) {  // its inverse may be beyond fp32
-#pragma unroll
-                    for (int i = 0; i < V; ++i) u[i] = v[k * V + i] / s;
-                } else {
-                    const float si = s == 0.f ? 0.f : 1.f / s;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) u[i] = v[k * V + i] * si;
+                for (int k = 1; k < K; ++k) t = nan_max(t, top[k]);
+                for (int d = min(team, 32) >> 1; d > 0; d >>= 1) t = nan_max(t, __shfl_xor_sync(0xffffffffu, t, d));
+                if (!WARP) {
+                    float* s_max = s_part + 32;
+                    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = t;
+                    __syncthreads();
+                    for (int w = 0; w < team >> 5; ++w) t = nan_max(t, s_max[w]);
                 }
+#pragma unroll
+                for (int k = 0; k < K; ++k) top[k] = t;
             } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int g = (c + i) / group;
-                    const float s = __uint_as_float(s_top[g]) / kTop;
-                    if (c + i == g * group) scales[g] = s;
-                    u[i] = s == 0.f ? 0.f : v[k * V + i] / s;
-                }
+                for (int k = 0; k < K; ++k)
+                    for (int d = min(lanes, 32) >> 1; d > 0; d >>= 1) top[k] = nan_max(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
+#pragma unroll
+                for (int d = 1; d < K; d *= 2)
+                    if (32 * d < lanes) {
+                        float other[K];
+#pragma unroll
+                        for (int k = 0; k < K; ++k) other[k] = (k ^ d) < K ? top[(k ^ d) < K ? k ^ d : k] : 0.f;
+#pragma unroll
+                        for (int k = 0; k < K; ++k) top[k] = nan_max(top[k], other[k]);
+                    }
             }
-            Bytes<V> o;
-            o.set(u);
-            *reinterpret_cast<Bytes<V>*>(q + c) = o;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = column(k);
+                if (!live || !inside(k)) continue;
+                float u[V];
+                scaled(top[k], v + k * V, u);
+                if (whole ? c == 0 : (c & (group - 1)) == 0) scales[whole ? 0 : c >> bits] = scale_of(top[k]);
+                Bytes<V> o;
+                o.set(u);
+                *reinterpret_cast<Bytes<V>*>(q + c) = o;
+            }
         }
     }
 
@@ -392,9 +416,10 @@ struct RmsRow {
 
 template <typename T, int V, int K, bool WARP, bool FULL, RmsMode MODE>
 __global__ void __launch_bounds__(WARP ? 256 : V == 1 ? 1024 : 512) rms_kernel(const RmsArgs a) {
-    __shared__ float s_part[2][32];
+    __shared__ float s_part[2][64];
     // the rows' places, then the groups' maxima; at the end the sums of d_gamma
     extern __shared__ __align__(16) unsigned char smem[];
+    if (MODE == kRmsBwd) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join begins as blocks end
     using Row = RmsRow<T, V, K, WARP, FULL, MODE>;
     Row op(a);
     const int teams = WARP ? int(blockDim.x) / op.team : 1, mine = WARP ? int(threadIdx.x) / op.team : 0;
@@ -410,7 +435,7 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 1 ? 1024 : 512) rms_kernel(c
     auto work = [&](int64_t row, int64_t at, bool live) {
         if constexpr (MODE == kRmsFwd)
             op.forward(now, out1 != nullptr, static_cast<T*>(a.out[0]) + at, out1 + at, a.rstd ? a.rstd + row : nullptr, live, s_part[half]);
-        else if constexpr (MODE == kRmsQuant)
+        else if constexpr (MODE == kRmsQuant || MODE == kRmsQuantAny)
             op.quantise(now, out1 != nullptr, static_cast<uint8_t*>(a.out[0]) + at, out1 + at, a.scales + row * a.groups, a.group, a.groups,
                         live, s_part[half], s_top + mine * a.groups);
         else
@@ -512,55 +537,65 @@ cudaError_t by_plan(const RmsPlan& p, F f) {
     return cudaErrorInvalidValue;
 }
 
-// Rows of a block of the gradient: twice the blocks that the card holds, while a team's sums stay short.
-inline int64_t bwd_block_rows(const RmsPlan& p, int64_t rows, int sms) {
+// Most blocks of the gradient, whose sums the workspace holds: so many on an SM, or more where a team's sums would get long.
+inline int bwd_resident_most(const RmsPlan& p) { return std::max(8, 1024 / p.threads); }
+inline int64_t bwd_blocks_most(const RmsPlan& p, int64_t rows, int sms) {
     const int64_t teams = p.threads / p.team;
-    const int64_t blocks = int64_t(sms) * std::max(2, 1024 / p.threads);
-    const int64_t even = ((rows + blocks - 1) / blocks + teams - 1) / teams * teams;
-    return std::min<int64_t>(even, kTeamRows * teams);
+    return std::min((rows + teams - 1) / teams, std::max(int64_t(sms) * bwd_resident_most(p), (rows + kTeamRows * teams - 1) / (kTeamRows * teams)));
 }
 
 template <typename T, RmsMode MODE>
 cudaError_t rms_launch(RmsArgs a, int sms, cudaStream_t st, int64_t* partials) {
+    constexpr bool kQuant = MODE == kRmsQuant || MODE == kRmsQuantAny;
     uintptr_t any = 0;
     for (const void* t : {a.in[0], a.in[1], a.in[2], static_cast<const void*>(a.out[0]), static_cast<const void*>(a.out[1])})
-        any |= reinterpret_cast<uintptr_t>(t) * (MODE == kRmsQuant && t == a.out[0] ? sizeof(T) : 1);
+        any |= reinterpret_cast<uintptr_t>(t) * (kQuant && t == a.out[0] ? sizeof(T) : 1);
     const RmsPlan p = rms_plan(a.rows, a.width, sizeof(T), any, sms);
+    if constexpr (MODE == kRmsQuant) {
+        const int lanes = a.group / p.v;
+        const bool even = a.group % p.v == 0 && (a.group & (a.group - 1)) == 0;
+        if (a.group < a.width && !(even && (lanes <= std::min(p.team, 32) || (p.warp && p.team == 32))))
+            return rms_launch<T, kRmsQuantAny>(a, sms, st, partials);
+    }
     a.team = p.team;
     a.n_in = MODE == kRmsBwd ? (a.in[2] ? 3 : 2) : a.in[1] ? 2 : 1;
     a.slot = p.v * int(sizeof(T)) == 16 ? a.width * int(sizeof(T)) : 0;  // rows off 16 bytes have no places
     const int64_t teams = p.threads / p.team;
-    const size_t rows = size_t(teams) * a.n_in * a.slot;  // one for each team
-    a.ahead = rows * (kAhead + 1) <= kRowsSmem ? kAhead : 1;
-    size_t smem = rows * (a.ahead + 1);
-    if (MODE == kRmsQuant) smem += size_t(teams) * a.groups * 4;
-    if (MODE == kRmsBwd) smem = std::max(smem, size_t(teams) * a.width * 4);
+    const size_t one = size_t(teams) * a.n_in * a.slot;  // a row for each team
     return by_plan<T>(p, [&](auto v, auto k, auto warp) {
         constexpr int V = decltype(v)::value, K = decltype(k)::value;
         constexpr bool W = decltype(warp)::value;
         auto kernel = rms_kernel<T, V, K, W, false, MODE>;
+        const bool full = V * sizeof(T) == 16 && p.team * p.k * p.v == a.width;
         if constexpr (V * sizeof(T) == 16)
-            if (p.team * p.k * p.v == a.width) kernel = rms_kernel<T, V, K, W, true, MODE>;
+            if (full) kernel = rms_kernel<T, V, K, W, true, MODE>;
+        static std::atomic<int> known[2];  // registers of a thread: the same on every device
+        int regs = known[full].load(std::memory_order_relaxed);
+        if (regs == 0) {
+            cudaFuncAttributes f;
+            cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+            if (e != cudaSuccess) return e;
+            known[full].store(regs = std::max(1, f.numRegs), std::memory_order_relaxed);
+        }
+        auto smem_of = [&](int ahead) {
+            const size_t b = one * (ahead + 1) + (MODE == kRmsQuantAny ? size_t(teams) * a.groups * 4 : 0);
+            return MODE == kRmsBwd ? std::max(b, size_t(teams) * a.width * 4) : b;
+        };
+        auto resident = [&](size_t smem) {
+            return std::max(1, std::min({MODE == kRmsBwd ? bwd_resident_most(p) : 32, 2048 / p.threads, 65536 / ((regs + 7) / 8 * 8 * p.threads), int((227 << 10) / (smem + 1280))}));
+        };
+        // three rows ahead where every team has several, else so many blocks as there is work for
+        a.ahead = smem_of(kAhead) <= kRowsSmem && a.rows >= sms * resident(smem_of(kAhead)) * teams * (kAhead + 1) ? kAhead : 1;
+        const size_t smem = smem_of(a.ahead);
         if (smem > 40 << 10) {  // with what is static, 48 KB need no leave
             cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
             if (e != cudaSuccess) return e;
         }
-        int64_t blocks;
+        int64_t blocks = std::min<int64_t>((a.rows + teams - 1) / teams, int64_t(sms) * resident(smem));
         if (MODE == kRmsBwd) {
-            a.block_rows = bwd_block_rows(p, a.rows, sms);
+            blocks = std::max(blocks, (a.rows + kTeamRows * teams - 1) / (kTeamRows * teams));
+            a.block_rows = ((a.rows + blocks - 1) / blocks + teams - 1) / teams * teams;
             blocks = (a.rows + a.block_rows - 1) / a.block_rows;
-        } else {
-            static std::atomic<int> known[2];  // registers of a thread: the same on every device
-            std::atomic<int>& registers = known[p.team * p.k * p.v == a.width];
-            int regs = registers.load(std::memory_order_relaxed);
-            if (regs == 0) {
-                cudaFuncAttributes f;
-                cudaError_t e = cudaFuncGetAttributes(&f, kernel);
-                if (e != cudaSuccess) return e;
-                registers.store(regs = std::max(1, f.numRegs), std::memory_order_relaxed);
-            }
-            const int resident = std::max(1, std::min({2048 / p.threads, 65536 / ((regs + 7) / 8 * 8 * p.threads), int((227 << 10) / (smem + 1280))}));
-            blocks = std::min<int64_t>((a.rows + teams - 1) / teams, int64_t(sms) * resident);
         }
         if (partials) *partials = blocks;
         kernel<<<unsigned(blocks), p.threads, smem, st>>>(a);

@@ -7,6 +7,7 @@ namespace {
 // d_gamma[c] = sum over the blocks of partial[b][c]: 32 channels a block, 32 threads for each.
 __global__ void __launch_bounds__(1024) rms_join_kernel(const float* partial, int blocks, int channels, float* out) {
     __shared__ float s[32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums are there
     const int c = blockIdx.x * 32 + threadIdx.x;
     float sum = 0.f;
     if (c < channels) {
@@ -33,10 +34,8 @@ size_t rms_workspace(const RmsShape& s, int sms) {
     if (s.rows == 0) return 0;
     // the tensors' alignment is not known here: the most blocks of any
     int64_t most = 0;
-    for (uintptr_t any : {0, 4, 2, 1}) {
-        const int64_t each = bwd_block_rows(rms_plan(s.rows, s.channels * s.inner, s.dtype == UVU_F32 ? 4 : 2, any, sms), s.rows, sms);
-        most = std::max(most, (s.rows + each - 1) / each);
-    }
+    for (uintptr_t any : {0, 4, 2, 1})
+        most = std::max(most, bwd_blocks_most(rms_plan(s.rows, s.channels * s.inner, s.dtype == UVU_F32 ? 4 : 2, any, sms), s.rows, sms));
     return size_t(most) * s.channels * 4;
 }
 
@@ -55,8 +54,17 @@ cudaError_t launch_rms_bwd(const RmsShape& s, const void* dy, const void* h, con
         default: break;
     }
     if (e != cudaSuccess) return e;
-    rms_join_kernel<<<(s.channels + 31) / 32, dim3(32, 32), 0, st>>>(a.partial, int(blocks), s.channels, dgamma);
-    return cudaGetLastError();
+    // it may begin while the last blocks of the sums run, and waits for them
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((s.channels + 31) / 32);
+    c.blockDim = dim3(32, 32);
+    c.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, rms_join_kernel, static_cast<const float*>(a.partial), int(blocks), s.channels, dgamma);
 }
 
 }  // namespace uvu
