@@ -49,6 +49,62 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& r) {
     }
 }
 
+// Two values rounded to 16 bits, `lo` in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// V consecutive values as they lie in memory, taken apart and put together two at a time: with one conversion a value the RMS norm
+// was bound by its 39 instructions a value (forward in bf16).
+template <typename T, int V>
+struct alignas(V * sizeof(T)) Pack {
+    T t[V];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[i] = T(0.f);
+    }
+    __device__ __forceinline__ void get(float* v) const {
+        if constexpr (sizeof(T) == 4 || V == 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = widen(t[i]);
+        } else {
+            uint32_t w[(V + 1) / 2];
+            __builtin_memcpy(w, t, sizeof(w));
+#pragma unroll
+            for (int i = 0; i < (V + 1) / 2; ++i) {
+                if constexpr (__is_same(T, __nv_bfloat16)) {
+                    v[2 * i] = __uint_as_float(w[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                    v[2 * i] = f.x, v[2 * i + 1] = f.y;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void set(const float* v) {
+        if constexpr (sizeof(T) == 4 || V == 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) t[i] = narrow<T>(v[i]);
+        } else {
+            uint32_t w[(V + 1) / 2];
+#pragma unroll
+            for (int i = 0; i < (V + 1) / 2; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+            __builtin_memcpy(t, w, sizeof(w));
+        }
+    }
+};
 // Pairs of fp32 values: one packed instruction does both (add, mul, fma .f32x2), which halves the
 // arithmetic that a value costs beside its special-function instructions.
 struct F2 {

@@ -10,7 +10,7 @@
 // The gradient adds no two threads' sums by atomic instructions, whose order would change the result.  It sorts the tokens by row (stable,
 // so that a row's tokens are added in their order), cuts the sorted tokens into pieces of equal length, however the rows lie,
 // and sums each piece in fp32 registers, 8 rows of d_out on their way at a time.  A row whose tokens lie in one piece is
-// written by it; one that goes on behind its piece is added up from the pieces' sums, in the pieces' order.  Rows without a token
+// written by it; one that goes on behind its piece is noted, and added up from the pieces' sums in the pieces' order.  Rows without a token
 // are zeros: the table is zeroed by blocks of the first kernel that the sort leaves idle.
 #include <algorithm>
 #include <cstdint>
@@ -23,11 +23,6 @@ namespace {
 
 __device__ __forceinline__ void next_may_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-template <typename T, int V>
-struct alignas(V * sizeof(T)) Some {
-    T v[V];
-};
 
 // ----------------------------------------------------------------------------------- the lookup
 
@@ -56,30 +51,36 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(int64_t tokens, uint32_t
             if (h < 0) h += inner, ++first;
             for (; h < V; h += inner) hits |= 1u << h;
         }
-        Some<T, V> o[kLookupTokens];
+        Pack<T, V> o[kLookupTokens];
 #pragma unroll
         for (int k = 0; k < kLookupTokens; ++k) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) o[k].v[i] = T(0.f);
+            o[k].clear();
             if (uint32_t(at[k]) < rows) {
                 const T* p = table + int64_t(at[k]) * channels + first;
                 if (PLAIN) {
-                    o[k] = *reinterpret_cast<const Some<T, V>*>(p);
+                    o[k] = *reinterpret_cast<const Pack<T, V>*>(p);
                 } else {
 #pragma unroll
                     for (int i = 0; i < V; ++i)
-                        if (hits >> i & 1) o[k].v[i] = *p++;
+                        if (hits >> i & 1) o[k].t[i] = *p++;
                 }
             }
         }
 #pragma unroll
         for (int k = 0; k < kLookupTokens; ++k) {
             const int64_t t = t0 + k * blockDim.y;
-            // zeros stay zeros: the scale is finite (the sign of a zero beside the column does not come from it)
+            float v[V];
+            o[k].get(v);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (PLAIN || (hits >> i & 1)) o[k].v[i] = uint32_t(at[k]) < rows ? narrow<T>(widen(o[k].v[i]) * scale) : T(0.f);
-            if (t < tokens) *reinterpret_cast<Some<T, V>*>(out + t * width + int64_t(c) * V) = o[k];
+            for (int i = 0; i < V; ++i) v[i] *= scale;
+            o[k].set(v);
+            // what is not looked up is zero, and not minus zero under a negative scale
+            if (uint32_t(at[k]) >= rows) o[k].clear();
+            if (!PLAIN)
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (!(hits >> i & 1)) o[k].t[i] = T(0.f);
+            if (t < tokens) *reinterpret_cast<Pack<T, V>*>(out + t * width + int64_t(c) * V) = o[k];
         }
     }
 }
@@ -95,7 +96,10 @@ constexpr int kDigit = 8, kBins = 1 << kDigit;
 constexpr int kKeys = 8;                   // of a thread and tile
 constexpr int kTile = kThreads * kKeys;
 constexpr int kMaxBlocks = 512;            // of a pass; a block takes consecutive tiles
-constexpr int kOneThreads = 1024, kOneBlock = kOneThreads * kKeys;
+constexpr int kOneThreads = 1024, kOneKeys = 16, kOneBlock = kOneThreads * kOneKeys;
+// Behind the two numbers of valid tokens those of the rows that go on behind the piece they begin in, by how far: see join_kernel.
+constexpr int kChains = 2, kReaches = 3;
+__device__ __forceinline__ constexpr int reach(int i) { return i == 0 ? 16 : 256; }  // pieces, of the first two
 constexpr int kOneSmem = 2 * kOneBlock * 4 + 2 * kOneBlock * 2 + (kOneThreads / 32) * kBins * 4;
 
 // Zeros over [p, p + bytes), by the blocks from `first` on of the grid.
@@ -108,9 +112,16 @@ __device__ __forceinline__ void zero(unsigned char* p, int64_t bytes, int first)
     for (int64_t i = head + vecs * 16 + me; i < bytes; i += threads) p[i] = 0;
 }
 
-// Ranks of a warp's next 32 keys within their bins, after those that `seen` (of the warp) counts; live: the lane has a key.
+// Ranks of a warp's next 32 keys within their bins, after those that `seen` (of the warp) counts; live: the lane has a key.  The lanes of a
+// bin find one another bit by bit.
 __device__ __forceinline__ uint32_t warp_rank(uint32_t* seen, uint32_t bin, bool live, int lane) {
-    const uint32_t same = __match_any_sync(0xffffffffu, live ? bin : kBins);
+    uint32_t same = __ballot_sync(0xffffffffu, live);
+#pragma unroll
+    for (int b = 0; b < kDigit; ++b) {
+        const bool set = bin >> b & 1;
+        const uint32_t with = __ballot_sync(0xffffffffu, set);
+        same &= set ? with : ~with;
+    }
     const uint32_t rank = (live ? seen[bin] : 0) + __popc(same & ((1u << lane) - 1));
     __syncwarp();
     if (live && lane == 31 - __clz(same)) seen[bin] = rank + 1;
@@ -133,6 +144,15 @@ __device__ __forceinline__ uint32_t before(uint32_t v, uint32_t* s_warp) {
     return run - v;
 }
 
+// A large table is zeroed beside the sort, not by blocks of it, which fill an SM each with their shared memory: it begins when the sort
+// has begun, and ends after it.
+constexpr int64_t kLargeTable = 4 << 20;
+__global__ void __launch_bounds__(kThreads) zero_kernel(unsigned char* table, int64_t bytes) {
+    next_may_begin();
+    zero(table, bytes, 0);
+    wait_for_last();
+}
+
 __global__ void __launch_bounds__(kOneThreads) sort_kernel(int n, uint32_t rows, int passes, const int32_t* index, uint32_t* keys_out,
                                                            int32_t* ids_out, int32_t* valid, unsigned char* table, int64_t table_bytes) {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -149,50 +169,55 @@ __global__ void __launch_bounds__(kOneThreads) sort_kernel(int n, uint32_t rows,
         const int shift = pass * kDigit, from = (pass & 1) * kOneBlock, to = kOneBlock - from;
         for (int i = tid; i < kOneThreads / 32 * kBins; i += kOneThreads) s_seen[i] = 0;
         __syncthreads();
-        uint32_t key[kKeys], rank[kKeys];
-        int id[kKeys];
-        bool live[kKeys];
+        uint32_t key[kOneKeys], rank[kOneKeys];
+        const int rounds = (m + kOneThreads - 1) / kOneThreads, used = (m + rounds * 32 - 1) / max(1, rounds * 32);  // warps with keys
+        auto place_of = [&](int k) { return k < rounds ? warp * (rounds * 32) + k * 32 + lane : m; };  // a warp's keys lie together
 #pragma unroll
-        for (int k = 0; k < kKeys; ++k) {  // a warp's keys lie together, 32 at a time
-            const int i = warp * (kKeys * 32) + k * 32 + lane;
-            id[k] = pass == 0 || i >= m ? i : s_id[from + i];
-            key[k] = i >= m ? 0 : pass == 0 ? uint32_t(index[i]) : s_key[from + i];
-            live[k] = i < m && key[k] < rows;
+        for (int k = 0; k < kOneKeys; ++k) {
+            const int i = place_of(k);
+            key[k] = i >= m ? rows : pass == 0 ? uint32_t(index[i]) : s_key[from + i];
         }
 #pragma unroll
-        for (int k = 0; k < kKeys; ++k) rank[k] = warp_rank(s_seen + warp * kBins, key[k] >> shift & (kBins - 1), live[k], lane);
+        for (int k = 0; k < kOneKeys; ++k)
+            if (k < rounds && warp < used) rank[k] = warp_rank(s_seen + warp * kBins, key[k] >> shift & (kBins - 1), key[k] < rows, lane);
         __syncthreads();
         // where each warp's keys of a bin begin
         uint32_t total = 0;
         if (tid < kBins)
-            for (int w = 0; w < kOneThreads / 32; ++w) total += s_seen[w * kBins + tid];
+            for (int w = 0; w < used; ++w) total += s_seen[w * kBins + tid];
         uint32_t run = before(total, s_sum);
         if (tid < kBins) {
             if (tid == kBins - 1) s_valid = int(run + total);
-            for (int w = 0; w < kOneThreads / 32; ++w) {
+            for (int w = 0; w < used; ++w) {
                 const uint32_t c = s_seen[w * kBins + tid];
                 s_seen[w * kBins + tid] = run;
                 run += c;
             }
         }
         __syncthreads();
-        m = s_valid;
         const bool last = pass == passes - 1;
 #pragma unroll
-        for (int k = 0; k < kKeys; ++k)
-            if (live[k]) {
+        for (int k = 0; k < kOneKeys; ++k) {
+            const int i = place_of(k);
+            if (key[k] < rows) {
                 const uint32_t p = s_seen[warp * kBins + (key[k] >> shift & (kBins - 1))] + rank[k];
+                const int id = pass == 0 ? i : s_id[from + i];
                 if (last) {
                     keys_out[p] = key[k];
-                    ids_out[p] = id[k];
+                    ids_out[p] = id;
                 } else {
                     s_key[to + p] = key[k];
-                    s_id[to + p] = uint16_t(id[k]);
+                    s_id[to + p] = uint16_t(id);
                 }
             }
+        }
+        m = s_valid;
         __syncthreads();
     }
-    if (tid == 0) *valid = m;
+    if (tid == 0) {
+        valid[0] = m;
+        for (int i = 0; i < kReaches; ++i) valid[kChains + i] = 0;
+    }
 }
 
 // The keys of a pass: the indices, or what the last pass left.
@@ -248,14 +273,17 @@ __global__ void __launch_bounds__(kMaxBlocks) bins_kernel(int blocks, uint32_t* 
 }
 
 __global__ void __launch_bounds__(kThreads) place_kernel(const Keys k, const uint32_t* counts, const uint32_t* totals, uint32_t* keys_out,
-                                                         int32_t* ids_out, int32_t* valid_out) {
+                                                         int32_t* ids_out, int32_t* valid, int parity) {
     __shared__ uint32_t s_base[kBins], s_sum[kBins / 32], s_warp[kThreads / 32][kBins];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     next_may_begin();
     wait_for_last();
     const int64_t n = k.count();
     const uint32_t total = totals[tid], first_of = before(total, s_sum);
-    if (blockIdx.x == 0 && tid == kBins - 1) *valid_out = int32_t(first_of + total);
+    if (blockIdx.x == 0 && tid == kBins - 1) {
+        valid[parity] = int32_t(first_of + total);
+        for (int i = 0; i < kReaches; ++i) valid[kChains + i] = 0;
+    }
     s_base[tid] = first_of + counts[int64_t(tid) * gridDim.x + blockIdx.x];
     for (int tile = 0; tile < k.tiles; ++tile) {
         const int64_t first = (int64_t(blockIdx.x) * k.tiles + tile) * kTile;
@@ -307,6 +335,7 @@ struct Sums {
     const uint32_t* keys;
     const int32_t *ids, *valid;
     float* part;          // [piece][2][channels]
+    int32_t *chains, *chain;  // the numbers of rows that go on behind the piece they begin in, and [3][pieces] these pieces, in any order
 };
 
 // Threads (x: vectors of channels, y: pieces).  part: the sum of the row that the piece begins with, where that row begins before it
@@ -332,20 +361,22 @@ __global__ void __launch_bounds__(kSumThreads) piece_kernel(const Sums s, const 
 #pragma unroll
             for (int i = 0; i < V; ++i) p[i] = sum[i];
         } else {
-            Some<T, V> o;
+            float f[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) o.v[i] = narrow<T>(sum[i] * s.scale);
-            *reinterpret_cast<Some<T, V>*>(dtable + int64_t(row) * s.channels + c) = o;
+            for (int i = 0; i < V; ++i) f[i] = sum[i] * s.scale;
+            Pack<T, V> o;
+            o.set(f);
+            *reinterpret_cast<Pack<T, V>*>(dtable + int64_t(row) * s.channels + c) = o;
         }
     };
     for (int64_t p = p0; p < p1; p += kBatch) {
         uint32_t key[kBatch];
-        Some<T, V> v[kBatch];
+        Pack<T, V> v[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
             if (p + b < p1) {
                 key[b] = s.keys[p + b];
-                v[b] = *reinterpret_cast<const Some<T, V>*>(from + int64_t(s.ids[p + b]) * width);
+                v[b] = *reinterpret_cast<const Pack<T, V>*>(from + int64_t(s.ids[p + b]) * width);
             }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
@@ -357,54 +388,77 @@ __global__ void __launch_bounds__(kSumThreads) piece_kernel(const Sums s, const 
 #pragma unroll
                     for (int i = 0; i < V; ++i) sum[i] = 0.f;
                 }
+                float f[V];
+                v[b].get(f);
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum[i] += widen(v[b].v[i]);
+                for (int i = 0; i < V; ++i) sum[i] += f[i];
             }
     }
-    flush(p1 < n && s.keys[p1] == row);
+    const bool on = p1 < n && s.keys[p1] == row;
+    flush(on);
+    if (on && !head && c == 0) {
+        auto reaches = [&](int far) { return (piece + far) * s.piece < n && s.keys[(piece + far) * s.piece] == row; };
+        const int which = !reaches(reach(0) + 1) ? 0 : !reaches(reach(1) + 1) ? 1 : 2;
+        s.chain[which * s.pieces + atomicAdd(s.chains + which, 1)] = int32_t(piece);
+    }
 }
 
-// The rows that go on behind the piece in which they begin: those of kJoinPieces pieces, and 64 channels, a block.
-constexpr int kJoinPieces = 8, kJoinWays = 4;
+// The rows that go on behind the piece in which they begin.  A task is one of them and so many channels: 256 where it reaches a few
+// pieces, else fewer, with the block's threads along the pieces too.
+constexpr int kJoinThreads = 256;
+template <int CHANNELS, typename T>
+__device__ void join(const Sums& s, int64_t n, int64_t first, int c0, float* s_sum, T* dtable) {
+    constexpr int kWays = kJoinThreads / CHANNELS;
+    const int tid = threadIdx.x, way = tid / CHANNELS, lane = tid % CHANNELS, c = c0 + lane;
+    const uint32_t row = s.keys[(first + 1) * s.piece];
+    // the last piece that begins with the row: as many places at once as there are threads
+    int64_t last = first + 1, span = (n + s.piece - 1) / s.piece - last;  // pieces last .. last + span - 1 may, the first does
+    if (CHANNELS == kJoinThreads) span = min(span, int64_t(reach(0)));
+    else if (CHANNELS == 64) span = min(span, int64_t(reach(1)));
+    while (span > 1) {
+        const int64_t step = (span + kJoinThreads - 1) / kJoinThreads;
+        const bool same = tid * step < span && s.keys[(last + tid * step) * s.piece] == row;
+        const int64_t skip = int64_t(__syncthreads_count(same) - 1) * step;  // sorted: those that begin with it come first
+        last += skip;
+        span = min(step, span - skip);
+    }
+    float sum = 0.f, lost = 0.f;  // what the additions cut off: a frequent row has thousands of pieces
+    if (c < s.channels) {
+        if (way == 0) sum = s.part[(first * 2 + 1) * s.channels + c];
+#pragma unroll 8
+        for (int64_t q = first + 1 + way; q <= last; q += kWays) {
+            const float v = s.part[q * 2 * s.channels + c], t = sum + v, back = t - sum;
+            lost += (sum - (t - back)) + (v - back);
+            sum = t;
+        }
+    }
+    sum += lost;
+    if (kWays > 1) {
+        __syncthreads();  // the last task's sums have been read
+        s_sum[way * CHANNELS + lane] = sum;
+        __syncthreads();
+        if (way == 0)
+#pragma unroll
+            for (int w = 1; w < kWays; ++w) sum += s_sum[w * CHANNELS + lane];
+    }
+    if (way == 0 && c < s.channels) dtable[int64_t(row) * s.channels + c] = narrow<T>(sum * s.scale);
+}
 template <typename T>
-__global__ void __launch_bounds__(64 * kJoinWays) join_kernel(const Sums s, T* dtable) {
-    __shared__ float s_sum[kJoinWays][64];
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Sums s, T* dtable) {
+    __shared__ float s_sum[kJoinThreads];
     wait_for_last();
     const int64_t n = *s.valid;
-    const int tid = threadIdx.x, way = tid >> 6, c = blockIdx.y * 64 + (tid & 63);
-    for (int64_t first = int64_t(blockIdx.x) * kJoinPieces; first < int64_t(blockIdx.x + 1) * kJoinPieces; ++first) {
-        const int64_t p1 = (first + 1) * s.piece;
-        if (p1 >= n) return;
-        const uint32_t row = s.keys[p1];
-        if (s.keys[p1 - 1] != row || (first > 0 && s.keys[first * s.piece - 1] == row)) continue;  // nothing goes on, or it began before
-        // the last piece that begins with the row: as many places at once as there are threads
-        int64_t last = first + 1, span = (n + s.piece - 1) / s.piece - last;  // pieces last .. last + span - 1 may, the first does
-        while (span > 1) {
-            const int64_t step = (span + 64 * kJoinWays - 1) / (64 * kJoinWays);
-            const bool same = tid * step < span && s.keys[(last + tid * step) * s.piece] == row;
-            const int64_t skip = int64_t(__syncthreads_count(same) - 1) * step;  // sorted: those that begin with it come first
-            last += skip;
-            span = min(step, span - skip);
-        }
-        float sum = 0.f, lost = 0.f;  // what the additions cut off: a frequent row has thousands of pieces
-        if (c < s.channels) {
-            if (way == 0) sum = s.part[(first * 2 + 1) * s.channels + c];
-#pragma unroll 4
-            for (int64_t q = first + 1 + way; q <= last; q += kJoinWays) {
-                const float v = s.part[q * 2 * s.channels + c], t = sum + v, back = t - sum;
-                lost += (sum - (t - back)) + (v - back);
-                sum = t;
-            }
-        }
-        __syncthreads();  // the last row's sums have been read
-        s_sum[way][tid & 63] = sum + lost;
-        __syncthreads();
-        if (way == 0 && c < s.channels) {
-            sum = s_sum[0][tid];
-#pragma unroll
-            for (int w = 1; w < kJoinWays; ++w) sum += s_sum[w][tid];
-            dtable[int64_t(row) * s.channels + c] = narrow<T>(sum * s.scale);
-        }
+    const auto slabs = [&](int channels) { return (s.channels + channels - 1) / channels; };
+    const int64_t far = int64_t(s.chains[2]) * slabs(16), middle = far + int64_t(s.chains[1]) * slabs(64),
+                  all = middle + int64_t(s.chains[0]) * slabs(kJoinThreads);
+    for (int64_t task = blockIdx.x; task < all; task += gridDim.x) {  // the longest first
+        const int which = task < far ? 2 : task < middle ? 1 : 0, channels = which == 2 ? 16 : which == 1 ? 64 : kJoinThreads;
+        const int64_t t = task - (which == 2 ? 0 : which == 1 ? far : middle), chain = t / slabs(channels);
+        const int64_t first = s.chain[which * s.pieces + chain];
+        const int c0 = int(t - chain * slabs(channels)) * channels;
+        if (which == 2) join<16>(s, n, first, c0, s_sum, dtable);
+        else if (which == 1) join<64>(s, n, first, c0, s_sum, dtable);
+        else join<kJoinThreads>(s, n, first, c0, s_sum, dtable);
     }
 }
 
@@ -450,7 +504,7 @@ SumPlan sum_plan(const EmbedShape& s, bool aligned) {
 
 struct Work {
     uint32_t *keys[2], *counts, *totals;
-    int32_t *ids[2], *valid;
+    int32_t *ids[2], *valid, *chain;
     float* part;
     size_t bytes;
 };
@@ -471,7 +525,8 @@ Work work_of(const EmbedShape& s, const SumPlan& m, void* ws) {
     }
     w.counts = reinterpret_cast<uint32_t*>(take(p.one ? 0 : size_t(p.blocks) * kBins * 4));
     w.totals = reinterpret_cast<uint32_t*>(take(kBins * 4));
-    w.valid = reinterpret_cast<int32_t*>(take(2 * sizeof(int32_t)));
+    w.valid = reinterpret_cast<int32_t*>(take((kChains + kReaches) * sizeof(int32_t)));
+    w.chain = reinterpret_cast<int32_t*>(take(size_t(m.pieces) * kReaches * 4));
     w.part = reinterpret_cast<float*>(take(size_t(m.pieces) * 2 * s.channels * 4));
     w.bytes = used;
     return w;
@@ -508,9 +563,11 @@ cudaError_t bwd(const EmbedShape& s, const int32_t* index, const void* dout, voi
     const int32_t *ids = w.ids[0], *valid = w.valid;
     if (p.one) {
         e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOneSmem);
+        const bool beside = bytes > kLargeTable;
         if (e == cudaSuccess)
-            e = launch(sort_kernel, dim3(1 + std::min(zeros, sms - 1)), dim3(kOneThreads), kOneSmem, false, st, int(s.tokens), uint32_t(s.rows),
-                       p.passes, index, w.keys[0], w.ids[0], w.valid, table, bytes);
+            e = launch(sort_kernel, dim3(beside ? 1 : 1 + std::min(zeros, sms - 1)), dim3(kOneThreads), kOneSmem, false, st, int(s.tokens),
+                       uint32_t(s.rows), p.passes, index, w.keys[0], w.ids[0], w.valid, table, bytes);
+        if (e == cudaSuccess && beside) e = launch(zero_kernel, dim3(zeros), dim3(kThreads), 0, true, st, table, bytes);
     } else {
         Keys k = {s.tokens, uint32_t(s.rows), index, nullptr, nullptr, nullptr, 0, p.tiles};
         for (int i = 0; i < p.passes && e == cudaSuccess; ++i) {
@@ -519,19 +576,20 @@ cudaError_t bwd(const EmbedShape& s, const int32_t* index, const void* dout, voi
             if (e == cudaSuccess) e = launch(bins_kernel, dim3(kBins), dim3(kMaxBlocks), 0, true, st, p.blocks, w.counts, w.totals);
             if (e == cudaSuccess)
                 e = launch(place_kernel, dim3(p.blocks), dim3(kThreads), 0, true, st, k, w.counts, w.totals, w.keys[i & 1], w.ids[i & 1],
-                           w.valid + (i & 1));
+                           w.valid, i & 1);
             k.keys = keys = w.keys[i & 1], k.ids = ids = w.ids[i & 1], k.valid = valid = w.valid + (i & 1);
         }
     }
     if (e != cudaSuccess) return e;
-    const Sums u = {m.pieces, m.piece, s.channels, s.inner, s.column, float(s.scale), keys, ids, valid, w.part};
+    const Sums u = {m.pieces, m.piece, s.channels, s.inner, s.column, float(s.scale), keys, ids, valid, w.part, w.valid + kChains, w.chain};
     const dim3 grid(unsigned((m.pieces + m.y - 1) / m.y), m.slabs), block(m.x, m.y);
     const T* d = static_cast<const T*>(dout);
     e = m.v == 1 ? launch(piece_kernel<T, 1>, grid, block, 0, true, st, u, d, static_cast<T*>(dtable))
                  : launch(piece_kernel<T, 16 / sizeof(T)>, grid, block, 0, true, st, u, d, static_cast<T*>(dtable));
     if (e != cudaSuccess || m.pieces < 2) return e;
-    return launch(join_kernel<T>, dim3(unsigned((m.pieces - 1 + kJoinPieces - 1) / kJoinPieces), (s.channels + 63) / 64), dim3(64 * kJoinWays), 0,
-                  true, st, u, static_cast<T*>(dtable));
+    const int64_t most = std::min<int64_t>(m.pieces - 1, s.rows) * ((s.channels + 15) / 16);  // tasks
+    return launch(join_kernel<T>, dim3(unsigned(std::min<int64_t>(most, sms * 8))), dim3(kJoinThreads), 0, true, st, u,
+                  static_cast<T*>(dtable));
 }
 
 template <typename T>
