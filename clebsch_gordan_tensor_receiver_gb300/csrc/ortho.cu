@@ -359,9 +359,9 @@ template <int BN>
 struct Tile {
     static constexpr int a_bytes = kPanel, b_bytes = BN * 128;            // of a plane and stage
     static constexpr int stage = 2 * (a_bytes + b_bytes);
-    static constexpr int stages = BN == 256 ? 2 : 3;
+    static constexpr int stages = BN == 256 ? 2 : BN == 128 ? 3 : 4;
     static constexpr int smem = stages * stage + 1024;
-    static constexpr int cols = BN == 256 ? 512 : 256;                    // of tensor memory
+    static constexpr int cols = 2 * BN;                                   // of tensor memory
 };
 
 __device__ __forceinline__ void sum_warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSumWarps * 32) : "memory"); }
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
     if (kSym) {
         i = 0;
         for (;; ++i) {
-            const int across = i / (BN / 128) + 1;
+            const int across = i * 128 / BN + (BN < 128 ? 128 / BN : 1);
             if (t < across) break;
             t -= across;
         }
@@ -466,8 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
             const char* A = p.A + int64_t(matrix) * 2 * p.a_plane + int64_t(i) * p.a_panels * kPanel;
             const char* B = p.B + int64_t(matrix) * 2 * p.b_plane;
             // a tile's last column blocks may lie outside the matrix: their columns are not used
-            const int b_blocks = kSym ? min(BN / 128, p.blocks - j * (BN / 128)) : 0;
-            const uint32_t bytes = 2 * (L::a_bytes + (kSym ? b_blocks * kPanel : L::b_bytes));
+            constexpr int kPart = BN < 128 ? BN * 128 : kPanel;  // bytes of a panel's rows in the tile
+            const int b_blocks = !kSym ? 0 : BN < 128 ? 1 : min(BN / 128, p.blocks - j * (BN / 128));
+            const uint32_t bytes = 2 * (L::a_bytes + (kSym ? b_blocks * kPart : L::b_bytes));
             int k = 0;
             for (; k < nk; ++k) {
                 const int s = k % L::stages;
@@ -480,8 +481,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
                     bulk_load(to + q * L::a_bytes, A + q * p.a_plane + int64_t(kp) * kPanel, kPanel, bar);
                     const uint32_t tb = to + 2 * L::a_bytes + q * L::b_bytes;
                     if (kSym) {
-                        for (int b = 0; b < b_blocks; ++b)
-                            bulk_load(tb + b * kPanel, B + q * p.b_plane + (int64_t(j * (BN / 128) + b) * p.b_panels + kp) * kPanel, kPanel, bar);
+                        for (int b = 0; b < b_blocks; ++b) {
+                            const int first = j * BN + b * 128;  // row of B
+                            bulk_load(tb + b * kPart, B + q * p.b_plane + (int64_t(first >> 7) * p.b_panels + kp) * kPanel + (first & 127) * 128,
+                                      kPart, bar);
+                        }
                     } else {
                         const char* src = B + q * p.b_plane + (int64_t(kp >> 1) * p.b_panels + j * (BN / 64)) * kPanel + (kp & 1) * (kPanel / 2);
 #pragma unroll
@@ -586,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
             if (kSym) {
                 sum_warps_sync();
                 // rows and columns change places
-                const int columns = min(share, (i - j * (BN / 128)) * 128 - first);  // those of blocks below the diagonal
+                const int columns = min(share, i * 128 - j * BN - first);  // those of blocks below the diagonal
 #pragma unroll 1
                 for (int t = threadIdx.x; t < columns * 16; t += kSumWarps * 32) {
                     const int c = first + (t >> 4), k = t & 15, C = j * BN + c;
@@ -996,24 +1000,27 @@ cudaError_t launch(void (*k)(P...), int64_t blocks, int threads, int cluster, bo
 
 int sym_tiles(int blocks, int bn) {
     int t = 0;
-    for (int i = 0; i < blocks; ++i) t += i / (bn / 128) + 1;
+    for (int i = 0; i < blocks; ++i) t += i * 128 / bn + (bn < 128 ? 128 / bn : 1);
     return t;
 }
 
-// One product of every matrix (T: the type of kLast's result).  Tiles of 256 columns where they fill the card: they read a third less of the operands than those of
-// 128, which give twice the blocks.
+// One product of every matrix (T: the type of kLast's result).  Tiles of 256 columns where they fill the card, since they read the least;
+// smaller ones where only they give every SM one: what follows the sums takes a block's threads as long as they do, for products of
+// 256 x 256 (25 of them, five steps: 117 us with tiles of 128, 99 with 64).
+template <int BN, Kind K, typename T>
+cudaError_t product(const Product& p, int64_t tiles, int sms, cudaStream_t st) {
+    int splits = 1;  // of a long sum, where there are few tiles
+    if (K == kGram)
+        while (splits < kMaxSplits && splits * 8 < BN && tiles * splits * 2 <= sms && p.k_panels >= splits * 2 * 4) splits *= 2;
+    return launch(product_kernel<BN, K, T>, tiles * splits, kThreads, splits, true, Tile<BN>::smem, st, p);
+}
 template <Kind K, typename T>
 cudaError_t product(Product p, int matrices, int columns, int sms, cudaStream_t st) {
     constexpr bool kSym = K == kGram || K == kSquare;
-    auto tiles = [&](int bn) { return kSym ? sym_tiles(p.blocks, bn) : p.blocks * (up(columns, bn) / bn); };
-    const bool wide = int64_t(tiles(256)) * matrices >= sms * 3 / 4;
-    p.tiles = tiles(wide ? 256 : 128);
-    int splits = 1;  // of a long sum, where there are few tiles
-    if (K == kGram)
-        while (splits < kMaxSplits && int64_t(p.tiles) * matrices * splits * 2 <= sms && p.k_panels >= splits * 2 * 4) splits *= 2;
-    const int64_t grid = int64_t(p.tiles) * matrices * splits;
-    return wide ? launch(product_kernel<256, K, T>, grid, kThreads, splits, true, Tile<256>::smem, st, p)
-                : launch(product_kernel<128, K, T>, grid, kThreads, splits, true, Tile<128>::smem, st, p);
+    auto tiles = [&](int bn) { return p.tiles = kSym ? sym_tiles(p.blocks, bn) : p.blocks * (up(columns, bn) / bn), int64_t(p.tiles) * matrices; };
+    if (tiles(256) >= sms * 3 / 4) return product<256, K, T>(p, tiles(256), sms, st);
+    if (tiles(64) <= sms) return product<64, K, T>(p, tiles(64), sms, st);
+    return product<128, K, T>(p, tiles(128), sms, st);
 }
 
 template <typename T>
