@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
 // A cluster has a matrix, each of its blocks up to 256 of X's columns (4 panels) and all of P.  P's terms are summed over the
 // cluster: the blocks' partial sums lie where P will be, each block adds up some rows and writes them to all.
 
-constexpr int kChipThreads = 544, kChipPanels = 4;  // 16 warps that add up and write, one that issues the matrix instructions
+constexpr int kChipThreads = 512, kChipPanels = 4;  // all add up and write; warp 0 issues the matrix instructions, which all wait for
 constexpr int kChipSmem = 2 * kChipPanels * kPanel + 4 * kPanel + 1024;
 constexpr int kChipBlocks = 8;  // of a cluster at most
 
@@ -640,7 +640,6 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
     char* xs = smem + 4 * kPanel;  // P: hi panels 0, 1, lo 0, 1; X: hi panels, lo panels
     const uint32_t sp = own_offset(uniform(smem_u32(smem))), sx = sp + 4 * kPanel;  // for descriptors
     const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const bool writes = warp < 16;
     cg::cluster_group cluster = cg::this_cluster();
     const int blocks = int(cluster.num_blocks()), rank = int(cluster.block_rank());
     const int matrix = blockIdx.x / blocks;
@@ -655,7 +654,7 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
         bar_init(bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 16) tmem_alloc(smem_u32(&s_tmem), 512);
+    if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 512);
 
     // X_0.  A thread has 8 columns of a row in each half panel (64 rows of 64 columns): lanes along the values that are consecutive in G
     float v[2 * kChipPanels][8];
@@ -665,26 +664,24 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
         c = (u >> 1) * 64 + (p.g.turned ? ((u & 1) * 4 + (t >> 7)) * 8 : (t & 7) * 8);
     };
     Squares squares;
-    if (writes) {
 #pragma unroll
-        for (int u = 0; u < 2 * kChipPanels; ++u)
-            if (u < 2 * p.panels) {
-                int r, c;
-                place(u, r, c);
-                const int left = r < p.g.m ? cols - c : 0;
-                if (p.g.turned) {
+    for (int u = 0; u < 2 * kChipPanels; ++u)
+        if (u < 2 * p.panels) {
+            int r, c;
+            place(u, r, c);
+            const int left = r < p.g.m ? cols - c : 0;
+            if (p.g.turned) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[u][k] = k < left ? widen(g[(c0 + c + k) * p.g.row + r]) : 0.f;
-                } else {
-                    load_some<T, 8>(g + (left > 0 ? r * p.g.row + c0 + c : 0), left, p.vec_in, v[u]);
-                }
+                for (int k = 0; k < 8; ++k) v[u][k] = k < left ? widen(g[(c0 + c + k) * p.g.row + r]) : 0.f;
+            } else {
+                load_some<T, 8>(g + (left > 0 ? r * p.g.row + c0 + c : 0), left, p.vec_in, v[u]);
             }
+        }
 #pragma unroll
-        for (int u = 0; u < 2 * kChipPanels; ++u)
-            if (u < 2 * p.panels) squares.add_all(v[u]);
-    }
+    for (int u = 0; u < 2 * kChipPanels; ++u)
+        if (u < 2 * p.panels) squares.add_all(v[u]);
     fence_before();
-    const double sum = block_squares<17>(squares);  // (and the tensor memory's address is there)
+    const double sum = block_squares<16>(squares);  // (and the tensor memory's address is there)
     fence_after();
     const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t*>(&s_tmem));
     if (threadIdx.x == 0) s_norm = sum;
@@ -700,27 +697,25 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
     }
     __syncthreads();
     const Factor inv = s_factor;
-    if (writes) {
 #pragma unroll
-        for (int u = 0; u < 2 * kChipPanels; ++u)
-            if (u < 2 * p.panels) {
-                int r, c;
-                place(u, r, c);
+    for (int u = 0; u < 2 * kChipPanels; ++u)
+        if (u < 2 * p.panels) {
+            int r, c;
+            place(u, r, c);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[u][k] = inv.of(v[u][k]) * kHeld;
-                Chunk(v[u]).store(xs + (c >> 6) * kPanel + in_panel(r, c & 63), x_plane);
-            }
-    }
+            for (int k = 0; k < 8; ++k) v[u][k] = inv.of(v[u][k]) * kHeld;
+            Chunk(v[u]).store(xs + (c >> 6) * kPanel + in_panel(r, c & 63), x_plane);
+        }
 
     volatile int* dead = &s_dead;
     unsigned* status = &ortho_status_word;
     const int quad = warp & 3, quarter = warp >> 2, row = quad * 32 + lane;
     const uint32_t lanes = uint32_t(quad * 32) << 16;
-    const uint32_t lead = warp == 16 ? elect_lane() : 0;
+    const uint32_t lead = warp == 0 ? elect_lane() : 0;
     const int k16 = (p.g.m + 15) / 16;            // instructions of a sum over the rows
     const int c16 = max(1, (cols + 15) / 16);     // and over this block's columns; one at least: zeros
     const int m16 = 16 * k16;                     // P's rows and columns in use; what lies beyond is read by no sum that counts
-    const bool rows_live = writes && quad * 32 < p.g.m, p_live = rows_live && quarter * 32 < m16;
+    const bool rows_live = quad * 32 < p.g.m, p_live = rows_live && quarter * 32 < m16;
     const uint32_t id_p = mma_desc<__half>(m16, false), id_x = mma_desc<__half>(width, true);
     const bool wide = width > 128;
     uint32_t phase = 0;
@@ -731,7 +726,7 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
         fence_before();
         ok = __syncthreads_and(ok);  // after a wait that was given up the block goes on to the end, for the others' sake
         if (!ok) return;
-        if (warp == 16) {
+        if (warp == 0) {
             fence_after();
             issue();
             mma_commit(lead, bar);
@@ -817,7 +812,7 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
             for (int u = 0; u < 2; ++u) {
                 const int t = threadIdx.x + u * 512;
                 const int row_of = t / chunks, r = rank * share + row_of;
-                if (writes && t < tasks && r < m16) {
+                if (t < tasks && r < m16) {
                     const int chunk = (t - row_of * chunks) * 2;
                     float4 x[kChipBlocks], y[kChipBlocks];
 #pragma unroll
@@ -842,7 +837,7 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
             for (int u = 0; u < 2; ++u) {
                 const int t = threadIdx.x + u * 512;
                 const int row_of = t / chunks, r = rank * share + row_of;
-                if (writes && t < tasks && r < m16) {
+                if (t < tasks && r < m16) {
                     const int c = (t - row_of * chunks) * 8;
                     const Chunk w(v[u]);
 #pragma unroll
@@ -914,7 +909,7 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
     }
     fence_before();
     __syncthreads();
-    if (warp == 16) {
+    if (warp == 0) {
         if (!ok) bar_wait_last(bar, phase ^ 1, status);
         __syncwarp();
         fence_after();
