@@ -370,13 +370,15 @@ template <int BN, Kind K, typename T>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
     using L = Tile<BN>;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t s_bars[2 * L::stages + 3];
+    __shared__ uint64_t s_bars[4 * L::stages + 3];
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = uniform(smem_u32(smem));
     const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const uint32_t full = smem_u32(s_bars), empty = full + 8 * L::stages, d_full = empty + 8 * L::stages, d_free = d_full + 8, fin = d_free + 8;
+    // A stage's planes arrive hi first (full) and lo behind (full_lo); B's hi and A's lo are free (empty) before A's hi and B's lo (empty_lo)
+    const uint32_t full = smem_u32(s_bars), full_lo = full + 8 * L::stages, empty = full_lo + 8 * L::stages, empty_lo = empty + 8 * L::stages,
+                   d_full = empty_lo + 8 * L::stages, d_free = d_full + 8, fin = d_free + 8;
     constexpr bool kSym = K == kGram || K == kSquare;
 
     // the tile: i 128 rows, j BN columns
@@ -405,7 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
         s_dead = 0;
         for (int s = 0; s < L::stages; ++s) {
             bar_init(full + 8 * s, 1);
+            bar_init(full_lo + 8 * s, 1);
             bar_init(empty + 8 * s, 1);
+            bar_init(empty_lo + 8 * s, 1);
         }
         bar_init(d_full, 1);
         bar_init(d_free, kSumWarps);
@@ -468,17 +472,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
             // a tile's last column blocks may lie outside the matrix: their columns are not used
             constexpr int kPart = BN < 128 ? BN * 128 : kPanel;  // bytes of a panel's rows in the tile
             const int b_blocks = !kSym ? 0 : BN < 128 ? 1 : min(BN / 128, p.blocks - j * (BN / 128));
-            const uint32_t bytes = 2 * (L::a_bytes + (kSym ? b_blocks * kPart : L::b_bytes));
+            const uint32_t bytes = L::a_bytes + (kSym ? b_blocks * kPart : L::b_bytes);  // of a plane
             int k = 0;
             for (; k < nk; ++k) {
-                const int s = k % L::stages;
-                if (k >= L::stages && !bar_wait(empty + 8 * s, (k / L::stages - 1) & 1, dead, status)) break;
-                const uint32_t to = sb + uint32_t(s * L::stage), bar = full + 8 * s;
-                arrive_tx(bar, bytes);
-                const int kp = k0 + k;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    bulk_load(to + q * L::a_bytes, A + q * p.a_plane + int64_t(kp) * kPanel, kPanel, bar);
+                const int s = k % L::stages, kp = k0 + k;
+                const uint32_t to = sb + uint32_t(s * L::stage), parity = (k / L::stages - 1) & 1;
+                auto load_a = [&](int q, uint32_t bar) { bulk_load(to + q * L::a_bytes, A + q * p.a_plane + int64_t(kp) * kPanel, kPanel, bar); };
+                auto load_b = [&](int q, uint32_t bar) {
                     const uint32_t tb = to + 2 * L::a_bytes + q * L::b_bytes;
                     if (kSym) {
                         for (int b = 0; b < b_blocks; ++b) {
@@ -491,10 +491,21 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
 #pragma unroll
                         for (int b = 0; b < BN / 64; ++b) bulk_load(tb + b * (kPanel / 2), src + b * kPanel, kPanel / 2, bar);
                     }
-                }
+                };
+                if (k >= L::stages && !bar_wait(empty + 8 * s, parity, dead, status)) break;
+                arrive_tx(full + 8 * s, bytes);
+                arrive_tx(full_lo + 8 * s, bytes);
+                load_b(0, full + 8 * s);
+                load_a(1, full_lo + 8 * s);
+                if (k >= L::stages) bar_wait_last(empty_lo + 8 * s, parity, status);  // 4 instructions behind: they end
+                load_a(0, full + 8 * s);
+                load_b(1, full_lo + 8 * s);
             }
             // what was loaded has landed before the block ends, where a wait was given up too
-            for (int l = max(0, k - L::stages); l < k; ++l) bar_wait_last(full + 8 * (l % L::stages), (l / L::stages) & 1, status);
+            for (int l = max(0, k - L::stages); l < k; ++l) {
+                bar_wait_last(full + 8 * (l % L::stages), (l / L::stages) & 1, status);
+                bar_wait_last(full_lo + 8 * (l % L::stages), (l / L::stages) & 1, status);
+            }
         }
         __syncwarp();
     } else {
@@ -520,12 +531,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) mma_ss(lead, d_hi, da(0, q), db(0, q), id, !first || q > 0);
             if (last) mma_commit(lead, d_full);
+            ok = warp_wait(full_lo + 8 * s, (k / L::stages) & 1, dead, status);
+            if (!ok) break;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                mma_ss(lead, d_lo, da(0, q), db(1, q), id, k > 0 || q > 0);
-                mma_ss(lead, d_lo, da(1, q), db(0, q), id, true);
-            }
+            for (int q = 0; q < 4; ++q) mma_ss(lead, d_lo, da(1, q), db(0, q), id, k > 0 || q > 0);
             mma_commit(lead, empty + 8 * s);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mma_ss(lead, d_lo, da(0, q), db(1, q), id, true);
+            mma_commit(lead, empty_lo + 8 * s);
         }
         // every instruction issued has finished before the sums are read to the end and the tensor memory goes
         mma_commit(lead, fin);
