@@ -1358,7 +1358,9 @@ uvu_status ortho_check(const uvu_ortho_shape* s) {
     if (!(s->eps >= 0) || !std::isfinite(float(s->eps))) return fail(UVU_ERR_INVALID_ARGUMENT, "eps must be a finite fp32 value >= 0");
     for (int64_t v : {s->g_matrix, s->g_row, s->o_matrix, s->o_row})
         if (v < 0 || v > (int64_t(1) << 40)) return fail(UVU_ERR_INVALID_ARGUMENT, "strides must be in [0, 2^40]");
-    if ((s->rows > 1 && s->o_row < s->cols) || (s->n_matrices > 1 && s->o_matrix == 0))
+    // matrices one after the other, or rows of one matrix between those of the others
+    const int64_t matrix = int64_t(s->rows - 1) * s->o_row + s->cols, row = int64_t(s->n_matrices - 1) * s->o_matrix + s->cols;
+    if ((s->rows > 1 && s->o_row < s->cols) || (s->n_matrices > 1 && (s->o_matrix < s->cols || (s->o_matrix < matrix && s->o_row < row))))
         return fail(UVU_ERR_INVALID_ARGUMENT, "the rows of out must not overlap");
     return UVU_OK;
 }

@@ -12,15 +12,21 @@
 // those of large matrices (1 / sqrt(m n)) normal numbers of fp16 and those near 1 far from its largest.
 //
 // An accumulating matrix instruction (16 terms) cuts its sum towards zero, by 2^-24 of it in the mean (measured: 2.8 2^-24 after
-// four of them, 7.7 after eight, on sums of one sign).  So the hi hi accumulator is taken into fp32 registers every 128 terms, while the
-// lo products, two thirds of the instructions, run, and the mean of what was cut is put back: a factor 1 + 2^-24 for each instruction.
-// Without it five steps on 64 x 1664 values were off by 2.4e-6, the plain form in fp32 by 9.6e-7.
+// four of them, 7.7 after eight, on sums of one sign).  So the hi hi sums leave their accumulator every 64 terms, while the lo products,
+// two thirds of the instructions, run (on chip they go to three accumulators in turn), and the mean of what was cut is put back: a
+// factor 1 + 2^-24 for each instruction.  Five steps on 64 x 1664 values are off by 8e-7, by 2.4e-6 without all that; fp32 sums: 9.6e-7.
 //
 // A matrix is kept in panels of 128 rows and 64 columns, 16 KB each, whose bytes lie as the matrix instruction reads them
 // (128-byte swizzle): a panel is loaded by one bulk copy, and no tensor map is needed.
 //
 // Two forms.  On chip, for m <= 128 and n <= 2048: a block, or a cluster of up to 8 that splits the columns, keeps X and P in shared
-// memory from the first step to the last; one launch.  Else a kernel for each product, of 128 x 256 or 128 x 128 tiles.
+// memory from the first step to the last; one launch.  Else a kernel for each product, of tiles of 128 rows and 256, 128 or 64 columns.
+//
+// What bounds it.  Large matrices: the tensor cores (two of 4096 x 2048 in fp32: 1.42 ms, 1.33 PFLOP/s of fp16 products with a step of
+// 250 us at first and 290 us when the card's power limit has lowered its clocks).  Small ones: the chain of three products a step, each of
+// which waits for the last one's planes: some 2000 cycles of products of 128 x 128 x 128 and 2700 of writing planes on chip (13 of
+// 128 x 128: 44 us), 9000 to 14,000 with loads and a launch otherwise (25 of 256 x 256 in bf16: 98 us).  All phases in one launch whose blocks
+// wait for one another's tiles took as long: the flags cost what the launches do.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -353,7 +359,6 @@ struct Product {
 constexpr int kSumWarps = 16;  // they add up and write; then one that loads, and one that issues the matrix instructions
 constexpr int kThreads = (kSumWarps + 2) * 32;
 constexpr int kMaxSplits = 8;  // of a long sum
-constexpr int kRunPanels = 1;  // panels of 64 terms between two readings of the hi hi accumulator
 
 template <int BN>
 struct Tile {
@@ -400,7 +405,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
         i = t - j * p.blocks;
     }
     const int k0 = int(int64_t(p.k_panels) * part / splits), k1 = int(int64_t(p.k_panels) * (part + 1) / splits), nk = k1 - k0;
-    const int runs = (nk + kRunPanels - 1) / kRunPanels;
 
     next_may_begin();
     if (threadIdx.x == 0) {
@@ -435,18 +439,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
 #pragma unroll
         for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
         bool ok = true;
-        for (int r = 0; r < runs && ok; ++r) {
+        for (int r = 0; r < nk && ok; ++r) {  // panel by panel: 64 terms (two cost as much, and cut twice as much)
             ok = warp_wait(d_full, r & 1, dead, status);
             if (!ok) break;
             fence_after();
-            const float f = uncut(4 * min(kRunPanels, nk - r * kRunPanels));
 #pragma unroll
             for (int b = 0; b < kCols / 16; ++b) {
                 float v[16];
                 tmem_ld16(from + 16 * b, v);
                 tmem_wait_ld(v);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) acc[16 * b + c] = fmaf(v[c], f, acc[16 * b + c]);
+                for (int c = 0; c < 16; ++c) acc[16 * b + c] = fmaf(v[c], uncut(4), acc[16 * b + c]);
             }
             fence_before();
             __syncwarp();
@@ -515,11 +518,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
         const uint32_t d_hi = tmem, d_lo = tmem + BN;
         bool ok = true;
         for (int k = 0; k < nk && ok; ++k) {
-            const int s = k % L::stages, r = k / kRunPanels;
-            const bool first = k % kRunPanels == 0, last = k % kRunPanels == kRunPanels - 1 || k == nk - 1;
+            const int s = k % L::stages;
             ok = warp_wait(full + 8 * s, (k / L::stages) & 1, dead, status);
-            if (ok && first && r > 0) {
-                ok = warp_wait(d_free, (r - 1) & 1, dead, status);
+            if (ok && k > 0) {
+                ok = warp_wait(d_free, (k - 1) & 1, dead, status);
                 fence_after();
             }
             if (!ok) break;
@@ -529,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Product p) {
                 return kSym ? desc_cols(b + plane * L::b_bytes, q) : desc_rows(b + plane * L::b_bytes, q, kPanel / 2);
             };
 #pragma unroll
-            for (int q = 0; q < 4; ++q) mma_ss(lead, d_hi, da(0, q), db(0, q), id, !first || q > 0);
-            if (last) mma_commit(lead, d_full);
+            for (int q = 0; q < 4; ++q) mma_ss(lead, d_hi, da(0, q), db(0, q), id, q > 0);
+            mma_commit(lead, d_full);
             ok = warp_wait(full_lo + 8 * s, (k / L::stages) & 1, dead, status);
             if (!ok) break;
 #pragma unroll

@@ -54,7 +54,8 @@ class Muon(torch.optim.Optimizer):
             buf.lerp_(p.grad, 1 - m)
             updates.append((p.grad.lerp(buf, m) if group["nesterov"] else buf).reshape(-1, *size))
         u = torch.cat(updates)
-        uvu.orthogonalize(u, u, steps=group["steps"], coefficients=group["coefficients"], eps=group["eps"])
+        with torch.cuda.device(u.device):
+            uvu.orthogonalize(u, u, steps=group["steps"], coefficients=group["coefficients"], eps=group["eps"])
         rate = -group["lr"] * max(1.0, size[0] / size[1]) ** 0.5
         at = 0
         for p, part in zip(params, updates):

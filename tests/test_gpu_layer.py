@@ -57,7 +57,8 @@ def nan_like(shape, kind="f32"):
 # tokens, rows, channels, inner, column
 EMBEDS = [(1, 1, 1, 1, 0), (1, 70000, 8, 1, 0), (61, 10, 128, 4, 0), (61, 10, 128, 4, 3), (5, 3, 7, 9, 4), (33, 300, 40, 1, 0),
           (1000, 1, 24, 1, 0), (1000, 5, 33, 1, 0), (257, 256, 16, 1, 0), (3000, 255, 12, 2, 1), (2049, 66000, 9, 1, 0), (9001, 89, 128, 4, 0),
-          (20000, 3, 1100, 1, 0), (40001, 119, 64, 1, 0), (300, 100, 5, 1, 0), (70000, 2000, 20, 1, 0), (12000, 65536, 256, 1, 0)]
+          (20000, 3, 1100, 1, 0), (40001, 119, 64, 1, 0), (300, 100, 5, 1, 0), (70000, 2000, 20, 1, 0), (12000, 65536, 256, 1, 0),
+          (16384, 7, 40, 1, 0), (16385, 70000, 8, 1, 0), (30000, 4, 16, 9, 2)]
 
 
 def embed_case(case, kind, pad=True):
@@ -147,7 +148,7 @@ def test_embedding_repeats_bit_for_bit():
 
 # rows, channels, inner
 NORMS = [(1, 1, 1), (100, 16, 4), (7, 24, 1), (33, 7, 9), (5, 40, 1), (300, 128, 4), (17, 512, 1), (64, 100, 1), (9, 1000, 1), (3, 1024, 1),
-         (5, 1025, 1), (2, 333, 9), (11, 2048, 1), (3, 8192, 1), (4, 8190, 1), (3, 8191, 1), (20011, 96, 1), (3000, 513, 1), (70001, 4, 1)]
+         (5, 1025, 1), (2, 333, 9), (11, 2048, 1), (3, 8192, 1), (4, 8190, 1), (3, 8191, 1), (20011, 96, 1), (3000, 513, 1), (70001, 4, 1), (9001, 1024, 1), (30001, 512, 1), (2500, 2048, 1), (20000, 33, 9)]
 
 
 def norm_case(case, kind):
@@ -259,7 +260,7 @@ def test_rms_norm_of_no_rows_and_repeats():
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("group", [0, 1, 32, 40, 64, 128])
-@pytest.mark.parametrize("case", [(1, 1, 1), (100, 16, 4), (9, 1000, 1), (5, 129, 1), (33, 128, 9), (3, 8192, 1), (7, 1100, 1), (301, 256, 1)],
+@pytest.mark.parametrize("case", [(1, 1, 1), (100, 16, 4), (9, 1000, 1), (5, 129, 1), (33, 128, 9), (3, 8192, 1), (7, 1100, 1), (301, 256, 1), (20001, 256, 1), (3000, 301, 1)],
                          ids=lambda c: "x".join(map(str, c)))
 def test_rms_norm_quant(case, group, kind):
     (x, res, _, _, gamma), (xr, rr, _, _, gr) = norm_case(case, kind)
@@ -328,6 +329,17 @@ def test_orthogonalize(case, kind):
     if kind == "f32" and case != (1, 1, 1):
         # what the limit cannot see: each value against fp32's usual error, with the steps' stretching of it
         check(values(out), np.stack([layer.newton_schulz(a, 5, MUON, 1e-7)[-1] for a in gr]), False)
+
+
+@pytest.mark.parametrize("shape", [(640, 650), (650, 600)], ids=str)
+def test_orthogonalize_many_large(shape):
+    """Enough matrices that the widest tiles are taken, of an odd number of row blocks: copies give the same results."""
+    rng = np.random.default_rng(12)
+    g, gr = rounded(gradient(shape, rng), "f32")
+    out = nan_like((16, *shape))
+    uvu.orthogonalize(g.expand(16, -1, -1), out)
+    check(values(out[0]), layer.newton_schulz(gr, 5, MUON, 1e-7)[-1], False)
+    assert all(torch.equal(out[0], o) for o in out)
 
 
 @pytest.mark.parametrize("steps, coefficients, eps, scale", [(0, MUON, 1e-7, 2.0), (1, (2.0, -1.5, 0.5), 0.0, 1.0), (9, (1.875, -1.25, 0.375), 1e-3, -0.5)],
@@ -430,6 +442,7 @@ def test_streams_and_graphs():
             g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for o in outs for a, b in zip(o, want))
+    assert uvu.orthogonalize_device_status() == 0
 
 
 @pytest.mark.parametrize("kind", KINDS)

@@ -68,7 +68,7 @@ def shape(**change):
 @pytest.mark.parametrize("change, status", [
     (dict(dtype=F64), 2), (dict(n_matrices=-1), 1), (dict(n_matrices=65536), 1), (dict(rows=0), 1), (dict(cols=16385), 1), (dict(steps=-1), 1),
     (dict(steps=65), 1), (dict(reserved=1), 1), (dict(a=float("nan")), 1), (dict(c=1e39), 1), (dict(scale=float("inf")), 1), (dict(eps=-1e-9), 1),
-    (dict(g_row=-1), 1), (dict(o_row=15), 1), (dict(o_matrix=0), 1)], ids=str)
+    (dict(g_row=-1), 1), (dict(o_row=15), 1), (dict(o_matrix=0), 1), (dict(o_matrix=127), 1), (dict(o_matrix=16, o_row=31), 1)], ids=str)
 def test_orthogonalize(change, status):
     assert refused(uvu.uvu_orthogonalize, shape(**change), A, A, A, 2 ** 40, None)[0] == status
     b = ctypes.c_size_t()
@@ -78,6 +78,8 @@ def test_orthogonalize(change, status):
 def test_orthogonalize_more():
     assert refused(uvu.uvu_orthogonalize, None, A, A, A, 0, None)[0] == 1
     uvu.uvu_orthogonalize(shape(n_matrices=0), None, None, None, 0, None)
+    b = ctypes.c_size_t()
+    uvu.uvu_orthogonalize_workspace(shape(o_matrix=16, o_row=32), ctypes.byref(b))  # rows of one matrix between those of the other
     assert refused(uvu.uvu_orthogonalize, shape(), None, A, A, 2 ** 40, None)[0] == 1
     assert refused(uvu.uvu_orthogonalize, shape(), A, A + 2, A, 2 ** 40, None)[0] == 1
     assert refused(uvu.uvu_orthogonalize, shape(g_row=32, g_matrix=256), A, A, A, 2 ** 40, None)[0] == 1  # in place at other strides
