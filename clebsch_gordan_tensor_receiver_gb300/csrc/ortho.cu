@@ -139,19 +139,18 @@ struct Squares {
             large += __shfl_xor_sync(0xffffffffu, large, d);
         }
     }
-    __device__ __forceinline__ double total() const { return double(small) * 0x1p-180 + double(mid) + double(large) * 0x1p180; }
+    __device__ __forceinline__ void add(const Squares& o) { small += o.small, mid += o.mid, large += o.large; }
 };
 // Over the block, in thread 0.
 template <int WARPS>
-__device__ __forceinline__ double block_squares(Squares q) {
+__device__ __forceinline__ Squares block_squares(Squares q) {
     __shared__ Squares s_part[WARPS];
     q.over_warp();
     if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = q;
     __syncthreads();
-    if (threadIdx.x >= 32) return 0;
     q = threadIdx.x < WARPS ? s_part[threadIdx.x] : Squares();
-    q.over_warp();
-    return threadIdx.x == 0 ? q.total() : 0;
+    if (threadIdx.x < 32) q.over_warp();
+    return q;
 }
 
 // X's rows and columns, and where the caller's matrix has them: X[r][c] at r * row + c, or at c * row + r where it is turned.
@@ -184,7 +183,7 @@ __device__ __forceinline__ void load_some(const T* p, int left, bool vec, float 
 
 // 8 values of a row a thread, 4 times at once.
 template <typename T>
-__global__ void __launch_bounds__(256) norm_kernel(int rows, int cols, int64_t g_matrix, int64_t g_row, bool vec, const T* g, double* part) {
+__global__ void __launch_bounds__(256) norm_kernel(int rows, int cols, int64_t g_matrix, int64_t g_row, bool vec, const T* g, Squares* part) {
     const T* a = g + int64_t(blockIdx.y) * g_matrix;
     const int chunks = (cols + 7) / 8;
     const int count = rows * chunks;
@@ -199,7 +198,7 @@ __global__ void __launch_bounds__(256) norm_kernel(int rows, int cols, int64_t g
 #pragma unroll
         for (int u = 0; u < 4; ++u) q.add_all(v[u]);
     }
-    const double total = block_squares<8>(q);
+    const Squares total = block_squares<8>(q);
     if (threadIdx.x == 0) part[blockIdx.y * kNormBlocks + blockIdx.x] = total;
 }
 
@@ -208,23 +207,28 @@ __global__ void __launch_bounds__(256) norm_kernel(int rows, int cols, int64_t g
 struct Factor {
     float first, second;
     __device__ __forceinline__ Factor() {}
-    __device__ __forceinline__ Factor(double squares, double eps) {
-        const double inv = squares == 0.0 ? 0.0 : isinf(squares) ? double(NAN) : 1.0 / (sqrt(squares) + eps);
-        first = inv > 0x1p100 ? 0x1p60f : 1.f;
-        second = float(inv / double(first));
+    __device__ __forceinline__ Factor(const Squares& q, double eps) {
+        first = 1.f;
+        if (q.small < 0x1p100f && q.large == 0.f && q.mid > 0x1p-60f && q.mid < 0x1p120f) {  // what `small` stands for is below 2^-80
+            second = 1.f / (sqrtf(q.mid) + float(eps));
+        } else {  // rarely: fp64 is slow here
+            const double squares = double(q.small) * 0x1p-180 + double(q.mid) + double(q.large) * 0x1p180;
+            const double inv = squares == 0.0 ? 0.0 : isinf(squares) ? double(NAN) : 1.0 / (sqrt(squares) + eps);
+            if (inv > 0x1p100) first = 0x1p60f;
+            second = float(inv / double(first));
+        }
     }
     __device__ __forceinline__ float of(float v) const { return v * first * second; }
 };
 
 // That of the block's matrix, in every thread of the block.
-__device__ __forceinline__ Factor inverse_norm(const double* part, int parts, double eps) {
+__device__ __forceinline__ Factor inverse_norm(const Squares* part, int parts, double eps) {
     __shared__ Factor s_inv;
     if (threadIdx.x < 32) {
-        double v = 0;
-        for (int i = threadIdx.x; i < parts; i += 32) v += part[i];
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-        if (threadIdx.x == 0) s_inv = Factor(v, eps);
+        Squares q;
+        for (int i = threadIdx.x; i < parts; i += 32) q.add(part[i]);
+        q.over_warp();
+        if (threadIdx.x == 0) s_inv = Factor(q, eps);
     }
     __syncthreads();
     return s_inv;
@@ -232,7 +236,7 @@ __device__ __forceinline__ Factor inverse_norm(const double* part, int parts, do
 
 // X_0's planes, a 64 x 64 piece a block: (column panel, half a row block, matrix).
 template <typename T>
-__global__ void __launch_bounds__(256) take_kernel(Side s, bool vec, const T* g, const double* part, int parts, double eps, int panels,
+__global__ void __launch_bounds__(256) take_kernel(Side s, bool vec, const T* g, const Squares* part, int parts, double eps, int panels,
                                                    size_t plane, char* x) {
     __shared__ float tile[64][65];
     const T* a = g + int64_t(blockIdx.z) * s.matrix;
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(256) take_kernel(Side s, bool vec, const T* g,
 // No steps: out = scale X_0.
 template <typename T>
 __global__ void __launch_bounds__(256) scale_kernel(int rows, int cols, int64_t g_matrix, int64_t g_row, int64_t o_matrix, int64_t o_row,
-                                                    float scale, const T* g, const double* part, int parts, double eps, T* out) {
+                                                    float scale, const T* g, const Squares* part, int parts, double eps, T* out) {
     const Factor inv = inverse_norm(part + int64_t(blockIdx.y) * kNormBlocks, parts, eps);
     const T* a = g + int64_t(blockIdx.y) * g_matrix;
     T* o = out + int64_t(blockIdx.y) * o_matrix;
@@ -321,9 +325,14 @@ template <typename T>
 __device__ __forceinline__ void give(const float* from, int threads, const Side& s, T* out, bool vec, int r0, int c0, int width) {
     const int chunks = s.turned ? 16 : width / 8;
     const int lines = s.turned ? min(width, s.n - c0) : min(128, s.m - r0);
+    const int step = threads / chunks, rest = threads - step * chunks;
+    int line = int(threadIdx.x) / chunks, k = int(threadIdx.x) - line * chunks;
 #pragma unroll 1
-    for (int i = threadIdx.x; i < lines * chunks; i += threads) {
-        const int line = i / chunks, k = i - line * chunks;
+    for (; line < lines; line += step, k += rest) {
+        if (k >= chunks) {
+            k -= chunks;
+            if (++line >= lines) break;
+        }
         float v[8];
         if (s.turned) {
             staged_column(from, line, k, width, v);
@@ -649,7 +658,7 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
     __shared__ uint64_t s_bar;
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
-    __shared__ double s_norm;
+    __shared__ Squares s_norm;
     __shared__ Factor s_factor;
     char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     char* xs = smem + 4 * kPanel;  // P: hi panels 0, 1, lo 0, 1; X: hi panels, lo panels
@@ -696,15 +705,15 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
     for (int u = 0; u < 2 * kChipPanels; ++u)
         if (u < 2 * p.panels) squares.add_all(v[u]);
     fence_before();
-    const double sum = block_squares<16>(squares);  // (and the tensor memory's address is there)
+    const Squares sum = block_squares<16>(squares);  // (and the tensor memory's address is there)
     fence_after();
     const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t*>(&s_tmem));
     if (threadIdx.x == 0) s_norm = sum;
     if (blocks > 1) {
         cluster.sync();
         if (threadIdx.x == 0) {
-            double total = 0;
-            for (int b = 0; b < blocks; ++b) total += *cluster.map_shared_rank(&s_norm, b);
+            Squares total;
+            for (int b = 0; b < blocks; ++b) total.add(*cluster.map_shared_rank(&s_norm, b));
             s_factor = Factor(total, p.eps);
         }
     } else if (threadIdx.x == 0) {
@@ -821,45 +830,47 @@ __global__ void __launch_bounds__(kChipThreads, 1) chip_kernel(const Chip p, con
             }
             cluster.sync();
             // each block adds up its share of the rows: 8 columns a thread, two times for two blocks of all 128 rows
-            const int chunks = m16 / 8, share = (m16 + blocks - 1) / blocks, tasks = share * chunks;
-            float v[2][8];
+            const int chunks = m16 / 8, share = (m16 + blocks - 1) / blocks;
+            auto exchange = [&](auto count) {
+                constexpr int B = decltype(count)::value, U = B == 2 ? 2 : 1;
+                float v[U][8];
+                int r[U], c[U];
+                bool on[U];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = threadIdx.x + u * 512;
-                const int row_of = t / chunks, r = rank * share + row_of;
-                if (t < tasks && r < m16) {
-                    const int chunk = (t - row_of * chunks) * 2;
-                    float4 x[kChipBlocks], y[kChipBlocks];
+                for (int u = 0; u < U; ++u) {
+                    const int t = threadIdx.x + u * kChipThreads, row_of = t / chunks;
+                    r[u] = rank * share + row_of, c[u] = (t - row_of * chunks) * 8;
+                    on[u] = row_of < share && r[u] < m16;
+                    if (on[u]) {
+                        float4 x[B], y[B];
 #pragma unroll
-                    for (int b = 0; b < kChipBlocks; ++b)
-                        if (b < blocks) {
+                        for (int b = 0; b < B; ++b) {
                             const float* other = cluster.map_shared_rank(part, b);
-                            x[b] = *reinterpret_cast<const float4*>(other + at(r, chunk));
-                            y[b] = *reinterpret_cast<const float4*>(other + at(r, chunk + 1));
+                            x[b] = *reinterpret_cast<const float4*>(other + at(r[u], c[u] / 4));
+                            y[b] = *reinterpret_cast<const float4*>(other + at(r[u], c[u] / 4 + 1));
                         }
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) v[u][q] = 0.f;
+                        for (int q = 0; q < 8; ++q) v[u][q] = 0.f;
 #pragma unroll
-                    for (int b = 0; b < kChipBlocks; ++b)
-                        if (b < blocks) {
+                        for (int b = 0; b < B; ++b) {
                             v[u][0] += x[b].x, v[u][1] += x[b].y, v[u][2] += x[b].z, v[u][3] += x[b].w;
                             v[u][4] += y[b].x, v[u][5] += y[b].y, v[u][6] += y[b].z, v[u][7] += y[b].w;
                         }
+                    }
                 }
-            }
-            cluster.sync();
+                cluster.sync();
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = threadIdx.x + u * 512;
-                const int row_of = t / chunks, r = rank * share + row_of;
-                if (t < tasks && r < m16) {
-                    const int c = (t - row_of * chunks) * 8;
-                    const Chunk w(v[u]);
+                for (int u = 0; u < U; ++u)
+                    if (on[u]) {
+                        const Chunk w(v[u]);
 #pragma unroll
-                    for (int b = 0; b < kChipBlocks; ++b)
-                        if (b < blocks) w.store(cluster.map_shared_rank(smem, b) + (c >> 6) * kPanel + in_panel(r, c & 63), p_plane);
-                }
-            }
+                        for (int b = 0; b < B; ++b)
+                            w.store(cluster.map_shared_rank(smem, b) + (c[u] >> 6) * kPanel + in_panel(r[u], c[u] & 63), p_plane);
+                    }
+            };
+            if (blocks == 2) exchange(std::integral_constant<int, 2>());
+            else if (blocks == 4) exchange(std::integral_constant<int, 4>());
+            else exchange(std::integral_constant<int, 8>());
             fence_async_all();
             cluster.sync();
         }
@@ -951,17 +962,19 @@ Sizes sizes_of(const OrthoShape& s) {
     z.p_panels = 2 * z.blocks;
     z.x_plane = size_t(z.blocks) * z.x_panels * kPanel;
     z.p_plane = size_t(z.blocks) * z.p_panels * kPanel;
-    z.fits = z.m <= 128 && z.n <= 64 * kChipPanels * kChipBlocks;
-    z.chip = z.fits && s.steps > 0;
     const int panels = up(z.n, 64) / 64;
     z.chip_blocks = 1;
     while (z.chip_blocks < kChipBlocks && panels > z.chip_blocks * kChipPanels) z.chip_blocks *= 2;
+    // Of the largest clusters the card holds some 9 at once (they do not span its groups of SMs): 16 matrices of 128 x 2000 took 176 us in
+    // two rounds, 122 us in tiles, and 8 took 90 against 148.
+    z.fits = z.m <= 128 && z.n <= 64 * kChipPanels * kChipBlocks && (z.chip_blocks < kChipBlocks || s.n_matrices <= 9);
+    z.chip = z.fits && s.steps > 0;
     z.chip_panels = (panels + z.chip_blocks - 1) / z.chip_blocks;
     return z;
 }
 
 struct Parts {
-    double* norm;
+    Squares* norm;
     char *x[2], *p, *q;
     size_t bytes;
 };
@@ -976,7 +989,7 @@ Parts parts_of(const OrthoShape& s, const Sizes& z, void* ws) {
     const size_t b = s.n_matrices;
     Parts p = {};
     // the same whatever the number of steps
-    p.norm = reinterpret_cast<double*>(take(b * kNormBlocks * 8));
+    p.norm = reinterpret_cast<Squares*>(take(b * kNormBlocks * sizeof(Squares)));
     if (!z.fits) {
         p.x[0] = take(b * 2 * z.x_plane);
         p.x[1] = take(b * 2 * z.x_plane);

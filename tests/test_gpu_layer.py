@@ -312,7 +312,7 @@ def gradient(shape, rng, few=None):
 
 
 ORTHOS = [(1, 1, 1), (2, 1, 40), (1, 40, 1), (3, 5, 7), (13, 128, 128), (2, 64, 1664), (1, 1664, 64), (4, 100, 130), (3, 129, 127), (1, 17, 3000),
-          (2, 256, 256), (1, 300, 700), (1, 700, 301), (1, 513, 640), (1, 128, 4100), (2, 127, 2049), (1, 1000, 1000), (40, 24, 16)]
+          (2, 256, 256), (1, 300, 700), (1, 700, 301), (1, 513, 640), (1, 128, 4100), (12, 40, 1800), (2, 127, 2049), (1, 1000, 1000), (40, 24, 16)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
