@@ -432,7 +432,7 @@ __device__ void join(const Sums& s, int64_t n, int64_t first, int c0, float* s_s
             sum = t;
         }
     }
-    sum += lost;
+    if (fabsf(sum) <= 3.4028235e38f) sum += lost;  // an infinity stays one: what it cut off is NaN
     if (kWays > 1) {
         __syncthreads();  // the last task's sums have been read
         s_sum[way * CHANNELS + lane] = sum;

@@ -105,6 +105,22 @@ def test_embedding_sums_are_not_lost():
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_embedding_gradient_keeps_infinities(kind):
+    """Rows whose tokens lie in one piece, a few, and many: an infinity's sum is that infinity, a NaN's and that of both signs NaN."""
+    counts = (3, 96, 1536, 9216)  # halves of them are values of every type
+    index = torch.repeat_interleave(torch.arange(4, dtype=torch.int32), torch.tensor(counts))
+    dout = torch.full((len(index), 5), 0.5)
+    for first, n in zip(np.cumsum((0,) + counts), counts):
+        dout[first + n // 2, 0] = dout[first, 3] = float("inf")
+        dout[first + n - 1, 1] = dout[first + 1, 3] = -float("inf")
+        dout[first, 2] = float("nan")
+    dtable = nan_like((4, 5), kind)
+    uvu.embed_bwd(index.cuda(), dout.to(dtable.dtype).cuda(), dtable)
+    inf = np.inf
+    np.testing.assert_array_equal(values(dtable), [[inf, -inf, np.nan, np.nan, n / 2] for n in counts])
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_embedding_views_and_padding(kind):
     """Tensors that begin off a 16-byte boundary; a batch of padding alone; NaN in rows and cotangents that nothing picks."""
     index, ix, table, tr, dout, dr = embed_case((500, 40, 64, 1, 0), kind)
