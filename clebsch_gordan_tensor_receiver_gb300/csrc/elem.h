@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace uvu {
 
@@ -69,39 +70,43 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
 // was bound by its 39 instructions a value (forward in bf16).
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Pack {
-    T t[V];
+    static constexpr bool kPairs = sizeof(T) == 2 && V % 2 == 0;  // held as words: as 16-bit values they would be loaded one by one
+    static constexpr int kEach = kPairs ? 2 : 1;
+    using Held = std::conditional_t<kPairs, uint32_t, T>;
+    Held t[V / kEach];
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int i = 0; i < V; ++i) t[i] = T(0.f);
+        for (int i = 0; i < V / kEach; ++i) t[i] = Held(0.f);
+    }
+    // Value i (known when compiled) of a pack that has been cleared, or all of whose others are there.
+    __device__ __forceinline__ void put(int i, T v) {
+        if constexpr (kPairs) {
+            uint16_t bits;
+            __builtin_memcpy(&bits, &v, 2);
+            t[i / 2] = __byte_perm(t[i / 2], bits, i % 2 ? 0x5410 : 0x3254);
+        } else {
+            t[i] = v;
+        }
     }
     __device__ __forceinline__ void get(float* v) const {
-        if constexpr (sizeof(T) == 4 || V == 1) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = widen(t[i]);
-        } else {
-            uint32_t w[(V + 1) / 2];
-            __builtin_memcpy(w, t, sizeof(w));
-#pragma unroll
-            for (int i = 0; i < (V + 1) / 2; ++i) {
-                if constexpr (__is_same(T, __nv_bfloat16)) {
-                    v[2 * i] = __uint_as_float(w[i] << 16);
-                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-                } else {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                    v[2 * i] = f.x, v[2 * i + 1] = f.y;
-                }
+        for (int i = 0; i < V / kEach; ++i) {
+            if constexpr (!kPairs) {
+                v[i] = widen(t[i]);
+            } else if constexpr (__is_same(T, __nv_bfloat16)) {
+                v[2 * i] = __uint_as_float(t[i] << 16);
+                v[2 * i + 1] = __uint_as_float(t[i] & 0xFFFF0000u);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&t[i]));
+                v[2 * i] = f.x, v[2 * i + 1] = f.y;
             }
         }
     }
     __device__ __forceinline__ void set(const float* v) {
-        if constexpr (sizeof(T) == 4 || V == 1) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) t[i] = narrow<T>(v[i]);
-        } else {
-            uint32_t w[(V + 1) / 2];
-#pragma unroll
-            for (int i = 0; i < (V + 1) / 2; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
-            __builtin_memcpy(t, w, sizeof(w));
+        for (int i = 0; i < V / kEach; ++i) {
+            if constexpr (kPairs) t[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+            else t[i] = narrow<T>(v[i]);
         }
     }
 };

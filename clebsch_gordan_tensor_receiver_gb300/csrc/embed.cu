@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(int64_t tokens, uint32_t
                 } else {
 #pragma unroll
                     for (int i = 0; i < V; ++i)
-                        if (hits >> i & 1) o[k].t[i] = *p++;
+                        if (hits >> i & 1) o[k].put(i, *p++);
                 }
             }
         }
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(int64_t tokens, uint32_t
             if (!PLAIN)
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (!(hits >> i & 1)) o[k].t[i] = T(0.f);
+                    if (!(hits >> i & 1)) o[k].put(i, T(0.f));
             if (t < tokens) *reinterpret_cast<Pack<T, V>*>(out + t * width + int64_t(c) * V) = o[k];
         }
     }
