@@ -29,6 +29,8 @@ namespace uvu {
 namespace {
 
 enum RmsMode { kRmsFwd, kRmsQuant, kRmsQuantAny, kRmsBwd };  // Any: groups that lanes do not share evenly
+// How a row ends: kCut, inside a step or where one ends; kFull, where the steps end; kOdd, 16-bit rows of odd length, see RmsRow
+enum RmsEnd { kCut, kFull, kOdd };
 
 constexpr int kTeamRows = 512;      // rows that a team adds up in one fp32 sum of d_gamma
 constexpr int kValues = 16;         // of a thread, at most
@@ -67,19 +69,26 @@ struct RmsArgs {
 
 // ------------------------------------------------------------------------------------ one row
 
-// V consecutive columns a thread and step, K steps; WARP: the team is a power of two of lanes, else the block; FULL: the steps end
-// with the row.
-template <typename T, int V, int K, bool WARP, bool FULL, RmsMode MODE>
+// V consecutive columns a thread and step, K steps; WARP: the team is a power of two of lanes, else the block.
+//
+// kOdd: every other row begins between two words.  A team's rows are an even number apart, so they all do or all do not: its words are
+// those of columns 0, 1, .. or 1, 2, .., and the single column left, the last one or the first, is the first lane's.
+template <typename T, int V, int K, bool WARP, RmsEnd END, RmsMode MODE>
 struct RmsRow {
-    float gamma[K * V];
-    float acc[MODE == kRmsBwd ? K * V : 1];
-    int lane, team, width;
+    static constexpr int kLone = END == kOdd ? 1 : 0, kN = K * V;  // the single column's value stands behind the others
+    float gamma[kN + kLone];
+    float acc[MODE == kRmsBwd ? kN + kLone : 1];
+    int lane, team, width, from, lone;
+    bool has_lone;
     float inv, eps;
 
-    __device__ __forceinline__ RmsRow(const RmsArgs& a) {
+    __device__ __forceinline__ RmsRow(const RmsArgs& a, int64_t row) {
         team = WARP ? a.team : int(blockDim.x);
         lane = WARP ? int(threadIdx.x) & (team - 1) : int(threadIdx.x);
         width = a.width;
+        from = END == kOdd ? int(row & 1) : 0;
+        lone = from ? 0 : width - 1;
+        has_lone = END == kOdd && lane == 0;
         inv = 1.f / float(width);
         eps = a.eps;
 #pragma unroll
@@ -87,12 +96,16 @@ struct RmsRow {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int e = column(k) + i;
-                gamma[k * V + i] = e < width ? a.gamma[e / a.inner] : 0.f;
+                gamma[k * V + i] = inside(k) && e < width ? a.gamma[e / a.inner] : 0.f;
                 if (MODE == kRmsBwd) acc[k * V + i] = 0.f;
             }
+        if constexpr (END == kOdd) {
+            gamma[kN] = has_lone ? a.gamma[lone / a.inner] : 0.f;
+            if (MODE == kRmsBwd) acc[kN] = 0.f;
+        }
     }
-    __device__ __forceinline__ int column(int k) const { return (k * team + lane) * V; }
-    __device__ __forceinline__ bool inside(int k) const { return FULL || column(k) < width; }
+    __device__ __forceinline__ int column(int k) const { return from + (k * team + lane) * V; }
+    __device__ __forceinline__ bool inside(int k) const { return END == kFull || (k * team + lane) * V < width - kLone; }
 
     // Over the team, in all of its threads.  s_part: another half from row to row, so that the last sum has been read.
     __device__ __forceinline__ float sum(float v, float* s_part) const {
@@ -137,6 +150,7 @@ struct RmsRow {
     }
     struct Read {
         Pack<T, V> t[kIn][K];
+        Pack<T, 1> lone[kIn];  // kOdd
         float r;
     };
     // From shared memory (places a.slot bytes apart), or from the tensors.
@@ -151,45 +165,56 @@ struct RmsRow {
                 if (there && inside(k)) in.t[j][k] = *reinterpret_cast<const Pack<T, V>*>(p + column(k));
                 else in.t[j][k].clear();
             }
+            if constexpr (END == kOdd) {
+                if (there && has_lone) in.lone[j] = *reinterpret_cast<const Pack<T, 1>*>(p + lone);
+                else in.lone[j].clear();
+            }
         }
     }
 
     // The values of h in v and its 1 / sqrt(mean h^2 + eps); h is written where there is a residual.
-    __device__ __forceinline__ float load(const Read& in, bool res, T* h, bool live, float* s_part, float (&v)[K * V]) const {
+    template <int W>
+    __device__ __forceinline__ static void add(const Pack<T, W>& x, const Pack<T, W>& r, bool res, T* h, bool write, float* v, float& s) {
+        x.get(v);
+        if (res) {
+            float u[W];
+            r.get(u);
+#pragma unroll
+            for (int i = 0; i < W; ++i) u[i] += v[i];
+            Pack<T, W> o;
+            o.set(u);
+            o.get(v);
+            if (write) *reinterpret_cast<Pack<T, W>*>(h) = o;
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) s = fmaf(v[i], v[i], s);
+    }
+    __device__ __forceinline__ float load(const Read& in, bool res, T* h, bool live, float* s_part, float (&v)[kN + kLone]) const {
         float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            in.t[0][k].get(v + k * V);
-            if (res) {
-                float u[V];
-                in.t[1][k].get(u);
-#pragma unroll
-                for (int i = 0; i < V; ++i) u[i] += v[k * V + i];
-                Pack<T, V> o;
-                o.set(u);
-                o.get(v + k * V);
-                if (live && inside(k)) *reinterpret_cast<Pack<T, V>*>(h + column(k)) = o;
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) s = fmaf(v[k * V + i], v[k * V + i], s);
-        }
+        for (int k = 0; k < K; ++k) add(in.t[0][k], in.t[1][k], res, h + column(k), live && inside(k), v + k * V, s);
+        if constexpr (END == kOdd) add(in.lone[0], in.lone[1], res, h + lone, live && has_lone, v + kN, s);
         return rsqrtf(fmaf(sum(s, s_part), inv, eps));
     }
 
+    template <int W>
+    __device__ __forceinline__ static void scale(const float* v, const float* gamma, float r, T* y) {
+        float u[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) u[i] = v[i] * r * gamma[i];
+        Pack<T, W> o;
+        o.set(u);
+        *reinterpret_cast<Pack<T, W>*>(y) = o;
+    }
     __device__ __forceinline__ void forward(const Read& in, bool res, T* y, T* h, float* rstd, bool live, float* s_part) const {
-        float v[K * V];
+        float v[kN + kLone];
         const float r = load(in, res, h, live, s_part, v);
         if (live && lane == 0 && rstd) *rstd = r;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (live && inside(k)) {
-                float u[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) u[i] = v[k * V + i] * r * gamma[k * V + i];
-                Pack<T, V> o;
-                o.set(u);
-                *reinterpret_cast<Pack<T, V>*>(y + column(k)) = o;
-            }
+            if (live && inside(k)) scale<V>(v + k * V, gamma + k * V, r, y + column(k));
+        if constexpr (END == kOdd)
+            if (live && has_lone) scale<1>(v + kN, gamma + kN, r, y + lone);
     }
 
     // One scale and what the values are multiplied with; `top`: the group's largest |y|.
@@ -210,9 +235,10 @@ struct RmsRow {
     // s_top (kRmsQuantAny): a word for each group of the row.
     __device__ __forceinline__ void quantise(const Read& in, bool res, uint8_t* q, T* h, float* scales, int group, int groups, bool live,
                                              float* s_part, unsigned* s_top) const {
-        float v[K * V];
+        float v[kN + kLone];
         const float r = load(in, res, h, live, s_part, v);
         float top[K];
+        if constexpr (END == kOdd) v[kN] *= r * gamma[kN];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             top[k] = 0.f;
@@ -226,7 +252,7 @@ struct RmsRow {
             sync();  // the last row's have been read
             for (int j = lane; j < groups; j += team) s_top[j] = 0u;
             sync();
-            const bool by_warp = team >= 32 && group % (32 * V) == 0;  // the lanes of a step share a group
+            const bool by_warp = END != kOdd && team >= 32 && group % (32 * V) == 0;  // the lanes of a step share a group
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int c = column(k), g = c / group;
@@ -242,6 +268,8 @@ struct RmsRow {
                     }
                 }
             }
+            if constexpr (END == kOdd)
+                if (live && has_lone) atomicMax(s_top + lone / group, __float_as_uint(fabsf(v[kN])));
             sync();
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -262,6 +290,8 @@ struct RmsRow {
                 o.set(u);
                 *reinterpret_cast<Bytes<V>*>(q + c) = o;
             }
+            if constexpr (END == kOdd)
+                if (live && has_lone) give_lone(__uint_as_float(s_top[lone / group]), v + kN, q);
             for (int j = lane; j < groups; j += team)
                 if (live) scales[j] = scale_of(__uint_as_float(s_top[j]));
         } else {
@@ -273,6 +303,7 @@ struct RmsRow {
                 float t = top[0];
 #pragma unroll
                 for (int k = 1; k < K; ++k) t = nan_max(t, top[k]);
+                if constexpr (END == kOdd) t = nan_max(t, fabsf(v[kN]));
                 for (int d = min(team, 32) >> 1; d > 0; d >>= 1) t = nan_max(t, __shfl_xor_sync(0xffffffffu, t, d));
                 if (!WARP) {
                     float* s_max = s_part + 32;
@@ -302,12 +333,21 @@ struct RmsRow {
                 if (!live || !inside(k)) continue;
                 float u[V];
                 scaled(top[k], v + k * V, u);
-                if (whole ? c == 0 : (c & (group - 1)) == 0) scales[whole ? 0 : c >> bits] = scale_of(top[k]);
+                if (whole ? k == 0 && lane == 0 : (c & (group - 1)) == 0) scales[whole ? 0 : c >> bits] = scale_of(top[k]);
                 Bytes<V> o;
                 o.set(u);
                 *reinterpret_cast<Bytes<V>*>(q + c) = o;
             }
+            if constexpr (END == kOdd)  // one group: others are kRmsQuantAny's
+                if (live && has_lone) give_lone(top[0], v + kN, q);
         }
+    }
+    __device__ __forceinline__ void give_lone(float top, const float* v, uint8_t* q) const {
+        float u[1];
+        scaled(top, v, u);
+        Bytes<1> o;
+        o.set(u);
+        q[lone] = o.b[0];
     }
 
     // A NaN is kept.
@@ -317,38 +357,46 @@ struct RmsRow {
         return c;
     }
 
+    // d_gamma += d_y u, and the sum of gamma d_y u
+    template <int W>
+    __device__ __forceinline__ static void gather(const Pack<T, W>& xv, const Pack<T, W>& gv, const float* gamma, float r, float* acc, float& dot) {
+        float x[W], g[W];
+        xv.get(x);
+        gv.get(g);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const float u = x[i] * r;
+            acc[i] = fmaf(g[i], u, acc[i]);
+            dot = fmaf(g[i] * gamma[i], u, dot);
+        }
+    }
+    template <int W>
+    __device__ __forceinline__ static void give(const Pack<T, W>& xv, const Pack<T, W>& gv, const Pack<T, W>& hv, const float* gamma, float r,
+                                                float rd, T* dx) {
+        float x[W], g[W], t[W];
+        xv.get(x);
+        gv.get(g);
+        hv.get(t);
+#pragma unroll
+        for (int i = 0; i < W; ++i) t[i] = fmaf(g[i] * gamma[i], r, fmaf(x[i], rd, t[i]));
+        Pack<T, W> o;
+        o.set(t);
+        *reinterpret_cast<Pack<T, W>*>(dx) = o;
+    }
     __device__ __forceinline__ void backward(const Read& in, T* dx, bool live, float* s_part) {
         const float r = in.r;
-        const Pack<T, V>(&xv)[K] = in.t[0], (&gv)[K] = in.t[1], (&hv)[K] = in.t[MODE == kRmsBwd ? 2 : 0];
-        // d_gamma += d_y u, mean(t u) = r mean(gamma d_y h)
+        constexpr int kDh = MODE == kRmsBwd ? 2 : 0;
         float dot = 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float x[V], g[V];
-            xv[k].get(x);
-            gv[k].get(g);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float u = x[i] * r;
-                acc[k * V + i] = fmaf(g[i], u, acc[k * V + i]);
-                dot = fmaf(g[i] * gamma[k * V + i], u, dot);
-            }
-        }
-        dot = sum(dot, s_part) * inv;
+        for (int k = 0; k < K; ++k) gather(in.t[0][k], in.t[1][k], gamma + k * V, r, acc + k * V, dot);
+        if constexpr (END == kOdd) gather(in.lone[0], in.lone[1], gamma + kN, r, acc + kN, dot);
+        dot = sum(dot, s_part) * inv;  // mean(t u)
         const float rd = -r * r * dot;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (live && inside(k)) {
-                float x[V], g[V], t[V];
-                xv[k].get(x);
-                gv[k].get(g);
-                hv[k].get(t);
-#pragma unroll
-                for (int i = 0; i < V; ++i) t[i] = fmaf(g[i] * gamma[k * V + i], r, fmaf(x[i], rd, t[i]));
-                Pack<T, V> o;
-                o.set(t);
-                *reinterpret_cast<Pack<T, V>*>(dx + column(k)) = o;
-            }
+            if (live && inside(k)) give(in.t[0][k], in.t[1][k], in.t[kDh][k], gamma + k * V, r, rd, dx + column(k));
+        if constexpr (END == kOdd)
+            if (live && has_lone) give(in.lone[0], in.lone[1], in.lone[kDh], gamma + kN, r, rd, dx + lone);
     }
 
     // The block's sums of d_gamma, over its teams and a channel's components in their order.  s_sum [teams][width]
@@ -359,7 +407,9 @@ struct RmsRow {
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (column(k) + i < width) s_sum[mine * width + column(k) + i] = acc[k * V + i];
+                if (inside(k) && column(k) + i < width) s_sum[mine * width + column(k) + i] = acc[k * V + i];
+        if constexpr (END == kOdd)
+            if (has_lone) s_sum[mine * width + lone] = acc[kN];
         __syncthreads();
         const int channels = width / a.inner;
         for (int c = threadIdx.x; c < channels; c += blockDim.x) {
@@ -374,21 +424,23 @@ struct RmsRow {
 
 // ----------------------------------------------------------------------------------- the kernel
 
-template <typename T, int V, int K, bool WARP, bool FULL, RmsMode MODE>
+template <typename T, int V, int K, bool WARP, RmsEnd END, RmsMode MODE>
 __global__ void __launch_bounds__(WARP ? 256 : V == 1 ? 1024 : 512) rms_kernel(const RmsArgs a) {
     __shared__ float s_part[2][64];
     // the rows' places, then the groups' maxima; at the end the sums of d_gamma
     extern __shared__ __align__(16) unsigned char smem[];
     if (MODE == kRmsBwd) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join begins as blocks end
-    using Row = RmsRow<T, V, K, WARP, FULL, MODE>;
-    Row op(a);
-    const int teams = WARP ? int(blockDim.x) / op.team : 1, mine = WARP ? int(threadIdx.x) / op.team : 0;
+    using Row = RmsRow<T, V, K, WARP, END, MODE>;
+    const int teams = WARP ? int(blockDim.x) / a.team : 1, mine = WARP ? int(threadIdx.x) / a.team : 0;
     T* out1 = static_cast<T*>(a.out[1]);
     unsigned* s_top = reinterpret_cast<unsigned*>(smem + teams * (a.ahead + 1) * a.n_in * a.slot);
-    // the gradient's rows of a block lie together, so that its sums are of rows in their order
-    const int64_t step = MODE == kRmsBwd ? teams : int64_t(gridDim.x) * teams;
-    const int64_t first = MODE == kRmsBwd ? blockIdx.x * a.block_rows : int64_t(blockIdx.x) * teams;
-    const int64_t end = MODE == kRmsBwd ? min(first + a.block_rows, a.rows) : a.rows;
+    // The gradient's rows of a block lie together, so that its sums are of rows in their order; not those of whole blocks and odd length,
+    // whose rows would not be an even number apart.
+    constexpr bool kTogether = MODE == kRmsBwd && (WARP || END != kOdd);
+    const int64_t step = kTogether ? teams : int64_t(gridDim.x) * teams;
+    const int64_t first = kTogether ? blockIdx.x * a.block_rows : int64_t(blockIdx.x) * teams;
+    const int64_t end = kTogether ? min(first + a.block_rows, a.rows) : a.rows;
+    Row op(a, first + mine);
     typename Row::Read now;
     const int64_t stride = step * a.width;  // values between a team's rows
     int half = 0;
@@ -455,16 +507,17 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 1 ? 1024 : 512) rms_kernel(c
 // ---------------------------------------------------------------------------------------- host
 
 struct RmsPlan {
-    bool warp;
+    bool warp, odd;
     int v, k, team, threads;
 };
-// Vectors of 16 bytes where every row begins on one, else of 4 bytes (two 16-bit values) or single values.  Teams as small as their
+// Vectors of 16 bytes where every row begins on one, else of 4 bytes (two 16-bit values; of an odd number all but one) or single values.  Teams as small as their
 // threads' 16 values allow, so that a warp has several narrow rows at work, but so many threads that there is work for every SM.
 inline RmsPlan rms_plan(int64_t rows, int width, int size, uintptr_t any, int sms) {
     RmsPlan p;
     const uintptr_t row = uintptr_t(width) * size | any;
-    p.v = row % 16 == 0 ? 16 / size : row % 4 == 0 ? 4 / size : 1;
-    const int vecs = (width + p.v - 1) / p.v, most = kValues / p.v;
+    p.odd = size == 2 && width % 2 == 1 && width > 1 && any % 4 == 0;
+    p.v = row % 16 == 0 ? 16 / size : p.odd || row % 4 == 0 ? 4 / size : 1;
+    const int vecs = p.odd ? width / 2 : (width + p.v - 1) / p.v, most = kValues / p.v;
     p.warp = vecs <= 32 * most;
     p.k = most;
     if (p.warp) {
@@ -501,7 +554,7 @@ cudaError_t by_plan(const RmsPlan& p, F f) {
 inline int bwd_resident_most(const RmsPlan& p) { return std::max(8, 1024 / p.threads); }
 inline int64_t bwd_blocks_most(const RmsPlan& p, int64_t rows, int sms) {
     const int64_t teams = p.threads / p.team;
-    return std::min((rows + teams - 1) / teams, std::max(int64_t(sms) * bwd_resident_most(p), (rows + kTeamRows * teams - 1) / (kTeamRows * teams)));
+    return std::min((rows + teams - 1) / teams, 1 + std::max(int64_t(sms) * bwd_resident_most(p), (rows + kTeamRows * teams - 1) / (kTeamRows * teams)));
 }
 
 template <typename T, RmsMode MODE>
@@ -513,7 +566,7 @@ cudaError_t rms_launch(RmsArgs a, int sms, cudaStream_t st, int64_t* partials) {
     const RmsPlan p = rms_plan(a.rows, a.width, sizeof(T), any, sms);
     if constexpr (MODE == kRmsQuant) {
         const int lanes = a.group / p.v;
-        const bool even = a.group % p.v == 0 && (a.group & (a.group - 1)) == 0;
+        const bool even = !p.odd && a.group % p.v == 0 && (a.group & (a.group - 1)) == 0;
         if (a.group < a.width && !(even && (lanes <= std::min(p.team, 32) || (p.warp && p.team == 32))))
             return rms_launch<T, kRmsQuantAny>(a, sms, st, partials);
     }
@@ -525,17 +578,19 @@ cudaError_t rms_launch(RmsArgs a, int sms, cudaStream_t st, int64_t* partials) {
     return by_plan<T>(p, [&](auto v, auto k, auto warp) {
         constexpr int V = decltype(v)::value, K = decltype(k)::value;
         constexpr bool W = decltype(warp)::value;
-        auto kernel = rms_kernel<T, V, K, W, false, MODE>;
+        auto kernel = rms_kernel<T, V, K, W, kCut, MODE>;
         const bool full = V * sizeof(T) == 16 && p.team * p.k * p.v == a.width;
         if constexpr (V * sizeof(T) == 16)
-            if (full) kernel = rms_kernel<T, V, K, W, true, MODE>;
-        static std::atomic<int> known[2];  // registers of a thread: the same on every device
-        int regs = known[full].load(std::memory_order_relaxed);
+            if (full) kernel = rms_kernel<T, V, K, W, kFull, MODE>;
+        if constexpr (V == 2 && sizeof(T) == 2)
+            if (p.odd) kernel = rms_kernel<T, V, K, W, kOdd, MODE>;
+        static std::atomic<int> known[2];  // registers of a thread, of the other end than kCut too: the same on every device
+        int regs = known[full || p.odd].load(std::memory_order_relaxed);
         if (regs == 0) {
             cudaFuncAttributes f;
             cudaError_t e = cudaFuncGetAttributes(&f, kernel);
             if (e != cudaSuccess) return e;
-            known[full].store(regs = std::max(1, f.numRegs), std::memory_order_relaxed);
+            known[full || p.odd].store(regs = std::max(1, f.numRegs), std::memory_order_relaxed);
         }
         auto smem_of = [&](int ahead) {
             const size_t b = one * (ahead + 1) + (MODE == kRmsQuantAny ? size_t(teams) * a.groups * 4 : 0);
@@ -552,8 +607,10 @@ cudaError_t rms_launch(RmsArgs a, int sms, cudaStream_t st, int64_t* partials) {
             if (e != cudaSuccess) return e;
         }
         int64_t blocks = std::min<int64_t>((a.rows + teams - 1) / teams, int64_t(sms) * resident(smem));
-        if (MODE == kRmsBwd) {
-            blocks = std::max(blocks, (a.rows + kTeamRows * teams - 1) / (kTeamRows * teams));
+        if (MODE == kRmsBwd) blocks = std::max(blocks, (a.rows + kTeamRows * teams - 1) / (kTeamRows * teams));
+        if (p.odd && !p.warp) {
+            if (blocks < a.rows) blocks += blocks & 1;  // a block's rows are so many apart
+        } else if (MODE == kRmsBwd) {
             a.block_rows = ((a.rows + blocks - 1) / blocks + teams - 1) / teams * teams;
             blocks = (a.rows + a.block_rows - 1) / a.block_rows;
         }

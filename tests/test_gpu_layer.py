@@ -242,6 +242,38 @@ def test_rms_norm_views_and_in_place(kind, width):
     assert torch.equal(xi, want_h) and torch.equal(ri, want_y) and torch.equal(di, want_dx)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("case", [(1, 3, 1), (2, 3, 1), (3, 521, 1), (4001, 521, 1), (2003, 1021, 1), (1001, 333, 3), (70001, 5, 1), (6001, 427, 1)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_rms_norm_odd_rows(case, kind):
+    """Rows of odd length, whose words begin a value off in every other one: values and gradients, nothing written before, between
+    or behind them, results over operands, and the same bits again."""
+    (x, res, dy, dh, gamma), (xr, rr, dyr, dhr, gr) = norm_case(case, kind)
+    n, count = case[0], x.numel()
+
+    def framed(t=None):
+        f = nan_like((count + 16,), kind)
+        if t is not None:
+            f[8:-8] = t.flatten()
+        return f, f[8:-8].view(case)
+
+    (fy, y), (fh, h), (fx, dx), rstd, dg = framed(), framed(), framed(), nan_like((n,)), nan_like(case[1:2])
+    uvu.rms_norm_fwd(x, gamma, y, rstd, residual=res, h=h)
+    uvu.rms_norm_bwd(dy, h, gamma, rstd, dx, dg, dh=dh)
+    hr = values(h)
+    within(h, xr + rr, UNIT[kind] * np.abs(xr + rr) + TINY[kind], "h")
+    near(y, layer.rms_norm(hr, gr, 1e-5)[0], kind, "y")
+    rdx, rdg = layer.rms_norm_vjp(hr, gr, 1e-5, dyr, dhr)
+    near_dx(dx, rdx, hr, gr, dyr, dhr, kind)
+    near(dg, rdg, "f32", "dgamma")
+    for f in (fy, fh, fx):
+        assert torch.isnan(f[:8]).all() and torch.isnan(f[-8:]).all()
+    (_, xi), (_, ri), (_, di), dg2 = framed(x), framed(res), framed(dy), nan_like(case[1:2])
+    uvu.rms_norm_fwd(xi, gamma, ri, rstd, residual=ri, h=xi)
+    uvu.rms_norm_bwd(di, xi, gamma, rstd, di, dg2, dh=dh)
+    assert torch.equal(xi, h) and torch.equal(ri, y) and torch.equal(di, dx) and torch.equal(dg2, dg)
+
+
 def test_rms_norm_rows_apart():
     """A row of NaN, of an infinity and of zeros leaves the others as they are; a sum over many equal rows keeps its bits."""
     x = torch.randn(9, 48, device="cuda")
@@ -276,7 +308,7 @@ def test_rms_norm_of_no_rows_and_repeats():
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("group", [0, 1, 32, 40, 64, 128])
-@pytest.mark.parametrize("case", [(1, 1, 1), (100, 16, 4), (9, 1000, 1), (5, 129, 1), (33, 128, 9), (3, 8192, 1), (7, 1100, 1), (301, 256, 1), (20001, 256, 1), (3000, 301, 1)],
+@pytest.mark.parametrize("case", [(1, 1, 1), (100, 16, 4), (9, 1000, 1), (5, 129, 1), (33, 128, 9), (3, 8192, 1), (7, 1100, 1), (301, 256, 1), (20001, 256, 1), (3000, 301, 1), (2, 7, 1), (2001, 777, 1)],
                          ids=lambda c: "x".join(map(str, c)))
 def test_rms_norm_quant(case, group, kind):
     (x, res, _, _, gamma), (xr, rr, _, _, gr) = norm_case(case, kind)
