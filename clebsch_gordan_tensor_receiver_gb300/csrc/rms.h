@@ -174,7 +174,7 @@ struct RmsRow {
 
     // The values of h in v and its 1 / sqrt(mean h^2 + eps); h is written where there is a residual.
     template <int W>
-    __device__ __forceinline__ static void add(const Pack<T, W>& x, const Pack<T, W>& r, bool res, T* h, bool write, float* v, float& s) {
+    __device__ __forceinline__ static void add(const Pack<T, W>& x, const Pack<T, W>& r, bool res, T* h, int column, bool write, float* v, float& s) {
         x.get(v);
         if (res) {
             float u[W];
@@ -184,7 +184,7 @@ struct RmsRow {
             Pack<T, W> o;
             o.set(u);
             o.get(v);
-            if (write) *reinterpret_cast<Pack<T, W>*>(h) = o;
+            if (write) *reinterpret_cast<Pack<T, W>*>(h + column) = o;
         }
 #pragma unroll
         for (int i = 0; i < W; ++i) s = fmaf(v[i], v[i], s);
@@ -192,8 +192,8 @@ struct RmsRow {
     __device__ __forceinline__ float load(const Read& in, bool res, T* h, bool live, float* s_part, float (&v)[kN + kLone]) const {
         float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) add(in.t[0][k], in.t[1][k], res, h + column(k), live && inside(k), v + k * V, s);
-        if constexpr (END == kOdd) add(in.lone[0], in.lone[1], res, h + lone, live && has_lone, v + kN, s);
+        for (int k = 0; k < K; ++k) add(in.t[0][k], in.t[1][k], res, h, column(k), live && inside(k), v + k * V, s);
+        if constexpr (END == kOdd) add(in.lone[0], in.lone[1], res, h, lone, live && has_lone, v + kN, s);
         return rsqrtf(fmaf(sum(s, s_part), inv, eps));
     }
 
