@@ -68,9 +68,10 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
 
 // V consecutive values as they lie in memory, taken apart and put together two at a time: with one conversion a value the RMS norm
 // was bound by its 39 instructions a value (forward in bf16).
-template <typename T, int V>
+// WORDS: 16-bit values are held as words.  As values they are loaded and cleared one by one where a condition stands before the load.
+template <typename T, int V, bool WORDS = true>
 struct alignas(V * sizeof(T)) Pack {
-    static constexpr bool kPairs = sizeof(T) == 2 && V % 2 == 0;  // held as words: as 16-bit values they would be loaded one by one
+    static constexpr bool kPairs = WORDS && sizeof(T) == 2 && V % 2 == 0;
     static constexpr int kEach = kPairs ? 2 : 1;
     using Held = std::conditional_t<kPairs, uint32_t, T>;
     Held t[V / kEach];
@@ -89,24 +90,33 @@ struct alignas(V * sizeof(T)) Pack {
         }
     }
     __device__ __forceinline__ void get(float* v) const {
+        if constexpr (sizeof(T) == 4 || V == 1) {
 #pragma unroll
-        for (int i = 0; i < V / kEach; ++i) {
-            if constexpr (!kPairs) {
-                v[i] = widen(t[i]);
-            } else if constexpr (__is_same(T, __nv_bfloat16)) {
-                v[2 * i] = __uint_as_float(t[i] << 16);
-                v[2 * i + 1] = __uint_as_float(t[i] & 0xFFFF0000u);
-            } else {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&t[i]));
-                v[2 * i] = f.x, v[2 * i + 1] = f.y;
+            for (int i = 0; i < V; ++i) v[i] = widen(t[i]);
+        } else {
+            uint32_t w[(V + 1) / 2];
+            __builtin_memcpy(w, t, sizeof(w));
+#pragma unroll
+            for (int i = 0; i < (V + 1) / 2; ++i) {
+                if constexpr (__is_same(T, __nv_bfloat16)) {
+                    v[2 * i] = __uint_as_float(w[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                    v[2 * i] = f.x, v[2 * i + 1] = f.y;
+                }
             }
         }
     }
     __device__ __forceinline__ void set(const float* v) {
+        if constexpr (sizeof(T) == 4 || V == 1) {
 #pragma unroll
-        for (int i = 0; i < V / kEach; ++i) {
-            if constexpr (kPairs) t[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
-            else t[i] = narrow<T>(v[i]);
+            for (int i = 0; i < V; ++i) t[i] = narrow<T>(v[i]);
+        } else {
+            uint32_t w[(V + 1) / 2];
+#pragma unroll
+            for (int i = 0; i < (V + 1) / 2; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+            __builtin_memcpy(t, w, sizeof(w));
         }
     }
 };
