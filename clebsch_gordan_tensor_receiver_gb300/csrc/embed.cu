@@ -12,8 +12,8 @@
 // so that a row's tokens are added in their order), cuts the sorted tokens into pieces of equal length, however the rows lie,
 // and sums each piece in fp32 registers, 8 rows of d_out on their way at a time.  A row whose tokens lie in one piece is
 // written by it; one that goes on behind its piece is noted, and added up from the pieces' sums in the pieces' order.  Rows without a token
-// are zeros: the table is zeroed by blocks of the first kernel that the sort leaves idle.  300,007 x 512 of f16 into 119 rows: 87 us, 21 of
-// them the sort; 8192 tokens of a 65,536 x 1024 table in bf16: 63 us, 34 of them the sort in one block, beside which the table is zeroed.
+// are zeros: the table is zeroed by blocks of the first kernel that the sort leaves idle.  300,007 x 512 of f16 into 119 rows: 84 us, 21 of
+// them the sort; 8192 tokens of a 65,536 x 1024 table in bf16: 55 us, 34 of them the sort in one block, beside which the table is zeroed.
 #include <algorithm>
 #include <cstdint>
 

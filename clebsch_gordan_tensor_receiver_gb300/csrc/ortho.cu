@@ -22,7 +22,7 @@
 // Two forms.  On chip, for m <= 128 and n <= 2048: a block, or a cluster of up to 8 that splits the columns, keeps X and P in shared
 // memory from the first step to the last; one launch.  Else a kernel for each product, of tiles of 128 rows and 256, 128 or 64 columns.
 //
-// What bounds it.  Large matrices: the tensor cores (two of 4096 x 2048 in fp32: 1.37 to 1.42 ms, 1.33 PFLOP/s of fp16 products with a step
+// What bounds it.  Large matrices: the tensor cores (two of 4096 x 2048 in fp32: 1.27 to 1.42 ms, 1.42 to 1.27 PFLOP/s of fp16 products with a step
 // of 250 us at first and 290 us when the card's power limit has lowered its clocks).  Small ones: the chain of three products a step, each of
 // which waits for the last one's planes: some 2000 cycles of products of 128 x 128 x 128 and 2300 of writing planes on chip (13 of
 // 128 x 128: 40 us; one of 64 x 1664 over a cluster of 8: 56 us), 9000 to 14,000 with loads and a launch otherwise (25 of 256 x 256 in bf16:

@@ -12,7 +12,7 @@
 // asynchronous copies that cost no registers: with one row ahead in registers the gradient had 48 KB in flight on an SM and ran at half of
 // the memory's rate.  Rows that do not begin on 16 bytes are read in words, one row ahead in registers (copied in whole chunks, with
 // what lies before and behind them, they took twice the time), also where every other one begins inside a word.  262,144 x 512 in bf16 with
-// the residual: 180 us forward (6.0 TB/s) and 166 us back (6.5 TB/s); 65,537 x 1024 to 8 bits 87 us (5.4 TB/s); 96,064 x 427 in f16: 63 us
+// the residual: 335 us forward and back (6.4 TB/s); 65,537 x 1024 to 8 bits 87 us (5.4 TB/s); 96,064 x 427 in f16: 63 us
 // (5.2 TB/s), 89 us (3.7 TB/s) and 91 us.  A thread has the same columns of every row that it sees, so gamma is read once, and d_gamma is
 // summed in registers, then over the block's teams in shared memory, and over the blocks, in their order, by a second kernel.
 #pragma once
