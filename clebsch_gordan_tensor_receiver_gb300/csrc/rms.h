@@ -12,7 +12,7 @@
 // asynchronous copies that cost no registers: with one row ahead in registers the gradient had 48 KB in flight on an SM and ran at half of
 // the memory's rate.  Rows that do not begin on 16 bytes are read in words, one row ahead in registers (copied in whole chunks, with
 // what lies before and behind them, they took twice the time), also where every other one begins inside a word.  262,144 x 512 in bf16 with
-// the residual: 335 us forward and back (6.4 TB/s); 65,537 x 1024 to 8 bits 87 us (5.4 TB/s); 96,064 x 427 in f16: 63 us
+// the residual: 335 us forward and back (6.4 TB/s); 65,537 x 1024 to 8 bits 88 us (5.4 TB/s); 96,064 x 427 in f16: 63 us
 // (5.2 TB/s), 89 us (3.7 TB/s) and 91 us.  A thread has the same columns of every row that it sees, so gamma is read once, and d_gamma is
 // summed in registers, then over the block's teams in shared memory, and over the blocks, in their order, by a second kernel.
 #pragma once
@@ -221,20 +221,41 @@ struct RmsRow {
             if (live && has_lone) scale<1>(v + kN, gamma + kN, r, y + lone);
     }
 
-    // One scale and what the values are multiplied with; `top`: the group's largest |y|.
-    __device__ __forceinline__ static float scale_of(float top) { return top * (1.f / kTop); }
-    template <int N>
-    __device__ __forceinline__ static void scaled(float top, const float* v, float (&u)[N]) {
-        if (top > 0x1p-116f && top < 0x1p120f) {
-            const float f = __fdividef(kTop, top);
-#pragma unroll
-            for (int i = 0; i < N; ++i) u[i] = v[i] * f;
-        } else {  // the inverse may be beyond fp32; zeros stay zeros, a NaN makes all NaN
-            const float s = scale_of(top);
-#pragma unroll
-            for (int i = 0; i < N; ++i) u[i] = s == 0.f ? 0.f : v[i] / s;
+    // A group's scale, s = top / 448 of its largest |y|, and its values divided by it: quotients in fp32, of which the 8 bits are formed (a
+    // product with the inverse can fall on the other side of the middle between two e4m3 values).  Zeros stay zeros, a NaN makes all NaN.
+    //
+    // Where nothing leaves fp32's range, by a quotient's last step (Markstein, "Computation of elementary functions on the IBM RISC
+    // System/6000 processor", 1990): q = v f with f = 1/s to some 2^-23, then q + (v - q s) f, whose error before it is rounded is 2^-44.
+    // As divisions: 114 us for 65,537 x 1024 from bf16.
+    struct Scale {
+        float s, f;
+        bool usual;
+        __device__ __forceinline__ explicit Scale(float top) {
+            usual = top > 0x1p-70f && top < 0x1p108f;  // a remainder that fp32 does not hold is of a value that rounds to zero
+            s = top * (1.f / kTop);
+            if (usual) s = fmaf(fmaf(-s, kTop, top), 1.f / kTop, s);
+            else s = top / kTop;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(s));
         }
-    }
+        template <int N>
+        __device__ __forceinline__ void divide(const float* v, float (&u)[N]) const {
+            if (usual) {
+#pragma unroll
+                for (int i = 0; i + 1 < N; i += 2) {
+                    const F2 w(v[i], v[i + 1]), q = w * F2(f, f);
+                    const float2 r = fma2(fma2(q, F2(-s, -s), w), F2(f, f), q).both();
+                    u[i] = r.x, u[i + 1] = r.y;
+                }
+                if constexpr (N % 2 == 1) {
+                    const float q = v[N - 1] * f;
+                    u[N - 1] = fmaf(fmaf(q, -s, v[N - 1]), f, q);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) u[i] = s == 0.f ? 0.f : v[i] / s;
+            }
+        }
+    };
 
     // s_top (kRmsQuantAny): a word for each group of the row.
     __device__ __forceinline__ void quantise(const Read& in, bool res, uint8_t* q, T* h, float* scales, int group, int groups, bool live,
@@ -242,13 +263,13 @@ struct RmsRow {
         float v[kN + kLone];
         const float r = load(in, res, h, live, s_part, v);
         float top[K];
-        if constexpr (END == kOdd) v[kN] *= r * gamma[kN];
+        if constexpr (END == kOdd) v[kN] = v[kN] * r * gamma[kN];  // in the forward's order: its y
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             top[k] = 0.f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                v[k * V + i] *= r * gamma[k * V + i];
+                v[k * V + i] = v[k * V + i] * r * gamma[k * V + i];
                 top[k] = nan_max(top[k], fabsf(v[k * V + i]));
             }
         }
@@ -281,12 +302,12 @@ struct RmsRow {
                 if (!live || !inside(k)) continue;
                 float u[V];
                 if ((c + V - 1) / group == g) {
-                    scaled(__uint_as_float(s_top[g]), v + k * V, u);
+                    Scale(__uint_as_float(s_top[g])).divide(v + k * V, u);
                 } else {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         float one[1];
-                        scaled(__uint_as_float(s_top[(c + i) / group]), v + k * V + i, one);
+                        Scale(__uint_as_float(s_top[(c + i) / group])).divide(v + k * V + i, one);
                         u[i] = one[0];
                     }
                 }
@@ -295,9 +316,9 @@ struct RmsRow {
                 *reinterpret_cast<Bytes<V>*>(q + c) = o;
             }
             if constexpr (END == kOdd)
-                if (live && has_lone) give_lone(__uint_as_float(s_top[lone / group]), v + kN, q);
+                if (live && has_lone) give_lone(Scale(__uint_as_float(s_top[lone / group])), v + kN, q);
             for (int j = lane; j < groups; j += team)
-                if (live) scales[j] = scale_of(__uint_as_float(s_top[j]));
+                if (live) scales[j] = Scale(__uint_as_float(s_top[j])).s;
         } else {
             // The largest |y| of a thread's group, for each step.  A group is the row, a power of two of a step's lanes, or a power of two
             // of a warp's whole steps.
@@ -315,8 +336,7 @@ struct RmsRow {
                     __syncthreads();
                     for (int w = 0; w < team >> 5; ++w) t = nan_max(t, s_max[w]);
                 }
-#pragma unroll
-                for (int k = 0; k < K; ++k) top[k] = t;
+                top[0] = t;
             } else {
 #pragma unroll
                 for (int k = 0; k < K; ++k)
@@ -331,24 +351,26 @@ struct RmsRow {
                         for (int k = 0; k < K; ++k) top[k] = nan_max(top[k], other[k]);
                     }
             }
+            Scale scale(top[0]);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int c = column(k);
+                if (k > 0 && !whole) scale = Scale(top[k]);
                 if (!live || !inside(k)) continue;
                 float u[V];
-                scaled(top[k], v + k * V, u);
-                if (whole ? k == 0 && lane == 0 : (c & (group - 1)) == 0) scales[whole ? 0 : c >> bits] = scale_of(top[k]);
+                scale.divide(v + k * V, u);
+                if (whole ? k == 0 && lane == 0 : (c & (group - 1)) == 0) scales[whole ? 0 : c >> bits] = scale.s;
                 Bytes<V> o;
                 o.set(u);
                 *reinterpret_cast<Bytes<V>*>(q + c) = o;
             }
             if constexpr (END == kOdd)  // one group: others are kRmsQuantAny's
-                if (live && has_lone) give_lone(top[0], v + kN, q);
+                if (live && has_lone) give_lone(scale, v + kN, q);
         }
     }
-    __device__ __forceinline__ void give_lone(float top, const float* v, uint8_t* q) const {
+    __device__ __forceinline__ void give_lone(const Scale& scale, const float* v, uint8_t* q) const {
         float u[1];
-        scaled(top, v, u);
+        scale.divide(v, u);
         Bytes<1> o;
         o.set(u);
         q[lone] = o.b[0];
