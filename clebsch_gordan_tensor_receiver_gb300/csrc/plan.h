@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <map>
 #include <memory>
@@ -185,6 +186,14 @@ cudaError_t launch_mix_fwd(const Plan& p, int64_t N, int W, const void* in, cons
                            cudaStream_t st);
 cudaError_t launch_mix_bwd(const Plan& p, int64_t N, int W, const void* in, const void* M, const void* g, void* d_in,
                            void* dM, void* ws, cudaStream_t st);
+// Leave for a kernel's dynamic shared memory of `bytes`.  The limit belongs to the kernel on the device, not to the call: all calls set the
+// same one, or a thread's smaller need, set between another thread's leave and launch, would make that launch fail.
+constexpr size_t kMostSmem = 225 << 10;  // of 227 KB; what such a kernel has beside it is less than 2 KB
+template <typename F>
+cudaError_t allow_most_smem(F* kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(std::max(bytes, kMostSmem)));
+}
+
 // Of the parts of a node-update operator's workspace.
 inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 // dropout.cu

@@ -629,7 +629,7 @@ cudaError_t rms_launch(RmsArgs a, int sms, cudaStream_t st, int64_t* partials) {
         a.ahead = smem_of(kAhead) <= kRowsSmem && a.rows >= sms * resident(smem_of(kAhead)) * teams * (kAhead + 1) ? kAhead : 1;
         const size_t smem = smem_of(a.ahead);
         if (smem > 40 << 10) {  // with what is static, 48 KB need no leave
-            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+            cudaError_t e = allow_most_smem(kernel, smem);
             if (e != cudaSuccess) return e;
         }
         int64_t blocks = std::min<int64_t>((a.rows + teams - 1) / teams, int64_t(sms) * resident(smem));
