@@ -418,7 +418,7 @@ cudaError_t fwd(const AttnArgs& a, int64_t row_tiles, cudaStream_t st) {
         constexpr int LG = decltype(lg)::value;
         constexpr bool ALIGNED = decltype(aligned)::value;
         auto k = a.hold ? attn_fwd_mma<T, NT, LG, ALIGNED, true> : attn_fwd_mma<T, NT, LG, ALIGNED, false>;
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total());
+        cudaError_t e = allow_most_smem(k, L.total());
         if (e != cudaSuccess) return e;
         k<<<dim3(unsigned(row_tiles), unsigned(a.Hkv), unsigned(a.splits)), (4 * NT + 1 + kLoadWarps) * 32, L.total(), st>>>(a, L);
         return cudaGetLastError();

@@ -468,7 +468,7 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t st) {
         constexpr bool ALIGNED = decltype(aligned)::value;
         auto k = a.hold ? attn_bwd_mma<T, LG, ALIGNED, true> : attn_bwd_mma<T, LG, ALIGNED, false>;
         const int smem = std::max(kv.total(), q.total());
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaError_t e = allow_most_smem(k, smem);
         if (e != cudaSuccess) return e;
         k<<<bwd_grid(a), kBwdWarps * 32, smem, st>>>(a, kv, q);
         return cudaGetLastError();

@@ -460,11 +460,11 @@ cudaError_t relayout_launch(int64_t N, int A, int B, bool inv, const void* in, v
     cudaError_t e;
     if (inv) {
         auto k = relayout<T, true>;
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        e = allow_most_smem(k, smem);
         if (e == cudaSuccess) k<<<grid, 256, smem, st>>>(N, A, B, TA, static_cast<const T*>(in), static_cast<T*>(out));
     } else {
         auto k = relayout<T, false>;
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        e = allow_most_smem(k, smem);
         if (e == cudaSuccess) k<<<grid, 256, smem, st>>>(N, A, B, TA, static_cast<const T*>(in), static_cast<T*>(out));
     }
     return e != cudaSuccess ? e : cudaGetLastError();

@@ -848,7 +848,7 @@ Form form_of(const NormShape& s, bool bwd, int sms) {
 
 template <typename F>
 cudaError_t allow_smem(F f, size_t bytes) {
-    return bytes <= 48 << 10 ? cudaSuccess : cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    return bytes <= 48 << 10 ? cudaSuccess : allow_most_smem(f, bytes);
 }
 
 template <typename... P, typename... Q>

@@ -153,7 +153,7 @@ template <typename T, bool W_SM>
 cudaError_t launch_t(int64_t E, const void* r, double r_cut, int p_env, const RadialNet& net, const void* W, void* h,
                      size_t smem, int sm_count, cudaStream_t st) {
     auto k = radial_hidden_kernel<T, W_SM>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    cudaError_t e = allow_most_smem(k, smem);
     int per_sm = 0;
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, kThreads, smem);
     if (e != cudaSuccess) return e;
@@ -548,7 +548,7 @@ cudaError_t launch_bwd_t(int64_t E, const void* r, double r_cut, int p_env, cons
     for (int l = 1; l <= net.n_layers; ++l)
         reg = reg && ((net.widths[l - 1] + 3) / 4) * (net.widths[l] / 4) <= kThreads;
     auto k = reg ? radial_hidden_bwd_kernel<T, TE, true> : radial_hidden_bwd_kernel<T, TE, false>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    cudaError_t e = allow_most_smem(k, smem);
     if (e != cudaSuccess) return e;
     const int n_w = weight_count(net);
     k<<<blocks, kThreads, smem, st>>>(E, static_cast<const T*>(r), T(r_cut), p_env, net, L, static_cast<const T*>(W), n_w,

@@ -574,19 +574,16 @@ cudaError_t launch_tc_gemm(TcJobs& J, cudaStream_t st) {
     const EncodeTiled enc = encoder();
     if (!enc) return cudaErrorNotSupported;
     const Layout L{J.bn, J.nraw, J.nb};
-    static int sms = 0;  // one resident CTA per SM; the attribute is per function
-    static int attr_bytes = 0;
+    static int sms = 0;  // one resident CTA per SM
     if (!sms) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return e;
     }
-    if (L.total() > attr_bytes) {
-        cudaError_t e = cudaFuncSetAttribute(tc_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total());
-        if (e != cudaSuccess) return e;
-        attr_bytes = L.total();
-    }
+    // the same for every layout, as allow_most_smem has it
+    cudaError_t e = cudaFuncSetAttribute(tc_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax - 1024);
+    if (e != cudaSuccess) return e;
     long long t = 0, extent = 0;
     for (int s = 0; s < J.nseg; ++s) {
         J.tile0[s] = int(t);
@@ -610,8 +607,7 @@ cudaError_t launch_tc_gemm(TcJobs& J, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const int ntn = (J.N + J.bn - 1) / J.bn, nk = (J.K + kBK - 1) / kBK;
     tc_pack_b<<<dim3(unsigned(J.nseg * ntn * nk), unsigned((J.bn * kBK + 1023) / 1024)), 256, 0, st>>>(J, ntn, nk);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const unsigned grid = unsigned(std::min<long long>(tiles, sms));
     // a CTA keeps one N tile in either order when the grid is a multiple of the N tiles (and then
     // the CTAs on one row tile run together, sharing its A through L2); otherwise N-major order

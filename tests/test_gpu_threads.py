@@ -96,3 +96,70 @@ def rms(rows, width, dtype, form):
                                            (((4000, 512), (9000, 512)), torch.bfloat16)], ids=["rows", "width", "bf16"])
 def test_rms_norm(monkeypatch, looped, shapes, dtype, form):
     both(monkeypatch, looped, f"uvu_rms_norm_{form}", [rms(*s, dtype, form) for s in shapes])
+
+
+# ------------------------------------------------------------------------ the operators of other files
+
+def i32(*a):
+    return torch.tensor(a, dtype=torch.int32, device="cuda")
+
+
+def space(need):
+    return torch.empty(max(16, need), dtype=torch.uint8, device="cuda")
+
+
+def norm(rows, graphs, form, channels=64, groups=4):
+    x, gamma, beta = rand(rows * graphs, channels), rand(channels), rand(channels)
+    offsets = i32(*range(0, rows * graphs + 1, rows))
+    y, mean, rstd = torch.empty_like(x), torch.empty(graphs, groups, device="cuda"), torch.empty(graphs, groups, device="cuda")
+    f, b = uvu.group_norm_workspace_bytes(x, graphs, groups, rows)
+    if form == "fwd":
+        ws = space(f)
+        return lambda s: uvu.group_norm_fwd(x, gamma, beta, offsets, groups, y, mean, rstd, max_rows=rows, workspace=ws, stream=s), [y, mean, rstd]
+    uvu.group_norm_fwd(x, gamma, beta, offsets, groups, y, mean, rstd, max_rows=rows)
+    dy, dx, dgamma, dbeta, ws = rand(*x.shape), torch.empty_like(x), torch.empty_like(gamma), torch.empty_like(beta), space(b)
+    return (lambda s: uvu.group_norm_bwd(dy, x, gamma, beta, offsets, groups, mean, rstd, dx, dgamma, dbeta, max_rows=rows, workspace=ws, stream=s),
+            [dx, dgamma, dbeta])
+
+
+@pytest.mark.parametrize("form, rows", [("fwd", (390, 410)), ("bwd", (200, 260))], ids=["fwd", "bwd"])  # 50 to 70 KB a block
+def test_group_norm(monkeypatch, looped, form, rows):
+    both(monkeypatch, looped, f"uvu_group_norm_{form}", [norm(n, 100, form) for n in rows])
+
+
+@pytest.mark.parametrize("heads", [2, 24], ids=["one", "two"])  # row tiles of a block
+def test_attention(monkeypatch, looped, heads):
+    def one(mask):
+        rows, states = 1000, 1000
+        at = uvu.Attention(heads, heads, 64, i32(0, rows), i32(0, states))
+        q, k, v = (rand(n, heads, 64, dtype=torch.bfloat16) for n in (rows, states, states))
+        keep = (torch.arange(states, device="cuda") % 3 > 0).to(torch.uint8) if mask else None
+        out, lse = torch.empty_like(q), torch.empty(rows, heads, device="cuda")
+        ws = space(at.workspace_bytes(q, k)[0])
+        return lambda s: at.fwd(q, k, v, out, lse, keep=keep, workspace=ws, stream=s), [out, lse]
+
+    both(monkeypatch, looped, "uvu_attn_fwd", [one(False), one(True)])
+
+
+def test_radial_network(monkeypatch, looped):
+    def one(widths):
+        plan = uvu.Plan("16x0e+16x1o", "1x0e+1x1o", 1)
+        weights = rand(sum(a * b for a, b in zip(widths, widths[1:]))) * 0.2
+        r, h = torch.rand(500, device="cuda") * 4 + 0.5, torch.empty(500, widths[-1], device="cuda")
+        return lambda s: plan.radial_hidden(r, 5.0, 5, widths, weights, h, stream=s), [h, plan]
+
+    made = [one([8, 32, 32]), one([8, 64, 64, 64])]
+    both(monkeypatch, looped, "uvu_radial_hidden", [(call, out[:1]) for call, out in made])
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float64"])
+def test_mixing(monkeypatch, looped, dtype):
+    def one(irreps, sh, lmax, u, w, nodes=20):
+        plan = uvu.Plan(irreps, sh, lmax, dtype)
+        t = torch.float32 if dtype == "float32" else torch.float64
+        inp, m = rand(nodes, u, plan.info.dim_out, dtype=t), rand(plan.info.n_paths, u, w, dtype=t)
+        out, ws = torch.empty(nodes, w, plan.info.dim_out, dtype=t, device="cuda"), space(plan.mix_workspace_bytes(nodes, w)[0])
+        return lambda s: plan.mix_fwd(nodes, w, inp, m, out, workspace=ws, stream=s), [out, plan]
+
+    made = [one("32x0e+32x1o", "1x0e+1x1o", 1, 32, 32), one("64x0e+64x1o+64x2e", "1x0e+1x1o+1x2e+1x3o", 3, 64, 512)]
+    both(monkeypatch, looped, "uvu_mix_fwd", [(call, out[:1]) for call, out in made])
