@@ -193,12 +193,31 @@ struct RmsRow {
 #pragma unroll
         for (int i = 0; i < W; ++i) s = fmaf(v[i], v[i], s);
     }
+    __device__ __forceinline__ static float rsqrt(float v) {  // of what is not subnormal
+        float r;
+        asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+        return r;
+    }
     __device__ __forceinline__ float load(const Read& in, bool res, T* h, bool live, float* s_part, float (&v)[kN + kLone]) const {
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) add(in.t[0][k], in.t[1][k], res, h, column(k), live && inside(k), v + k * V, s);
         if constexpr (END == kOdd) add(in.lone[0], in.lone[1], res, h, lone, live && has_lone, v + kN, s);
-        return rsqrtf(fmaf(sum(s, s_part), inv, eps));
+        const float mean = fmaf(sum(s, s_part), inv, eps);
+        float r = rsqrt(mean);
+        // Squares beyond fp32, or below it where eps does not hide them: rarely, and then once more at another scale (all lanes of a warp
+        // take part in its teams' sums).  One comparison of the bits: 2^-80 <= mean < 2^126.
+        const bool beyond = __float_as_uint(mean) - 0x17800000u >= 0x7E800000u - 0x17800000u;
+        if (__builtin_expect(WARP ? __any_sync(0xffffffffu, beyond) : beyond, 0)) {
+            const float f = mean < 1.f ? 0x1p90f : 0x1p-80f;
+            s = 0.f;
+#pragma unroll
+            for (int i = 0; i < kN + kLone; ++i) s = fmaf(v[i] * f, v[i] * f, s);
+            if (!WARP) __syncthreads();  // the first sums have been read
+            s = sum(s, s_part);
+            if (beyond) r = rsqrt(fmaf(s, inv, eps * f * f)) * f;
+        }
+        return r;
     }
 
     template <int W>
@@ -398,13 +417,13 @@ struct RmsRow {
     }
     template <int W>
     __device__ __forceinline__ static void give(const Values<W>& xv, const Values<W>& gv, const Values<W>& hv, const float* gamma, float r,
-                                                float rd, T* dx) {
+                                                float mean, T* dx) {
         float x[W], g[W], t[W];
         xv.get(x);
         gv.get(g);
         hv.get(t);
 #pragma unroll
-        for (int i = 0; i < W; ++i) t[i] = fmaf(g[i] * gamma[i], r, fmaf(x[i], rd, t[i]));
+        for (int i = 0; i < W; ++i) t[i] = fmaf(fmaf(-x[i] * r, mean, g[i] * gamma[i]), r, t[i]);  // r r may be beyond fp32
         Values<W> o;
         o.set(t);
         *reinterpret_cast<Values<W>*>(dx) = o;
@@ -416,13 +435,12 @@ struct RmsRow {
 #pragma unroll
         for (int k = 0; k < K; ++k) gather(in.t[0][k], in.t[1][k], gamma + k * V, r, acc + k * V, dot);
         if constexpr (END == kOdd) gather(in.lone[0], in.lone[1], gamma + kN, r, acc + kN, dot);
-        dot = sum(dot, s_part) * inv;  // mean(t u)
-        const float rd = -r * r * dot;
+        const float mean = sum(dot, s_part) * inv;  // of t u
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (live && inside(k)) give(in.t[0][k], in.t[1][k], in.t[kDh][k], gamma + k * V, r, rd, dx + column(k));
+            if (live && inside(k)) give(in.t[0][k], in.t[1][k], in.t[kDh][k], gamma + k * V, r, mean, dx + column(k));
         if constexpr (END == kOdd)
-            if (live && has_lone) give(in.lone[0], in.lone[1], in.lone[kDh], gamma + kN, r, rd, dx + lone);
+            if (live && has_lone) give(in.lone[0], in.lone[1], in.lone[kDh], gamma + kN, r, mean, dx + lone);
     }
 
     // The block's sums of d_gamma, over its teams and a channel's components in their order.  s_sum [teams][width]
