@@ -1327,8 +1327,9 @@ uvu_status rms_shape(uvu_dtype dtype, int64_t n_rows, int channels, int inner, d
     UVU_TRY(block_dtype(dtype));
     if (n_rows < 0 || n_rows >= std::numeric_limits<int32_t>::max())
         return fail(UVU_ERR_INVALID_ARGUMENT, "n_rows must be in [0, 2^31 - 1)");
-    if (channels < 1 || inner < 1 || channels > 8192 || inner > 8192 || channels * inner > 8192)
-        return fail(UVU_ERR_INVALID_ARGUMENT, "channels * inner must be in [1, 8192]");
+    const int64_t width = int64_t(channels) * inner;
+    if (channels < 1 || inner < 1 || width > (channels <= kRmsWideChannels ? kRmsWide : kRmsRow))
+        return fail(UVU_ERR_INVALID_ARGUMENT, "channels * inner must be in [1, 36864], of more than 4096 channels in [1, 8192]");
     if (!(eps >= 0) || !std::isfinite(float(eps))) return fail(UVU_ERR_INVALID_ARGUMENT, "eps must be a finite fp32 value >= 0");
     *s = RmsShape{dtype, n_rows, channels, inner, eps};
     return UVU_OK;

@@ -224,6 +224,16 @@ cudaError_t launch_rms_quant(const RmsShape& s, int group, const void* x, const 
                              float* scales, int sms, cudaStream_t st);
 cudaError_t launch_rms_bwd(const RmsShape& s, const void* dy, const void* h, const float* gamma, const float* rstd, const void* dh,
                            void* dx, float* dgamma, void* ws, int sms, cudaStream_t st);
+// rms_wide.cu: rows of more than kRmsRow values
+constexpr int kRmsRow = 8192, kRmsWide = 36864, kRmsWideChannels = 4096;
+inline bool rms_wide(const RmsShape& s) { return s.channels * s.inner > kRmsRow; }
+int64_t rms_wide_blocks(int64_t rows, int sms);  // whose sums of d_gamma [blocks][channels] the gradient leaves in `partial`
+cudaError_t launch_rms_wide_fwd(const RmsShape& s, const void* x, const void* residual, const float* gamma, void* h, void* y, float* rstd,
+                                int sms, cudaStream_t st);
+cudaError_t launch_rms_wide_quant(const RmsShape& s, int group, const void* x, const void* residual, const float* gamma, void* h, void* q,
+                                  float* scales, int sms, cudaStream_t st);
+cudaError_t launch_rms_wide_bwd(const RmsShape& s, const void* dy, const void* h, const float* gamma, const float* rstd, const void* dh,
+                                void* dx, float* partial, int sms, cudaStream_t st, int64_t* blocks);
 // ortho.cu
 using OrthoShape = uvu_ortho_shape;
 size_t ortho_workspace(const OrthoShape& s);

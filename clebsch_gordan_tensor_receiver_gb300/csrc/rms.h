@@ -1,4 +1,4 @@
-// What the kernels of the RMS norm share (rms_fwd.cu, rms_quant.cu, rms_bwd.cu).
+// What the kernels of the RMS norm share (rms_fwd.cu, rms_quant.cu, rms_bwd.cu; rows of more than 8192 values: rms_wide.cu).
 //
 //     h = round(x + residual),  r = (mean h^2 + eps)^(-1/2),  y = h r gamma          (a row: channels * inner values)
 //     8 bits, for each group of a row:  s = max |y| / 448,  q = e4m3(y / s)
@@ -51,6 +51,59 @@ struct alignas(V) Bytes {
 #pragma unroll
             for (int i = 0; i < (V + 1) / 2; ++i) w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
             __builtin_memcpy(b, w, sizeof(w));
+        }
+    }
+};
+
+// A NaN is kept.
+__device__ __forceinline__ float nan_max(float a, float b) {
+    float c;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+    return c;
+}
+__device__ __forceinline__ float inv_sqrt(float v) {  // of what is not subnormal
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// Of a mean of squares that eps is added to: whether squares may have left fp32, or may lie below it where eps does not hide them.  One
+// comparison of the bits: not 2^-80 <= mean < 2^126.
+__device__ __forceinline__ bool squares_beyond(float mean) { return __float_as_uint(mean) - 0x17800000u >= 0x7E800000u - 0x17800000u; }
+// The values' factor for another try.
+__device__ __forceinline__ float squares_factor(float mean) { return mean < 1.f ? 0x1p90f : 0x1p-80f; }
+
+// A group's scale, s = top / 448 of its largest |y|, and its values divided by it: quotients in fp32, of which the 8 bits are formed (a
+// product with the inverse can fall on the other side of the middle between two e4m3 values).  Zeros stay zeros, a NaN makes all NaN.
+//
+// Where nothing leaves fp32's range, by a quotient's last step (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990): q = v f with f = 1/s to some 2^-23, then q + (v - q s) f, whose error before it is rounded is 2^-44.
+// As divisions: 114 us for 65,537 x 1024 from bf16.
+struct Scale {
+    float s, f;
+    bool usual;
+    __device__ __forceinline__ explicit Scale(float top) {
+        usual = top > 0x1p-70f && top < 0x1p108f;  // a remainder that fp32 does not hold is of a value that rounds to zero
+        s = top * (1.f / kTop);
+        if (usual) s = fmaf(fmaf(-s, kTop, top), 1.f / kTop, s);
+        else s = top / kTop;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(s));
+    }
+    template <int N>
+    __device__ __forceinline__ void divide(const float* v, float (&u)[N]) const {
+        if (usual) {
+#pragma unroll
+            for (int i = 0; i + 1 < N; i += 2) {
+                const F2 w(v[i], v[i + 1]), q = w * F2(f, f);
+                const float2 r = fma2(fma2(q, F2(-s, -s), w), F2(f, f), q).both();
+                u[i] = r.x, u[i + 1] = r.y;
+            }
+            if constexpr (N % 2 == 1) {
+                const float q = v[N - 1] * f;
+                u[N - 1] = fmaf(fmaf(q, -s, v[N - 1]), f, q);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) u[i] = s == 0.f ? 0.f : v[i] / s;
         }
     }
 };
@@ -193,29 +246,23 @@ struct RmsRow {
 #pragma unroll
         for (int i = 0; i < W; ++i) s = fmaf(v[i], v[i], s);
     }
-    __device__ __forceinline__ static float rsqrt(float v) {  // of what is not subnormal
-        float r;
-        asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-        return r;
-    }
     __device__ __forceinline__ float load(const Read& in, bool res, T* h, bool live, float* s_part, float (&v)[kN + kLone]) const {
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) add(in.t[0][k], in.t[1][k], res, h, column(k), live && inside(k), v + k * V, s);
         if constexpr (END == kOdd) add(in.lone[0], in.lone[1], res, h, lone, live && has_lone, v + kN, s);
         const float mean = fmaf(sum(s, s_part), inv, eps);
-        float r = rsqrt(mean);
-        // Squares beyond fp32, or below it where eps does not hide them: rarely, and then once more at another scale (all lanes of a warp
-        // take part in its teams' sums).  One comparison of the bits: 2^-80 <= mean < 2^126.
-        const bool beyond = __float_as_uint(mean) - 0x17800000u >= 0x7E800000u - 0x17800000u;
+        float r = inv_sqrt(mean);
+        // rarely, and then once more at another scale (all lanes of a warp take part in its teams' sums)
+        const bool beyond = squares_beyond(mean);
         if (__builtin_expect(WARP ? __any_sync(0xffffffffu, beyond) : beyond, 0)) {
-            const float f = mean < 1.f ? 0x1p90f : 0x1p-80f;
+            const float f = squares_factor(mean);
             s = 0.f;
 #pragma unroll
             for (int i = 0; i < kN + kLone; ++i) s = fmaf(v[i] * f, v[i] * f, s);
             if (!WARP) __syncthreads();  // the first sums have been read
             s = sum(s, s_part);
-            if (beyond) r = rsqrt(fmaf(s, inv, eps * f * f)) * f;
+            if (beyond) r = inv_sqrt(fmaf(s, inv, eps * f * f)) * f;
         }
         return r;
     }
@@ -239,42 +286,6 @@ struct RmsRow {
         if constexpr (END == kOdd)
             if (live && has_lone) scale<1>(v + kN, gamma + kN, r, y + lone);
     }
-
-    // A group's scale, s = top / 448 of its largest |y|, and its values divided by it: quotients in fp32, of which the 8 bits are formed (a
-    // product with the inverse can fall on the other side of the middle between two e4m3 values).  Zeros stay zeros, a NaN makes all NaN.
-    //
-    // Where nothing leaves fp32's range, by a quotient's last step (Markstein, "Computation of elementary functions on the IBM RISC
-    // System/6000 processor", 1990): q = v f with f = 1/s to some 2^-23, then q + (v - q s) f, whose error before it is rounded is 2^-44.
-    // As divisions: 114 us for 65,537 x 1024 from bf16.
-    struct Scale {
-        float s, f;
-        bool usual;
-        __device__ __forceinline__ explicit Scale(float top) {
-            usual = top > 0x1p-70f && top < 0x1p108f;  // a remainder that fp32 does not hold is of a value that rounds to zero
-            s = top * (1.f / kTop);
-            if (usual) s = fmaf(fmaf(-s, kTop, top), 1.f / kTop, s);
-            else s = top / kTop;
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(s));
-        }
-        template <int N>
-        __device__ __forceinline__ void divide(const float* v, float (&u)[N]) const {
-            if (usual) {
-#pragma unroll
-                for (int i = 0; i + 1 < N; i += 2) {
-                    const F2 w(v[i], v[i + 1]), q = w * F2(f, f);
-                    const float2 r = fma2(fma2(q, F2(-s, -s), w), F2(f, f), q).both();
-                    u[i] = r.x, u[i + 1] = r.y;
-                }
-                if constexpr (N % 2 == 1) {
-                    const float q = v[N - 1] * f;
-                    u[N - 1] = fmaf(fmaf(q, -s, v[N - 1]), f, q);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) u[i] = s == 0.f ? 0.f : v[i] / s;
-            }
-        }
-    };
 
     // s_top (kRmsQuantAny): a word for each group of the row.
     __device__ __forceinline__ void quantise(const Read& in, bool res, uint8_t* q, T* h, float* scales, int group, int groups, bool live,
@@ -393,13 +404,6 @@ struct RmsRow {
         Bytes<1> o;
         o.set(u);
         q[lone] = o.b[0];
-    }
-
-    // A NaN is kept.
-    __device__ static __forceinline__ float nan_max(float a, float b) {
-        float c;
-        asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
-        return c;
     }
 
     // d_gamma += d_y u, and the sum of gamma d_y u
@@ -670,6 +674,26 @@ inline RmsArgs rms_args(const RmsShape& s) {
     a.width = s.channels * s.inner;
     a.inner = s.inner;
     a.eps = float(s.eps);
+    return a;
+}
+inline RmsArgs rms_fwd_args(const RmsShape& s, const void* x, const void* residual, const float* gamma, void* h, void* y, float* rstd) {
+    RmsArgs a = rms_args(s);
+    a.in[0] = x, a.in[1] = residual, a.gamma = gamma, a.out[0] = y, a.out[1] = h, a.rstd = rstd;
+    return a;
+}
+inline RmsArgs rms_quant_args(const RmsShape& s, int group, const void* x, const void* residual, const float* gamma, void* h, void* q,
+                              float* scales) {
+    RmsArgs a = rms_args(s);
+    a.in[0] = x, a.in[1] = residual, a.gamma = gamma, a.out[0] = q, a.out[1] = h, a.scales = scales;
+    a.group = group ? std::min(group, a.width) : a.width;
+    a.groups = (a.width + a.group - 1) / a.group;
+    return a;
+}
+inline RmsArgs rms_bwd_args(const RmsShape& s, const void* dy, const void* h, const float* gamma, const float* rstd, const void* dh, void* dx,
+                            float* partial) {
+    RmsArgs a = rms_args(s);
+    a.in[0] = h, a.in[1] = dy, a.in[2] = dh, a.out[0] = dx, a.gamma = gamma;
+    a.rstd = const_cast<float*>(rstd), a.partial = partial;
     return a;
 }
 

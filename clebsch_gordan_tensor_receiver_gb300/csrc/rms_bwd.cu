@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(1024) rms_join_kernel(const float* partial, in
 
 size_t rms_workspace(const RmsShape& s, int sms) {
     if (s.rows == 0) return 0;
+    if (rms_wide(s)) return size_t(rms_wide_blocks(s.rows, sms)) * s.channels * 4;
     // the tensors' alignment is not known here: the most blocks of any
     int64_t most = 0;
     for (uintptr_t any : {0, 4, 2, 1})
@@ -42,16 +43,18 @@ size_t rms_workspace(const RmsShape& s, int sms) {
 cudaError_t launch_rms_bwd(const RmsShape& s, const void* dy, const void* h, const float* gamma, const float* rstd, const void* dh,
                            void* dx, float* dgamma, void* ws, int sms, cudaStream_t st) {
     if (s.rows == 0) return cudaMemsetAsync(dgamma, 0, size_t(s.channels) * 4, st);
-    RmsArgs a = rms_args(s);
-    a.in[0] = h, a.in[1] = dy, a.in[2] = dh, a.out[0] = dx, a.gamma = gamma;
-    a.rstd = const_cast<float*>(rstd), a.partial = static_cast<float*>(ws);
+    const RmsArgs a = rms_bwd_args(s, dy, h, gamma, rstd, dh, dx, static_cast<float*>(ws));
     int64_t blocks = 0;
     cudaError_t e = cudaErrorInvalidValue;
-    switch (s.dtype) {
-        case UVU_F32: e = rms_launch<float, kRmsBwd>(a, sms, st, &blocks); break;
-        case UVU_BF16: e = rms_launch<__nv_bfloat16, kRmsBwd>(a, sms, st, &blocks); break;
-        case UVU_F16: e = rms_launch<__half, kRmsBwd>(a, sms, st, &blocks); break;
-        default: break;
+    if (rms_wide(s)) {
+        e = launch_rms_wide_bwd(s, dy, h, gamma, rstd, dh, dx, a.partial, sms, st, &blocks);
+    } else {
+        switch (s.dtype) {
+            case UVU_F32: e = rms_launch<float, kRmsBwd>(a, sms, st, &blocks); break;
+            case UVU_BF16: e = rms_launch<__nv_bfloat16, kRmsBwd>(a, sms, st, &blocks); break;
+            case UVU_F16: e = rms_launch<__half, kRmsBwd>(a, sms, st, &blocks); break;
+            default: break;
+        }
     }
     if (e != cudaSuccess) return e;
     // it may begin while the last blocks of the sums run, and waits for them

@@ -5,10 +5,8 @@ namespace uvu {
 
 cudaError_t launch_rms_quant(const RmsShape& s, int group, const void* x, const void* residual, const float* gamma, void* h, void* q,
                              float* scales, int sms, cudaStream_t st) {
-    RmsArgs a = rms_args(s);
-    a.in[0] = x, a.in[1] = residual, a.gamma = gamma, a.out[0] = q, a.out[1] = h, a.scales = scales;
-    a.group = group ? std::min(group, a.width) : a.width;
-    a.groups = (a.width + a.group - 1) / a.group;
+    if (rms_wide(s)) return launch_rms_wide_quant(s, group, x, residual, gamma, h, q, scales, sms, st);
+    const RmsArgs a = rms_quant_args(s, group, x, residual, gamma, h, q, scales);
     switch (s.dtype) {
         case UVU_F32: return rms_launch<float, kRmsQuant>(a, sms, st, nullptr);
         case UVU_BF16: return rms_launch<__nv_bfloat16, kRmsQuant>(a, sms, st, nullptr);

@@ -632,7 +632,8 @@ uvu_status uvu_embed_workspace(uvu_dtype dtype, int64_t n_tokens, int64_t n_rows
  * x, residual, h, y [n_rows][channels][inner] contiguous, the mean over the channels * inner values of a row, gamma
  * [channels] fp32: the components of an irrep share its channel's value, so equivariant features stay equivariant.
  * The norm is of h as it is stored.  residual and h may both be NULL (h is x then).  rstd [n_rows] fp32 is written for
- * the backward, or NULL.  channels * inner is at most 8192; eps >= 0 (0 with no row of zeros, nor one whose rstd is beyond fp32: values
+ * the backward, or NULL.  channels * inner is at most 36864 (4096 channels of 9 components), of more than 4096 channels at most 8192;
+ * eps >= 0 (0 with no row of zeros, nor one whose rstd is beyond fp32: values
  * below 3e-39).  h may be x or residual; y may be x or residual where h is another one.  The squares are summed in fp32, at a scale at
  * which they neither overflow nor vanish.
  * Launches: 1 kernel. */

@@ -6,7 +6,7 @@ import torch
 
 from clebsch_gordan_tensor_receiver_gb300 import uvu
 from oracle import layer
-from test_gpu_layer import UNIT, nan_like, norm_case, rounded, values, within
+from test_gpu_layer import KINDS, TINY, UNIT, nan_like, near, near_dx, norm_case, rounded, values, within
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,83 @@ def test_rms_norm_of_any_eps():
     ref = (values(x[:, :1])[:, 0] ** 2 + float(np.float32(3e38))) ** -0.5
     within(rstd, ref, 2.0 ** -20 * ref)  # the second is below 2^-126: 22 bits
     within(y, values(x) * ref[:, None], 2.0 ** -20 * np.abs(values(x) * ref[:, None]))
+
+
+WIDE = [(5, 1024, 9), (1, 4096, 9), (3, 2731, 3), (7, 4000, 4), (700, 1024, 9), (2, 1, 8193), (4, 1000, 12)]  # rows of more than 8192 values
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("residual", [False, True], ids=["plain", "residual"])
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: "x".join(map(str, c)))
+def test_rms_norm_wide(case, residual, kind):
+    """Values and gradients; tensors that begin off 16 bytes, and results over operands, are the same within rounding; repeats bit for bit."""
+    (x, res, dy, dh, gamma), (xr, rr, dyr, dhr, gr) = norm_case(case, kind)
+    shift = lambda t: torch.cat([t.flatten()[:1], t.flatten()])[1:].view(t.shape)  # noqa: E731
+    n = case[0]
+    runs = []
+    for move in (lambda t: t, lambda t: t.clone(), shift):
+        a, b, c, d = (move(t) for t in (x, res, dy, dh))
+        y, h, dx = (move(nan_like(case, kind)) for _ in range(3))
+        rstd, dg = nan_like((n,)), nan_like(case[1:2])
+        uvu.rms_norm_fwd(a, gamma, y, rstd, **(dict(residual=b, h=h) if residual else {}))
+        h = h if residual else a
+        uvu.rms_norm_bwd(c, h, gamma, rstd, dx, dg, dh=d if residual else None)
+        hr = values(h)
+        within(h, xr + rr if residual else xr, UNIT[kind] * np.abs(xr + rr) + TINY[kind], "h")
+        ry, rrstd = layer.rms_norm(hr, gr, 1e-5)
+        near(y, ry, kind, "y")
+        near(rstd, rrstd, "f32", "rstd")
+        rdx, rdg = layer.rms_norm_vjp(hr, gr, 1e-5, dyr, dhr if residual else None)
+        near_dx(dx, rdx, hr, gr, dyr, dhr if residual else np.zeros_like(dhr), kind)
+        near(dg, rdg, "f32", "dgamma")
+        runs.append((y, h, rstd, dx, dg))
+    assert all(torch.equal(p, q) for p, q in zip(runs[0], runs[1]))
+    if residual:  # h over x, y over the residual; dx over dy
+        xi, ri, di, dg, rstd = x.clone(), res.clone(), dy.clone(), nan_like(case[1:2]), nan_like((n,))
+        uvu.rms_norm_fwd(xi, gamma, ri, rstd, residual=ri, h=xi)
+        uvu.rms_norm_bwd(di, xi, gamma, rstd, di, dg, dh=dh)
+        assert all(torch.equal(p, q) for p, q in zip(runs[0], (ri, xi, rstd, di, dg)))
+
+
+@pytest.mark.parametrize("group", [0, 1, 40, 128, 512])
+@pytest.mark.parametrize("case", [c for c in WIDE if c[0] < 100], ids=lambda c: "x".join(map(str, c)))
+def test_rms_norm_wide_quant(case, group):
+    test_rms_norm_quant_is_the_forward_divided_and_rounded(case, group)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shifted", [False, True])
+def test_rms_norm_wide_quant_of_16_bits(shifted, kind):
+    """Bytes of rows of 8193 and 9216 values, on and off the vectors' alignment, nothing written before or behind them."""
+    for case in ((3, 2731, 3), (5, 1024, 9)):
+        (x, res, _, _, gamma), _ = norm_case(case, kind)
+        n, width = case[0], case[1] * case[2]
+        at = 33 if shifted else 32
+        flat = torch.full((n * width + 64,), 0x55, dtype=torch.uint8, device="cuda")
+        q, s, h = flat[at:at + n * width].view(case), nan_like((n, -(-width // 96))), nan_like(case, kind)
+        uvu.rms_norm_quant(x, gamma, q, s, group=96, residual=res, h=h)
+        y = layer.rms_norm(values(h), values(gamma), 1e-5)[0].reshape(n, width)
+        ref = layer.scales(y, 96)
+        np.testing.assert_allclose(values(s), ref, rtol=2.0 ** -20)
+        v = y / np.repeat(ref, 96, axis=1)[:, :width]
+        got = q.view(torch.float8_e4m3fn).float().view(n, width)
+        within(got, v, 0.5 * layer.e4m3_step(np.minimum(np.abs(v) * (1 + 2.0 ** -19), 448)) + 2.0 ** -19 * np.abs(v))
+        assert (flat[:at] == 0x55).all() and (flat[at + n * width:] == 0x55).all()
+
+
+def test_rms_norm_wide_of_any_size():
+    """As test_rms_norm_of_any_size, for rows of 9216 values."""
+    sizes = np.array([1.0, 1e-30, 1e-21, 2e17, 1e30, 3e37])
+    x, xr = rounded(np.random.default_rng(3).standard_normal((6, 1024, 9)) * sizes[:, None, None], "f32")
+    gamma, y, rstd, dx, dg = torch.ones(1024, device="cuda"), nan_like(x.shape), nan_like((6,)), nan_like(x.shape), nan_like((1024,))
+    uvu.rms_norm_fwd(x, gamma, y, rstd, eps=0.0)
+    ry, rr = layer.rms_norm(xr, np.ones(1024), 0.0)
+    within(rstd, rr, 64 * 2.0 ** -24 * rr)
+    within(y, ry, 64 * 2.0 ** -24 * np.abs(ry) + 2.0 ** -149)
+    dy, dyr = rounded(np.random.default_rng(4).standard_normal(x.shape), "f32")
+    uvu.rms_norm_bwd(dy, x, gamma, rstd, dx, dg)
+    rdx, rdg = layer.rms_norm_vjp(xr, np.ones(1024), 0.0, dyr)
+    u = xr * rr[:, None, None]
+    terms = rr[:, None, None] * (np.abs(dyr) + np.abs(u) * np.mean(np.abs(dyr * u), axis=(1, 2), keepdims=True))
+    within(dx, rdx, 128 * 2.0 ** -24 * terms + 2.0 ** -149)
+    within(dg, rdg, 128 * 2.0 ** -24 * np.abs(dyr * u).sum((0, 2)))
