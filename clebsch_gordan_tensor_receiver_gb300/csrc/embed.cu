@@ -11,7 +11,8 @@
 // The gradient adds no two threads' sums by atomic instructions, whose order would change the result.  It sorts the tokens by row (stable,
 // so that a row's tokens are added in their order), cuts the sorted tokens into pieces of equal length, however the rows lie,
 // and sums each piece in fp32 registers, 8 rows of d_out on their way at a time.  A row whose tokens lie in one piece is
-// written by it; one that goes on behind its piece is noted, and added up from the pieces' sums in the pieces' order.  Rows without a token
+// written by it; one that goes on behind its piece is noted, and added up from the pieces' sums, in their order where it reaches up to 16
+// more, else by 4 or 16 ways that take turns.  Rows without a token
 // are zeros: the table is zeroed by blocks of the first kernel that the sort leaves idle.  300,007 x 512 of f16 into 119 rows: 84 us, 21 of
 // them the sort; 8192 tokens of a 65,536 x 1024 table in bf16: 55 us, 34 of them the sort in one block, beside which the table is zeroed.
 #include <algorithm>
@@ -486,21 +487,26 @@ struct SumPlan {
     int v, x, y, slabs, piece;
     int64_t pieces;
 };
-// Pieces as long as they may be with some 64 warps on every SM: short ones write more partial sums, long ones leave SMs idle.  The
-// result does not depend on the card: 152 SMs are reckoned with.
+// Pieces as long as they may be with some 64 warps on every SM: short ones write more partial sums, long ones leave SMs idle.  They
+// decide in which order the sums are formed, so they depend on sizes and type alone: 152 SMs are reckoned with, and tensors on 16 bytes,
+// whether they lie so or not.
 SumPlan sum_plan(const EmbedShape& s, bool aligned) {
-    const int size = s.dtype == UVU_F32 ? 4 : 2;
+    const int size = s.dtype == UVU_F32 ? 4 : 2, v = s.inner == 1 && int64_t(s.channels) * size % 16 == 0 ? 16 / size : 1;
     SumPlan p;
-    p.v = aligned && s.inner == 1 && int64_t(s.channels) * size % 16 == 0 ? 16 / size : 1;
-    const int vecs = s.channels / p.v;
-    p.x = 1;
-    while (p.x < kSumThreads && p.x < vecs) p.x *= 2;
-    p.y = kSumThreads / p.x;
-    p.slabs = (vecs + p.x - 1) / p.x;
+    auto lay = [&](int width) {
+        p.v = width;
+        const int vecs = s.channels / p.v;
+        p.x = 1;
+        while (p.x < kSumThreads && p.x < vecs) p.x *= 2;
+        p.y = kSumThreads / p.x;
+        p.slabs = (vecs + p.x - 1) / p.x;
+    };
+    lay(v);
     const int64_t threads = int64_t(152) * 64 * 32, most = std::max<int64_t>(1, threads / (int64_t(p.x) * p.slabs));
     p.piece = kBatch;
     while (p.piece < 512 && (s.tokens + p.piece - 1) / p.piece > most) p.piece *= 2;
     p.pieces = (s.tokens + p.piece - 1) / p.piece;
+    if (!aligned) lay(1);
     return p;
 }
 
@@ -510,7 +516,7 @@ struct Work {
     float* part;
     size_t bytes;
 };
-Work work_of(const EmbedShape& s, const SumPlan& m, void* ws) {
+Work work_of(const EmbedShape& s, int64_t pieces, void* ws) {
     const SortPlan p = sort_plan(s);
     char* at = static_cast<char*>(ws);
     size_t used = 0;
@@ -528,8 +534,8 @@ Work work_of(const EmbedShape& s, const SumPlan& m, void* ws) {
     w.counts = reinterpret_cast<uint32_t*>(take(p.one ? 0 : size_t(p.blocks) * kBins * 4));
     w.totals = reinterpret_cast<uint32_t*>(take(kBins * 4));
     w.valid = reinterpret_cast<int32_t*>(take((kChains + kReaches) * sizeof(int32_t)));
-    w.chain = reinterpret_cast<int32_t*>(take(size_t(m.pieces) * kReaches * 4));
-    w.part = reinterpret_cast<float*>(take(size_t(m.pieces) * 2 * s.channels * 4));
+    w.chain = reinterpret_cast<int32_t*>(take(size_t(pieces) * kReaches * 4));
+    w.part = reinterpret_cast<float*>(take(size_t(pieces) * 2 * s.channels * 4));
     w.bytes = used;
     return w;
 }
@@ -554,9 +560,7 @@ template <typename T>
 cudaError_t bwd(const EmbedShape& s, const int32_t* index, const void* dout, void* dtable, void* ws, int sms, cudaStream_t st) {
     const SortPlan p = sort_plan(s);
     const SumPlan m = sum_plan(s, ((reinterpret_cast<uintptr_t>(dout) | reinterpret_cast<uintptr_t>(dtable)) & 15u) == 0);
-    // the workspace is laid out for the most pieces of either alignment
-    const SumPlan m0 = sum_plan(s, true), m1 = sum_plan(s, false);
-    const Work w = work_of(s, m0.pieces > m1.pieces ? m0 : m1, ws);
+    const Work w = work_of(s, m.pieces, ws);
     unsigned char* table = static_cast<unsigned char*>(dtable);
     const int64_t bytes = s.rows * s.channels * int64_t(sizeof(T));
     const int zeros = int(std::min<int64_t>((bytes + 16383) / 16384, sms * 6));  // blocks that zero the table
@@ -622,8 +626,7 @@ cudaError_t fwd(const EmbedShape& s, const int32_t* index, const void* table, vo
 
 size_t embed_workspace(const EmbedShape& s) {
     if (s.tokens == 0) return 0;
-    const SumPlan a = sum_plan(s, true), b = sum_plan(s, false);
-    return work_of(s, a.pieces > b.pieces ? a : b, nullptr).bytes;
+    return work_of(s, sum_plan(s, true).pieces, nullptr).bytes;
 }
 
 cudaError_t launch_embed_fwd(const EmbedShape& s, const int32_t* index, const void* table, void* out, int sms, cudaStream_t st) {

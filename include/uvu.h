@@ -619,7 +619,7 @@ uvu_status uvu_embed_fwd(uvu_dtype dtype, int64_t n_tokens, int64_t n_rows, int 
 /* VJP of uvu_embed_fwd for the cotangent dout [n_tokens][channels][inner], of which only `column` is read:
  *     dtable[r][c] = scale * sum of dout[t][c][column] over the tokens t with index[t] = r,
  * all of dtable [n_rows][channels] overwritten, rows without a token with zeros.  The sums are fp32, in an
- * order that the indices alone determine.  `workspace`: at least uvu_embed_workspace() bytes, 16-byte aligned. */
+ * order that the indices, the sizes and the type alone determine.  `workspace`: at least uvu_embed_workspace() bytes, 16-byte aligned. */
 uvu_status uvu_embed_bwd(uvu_dtype dtype, int64_t n_tokens, int64_t n_rows, int channels, int inner, int column, double scale,
                          const int32_t *index, const void *dout, void *dtable, void *workspace, size_t workspace_bytes,
                          uvu_stream_t stream);

@@ -6,9 +6,26 @@ import torch
 
 from clebsch_gordan_tensor_receiver_gb300 import uvu
 from oracle import layer
-from test_gpu_layer import KINDS, TINY, UNIT, nan_like, near, near_dx, norm_case, rounded, values, within
+from test_gpu_layer import KINDS, TINY, UNIT, embed_case, nan_like, near, near_dx, norm_case, rounded, values, within
 
 pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------- embedding
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("case", [(40001, 119, 64, 1, 0), (20000, 300, 512, 1, 0), (9001, 3, 128, 1, 0), (300, 7, 24, 1, 0)], ids=lambda c: "x".join(map(str, c)))
+def test_embedding_gradient_wherever_it_lies(case, kind):
+    """Tensors that begin off 16 bytes give the same bits: the order of the sums does not depend on where they lie."""
+    tokens, rows, c, _, _ = case
+    _, ix, _, _, dout, _ = embed_case(case, kind)
+    dout = dout.view(tokens, c)
+    want = nan_like((rows, c), kind)
+    uvu.embed_bwd(ix, dout, want)
+    flat, out = torch.cat([dout.flatten()[:1], dout.flatten()]), nan_like((rows * c + 1,), kind)
+    for d, o in ((flat[1:].view(tokens, c), nan_like((rows, c), kind)), (dout, out[1:].view(rows, c)), (flat[1:].view(tokens, c), out[1:].view(rows, c))):
+        uvu.embed_bwd(ix, d, o)
+        assert torch.equal(o, want)
 
 
 # -------------------------------------------------------------------------------------- RMS norm
