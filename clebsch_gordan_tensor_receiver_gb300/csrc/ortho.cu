@@ -203,19 +203,20 @@ __global__ void __launch_bounds__(256) norm_kernel(int rows, int cols, int64_t g
     if (threadIdx.x == 0) part[blockIdx.y * kNormBlocks + blockIdx.x] = total;
 }
 
-// The factor 1 / (|G| + eps), as two: fp32 does not hold the inverse of the smallest norms.  Zeros stay zeros, with eps = 0 too; an
-// infinity makes the whole matrix NaN, as a NaN does.
+// The factor 1 / (|G| + eps), as two: fp32 does not hold the inverse of the smallest norms, nor all bits of that of the largest.  Zeros
+// stay zeros, with eps = 0 too; an infinity makes the whole matrix NaN, as a NaN does.
 struct Factor {
     float first, second;
     __device__ __forceinline__ Factor() {}
     __device__ __forceinline__ Factor(const Squares& q, double eps) {
         first = 1.f;
-        if (q.small < 0x1p100f && q.large == 0.f && q.mid > 0x1p-60f && q.mid < 0x1p120f) {  // what `small` stands for is below 2^-80
+        if (q.small < 0x1p100f && q.large == 0.f && q.mid > 0x1p-60f && q.mid < 0x1p120f && eps < 0x1p100) {  // what `small` stands for is below 2^-80
             second = 1.f / (sqrtf(q.mid) + float(eps));
         } else {  // rarely: fp64 is slow here
             const double squares = double(q.small) * 0x1p-180 + double(q.mid) + double(q.large) * 0x1p180;
             const double inv = squares == 0.0 ? 0.0 : isinf(squares) ? double(NAN) : 1.0 / (sqrt(squares) + eps);
             if (inv > 0x1p100) first = 0x1p60f;
+            if (inv < 0x1p-100) first = 0x1p-60f;
             second = float(inv / double(first));
         }
     }

@@ -5,8 +5,9 @@ import pytest
 import torch
 
 from clebsch_gordan_tensor_receiver_gb300 import uvu
+from gpu_util import check
 from oracle import layer
-from test_gpu_layer import KINDS, TINY, UNIT, embed_case, nan_like, near, near_dx, norm_case, rounded, values, within
+from test_gpu_layer import KINDS, MUON, TINY, UNIT, embed_case, nan_like, near, near_dx, norm_case, rounded, values, within
 
 pytestmark = pytest.mark.gpu
 
@@ -174,3 +175,21 @@ def test_rms_norm_wide_of_any_size():
     terms = rr[:, None, None] * (np.abs(dyr) + np.abs(u) * np.mean(np.abs(dyr * u), axis=(1, 2), keepdims=True))
     within(dx, rdx, 128 * 2.0 ** -24 * terms + 2.0 ** -149)
     within(dg, rdg, 128 * 2.0 ** -24 * np.abs(dyr * u).sum((0, 2)))
+
+
+# ----------------------------------------------------------------------------------- Newton-Schulz
+
+@pytest.mark.parametrize("eps", [0.0, 1e38])
+@pytest.mark.parametrize("size", [1e36, 3e38])
+@pytest.mark.parametrize("shape", [(30, 50), (300, 200)], ids=str)
+def test_orthogonalize_largest_norms(shape, size, eps):
+    """1 / (|G| + eps) below 2^-126.  Without steps each value has the norm's error (of 36 additions to a value, in fp32, halved by the root),
+    the factor's rounding and the product's: 24 roundings of 2^-24 at most."""
+    g, gr = rounded(np.random.default_rng(7).uniform(-1, 1, shape) * size, "f32")
+    out = nan_like(shape)
+    uvu.orthogonalize(g, out, steps=0, eps=eps)
+    ref = gr / (np.linalg.norm(gr / size) * size + float(np.float32(eps)))
+    within(out, ref, 24 * 2.0 ** -24 * np.abs(ref) + 2.0 ** -149)
+    # with steps: the limit of test_orthogonalize_any_size, at this size
+    uvu.orthogonalize(g, out, eps=0.0)
+    check(values(out), layer.newton_schulz(gr / size, 5, MUON, 0.0)[-1], False)
