@@ -9,7 +9,8 @@
 // and a sign, and hi hi + 2^-11 (hi lo + lo hi) is formed in two fp32 accumulators; lo lo (2^-24 of the product) is left out.  Errors
 // matter here: a step stretches what is small in X by a = 3.4, five of them by 485, so 16-bit operands alone would be off by 1%
 // and more where few singular values hold most of a gradient.  Values are held at 2^8 times their size, which keeps
-// those of large matrices (1 / sqrt(m n)) normal numbers of fp16 and those near 1 far from its largest.
+// those of large matrices (1 / sqrt(m n)) normal numbers of fp16 and those near 1 far from its largest.  Below 2^-22 the bits get fewer, to an
+// error of 2^-44: that matters where a gradient's norm lies far below eps.
 //
 // An accumulating matrix instruction (16 terms) cuts its sum towards zero, by 2^-24 of it in the mean (measured: 2.8 2^-24 after
 // four of them, 7.7 after eight, on sums of one sign).  So the hi hi sums leave their accumulator every 64 terms, while the lo products,

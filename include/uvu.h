@@ -665,8 +665,10 @@ uvu_status uvu_rms_norm_workspace(uvu_dtype dtype, int64_t n_rows, int channels,
  * (a tall G is turned before and after, which changes nothing but the work).  Batches are mixing matrices [P][U][W], or
  * one dense layer.  Strides in elements; the values of a row are consecutive; out may be g with the same strides, and must not
  * overlap it otherwise.  rows, cols in [1, 16384], steps in [0, 64].  Products are of fp32 accuracy, from two fp16 terms a
- * value on the tensor cores, for values of X and X X^T up to 250 (Muon's coefficients keep them below 2); beyond, NaN.  A matrix of zeros gives
- * zeros; one with a NaN or an infinity gives NaN; other matrices of the batch are not affected. */
+ * value on the tensor cores, for values of X, X X^T and a I + b X X^T + c (X X^T)^2 up to 250 (Muon's coefficients keep them below 5); beyond,
+ * NaN.  The terms hold a value of X to 2^-23 of itself or to 2^-44, whichever is more: a G whose norm is far below eps has an X that much
+ * smaller than one, and keeps fewer bits (of 4096 x 2048 values at a norm of 1e-12 and eps = 1e-7 some 15).  A matrix of
+ * zeros gives zeros; one with a NaN or an infinity gives NaN; other matrices of the batch are not affected. */
 typedef struct {
     uvu_dtype dtype;
     int32_t n_matrices, rows, cols, steps;

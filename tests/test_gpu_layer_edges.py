@@ -7,7 +7,7 @@ import torch
 from clebsch_gordan_tensor_receiver_gb300 import uvu
 from gpu_util import check
 from oracle import layer
-from test_gpu_layer import KINDS, MUON, TINY, UNIT, embed_case, nan_like, near, near_dx, norm_case, rounded, values, within
+from test_gpu_layer import KINDS, MUON, TINY, UNIT, embed_case, gradient, nan_like, near, near_dx, norm_case, ortho_limit, rounded, values, within
 
 pytestmark = pytest.mark.gpu
 
@@ -193,3 +193,27 @@ def test_orthogonalize_largest_norms(shape, size, eps):
     # with steps: the limit of test_orthogonalize_any_size, at this size
     uvu.orthogonalize(g, out, eps=0.0)
     check(values(out), layer.newton_schulz(gr / size, 5, MUON, 0.0)[-1], False)
+
+
+@pytest.mark.parametrize("norm", [1e-9, 1e-11, 1e-13])
+@pytest.mark.parametrize("shape", [(96, 160), (300, 200), (60, 2000)], ids=str)
+def test_orthogonalize_far_below_eps(shape, norm):
+    """Gradients whose norm is far below eps: X has values that two fp16 terms hold to 2^-44 at least.  Each of the steps writes X with that error
+    and stretches what was there before by at most a, beside the products' errors of ortho_limit."""
+    rng = np.random.default_rng(8)
+    a = gradient(shape, rng)
+    g, gr = rounded(a * (norm / np.linalg.norm(a)), "f32")
+    out = nan_like(shape)
+    uvu.orthogonalize(g, out, eps=1e-7)
+    xs = layer.newton_schulz(gr, 5, MUON, 1e-7)
+    held = 2.0 ** -44 * g.numel() ** 0.5 * sum(MUON[0] ** k for k in range(1, 6))
+    assert np.linalg.norm(values(out) - xs[-1]) <= ortho_limit(xs, "f32") + held
+
+
+@pytest.mark.parametrize("shape", [(30, 50), (300, 200)], ids=str)
+def test_orthogonalize_beyond_its_range(shape):
+    """a I + b P + c P P beyond 250 is not held: NaN, not wrong values."""
+    g = torch.randn(shape, device="cuda")
+    out = torch.zeros(shape, device="cuda")
+    uvu.orthogonalize(g, out, steps=1, coefficients=(300.0, 0.0, 0.0))
+    assert torch.isnan(out).all()
