@@ -14,7 +14,10 @@ class Muon(torch.optim.Optimizer):
     """Momentum, then W <- (1 - lr weight_decay) W - lr max(1, rows / cols)^(1/2) O, with O the momentum (looked ahead where
     `nesterov`) made nearly orthogonal, matrix by matrix.  Parameters are [rows][cols] or batches [matrices][rows][cols]; those of
     one type and size are made orthogonal in one call.  Other parameters (tables, norms' gamma, biases) belong to another
-    optimiser."""
+    optimiser.
+
+    The momentum and the update are fp32 for 16-bit parameters too: a 16-bit average takes no step of less than half its
+    own (with momentum 0.95 and bf16, a gradient within 8% of it changes nothing).  The parameter itself rounds once for the decay and once for the update."""
 
     def __init__(self, params, lr: float = 0.02, momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
                  steps: int = 5, coefficients=uvu.MUON, eps: float = 1e-7):
@@ -26,6 +29,15 @@ class Muon(torch.optim.Optimizer):
             for p in group["params"]:
                 if p.dim() not in (2, 3):
                     raise ValueError(f"Muon takes matrices or batches of matrices, not a parameter of shape {tuple(p.shape)}")
+
+    def load_state_dict(self, state_dict):
+        """As PyTorch's, which casts what it loads to the parameter's type; the momentum stays in fp32."""
+        super().load_state_dict(state_dict)
+        numbers = (i for group in state_dict["param_groups"] for i in group["params"])
+        for i, p in zip(numbers, (p for group in self.param_groups for p in group["params"])):
+            buf = state_dict["state"].get(i, {}).get("momentum")
+            if buf is not None:
+                self.state[p]["momentum"] = buf.to(p.device, torch.float32, copy=True)
 
     @torch.no_grad()
     def step(self, closure=None):
@@ -49,10 +61,11 @@ class Muon(torch.optim.Optimizer):
         for p in params:
             state = self.state[p]
             if "momentum" not in state:
-                state["momentum"] = torch.zeros_like(p, memory_format=torch.contiguous_format)
+                state["momentum"] = torch.zeros_like(p, dtype=torch.float32, memory_format=torch.contiguous_format)
             buf = state["momentum"]
-            buf.lerp_(p.grad, 1 - m)
-            updates.append((p.grad.lerp(buf, m) if group["nesterov"] else buf).reshape(-1, *size))
+            grad = p.grad.float()
+            buf.lerp_(grad, 1 - m)
+            updates.append((grad.lerp(buf, m) if group["nesterov"] else buf).reshape(-1, *size))
         u = torch.cat(updates)
         with torch.cuda.device(u.device):
             uvu.orthogonalize(u, u, steps=group["steps"], coefficients=group["coefficients"], eps=group["eps"])

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from clebsch_gordan_tensor_receiver_gb300 import uvu
+from clebsch_gordan_tensor_receiver_gb300 import optim, uvu
 from gpu_util import check
 from oracle import layer
 from test_gpu_layer import KINDS, MUON, TINY, UNIT, embed_case, gradient, nan_like, near, near_dx, norm_case, ortho_limit, rounded, values, within
@@ -217,3 +217,63 @@ def test_orthogonalize_beyond_its_range(shape):
     out = torch.zeros(shape, device="cuda")
     uvu.orthogonalize(g, out, steps=1, coefficients=(300.0, 0.0, 0.0))
     assert torch.isnan(out).all()
+
+
+# --------------------------------------------------------------------------------------------- Muon
+
+def muon_reference(start, grads, lr, momentum, nesterov, decay):
+    """Parameters and momentum after the gradients, in fp64."""
+    p, buf = start.copy(), np.zeros_like(start)
+    for g in grads:
+        buf = momentum * buf + (1 - momentum) * g
+        u = ((1 - momentum) * g + momentum * buf if nesterov else buf).reshape(-1, *p.shape[-2:])
+        o = np.stack([layer.newton_schulz(a, 5, MUON, 1e-7)[-1] for a in u]).reshape(p.shape)
+        p = p * (1 - lr * decay) - lr * max(1, p.shape[-2] / p.shape[-1]) ** 0.5 * o
+    return p, buf
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nesterov", [True, False])
+def test_muon_of_any_type(kind, nesterov):
+    """Matrices, batches and a transposed parameter whose gradient is transposed too.  The momentum is fp32: each step rounds it three times
+    at most.  A parameter has two roundings a step, of at most its largest value on the way, beside what gpu_util.check allows of an update."""
+    rng = np.random.default_rng(13)
+    steps, shapes = 12, [(3, 20, 12), (20, 12), (30, 44)]
+    first = [rounded(rng.standard_normal(s), kind) for s in shapes]
+    params = [t.clone().requires_grad_(True) for t, _ in first]
+    params[2] = first[2][0].t().contiguous().t().requires_grad_(True)
+    assert not params[2].is_contiguous()
+    grads = [[rounded(0.5 + rng.standard_normal(s), kind) for s in shapes] for _ in range(steps)]
+    opt = optim.Muon(params, lr=0.05, momentum=0.9, nesterov=nesterov, weight_decay=0.01)
+    for step in grads:
+        for p, (g, _) in zip(params, step):
+            p.grad = g.clone()
+        params[2].grad = step[2][0].t().contiguous().t()
+        opt.step()
+    for i, p in enumerate(params):
+        ref, buf = muon_reference(first[i][1], [g[i][1] for g in grads], 0.05, 0.9, nesterov, 0.01)
+        got = opt.state[p]["momentum"]
+        assert got.dtype == torch.float32 and p.dtype == first[i][0].dtype
+        within(got, buf, 3 * steps * 2.0 ** -24 * max(np.abs(g[i][1]).max() for g in grads), "momentum")
+        largest = max(np.abs(first[i][1]).max(), np.abs(ref).max()) + 0.05 * steps
+        within(p.detach(), ref, 2 * steps * UNIT[kind] * largest * (kind != "f32") + 1e-4 * (1 + np.abs(ref)), "parameter")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_muon_goes_on_from_a_saved_state(kind):
+    rng = np.random.default_rng(14)
+    start, _ = rounded(rng.standard_normal((24, 40)), kind)
+    grads = [rounded(rng.standard_normal((24, 40)), kind)[0] for _ in range(3)]
+    a, b = (start.clone().requires_grad_(True) for _ in range(2))
+    opt = optim.Muon([a])
+    for g in grads[:2]:
+        a.grad = g
+        opt.step()
+    again = optim.Muon([b], lr=0.5)
+    again.load_state_dict(opt.state_dict())
+    b.data.copy_(a.data)
+    assert again.state[b]["momentum"].dtype == torch.float32 and torch.equal(again.state[b]["momentum"], opt.state[a]["momentum"])
+    for p, o in ((a, opt), (b, again)):
+        p.grad = grads[2]
+        o.step()
+    assert torch.equal(a, b) and torch.equal(again.state[b]["momentum"], opt.state[a]["momentum"])
