@@ -25,10 +25,13 @@ class Muon(torch.optim.Optimizer):
             raise ValueError("lr and weight_decay must be >= 0 and momentum in [0, 1)")
         super().__init__(params, dict(lr=lr, momentum=momentum, nesterov=nesterov, weight_decay=weight_decay, steps=steps,
                                       coefficients=tuple(coefficients), eps=eps))
-        for group in self.param_groups:
-            for p in group["params"]:
-                if p.dim() not in (2, 3):
-                    raise ValueError(f"Muon takes matrices or batches of matrices, not a parameter of shape {tuple(p.shape)}")
+
+    def add_param_group(self, param_group):
+        super().add_param_group(param_group)
+        for p in self.param_groups[-1]["params"]:
+            if p.dim() not in (2, 3):
+                self.param_groups.pop()
+                raise ValueError(f"Muon takes matrices or batches of matrices, not a parameter of shape {tuple(p.shape)}")
 
     def load_state_dict(self, state_dict):
         """As PyTorch's, which casts what it loads to the parameter's type; the momentum stays in fp32."""

@@ -1,7 +1,8 @@
 """Limits of the arguments of the operators around a layer, and the optimiser's own checks: these tests need no GPU."""
 import pytest
+import torch
 
-from clebsch_gordan_tensor_receiver_gb300 import uvu
+from clebsch_gordan_tensor_receiver_gb300 import optim, uvu
 
 F32, BF16 = uvu.UVU_F32, uvu.UVU_BF16
 
@@ -24,3 +25,17 @@ def test_width_of_rms_norm(channels, inner, fits, dtype):
         else:
             status, text = refused(call)
             assert status == 1 and "channels * inner" in text
+
+
+def test_muon_groups_of_matrices():
+    """A group that is added later is held to the same; one that is refused leaves the optimiser as it was."""
+    matrix, vector, volume = (torch.zeros(s, requires_grad=True) for s in ((3, 4), (3,), (2, 3, 4, 5)))
+    opt = optim.Muon([matrix])
+    for bad in (vector, volume):
+        with pytest.raises(ValueError, match="matrices"):
+            opt.add_param_group({"params": [bad]})
+        assert len(opt.param_groups) == 1
+    opt.add_param_group({"params": [torch.zeros(2, 3, 4, requires_grad=True)], "lr": 0.1})
+    assert [g["lr"] for g in opt.param_groups] == [0.02, 0.1]
+    with pytest.raises(ValueError, match="matrices"):
+        optim.Muon([{"params": [matrix]}, {"params": [vector]}])
