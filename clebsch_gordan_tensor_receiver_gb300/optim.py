@@ -10,6 +10,9 @@ import torch
 from . import uvu
 
 
+MOST = 65535  # matrices of one call
+
+
 class Muon(torch.optim.Optimizer):
     """Momentum, then W <- (1 - lr weight_decay) W - lr max(1, rows / cols)^(1/2) O, with O the momentum (looked ahead where
     `nesterov`) made nearly orthogonal, matrix by matrix.  Parameters are [rows][cols] or batches [matrices][rows][cols]; those of
@@ -71,7 +74,8 @@ class Muon(torch.optim.Optimizer):
             updates.append((grad.lerp(buf, m) if group["nesterov"] else buf).reshape(-1, *size))
         u = torch.cat(updates)
         with torch.cuda.device(u.device):
-            uvu.orthogonalize(u, u, steps=group["steps"], coefficients=group["coefficients"], eps=group["eps"])
+            for part in u.split(MOST):
+                uvu.orthogonalize(part, part, steps=group["steps"], coefficients=group["coefficients"], eps=group["eps"])
         rate = -group["lr"] * max(1.0, size[0] / size[1]) ** 0.5
         at = 0
         for p, part in zip(params, updates):

@@ -277,3 +277,16 @@ def test_muon_goes_on_from_a_saved_state(kind):
         p.grad = grads[2]
         o.step()
     assert torch.equal(a, b) and torch.equal(again.state[b]["momentum"], opt.state[a]["momentum"])
+
+
+def test_muon_of_many_matrices():
+    """More matrices of one size than a call takes."""
+    n = 70_000
+    g = torch.randn(n, 2, 3, device="cuda")
+    p = torch.zeros(n, 2, 3, device="cuda", requires_grad=True)
+    p.grad = g
+    optim.Muon([p], lr=1.0, momentum=0.0).step()
+    for part in (slice(0, 50), slice(65530, 65540), slice(n - 50, n)):
+        want = torch.empty_like(g[part])
+        uvu.orthogonalize(g[part].contiguous(), want)
+        assert torch.equal(p.detach()[part], -want)
