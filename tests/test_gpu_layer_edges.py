@@ -5,9 +5,12 @@ import pytest
 import torch
 
 from clebsch_gordan_tensor_receiver_gb300 import optim, uvu
-from gpu_util import check
+from gpu_util import check, dev
 from oracle import layer
-from test_gpu_layer import KINDS, MUON, TINY, UNIT, embed_case, gradient, nan_like, near, near_dx, norm_case, ortho_limit, rounded, values, within
+from test_gpu_layer import (KINDS, MUON, TINY, TYPES, UNIT, embed_case, gradient, nan_like, near, near_dx, norm_case, ortho_limit, rounded,
+                            values, within)
+from test_gpu_layer import test_orthogonalize as orthogonalize_case
+from test_gpu_workspace_bounds import Guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -27,6 +30,29 @@ def test_embedding_gradient_wherever_it_lies(case, kind):
     for d, o in ((flat[1:].view(tokens, c), nan_like((rows, c), kind)), (dout, out[1:].view(rows, c)), (flat[1:].view(tokens, c), out[1:].view(rows, c))):
         uvu.embed_bwd(ix, d, o)
         assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("tokens", [500, 20000])
+def test_embedding_of_many_rows(tokens):
+    """A table of more than 2^24 rows, whose tokens are sorted in four passes, in one block and in several."""
+    rows = 2 ** 24 + 77
+    rng = np.random.default_rng(tokens)
+    index = rng.integers(0, rows, size=tokens).astype(np.int32)
+    index[:5], index[5:8] = rows - 1, (-1, rows, 2 ** 24)
+    index[tokens // 2:] = index[:tokens - tokens // 2]
+    ix, dout = dev(index), torch.randn(tokens, 2, device="cuda")
+    dtable = nan_like((rows, 2))
+    uvu.embed_bwd(ix, dout, dtable)
+    keep = (index >= 0) & (index < rows)
+    used, which = np.unique(index[keep], return_inverse=True)
+    ref, size, count = layer.embed_vjp(which.astype(np.int32), values(dout)[keep][:, :, None], len(used), 1.0, 0)
+    within(dtable[dev(used.astype(np.int64))], ref, (np.maximum(count, 1)[:, None] + 2) * 2.0 ** -24 * size)
+    assert not dtable.index_fill_(0, dev(used.astype(np.int64)), 0.0).any()
+    out = nan_like((tokens, 2))
+    table = dtable
+    table[:, 0] = torch.arange(rows, device="cuda") % 1000
+    uvu.embed_fwd(ix, table, out)
+    assert torch.equal(out[:, 0].cpu(), torch.from_numpy(np.where(keep, index % 1000, 0)).float()) and not out[:, 1].any()
 
 
 # -------------------------------------------------------------------------------------- RMS norm
@@ -179,6 +205,16 @@ def test_rms_norm_wide_of_any_size():
 
 # ----------------------------------------------------------------------------------- Newton-Schulz
 
+CLUSTERS = [(2, 128, 512), (3, 40, 300), (1, 500, 100), (2, 40, 1800), (1, 113, 2000), (1, 1030, 17), (9, 128, 2048), (2, 31, 700)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("case", CLUSTERS, ids=lambda c: "x".join(map(str, c)))
+def test_orthogonalize_clusters(case, kind):
+    """Clusters of 2, 4 and 8 blocks, with rows that they share evenly and not."""
+    orthogonalize_case(case, kind)
+
+
 @pytest.mark.parametrize("eps", [0.0, 1e38])
 @pytest.mark.parametrize("size", [1e36, 3e38])
 @pytest.mark.parametrize("shape", [(30, 50), (300, 200)], ids=str)
@@ -290,3 +326,69 @@ def test_muon_of_many_matrices():
         want = torch.empty_like(g[part])
         uvu.orthogonalize(g[part].contiguous(), want)
         assert torch.equal(p.detach()[part], -want)
+
+
+# --------------------------------------------------------------------------------- as they are used
+
+def test_graphs_of_every_sort():
+    """The sort in several blocks, and the one beside which a large table is zeroed, on a side stream and in two captured graphs."""
+    rng = np.random.default_rng(15)
+    cases = []
+    for tokens, rows in ((20000, 3000), (3000, 70000), (40000, 70000)):
+        cases.append((dev(rng.integers(-1, rows, size=tokens).astype(np.int32)), torch.randn(tokens, 32, device="cuda"), rows))
+
+    def new():
+        return [nan_like((rows, 32)) for _, _, rows in cases]
+
+    def step(out, **kw):
+        for (ix, dout, _), o in zip(cases, out):
+            uvu.embed_bwd(ix, dout, o, **kw)
+
+    want, got, side = new(), new(), torch.cuda.Stream()
+    step(want)
+    side.wait_stream(torch.cuda.current_stream())
+    step(got, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    outs, graphs = [new(), new()], []
+    for o in outs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            step(o)
+    for _ in range(2):
+        for o in outs:
+            for t in o:
+                t.fill_(float("nan"))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for o in outs for a, b in zip(o, want))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("off", [0, 1], ids=["aligned", "off"])
+def test_workspaces_hold_what_they_are_asked_for(kind, off):
+    """Workspaces of exactly the bytes that are asked for, of gradients on and off 16 bytes: nothing is written behind them, nor behind results."""
+    g = Guarded()
+
+    def at(t):
+        return torch.cat([t.flatten()[:1], t.flatten()])[1:].view(t.shape) if off else t
+
+    for case in ((300, 119, 64, 1, 0), (40001, 119, 64, 1, 0), (20000, 70000, 24, 1, 0), (5000, 9, 33, 4, 2), (9, 3, 7, 1, 0)):
+        tokens, rows, c, inner, column = case
+        _, ix, _, _, dout, _ = embed_case(case, kind)
+        dout, dtable = at(dout), g.out(rows, c, dtype=TYPES[kind])
+        uvu.embed_bwd(ix, dout, dtable, column=column, workspace=g.ws(uvu.embed_workspace_bytes(dout, dtable)))
+    for case in ((5000, 128, 4), (3, 8191, 1), (70001, 5, 1), (6001, 427, 1), (1, 3, 1), (700, 1024, 9), (3, 2731, 3)):
+        x, _, dy, dh, gamma = norm_case(case, kind)[0]
+        x, dy, dh = at(x), at(dy), at(dh)
+        y, rstd = torch.empty_like(x), g.out(case[0])
+        uvu.rms_norm_fwd(x, gamma, y, rstd)
+        uvu.rms_norm_bwd(dy, x, gamma, rstd, g.out(*case, dtype=TYPES[kind]), g.out(case[1]), dh=dh, workspace=g.ws(uvu.rms_norm_workspace_bytes(x)))
+    for case in ((2, 128, 512), (12, 40, 1800), (3, 129, 127), (2, 256, 256), (1, 700, 301), (1, 1, 1)):
+        a = at(torch.randn(case, device="cuda").to(TYPES[kind]))
+        need = uvu.orthogonalize_workspace_bytes(a)
+        for steps in (0, 1, 5):
+            uvu.orthogonalize(a, g.out(*case, dtype=TYPES[kind]), steps=steps, workspace=g.ws(need))
+    g.check()
+    assert uvu.orthogonalize_device_status() == 0
