@@ -12,8 +12,8 @@
 // asynchronous copies that cost no registers: with one row ahead in registers the gradient had 48 KB in flight on an SM and ran at half of
 // the memory's rate.  Rows that do not begin on 16 bytes are read in words, one row ahead in registers (copied in whole chunks, with
 // what lies before and behind them, they took twice the time), also where every other one begins inside a word.  262,144 x 512 in bf16 with
-// the residual: 335 us forward and back (6.4 TB/s); 65,537 x 1024 to 8 bits 88 us (5.4 TB/s); 96,064 x 427 in f16: 63 us
-// (5.2 TB/s), 89 us (3.7 TB/s) and 91 us.  A thread has the same columns of every row that it sees, so gamma is read once, and d_gamma is
+// the residual: 341 us forward and back (6.3 TB/s); 65,537 x 1024 to 8 bits 88 us (5.4 TB/s); 96,064 x 427 in f16 with the residual: 63 us
+// (5.2 TB/s) forward, 90 us (3.7 TB/s) back, to 8 bits 71 us (4.0 TB/s), with groups of 64, which lanes do not share evenly, 172 us.  A thread has the same columns of every row that it sees, so gamma is read once, and d_gamma is
 // summed in registers, then over the block's teams in shared memory, and over the blocks, in their order, by a second kernel.
 #pragma once
 
@@ -77,20 +77,29 @@ __device__ __forceinline__ float squares_factor(float mean) { return mean < 1.f 
 //
 // Where nothing leaves fp32's range, by a quotient's last step (Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990): q = v f with f = 1/s to some 2^-23, then q + (v - q s) f, whose error before it is rounded is 2^-44.
-// As divisions: 114 us for 65,537 x 1024 from bf16.
+// As divisions: 114 us for 65,537 x 1024 from bf16.  Whether a scale is too small or large for it is asked once a row, by a
+// whole warp: a branch for each vector made 96,064 x 428 take 88 us where this takes 60.
 struct Scale {
-    float s, f;
-    bool usual;
+    float s, f;  // f: NaN where fp32's range may be left; 0 for zeros
+    __device__ __forceinline__ Scale() {}
+    __device__ __forceinline__ Scale(float scale, float inverse) : s(scale), f(inverse) {}
     __device__ __forceinline__ explicit Scale(float top) {
-        usual = top > 0x1p-70f && top < 0x1p108f;  // a remainder that fp32 does not hold is of a value that rounds to zero
-        s = top * (1.f / kTop);
-        if (usual) s = fmaf(fmaf(-s, kTop, top), 1.f / kTop, s);
-        else s = top / kTop;
+        const float q = top * (1.f / kTop);
+        s = fmaf(fmaf(-q, kTop, top), 1.f / kTop, q);
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(s));
+        // not 2^-70 <= top < 2^108, by one comparison of the bits (a remainder that fp32 does not hold is of a value that rounds to zero)
+        if (__builtin_expect(__float_as_uint(top) - 0x1C800000u >= 0x75800000u - 0x1C800000u, 0)) {
+            s = top / kTop;
+            f = s == 0.f ? 0.f : NAN;
+        }
     }
-    template <int N>
+    __device__ __forceinline__ bool rare() const { return f != f; }
+    template <bool RARE, int N>
     __device__ __forceinline__ void divide(const float* v, float (&u)[N]) const {
-        if (usual) {
+        if constexpr (RARE) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) u[i] = s == 0.f ? 0.f : v[i] / s;
+        } else {
 #pragma unroll
             for (int i = 0; i + 1 < N; i += 2) {
                 const F2 w(v[i], v[i + 1]), q = w * F2(f, f);
@@ -101,9 +110,6 @@ struct Scale {
                 const float q = v[N - 1] * f;
                 u[N - 1] = fmaf(fmaf(q, -s, v[N - 1]), f, q);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) u[i] = s == 0.f ? 0.f : v[i] / s;
         }
     }
 };
@@ -287,7 +293,7 @@ struct RmsRow {
             if (live && has_lone) scale<1>(v + kN, gamma + kN, r, y + lone);
     }
 
-    // s_top (kRmsQuantAny): a word for each group of the row.
+    // s_top (kRmsQuantAny): two words for each group of the row.
     __device__ __forceinline__ void quantise(const Read& in, bool res, uint8_t* q, T* h, float* scales, int group, int groups, bool live,
                                              float* s_part, unsigned* s_top) const {
         float v[kN + kLone];
@@ -326,29 +332,43 @@ struct RmsRow {
             if constexpr (END == kOdd)
                 if (live && has_lone) atomicMax(s_top + lone / group, __float_as_uint(fabsf(v[kN])));
             sync();
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int c = column(k), g = c / group;
-                if (!live || !inside(k)) continue;
-                float u[V];
-                if ((c + V - 1) / group == g) {
-                    Scale(__uint_as_float(s_top[g])).divide(v + k * V, u);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        float one[1];
-                        Scale(__uint_as_float(s_top[(c + i) / group])).divide(v + k * V + i, one);
-                        u[i] = one[0];
-                    }
-                }
-                Bytes<V> o;
-                o.set(u);
-                *reinterpret_cast<Bytes<V>*>(q + c) = o;
+            float *s_scale = reinterpret_cast<float*>(s_top), *s_inverse = s_scale + groups;
+            bool rare = false;
+            for (int j = lane; j < groups; j += team) {
+                const Scale scale(__uint_as_float(s_top[j]));
+                s_scale[j] = scale.s, s_inverse[j] = scale.f;
+                if (live) scales[j] = scale.s;
+                rare |= scale.rare();
             }
-            if constexpr (END == kOdd)
-                if (live && has_lone) give_lone(Scale(__uint_as_float(s_top[lone / group])), v + kN, q);
-            for (int j = lane; j < groups; j += team)
-                if (live) scales[j] = Scale(__uint_as_float(s_top[j])).s;
+            if (WARP) __syncwarp();
+            else rare = __syncthreads_or(rare);
+            auto scale_of = [&](int g) { return Scale(s_scale[g], s_inverse[g]); };
+            auto give = [&](auto rare) {
+                constexpr bool RARE = decltype(rare)::value;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const int c = column(k), g = c / group;
+                    if (!live || !inside(k)) continue;
+                    float u[V];
+                    if ((c + V - 1) / group == g) {
+                        scale_of(g).template divide<RARE>(v + k * V, u);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            float one[1];
+                            scale_of((c + i) / group).template divide<RARE>(v + k * V + i, one);
+                            u[i] = one[0];
+                        }
+                    }
+                    Bytes<V> o;
+                    o.set(u);
+                    *reinterpret_cast<Bytes<V>*>(q + c) = o;
+                }
+                if constexpr (END == kOdd)
+                    if (live && has_lone) give_lone<RARE>(scale_of(lone / group), v + kN, q);
+            };
+            if (__builtin_expect(__any_sync(0xffffffffu, rare), 0)) give(std::true_type());
+            else give(std::false_type());
         } else {
             // The largest |y| of a thread's group, for each step.  A group is the row, a power of two of a step's lanes, or a power of two
             // of a warp's whole steps.
@@ -381,26 +401,43 @@ struct RmsRow {
                         for (int k = 0; k < K; ++k) top[k] = nan_max(top[k], other[k]);
                     }
             }
-            Scale scale(top[0]);
+            // one group: `whole`, and rows of odd length (others of those are kRmsQuantAny's)
+            auto give = [&](auto rare, auto scale) {
+                constexpr bool RARE = decltype(rare)::value;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int c = column(k);
-                if (k > 0 && !whole) scale = Scale(top[k]);
-                if (!live || !inside(k)) continue;
-                float u[V];
-                scale.divide(v + k * V, u);
-                if (whole ? k == 0 && lane == 0 : (c & (group - 1)) == 0) scales[whole ? 0 : c >> bits] = scale.s;
-                Bytes<V> o;
-                o.set(u);
-                *reinterpret_cast<Bytes<V>*>(q + c) = o;
+                for (int k = 0; k < K; ++k) {
+                    const int c = column(k);
+                    if (!live || !inside(k)) continue;
+                    float u[V];
+                    scale(k).template divide<RARE>(v + k * V, u);
+                    if (whole ? k == 0 && lane == 0 : (c & (group - 1)) == 0) scales[whole ? 0 : c >> bits] = scale(k).s;
+                    Bytes<V> o;
+                    o.set(u);
+                    *reinterpret_cast<Bytes<V>*>(q + c) = o;
+                }
+                if constexpr (END == kOdd)
+                    if (live && has_lone) give_lone<RARE>(scale(0), v + kN, q);
+            };
+            auto give_either = [&](bool rare, auto scale) {
+                if (__builtin_expect(__any_sync(0xffffffffu, rare), 0)) give(std::true_type(), scale);
+                else give(std::false_type(), scale);
+            };
+            if (whole) {
+                const Scale one(top[0]);
+                give_either(one.rare(), [&](int) { return one; });
+            } else if constexpr (END != kOdd) {
+                Scale each[K];
+                bool rare = false;
+#pragma unroll
+                for (int k = 0; k < K; ++k) each[k] = Scale(top[k]), rare |= each[k].rare();
+                give_either(rare, [&](int k) { return each[k]; });
             }
-            if constexpr (END == kOdd)  // one group: others are kRmsQuantAny's
-                if (live && has_lone) give_lone(scale, v + kN, q);
         }
     }
+    template <bool RARE>
     __device__ __forceinline__ void give_lone(const Scale& scale, const float* v, uint8_t* q) const {
         float u[1];
-        scale.divide(v, u);
+        scale.template divide<RARE>(v, u);
         Bytes<1> o;
         o.set(u);
         q[lone] = o.b[0];
@@ -497,7 +534,7 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 1 ? 1024 : 512) rms_kernel(c
             op.forward(now, out1 != nullptr, static_cast<T*>(a.out[0]) + at, out1 + at, a.rstd ? a.rstd + row : nullptr, live, s_part[half]);
         else if constexpr (MODE == kRmsQuant || MODE == kRmsQuantAny)
             op.quantise(now, out1 != nullptr, static_cast<uint8_t*>(a.out[0]) + at, out1 + at, a.scales + row * a.groups, a.group, a.groups,
-                        live, s_part[half], s_top + mine * a.groups);
+                        live, s_part[half], s_top + mine * 2 * a.groups);
         else
             op.backward(now, static_cast<T*>(a.out[0]) + at, live, s_part[half]);
         half ^= 1;
@@ -641,7 +678,7 @@ cudaError_t rms_launch(RmsArgs a, int sms, cudaStream_t st, int64_t* partials) {
             known[full || p.odd].store(regs = std::max(1, f.numRegs), std::memory_order_relaxed);
         }
         auto smem_of = [&](int ahead) {
-            const size_t b = one * (ahead + 1) + (MODE == kRmsQuantAny ? size_t(teams) * a.groups * 4 : 0);
+            const size_t b = one * (ahead + 1) + (MODE == kRmsQuantAny ? size_t(teams) * a.groups * 8 : 0);
             return MODE == kRmsBwd ? std::max(b, size_t(teams) * a.width * 4) : b;
         };
         auto resident = [&](size_t smem) {

@@ -143,18 +143,23 @@ __global__ void __launch_bounds__(kWideThreads) rms_wide_kernel(const RmsArgs a)
             });
             __syncthreads();
             uint8_t* q = static_cast<uint8_t*>(a.out[0]) + at;
+            auto divide = [&](int g, const float* v, auto& u) {
+                const Scale scale(__uint_as_float(s_top[g]));
+                if (__builtin_expect(scale.rare(), 0)) scale.template divide<true>(v, u);
+                else scale.template divide<false>(v, u);
+            };
             each<V>(a.width, [&](int c, bool inside) {
                 if (!inside) return;
                 float v[V], u[V];
                 normal(c, v);
                 const int g = c / a.group;
                 if ((c + V - 1) / a.group == g) {
-                    Scale(__uint_as_float(s_top[g])).divide(v, u);
+                    divide(g, v, u);
                 } else {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         float one[1];
-                        Scale(__uint_as_float(s_top[(c + i) / a.group])).divide(v + i, one);
+                        divide((c + i) / a.group, v + i, one);
                         u[i] = one[0];
                     }
                 }

@@ -113,6 +113,30 @@ def test_rms_norm_of_any_size(width, eps, kind):
         assert torch.equal(q.cpu().float(), v.float())
 
 
+@pytest.mark.parametrize("group", [0, 1, 32, 40, 64])
+@pytest.mark.parametrize("case", [(40, 24, 1), (40, 33, 1), (40, 300, 1), (40, 512, 1), (40, 1000, 1), (40, 2003, 3), (40, 1024, 9)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_rms_norm_quant_of_any_size(case, group):
+    """Scales of all sizes, of groups of zeros and of NaN, beside usual ones: those of the forward, and its values divided by them.  (Scales
+    of y below 448 2^-126 are subnormal, and so are their quotients' remainders: the division is the card's there.)"""
+    n, c, inner = case
+    width = c * inner
+    rng = np.random.default_rng(width)
+    size = np.resize([1.0, 1e-22, 1e-30, 1e-36, 1e-44, 0.0, 1.0, np.nan], n)[:, None, None]
+    x, _ = rounded(rng.standard_normal(case) * size, "f32")
+    gamma, _ = rounded((1 + 0.2 * rng.standard_normal(c)) * np.resize([1.0] * 40 + [0.0] * 45 + [1e34] * 7, c), "f32")
+    each = group or width
+    groups = -(-width // each)
+    q, s, y = torch.zeros(case, dtype=torch.float8_e4m3fn, device="cuda"), nan_like((n, groups)), nan_like(case)
+    uvu.rms_norm_quant(x, gamma, q, s, group=group, eps=1e-5)
+    uvu.rms_norm_fwd(x, gamma, y, eps=1e-5)
+    y = torch.nn.functional.pad(y.cpu().view(n, width), (0, groups * each - width)).view(n, groups, each)
+    want = y.abs().amax(2) / 448
+    assert torch.equal(s.cpu().nan_to_num(-1.0), want.nan_to_num(-1.0))
+    v = torch.where(want[:, :, None] == 0, 0.0, y / want[:, :, None]).clamp(-448, 448).view(n, -1)[:, :width]
+    assert torch.equal(q.cpu().view(n, width).float().nan_to_num(-999.0), v.to(torch.float8_e4m3fn).float().nan_to_num(-999.0))
+
+
 def test_rms_norm_of_any_eps():
     """The largest eps beside the largest rows."""
     x = torch.tensor([[1.0] * 40, [3e38] * 40, [2.0 ** 63] * 40], device="cuda")
