@@ -7,14 +7,15 @@
 // gamma is one value a channel, shared by the `inner` components of an irrep, so y is as equivariant as x.  The norm is of h as
 // it is stored: what the next layer and the gradient read is what was normalised.
 //
-// Bound by memory: every tensor moves once.  A row belongs to a team, a part of a warp or a block, whose threads hold it in registers, 16
-// values each at most, between the sum and the result.  The team's next rows are on their way to shared memory meanwhile, by
-// asynchronous copies that cost no registers: with one row ahead in registers the gradient had 48 KB in flight on an SM and ran at half of
-// the memory's rate.  Rows that do not begin on 16 bytes are read in words, one row ahead in registers (copied in whole chunks, with
-// what lies before and behind them, they took twice the time), also where every other one begins inside a word.  262,144 x 512 in bf16 with
-// the residual: 341 us forward and back (6.3 TB/s); 65,537 x 1024 to 8 bits 88 us (5.4 TB/s); 96,064 x 427 in f16 with the residual: 63 us
-// (5.2 TB/s) forward, 90 us (3.7 TB/s) back, to 8 bits 71 us (4.0 TB/s), with groups of 64, which lanes do not share evenly, 172 us.  A thread has the same columns of every row that it sees, so gamma is read once, and d_gamma is
-// summed in registers, then over the block's teams in shared memory, and over the blocks, in their order, by a second kernel.
+// Bound by memory: every tensor moves once. A row belongs to a team, a part of a warp or a block, whose threads hold it in registers, 16
+// values each at most, between the sum and the result. The team's next rows are on their way to shared memory meanwhile, by asynchronous
+// copies that cost no registers: with one row ahead in registers the gradient had 48 KB in flight on an SM and ran at half of the memory's
+// rate. Rows that do not begin on 16 bytes are read in words, one row ahead in registers (copied in whole chunks, with what lies before and
+// behind them, they took twice the time), also where every other one begins inside a word. 262,144 x 512 in bf16 with the residual: 341 us
+// forward and back (6.3 TB/s); 65,537 x 1024 to 8 bits 88 us (5.4 TB/s); 96,064 x 427 in f16 with the residual: 63 us (5.2 TB/s) forward,
+// 90 us (3.7 TB/s) back, to 8 bits 71 us (4.0 TB/s), with groups of 64, which lanes do not share evenly, 172 us. A thread has the same
+// columns of every row that it sees, so gamma is read once, and d_gamma is summed in registers, then over the block's teams in shared
+// memory, and over the blocks, in their order, by a second kernel.
 #pragma once
 
 #include <cuda_fp8.h>

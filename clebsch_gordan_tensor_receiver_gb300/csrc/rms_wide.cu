@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(kWideThreads) rms_wide_bwd_kernel(const RmsArg
 // f(V): vectors of 16 bytes where every row of every tensor begins on one (an 8-bit one: on V bytes), else single values.
 template <typename T, typename F>
 cudaError_t by_alignment(const RmsArgs& a, bool quant, F f) {
-    uintptr_t any = uintptr_t(a.width) * sizeof(T) | reinterpret_cast<uintptr_t>(a.out[0]) * (quant ? sizeof(T) : 1) | reinterpret_cast<uintptr_t>(a.out[1]);
+    uintptr_t any = uintptr_t(a.width) * sizeof(T) | reinterpret_cast<uintptr_t>(a.out[0]) * (quant ? sizeof(T) : 1);
+    any |= reinterpret_cast<uintptr_t>(a.out[1]);
     for (const void* t : a.in) any |= reinterpret_cast<uintptr_t>(t);
     return any % 16 == 0 ? f(std::integral_constant<int, 16 / int(sizeof(T))>()) : f(std::integral_constant<int, 1>());
 }
@@ -240,7 +241,9 @@ template <typename T>
 cudaError_t wide_launch(const RmsArgs& a, RmsMode mode, int sms, cudaStream_t st) {
     return by_alignment<T>(a, mode == kRmsQuant, [&](auto v) {
         constexpr int V = decltype(v)::value;
-        auto kernel = mode == kRmsFwd ? rms_wide_kernel<T, V, kRmsFwd> : mode == kRmsQuant ? rms_wide_kernel<T, V, kRmsQuant> : rms_wide_bwd_kernel<T, V>;
+        auto kernel = mode == kRmsFwd     ? rms_wide_kernel<T, V, kRmsFwd>
+                      : mode == kRmsQuant ? rms_wide_kernel<T, V, kRmsQuant>
+                                          : rms_wide_bwd_kernel<T, V>;
         const size_t smem = mode == kRmsFwd ? 0 : size_t(mode == kRmsQuant ? a.groups : a.width) * 4;
         if (smem > 40 << 10) {
             cudaError_t e = allow_most_smem(kernel, smem);
